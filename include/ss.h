@@ -351,6 +351,150 @@ ss_status ss_ssd_fwd(const ss_ssd_problem *p, const void *x, const void *dt, con
                      const int32_t *seq_idx, const float *h0, void *y, float *final_state,
                      void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * ---- serving a Mamba-2 layer: packed prompts and single tokens over state slots ----
+ * A server holds one pool of states for all its requests ("mamba-metal"
+ * README, "O(1) per token via state caching": the SSM state and the conv1d
+ * window are carried across calls), and a request has a slot of it:
+ *   conv_state : (nslots, channels, W-1) fp32, windows as in ss_conv1d_step
+ *   state      : (nslots, nheads, headdim, dstate) fp32, as ss_ssd_fwd's final_state
+ * The calls below update both in place.  Prompts are packed: the rows (tokens)
+ * of sequence s are cu_seqlens[s] .. cu_seqlens[s+1]-1.
+ *   cu_seqlens : device int32[nseqs+1], not decreasing, within 0 .. tokens.
+ *                Rows outside every sequence (before the first, behind the
+ *                last) are not read, and their outputs stay as they were.  A
+ *                sequence may be empty.  Offsets are clamped to that range
+ *                (an end to its start), so that no content makes a kernel
+ *                leave its buffers; what rows then give is not specified.
+ *   slots      : device int32[nseqs] ([rows] for a step): the slot of each, or
+ *                NULL: sequence (row) i has slot i, and nslots must be at least
+ *                their number.  An index outside 0 .. nslots-1 (-1, say) is no
+ *                slot: such a sequence starts from zero and keeps no state;
+ *                such a row of a step is not computed and its output stays as
+ *                it was (padding of a captured batch).  No two may name the
+ *                same slot: which of them it then holds is not specified.
+ *   has_state  : device int32[nseqs]; nonzero: the sequence continues from its
+ *                slot's state; zero (NULL: all): it starts from zero, whatever
+ *                the slot holds.
+ * Rows may lie further apart than they are long (strides in elements, at most
+ * 2^21), so that the parts of a projection's output rows are taken as they
+ * lie.  No output may share a byte with any other buffer, slots' pools among
+ * them (SS_ERR_UNSUPPORTED).  Nothing is kept between calls but the pools;
+ * calls that use the same slots or the same workspace must be ordered by the
+ * caller.  1 <= tokens <= 2^30, 1 <= nseqs <= 2^20.
+ */
+
+/*
+ * Depthwise causal conv1d (+ SiLU) of packed prompts, time-major:
+ *   out[t,d] = silu(bias[d] + sum_{k<W} w[d,k] * x[t-W+1+k,d]),
+ * the inputs before a sequence's first row being its slot's window, or zeros.
+ *   x, out : (tokens, dim) io dtype (fp32, fp16 or bf16), rows x_stride /
+ *            out_stride apart; aligned to the element.  16-byte aligned rows
+ *            of whole 16-byte vectors run faster.
+ *   w      : (dim, W) fp32; bias: (dim) fp32 or NULL, as in ss_conv1d_fwd.
+ *   conv_state : afterwards every sequence's slot holds its last W-1 inputs
+ *            (oldest first; of the window before where it is shorter).  May be
+ *            NULL for W = 1 only.
+ */
+typedef struct ss_conv_prompt_problem {
+    int64_t tokens;      /* rows of x and out */
+    int64_t nseqs;
+    int64_t dim;         /* channels, at most 2^21 */
+    int64_t nslots;
+    int64_t x_stride;    /* elements between rows, >= dim */
+    int64_t out_stride;
+    int32_t width;       /* W, 1..4 */
+    int32_t io_dtype;
+    int32_t silu;        /* nonzero: SiLU */
+    int32_t reserved;    /* must be 0 */
+} ss_conv_prompt_problem;
+
+ss_status ss_conv1d_prompt(const ss_conv_prompt_problem *p, const void *x, const float *w, const float *bias,
+                           const int32_t *cu_seqlens, const int32_t *slots, const int32_t *has_state,
+                           float *conv_state, void *out, void *stream);
+
+/*
+ * Mamba-2 SSD scan (the recurrence of ss_ssd_fwd) of packed prompts, each from
+ * and into its slot's state.
+ *   x, z, y : (tokens, nheads, 64) io dtype (fp16 or bf16), tokens x_stride /
+ *             z_stride apart, y without gaps; z may be NULL
+ *   Bm, Cm  : (tokens, ngroups, dstate) io dtype, tokens b_stride / c_stride apart
+ *   dt      : (tokens, nheads) io dtype, tokens dt_stride apart
+ *   A, D, dt_bias : (nheads) fp32; D and dt_bias may be NULL
+ * Strides of x, z, Bm and Cm are multiples of 8; pointers are 16-byte aligned
+ * but for dt's, which is aligned to the element.  Outputs and states carry
+ * fp32's error (y before its rounding): computed operands are multiplied as
+ * pairs of bf16 values.  A value that is not finite spreads to other steps of
+ * the same 256-step chunk of its sequence, earlier ones among them, and to no
+ * other sequence.
+ */
+typedef struct ss_ssd_prompt_problem {
+    int64_t tokens;
+    int64_t nseqs;
+    int64_t nslots;
+    int64_t nheads;
+    int64_t ngroups;      /* divides nheads */
+    int64_t x_stride;     /* elements between tokens */
+    int64_t b_stride;
+    int64_t c_stride;
+    int64_t z_stride;     /* ignored without z */
+    int64_t dt_stride;
+    int32_t headdim;      /* 64 */
+    int32_t dstate;       /* 32, 64, 96 or 128 */
+    int32_t io_dtype;     /* SS_F16 or SS_BF16 */
+    int32_t dt_softplus;  /* nonzero: Delta = softplus(dt + dt_bias) */
+} ss_ssd_prompt_problem;
+
+/* Bytes of device workspace ss_ssd_prompt needs, by sizes alone (the lengths do
+ * not matter): for each of tokens / 256 + nseqs chunk places, a state and a
+ * decay per head and C B^T (256 x 256) per group, fp32.  Its contents on entry
+ * do not matter.  0 for an invalid problem. */
+size_t ss_ssd_prompt_workspace_size(const ss_ssd_prompt_problem *p);
+
+ss_status ss_ssd_prompt(const ss_ssd_prompt_problem *p, const void *x, const void *dt, const float *A,
+                        const void *Bm, const void *Cm, const float *D, const void *z, const float *dt_bias,
+                        const int32_t *cu_seqlens, const int32_t *slots, const int32_t *has_state,
+                        float *state, void *y, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token of `rows` requests through convolution and scan:
+ *   xBC  = silu(conv_bias + conv_w . [window, xbc[r]]), the window then drops
+ *          its oldest input and appends xbc[r]; split into x, B and C,
+ *   H    = exp(Delta A) H + Delta x B^T,  y[r] = (H C + D x) * SiLU(z),
+ * the window and H in the row's slot, all in fp32 (the convolved channels are
+ * not rounded in between).
+ *   xbc    : (rows, nheads*64 + 2*ngroups*dstate) io dtype (fp16 or bf16): the
+ *            channels of x, then B, then C, before the convolution
+ *   dt     : (rows, nheads);  z : (rows, nheads, 64) or NULL;  io dtype.  These
+ *            three are aligned to the element, rows the given strides apart.
+ *   conv_w : (channels, W) fp32;  conv_bias : (channels) fp32 or NULL
+ *   y      : (rows, nheads, 64) io dtype, without gaps
+ *   workspace : ss_ssd_step_workspace_size() bytes (the convolved channels);
+ *            its contents on entry do not matter
+ */
+typedef struct ss_ssd_step_problem {
+    int64_t rows;
+    int64_t nslots;
+    int64_t nheads;
+    int64_t ngroups;
+    int64_t xbc_stride;   /* elements between rows */
+    int64_t z_stride;     /* ignored without z */
+    int64_t dt_stride;
+    int32_t headdim;      /* 64 */
+    int32_t dstate;       /* 32, 64, 96 or 128 */
+    int32_t width;        /* W, 1..4 */
+    int32_t io_dtype;
+    int32_t dt_softplus;
+    int32_t reserved;     /* must be 0 */
+} ss_ssd_step_problem;
+
+size_t ss_ssd_step_workspace_size(const ss_ssd_step_problem *p);
+
+ss_status ss_ssd_step(const ss_ssd_step_problem *p, const void *xbc, const void *dt, const float *A,
+                      const float *conv_w, const float *conv_bias, const float *D, const void *z,
+                      const float *dt_bias, const int32_t *slots, float *conv_state, float *state,
+                      void *y, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Number of floats of the checkpoint buffer: batch*dim*ceil(seqlen/64)*dstate (0 if invalid). */
 size_t ss_ckpt_count(const ss_problem *p);
 

@@ -7,8 +7,9 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libss.so")
-SOURCES = ["ss_fwd.hip", "ss_bwd.hip", "ss_conv.hip", "ss_ssd.hip", "ss_probe.hip", "ss_noalloc.hip", "ss_abi.cpp"]
-HEADERS = ["ss_device.h", "ss_internal.h"]
+SOURCES = ["ss_fwd.hip", "ss_bwd.hip", "ss_conv.hip", "ss_ssd.hip", "ss_prompt.hip", "ss_serve.hip", "ss_probe.hip",
+           "ss_noalloc.hip", "ss_abi.cpp"]
+HEADERS = ["ss_device.h", "ss_internal.h", "ss_mfma.h", "ss_packed.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

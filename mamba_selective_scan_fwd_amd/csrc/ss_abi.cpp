@@ -525,6 +525,210 @@ ss_status ss_ssd_fwd(const ss_ssd_problem* p, const void* x, const void* dt, con
   return from_hip(ss::launch_ssd(k, static_cast<hipStream_t>(stream)));
 }
 
+namespace {
+constexpr int64_t kMaxTokens = (int64_t)1 << 30;
+constexpr int64_t kMaxSeqs = (int64_t)1 << 20;
+// the longest row distance: 256 rows of 2-byte elements within 2^30 bytes, the
+// kernels' 32-bit offsets inside a chunk
+constexpr int64_t kMaxStride = (int64_t)1 << 21;
+constexpr int64_t kMaxSlots = ((int64_t)1 << 31) - 1;
+
+bool aligned_to(const void* ptr, int64_t n) { return (uintptr_t)ptr % (uintptr_t)n == 0; }
+// bytes from the first element of `rows` strided rows to behind the last one
+size_t rows_bytes(int64_t rows, int64_t stride, int64_t row, int64_t elem) {
+  return (size_t)(((rows - 1) * stride + row) * elem);
+}
+ss_status check_packed(int64_t tokens, int64_t nseqs, int64_t nslots) {
+  if (tokens < 1 || nseqs < 1 || nslots < 1) return SS_ERR_BAD_SHAPE;
+  if (tokens > kMaxTokens || nseqs > kMaxSeqs || nslots > kMaxSlots) return SS_ERR_BAD_SHAPE;
+  return SS_OK;
+}
+ss_status check_conv_prompt(const ss_conv_prompt_problem* p) {
+  if (!p) return SS_ERR_NULL_ARG;
+  const ss_status s = check_packed(p->tokens, p->nseqs, p->nslots);
+  if (s != SS_OK) return s;
+  if (p->dim < 1 || p->x_stride < p->dim || p->out_stride < p->dim) return SS_ERR_BAD_SHAPE;
+  if (p->dim > kMaxStride || p->x_stride > kMaxStride || p->out_stride > kMaxStride) return SS_ERR_BAD_SHAPE;
+  if (p->io_dtype != SS_F32 && p->io_dtype != SS_F16 && p->io_dtype != SS_BF16) return SS_ERR_BAD_DTYPE;
+  if (p->width < 1 || p->width > 4 || p->reserved != 0) return SS_ERR_UNSUPPORTED;
+  // a workgroup is four waves of 64 channels and 16 rows at the least
+  if ((p->tokens / 16 + p->nseqs) * ((p->dim + 63) / 64) / 4 > kMaxGrid - 1) return SS_ERR_BAD_SHAPE;
+  return SS_OK;
+}
+// the sizes that prompts and steps of the SSD share
+ss_status check_ssd_layer(int64_t nheads, int64_t ngroups, int32_t headdim, int32_t dstate, int32_t io_dtype) {
+  if (nheads < 1 || ngroups < 1) return SS_ERR_BAD_SHAPE;
+  if (io_dtype != SS_F16 && io_dtype != SS_BF16) return SS_ERR_BAD_DTYPE;
+  if (headdim != 64) return SS_ERR_UNSUPPORTED;
+  if (dstate != 32 && dstate != 64 && dstate != 96 && dstate != 128) return SS_ERR_UNSUPPORTED;
+  if (nheads > kMaxStride / 64 || nheads % ngroups != 0) return SS_ERR_UNSUPPORTED;
+  return SS_OK;
+}
+int64_t prompt_chunks(const ss_ssd_prompt_problem* p) { return p->tokens / 256 + p->nseqs; }
+ss_status check_prompt(const ss_ssd_prompt_problem* p) {
+  if (!p) return SS_ERR_NULL_ARG;
+  ss_status s = check_packed(p->tokens, p->nseqs, p->nslots);
+  if (s != SS_OK) return s;
+  s = check_ssd_layer(p->nheads, p->ngroups, p->headdim, p->dstate, p->io_dtype);
+  if (s != SS_OK) return s;
+  const int64_t gn = p->ngroups * p->dstate, hp = p->nheads * 64;
+  if (p->x_stride < hp || p->b_stride < gn || p->c_stride < gn || p->dt_stride < p->nheads) return SS_ERR_BAD_SHAPE;
+  if (p->x_stride > kMaxStride || p->b_stride > kMaxStride || p->c_stride > kMaxStride || p->dt_stride > kMaxStride)
+    return SS_ERR_BAD_SHAPE;
+  if (p->x_stride % 8 || p->b_stride % 8 || p->c_stride % 8) return SS_ERR_MISALIGNED;
+  const int64_t chunks = prompt_chunks(p);
+  if (chunks * (p->nheads + 4 * p->ngroups) > kMaxGrid) return SS_ERR_BAD_SHAPE;
+  if (p->nseqs * p->nheads * (p->dstate / 16) > kMaxGrid) return SS_ERR_BAD_SHAPE;
+  return SS_OK;
+}
+size_t prompt_state_bytes(const ss_ssd_prompt_problem* p) {
+  return align256((size_t)(prompt_chunks(p) * p->nheads) * (size_t)(64 * p->dstate) * 4);
+}
+size_t prompt_decay_bytes(const ss_ssd_prompt_problem* p) {
+  return align256((size_t)(prompt_chunks(p) * p->nheads) * 4);
+}
+int64_t step_channels(const ss_ssd_step_problem* p) { return p->nheads * 64 + 2 * p->ngroups * p->dstate; }
+ss_status check_step_rows(const ss_ssd_step_problem* p) {
+  if (!p) return SS_ERR_NULL_ARG;
+  if (p->rows < 1 || p->nslots < 1 || p->rows > kMaxSeqs || p->nslots > kMaxSlots) return SS_ERR_BAD_SHAPE;
+  const ss_status s = check_ssd_layer(p->nheads, p->ngroups, p->headdim, p->dstate, p->io_dtype);
+  if (s != SS_OK) return s;
+  if (p->width < 1 || p->width > 4 || p->reserved != 0) return SS_ERR_UNSUPPORTED;
+  const int64_t ch = step_channels(p);
+  if (p->xbc_stride < ch || p->dt_stride < p->nheads) return SS_ERR_BAD_SHAPE;
+  if (p->xbc_stride > kMaxStride || p->dt_stride > kMaxStride) return SS_ERR_BAD_SHAPE;
+  if (p->rows * p->nheads > kMaxGrid || p->rows * ((ch + 255) / 256) > kMaxGrid) return SS_ERR_BAD_SHAPE;
+  return SS_OK;
+}
+}  // namespace
+
+ss_status ss_conv1d_prompt(const ss_conv_prompt_problem* p, const void* x, const float* w, const float* bias,
+                           const int32_t* cu_seqlens, const int32_t* slots, const int32_t* has_state,
+                           float* conv_state, void* out, void* stream) {
+  const ss_status s = check_conv_prompt(p);
+  if (s != SS_OK) return s;
+  if (!x || !w || !cu_seqlens || !out || (!conv_state && p->width > 1)) return SS_ERR_NULL_ARG;
+  const int64_t e = elem_size(p->io_dtype);
+  if (!aligned_to(x, e) || !aligned_to(out, e)) return SS_ERR_MISALIGNED;
+  const void* ptrs[] = {w, bias, cu_seqlens, slots, has_state, conv_state};
+  for (const void* q : ptrs)
+    if (q && !aligned(q)) return SS_ERR_MISALIGNED;
+  if (!slots && p->nslots < p->nseqs) return SS_ERR_UNSUPPORTED;
+  {
+    const size_t ib = (size_t)p->nseqs * 4;
+    const Span in[] = {{x, rows_bytes(p->tokens, p->x_stride, p->dim, e)}, {w, (size_t)(p->dim * p->width) * 4},
+                       {bias, (size_t)p->dim * 4}, {cu_seqlens, ib + 4}, {slots, ib}, {has_state, ib}};
+    const Span outs[] = {{out, rows_bytes(p->tokens, p->out_stride, p->dim, e)},
+                         {conv_state, (size_t)p->nslots * (size_t)(p->dim * (p->width - 1)) * 4}};
+    if (conflict(in, outs)) return SS_ERR_UNSUPPORTED;
+  }
+  ss::ConvPromptParams k{};
+  k.io = p->io_dtype; k.width = p->width; k.silu = p->silu != 0;
+  k.x = x; k.w = w; k.bias = bias; k.cu = cu_seqlens; k.slots = slots; k.has_state = has_state;
+  k.conv_state = conv_state; k.out = out;
+  k.x_stride = p->x_stride; k.out_stride = p->out_stride;
+  k.tokens = (int32_t)p->tokens; k.nseqs = (int32_t)p->nseqs; k.dim = (int32_t)p->dim; k.nslots = (int32_t)p->nslots;
+  k.vec = aligned(x) && aligned(out) && (p->dim * e) % 16 == 0 && (p->x_stride * e) % 16 == 0 &&
+          (p->out_stride * e) % 16 == 0;
+  return from_hip(ss::launch_conv_prompt(k, static_cast<hipStream_t>(stream)));
+}
+
+size_t ss_ssd_prompt_workspace_size(const ss_ssd_prompt_problem* p) {
+  if (check_prompt(p) != SS_OK) return 0;
+  return prompt_state_bytes(p) + prompt_decay_bytes(p) +
+         (size_t)(prompt_chunks(p) * p->ngroups) * (size_t)(256 * 256) * 4;
+}
+
+ss_status ss_ssd_prompt(const ss_ssd_prompt_problem* p, const void* x, const void* dt, const float* A, const void* Bm,
+                        const void* Cm, const float* D, const void* z, const float* dt_bias,
+                        const int32_t* cu_seqlens, const int32_t* slots, const int32_t* has_state, float* state,
+                        void* y, void* workspace, size_t workspace_bytes, void* stream) {
+  const ss_status s = check_prompt(p);
+  if (s != SS_OK) return s;
+  if (!x || !dt || !A || !Bm || !Cm || !cu_seqlens || !state || !y) return SS_ERR_NULL_ARG;
+  const int64_t hp = p->nheads * 64, gn = p->ngroups * p->dstate;
+  if (z && (p->z_stride < hp || p->z_stride > kMaxStride)) return SS_ERR_BAD_SHAPE;
+  if (z && p->z_stride % 8) return SS_ERR_MISALIGNED;
+  const void* ptrs[] = {x, A, Bm, Cm, D, z, dt_bias, cu_seqlens, slots, has_state, state, y, workspace};
+  for (const void* q : ptrs)
+    if (q && !aligned(q)) return SS_ERR_MISALIGNED;
+  if (!aligned_to(dt, 2)) return SS_ERR_MISALIGNED;
+  if (!slots && p->nslots < p->nseqs) return SS_ERR_UNSUPPORTED;
+  const size_t need = ss_ssd_prompt_workspace_size(p);
+  if (!workspace || workspace_bytes < need) return SS_ERR_UNSUPPORTED;
+  {
+    const size_t ib = (size_t)p->nseqs * 4, vb = (size_t)p->nheads * 4;
+    const Span in[] = {{x, rows_bytes(p->tokens, p->x_stride, hp, 2)},
+                       {z, rows_bytes(p->tokens, z ? p->z_stride : hp, hp, 2)},
+                       {Bm, rows_bytes(p->tokens, p->b_stride, gn, 2)},
+                       {Cm, rows_bytes(p->tokens, p->c_stride, gn, 2)},
+                       {dt, rows_bytes(p->tokens, p->dt_stride, p->nheads, 2)},
+                       {A, vb}, {D, vb}, {dt_bias, vb}, {cu_seqlens, ib + 4}, {slots, ib}, {has_state, ib}};
+    const Span outs[] = {{y, (size_t)(p->tokens * hp) * 2},
+                         {state, (size_t)p->nslots * (size_t)(hp * p->dstate) * 4},
+                         {workspace, need}};
+    if (conflict(in, outs)) return SS_ERR_UNSUPPORTED;
+  }
+  ss::SsdPromptParams k{};
+  k.io = p->io_dtype; k.softplus = p->dt_softplus != 0;
+  k.x = x; k.dt = dt; k.Bm = Bm; k.Cm = Cm; k.z = z; k.A = A; k.D = D; k.dt_bias = dt_bias;
+  k.cu = cu_seqlens; k.slots = slots; k.has_state = has_state; k.state = state; k.y = y;
+  char* ws = static_cast<char*>(workspace);
+  k.ws_state = reinterpret_cast<float*>(ws);
+  k.ws_decay = reinterpret_cast<float*>(ws + prompt_state_bytes(p));
+  k.ws_cb = reinterpret_cast<float*>(ws + prompt_state_bytes(p) + prompt_decay_bytes(p));
+  k.x_stride = p->x_stride; k.b_stride = p->b_stride; k.c_stride = p->c_stride; k.z_stride = p->z_stride;
+  k.dt_stride = p->dt_stride;
+  k.tokens = (int32_t)p->tokens; k.nseqs = (int32_t)p->nseqs; k.nslots = (int32_t)p->nslots;
+  k.nheads = (int32_t)p->nheads; k.ngroups = (int32_t)p->ngroups; k.dstate = p->dstate;
+  k.chunks = (int32_t)prompt_chunks(p);
+  return from_hip(ss::launch_ssd_prompt(k, static_cast<hipStream_t>(stream)));
+}
+
+size_t ss_ssd_step_workspace_size(const ss_ssd_step_problem* p) {
+  if (check_step_rows(p) != SS_OK) return 0;
+  return (size_t)(p->rows * step_channels(p)) * 4;
+}
+
+ss_status ss_ssd_step(const ss_ssd_step_problem* p, const void* xbc, const void* dt, const float* A,
+                      const float* conv_w, const float* conv_bias, const float* D, const void* z,
+                      const float* dt_bias, const int32_t* slots, float* conv_state, float* state, void* y,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  const ss_status s = check_step_rows(p);
+  if (s != SS_OK) return s;
+  if (!xbc || !dt || !A || !conv_w || !state || !y || (!conv_state && p->width > 1)) return SS_ERR_NULL_ARG;
+  const int64_t hp = p->nheads * 64, ch = step_channels(p);
+  if (z && (p->z_stride < hp || p->z_stride > kMaxStride)) return SS_ERR_BAD_SHAPE;
+  const void* ptrs[] = {A, conv_w, conv_bias, D, dt_bias, slots, conv_state, state, y, workspace};
+  for (const void* q : ptrs)
+    if (q && !aligned(q)) return SS_ERR_MISALIGNED;
+  if (!aligned_to(xbc, 2) || !aligned_to(dt, 2) || !aligned_to(z, 2)) return SS_ERR_MISALIGNED;
+  if (!slots && p->nslots < p->rows) return SS_ERR_UNSUPPORTED;
+  const size_t need = ss_ssd_step_workspace_size(p);
+  if (!workspace || workspace_bytes < need) return SS_ERR_UNSUPPORTED;
+  {
+    const size_t vb = (size_t)p->nheads * 4, cb = (size_t)ch * 4;
+    const Span in[] = {{xbc, rows_bytes(p->rows, p->xbc_stride, ch, 2)},
+                       {dt, rows_bytes(p->rows, p->dt_stride, p->nheads, 2)},
+                       {z, rows_bytes(p->rows, z ? p->z_stride : hp, hp, 2)},
+                       {A, vb}, {D, vb}, {dt_bias, vb}, {conv_w, cb * p->width}, {conv_bias, cb},
+                       {slots, (size_t)p->rows * 4}};
+    const Span outs[] = {{y, (size_t)(p->rows * hp) * 2},
+                         {conv_state, (size_t)p->nslots * cb * (size_t)(p->width - 1)},
+                         {state, (size_t)p->nslots * (size_t)(hp * p->dstate) * 4},
+                         {workspace, need}};
+    if (conflict(in, outs)) return SS_ERR_UNSUPPORTED;
+  }
+  ss::SsdStepParams k{};
+  k.io = p->io_dtype; k.softplus = p->dt_softplus != 0; k.width = p->width;
+  k.xbc = xbc; k.dt = dt; k.z = z; k.A = A; k.D = D; k.dt_bias = dt_bias; k.conv_w = conv_w; k.conv_bias = conv_bias;
+  k.slots = slots; k.conv_state = conv_state; k.state = state; k.y = y; k.ws_xbc = static_cast<float*>(workspace);
+  k.xbc_stride = p->xbc_stride; k.dt_stride = p->dt_stride; k.z_stride = p->z_stride;
+  k.rows = (int32_t)p->rows; k.nslots = (int32_t)p->nslots; k.nheads = (int32_t)p->nheads;
+  k.ngroups = (int32_t)p->ngroups; k.dstate = p->dstate; k.channels = (int32_t)ch;
+  return from_hip(ss::launch_ssd_step(k, static_cast<hipStream_t>(stream)));
+}
+
 ss_status ss_copy_probe(const void* src, void* dst, size_t bytes, void* stream) {
   if (!src || !dst) return SS_ERR_NULL_ARG;
   if (!aligned(src) || !aligned(dst)) return SS_ERR_MISALIGNED;

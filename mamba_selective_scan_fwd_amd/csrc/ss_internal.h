@@ -159,6 +159,72 @@ struct SsdParams {
   int64_t batch, seqlen, nheads, ngroups, dstate, nchunks;
 };
 
+// Packed sequences: rows cu[s] .. cu[s + 1] - 1 belong to sequence s.
+struct ConvPromptParams {
+  int32_t io;
+  int32_t width;
+  int32_t silu;
+  bool vec;                  // 16-byte rows of channels (see conv1d_prompt_kernel)
+  const void* x;             // (tokens, dim), rows x_stride apart
+  const float* w;            // (dim, W)
+  const float* bias;         // (dim) or null
+  const int32_t* cu;         // (nseqs + 1)
+  const int32_t* slots;      // (nseqs) or null: sequence s has slot s
+  const int32_t* has_state;  // (nseqs) or null: none has
+  float* conv_state;         // (nslots, dim, W-1)
+  void* out;                 // (tokens, dim), rows out_stride apart
+  int64_t x_stride, out_stride;
+  int32_t tokens, nseqs, dim, nslots;
+};
+
+struct SsdStepParams {
+  int32_t io;
+  int32_t softplus;
+  int32_t width;
+  const void* xbc;           // (rows, nheads * 64 + 2 * ngroups * dstate), rows xbc_stride apart
+  const void* dt;            // (rows, nheads)
+  const void* z;             // (rows, nheads, 64) or null
+  const float* A;
+  const float* D;            // or null
+  const float* dt_bias;      // or null
+  const float* conv_w;       // (channels, W)
+  const float* conv_bias;    // (channels) or null
+  const int32_t* slots;      // (rows) or null: row r has slot r
+  float* conv_state;         // (nslots, channels, W-1)
+  float* state;              // (nslots, nheads, 64, dstate)
+  void* y;                   // (rows, nheads, 64)
+  float* ws_xbc;             // workspace: (rows, channels) the convolved channels
+  int64_t xbc_stride, dt_stride, z_stride;
+  int32_t rows, nslots, nheads, ngroups, dstate, channels;
+};
+
+struct SsdPromptParams {
+  int32_t io;
+  int32_t softplus;
+  const void* x;             // (tokens, nheads, 64), tokens x_stride apart
+  const void* dt;            // (tokens, nheads)
+  const void* Bm;            // (tokens, ngroups, dstate)
+  const void* Cm;
+  const void* z;             // like x, or null
+  const float* A;
+  const float* D;            // or null
+  const float* dt_bias;      // or null
+  const int32_t* cu;         // (nseqs + 1)
+  const int32_t* slots;      // (nseqs) or null: sequence s has slot s
+  const int32_t* has_state;  // (nseqs) or null: none has
+  float* state;              // (nslots, nheads, 64, dstate)
+  void* y;                   // (tokens, nheads, 64)
+  float* ws_state;           // (chunks, nheads, 64, dstate): a chunk's own state, then the state that enters it
+  float* ws_decay;           // (chunks, nheads): the decay over a chunk
+  float* ws_cb;              // (chunks, ngroups, 256 * 256): C B^T in operand order
+  int64_t x_stride, b_stride, c_stride, z_stride, dt_stride;
+  int32_t tokens, nseqs, nslots, nheads, ngroups, dstate;
+  int32_t chunks;            // chunk places: tokens / 256 + nseqs
+};
+
+hipError_t launch_conv_prompt(const ConvPromptParams& p, hipStream_t st);
+hipError_t launch_ssd_step(const SsdStepParams& p, hipStream_t st);
+hipError_t launch_ssd_prompt(const SsdPromptParams& p, hipStream_t st);
 hipError_t launch_fwd(const FwdParams& p, int64_t nchunks, hipStream_t st);
 int64_t device_cus();
 hipError_t launch_ssd(const SsdParams& p, hipStream_t st);

@@ -1,0 +1,552 @@
+// ss_prompt.hip -- the Mamba-2 SSD scan of packed prompts on MFMA (gfx950).
+//
+// Page "Mamba" (walkthrough), "Deep dive: Mamba-2 and state-space duality":
+// per head, with the state H[p][n] (headdim 64 x dstate N),
+//   H_t = exp(Delta_t A) H_{t-1} + Delta_t x_t B_t^T,  y_t = H_t C_t + D x_t,
+// computed in chunks of Q = 256 steps; with cs the running sum of Delta A from
+// a chunk's first step,
+//   S   = sum_j exp(cs_last - cs_j) Delta_j x_j B_j^T          (the chunk's own state)
+//   E'  = exp(cs_last) E + S                                   (E enters the chunk)
+//   Y_i = exp(cs_i) E C_i + sum_{j<=i} exp(cs_i - cs_j) Delta_j (C_i . B_j) x_j.
+// The prompts of a batch lie one behind the other (cu: their row offsets);
+// chunks are counted from each prompt's first row (ss_packed.h), so that no
+// chunk holds two prompts, and every prompt's state comes from and goes to
+// its slot of a pool.  Three kernels:
+//   prompt_state_kernel  per (chunk, head): S, and the decay over the chunk;
+//                        further workgroups compute C B^T per (chunk, group);
+//   prompt_pass_kernel   per (prompt, head, 1024 elements): E of every chunk,
+//                        in the place of its S, and the final state;
+//   prompt_scan_kernel   per (chunk, head): Y, skip, gate.
+// All chunks of a prompt run at once, whatever its length; only the
+// element-wise pass walks them in order.
+//
+// Precision: products of 16-bit inputs run on the matrix cores as they are.
+// A computed operand v (weighted x, E, the decayed C B^T) is split into two
+// bf16 values, hi = bf16(v) and lo = bf16(v - hi), |v - hi - lo| <= 2^-18 |v|,
+// and multiplied in two passes, so that states and outputs carry fp32's error
+// rather than bf16's; fp16 inputs split exactly the same way (11 bits into
+// 16), which keeps bf16's range for the products.  States stay in fp32.
+#include "ss_device.h"
+#include "ss_internal.h"
+#include "ss_mfma.h"
+#include "ss_packed.h"
+
+namespace ss {
+namespace {
+
+constexpr int kLogQ = 8;
+constexpr int kQ = 1 << kLogQ;  // chunk length
+constexpr int kP = 64;          // headdim
+constexpr int kJB = 64;         // time piece of a chunk
+using BF = mfma_t<SS_BF16>;
+
+// v0, v1 as packed bf16 words hi and lo
+__device__ __forceinline__ void split2(float v0, float v1, uint32_t& hi, uint32_t& lo) {
+  hi = pack2<SS_BF16>(v0, v1);
+  lo = pack2<SS_BF16>(v0 - __uint_as_float(hi << 16), v1 - __uint_as_float(hi & 0xffff0000u));
+}
+template <int IO>
+__device__ __forceinline__ float low16(uint32_t w) { return bits_f32<IO>((raw_t<IO>)(w & 0xffffu)); }
+template <int IO>
+__device__ __forceinline__ float high16(uint32_t w) { return bits_f32<IO>((raw_t<IO>)(w >> 16)); }
+// eight 16-bit values as bf16 hi and lo parts (bf16 input is its own hi)
+template <int IO>
+__device__ __forceinline__ void split8(u32x4v w, u32x4v& hi, u32x4v& lo) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t a, b;
+    split2(low16<IO>(w[q]), high16<IO>(w[q]), a, b);
+    hi[q] = a;
+    lo[q] = b;
+  }
+}
+__device__ __forceinline__ bf16x8 bfv(u32x4v w) { return as_vec<SS_BF16>(w); }
+
+// The rows of a chunk of an operand: `at` points at its first row's columns
+// (wave-uniform), rows are `row` bytes apart, and rows from `rows` on read as
+// zeros through the range check.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_view(const void* at, int64_t row, int rows) {
+  return make_rsrc(at, at ? (uint32_t)(rows * row) : 0u);
+}
+
+template <int IO>
+__device__ __forceinline__ float step_size(const SsdPromptParams& p, float raw, int h) {
+  const float xd = raw + (p.dt_bias ? p.dt_bias[h] : 0.0f);
+  return p.softplus ? softplus_f(xd) : xd;
+}
+
+// ---- pass 1: the chunks' own states, and C B^T --------------------------------
+// State workgroup = (chunk, head), 256 threads: S^T[n][p] = sum_j B_j[n] (w_j x_j[p])
+// over pieces of 64 steps staged in LDS as time-major tiles; wave w holds the
+// channels 16 w .. and all states.  w_j = exp(sum of Delta A behind j) Delta_j
+// comes from a sum that runs backwards, so that no difference of long sums
+// enters the state.
+template <int IO, int N>
+__device__ __forceinline__ void state_role(const SsdPromptParams& p, int place, int h) {
+  constexpr bool kTwo = IO == SS_F16;  // B needs a lo part
+  __shared__ __attribute__((aligned(16))) float sW[kQ];
+  __shared__ float sWave[4];
+  __shared__ __attribute__((aligned(16))) uint16_t sX[2][kJB * kP];
+  __shared__ __attribute__((aligned(16))) uint16_t sB[kTwo ? 2 : 1][N / 32][kJB * 32];
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  const SeqChunk q = find_chunk<kLogQ>(p.cu, p.nseqs, p.tokens, place);
+  if (q.chunk < 0 || q.chunk * kQ >= q.len) return;
+  const int left = q.len - q.chunk * kQ, rows = left < kQ ? left : kQ;
+  const int64_t row0 = q.begin + (int64_t)q.chunk * kQ;
+  const int g = h / (p.nheads / p.ngroups);
+  const int64_t xrow = p.x_stride * 2, brow = p.b_stride * 2;
+  const auto xv = rows_view(static_cast<const char*>(p.x) + row0 * xrow + h * kP * 2, xrow, rows);
+  const auto bv = rows_view(static_cast<const char*>(p.Bm) + row0 * brow + g * N * 2, brow, rows);
+  u32x4v xr[2], br[N / 32];
+  auto load_piece = [&](int j0) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) xr[k] = vload16(xv, (uint32_t)((j0 + tid / 8 + 32 * k) * xrow + (tid % 8) * 16));
+#pragma unroll
+    for (int k = 0; k < N / 32; ++k) br[k] = vload16(bv, (uint32_t)((j0 + tid / 4) * brow + k * 64 + (tid % 4) * 16));
+  };
+  load_piece(0);
+  {
+    const bool in = tid < rows;
+    const float delta = in ? step_size<IO>(p, load_io<IO>(p.dt, (row0 + tid) * p.dt_stride + h), h) : 0.0f;
+    const float da = delta * p.A[h];
+    float v = da;  // sum from this step to the end of the wave's 64
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const float o = __shfl_down(v, off, 64);
+      if (lane + off < 64) v += o;
+    }
+    if (lane == 0) sWave[wave] = v;
+    __syncthreads();
+    float behind = __shfl_down(v, 1, 64);
+    if (lane == 63) behind = 0.0f;
+    for (int w = 3; w > wave; --w) behind += sWave[w];
+    sW[tid] = in ? exp2_hw(behind * kLog2e) * delta : 0.0f;
+    if (tid == 0)
+      p.ws_decay[(int64_t)place * p.nheads + h] = exp2_hw((sWave[0] + sWave[1] + sWave[2] + sWave[3]) * kLog2e);
+    __syncthreads();
+  }
+  const int xo[2] = {tm_lane_off<kP>(16 * wave, 0, lane), tm_lane_off<kP>(16 * wave, 1, lane)};
+  const int bo[2][2] = {{tm_lane_off<32>(0, 0, lane), tm_lane_off<32>(0, 1, lane)},
+                        {tm_lane_off<32>(16, 0, lane), tm_lane_off<32>(16, 1, lane)}};
+  f32x4 acc[N / 16];
+#pragma unroll
+  for (int t = 0; t < N / 16; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int j0 = 0; j0 < rows; j0 += kJB) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int row = tid / 8 + 32 * k;
+      const float w = sW[j0 + row];
+      u32x4v hi, lo;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t a, b;
+        split2(low16<IO>(xr[k][e]) * w, high16<IO>(xr[k][e]) * w, a, b);
+        hi[e] = a;
+        lo[e] = b;
+      }
+      *reinterpret_cast<u32x4v*>(&sX[0][tm_off<kP>(row, 8 * (tid % 8))]) = hi;
+      *reinterpret_cast<u32x4v*>(&sX[1][tm_off<kP>(row, 8 * (tid % 8))]) = lo;
+    }
+#pragma unroll
+    for (int k = 0; k < N / 32; ++k) {
+      const int at = tm_off<32>(tid / 4, 8 * (tid % 4));
+      if constexpr (kTwo) {
+        u32x4v hi, lo;
+        split8<IO>(br[k], hi, lo);
+        *reinterpret_cast<u32x4v*>(&sB[0][k][at]) = hi;
+        *reinterpret_cast<u32x4v*>(&sB[1][k][at]) = lo;
+      } else {
+        *reinterpret_cast<u32x4v*>(&sB[0][k][at]) = br[k];
+      }
+    }
+    __syncthreads();
+    if (j0 + kJB < rows) load_piece(j0 + kJB);  // lands while this piece is multiplied
+#pragma unroll
+    for (int ks = 0; ks < kJB; ks += 32) {
+      const bf16x8 xh = bfv(tm_frag(&sX[0][ks * kP], xo[0], xo[1]));  // [k = step][n = channel]
+      const bf16x8 xl = bfv(tm_frag(&sX[1][ks * kP], xo[0], xo[1]));
+#pragma unroll
+      for (int t = 0; t < N / 16; ++t) {
+        const bf16x8 bh = bfv(tm_frag(&sB[0][t / 2][ks * 32], bo[t % 2][0], bo[t % 2][1]));  // [m = state][k = step]
+        acc[t] = BF::run(bh, xl, acc[t]);
+        acc[t] = BF::run(bh, xh, acc[t]);
+        if constexpr (kTwo) {
+          const bf16x8 bl = bfv(tm_frag(&sB[kTwo ? 1 : 0][t / 2][ks * 32], bo[t % 2][0], bo[t % 2][1]));
+          acc[t] = BF::run(bl, xl, acc[t]);
+          acc[t] = BF::run(bl, xh, acc[t]);
+        }
+      }
+    }
+    __syncthreads();
+  }
+  float* S = p.ws_state + ((int64_t)place * p.nheads + h) * (kP * N) + (16 * wave + lane % 16) * N + 4 * (lane / 16);
+#pragma unroll
+  for (int t = 0; t < N / 16; ++t) *reinterpret_cast<f32x4*>(S + 16 * t) = acc[t];
+}
+
+// C B^T workgroup = (chunk, group, band of 64 rows): for the band's rows i and
+// the columns j up to its end, in fp32, in the order in which the output pass
+// reads its operands: element (i, j) of row tile it = i / 16 and k-step
+// kt = j / 32 is float j % 8 of lane i % 16 + 16 ((j % 32) / 8), 8 floats a
+// lane, so that pass reads whole contiguous kilobytes.  Wave w has row tile
+// 4 band + w; the product is built transposed (B C^T), so that a lane holds 4
+// consecutive columns of one row.
+__device__ __forceinline__ int64_t cb_at(int it, int kt) { return (int64_t)(it * (kQ / 32) + kt) * 512; }
+
+template <int IO, int N>
+__device__ __forceinline__ void cb_role(const SsdPromptParams& p, int place, int g, int band) {
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const SeqChunk q = find_chunk<kLogQ>(p.cu, p.nseqs, p.tokens, place);
+  if (q.chunk < 0 || q.chunk * kQ >= q.len) return;
+  const int left = q.len - q.chunk * kQ, rows = left < kQ ? left : kQ;
+  const int it = 4 * band + wave;
+  if (16 * it >= rows) return;
+  const int64_t row0 = q.begin + (int64_t)q.chunk * kQ;
+  const int64_t brow = p.b_stride * 2, crow = p.c_stride * 2;
+  const auto bv = rows_view(static_cast<const char*>(p.Bm) + row0 * brow + g * N * 2, brow, rows);
+  const auto cv = rows_view(static_cast<const char*>(p.Cm) + row0 * crow + g * N * 2, crow, rows);
+  u32x4v c[N / 32];
+#pragma unroll
+  for (int ks = 0; ks < N / 32; ++ks)
+    c[ks] = vload16(cv, (uint32_t)((16 * it + lane % 16) * crow + (32 * ks + 8 * (lane / 16)) * 2));
+  float* CB = p.ws_cb + ((int64_t)place * p.ngroups + g) * (kQ * kQ);
+  for (int jt = 0; jt < 4 * band + 4; ++jt) {
+    f32x4 acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int ks = 0; ks < N / 32; ++ks) {
+      const u32x4v b = vload16(bv, (uint32_t)((16 * jt + lane % 16) * brow + (32 * ks + 8 * (lane / 16)) * 2));
+      acc = mfma_t<IO>::run(as_vec<IO>(b), as_vec<IO>(c[ks]), acc);
+    }
+    const int to = lane % 16 + 16 * (2 * (jt & 1) + lane / 32);
+    *reinterpret_cast<f32x4*>(CB + cb_at(it, jt / 2) + to * 8 + 4 * ((lane / 16) & 1)) = acc;
+  }
+}
+
+template <int IO, int N>
+__global__ void __launch_bounds__(256) prompt_state_kernel(SsdPromptParams p) {
+  const int states = p.chunks * p.nheads;
+  const int lb = (int)xcd_logical_block();
+  if (lb < states) {
+    state_role<IO, N>(p, lb / p.nheads, lb % p.nheads);
+  } else {
+    const int r = lb - states;
+    cb_role<IO, N>(p, r / (4 * p.ngroups), (r / 4) % p.ngroups, r % 4);
+  }
+}
+
+// ---- pass 2: the states between the chunks -----------------------------------------
+// Workgroup = (prompt, head, 1024 elements), a thread 4 elements: E <- the
+// slot's state (or 0); per chunk, S <- E in memory and E <- decay E + S.  Four
+// chunks' S are loaded ahead.
+template <int N>
+__global__ void __launch_bounds__(256) prompt_pass_kernel(SsdPromptParams p) {
+  constexpr int kParts = kP * N / 1024, kAhead = 4;
+  const int part = (int)(blockIdx.x % kParts);
+  const int h = (int)((blockIdx.x / kParts) % (uint32_t)p.nheads);
+  const int s = (int)(blockIdx.x / kParts / (uint32_t)p.nheads);
+  const int e = part * 1024 + 4 * (int)threadIdx.x;
+  const int begin = uniform(seq_row(p.cu, s, p.tokens)), end = uniform(seq_row(p.cu, s + 1, p.tokens));
+  const int n = end > begin ? (end - begin + kQ - 1) >> kLogQ : 0;
+  const int first = (begin >> kLogQ) + s;
+  const int slot = uniform(slot_of(p.slots, s, p.nslots));
+  f32x4* state = reinterpret_cast<f32x4*>(p.state + ((int64_t)(slot < 0 ? 0 : slot) * p.nheads + h) * (kP * N) + e);
+  f32x4 E = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  if (slot >= 0 && p.has_state && p.has_state[s] != 0) E = *state;
+  float* ws = p.ws_state + ((int64_t)first * p.nheads + h) * (kP * N) + e;
+  const float* dec = p.ws_decay + (int64_t)first * p.nheads + h;
+  const int64_t step = (int64_t)p.nheads * (kP * N);
+  f32x4 S[kAhead];
+  float d[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    if (k < n) {
+      S[k] = *reinterpret_cast<const f32x4*>(ws + k * step);
+      d[k] = dec[(int64_t)k * p.nheads];
+    }
+  for (int c = 0; c < n; c += kAhead) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (c + k < n) {
+        const f32x4 own = S[k];
+        const float decay = d[k];
+        if (c + k + kAhead < n) {
+          S[k] = *reinterpret_cast<const f32x4*>(ws + (c + k + kAhead) * step);
+          d[k] = dec[(int64_t)(c + k + kAhead) * p.nheads];
+        }
+        *reinterpret_cast<f32x4*>(ws + (c + k) * step) = E;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) E[i] = fmaf(decay, E[i], own[i]);
+      }
+  }
+  if (slot >= 0) *state = E;
+}
+
+// ---- pass 3: outputs of a chunk ------------------------------------------------------
+// Workgroup = (chunk, head), 512 threads.  Y is built transposed, Y^T[p][i], so
+// that a lane ends with 4 consecutive channels of one step i.  The chunk's 256
+// rows are 8 blocks of 32; waves w and w + 4 take the two 16-row halves of
+// blocks w and 7 - w, so that every wave does the same causal work:
+//   Y^T = E C^T scaled by exp(cs_i)  +  x^T M^T,
+// M[i][j] = CB[i][j] exp(cs_i - cs_j) Delta_j for j <= i, built in registers.
+// cs is kept as its sum inside a piece of 64 steps (sCs) and the sums over
+// whole pieces (sTot): pairs inside a piece take a difference of the former, a
+// pair across pieces two factors, exp(cs_i - end of j's piece) and
+// exp(end of j's piece - cs_j), one exp per row and one per column.
+constexpr int kScanThreads = 512;
+template <int IO, int N>
+__global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptParams p) {
+  constexpr bool kTwo = IO == SS_F16;  // x and C need a lo part
+  constexpr int kHS = N + 8;           // row stride of E in LDS: 16 rows' fragments in different banks
+  __shared__ __attribute__((aligned(16))) float sDelta[kQ];
+  __shared__ __attribute__((aligned(16))) float sCs[kQ];   // Delta A summed from the piece's first step
+  __shared__ __attribute__((aligned(16))) float sWp[kQ];   // exp(piece's end - cs_j) Delta_j
+  __shared__ float sTot[4];
+  __shared__ __attribute__((aligned(16))) uint16_t sX[kTwo ? 2 : 1][kQ * kP];
+  __shared__ __attribute__((aligned(16))) uint16_t sE[2][kP * kHS];
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  const int lb = (int)xcd_logical_block();  // the heads of one chunk share its C and CB in an XCD's L2
+  const int h = lb % p.nheads, place = lb / p.nheads;
+  const SeqChunk q = find_chunk<kLogQ>(p.cu, p.nseqs, p.tokens, place);
+  if (q.chunk < 0 || q.chunk * kQ >= q.len) return;
+  const int left = q.len - q.chunk * kQ, rows = left < kQ ? left : kQ;
+  const int64_t row0 = q.begin + (int64_t)q.chunk * kQ;
+  const int g = h / (p.nheads / p.ngroups);
+  const int64_t xrow = p.x_stride * 2, crow = p.c_stride * 2;
+  const int half = wave / 4;
+  const int blk[2] = {wave % 4, 7 - wave % 4};
+  const int ir[2] = {32 * blk[0] + 16 * half, 32 * blk[1] + 16 * half};  // first row of each block
+
+  // ---- prologue: every operand's load, then the sums, then LDS
+  const auto xv = rows_view(static_cast<const char*>(p.x) + row0 * xrow + h * kP * 2, xrow, rows);
+  u32x4v xr[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) xr[k] = vload16(xv, (uint32_t)((tid / 8 + 64 * k) * xrow + (tid % 8) * 16));
+  const f32x4* E = reinterpret_cast<const f32x4*>(p.ws_state + ((int64_t)place * p.nheads + h) * (kP * N));
+  f32x4 er[N / 32];
+#pragma unroll
+  for (int k = 0; k < N / 32; ++k) er[k] = E[tid + kScanThreads * k];
+  const bool in = tid < rows;
+  const float delta = in ? step_size<IO>(p, load_io<IO>(p.dt, (row0 + tid) * p.dt_stride + h), h) : 0.0f;
+  const auto cv = rows_view(static_cast<const char*>(p.Cm) + row0 * crow + g * N * 2, crow, rows);
+  u32x4v cf[2][N / 32];
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int ks = 0; ks < N / 32; ++ks)
+      cf[b][ks] = vload16(cv, (uint32_t)((ir[b] + lane % 16) * crow + (32 * ks + 8 * (lane / 16)) * 2));
+  if (tid < kQ) {
+    float v = delta * p.A[h];
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const float o = __shfl_up(v, off, 64);
+      if (lane >= off) v += o;
+    }
+    const float tot = __shfl(v, 63, 64);
+    sDelta[tid] = delta;
+    sCs[tid] = v;
+    sWp[tid] = exp2_hw((tot - v) * kLog2e) * delta;
+    if (lane == 63) sTot[wave] = v;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int at = tm_off<kP>(tid / 8 + 64 * k, 8 * (tid % 8));
+    if constexpr (kTwo) {
+      u32x4v hi, lo;
+      split8<IO>(xr[k], hi, lo);
+      *reinterpret_cast<u32x4v*>(&sX[0][at]) = hi;
+      *reinterpret_cast<u32x4v*>(&sX[kTwo ? 1 : 0][at]) = lo;
+    } else {
+      *reinterpret_cast<u32x4v*>(&sX[0][at]) = xr[k];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < N / 32; ++k) {
+    const int item = 4 * (tid + kScanThreads * k);  // E[item / N][item % N ..]
+    const int at = (item / N) * kHS + item % N;
+    uint32_t a0, a1, b0, b1;
+    split2(er[k][0], er[k][1], a0, b0);
+    split2(er[k][2], er[k][3], a1, b1);
+    *reinterpret_cast<uint2*>(&sE[0][at]) = make_uint2(a0, a1);
+    *reinterpret_cast<uint2*>(&sE[1][at]) = make_uint2(b0, b1);
+  }
+  __syncthreads();
+  // sums over the whole pieces before each piece
+  float before[4];
+  before[0] = 0.0f;
+#pragma unroll
+  for (int k = 1; k < 4; ++k) before[k] = before[k - 1] + sTot[k - 1];
+
+  // ---- Y_off = E C^T, scaled by exp(cs_i)
+  f32x4 acc[2][4];  // [block][p tile]: p = 16 pt + 4 (lane / 16) + r, i = ir + lane % 16
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int pt = 0; pt < 4; ++pt) acc[b][pt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int ks = 0; ks < N / 32; ++ks) {
+    u32x4v ch[2], cl[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if constexpr (kTwo) split8<IO>(cf[b][ks], ch[b], cl[b]);
+      else ch[b] = cf[b][ks];
+    }
+#pragma unroll
+    for (int pt = 0; pt < 4; ++pt) {
+      const int at = (16 * pt + lane % 16) * kHS + 32 * ks + 8 * (lane / 16);
+      const bf16x8 eh = bfv(*reinterpret_cast<const u32x4v*>(&sE[0][at]));
+      const bf16x8 el = bfv(*reinterpret_cast<const u32x4v*>(&sE[1][at]));
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        acc[b][pt] = BF::run(el, bfv(ch[b]), acc[b][pt]);
+        if constexpr (kTwo) acc[b][pt] = BF::run(eh, bfv(cl[b]), acc[b][pt]);
+        acc[b][pt] = BF::run(eh, bfv(ch[b]), acc[b][pt]);
+      }
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const float bf = blk[b] / 2 == 0 ? before[0] : blk[b] / 2 == 1 ? before[1] : blk[b] / 2 == 2 ? before[2] : before[3];
+    const float sc = exp2_hw((sCs[ir[b] + lane % 16] + bf) * kLog2e);
+#pragma unroll
+    for (int pt = 0; pt < 4; ++pt) acc[b][pt] *= sc;
+  }
+
+  // ---- Y_diag += x^T M^T, piece by piece
+  const float* CB = p.ws_cb + ((int64_t)place * p.ngroups + g) * (kQ * kQ);
+  const auto zv = rows_view(p.z ? static_cast<const char*>(p.z) + row0 * p.z_stride * 2 + h * kP * 2 : nullptr,
+                            p.z_stride * 2, rows);
+  const float Dh = p.D ? p.D[h] : 0.0f;
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    if (ir[b] >= rows) continue;
+    const int i = ir[b] + lane % 16;  // this lane's row
+    const int dpiece = blk[b] / 2;    // the piece that holds it
+    const float csi = sCs[i];
+    const float* cb = CB + cb_at(ir[b] / 16, 0) + lane * 8;
+    uint2 zr[4];
+#pragma unroll
+    for (int pt = 0; pt < 4; ++pt)
+      zr[pt] = vload8(zv, (uint32_t)(i * p.z_stride * 2 + (16 * pt + 4 * (lane / 16)) * 2));
+    f32x4 cur[2][2], nxt[2][2];
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) cur[ks][e] = *reinterpret_cast<const f32x4*>(cb + ks * 512 + 4 * e);
+    for (int piece = 0; piece <= dpiece; ++piece) {
+      const int jb = kJB * piece;
+      if (piece < dpiece) {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            nxt[ks][e] = *reinterpret_cast<const f32x4*>(cb + (2 * piece + 2 + ks) * 512 + 4 * e);
+      }
+      const bool diag = piece == dpiece;
+      float between = csi;  // Delta A from the end of this piece to row i
+      for (int k = piece + 1; k < dpiece; ++k) between += sTot[k];
+      const float ei = exp2_hw(between * kLog2e);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const int j0 = jb + 32 * ks + 8 * (lane / 16);
+        float m[8];
+        if (diag) {
+          const f32x4 c0 = *reinterpret_cast<const f32x4*>(&sCs[j0]), c1 = *reinterpret_cast<const f32x4*>(&sCs[j0 + 4]);
+          const f32x4 d0 = *reinterpret_cast<const f32x4*>(&sDelta[j0]),
+                      d1 = *reinterpret_cast<const f32x4*>(&sDelta[j0 + 4]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float csj = e < 4 ? c0[e & 3] : c1[e & 3], dj = e < 4 ? d0[e & 3] : d1[e & 3];
+            const float v = cur[ks][e / 4][e & 3] * exp2_hw((csi - csj) * kLog2e) * dj;
+            m[e] = j0 + e <= i ? v : 0.0f;
+          }
+        } else {
+          const f32x4 w0 = *reinterpret_cast<const f32x4*>(&sWp[j0]), w1 = *reinterpret_cast<const f32x4*>(&sWp[j0 + 4]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m[e] = cur[ks][e / 4][e & 3] * ((e < 4 ? w0[e & 3] : w1[e & 3]) * ei);
+        }
+        u32x4v mh, ml;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t a, c;
+          split2(m[2 * e], m[2 * e + 1], a, c);
+          mh[e] = a;
+          ml[e] = c;
+        }
+#pragma unroll
+        for (int pt = 0; pt < 4; ++pt) {  // A[m = p][k = step] = x^T, from the time-major tile
+          const int o0 = tm_lane_off<kP>(16 * pt, 0, lane), o1 = tm_lane_off<kP>(16 * pt, 1, lane);
+          const bf16x8 xh = bfv(tm_frag(&sX[0][(jb + 32 * ks) * kP], o0, o1));
+          acc[b][pt] = BF::run(xh, bfv(ml), acc[b][pt]);
+          if constexpr (kTwo) {
+            const bf16x8 xl = bfv(tm_frag(&sX[kTwo ? 1 : 0][(jb + 32 * ks) * kP], o0, o1));
+            acc[b][pt] = BF::run(xl, bfv(mh), acc[b][pt]);
+          }
+          acc[b][pt] = BF::run(xh, bfv(mh), acc[b][pt]);
+        }
+      }
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) cur[ks][e] = nxt[ks][e];
+    }
+    // ---- D skip, gate, store
+    if (i < rows) {
+      char* y = static_cast<char*>(p.y) + ((row0 + i) * p.nheads + h) * (int64_t)(kP * 2);
+#pragma unroll
+      for (int pt = 0; pt < 4; ++pt) {
+        const int p0 = 16 * pt + 4 * (lane / 16);
+        const uint2 xw = *reinterpret_cast<const uint2*>(&sX[0][tm_off<kP>(i, p0)]);
+        float x[4] = {__uint_as_float(xw.x << 16), __uint_as_float(xw.x & 0xffff0000u), __uint_as_float(xw.y << 16),
+                      __uint_as_float(xw.y & 0xffff0000u)};
+        if constexpr (kTwo) {
+          const uint2 lw = *reinterpret_cast<const uint2*>(&sX[kTwo ? 1 : 0][tm_off<kP>(i, p0)]);
+          x[0] += __uint_as_float(lw.x << 16);
+          x[1] += __uint_as_float(lw.x & 0xffff0000u);
+          x[2] += __uint_as_float(lw.y << 16);
+          x[3] += __uint_as_float(lw.y & 0xffff0000u);
+        }
+        float o[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[r] = fmaf(Dh, x[r], acc[b][pt][r]);
+        if (p.z) {
+          o[0] *= silu_f(low16<IO>(zr[pt].x));
+          o[1] *= silu_f(high16<IO>(zr[pt].x));
+          o[2] *= silu_f(low16<IO>(zr[pt].y));
+          o[3] *= silu_f(high16<IO>(zr[pt].y));
+        }
+        *reinterpret_cast<uint2*>(y + p0 * 2) = make_uint2(pack2<IO>(o[0], o[1]), pack2<IO>(o[2], o[3]));
+      }
+    }
+  }
+}
+
+template <int IO, int N>
+hipError_t launch_prompt_n(const SsdPromptParams& p, hipStream_t st) {
+  const uint32_t chunks = (uint32_t)p.chunks, heads = (uint32_t)p.nheads;
+  hipLaunchKernelGGL((prompt_state_kernel<IO, N>), dim3(chunks * heads + chunks * (uint32_t)p.ngroups * 4), dim3(256), 0,
+                     st, p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((prompt_pass_kernel<N>), dim3((uint32_t)p.nseqs * heads * (kP * N / 1024)), dim3(256), 0, st, p);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((prompt_scan_kernel<IO, N>), dim3(chunks * heads), dim3(kScanThreads), 0, st, p);
+  return hipGetLastError();
+}
+template <int IO>
+hipError_t launch_prompt_io(const SsdPromptParams& p, hipStream_t st) {
+  switch (p.dstate) {
+    case 32: return launch_prompt_n<IO, 32>(p, st);
+    case 64: return launch_prompt_n<IO, 64>(p, st);
+    case 96: return launch_prompt_n<IO, 96>(p, st);
+    default: return launch_prompt_n<IO, 128>(p, st);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_ssd_prompt(const SsdPromptParams& p, hipStream_t st) {
+  return p.io == SS_F16 ? launch_prompt_io<SS_F16>(p, st) : launch_prompt_io<SS_BF16>(p, st);
+}
+
+}  // namespace ss

@@ -37,13 +37,37 @@ class ss_ssd_problem(ctypes.Structure):
                 ("io_dtype", ctypes.c_int32), ("dt_softplus", ctypes.c_int32)]
 
 
+class ss_conv_prompt_problem(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("nseqs", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("nslots", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+                ("width", ctypes.c_int32), ("io_dtype", ctypes.c_int32), ("silu", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class ss_ssd_prompt_problem(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("nseqs", ctypes.c_int64), ("nslots", ctypes.c_int64),
+                ("nheads", ctypes.c_int64), ("ngroups", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("b_stride", ctypes.c_int64), ("c_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64),
+                ("dt_stride", ctypes.c_int64), ("headdim", ctypes.c_int32), ("dstate", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("dt_softplus", ctypes.c_int32)]
+
+
+class ss_ssd_step_problem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("nslots", ctypes.c_int64), ("nheads", ctypes.c_int64),
+                ("ngroups", ctypes.c_int64), ("xbc_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64),
+                ("dt_stride", ctypes.c_int64), ("headdim", ctypes.c_int32), ("dstate", ctypes.c_int32),
+                ("width", ctypes.c_int32), ("io_dtype", ctypes.c_int32), ("dt_softplus", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 _vp = ctypes.c_void_p
 _lib = None
 
 # every symbol declared in include/ss.h
 EXPORTS = ("ss_fwd", "ss_fwd_step", "ss_bwd", "ss_fwd_workspace_size", "ss_fwd_workspace_min", "ss_bwd_workspace_size",
            "ss_ckpt_count", "ss_status_str", "ss_copy_probe", "ss_alu_probe", "ss_conv1d_fwd", "ss_conv1d_step",
-           "ss_ssd_fwd", "ss_ssd_workspace_size", "ss_fwd_noalloc", "ss_fwd_noalloc_max_workspace")
+           "ss_ssd_fwd", "ss_ssd_workspace_size", "ss_fwd_noalloc", "ss_fwd_noalloc_max_workspace", "ss_conv1d_prompt",
+           "ss_ssd_prompt", "ss_ssd_prompt_workspace_size", "ss_ssd_step", "ss_ssd_step_workspace_size")
 PROBE_KINDS = {"fma": 0, "exp": 1, "dpp_mul": 2, "scan_step": 3}
 
 
@@ -87,6 +111,19 @@ def load_library(path: str = LIB_PATH):
     lib.ss_ssd_workspace_size.argtypes = [SP]
     lib.ss_ssd_fwd.restype = ctypes.c_int
     lib.ss_ssd_fwd.argtypes = [SP] + [_vp] * 12 + [_vp, ctypes.c_size_t, _vp]
+    VP = ctypes.POINTER(ss_conv_prompt_problem)
+    lib.ss_conv1d_prompt.restype = ctypes.c_int
+    lib.ss_conv1d_prompt.argtypes = [VP] + [_vp] * 8 + [_vp]
+    RP = ctypes.POINTER(ss_ssd_prompt_problem)
+    lib.ss_ssd_prompt_workspace_size.restype = ctypes.c_size_t
+    lib.ss_ssd_prompt_workspace_size.argtypes = [RP]
+    lib.ss_ssd_prompt.restype = ctypes.c_int
+    lib.ss_ssd_prompt.argtypes = [RP] + [_vp] * 13 + [_vp, ctypes.c_size_t, _vp]
+    TP = ctypes.POINTER(ss_ssd_step_problem)
+    lib.ss_ssd_step_workspace_size.restype = ctypes.c_size_t
+    lib.ss_ssd_step_workspace_size.argtypes = [TP]
+    lib.ss_ssd_step.restype = ctypes.c_int
+    lib.ss_ssd_step.argtypes = [TP] + [_vp] * 12 + [_vp, ctypes.c_size_t, _vp]
     lib.ss_copy_probe.restype = ctypes.c_int
     lib.ss_copy_probe.argtypes = [_vp, _vp, ctypes.c_size_t, _vp]
     lib.ss_alu_probe.restype = ctypes.c_int
@@ -485,6 +522,226 @@ def ssd_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, dt_softplus=True, h0
                           _ptr(dt_bias), _ptr(seq_idx), _ptr(h0), _ptr(y), _ptr(fin), _ptr(workspace), wsz,
                           _stream(x.device)))
     return (y, fin) if return_final_state else y
+
+
+def _rows(t, dtype, name, shape, vector=True):
+    """(tensor, elements between rows) for an operand whose rows (shape[1:]) lie whole but possibly
+    apart, such as the columns of a projection's output; copied only where they do not, or where
+    vector access needs rows on 16-byte boundaries and they are not."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    size = 1
+    whole = True
+    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        whole = whole and (n == 1 or st == size)
+        size *= n
+    stride = t.stride(0) if t.shape[0] > 1 else size
+    if not whole or stride < size or stride > 1 << 21 or \
+            (vector and (t.data_ptr() % 16 or stride * t.element_size() % 16)):
+        t, stride = t.contiguous(), size
+        if vector and t.data_ptr() % 16:
+            t = t.clone()
+    return t, stride
+
+
+def _inplace(t, dtype, name, shape):
+    """A tensor that the call writes: taken as it is or refused, never copied."""
+    if t is None:
+        return None
+    if not (t.is_cuda and t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous()
+            and t.data_ptr() % 16 == 0):
+        raise ValueError("%s must be a contiguous, 16-byte aligned %s device tensor of shape %s"
+                         % (name, dtype, tuple(shape)))
+    return t
+
+
+def _on(device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError("all tensors must be on %s, got one on %s" % (device, t.device))
+
+
+def _launch(device, fn, *args):
+    """The C call on the current stream of the tensors' device, whichever device is current."""
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _stream(device))
+    if status != 0:
+        _check(status)
+
+
+def _scratch(workspace, nbytes, device):
+    """The given workspace (the library checks its size), or a new one."""
+    if workspace is None:
+        workspace = torch.empty((nbytes + 3) // 4, dtype=torch.float32, device=device)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def conv1d_prompt(x, w, cu_seqlens, conv_state, bias=None, silu=True, slots=None, has_state=None, out=None):
+    """Depthwise causal conv1d (+ SiLU) of packed prompts, time-major.  x: (T, D) fp32/fp16/bf16, rows
+    may lie apart (a slice of the projection's output); w: (D, W) fp32; bias: (D,) fp32; cu_seqlens:
+    (S + 1,) int32 row offsets of the prompts; conv_state: (slots, D, W-1) fp32, the windows, updated
+    in place; slots: (S,) int32 slot of each prompt (default: its index; outside the pool: none);
+    has_state: (S,) int32, nonzero where a prompt continues from its window (default: none does).
+    Returns out (T, D); rows of no prompt are not written (pass out to keep them)."""
+    lib = load_library()
+    io = x.dtype
+    if io not in _IO:
+        raise TypeError("unsupported dtype %s" % io)
+    T, Dd = x.shape
+    W, S = w.shape[-1], cu_seqlens.numel() - 1
+    x, xs = _rows(x, io, "x", (T, Dd), vector=False)
+    w = _prep(w.reshape(Dd, W), torch.float32, "w", (Dd, W))
+    bias = _prep(bias, torch.float32, "bias", (Dd,))
+    cu_seqlens = _prep(cu_seqlens, torch.int32, "cu_seqlens", (S + 1,))
+    slots = _prep(slots, torch.int32, "slots", (S,))
+    has_state = _prep(has_state, torch.int32, "has_state", (S,))
+    nslots = conv_state.shape[0]
+    conv_state = _inplace(conv_state, torch.float32, "conv_state", (nslots, Dd, W - 1))
+    if out is None:
+        out, os_ = torch.empty((T, Dd), dtype=io, device=x.device), Dd
+    else:
+        given = out
+        out, os_ = _rows(out, io, "out", (T, Dd), vector=False)
+        if out is not given:
+            raise ValueError("the rows of out must lie whole, at most 2^21 elements apart")
+    _on(x.device, w, bias, cu_seqlens, slots, has_state, conv_state, out)
+    pr = ss_conv_prompt_problem(T, S, Dd, nslots, xs, os_, W, _IO[io], 1 if silu else 0, 0)
+    _launch(x.device, lib.ss_conv1d_prompt, ctypes.byref(pr), _ptr(x), _ptr(w), _ptr(bias), _ptr(cu_seqlens),
+            _ptr(slots), _ptr(has_state), _ptr(conv_state) if W > 1 else None, _ptr(out))
+    return out
+
+
+def ssd_prompt(x, dt, A, Bm, Cm, cu_seqlens, state, D=None, z=None, dt_bias=None, dt_softplus=True, slots=None,
+               has_state=None, y=None, workspace=None):
+    """Mamba-2 SSD scan of packed prompts from and into state slots.  x, z: (T, H, 64); dt: (T, H);
+    Bm, Cm: (T, G, N) in fp16 or bf16, tokens may lie apart (slices of the convolution's output);
+    A, D, dt_bias: (H,) fp32; cu_seqlens, slots, has_state as in conv1d_prompt; state: (slots, H, 64, N)
+    fp32, updated in place.  Returns y (T, H, 64); rows of no prompt are not written."""
+    lib = load_library()
+    io = x.dtype
+    if io not in (torch.float16, torch.bfloat16):
+        raise TypeError("ssd_prompt takes fp16 or bf16 data, got %s" % io)
+    T, Hn, P = x.shape
+    G, N, S = Bm.shape[1], Bm.shape[2], cu_seqlens.numel() - 1
+    x, xs = _rows(x, io, "x", (T, Hn, P))
+    z, zs = _rows(z, io, "z", (T, Hn, P))
+    Bm, bs = _rows(Bm, io, "Bm", (T, G, N))
+    Cm, cs = _rows(Cm, io, "Cm", (T, G, N))
+    dt, ds = _rows(dt, io, "dt", (T, Hn), vector=False)
+    A = _prep(A, torch.float32, "A", (Hn,))
+    D = _prep(D, torch.float32, "D", (Hn,))
+    dt_bias = _prep(dt_bias, torch.float32, "dt_bias", (Hn,))
+    cu_seqlens = _prep(cu_seqlens, torch.int32, "cu_seqlens", (S + 1,))
+    slots = _prep(slots, torch.int32, "slots", (S,))
+    has_state = _prep(has_state, torch.int32, "has_state", (S,))
+    nslots = state.shape[0]
+    state = _inplace(state, torch.float32, "state", (nslots, Hn, P, N))
+    y = torch.empty((T, Hn, P), dtype=io, device=x.device) if y is None else _inplace(y, io, "y", (T, Hn, P))
+    _on(x.device, z, Bm, Cm, dt, A, D, dt_bias, cu_seqlens, slots, has_state, state, y, workspace)
+    pr = ss_ssd_prompt_problem(T, S, nslots, Hn, G, xs, bs, cs, zs, ds, P, N, _IO[io], 1 if dt_softplus else 0)
+    workspace, wsz = _scratch(workspace, lib.ss_ssd_prompt_workspace_size(ctypes.byref(pr)), x.device)
+    _launch(x.device, lib.ss_ssd_prompt, ctypes.byref(pr), _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D),
+            _ptr(z), _ptr(dt_bias), _ptr(cu_seqlens), _ptr(slots), _ptr(has_state), _ptr(state), _ptr(y),
+            _ptr(workspace), wsz)
+    return y
+
+
+def _step_problem(xbc, state, w, ngroups, xs, zs, ds, dt_softplus):
+    nslots, Hn, P, N = state.shape
+    return ss_ssd_step_problem(xbc.shape[0], nslots, Hn, ngroups, xs, zs, ds, P, N, w.shape[-1], _IO[xbc.dtype],
+                               1 if dt_softplus else 0, 0)
+
+
+def ssd_step(xbc, dt, A, conv_w, conv_state, state, ngroups=1, conv_bias=None, D=None, z=None, dt_bias=None,
+             dt_softplus=True, slots=None, y=None, workspace=None):
+    """One token of many requests through a Mamba-2 layer's convolution and scan, over state slots.
+    xbc: (n, H*64 + 2*G*N) fp16/bf16, the channels of x, B and C before the convolution; dt: (n, H);
+    z: (n, H, 64); all three rows may lie apart; conv_w: (channels, W) fp32; conv_bias: (channels,) fp32;
+    conv_state: (slots, channels, W-1) fp32 and state: (slots, H, 64, N) fp32, updated in place; slots:
+    (n,) int32 slot of each row (default: its index; outside the pool, -1 say: the row is skipped).
+    Returns y (n, H, 64)."""
+    lib = load_library()
+    io = xbc.dtype
+    if io not in (torch.float16, torch.bfloat16):
+        raise TypeError("ssd_step takes fp16 or bf16 data, got %s" % io)
+    n = xbc.shape[0]
+    nslots, Hn, P, N = state.shape
+    ch, W = Hn * P + 2 * ngroups * N, conv_w.shape[-1]
+    xbc, xs = _rows(xbc, io, "xbc", (n, ch), vector=False)
+    dt, ds = _rows(dt, io, "dt", (n, Hn), vector=False)
+    z, zs = _rows(z, io, "z", (n, Hn, P), vector=False)
+    A = _prep(A, torch.float32, "A", (Hn,))
+    D = _prep(D, torch.float32, "D", (Hn,))
+    dt_bias = _prep(dt_bias, torch.float32, "dt_bias", (Hn,))
+    conv_w = _prep(conv_w.reshape(ch, W), torch.float32, "conv_w", (ch, W))
+    conv_bias = _prep(conv_bias, torch.float32, "conv_bias", (ch,))
+    slots = _prep(slots, torch.int32, "slots", (n,))
+    conv_state = _inplace(conv_state, torch.float32, "conv_state", (nslots, ch, W - 1))
+    state = _inplace(state, torch.float32, "state", (nslots, Hn, P, N))
+    y = torch.empty((n, Hn, P), dtype=io, device=xbc.device) if y is None else _inplace(y, io, "y", (n, Hn, P))
+    _on(xbc.device, dt, z, A, D, dt_bias, conv_w, conv_bias, slots, conv_state, state, y, workspace)
+    pr = _step_problem(xbc, state, conv_w, ngroups, xs, zs, ds, dt_softplus)
+    workspace, wsz = _scratch(workspace, lib.ss_ssd_step_workspace_size(ctypes.byref(pr)), xbc.device)
+    _launch(xbc.device, lib.ss_ssd_step, ctypes.byref(pr), _ptr(xbc), _ptr(dt), _ptr(A), _ptr(conv_w),
+            _ptr(conv_bias), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(slots), _ptr(conv_state) if W > 1 else None,
+            _ptr(state), _ptr(y), _ptr(workspace), wsz)
+    return y
+
+
+class SsdStepCall:
+    """ssd_step validated once and replayed with one C call per launch (the serving pattern of StepCall:
+    preallocated token, slot and output buffers refilled in place; the tensors must stay alive and
+    unmoved).  Takes its operands as they are: rows whole, weights contiguous."""
+
+    def __init__(self, xbc, dt, A, conv_w, conv_state, state, y, ngroups=1, conv_bias=None, D=None, z=None,
+                 dt_bias=None, dt_softplus=True, slots=None, stream=None):
+        lib = load_library()
+        io = xbc.dtype
+        if io not in (torch.float16, torch.bfloat16):
+            raise TypeError("ssd_step takes fp16 or bf16 data, got %s" % io)
+        n = xbc.shape[0]
+        nslots, Hn, P, N = state.shape
+        ch, W = Hn * P + 2 * ngroups * N, conv_w.shape[-1]
+        strides = []
+        for t, name, shape in ((xbc, "xbc", (n, ch)), (z, "z", (n, Hn, P)), (dt, "dt", (n, Hn))):
+            same, st = _rows(t, io, name, shape, vector=False)
+            if same is not t:
+                raise ValueError("the rows of %s must lie whole, at most 2^21 elements apart" % name)
+            strides.append(st)
+        for t, dtype, name, shape in ((A, torch.float32, "A", (Hn,)), (D, torch.float32, "D", (Hn,)),
+                                      (dt_bias, torch.float32, "dt_bias", (Hn,)),
+                                      (conv_w, torch.float32, "conv_w", (ch, W)),
+                                      (conv_bias, torch.float32, "conv_bias", (ch,)),
+                                      (slots, torch.int32, "slots", (n,)),
+                                      (conv_state, torch.float32, "conv_state", (nslots, ch, W - 1)),
+                                      (state, torch.float32, "state", (nslots, Hn, P, N)), (y, io, "y", (n, Hn, P))):
+            _inplace(t, dtype, name, shape)
+        if y is None:
+            raise ValueError("SsdStepCall needs its output y")
+        _on(xbc.device, dt, z, A, D, dt_bias, conv_w, conv_bias, slots, conv_state, state, y)
+        self.pr = _step_problem(xbc, state, conv_w, ngroups, *strides, dt_softplus)
+        self.device = xbc.device
+        self.ws, wsz = _scratch(None, lib.ss_ssd_step_workspace_size(ctypes.byref(self.pr)), xbc.device)
+        self.keep = (xbc, dt, A, conv_w, conv_bias, D, z, dt_bias, slots, conv_state, state, y)
+        st = stream if stream is not None else torch.cuda.current_stream(xbc.device)
+        self.args = (ctypes.byref(self.pr), _ptr(xbc), _ptr(dt), _ptr(A), _ptr(conv_w), _ptr(conv_bias), _ptr(D),
+                     _ptr(z), _ptr(dt_bias), _ptr(slots), _ptr(conv_state) if W > 1 else None, _ptr(state), _ptr(y),
+                     _ptr(self.ws), wsz, ctypes.c_void_p(st.cuda_stream))
+        self.fn = lib.ss_ssd_step
+
+    def __call__(self):
+        status = self.fn(*self.args)
+        if status != 0:
+            _check(status)
 
 
 def copy_probe(src, dst):
