@@ -295,6 +295,29 @@ ss_status ss_conv1d_step(const ss_conv_problem *p, const void *x_t, const float 
                          const float *window_in, float *window_out, void *out_t, void *stream);
 
 /*
+ * Gradients of ss_conv1d_fwd for the loss sum(dout * out) +
+ * sum(dconv_final * conv_final); p, x, w, bias, seq_idx and conv_init are the
+ * forward's.
+ *   dout, dx    : (batch, dim, seqlen) io dtype
+ *   dw          : (dim, W) fp32;  dbias: (dim) fp32, given iff bias is
+ *   dconv_final : optional (batch, dim, W-1) fp32 (NULL = zero)
+ *   dconv_init  : optional (batch, dim, W-1) fp32 output, the gradient w.r.t.
+ *                 the inputs before t = 0 (also where conv_init is NULL)
+ *   workspace   : ss_conv1d_bwd_workspace_size() bytes (NULL when that is 0);
+ *                 its contents on entry do not matter
+ * Every output is overwritten; sums have a fixed order.  Returns
+ * SS_ERR_NULL_ARG when dbias and bias are not given together,
+ * SS_ERR_UNSUPPORTED when the workspace is missing or too small or when an
+ * output or the workspace overlaps any other buffer (no in-place).
+ */
+size_t ss_conv1d_bwd_workspace_size(const ss_conv_problem *p);
+
+ss_status ss_conv1d_bwd(const ss_conv_problem *p, const void *x, const float *w, const float *bias,
+                        const int32_t *seq_idx, const float *conv_init, const void *dout,
+                        const float *dconv_final, void *dx, float *dw, float *dbias, float *dconv_init,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * ---- Mamba-2 SSD chunked scan ----------------------------------------------
  * Page "Mamba" (walkthrough), "Deep dive: Mamba-2 and state-space duality":
  * A is a scalar per head and a group of heads shares B and C.  Per batch row
@@ -349,6 +372,35 @@ size_t ss_ssd_workspace_size(const ss_ssd_problem *p);
 ss_status ss_ssd_fwd(const ss_ssd_problem *p, const void *x, const void *dt, const float *A,
                      const void *Bm, const void *Cm, const float *D, const void *z, const float *dt_bias,
                      const int32_t *seq_idx, const float *h0, void *y, float *final_state,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of ss_ssd_fwd for the loss sum(dy * y) + sum(dfinal *
+ * final_state); p and the inputs are the forward's.  The states are rebuilt,
+ * nothing of the forward is needed but its inputs.
+ *   dx, dz  : (batch, seqlen, nheads, 64) io dtype;  ddt: (batch, seqlen, nheads) io dtype
+ *   dB, dC  : (batch, seqlen, ngroups, dstate) io dtype, summed over a group's heads in fp32
+ *   dA, dD, ddt_bias : (nheads) fp32, summed over batch and time
+ *   dfinal  : optional (batch, nheads, 64, dstate) fp32 (NULL = zero)
+ *   dh0     : optional (batch, nheads, 64, dstate) fp32 output, the gradient
+ *             w.r.t. the initial state (also where h0 is NULL)
+ *   workspace : ss_ssd_bwd_workspace_size(p, z is given) bytes; its contents on
+ *             entry do not matter
+ * dz is given iff z is, dD iff D, ddt_bias iff dt_bias (SS_ERR_NULL_ARG).
+ * Every output is overwritten; sums have a fixed order.  Computed operands are
+ * multiplied as sums of bf16 parts and states kept in fp32, so that
+ * gradients carry nearly fp32's error (those in the io dtype before their
+ * rounding).
+ * Other errors as ss_ssd_fwd; no output or workspace may overlap any other
+ * buffer (SS_ERR_UNSUPPORTED).  As in the forward, a value that is not finite
+ * spreads within its row.
+ */
+size_t ss_ssd_bwd_workspace_size(const ss_ssd_problem *p, int32_t gated);
+
+ss_status ss_ssd_bwd(const ss_ssd_problem *p, const void *x, const void *dt, const float *A, const void *Bm,
+                     const void *Cm, const float *D, const void *z, const float *dt_bias,
+                     const int32_t *seq_idx, const float *h0, const void *dy, const float *dfinal, void *dx,
+                     void *ddt, float *dA, void *dB, void *dC, float *dD, void *dz, float *ddt_bias, float *dh0,
                      void *workspace, size_t workspace_bytes, void *stream);
 
 /*
@@ -423,8 +475,8 @@ ss_status ss_conv1d_prompt(const ss_conv_prompt_problem *p, const void *x, const
  *   A, D, dt_bias : (nheads) fp32; D and dt_bias may be NULL
  * Strides of x, z, Bm and Cm are multiples of 8; pointers are 16-byte aligned
  * but for dt's, which is aligned to the element.  Outputs and states carry
- * fp32's error (y before its rounding): computed operands are multiplied as
- * pairs of bf16 values.  A value that is not finite spreads to other steps of
+ * nearly fp32's error (y before its rounding): computed operands are
+ * multiplied as sums of bf16 parts.  A value that is not finite spreads to other steps of
  * the same 256-step chunk of its sequence, earlier ones among them, and to no
  * other sequence.
  */

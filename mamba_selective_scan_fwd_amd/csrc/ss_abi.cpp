@@ -20,6 +20,7 @@ constexpr int64_t kTargetWaves = 1024;
 // fits the 32-bit grid size of a dispatch
 constexpr int64_t kMaxGrid = ((int64_t)1 << 23) - 1;
 constexpr int64_t kMaxSeqlen = (int64_t)1 << 24;
+constexpr int64_t kConvBwdGroups = 4096;  // workgroups of the convolution's backward, where the sizes allow
 
 bool aligned(const void* ptr) { return ((uintptr_t)ptr & 15u) == 0; }
 
@@ -437,6 +438,59 @@ ss_status ss_conv1d_step(const ss_conv_problem* p, const void* x_t, const float*
 }
 
 namespace {
+// workgroups per channel of the convolution's backward: enough for two per
+// resident slot of the GPU, each with at least one unit of 256 chunks
+int64_t conv_bwd_parts(const ss_conv_problem* p) {
+  const int64_t units = ss::conv_bwd_units(p->batch, p->seqlen);
+  const int64_t want = (kConvBwdGroups + p->dim - 1) / p->dim;
+  return want < units ? want : units;
+}
+ss_status check_conv_bwd(const ss_conv_problem* p) {
+  const ss_status s = check_conv(p, true);
+  if (s != SS_OK) return s;
+  if (p->dim > kMaxGrid || p->dim * conv_bwd_parts(p) > kMaxGrid) return SS_ERR_BAD_SHAPE;
+  return SS_OK;
+}
+}  // namespace
+
+size_t ss_conv1d_bwd_workspace_size(const ss_conv_problem* p) {
+  if (check_conv_bwd(p) != SS_OK) return 0;
+  const int64_t parts = conv_bwd_parts(p);
+  return parts > 1 ? (size_t)(parts * p->dim * (p->width + 1)) * sizeof(float) : 0;
+}
+
+ss_status ss_conv1d_bwd(const ss_conv_problem* p, const void* x, const float* w, const float* bias,
+                        const int32_t* seq_idx, const float* conv_init, const void* dout, const float* dconv_final,
+                        void* dx, float* dw, float* dbias, float* dconv_init, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  const ss_status s = check_conv_bwd(p);
+  if (s != SS_OK) return s;
+  if (!x || !w || !dout || !dx || !dw || (bias == nullptr) != (dbias == nullptr)) return SS_ERR_NULL_ARG;
+  const void* ptrs[] = {x, w, bias, seq_idx, conv_init, dout, dconv_final, dx, dw, dbias, dconv_init, workspace};
+  for (const void* q : ptrs)
+    if (q && !aligned(q)) return SS_ERR_MISALIGNED;
+  const size_t need = ss_conv1d_bwd_workspace_size(p);
+  if (need && (!workspace || workspace_bytes < need)) return SS_ERR_UNSUPPORTED;
+  {
+    const size_t bytes = (size_t)(p->batch * p->dim * p->seqlen * elem_size(p->io_dtype));
+    const size_t win = (size_t)(p->batch * p->dim * (p->width - 1)) * sizeof(float);
+    const size_t wb = (size_t)(p->dim * p->width) * sizeof(float), vb = (size_t)p->dim * sizeof(float);
+    const Span in[] = {{x, bytes}, {w, wb}, {bias, vb}, {seq_idx, (size_t)(p->batch * p->seqlen) * 4},
+                       {conv_init, win}, {dout, bytes}, {dconv_final, win}};
+    const Span outs[] = {{dx, bytes}, {dw, wb}, {dbias, vb}, {dconv_init, win}, {need ? workspace : nullptr, need}};
+    if (conflict(in, outs)) return SS_ERR_UNSUPPORTED;
+  }
+  ss::ConvBwdParams k{};
+  k.io = p->io_dtype; k.width = p->width; k.silu = p->silu != 0; k.parts = (int32_t)conv_bwd_parts(p);
+  k.x = x; k.w = w; k.bias = bias; k.seq_idx = seq_idx; k.conv_init = conv_init; k.dout = dout;
+  k.dconv_final = dconv_final; k.dx = dx; k.dw = dw; k.dbias = dbias; k.dconv_init = dconv_init;
+  k.ws = static_cast<float*>(workspace);
+  k.batch = p->batch; k.dim = p->dim; k.seqlen = p->seqlen;
+  k.units = ss::conv_bwd_units(p->batch, p->seqlen);
+  return from_hip(ss::launch_conv_bwd(k, static_cast<hipStream_t>(stream)));
+}
+
+namespace {
 constexpr int64_t kSsdChunk = 256;
 ss_status check_ssd(const ss_ssd_problem* p) {
   if (!p) return SS_ERR_NULL_ARG;
@@ -523,6 +577,114 @@ ss_status ss_ssd_fwd(const ss_ssd_problem* p, const void* x, const void* dt, con
   k.batch = p->batch; k.seqlen = p->seqlen; k.nheads = p->nheads; k.ngroups = p->ngroups; k.dstate = p->dstate;
   k.nchunks = (p->seqlen + kSsdChunk - 1) / kSsdChunk;
   return from_hip(ss::launch_ssd(k, static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+ss_status check_ssd_bwd(const ss_ssd_problem* p) {
+  const ss_status s = check_ssd(p);
+  if (s != SS_OK) return s;
+  const double places = (double)p->batch * (double)((p->seqlen + kSsdChunk - 1) / kSsdChunk);
+  if (places * (2.0 * (double)p->nheads + 8.0 * (double)p->ngroups) > (double)kMaxGrid) return SS_ERR_BAD_SHAPE;
+  if ((double)p->batch * (double)p->nheads * (p->dstate / 16) > (double)kMaxGrid) return SS_ERR_BAD_SHAPE;
+  return SS_OK;
+}
+// the workspace of the SSD's backward: one piece after the other, each on a
+// 256-byte boundary
+struct SsdBwdLayout {
+  size_t total = 0;
+  size_t take(size_t bytes) {
+    const size_t at = total;
+    total += align256(bytes);
+    return at;
+  }
+  size_t E, R, decay, dot, cb, bc, delta, cs, cl, seg, rowin, colin, row, col, e, out, xg, xd, span, part, x[2], g[3], b[2], c[2];
+};
+SsdBwdLayout ssd_bwd_layout(const ss_ssd_problem* p, bool gated) {
+  const bool f16 = p->io_dtype == SS_F16;
+  const size_t places = (size_t)(p->batch * ((p->seqlen + kSsdChunk - 1) / kSsdChunk));
+  const size_t ph = places * (size_t)p->nheads, st = ph * (size_t)(64 * p->dstate) * 4, q = ph * 256 * 4;
+  const size_t cb = places * (size_t)p->ngroups * (256 * 256) * 4;
+  const size_t rows = (size_t)(p->batch * p->seqlen);
+  const size_t xb = rows * (size_t)p->nheads * 64 * 2, vb = rows * (size_t)(p->ngroups * p->dstate) * 2;
+  SsdBwdLayout l;
+  l.E = l.take(st); l.R = l.take(st); l.decay = l.take(ph * 4); l.dot = l.take(ph * (size_t)p->dstate);
+  l.bc = l.take(cb); l.cb = l.take(gated ? cb : 0);
+  l.delta = l.take(q); l.cs = l.take(q); l.cl = l.take(q); l.seg = l.take(places * 256 * 4);
+  l.rowin = l.take(4 * q); l.colin = l.take(4 * q); l.row = l.take(2 * q); l.col = l.take(2 * q);
+  l.e = l.take(2 * q); l.out = l.take(2 * q); l.xg = l.take(2 * q); l.xd = l.take(2 * q); l.span = l.take(ph * 32 * 4);
+  l.part = l.take(ph * 3 * 4);
+  for (int i = 0; i < 3; ++i) l.g[i] = l.take(gated || (f16 && i < 2) ? xb : 0);
+  for (int i = 0; i < 2; ++i) {
+    l.x[i] = l.take(f16 ? xb : 0);
+    l.b[i] = l.take(f16 ? vb : 0);
+    l.c[i] = l.take(f16 ? vb : 0);
+  }
+  return l;
+}
+}  // namespace
+
+size_t ss_ssd_bwd_workspace_size(const ss_ssd_problem* p, int32_t gated) {
+  if (check_ssd_bwd(p) != SS_OK) return 0;
+  return ssd_bwd_layout(p, gated != 0).total;
+}
+
+ss_status ss_ssd_bwd(const ss_ssd_problem* p, const void* x, const void* dt, const float* A, const void* Bm,
+                     const void* Cm, const float* D, const void* z, const float* dt_bias, const int32_t* seq_idx,
+                     const float* h0, const void* dy, const float* dfinal, void* dx, void* ddt, float* dA, void* dB,
+                     void* dC, float* dD, void* dz, float* ddt_bias, float* dh0, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  const ss_status s = check_ssd_bwd(p);
+  if (s != SS_OK) return s;
+  if (!x || !dt || !A || !Bm || !Cm || !dy || !dx || !ddt || !dA || !dB || !dC) return SS_ERR_NULL_ARG;
+  if ((z == nullptr) != (dz == nullptr) || (D == nullptr) != (dD == nullptr) ||
+      (dt_bias == nullptr) != (ddt_bias == nullptr))
+    return SS_ERR_NULL_ARG;
+  const void* ptrs[] = {x, dt, A, Bm, Cm, D, z, dt_bias, seq_idx, h0, dy, dfinal, dx, ddt, dA, dB, dC,
+                        dD, dz, ddt_bias, dh0, workspace};
+  for (const void* q : ptrs)
+    if (q && !aligned(q)) return SS_ERR_MISALIGNED;
+  const SsdBwdLayout l = ssd_bwd_layout(p, z != nullptr);
+  if (!workspace || workspace_bytes < l.total) return SS_ERR_UNSUPPORTED;
+  {
+    const size_t rows = (size_t)(p->batch * p->seqlen);
+    const size_t xb = rows * (size_t)p->nheads * 64 * 2, dtb = rows * (size_t)p->nheads * 2;
+    const size_t vb = rows * (size_t)(p->ngroups * p->dstate) * 2, nb = (size_t)p->nheads * 4;
+    const size_t hb = (size_t)(p->batch * p->nheads) * 64 * (size_t)p->dstate * 4;
+    const Span in[] = {{x, xb}, {dt, dtb}, {A, nb}, {Bm, vb}, {Cm, vb}, {D, nb}, {z, xb}, {dt_bias, nb},
+                       {seq_idx, rows * 4}, {h0, hb}, {dy, xb}, {dfinal, hb}};
+    const Span outs[] = {{dx, xb}, {ddt, dtb}, {dA, nb}, {dB, vb}, {dC, vb}, {dD, nb}, {dz, xb}, {ddt_bias, nb},
+                         {dh0, hb}, {workspace, l.total}};
+    if (conflict(in, outs)) return SS_ERR_UNSUPPORTED;
+  }
+  char* ws = static_cast<char*>(workspace);
+  auto f32_at = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
+  const bool f16 = p->io_dtype == SS_F16;
+  auto planes = [&](int n, const size_t* at, const void* in, const uint16_t** to) {
+    if (n == 1) to[0] = static_cast<const uint16_t*>(in);
+    else
+      for (int i = 0; i < n; ++i) to[i] = reinterpret_cast<const uint16_t*>(ws + at[i]);
+  };
+  ss::SsdBwdParams k{};
+  k.softplus = p->dt_softplus != 0;
+  k.x = x; k.dt = dt; k.Bm = Bm; k.Cm = Cm; k.z = z; k.dy = dy; k.A = A; k.D = D; k.dt_bias = dt_bias;
+  k.seq_idx = seq_idx; k.h0 = h0; k.dfinal = dfinal;
+  k.dx = dx; k.ddt = ddt; k.dB = dB; k.dC = dC; k.dz = dz; k.dA = dA; k.dD = dD; k.ddt_bias = ddt_bias; k.dh0 = dh0;
+  const int parts = f16 ? 2 : 1;
+  planes(parts, l.x, x, k.xp);
+  planes(z ? 3 : parts, l.g, dy, k.gp);
+  planes(parts, l.b, Bm, k.bp);
+  planes(parts, l.c, Cm, k.cp);
+  k.ws_E = f32_at(l.E); k.ws_R = f32_at(l.R); k.ws_decay = f32_at(l.decay); k.ws_dot = f32_at(l.dot);
+  k.ws_cb = f32_at(l.cb); k.ws_bc = f32_at(l.bc); k.ws_delta = f32_at(l.delta); k.ws_cs = f32_at(l.cs); k.ws_cl = f32_at(l.cl);
+  k.ws_seg = reinterpret_cast<int32_t*>(ws + l.seg);
+  k.ws_rowin = reinterpret_cast<double*>(ws + l.rowin); k.ws_colin = reinterpret_cast<double*>(ws + l.colin);
+  k.ws_e = f32_at(l.e); k.ws_span = f32_at(l.span);
+  k.ws_row = f32_at(l.row); k.ws_col = f32_at(l.col); k.ws_out = f32_at(l.out); k.ws_xg = f32_at(l.xg);
+  k.ws_xd = f32_at(l.xd); k.ws_part = f32_at(l.part);
+  k.batch = p->batch; k.seqlen = p->seqlen;
+  k.nheads = (int32_t)p->nheads; k.ngroups = (int32_t)p->ngroups; k.dstate = p->dstate;
+  k.nchunks = (int32_t)((p->seqlen + kSsdChunk - 1) / kSsdChunk);
+  return from_hip(ss::launch_ssd_bwd(p->io_dtype, k, static_cast<hipStream_t>(stream)));
 }
 
 namespace {

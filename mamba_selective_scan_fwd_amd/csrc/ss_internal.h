@@ -159,6 +159,79 @@ struct SsdParams {
   int64_t batch, seqlen, nheads, ngroups, dstate, nchunks;
 };
 
+struct ConvBwdParams {
+  int32_t io;
+  int32_t width;
+  int32_t silu;
+  int32_t parts;             // workgroups per channel, each with every parts-th unit
+  const void* x;             // (batch, dim, seqlen)
+  const float* w;            // (dim, W)
+  const float* bias;         // (dim) or null
+  const int32_t* seq_idx;    // (batch, seqlen) or null
+  const float* conv_init;    // (batch, dim, W-1) or null
+  const void* dout;
+  const float* dconv_final;  // (batch, dim, W-1) or null
+  void* dx;
+  float* dw;
+  float* dbias;              // or null
+  float* dconv_init;         // or null
+  float* ws;                 // (parts, dim, W+1) partial sums, parts > 1
+  int64_t batch, dim, seqlen, units;
+};
+
+struct SsdBwdParams {
+  int32_t softplus;
+  const void* x;             // (batch, seqlen, nheads, 64)
+  const void* dt;            // (batch, seqlen, nheads)
+  const void* Bm;            // (batch, seqlen, ngroups, dstate)
+  const void* Cm;
+  const void* z;             // like x, or null
+  const void* dy;            // like x
+  const float* A;
+  const float* D;            // or null
+  const float* dt_bias;      // or null
+  const int32_t* seq_idx;    // (batch, seqlen) or null
+  const float* h0;           // (batch, nheads, 64, dstate) or null
+  const float* dfinal;       // like h0, or null
+  void* dx;
+  void* ddt;
+  void* dB;
+  void* dC;
+  void* dz;                  // iff z
+  float* dA;
+  float* dD;                 // iff D
+  float* ddt_bias;           // iff dt_bias
+  float* dh0;                // or null
+  // The matrix cores' operands as planes of bf16 parts (part 0 is the input
+  // itself where the data are bf16; the others null); g is dy silu(z), in three
+  // parts if gated.  Planes that are not inputs lie in the workspace.
+  const uint16_t *xp[2], *gp[3], *bp[2], *cp[2];
+  // workspace; a place is a chunk of a batch row
+  float* ws_E;               // (places, nheads, 64, dstate): a chunk's own state, then the state entering it
+  float* ws_R;               // the same of the gradients: what the chunk adds, then what enters from behind
+  float* ws_decay;           // (places, nheads)
+  float* ws_dot;             // (places, nheads, dstate / 4): parts of decay <R, E>
+  float* ws_cb;              // (places, ngroups, 256 * 256): C B^T in operand order (gated only)
+  float* ws_bc;              // B C^T in operand order
+  float* ws_delta;           // (places, nheads, 256): Delta
+  float* ws_cs;              // (places, nheads, 256): Delta A summed from the start of each 64 steps,
+  float* ws_cl;              // and what that float leaves of the sum
+  int32_t* ws_seg;           // (places, 256): document starts at or before each step (with seq_idx)
+  // (2, places, nheads, 256), one half per half of a workgroup (bwd_group); W, e, r as there:
+  double* ws_rowin;          // W of a step's row with its own 64 steps,
+  double* ws_colin;          // of its column with them,
+  float* ws_row;             // of its row with earlier 64s,
+  float* ws_col;             // of its column with later 64s,
+  float* ws_e;               // e
+  float* ws_out;             // r
+  float* ws_xg;              // x . G B
+  float* ws_xd;              // x . g
+  float* ws_span;            // (places, nheads, 4, 8): parts of W with whole 64s between
+  float* ws_part;            // (places, nheads, 3): parts of dA, ddt_bias, dD
+  int64_t batch, seqlen;
+  int32_t nheads, ngroups, dstate, nchunks;
+};
+
 // Packed sequences: rows cu[s] .. cu[s + 1] - 1 belong to sequence s.
 struct ConvPromptParams {
   int32_t io;
@@ -222,6 +295,9 @@ struct SsdPromptParams {
   int32_t chunks;            // chunk places: tokens / 256 + nseqs
 };
 
+int64_t conv_bwd_units(int64_t batch, int64_t seqlen);
+hipError_t launch_conv_bwd(const ConvBwdParams& p, hipStream_t st);
+hipError_t launch_ssd_bwd(int32_t io, const SsdBwdParams& p, hipStream_t st);
 hipError_t launch_conv_prompt(const ConvPromptParams& p, hipStream_t st);
 hipError_t launch_ssd_step(const SsdStepParams& p, hipStream_t st);
 hipError_t launch_ssd_prompt(const SsdPromptParams& p, hipStream_t st);

@@ -90,4 +90,58 @@ __device__ __forceinline__ u32x4v tm_frag(const uint16_t* at, int off_lo, int of
   return __builtin_bit_cast(u32x4v, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
+// ---- operands as sums of bf16 values -------------------------------------------
+// A computed operand v is split into bf16 parts, each the rounding of what the
+// parts before it leave: |v - p0 - p1| <= 2^-18 |v|, |v - p0 - p1 - p2| <= 2^-27
+// |v|, and multiplied part by part.  Two parts serve what is rounded to 16 bits
+// in the end, three what stays in fp32 (states, and the sums of the decays'
+// gradients), so that neither shows bf16's error.  bf16 data are one part, fp16
+// data two without error (11 bits into 16).  Of two split operands, the
+// products of parts i and j with i + j <= 2 (three parts) or <= 1 are formed:
+// the rest is below what the split itself leaves.
+using BF = mfma_t<SS_BF16>;
+
+// v0, v1 as packed bf16 words hi and lo
+__device__ __forceinline__ void split2(float v0, float v1, uint32_t& hi, uint32_t& lo) {
+  hi = pack2<SS_BF16>(v0, v1);
+  lo = pack2<SS_BF16>(v0 - __uint_as_float(hi << 16), v1 - __uint_as_float(hi & 0xffff0000u));
+}
+// and as three
+__device__ __forceinline__ void split3(float v0, float v1, uint32_t (&w)[3]) {
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    w[k] = pack2<SS_BF16>(v0, v1);
+    v0 -= __uint_as_float(w[k] << 16);
+    v1 -= __uint_as_float(w[k] & 0xffff0000u);
+  }
+}
+template <int IO>
+__device__ __forceinline__ float low16(uint32_t w) { return bits_f32<IO>((raw_t<IO>)(w & 0xffffu)); }
+template <int IO>
+__device__ __forceinline__ float high16(uint32_t w) { return bits_f32<IO>((raw_t<IO>)(w >> 16)); }
+// eight 16-bit values as bf16 hi and lo parts (bf16 input is its own hi)
+template <int IO>
+__device__ __forceinline__ void split8(u32x4v w, u32x4v& hi, u32x4v& lo) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t a, b;
+    split2(low16<IO>(w[q]), high16<IO>(w[q]), a, b);
+    hi[q] = a;
+    lo[q] = b;
+  }
+}
+__device__ __forceinline__ bf16x8 bfv(u32x4v w) { return as_vec<SS_BF16>(w); }
+
+// The rows of a chunk of an operand: `at` points at its first row's columns
+// (wave-uniform), rows are `row` bytes apart, and rows from `rows` on read as
+// zeros through the range check.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_view(const void* at, int64_t row, int rows) {
+  return make_rsrc(at, at ? (uint32_t)(rows * row) : 0u);
+}
+
+// C B^T tiles in operand order: element (i, j) of row tile it = i / 16 and
+// k-step kt = j / 32 is float j % 8 of lane i % 16 + 16 ((j % 32) / 8), 8 floats
+// a lane, so that a wave reads whole contiguous kilobytes.
+__device__ __forceinline__ int64_t cb_at(int it, int kt) { return (int64_t)(it * 8 + kt) * 512; }
+
 }  // namespace ss

@@ -21,11 +21,9 @@
 // element-wise pass walks them in order.
 //
 // Precision: products of 16-bit inputs run on the matrix cores as they are.
-// A computed operand v (weighted x, E, the decayed C B^T) is split into two
-// bf16 values, hi = bf16(v) and lo = bf16(v - hi), |v - hi - lo| <= 2^-18 |v|,
-// and multiplied in two passes, so that states and outputs carry fp32's error
-// rather than bf16's; fp16 inputs split exactly the same way (11 bits into
-// 16), which keeps bf16's range for the products.  States stay in fp32.
+// Computed operands are multiplied as sums of bf16 parts (ss_mfma.h): the
+// weighted x that makes the states in three, E and the decayed C B^T, which
+// make y, in two.  States stay in fp32.
 #include "ss_device.h"
 #include "ss_internal.h"
 #include "ss_mfma.h"
@@ -38,36 +36,6 @@ constexpr int kLogQ = 8;
 constexpr int kQ = 1 << kLogQ;  // chunk length
 constexpr int kP = 64;          // headdim
 constexpr int kJB = 64;         // time piece of a chunk
-using BF = mfma_t<SS_BF16>;
-
-// v0, v1 as packed bf16 words hi and lo
-__device__ __forceinline__ void split2(float v0, float v1, uint32_t& hi, uint32_t& lo) {
-  hi = pack2<SS_BF16>(v0, v1);
-  lo = pack2<SS_BF16>(v0 - __uint_as_float(hi << 16), v1 - __uint_as_float(hi & 0xffff0000u));
-}
-template <int IO>
-__device__ __forceinline__ float low16(uint32_t w) { return bits_f32<IO>((raw_t<IO>)(w & 0xffffu)); }
-template <int IO>
-__device__ __forceinline__ float high16(uint32_t w) { return bits_f32<IO>((raw_t<IO>)(w >> 16)); }
-// eight 16-bit values as bf16 hi and lo parts (bf16 input is its own hi)
-template <int IO>
-__device__ __forceinline__ void split8(u32x4v w, u32x4v& hi, u32x4v& lo) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint32_t a, b;
-    split2(low16<IO>(w[q]), high16<IO>(w[q]), a, b);
-    hi[q] = a;
-    lo[q] = b;
-  }
-}
-__device__ __forceinline__ bf16x8 bfv(u32x4v w) { return as_vec<SS_BF16>(w); }
-
-// The rows of a chunk of an operand: `at` points at its first row's columns
-// (wave-uniform), rows are `row` bytes apart, and rows from `rows` on read as
-// zeros through the range check.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_view(const void* at, int64_t row, int rows) {
-  return make_rsrc(at, at ? (uint32_t)(rows * row) : 0u);
-}
 
 template <int IO>
 __device__ __forceinline__ float step_size(const SsdPromptParams& p, float raw, int h) {
@@ -86,7 +54,7 @@ __device__ __forceinline__ void state_role(const SsdPromptParams& p, int place, 
   constexpr bool kTwo = IO == SS_F16;  // B needs a lo part
   __shared__ __attribute__((aligned(16))) float sW[kQ];
   __shared__ float sWave[4];
-  __shared__ __attribute__((aligned(16))) uint16_t sX[2][kJB * kP];
+  __shared__ __attribute__((aligned(16))) uint16_t sX[3][kJB * kP];
   __shared__ __attribute__((aligned(16))) uint16_t sB[kTwo ? 2 : 1][N / 32][kJB * 32];
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
   const SeqChunk q = find_chunk<kLogQ>(p.cu, p.nseqs, p.tokens, place);
@@ -136,16 +104,16 @@ __device__ __forceinline__ void state_role(const SsdPromptParams& p, int place, 
     for (int k = 0; k < 2; ++k) {
       const int row = tid / 8 + 32 * k;
       const float w = sW[j0 + row];
-      u32x4v hi, lo;
+      u32x4v part[3];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        uint32_t a, b;
-        split2(low16<IO>(xr[k][e]) * w, high16<IO>(xr[k][e]) * w, a, b);
-        hi[e] = a;
-        lo[e] = b;
+        uint32_t v[3];
+        split3(low16<IO>(xr[k][e]) * w, high16<IO>(xr[k][e]) * w, v);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) part[i][e] = v[i];
       }
-      *reinterpret_cast<u32x4v*>(&sX[0][tm_off<kP>(row, 8 * (tid % 8))]) = hi;
-      *reinterpret_cast<u32x4v*>(&sX[1][tm_off<kP>(row, 8 * (tid % 8))]) = lo;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x4v*>(&sX[i][tm_off<kP>(row, 8 * (tid % 8))]) = part[i];
     }
 #pragma unroll
     for (int k = 0; k < N / 32; ++k) {
@@ -163,17 +131,16 @@ __device__ __forceinline__ void state_role(const SsdPromptParams& p, int place, 
     if (j0 + kJB < rows) load_piece(j0 + kJB);  // lands while this piece is multiplied
 #pragma unroll
     for (int ks = 0; ks < kJB; ks += 32) {
-      const bf16x8 xh = bfv(tm_frag(&sX[0][ks * kP], xo[0], xo[1]));  // [k = step][n = channel]
-      const bf16x8 xl = bfv(tm_frag(&sX[1][ks * kP], xo[0], xo[1]));
+      bf16x8 xp[3];  // [k = step][n = channel]
+#pragma unroll
+      for (int i = 0; i < 3; ++i) xp[i] = bfv(tm_frag(&sX[i][ks * kP], xo[0], xo[1]));
 #pragma unroll
       for (int t = 0; t < N / 16; ++t) {
-        const bf16x8 bh = bfv(tm_frag(&sB[0][t / 2][ks * 32], bo[t % 2][0], bo[t % 2][1]));  // [m = state][k = step]
-        acc[t] = BF::run(bh, xl, acc[t]);
-        acc[t] = BF::run(bh, xh, acc[t]);
-        if constexpr (kTwo) {
-          const bf16x8 bl = bfv(tm_frag(&sB[kTwo ? 1 : 0][t / 2][ks * 32], bo[t % 2][0], bo[t % 2][1]));
-          acc[t] = BF::run(bl, xl, acc[t]);
-          acc[t] = BF::run(bl, xh, acc[t]);
+#pragma unroll
+        for (int j = 0; j < (kTwo ? 2 : 1); ++j) {
+          const bf16x8 bp = bfv(tm_frag(&sB[j][t / 2][ks * 32], bo[t % 2][0], bo[t % 2][1]));  // [m = state][k = step]
+#pragma unroll
+          for (int i = 2 - j; i >= 0; --i) acc[t] = BF::run(bp, xp[i], acc[t]);
         }
       }
     }
@@ -191,8 +158,6 @@ __device__ __forceinline__ void state_role(const SsdPromptParams& p, int place, 
 // lane, so that pass reads whole contiguous kilobytes.  Wave w has row tile
 // 4 band + w; the product is built transposed (B C^T), so that a lane holds 4
 // consecutive columns of one row.
-__device__ __forceinline__ int64_t cb_at(int it, int kt) { return (int64_t)(it * (kQ / 32) + kt) * 512; }
-
 template <int IO, int N>
 __device__ __forceinline__ void cb_role(const SsdPromptParams& p, int place, int g, int band) {
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;

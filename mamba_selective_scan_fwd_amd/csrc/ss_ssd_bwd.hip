@@ -1,0 +1,1167 @@
+// ss_ssd_bwd.hip -- gradients of the Mamba-2 SSD scan on MFMA (gfx950).
+//
+// Of the scan of ss_ssd.hip (page "Mamba" (walkthrough), "Deep dive: Mamba-2
+// and state-space duality"), per head, a_t = exp(Delta_t A), state H[p][n]:
+//   H_t = a_t H_{t-1} + Delta_t x_t B_t^T,  y_t = (H_t C_t + D x_t) silu(z_t).
+// With g = dy silu(z) and G_t the gradient of H_t,
+//   G_t = g_t C_t^T + a_{t+1} G_{t+1} (the final state's gradient behind the end),
+//   dC_t = H_t^T g_t,  dB_t = Delta_t G_t^T x_t,  dx_t = Delta_t G_t B_t + D g_t,
+//   da_t = a_t <G_t, H_{t-1}>  (the gradient of Delta_t A),
+//   dDelta_t = x_t . G_t B_t + A da_t,  dh0 = a_0 G_0.
+// Computed in chunks of Q = 256 steps, cs the running sum of Delta A in a
+// chunk, E the state that enters it and R the gradient of the state that
+// leaves it:
+//   E' = exp(cs_last) E + sum_j exp(cs_last - cs_j) Delta_j x_j B_j^T
+//   R' = exp(cs_last) R + sum_i exp(cs_i) g_i C_i^T   (R' leaves the chunk before)
+//   G_j B_j = sum_{i>=j} exp(cs_i - cs_j) (C_i . B_j) g_i + exp(cs_last - cs_j) R B_j
+//   S_ij = exp(cs_i - cs_j) Delta_j (g_i . x_j),  j <= i, summed over a group's heads:
+//   dC_i = sum_j S_ij B_j + sum_h exp(cs_i) E^T g_i
+//   dB_j = sum_i S_ij C_i + sum_h Delta_j exp(cs_last - cs_j) R^T x_j
+// and for the decays, with W_ij = (C_i . B_j) S_ij, e_i = exp(cs_i) C_i . E^T g_i and
+// r_j = Delta_j exp(cs_last - cs_j) B_j . R^T x_j,
+//   da_t = sum_{j < t <= i} W_ij + sum_{i>=t} e_i + sum_{j<t} r_j + exp(cs_last) <R, E>.
+// The pairs around a step t of a piece k of 64 steps are summed as
+//   i and j in k:         sum_{i>=t} (sum_{j<i} W_ij - sum_{m>i} W_mi), over k alone,
+//   i in k, j before k:   sum_{i>=t} sum_j W_ij;  j in k, i behind: sum_{j<t} sum_i W_ij,
+//   i behind k, j before: one number for the piece.
+// Only the first has terms that cancel (pairs that do not span t), and its
+// errors would add up over the steps: both of its sums take the same products
+// in 64 bits.  Kernels:
+//   bwd_planes   (fp16 or gated) the operands' planes of bf16 parts, g among them
+//   bwd_state    per (chunk, head): what a chunk adds to E and to R; further
+//                workgroups: B C^T (and C B^T if gated) per (chunk, group)
+//   bwd_pass     per (row, head, 1024 elements): E of every chunk, then R and
+//                <R, E> backwards, dh0
+//   bwd_scan     per (chunk, head): G_j B_j, dx; if gated another one rebuilds y for dz
+//   bwd_group    per (chunk, group, 64 rows, dC or dB): all heads of the group,
+//                S and its sums, dC or dB
+//   bwd_delta    per (chunk, head): da, ddt, and the chunk's part of dA, ddt_bias, dD
+//   bwd_sum      per head: dA, ddt_bias, dD
+// No atomics: every sum has a fixed order.  Computed operands are multiplied
+// as sums of bf16 parts (ss_mfma.h), three where the result stays in fp32 (E,
+// R, t and S's products, which dA, ddt_bias, dD and dh0 sum up), two where it
+// is rounded to 16 bits (dx, dz, dB, dC); states and sums are fp32.
+#include "ss_device.h"
+#include "ss_internal.h"
+#include "ss_mfma.h"
+
+namespace ss {
+namespace {
+
+constexpr int kQ = 256;  // chunk length
+constexpr int kP = 64;   // headdim
+constexpr int kJB = 64;  // time piece of a chunk
+
+// MODE: 0 bf16, 1 bf16 with a gate, 2 fp16, 3 fp16 with a gate
+template <int MODE> constexpr int io_of() { return MODE >= 2 ? SS_F16 : SS_BF16; }
+template <int MODE> constexpr int data_parts() { return MODE >= 2 ? 2 : 1; }               // of x, B, C
+template <int MODE> constexpr int g_parts() { return MODE % 2 ? 3 : data_parts<MODE>(); }  // of g
+
+struct Chunk {
+  int place, rows;
+  int64_t row0;  // first row, counted over the batch
+};
+__device__ __forceinline__ Chunk chunk_of(const SsdBwdParams& p, int place) {
+  Chunk q;
+  q.place = place;
+  const int b = place / p.nchunks, c = place - b * p.nchunks;
+  const int64_t left = p.seqlen - (int64_t)c * kQ;
+  q.rows = left < kQ ? (int)left : kQ;
+  q.row0 = b * p.seqlen + (int64_t)c * kQ;
+  return q;
+}
+// a plane's view from a chunk's first row on
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t plane_view(const uint16_t* at, int64_t row0, int64_t row, int col,
+                                                             int rows) {
+  return rows_view(at ? at + row0 * row + col : nullptr, row * 2, rows);
+}
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// four values from their parts' words
+template <int NP>
+__device__ __forceinline__ void join4(const uint2 (&w)[NP], float (&v)[4]) {
+#pragma unroll
+  for (int i = NP - 1; i >= 0; --i) {
+    const float a[4] = {lo_f(w[i].x), hi_f(w[i].x), lo_f(w[i].y), hi_f(w[i].y)};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = i == NP - 1 ? a[e] : v[e] + a[e];
+  }
+}
+
+// ---- the operands' planes ---------------------------------------------------------
+struct PlaneJob {
+  const void* src;
+  const void* gate;  // null, or multiply by silu(gate)
+  uint16_t* part[3];
+  int parts;
+  int64_t n;         // multiple of 8
+  int64_t blocks;
+};
+struct PlaneJobs { PlaneJob j[4]; int n; };
+constexpr int64_t kPlaneBlocks = 16384;  // workgroups of one plane
+template <int IO>
+__global__ void __launch_bounds__(256) bwd_planes_kernel(PlaneJobs a) {
+  int64_t blk = blockIdx.x;
+  int k = 0;
+  while (k + 1 < a.n && blk >= a.j[k].blocks) blk -= a.j[k++].blocks;
+  const PlaneJob q = a.j[k];
+  for (int64_t i = (blk * 256 + threadIdx.x) * 8; i < q.n; i += q.blocks * 2048) {
+    const u32x4v w = *reinterpret_cast<const u32x4v*>(static_cast<const uint16_t*>(q.src) + i);
+    u32x4v z = u32x4v{0u, 0u, 0u, 0u};
+    if (q.gate) z = *reinterpret_cast<const u32x4v*>(static_cast<const uint16_t*>(q.gate) + i);
+    u32x4v part[3];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float v0 = low16<IO>(w[e]), v1 = high16<IO>(w[e]);
+      if (q.gate) {
+        v0 *= silu_f(low16<IO>(z[e]));
+        v1 *= silu_f(high16<IO>(z[e]));
+      }
+      uint32_t v[3];
+      split3(v0, v1, v);
+#pragma unroll
+      for (int m = 0; m < 3; ++m) part[m][e] = v[m];
+    }
+#pragma unroll
+    for (int m = 0; m < 3; ++m)
+      if (m < q.parts) *reinterpret_cast<u32x4v*>(q.part[m] + i) = part[m];
+  }
+}
+
+// ---- what a chunk adds to E and to R ------------------------------------------------
+// As prompt_state_kernel: out^T[n][p] = sum_t V_t[n] (w_t u_t[p]), pieces of 64
+// steps staged in LDS as time-major tiles, wave w holding channels 16 w ...
+// E: u = x, V = B, w_j = exp(sum of Delta A behind j) Delta_j, from the last
+// document start on; R: u = g, V = C, w_i = exp(cs_i), before the first start.
+template <int MODE, int N>
+struct StateLds {
+  __attribute__((aligned(16))) float w[kQ];
+  float wave[4];
+  int first[4], count[4];
+  __attribute__((aligned(16))) uint16_t u[3][kJB * kP];
+  __attribute__((aligned(16))) uint16_t v[data_parts<MODE>()][N / 32][kJB * 32];
+};
+template <int MODE, int N, bool R>
+__device__ __forceinline__ void state_role(const SsdBwdParams& p, int place, int h, StateLds<MODE, N>& lds) {
+  constexpr int UP = R ? g_parts<MODE>() : data_parts<MODE>(), VP = data_parts<MODE>();
+  constexpr int IO = io_of<MODE>();
+  auto& sW = lds.w;
+  auto& sWave = lds.wave;
+  auto& sFirst = lds.first;
+  auto& sCount = lds.count;
+  auto& sU = lds.u;
+  auto& sV = lds.v;
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  const Chunk q = chunk_of(p, place);
+  const int g = h / (p.nheads / p.ngroups);
+  const int64_t urow = (int64_t)p.nheads * kP, vrow = (int64_t)p.ngroups * N;
+  __amdgpu_buffer_rsrc_t uv[UP], vv[VP];
+#pragma unroll
+  for (int i = 0; i < UP; ++i) uv[i] = plane_view(R ? p.gp[i] : p.xp[i % 2], q.row0, urow, h * kP, q.rows);
+#pragma unroll
+  for (int i = 0; i < VP; ++i) vv[i] = plane_view(R ? p.cp[i] : p.bp[i], q.row0, vrow, g * N, q.rows);
+  u32x4v ur[UP][2], vr[VP][N / 32];
+  auto load_piece = [&](int j0) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t off = (uint32_t)((j0 + tid / 8 + 32 * k) * urow * 2 + (tid % 8) * 16);
+#pragma unroll
+      for (int i = 0; i < UP; ++i) ur[i][k] = vload16(uv[i], off);
+    }
+#pragma unroll
+    for (int k = 0; k < N / 32; ++k) {
+      const uint32_t off = (uint32_t)((j0 + tid / 4) * vrow * 2 + k * 64 + (tid % 4) * 16);
+#pragma unroll
+      for (int i = 0; i < VP; ++i) vr[i][k] = vload16(vv[i], off);
+    }
+  };
+  load_piece(0);
+  {
+    const bool in = tid < q.rows;
+    float delta = 0.0f;
+    if (in) {
+      const float xd = load_io<IO>(p.dt, (q.row0 + tid) * p.nheads + h) + (p.dt_bias ? p.dt_bias[h] : 0.0f);
+      delta = p.softplus ? softplus_f(xd) : xd;
+    }
+    // documents: starts at or before each step of the chunk
+    int seg = 0, starts = 0, first = kQ;
+    if (p.seq_idx) {
+      const int64_t t = q.row0 + tid;
+      const bool st = in && t % p.seqlen != 0 && p.seq_idx[t] != p.seq_idx[t - 1];
+      const uint64_t m = __builtin_amdgcn_ballot_w64(st);
+      if (lane == 0) {
+        sCount[wave] = (int)__builtin_popcountll(m);
+        sFirst[wave] = m ? 64 * wave + (int)__builtin_ctzll(m) : kQ;
+      }
+      seg = (int)__builtin_popcountll(m & (lane == 63 ? ~0ull : (2ull << lane) - 1));
+    }
+    // R: the sum up to this step in the wave's 64; E: from this step on.  The
+    // former's differences decide the weights of neighbouring steps, whose
+    // exponents are small where the sums are not: it is formed in 64 bits and
+    // kept as two floats.
+    float v = delta * p.A[h], low = 0.0f;
+    if constexpr (R) {
+      double c = (double)delta * (double)p.A[h];
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const double o = __shfl_up(c, off, 64);
+        if (lane >= off) c += o;
+      }
+      v = (float)c;
+      low = (float)(c - (double)v);
+    } else {
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const float o = __shfl_down(v, off, 64);
+        if (lane + off < 64) v += o;
+      }
+    }
+    if (lane == (R ? 63 : 0)) sWave[wave] = v;
+    __syncthreads();
+    if (p.seq_idx) {
+      for (int w = 0; w < wave; ++w) seg += sCount[w];
+      starts = sCount[0] + sCount[1] + sCount[2] + sCount[3];
+      first = min(min(sFirst[0], sFirst[1]), min(sFirst[2], sFirst[3]));
+    }
+    const int64_t at = ((int64_t)place * p.nheads + h) * kQ + tid;
+    float w;
+    if constexpr (R) {
+      p.ws_cs[at] = v;
+      p.ws_cl[at] = low;
+      for (int k = 0; k < wave; ++k) v += sWave[k];
+      w = tid < first ? exp2_hw(v * kLog2e) : 0.0f;
+    } else {
+      p.ws_delta[at] = delta;
+      float behind = __shfl_down(v, 1, 64);
+      if (lane == 63) behind = 0.0f;
+      for (int k = 3; k > wave; --k) behind += sWave[k];
+      w = seg == starts ? exp2_hw(behind * kLog2e) * delta : 0.0f;
+      if (p.seq_idx && h == 0) p.ws_seg[(int64_t)place * kQ + tid] = seg;
+      if (tid == 0)
+        p.ws_decay[(int64_t)place * p.nheads + h] =
+            starts ? 0.0f : exp2_hw((sWave[0] + sWave[1] + sWave[2] + sWave[3]) * kLog2e);
+    }
+    sW[tid] = in ? w : 0.0f;
+    __syncthreads();
+  }
+  const int uo[2] = {tm_lane_off<kP>(16 * wave, 0, lane), tm_lane_off<kP>(16 * wave, 1, lane)};
+  const int vo[2][2] = {{tm_lane_off<32>(0, 0, lane), tm_lane_off<32>(0, 1, lane)},
+                        {tm_lane_off<32>(16, 0, lane), tm_lane_off<32>(16, 1, lane)}};
+  f32x4 acc[N / 16];
+#pragma unroll
+  for (int t = 0; t < N / 16; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int j0 = 0; j0 < q.rows; j0 += kJB) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int row = tid / 8 + 32 * k;
+      const float w = sW[j0 + row];
+      u32x4v part[3];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float a = lo_f(ur[UP - 1][k][e]), b = hi_f(ur[UP - 1][k][e]);
+#pragma unroll
+        for (int i = UP - 2; i >= 0; --i) {
+          a += lo_f(ur[i][k][e]);
+          b += hi_f(ur[i][k][e]);
+        }
+        uint32_t v[3];
+        split3(a * w, b * w, v);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) part[i][e] = v[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x4v*>(&sU[i][tm_off<kP>(row, 8 * (tid % 8))]) = part[i];
+    }
+#pragma unroll
+    for (int k = 0; k < N / 32; ++k)
+#pragma unroll
+      for (int i = 0; i < VP; ++i)
+        *reinterpret_cast<u32x4v*>(&sV[i][k][tm_off<32>(tid / 4, 8 * (tid % 4))]) = vr[i][k];
+    __syncthreads();
+    if (j0 + kJB < q.rows) load_piece(j0 + kJB);  // lands while this piece is multiplied
+#pragma unroll
+    for (int ks = 0; ks < kJB; ks += 32) {
+      bf16x8 up[3];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) up[i] = bfv(tm_frag(&sU[i][ks * kP], uo[0], uo[1]));
+#pragma unroll
+      for (int t = 0; t < N / 16; ++t)
+#pragma unroll
+        for (int j = 0; j < VP; ++j) {
+          const bf16x8 vp = bfv(tm_frag(&sV[j][t / 2][ks * 32], vo[t % 2][0], vo[t % 2][1]));
+#pragma unroll
+          for (int i = 2 - j; i >= 0; --i) acc[t] = BF::run(vp, up[i], acc[t]);
+        }
+    }
+    __syncthreads();
+  }
+  float* S = (R ? p.ws_R : p.ws_E) + ((int64_t)place * p.nheads + h) * (kP * N) + (16 * wave + lane % 16) * N +
+             4 * (lane / 16);
+#pragma unroll
+  for (int t = 0; t < N / 16; ++t) *reinterpret_cast<f32x4*>(S + 16 * t) = acc[t];
+}
+
+// C B^T (REV false: rows i of C, columns j of B up to the row's piece) or B C^T
+// (REV true: rows j of B, columns i of C from the row's piece to the last) of a
+// chunk in operand order, fp32; rows past the chunk come out as zeros.
+template <int MODE, int N, bool REV>
+__device__ __forceinline__ void cb_role(const SsdBwdParams& p, int place, int g, int band) {
+  constexpr int IO = io_of<MODE>();
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const Chunk q = chunk_of(p, place);
+  const int it = 4 * band + wave;
+  if (16 * it >= q.rows) return;
+  const int64_t row = (int64_t)p.ngroups * N;
+  const auto bv = plane_view(static_cast<const uint16_t*>(REV ? p.Cm : p.Bm), q.row0, row, g * N, q.rows);
+  const auto cv = plane_view(static_cast<const uint16_t*>(REV ? p.Bm : p.Cm), q.row0, row, g * N, q.rows);
+  u32x4v c[N / 32];
+#pragma unroll
+  for (int ks = 0; ks < N / 32; ++ks)
+    c[ks] = vload16(cv, (uint32_t)((16 * it + lane % 16) * row * 2 + (32 * ks + 8 * (lane / 16)) * 2));
+  float* CB = (REV ? p.ws_bc : p.ws_cb) + ((int64_t)place * p.ngroups + g) * (kQ * kQ);
+  const int j1 = REV ? 4 * ((q.rows + kJB - 1) / kJB) : 4 * band + 4;
+  for (int jt = REV ? 4 * band : 0; jt < j1; ++jt) {
+    f32x4 acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int ks = 0; ks < N / 32; ++ks) {
+      const u32x4v b = vload16(bv, (uint32_t)((16 * jt + lane % 16) * row * 2 + (32 * ks + 8 * (lane / 16)) * 2));
+      acc = mfma_t<IO>::run(as_vec<IO>(b), as_vec<IO>(c[ks]), acc);
+    }
+    const int to = lane % 16 + 16 * (2 * (jt & 1) + lane / 32);
+    *reinterpret_cast<f32x4*>(CB + cb_at(it, jt / 2) + to * 8 + 4 * ((lane / 16) & 1)) = acc;
+  }
+}
+
+template <int MODE, int N>
+__global__ void __launch_bounds__(256) bwd_state_kernel(SsdBwdParams p) {
+  __shared__ StateLds<MODE, N> lds;
+  const int places = (int)p.batch * p.nchunks, states = places * p.nheads, cbs = places * p.ngroups * 4;
+  int lb = (int)xcd_logical_block();
+  if (lb < 2 * states) {
+    const int place = lb / (2 * p.nheads), r = lb - place * 2 * p.nheads;
+    if (r < p.nheads) state_role<MODE, N, false>(p, place, r, lds);
+    else state_role<MODE, N, true>(p, place, r - p.nheads, lds);
+  } else {
+    lb -= 2 * states;
+    if (lb < cbs) {
+      cb_role<MODE, N, true>(p, lb / (4 * p.ngroups), (lb / 4) % p.ngroups, lb % 4);
+    } else {
+      lb -= cbs;
+      cb_role<MODE, N, false>(p, lb / (4 * p.ngroups), (lb / 4) % p.ngroups, lb % 4);
+    }
+  }
+}
+
+// ---- E forwards, R backwards ----------------------------------------------------------
+// Workgroup = (batch row, head, 1024 elements), a thread 4 elements.  <R, E> of a
+// chunk: each wave leaves the sum of its 256 elements.
+template <int N>
+__global__ void __launch_bounds__(256) bwd_pass_kernel(SsdBwdParams p) {
+  constexpr int kParts = kP * N / 1024, kAhead = 4;
+  const int part = (int)(blockIdx.x % kParts);
+  const int h = (int)((blockIdx.x / kParts) % (uint32_t)p.nheads);
+  const int64_t b = blockIdx.x / kParts / (uint32_t)p.nheads;
+  const int e = part * 1024 + 4 * (int)threadIdx.x, n = p.nchunks;
+  const int64_t first = b * n * p.nheads + h, step = (int64_t)p.nheads * (kP * N);
+  const float* dec = p.ws_decay + first;
+  const int64_t row = (b * p.nheads + h) * (kP * N) + e;
+  float* wE = p.ws_E + first * (kP * N) + e;
+  float* wR = p.ws_R + first * (kP * N) + e;
+  f32x4 S[kAhead], F[kAhead];
+  float d[kAhead];
+  {
+    f32x4 E = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (p.h0) E = *reinterpret_cast<const f32x4*>(p.h0 + row);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (k < n) {
+        S[k] = *reinterpret_cast<const f32x4*>(wE + k * step);
+        d[k] = dec[(int64_t)k * p.nheads];
+      }
+    for (int c = 0; c < n; c += kAhead) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (c + k < n) {
+          const f32x4 own = S[k];
+          const float decay = d[k];
+          if (c + k + kAhead < n) {
+            S[k] = *reinterpret_cast<const f32x4*>(wE + (c + k + kAhead) * step);
+            d[k] = dec[(int64_t)(c + k + kAhead) * p.nheads];
+          }
+          *reinterpret_cast<f32x4*>(wE + (c + k) * step) = E;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) E[i] = fmaf(decay, E[i], own[i]);
+        }
+    }
+  }
+  f32x4 Rg = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  if (p.dfinal) Rg = *reinterpret_cast<const f32x4*>(p.dfinal + row);
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    if (k < n) {
+      S[k] = *reinterpret_cast<const f32x4*>(wR + (n - 1 - k) * step);
+      F[k] = *reinterpret_cast<const f32x4*>(wE + (n - 1 - k) * step);  // this thread's own store
+      d[k] = dec[(int64_t)(n - 1 - k) * p.nheads];
+    }
+  for (int c = 0; c < n; c += kAhead) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (c + k < n) {
+        const int at = n - 1 - c - k, nx = at - kAhead;
+        const f32x4 own = S[k], E = F[k];
+        const float decay = d[k];
+        if (nx >= 0) {
+          S[k] = *reinterpret_cast<const f32x4*>(wR + nx * step);
+          F[k] = *reinterpret_cast<const f32x4*>(wE + nx * step);
+          d[k] = dec[(int64_t)nx * p.nheads];
+        }
+        *reinterpret_cast<f32x4*>(wR + at * step) = Rg;
+        float v = Rg[0] * E[0] + Rg[1] * E[1] + (Rg[2] * E[2] + Rg[3] * E[3]);
+        v = row_sum(v);
+        v += __shfl_xor(v, 16, 64);
+        v += __shfl_xor(v, 32, 64);
+        if (threadIdx.x % 64 == 0)
+          p.ws_dot[(first + (int64_t)at * p.nheads) * (4 * kParts) + 4 * part + threadIdx.x / 64] = decay * v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) Rg[i] = fmaf(decay, Rg[i], own[i]);
+      }
+  }
+  if (p.dh0) *reinterpret_cast<f32x4*>(p.dh0 + row) = Rg;
+}
+
+// ---- dx (REV), or y for dz --------------------------------------------------------------
+// Workgroup = (chunk, head), 512 threads, laid out as prompt_scan_kernel: out
+// rows o, source rows s, out^T[p][o] = sum_s u_s[p] M[o][s] + f_o sum_n K[p][n] v_o[n].
+//   REV:  s >= o, u = g, M = exp(cs_s - cs_o) (C_s . B_o),         K = R, v = B, f = exp(cs_last - cs_o)
+//   else: s <= o, u = x, M = exp(cs_o - cs_s) Delta_s (C_o . B_s), K = E, v = C, f = exp(cs_o)
+// A pair in different pieces of 64 takes a factor per row and one per column,
+// both through the piece's end, a pair inside a piece the exp of a difference.
+constexpr int kScanThreads = 512;
+template <int MODE, int N, bool REV>
+__global__ void __launch_bounds__(kScanThreads, MODE == 0 ? 4 : 2) bwd_scan_kernel(SsdBwdParams p) {
+  constexpr int IO = io_of<MODE>();
+  // two parts at the most: dx and dz are rounded to 16 bits
+  constexpr int UP = REV ? (g_parts<MODE>() > 1 ? 2 : 1) : data_parts<MODE>(), VP = data_parts<MODE>();
+  constexpr int kHS = N + 8;
+  __shared__ __attribute__((aligned(16))) float sDelta[kQ];
+  __shared__ __attribute__((aligned(16))) float sCs[kQ];   // Delta A summed from the piece's first step
+  __shared__ __attribute__((aligned(16))) float sCol[kQ];  // a source row's factor
+  __shared__ __attribute__((aligned(16))) int sSeg[kQ];
+  __shared__ float sTot[4];
+  __shared__ __attribute__((aligned(16))) uint16_t sU[UP][kQ * kP];
+  __shared__ __attribute__((aligned(16))) uint16_t sK[2][kP * kHS];
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  const int lb = (int)xcd_logical_block();  // the heads of one chunk share its B, C and C B^T in an XCD's L2
+  const int h = lb % p.nheads;
+  const Chunk q = chunk_of(p, lb / p.nheads);
+  const int rows = q.rows, g = h / (p.nheads / p.ngroups);
+  const int64_t xrow = (int64_t)p.nheads * kP, vrow = (int64_t)p.ngroups * N;
+  const int64_t ph = (int64_t)q.place * p.nheads + h;
+  const int half = wave / 4;
+  const int blk[2] = {wave % 4, 7 - wave % 4};
+  const int orow[2] = {32 * blk[0] + 16 * half, 32 * blk[1] + 16 * half};
+  const int lastp = (rows - 1) / kJB;
+
+  u32x4v ur[UP][4];
+#pragma unroll
+  for (int i = 0; i < UP; ++i) {
+    const auto uv = plane_view(REV ? p.gp[i] : p.xp[i], q.row0, xrow, h * kP, rows);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      ur[i][k] = vload16(uv, (uint32_t)((tid / 8 + 64 * k) * xrow * 2 + (tid % 8) * 16));
+  }
+  const f32x4* K = reinterpret_cast<const f32x4*>((REV ? p.ws_R : p.ws_E) + ph * (kP * N));
+  f32x4 kr[N / 32];
+#pragma unroll
+  for (int k = 0; k < N / 32; ++k) kr[k] = K[tid + kScanThreads * k];
+  u32x4v vf[VP][2][N / 32];
+#pragma unroll
+  for (int i = 0; i < VP; ++i) {
+    const auto vv = plane_view(REV ? p.bp[i] : p.cp[i], q.row0, vrow, g * N, rows);
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int ks = 0; ks < N / 32; ++ks)
+        vf[i][b][ks] = vload16(vv, (uint32_t)((orow[b] + lane % 16) * vrow * 2 + (32 * ks + 8 * (lane / 16)) * 2));
+  }
+  if (tid < kQ) {
+    const float delta = p.ws_delta[ph * kQ + tid], cs = p.ws_cs[ph * kQ + tid];
+    const float tot = __shfl(cs, 63, 64);
+    sDelta[tid] = delta;
+    sCs[tid] = cs;
+    sCol[tid] = REV ? exp2_hw(cs * kLog2e) : exp2_hw((tot - cs) * kLog2e) * delta;
+    if (lane == 63) sTot[wave] = cs;
+    if (p.seq_idx) sSeg[tid] = p.ws_seg[(int64_t)q.place * kQ + tid];
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int at = tm_off<kP>(tid / 8 + 64 * k, 8 * (tid % 8));
+#pragma unroll
+    for (int i = 0; i < UP; ++i) *reinterpret_cast<u32x4v*>(&sU[i][at]) = ur[i][k];
+  }
+#pragma unroll
+  for (int k = 0; k < N / 32; ++k) {
+    const int item = 4 * (tid + kScanThreads * k);
+    const int at = (item / N) * kHS + item % N;
+    uint32_t a0, a1, b0, b1;
+    split2(kr[k][0], kr[k][1], a0, b0);
+    split2(kr[k][2], kr[k][3], a1, b1);
+    *reinterpret_cast<uint2*>(&sK[0][at]) = make_uint2(a0, a1);
+    *reinterpret_cast<uint2*>(&sK[1][at]) = make_uint2(b0, b1);
+  }
+  __syncthreads();
+
+  f32x4 acc[2][4];  // [block][p tile]: p = 16 pt + 4 (lane / 16) + r, o = orow + lane % 16
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int pt = 0; pt < 4; ++pt) acc[b][pt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int ks = 0; ks < N / 32; ++ks)
+#pragma unroll
+    for (int pt = 0; pt < 4; ++pt) {
+      const int at = (16 * pt + lane % 16) * kHS + 32 * ks + 8 * (lane / 16);
+      const bf16x8 kh = bfv(*reinterpret_cast<const u32x4v*>(&sK[0][at]));
+      const bf16x8 kl = bfv(*reinterpret_cast<const u32x4v*>(&sK[1][at]));
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        acc[b][pt] = BF::run(kl, bfv(vf[0][b][ks]), acc[b][pt]);
+        if constexpr (VP > 1) acc[b][pt] = BF::run(kh, bfv(vf[VP - 1][b][ks]), acc[b][pt]);
+        acc[b][pt] = BF::run(kh, bfv(vf[0][b][ks]), acc[b][pt]);
+      }
+    }
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const int o = orow[b] + lane % 16, piece = blk[b] / 2;
+    float arg = REV ? sTot[piece] - sCs[o] : sCs[o];
+    if constexpr (REV) {
+      for (int k = piece + 1; k < 4; ++k) arg += sTot[k];
+    } else {
+      for (int k = 0; k < piece; ++k) arg += sTot[k];
+    }
+    float f = exp2_hw(arg * kLog2e);
+    if (p.seq_idx && sSeg[o] != (REV ? sSeg[rows - 1] : 0)) f = 0.0f;
+#pragma unroll
+    for (int pt = 0; pt < 4; ++pt) acc[b][pt] *= f;
+  }
+
+  const float* CB = (REV ? p.ws_bc : p.ws_cb) + ((int64_t)q.place * p.ngroups + g) * (kQ * kQ);
+  const float Dh = p.D ? p.D[h] : 0.0f;
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    if (orow[b] >= rows) continue;
+    const int o = orow[b] + lane % 16, piece = blk[b] / 2;
+    const float cso = sCs[o], tot = sTot[piece];
+    const int sego = p.seq_idx ? sSeg[o] : 0;
+    const float* cb = CB + cb_at(orow[b] / 16, 0) + lane * 8;
+    const int s0 = REV ? piece : 0, s1 = REV ? lastp : piece;
+    f32x4 cur[2][2], nxt[2][2];
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) cur[ks][e] = *reinterpret_cast<const f32x4*>(cb + (2 * s0 + ks) * 512 + 4 * e);
+    for (int sp = s0; sp <= s1; ++sp) {
+      if (sp < s1) {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) nxt[ks][e] = *reinterpret_cast<const f32x4*>(cb + (2 * sp + 2 + ks) * 512 + 4 * e);
+      }
+      const bool diag = sp == piece;
+      float arg = REV ? tot - cso : cso;  // Delta A between this row and the source piece's end towards it
+      for (int k = REV ? piece + 1 : sp + 1; k < (REV ? sp : piece); ++k) arg += sTot[k];
+      const float fo = exp2_hw(arg * kLog2e);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const int s = kJB * sp + 32 * ks + 8 * (lane / 16);
+        float m[8];
+        if (diag) {
+          const f32x4 c0 = *reinterpret_cast<const f32x4*>(&sCs[s]), c1 = *reinterpret_cast<const f32x4*>(&sCs[s + 4]);
+          const f32x4 d0 = *reinterpret_cast<const f32x4*>(&sDelta[s]),
+                      d1 = *reinterpret_cast<const f32x4*>(&sDelta[s + 4]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float css = e < 4 ? c0[e & 3] : c1[e & 3];
+            float v = cur[ks][e / 4][e & 3] * exp2_hw((REV ? css - cso : cso - css) * kLog2e);
+            if constexpr (!REV) v *= e < 4 ? d0[e & 3] : d1[e & 3];
+            m[e] = (REV ? s + e >= o : s + e <= o) ? v : 0.0f;
+          }
+        } else {
+          const f32x4 w0 = *reinterpret_cast<const f32x4*>(&sCol[s]), w1 = *reinterpret_cast<const f32x4*>(&sCol[s + 4]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m[e] = cur[ks][e / 4][e & 3] * ((e < 4 ? w0[e & 3] : w1[e & 3]) * fo);
+        }
+        if (p.seq_idx) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m[e] = sSeg[s + e] == sego ? m[e] : 0.0f;
+        }
+        u32x4v mh, ml;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t a, c;
+          split2(m[2 * e], m[2 * e + 1], a, c);
+          mh[e] = a;
+          ml[e] = c;
+        }
+#pragma unroll
+        for (int pt = 0; pt < 4; ++pt) {
+          const int o0 = tm_lane_off<kP>(16 * pt, 0, lane), o1 = tm_lane_off<kP>(16 * pt, 1, lane);
+          const bf16x8 a = bfv(tm_frag(&sU[0][(kJB * sp + 32 * ks) * kP], o0, o1));
+          acc[b][pt] = BF::run(a, bfv(ml), acc[b][pt]);
+          if constexpr (UP > 1) {
+            const bf16x8 a2 = bfv(tm_frag(&sU[UP - 1][(kJB * sp + 32 * ks) * kP], o0, o1));
+            acc[b][pt] = BF::run(a2, bfv(mh), acc[b][pt]);
+          }
+          acc[b][pt] = BF::run(a, bfv(mh), acc[b][pt]);
+        }
+      }
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) cur[ks][e] = nxt[ks][e];
+    }
+    const int64_t out = (q.row0 + o) * xrow + h * kP;
+    if (o >= rows) continue;
+    const float delta = sDelta[o];
+#pragma unroll
+    for (int pt = 0; pt < 4; ++pt) {
+      const int p0 = 16 * pt + 4 * (lane / 16);
+      uint2 uw[UP];
+#pragma unroll
+      for (int i = 0; i < UP; ++i) uw[i] = *reinterpret_cast<const uint2*>(&sU[i][tm_off<kP>(o, p0)]);
+      float u[4], r[4];  // of row o: g, or x
+      join4<UP>(uw, u);
+      if constexpr (REV) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = fmaf(Dh, u[e], delta * acc[b][pt][e]);
+      } else {
+        const uint2 zw = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.z) + out + p0);
+        const uint2 dw = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.dy) + out + p0);
+        const float z[4] = {low16<IO>(zw.x), high16<IO>(zw.x), low16<IO>(zw.y), high16<IO>(zw.y)};
+        const float dy[4] = {low16<IO>(dw.x), high16<IO>(dw.x), low16<IO>(dw.y), high16<IO>(dw.y)};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float sg = sigmoid_f(z[e]);
+          r[e] = dy[e] * fmaf(Dh, u[e], acc[b][pt][e]) * (sg * fmaf(z[e], 1.0f - sg, 1.0f));
+        }
+      }
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(REV ? p.dx : p.dz) + out + p0) =
+          make_uint2(pack2<IO>(r[0], r[1]), pack2<IO>(r[2], r[3]));
+    }
+  }
+}
+
+// ---- dC and dB -------------------------------------------------------------------------
+// Workgroup = (chunk, group, 64 rows f, dC or dB), 512 threads, all heads of the
+// group in turn; with the other rows s of the chunk (dC: s <= f, dB: s >= f),
+//   dC: f = i, s = j: F = g, O = x, K = E, v = C, u = B, w_f = exp(cs_f)
+//   dB: f = j, s = i: F = x, O = g, K = R, v = B, u = C, w_f = Delta_f exp(cs_last - cs_f)
+// per head: t_f[n] = w_f sum_p K[p][n] F_f[p], added up over the heads;
+// v_f . t_f (e or r); S_fs from O_s . F_f, added up over the heads in
+// registers, and its row of W (row or col); after the heads, sum_s S_fs u_s.
+// Wave w has the row tile w % 4; of the states and of every piece's four s
+// tiles, waves 0-3 have the first half and waves 4-7 the second.  Both halves'
+// sums of a row are left apart (bwd_delta adds them); the product with u joins
+// them through LDS.  S is built with s along a lane's 4 values, and enters the
+// last product as it is: a k-step's 32 steps are taken in the order in which
+// two of its tiles hold them (u's fragments are read in that order too).
+// dB's sums leave out Delta_f, so that x_f . G_f B_f (what dDelta_f takes
+// directly) comes from the same numbers, diagonal included, undivided.
+constexpr int kGroupThreads = 512;
+// O in LDS: rows of 64 channels, their 16-byte pieces swapped by the row, so
+// that 8 rows' pieces of one column lie in different banks
+__device__ __forceinline__ int o_off(int row, int col) { return row * kP + 8 * ((col >> 3) ^ (row & 7)) + (col & 7); }
+template <int MODE, int N, bool DB>
+__global__ void __launch_bounds__(kGroupThreads, 2) bwd_group_kernel(SsdBwdParams p) {
+  constexpr int IO = io_of<MODE>();
+  constexpr int FP = DB ? data_parts<MODE>() : g_parts<MODE>(), OP = DB ? g_parts<MODE>() : data_parts<MODE>();
+  constexpr int UP = data_parts<MODE>();
+  constexpr int NT = N / 32;  // state tiles of a wave
+  constexpr size_t kOBytes = (size_t)OP * kQ * kP * 2, kKBytes = (size_t)3 * kP * N * 2;
+  constexpr size_t kUBytes = (size_t)UP * kJB * N * 2, kJoin = (size_t)4 * (N / 16) * 64 * 16;
+  constexpr size_t kA = kOBytes + kKBytes, kB = kUBytes > kJoin ? kUBytes : kJoin;
+  __shared__ __attribute__((aligned(16))) unsigned char sMem[kA > kB ? kA : kB];
+  __shared__ __attribute__((aligned(16))) float sCs[kQ], sCl[kQ];  // Delta A from the piece's first step, two floats
+  __shared__ __attribute__((aligned(16))) float sCol[kQ];    // an s row's factor
+  __shared__ __attribute__((aligned(16))) float sDelta[kQ];
+  __shared__ float sBehind[kQ];                              // Delta A behind a row to its piece's end
+  __shared__ __attribute__((aligned(16))) int sSeg[kQ];
+  __shared__ float sTot[4];
+  uint16_t* sO = reinterpret_cast<uint16_t*>(sMem);                 // [part][s][o_off]
+  uint16_t* sK = reinterpret_cast<uint16_t*>(sMem + kOBytes);       // [part][slice][64 p x 32 n], time-major tiles
+  uint16_t* sU = reinterpret_cast<uint16_t*>(sMem);                 // after the heads: [part][slice][64 s x 32 n]
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, quad = lane / 16;
+  const int rt = wave % 4, half = wave / 4;
+  const int lb = (int)xcd_logical_block();
+  const int rb = lb % 4, g = (lb / 4) % p.ngroups;
+  const Chunk q = chunk_of(p, lb / (4 * p.ngroups));
+  const int rows = q.rows, f0 = kJB * rb;
+  if (f0 >= rows) return;
+  const int f = f0 + 16 * rt + lane % 16;  // this lane's row
+  const int lastp = (rows - 1) / kJB;
+  const int ob0 = DB ? rb : 0, ob1 = DB ? lastp : rb;  // pieces of s
+  const int hpg = p.nheads / p.ngroups;
+  const int64_t xrow = (int64_t)p.nheads * kP, vrow = (int64_t)p.ngroups * N;
+  const auto vv = plane_view(static_cast<const uint16_t*>(DB ? p.Bm : p.Cm), q.row0, vrow, g * N, rows);
+  const auto uv = plane_view(static_cast<const uint16_t*>(DB ? p.Cm : p.Bm), q.row0, vrow, g * N, rows);
+
+  // u_s . v_f of the wave's tiles (the same for every head); v_f of its states
+  f32x4 cb[4][2];
+  {
+    u32x4v vq[N / 32];
+#pragma unroll
+    for (int ks = 0; ks < N / 32; ++ks) vq[ks] = vload16(vv, (uint32_t)(f * vrow * 2 + (32 * ks + 8 * quad) * 2));
+#pragma unroll
+    for (int ob = 0; ob < 4; ++ob)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        f32x4 a = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (ob >= ob0 && ob <= ob1) {
+          const int s = kJB * ob + 16 * (2 * half + t) + lane % 16;
+#pragma unroll
+          for (int ks = 0; ks < N / 32; ++ks)
+            a = mfma_t<IO>::run(as_vec<IO>(vload16(uv, (uint32_t)(s * vrow * 2 + (32 * ks + 8 * quad) * 2))),
+                                as_vec<IO>(vq[ks]), a);
+        }
+        cb[ob][t] = a;
+      }
+  }
+  uint2 vn[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) vn[t] = vload8(vv, (uint32_t)(f * vrow * 2 + (16 * (NT * half + t) + 4 * quad) * 2));
+  if (p.seq_idx && tid < kQ) sSeg[tid] = p.ws_seg[(int64_t)q.place * kQ + tid];
+
+  f32x4 S[4][2], tot[NT];
+#pragma unroll
+  for (int ob = 0; ob < 4; ++ob)
+#pragma unroll
+    for (int t = 0; t < 2; ++t) S[ob][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int t = 0; t < NT; ++t) tot[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  for (int hg = 0; hg < hpg; ++hg) {
+    const int h = g * hpg + hg;
+    const int64_t ph = (int64_t)q.place * p.nheads + h;
+    u32x4v F[FP][2];
+#pragma unroll
+    for (int i = 0; i < FP; ++i) {
+      const auto fv = plane_view(DB ? p.xp[i % 2] : p.gp[i], q.row0, xrow, h * kP, rows);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) F[i][ks] = vload16(fv, (uint32_t)(f * xrow * 2 + (32 * ks + 8 * quad) * 2));
+    }
+    u32x4v orr[OP][4];
+#pragma unroll
+    for (int i = 0; i < OP; ++i) {
+      const auto ov = plane_view(DB ? p.gp[i] : p.xp[i % 2], q.row0, xrow, h * kP, rows);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k >= ob0 && k <= ob1) orr[i][k] = vload16(ov, (uint32_t)((tid / 8 + 64 * k) * xrow * 2 + (tid % 8) * 16));
+    }
+    const f32x4* K = reinterpret_cast<const f32x4*>((DB ? p.ws_R : p.ws_E) + ph * (kP * N));
+    f32x4 kr[N / 32];
+#pragma unroll
+    for (int k = 0; k < N / 32; ++k) kr[k] = K[tid + kGroupThreads * k];
+    float delta = 0.0f, cs = 0.0f, cl = 0.0f;
+    if (tid < kQ) {
+      delta = p.ws_delta[ph * kQ + tid];
+      cs = p.ws_cs[ph * kQ + tid];
+      cl = p.ws_cl[ph * kQ + tid];
+    }
+    __syncthreads();  // the previous head's operands are used up
+    if (tid < kQ) {
+      const float behind = (__shfl(cs, 63, 64) - cs) + (__shfl(cl, 63, 64) - cl);
+      sCs[tid] = cs;
+      sCl[tid] = cl;
+      sDelta[tid] = delta;
+      sCol[tid] = exp2_hw((DB ? cs : behind) * kLog2e);
+      sBehind[tid] = behind;
+      if (lane == 63) sTot[wave] = cs;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k >= ob0 && k <= ob1) {
+        const int at = o_off(tid / 8 + 64 * k, 8 * (tid % 8));
+#pragma unroll
+        for (int i = 0; i < OP; ++i) *reinterpret_cast<u32x4v*>(&sO[i * kQ * kP + at]) = orr[i][k];
+      }
+#pragma unroll
+    for (int k = 0; k < N / 32; ++k) {
+      const int item = 4 * (tid + kGroupThreads * k), pr = item / N, n = item % N;
+      const int at = (n / 32) * (kP * 32) + tm_off<32>(pr, n % 32);
+      uint32_t a[3], b[3];
+      split3(kr[k][0], kr[k][1], a);
+      split3(kr[k][2], kr[k][3], b);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2*>(&sK[i * kP * N + at]) = make_uint2(a[i], b[i]);
+    }
+    __syncthreads();
+
+    const float csf = sCs[f], clf = sCl[f], df = sDelta[f], behind = sBehind[f];
+    const int segf = p.seq_idx ? sSeg[f] : 0;
+    // t_f and v_f . t_f
+    float wf = DB ? behind : csf;
+    if constexpr (DB) {
+      for (int k = rb + 1; k < 4; ++k) wf += sTot[k];
+    } else {
+      for (int k = 0; k < rb; ++k) wf += sTot[k];
+    }
+    wf = exp2_hw(wf * kLog2e);
+    if (p.seq_idx && segf != (DB ? sSeg[rows - 1] : 0)) wf = 0.0f;
+    float vt = 0.0f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int nt = NT * half + t;  // states 16 nt ..
+      f32x4 a = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const uint16_t* tile = sK + (nt / 2) * (kP * 32) + 32 * ks * 32;
+        const int o0 = tm_lane_off<32>(16 * (nt % 2), 0, lane), o1 = tm_lane_off<32>(16 * (nt % 2), 1, lane);
+#pragma unroll
+        for (int j = 2; j >= 0; --j) {
+          const bf16x8 kp = bfv(tm_frag(tile + j * kP * N, o0, o1));
+#pragma unroll
+          for (int i = FP - 1; i >= 0; --i)
+            if (i + j <= 2) a = BF::run(kp, bfv(F[i][ks]), a);
+        }
+      }
+      const float v[4] = {low16<IO>(vn[t].x), high16<IO>(vn[t].x), low16<IO>(vn[t].y), high16<IO>(vn[t].y)};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        a[r] *= wf;
+        vt = fmaf(v[r], a[r], vt);
+        tot[t][r] = DB ? fmaf(df, a[r], tot[t][r]) : tot[t][r] + a[r];
+      }
+    }
+    // S and W
+    // W of this lane's row: inside its piece, of other pieces, and of the first
+    // one and two of them; dB: all of it without Delta_f; O_f . F_f
+    double in = 0.0;
+    float off = 0.0f, first = 0.0f, second = 0.0f, all = 0.0f, xd = 0.0f;
+    const float ef = exp2_hw((DB ? behind : csf) * kLog2e);
+#pragma unroll
+    for (int ob = 0; ob < 4; ++ob) {
+      if (ob < ob0 || ob > ob1) continue;
+      const bool diag = ob == rb;
+      // across pieces: exp(cs_i) exp(behind_j) exp(pieces between), in this order
+      // for dB and dC, so that both form the same W
+      float between = 0.0f;
+      for (int k = DB ? rb + 1 : ob + 1; k < (DB ? ob : rb); ++k) between += sTot[k];
+      between = exp2_hw(between * kLog2e);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int st = kJB * ob + 16 * (2 * half + t);
+        f32x4 a = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          const int at = o_off(st + lane % 16, 32 * ks + 8 * quad);
+#pragma unroll
+          for (int j = OP - 1; j >= 0; --j) {
+            const bf16x8 op = bfv(*reinterpret_cast<const u32x4v*>(&sO[j * kQ * kP + at]));
+#pragma unroll
+            for (int i = FP - 1; i >= 0; --i)
+              if (i + j <= 2) a = BF::run(op, bfv(F[i][ks]), a);
+          }
+        }
+        const int s = st + 4 * quad;
+        f32x4 fac, ds;  // the decay from s to f (f to s), Delta of the pair's earlier step
+        if constexpr (DB) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) ds[r] = df;
+        } else {
+          ds = *reinterpret_cast<const f32x4*>(&sDelta[s]);
+        }
+        if (diag) {
+          const f32x4 c = *reinterpret_cast<const f32x4*>(&sCs[s]), l = *reinterpret_cast<const f32x4*>(&sCl[s]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float from = (csf - c[r]) + (clf - l[r]);  // Delta A from s to f
+            const float v = exp2_hw((DB ? -from : from) * kLog2e);
+            fac[r] = (DB ? s + r >= f : s + r <= f) ? v : 0.0f;
+          }
+        } else {
+          fac = *reinterpret_cast<const f32x4*>(&sCol[s]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) fac[r] = fac[r] * ef * between;
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float v = a[r] * fac[r];
+          if (p.seq_idx) v = sSeg[s + r] == segf ? v : 0.0f;
+          const float vd = v * ds[r];
+          S[ob][t][r] += vd;
+          if constexpr (DB) all = fmaf(cb[ob][t][r], v, all);
+          if (diag) {
+            in += s + r != f ? (double)cb[ob][t][r] * (double)vd : 0.0;
+            if constexpr (DB) xd += s + r == f ? a[r] : 0.0f;
+          } else {
+            off = fmaf(cb[ob][t][r], vd, off);
+          }
+        }
+      }
+      if (ob == 0) first = off;
+      if (ob == 1) second = off;
+    }
+    auto over_quads = [](float v) {
+      v += __shfl_xor(v, 16, 64);
+      return v + __shfl_xor(v, 32, 64);
+    };
+    const int64_t to = ((int64_t)half * p.batch * p.nchunks * p.nheads + ph) * kQ + f;
+    in += __shfl_xor(in, 16, 64);
+    in += __shfl_xor(in, 32, 64);
+    off = over_quads(off);
+    vt = over_quads(vt);
+    if constexpr (DB) {
+      all = over_quads(all);
+      xd = over_quads(xd);
+      if (lane < 16) {
+        p.ws_colin[to] = in;
+        p.ws_col[to] = off;
+        p.ws_out[to] = df * vt;
+        p.ws_xg[to] = all + vt;
+        p.ws_xd[to] = xd;
+      }
+    } else {
+      if (lane < 16) {
+        p.ws_rowin[to] = in;
+        p.ws_row[to] = off;
+        p.ws_e[to] = vt;
+      }
+      if (rb >= 2) {  // the pairs that a whole piece lies between
+        float v[2] = {first, rb == 3 ? second : first};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          v[k] = row_sum(over_quads(f < rows ? v[k] : 0.0f));
+          if (lane == 0) p.ws_span[(ph * 4 + 2 * (rb - 2) + k) * 8 + wave] = v[k];
+        }
+      }
+    }
+  }
+
+  // ---- sum_s S_fs u_s, this wave's half of every piece, all states
+  f32x4 acc[N / 16];
+#pragma unroll
+  for (int t = 0; t < N / 16; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  __amdgpu_buffer_rsrc_t up[UP];
+#pragma unroll
+  for (int i = 0; i < UP; ++i) up[i] = plane_view(DB ? p.cp[i] : p.bp[i], q.row0, vrow, g * N, rows);
+#pragma unroll
+  for (int ob = 0; ob < 4; ++ob) {
+    if (ob < ob0 || ob > ob1) continue;  // uniform over the workgroup
+    __syncthreads();
+    for (int item = tid; item < kJB * N / 8; item += kGroupThreads) {
+      const int s = item / (N / 8), n = 8 * (item % (N / 8));
+      const uint32_t off = (uint32_t)((kJB * ob + s) * vrow * 2 + n * 2);
+      const int at = (n / 32) * (kJB * 32) + tm_off<32>(s, n % 32);
+#pragma unroll
+      for (int i = 0; i < UP; ++i) *reinterpret_cast<u32x4v*>(&sU[i * kJB * N + at]) = vload16(up[i], off);
+    }
+    __syncthreads();
+    u32x4v sh, sl;  // S of the two tiles: the k-step's steps 4 quad + r and 16 + 4 quad + r
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t a, b;
+        split2(S[ob][t][2 * e], S[ob][t][2 * e + 1], a, b);
+        sh[2 * t + e] = a;
+        sl[2 * t + e] = b;
+      }
+    const int j = lane % 16;
+#pragma unroll
+    for (int t = 0; t < N / 16; ++t) {
+      const int c = 16 * (t % 2) + 4 * (j % 4);
+      const uint16_t* tile = sU + (t / 2) * (kJB * 32) + 32 * half * 32;
+      const int o0 = tm_off<32>(4 * quad + j / 4, c), o1 = tm_off<32>(16 + 4 * quad + j / 4, c);
+      const bf16x8 uh = bfv(tm_frag(tile, o0, o1));
+      acc[t] = BF::run(uh, bfv(sl), acc[t]);
+      if constexpr (UP > 1) acc[t] = BF::run(bfv(tm_frag(tile + kJB * N, o0, o1)), bfv(sh), acc[t]);
+      acc[t] = BF::run(uh, bfv(sh), acc[t]);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < N / 16; ++t)
+    if (t / NT == half) acc[t] += tot[t % NT];
+  __syncthreads();
+  f32x4* join = reinterpret_cast<f32x4*>(sMem);
+  if (half == 1) {
+#pragma unroll
+    for (int t = 0; t < N / 16; ++t) join[(rt * (N / 16) + t) * 64 + lane] = acc[t];
+  }
+  __syncthreads();
+  if (half == 0 && f < rows) {
+    uint16_t* out = static_cast<uint16_t*>(DB ? p.dB : p.dC) + (q.row0 + f) * vrow + g * N;
+#pragma unroll
+    for (int t = 0; t < N / 16; ++t) {
+      const f32x4 v = acc[t] + join[(rt * (N / 16) + t) * 64 + lane];
+      *reinterpret_cast<uint2*>(out + 16 * t + 4 * quad) = make_uint2(pack2<IO>(v[0], v[1]), pack2<IO>(v[2], v[3]));
+    }
+  }
+}
+
+// ---- da, ddt ----------------------------------------------------------------------------
+// sum of v over the workgroup's 256 threads, in every thread
+__device__ __forceinline__ float block_sum(float v, float* sWave) {
+  v = row_sum(v);
+  v += __shfl_xor(v, 16, 64);
+  v += __shfl_xor(v, 32, 64);
+  __syncthreads();
+  if (threadIdx.x % 64 == 0) sWave[threadIdx.x / 64] = v;
+  __syncthreads();
+  return (sWave[0] + sWave[1]) + (sWave[2] + sWave[3]);
+}
+
+template <int IO>
+__global__ void __launch_bounds__(256) bwd_delta_kernel(SsdBwdParams p) {
+  __shared__ float sA[4], sB[4];
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;  // a wave is a piece
+  const int h = (int)(blockIdx.x % (uint32_t)p.nheads);
+  const Chunk q = chunk_of(p, (int)(blockIdx.x / (uint32_t)p.nheads));
+  const int64_t ph = (int64_t)q.place * p.nheads + h, at = ph * kQ + tid;
+  const int64_t other = p.batch * p.nchunks * p.nheads * kQ;  // the second half's sums
+  const bool in = tid < q.rows;
+  double pair = 0.0;
+  float row = 0.0f, col = 0.0f, e = 0.0f, out = 0.0f, xg = 0.0f, xd = 0.0f, delta = 0.0f, raw = 0.0f;
+  if (in) {
+    pair = (p.ws_rowin[at] + p.ws_rowin[other + at]) - (p.ws_colin[at] + p.ws_colin[other + at]);
+    row = p.ws_row[at] + p.ws_row[other + at];
+    col = p.ws_col[at] + p.ws_col[other + at];
+    e = p.ws_e[at] + p.ws_e[other + at];
+    out = p.ws_out[at] + p.ws_out[other + at];
+    xg = p.ws_xg[at] + p.ws_xg[other + at];
+    xd = p.ws_xd[at] + p.ws_xd[other + at];
+    delta = p.ws_delta[at];
+    raw = load_io<IO>(p.dt, (q.row0 + tid) * p.nheads + h) + (p.dt_bias ? p.dt_bias[h] : 0.0f);
+  }
+  const int nd = p.dstate / 4;
+  float dot = 0.0f;
+  for (int k = lane; k < nd; k += 64) dot += p.ws_dot[ph * nd + k];
+  // the pairs around the whole piece: of rows in piece 2 with piece 0 (entries
+  // 0, 1 the same), of rows in piece 3 with piece 0 (2) and pieces 0, 1 (3)
+  if (lane < 16) {
+    const float* span = p.ws_span + ph * 32;
+    if (wave == 1 && q.rows > 2 * kJB && lane < 8) dot += span[lane];
+    if (wave == 1 && q.rows > 3 * kJB && lane >= 8) dot += span[16 + lane - 8];
+    if (wave == 2 && q.rows > 3 * kJB && lane < 8) dot += span[24 + lane];
+  }
+  dot = row_sum(dot);
+  dot += __shfl_xor(dot, 16, 64);
+  dot += __shfl_xor(dot, 32, 64);
+  // from this step on (pair, row, e), and before this step (col, out)
+  float b = out;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const double u0 = __shfl_down(pair, off, 64);
+    const float u1 = __shfl_down(row, off, 64), u2 = __shfl_down(e, off, 64);
+    const float v1 = __shfl_up(col, off, 64), v2 = __shfl_up(b, off, 64);
+    if (lane + off < 64) {
+      pair += u0;
+      row += u1;
+      e += u2;
+    }
+    if (lane >= off) {
+      col += v1;
+      b += v2;
+    }
+  }
+  if (lane == 0) sA[wave] = e;
+  if (lane == 63) sB[wave] = b;
+  __syncthreads();
+  float a = (float)pair + row;
+  const float before = __shfl_up(col, 1, 64);
+  b = __shfl_up(b, 1, 64);
+  if (lane == 0) b = 0.0f;
+  if (lane > 0) a += before;
+  for (int k = wave + 1; k < 4; ++k) e += sA[k];
+  for (int k = 0; k < wave; ++k) b += sB[k];
+  a += e;
+  const float da = in ? a + b + dot : 0.0f;
+  float dr = fmaf(p.A[h], da, xg);
+  if (p.softplus) dr *= sigmoid_f(raw);
+  if (in) store_io<IO>(p.ddt, (q.row0 + tid) * p.nheads + h, dr);
+  __syncthreads();
+  const float s0 = block_sum(delta * da, sA), s1 = block_sum(in ? dr : 0.0f, sB), s2 = block_sum(xd, sA);
+  if (tid == 0) {
+    float* part = p.ws_part + ph * 3;
+    part[0] = s0;
+    part[1] = s1;
+    part[2] = s2;
+  }
+}
+
+__global__ void __launch_bounds__(256) bwd_sum_kernel(SsdBwdParams p) {
+  __shared__ float sW[4];
+  const int h = blockIdx.x;
+  const int places = (int)p.batch * p.nchunks;
+  float v[3] = {0.0f, 0.0f, 0.0f};
+  for (int k = threadIdx.x; k < places; k += 256)
+#pragma unroll
+    for (int e = 0; e < 3; ++e) v[e] += p.ws_part[((int64_t)k * p.nheads + h) * 3 + e];
+#pragma unroll
+  for (int e = 0; e < 3; ++e) v[e] = block_sum(v[e], sW);
+  if (threadIdx.x == 0) {
+    p.dA[h] = v[0];
+    if (p.ddt_bias) p.ddt_bias[h] = v[1];
+    if (p.dD) p.dD[h] = v[2];
+  }
+}
+
+#define SS_LAUNCH(k, grid, block)                                       \
+  do {                                                                  \
+    hipLaunchKernelGGL(k, dim3((uint32_t)(grid)), dim3(block), 0, st, p); \
+    const hipError_t e_ = hipGetLastError();                            \
+    if (e_ != hipSuccess) return e_;                                    \
+  } while (0)
+
+template <int MODE, int N>
+hipError_t launch_n(const SsdBwdParams& p, hipStream_t st) {
+  const int64_t places = p.batch * p.nchunks, heads = places * p.nheads, groups = places * p.ngroups * 4;
+  constexpr bool gate = MODE % 2 != 0;
+  SS_LAUNCH((bwd_state_kernel<MODE, N>), 2 * heads + groups * (gate ? 2 : 1), 256);
+  SS_LAUNCH((bwd_pass_kernel<N>), p.batch * p.nheads * (kP * N / 1024), 256);
+  SS_LAUNCH((bwd_scan_kernel<MODE, N, true>), heads, kScanThreads);
+  if constexpr (gate) SS_LAUNCH((bwd_scan_kernel<MODE, N, false>), heads, kScanThreads);
+  SS_LAUNCH((bwd_group_kernel<MODE, N, false>), groups, kGroupThreads);
+  SS_LAUNCH((bwd_group_kernel<MODE, N, true>), groups, kGroupThreads);
+  SS_LAUNCH((bwd_delta_kernel<io_of<MODE>()>), heads, 256);
+  SS_LAUNCH(bwd_sum_kernel, p.nheads, 256);
+  return hipSuccess;
+}
+template <int MODE>
+hipError_t launch_mode(const SsdBwdParams& p, hipStream_t st) {
+  switch (p.dstate) {
+    case 32: return launch_n<MODE, 32>(p, st);
+    case 64: return launch_n<MODE, 64>(p, st);
+    case 96: return launch_n<MODE, 96>(p, st);
+    default: return launch_n<MODE, 128>(p, st);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_ssd_bwd(int32_t io, const SsdBwdParams& p, hipStream_t st) {
+  PlaneJobs a{};
+  const int64_t rows = p.batch * p.seqlen;
+  const int parts = io == SS_F16 ? 2 : 1;
+  auto add = [&](const void* src, const void* gate, const uint16_t* const* to, int n_parts, int64_t n) {
+    if (n_parts == 1) return;
+    PlaneJob& j = a.j[a.n++];
+    j = PlaneJob{src, gate, {}, n_parts, n, n / 2048 < kPlaneBlocks ? (n + 2047) / 2048 : kPlaneBlocks};
+    for (int i = 0; i < n_parts; ++i) j.part[i] = const_cast<uint16_t*>(to[i]);
+  };
+  add(p.dy, p.z, p.gp, p.z ? 3 : parts, rows * p.nheads * kP);
+  add(p.x, nullptr, p.xp, parts, rows * p.nheads * kP);
+  add(p.Bm, nullptr, p.bp, parts, rows * p.ngroups * p.dstate);
+  add(p.Cm, nullptr, p.cp, parts, rows * p.ngroups * p.dstate);
+  if (a.n) {
+    int64_t blocks = 0;
+    for (int k = 0; k < a.n; ++k) blocks += a.j[k].blocks;
+    if (io == SS_F16) hipLaunchKernelGGL((bwd_planes_kernel<SS_F16>), dim3((uint32_t)blocks), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((bwd_planes_kernel<SS_BF16>), dim3((uint32_t)blocks), dim3(256), 0, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (io == SS_F16) return p.z ? launch_mode<3>(p, st) : launch_mode<2>(p, st);
+  return p.z ? launch_mode<1>(p, st) : launch_mode<0>(p, st);
+}
+
+}  // namespace ss

@@ -67,7 +67,8 @@ _lib = None
 EXPORTS = ("ss_fwd", "ss_fwd_step", "ss_bwd", "ss_fwd_workspace_size", "ss_fwd_workspace_min", "ss_bwd_workspace_size",
            "ss_ckpt_count", "ss_status_str", "ss_copy_probe", "ss_alu_probe", "ss_conv1d_fwd", "ss_conv1d_step",
            "ss_ssd_fwd", "ss_ssd_workspace_size", "ss_fwd_noalloc", "ss_fwd_noalloc_max_workspace", "ss_conv1d_prompt",
-           "ss_ssd_prompt", "ss_ssd_prompt_workspace_size", "ss_ssd_step", "ss_ssd_step_workspace_size")
+           "ss_ssd_prompt", "ss_ssd_prompt_workspace_size", "ss_ssd_step", "ss_ssd_step_workspace_size",
+           "ss_ssd_bwd", "ss_ssd_bwd_workspace_size", "ss_conv1d_bwd", "ss_conv1d_bwd_workspace_size")
 PROBE_KINDS = {"fma": 0, "exp": 1, "dpp_mul": 2, "scan_step": 3}
 
 
@@ -111,6 +112,14 @@ def load_library(path: str = LIB_PATH):
     lib.ss_ssd_workspace_size.argtypes = [SP]
     lib.ss_ssd_fwd.restype = ctypes.c_int
     lib.ss_ssd_fwd.argtypes = [SP] + [_vp] * 12 + [_vp, ctypes.c_size_t, _vp]
+    lib.ss_conv1d_bwd_workspace_size.restype = ctypes.c_size_t
+    lib.ss_conv1d_bwd_workspace_size.argtypes = [CP]
+    lib.ss_conv1d_bwd.restype = ctypes.c_int
+    lib.ss_conv1d_bwd.argtypes = [CP] + [_vp] * 11 + [_vp, ctypes.c_size_t, _vp]
+    lib.ss_ssd_bwd_workspace_size.restype = ctypes.c_size_t
+    lib.ss_ssd_bwd_workspace_size.argtypes = [SP, ctypes.c_int32]
+    lib.ss_ssd_bwd.restype = ctypes.c_int
+    lib.ss_ssd_bwd.argtypes = [SP] + [_vp] * 21 + [_vp, ctypes.c_size_t, _vp]
     VP = ctypes.POINTER(ss_conv_prompt_problem)
     lib.ss_conv1d_prompt.restype = ctypes.c_int
     lib.ss_conv1d_prompt.argtypes = [VP] + [_vp] * 8 + [_vp]
@@ -655,6 +664,88 @@ def ssd_prompt(x, dt, A, Bm, Cm, cu_seqlens, state, D=None, z=None, dt_bias=None
     return y
 
 
+def conv1d_bwd(x, w, dout, bias=None, silu=True, seq_idx=None, conv_init=None, dconv_final=None,
+               want_dconv_init=False, workspace=None):
+    """Gradients of conv1d for the loss sum(dout * out) + sum(dconv_final * conv_final); x, w, bias,
+    silu, seq_idx and conv_init as given to it.  Returns a dict: dx (B, D, L) in x's dtype, dw (D, W)
+    and dbias (D,) (with bias) fp32, dconv_init (B, D, W-1) fp32 when want_dconv_init."""
+    lib = load_library()
+    io = x.dtype
+    if io not in _IO:
+        raise TypeError("unsupported dtype %s" % io)
+    Bsz, Dd, L = x.shape
+    W = w.shape[-1]
+    x = _prep(x, io, "x")
+    dout = _prep(dout, io, "dout", (Bsz, Dd, L))
+    w = _prep(w.reshape(Dd, W), torch.float32, "w", (Dd, W))
+    bias = _prep(bias, torch.float32, "bias", (Dd,))
+    seq_idx = _prep(seq_idx, torch.int32, "seq_idx", (Bsz, L))
+    conv_init = _prep(conv_init, torch.float32, "conv_init", (Bsz, Dd, W - 1))
+    dconv_final = _prep(dconv_final, torch.float32, "dconv_final", (Bsz, Dd, W - 1))
+    _on(x.device, dout, w, bias, seq_idx, conv_init, dconv_final, workspace)
+    f32 = dict(dtype=torch.float32, device=x.device)
+    g = {"dx": torch.empty_like(x), "dw": torch.empty((Dd, W), **f32)}
+    if bias is not None:
+        g["dbias"] = torch.empty((Dd,), **f32)
+    if want_dconv_init:
+        g["dconv_init"] = torch.empty((Bsz, Dd, W - 1), **f32)
+    pr = ss_conv_problem(Bsz, Dd, L, W, _IO[io], 1 if silu else 0, 0)
+    workspace, wsz = _scratch(workspace, lib.ss_conv1d_bwd_workspace_size(ctypes.byref(pr)), x.device)
+    win = (lambda t: _ptr(t) if W > 1 else None)
+    _launch(x.device, lib.ss_conv1d_bwd, ctypes.byref(pr), _ptr(x), _ptr(w), _ptr(bias), _ptr(seq_idx),
+            win(conv_init), _ptr(dout), win(dconv_final), _ptr(g["dx"]), _ptr(g["dw"]), _ptr(g.get("dbias")),
+            win(g.get("dconv_init")), _ptr(workspace), wsz)
+    return g
+
+
+def ssd_bwd(x, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, dt_softplus=True, seq_idx=None, h0=None,
+            dfinal=None, want_dh0=False, workspace=None):
+    """Gradients of ssd_fwd for the loss sum(dy * y) + sum(dfinal * final_state); the inputs as given to
+    it (nothing else of the forward is needed).  Returns a dict: dx, ddt, dB, dC and dz (with z) in the
+    data's dtype, dA, dD (with D) and ddt_bias (with dt_bias) fp32, dh0 fp32 when want_dh0."""
+    lib = load_library()
+    io = x.dtype
+    if io not in (torch.float16, torch.bfloat16):
+        raise TypeError("ssd_bwd takes fp16 or bf16 data, got %s" % io)
+    Bsz, L, Hn, P = x.shape
+    G, N = Bm.shape[2], Bm.shape[3]
+    x = _prep(x, io, "x")
+    dy = _prep(dy, io, "dy", (Bsz, L, Hn, P))
+    dt = _prep(dt, io, "dt", (Bsz, L, Hn))
+    Bm = _prep(Bm, io, "Bm", (Bsz, L, G, N))
+    Cm = _prep(Cm, io, "Cm", (Bsz, L, G, N))
+    z = _prep(z, io, "z", (Bsz, L, Hn, P))
+    A = _prep(A, torch.float32, "A", (Hn,))
+    D = _prep(D, torch.float32, "D", (Hn,))
+    dt_bias = _prep(dt_bias, torch.float32, "dt_bias", (Hn,))
+    h0 = _prep(h0, torch.float32, "h0", (Bsz, Hn, P, N))
+    dfinal = _prep(dfinal, torch.float32, "dfinal", (Bsz, Hn, P, N))
+    seq_idx = _prep(seq_idx, torch.int32, "seq_idx", (Bsz, L))
+    _on(x.device, dy, dt, Bm, Cm, z, A, D, dt_bias, h0, dfinal, seq_idx, workspace)
+    pr = ss_ssd_problem(Bsz, L, Hn, G, P, N, _IO[io], 1 if dt_softplus else 0)
+    wsz = lib.ss_ssd_bwd_workspace_size(ctypes.byref(pr), 0 if z is None else 1)
+    if wsz == 0:
+        raise RuntimeError("ss_ssd_bwd: unsupported problem (headdim must be 64, dstate 32/64/96/128, "
+                           "ngroups dividing nheads, sizes within the launch limits)")
+    f32 = dict(dtype=torch.float32, device=x.device)
+    g = {"dx": torch.empty_like(x), "ddt": torch.empty_like(dt), "dA": torch.empty((Hn,), **f32),
+         "dB": torch.empty_like(Bm), "dC": torch.empty_like(Cm)}
+    if D is not None:
+        g["dD"] = torch.empty((Hn,), **f32)
+    if z is not None:
+        g["dz"] = torch.empty_like(z)
+    if dt_bias is not None:
+        g["ddt_bias"] = torch.empty((Hn,), **f32)
+    if want_dh0:
+        g["dh0"] = torch.empty((Bsz, Hn, P, N), **f32)
+    workspace, wsz = _scratch(workspace, wsz, x.device)
+    _launch(x.device, lib.ss_ssd_bwd, ctypes.byref(pr), _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D),
+            _ptr(z), _ptr(dt_bias), _ptr(seq_idx), _ptr(h0), _ptr(dy), _ptr(dfinal), _ptr(g["dx"]), _ptr(g["ddt"]),
+            _ptr(g["dA"]), _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g.get("dD")), _ptr(g.get("dz")),
+            _ptr(g.get("ddt_bias")), _ptr(g.get("dh0")), _ptr(workspace), wsz)
+    return g
+
+
 def _step_problem(xbc, state, w, ngroups, xs, zs, ds, dt_softplus):
     nslots, Hn, P, N = state.shape
     return ss_ssd_step_problem(xbc.shape[0], nslots, Hn, ngroups, xs, zs, ds, P, N, w.shape[-1], _IO[xbc.dtype],
@@ -822,3 +913,54 @@ def selective_scan_fn(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, delt
     change of document id; h0 (B, D, N) fp32 is the initial state."""
     return SelectiveScanFn.apply(u, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus, return_last_state,
                                  seq_idx, h0)
+
+
+class Conv1dFn(torch.autograd.Function):
+    """autograd wrapper: forward = ss_conv1d_fwd, backward = ss_conv1d_bwd.  Differentiable in x, w,
+    bias and the window before the row; conv_final is a second output with return_final."""
+
+    @staticmethod
+    def forward(ctx, x, w, bias, silu, seq_idx, conv_init, return_final):
+        ctx.save_for_backward(x, w, bias, seq_idx, conv_init)
+        ctx.silu, ctx.width = silu, w.shape[-1]
+        return conv1d(x, w, bias, silu=silu, seq_idx=seq_idx, conv_init=conv_init, return_final=return_final)
+
+    @staticmethod
+    def backward(ctx, dout, dfinal=None):
+        x, w, bias, seq_idx, conv_init = ctx.saved_tensors
+        g = conv1d_bwd(x, w, dout.contiguous(), bias=bias, silu=ctx.silu, seq_idx=seq_idx, conv_init=conv_init,
+                       dconv_final=dfinal if dfinal is None or ctx.width > 1 else None,
+                       want_dconv_init=ctx.needs_input_grad[5])
+        return (g["dx"], g["dw"].reshape(w.shape), g.get("dbias"), None, None, g.get("dconv_init"), None)
+
+
+def conv1d_fn(x, w, bias=None, silu=True, seq_idx=None, conv_init=None, return_final=False):
+    """conv1d, differentiable: out, or (out, conv_final) with return_final."""
+    return Conv1dFn.apply(x, w, bias, silu, seq_idx, conv_init, return_final)
+
+
+class SsdScanFn(torch.autograd.Function):
+    """autograd wrapper: forward = ss_ssd_fwd, backward = ss_ssd_bwd (the states are rebuilt, so only
+    the inputs are kept).  Differentiable in every floating input; with return_final_state the final
+    state is a second output."""
+
+    @staticmethod
+    def forward(ctx, x, dt, A, Bm, Cm, D, z, dt_bias, dt_softplus, seq_idx, h0, return_final_state):
+        ctx.save_for_backward(x, dt, A, Bm, Cm, D, z, dt_bias, seq_idx, h0)
+        ctx.dt_softplus = dt_softplus
+        return ssd_fwd(x, dt, A, Bm, Cm, D=D, z=z, dt_bias=dt_bias, dt_softplus=dt_softplus, h0=h0,
+                       return_final_state=return_final_state, seq_idx=seq_idx)
+
+    @staticmethod
+    def backward(ctx, dy, dfinal=None):
+        x, dt, A, Bm, Cm, D, z, dt_bias, seq_idx, h0 = ctx.saved_tensors
+        g = ssd_bwd(x, dt, A, Bm, Cm, dy.contiguous(), D=D, z=z, dt_bias=dt_bias, dt_softplus=ctx.dt_softplus,
+                    seq_idx=seq_idx, h0=h0, dfinal=dfinal, want_dh0=ctx.needs_input_grad[10])
+        return (g["dx"], g["ddt"], g["dA"], g["dB"], g["dC"], g.get("dD"), g.get("dz"), g.get("ddt_bias"), None, None,
+                g.get("dh0"), None)
+
+
+def ssd_scan_fn(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, dt_softplus=True, seq_idx=None, h0=None,
+                return_final_state=False):
+    """ssd_fwd, differentiable: y, or (y, final_state) with return_final_state."""
+    return SsdScanFn.apply(x, dt, A, Bm, Cm, D, z, dt_bias, dt_softplus, seq_idx, h0, return_final_state)
