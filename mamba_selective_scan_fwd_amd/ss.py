@@ -8,6 +8,7 @@ raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -533,65 +534,114 @@ def ssd_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, dt_softplus=True, h0
     return (y, fin) if return_final_state else y
 
 
-def _rows(t, dtype, name, shape, vector=True):
-    """(tensor, elements between rows) for an operand whose rows (shape[1:]) lie whole but possibly
+# The layer operators below check their tensors with few Python steps: for a
+# single token the call itself is what a program waits for.
+def _refuse(t, dtype, name, shape, dev):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    raise ValueError("%s must be on cuda:%d, where the data are, got %s" % (name, dev, t.device))
+
+
+def _in(t, dtype, name, shape, dev, keep):
+    """An operand's address (None: no operand); copied, and the copy put into keep, only if it is not
+    contiguous and 16-byte aligned."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(t, dtype, name, shape, dev)
+    at = t.data_ptr()
+    if at & 15 or not t.is_contiguous():
+        t = t.contiguous()
+        if t.data_ptr() & 15:
+            t = t.clone()
+        keep.append(t)
+        at = t.data_ptr()
+    return at
+
+
+def _rows(t, dtype, name, shape, dev, keep, vector=True):
+    """(address, elements between rows) of an operand whose rows (shape[1:]) lie whole but possibly
     apart, such as the columns of a projection's output; copied only where they do not, or where
     vector access needs rows on 16-byte boundaries and they are not."""
     if t is None:
         return None, 0
-    if not t.is_cuda:
-        raise ValueError("%s must be a device tensor" % name)
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    size = 1
-    whole = True
-    for n, st in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        whole = whole and (n == 1 or st == size)
-        size *= n
-    stride = t.stride(0) if t.shape[0] > 1 else size
-    if not whole or stride < size or stride > 1 << 21 or \
-            (vector and (t.data_ptr() % 16 or stride * t.element_size() % 16)):
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(t, dtype, name, shape, dev)
+    strides = t.stride()
+    size, whole = 1, True
+    for k in range(len(shape) - 1, 0, -1):
+        whole = whole and (strides[k] == size or shape[k] == 1)
+        size *= shape[k]
+    stride, at = strides[0] if shape[0] > 1 else size, t.data_ptr()
+    if not whole or stride < size or stride > 1 << 21 or (vector and (at & 15 or stride * t.element_size() & 15)):
         t, stride = t.contiguous(), size
-        if vector and t.data_ptr() % 16:
+        if vector and t.data_ptr() & 15:
             t = t.clone()
-    return t, stride
+        keep.append(t)
+        at = t.data_ptr()
+    return at, stride
 
 
-def _inplace(t, dtype, name, shape):
-    """A tensor that the call writes: taken as it is or refused, never copied."""
+def _inplace(t, dtype, name, shape, dev):
+    """The address of a tensor that the call writes: taken as it is or refused, never copied."""
     if t is None:
         return None
-    if not (t.is_cuda and t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous()
-            and t.data_ptr() % 16 == 0):
-        raise ValueError("%s must be a contiguous, 16-byte aligned %s device tensor of shape %s"
-                         % (name, dtype, tuple(shape)))
-    return t
+    at = t.data_ptr()
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or at & 15 or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous, 16-byte aligned %s tensor of shape %s on cuda:%d"
+                         % (name, dtype, shape, dev))
+    return at
 
 
-def _on(device, *tensors):
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError("all tensors must be on %s, got one on %s" % (device, t.device))
+def _device(t):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("the operands must be device tensors")
+    return dev
 
 
-def _launch(device, fn, *args):
+@functools.lru_cache(maxsize=256)
+def _problem(kind, size, sizes, *fields):
+    """(problem, bytes of its workspace) of a C call, by its sizes."""
+    pr = kind(*fields)
+    return pr, getattr(load_library(), size)(ctypes.byref(pr), *sizes) if size else 0
+
+
+def _launch(dev, fn, problem, *args):
     """The C call on the current stream of the tensors' device, whichever device is current."""
-    if torch.cuda.current_device() == device.index:
-        status = fn(*args, _stream(device))
+    stream = torch._C._cuda_getCurrentRawStream(dev)  # torch.cuda.current_stream(dev).cuda_stream, 1 us sooner
+    if torch.cuda.current_device() == dev:
+        status = fn(problem, *args, stream)
     else:
-        with torch.cuda.device(device):
-            status = fn(*args, _stream(device))
+        with torch.cuda.device(dev):
+            status = fn(problem, *args, stream)
     if status != 0:
         _check(status)
 
 
-def _scratch(workspace, nbytes, device):
-    """The given workspace (the library checks its size), or a new one."""
+def _scratch(workspace, nbytes, dev):
+    """The given workspace (the library checks its size), or a new one: the tensor, its address, its bytes."""
     if workspace is None:
-        workspace = torch.empty((nbytes + 3) // 4, dtype=torch.float32, device=device)
-    return workspace, workspace.numel() * workspace.element_size()
+        if not nbytes:
+            return None, None, 0
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=_DEVICES[dev])
+        return workspace, workspace.data_ptr(), nbytes
+    if workspace.get_device() != dev:
+        raise ValueError("the workspace must be on cuda:%d" % dev)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+class _Devices(dict):
+    def __missing__(self, dev):
+        self[dev] = torch.device("cuda", dev)
+        return self[dev]
+
+
+_DEVICES = _Devices()
 
 
 def conv1d_prompt(x, w, cu_seqlens, conv_state, bias=None, silu=True, slots=None, has_state=None, out=None):
@@ -605,27 +655,23 @@ def conv1d_prompt(x, w, cu_seqlens, conv_state, bias=None, silu=True, slots=None
     io = x.dtype
     if io not in _IO:
         raise TypeError("unsupported dtype %s" % io)
+    dev, keep, f32, i32 = _device(x), [], torch.float32, torch.int32
     T, Dd = x.shape
-    W, S = w.shape[-1], cu_seqlens.numel() - 1
-    x, xs = _rows(x, io, "x", (T, Dd), vector=False)
-    w = _prep(w.reshape(Dd, W), torch.float32, "w", (Dd, W))
-    bias = _prep(bias, torch.float32, "bias", (Dd,))
-    cu_seqlens = _prep(cu_seqlens, torch.int32, "cu_seqlens", (S + 1,))
-    slots = _prep(slots, torch.int32, "slots", (S,))
-    has_state = _prep(has_state, torch.int32, "has_state", (S,))
-    nslots = conv_state.shape[0]
-    conv_state = _inplace(conv_state, torch.float32, "conv_state", (nslots, Dd, W - 1))
+    W, S, nslots = w.shape[-1], cu_seqlens.numel() - 1, conv_state.shape[0]
+    if w.dim() != 2:
+        w = w.reshape(Dd, W)
     if out is None:
-        out, os_ = torch.empty((T, Dd), dtype=io, device=x.device), Dd
-    else:
-        given = out
-        out, os_ = _rows(out, io, "out", (T, Dd), vector=False)
-        if out is not given:
-            raise ValueError("the rows of out must lie whole, at most 2^21 elements apart")
-    _on(x.device, w, bias, cu_seqlens, slots, has_state, conv_state, out)
-    pr = ss_conv_prompt_problem(T, S, Dd, nslots, xs, os_, W, _IO[io], 1 if silu else 0, 0)
-    _launch(x.device, lib.ss_conv1d_prompt, ctypes.byref(pr), _ptr(x), _ptr(w), _ptr(bias), _ptr(cu_seqlens),
-            _ptr(slots), _ptr(has_state), _ptr(conv_state) if W > 1 else None, _ptr(out))
+        out = torch.empty((T, Dd), dtype=io, device=x.device)
+    xa, xs = _rows(x, io, "x", (T, Dd), dev, keep, False)
+    oa, os_ = _rows(out, io, "out", (T, Dd), dev, [], False)
+    if oa != out.data_ptr():
+        raise ValueError("the rows of out must lie whole, at most 2^21 elements apart")
+    pr, _ = _problem(ss_conv_prompt_problem, None, (), T, S, Dd, nslots, xs, os_, W, _IO[io], 1 if silu else 0, 0)
+    st = _inplace(conv_state, f32, "conv_state", (nslots, Dd, W - 1), dev)
+    _launch(dev, lib.ss_conv1d_prompt, pr, xa, _in(w, f32, "w", (Dd, W), dev, keep),
+            _in(bias, f32, "bias", (Dd,), dev, keep), _in(cu_seqlens, i32, "cu_seqlens", (S + 1,), dev, keep),
+            _in(slots, i32, "slots", (S,), dev, keep), _in(has_state, i32, "has_state", (S,), dev, keep),
+            st if W > 1 else None, oa)
     return out
 
 
@@ -639,28 +685,25 @@ def ssd_prompt(x, dt, A, Bm, Cm, cu_seqlens, state, D=None, z=None, dt_bias=None
     io = x.dtype
     if io not in (torch.float16, torch.bfloat16):
         raise TypeError("ssd_prompt takes fp16 or bf16 data, got %s" % io)
+    dev, keep, f32, i32 = _device(x), [], torch.float32, torch.int32
     T, Hn, P = x.shape
-    G, N, S = Bm.shape[1], Bm.shape[2], cu_seqlens.numel() - 1
-    x, xs = _rows(x, io, "x", (T, Hn, P))
-    z, zs = _rows(z, io, "z", (T, Hn, P))
-    Bm, bs = _rows(Bm, io, "Bm", (T, G, N))
-    Cm, cs = _rows(Cm, io, "Cm", (T, G, N))
-    dt, ds = _rows(dt, io, "dt", (T, Hn), vector=False)
-    A = _prep(A, torch.float32, "A", (Hn,))
-    D = _prep(D, torch.float32, "D", (Hn,))
-    dt_bias = _prep(dt_bias, torch.float32, "dt_bias", (Hn,))
-    cu_seqlens = _prep(cu_seqlens, torch.int32, "cu_seqlens", (S + 1,))
-    slots = _prep(slots, torch.int32, "slots", (S,))
-    has_state = _prep(has_state, torch.int32, "has_state", (S,))
-    nslots = state.shape[0]
-    state = _inplace(state, torch.float32, "state", (nslots, Hn, P, N))
-    y = torch.empty((T, Hn, P), dtype=io, device=x.device) if y is None else _inplace(y, io, "y", (T, Hn, P))
-    _on(x.device, z, Bm, Cm, dt, A, D, dt_bias, cu_seqlens, slots, has_state, state, y, workspace)
-    pr = ss_ssd_prompt_problem(T, S, nslots, Hn, G, xs, bs, cs, zs, ds, P, N, _IO[io], 1 if dt_softplus else 0)
-    workspace, wsz = _scratch(workspace, lib.ss_ssd_prompt_workspace_size(ctypes.byref(pr)), x.device)
-    _launch(x.device, lib.ss_ssd_prompt, ctypes.byref(pr), _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D),
-            _ptr(z), _ptr(dt_bias), _ptr(cu_seqlens), _ptr(slots), _ptr(has_state), _ptr(state), _ptr(y),
-            _ptr(workspace), wsz)
+    _, G, N = Bm.shape
+    S, nslots = cu_seqlens.numel() - 1, state.shape[0]
+    if y is None:
+        y = torch.empty((T, Hn, P), dtype=io, device=x.device)
+    xa, xs = _rows(x, io, "x", (T, Hn, P), dev, keep)
+    za, zs = _rows(z, io, "z", (T, Hn, P), dev, keep)
+    ba, bs = _rows(Bm, io, "Bm", (T, G, N), dev, keep)
+    ca, cs = _rows(Cm, io, "Cm", (T, G, N), dev, keep)
+    da, ds = _rows(dt, io, "dt", (T, Hn), dev, keep, False)
+    pr, wsz = _problem(ss_ssd_prompt_problem, "ss_ssd_prompt_workspace_size", (), T, S, nslots, Hn, G, xs, bs, cs, zs,
+                       ds, P, N, _IO[io], 1 if dt_softplus else 0)
+    workspace, wa, wsz = _scratch(workspace, wsz, dev)
+    _launch(dev, lib.ss_ssd_prompt, pr, xa, da, _in(A, f32, "A", (Hn,), dev, keep), ba, ca,
+            _in(D, f32, "D", (Hn,), dev, keep), za, _in(dt_bias, f32, "dt_bias", (Hn,), dev, keep),
+            _in(cu_seqlens, i32, "cu_seqlens", (S + 1,), dev, keep), _in(slots, i32, "slots", (S,), dev, keep),
+            _in(has_state, i32, "has_state", (S,), dev, keep), _inplace(state, f32, "state", (nslots, Hn, P, N), dev),
+            _inplace(y, io, "y", (T, Hn, P), dev), wa, wsz)
     return y
 
 
@@ -673,28 +716,32 @@ def conv1d_bwd(x, w, dout, bias=None, silu=True, seq_idx=None, conv_init=None, d
     io = x.dtype
     if io not in _IO:
         raise TypeError("unsupported dtype %s" % io)
+    dev, keep, f32 = _device(x), [], torch.float32
     Bsz, Dd, L = x.shape
     W = w.shape[-1]
-    x = _prep(x, io, "x")
-    dout = _prep(dout, io, "dout", (Bsz, Dd, L))
-    w = _prep(w.reshape(Dd, W), torch.float32, "w", (Dd, W))
-    bias = _prep(bias, torch.float32, "bias", (Dd,))
-    seq_idx = _prep(seq_idx, torch.int32, "seq_idx", (Bsz, L))
-    conv_init = _prep(conv_init, torch.float32, "conv_init", (Bsz, Dd, W - 1))
-    dconv_final = _prep(dconv_final, torch.float32, "dconv_final", (Bsz, Dd, W - 1))
-    _on(x.device, dout, w, bias, seq_idx, conv_init, dconv_final, workspace)
-    f32 = dict(dtype=torch.float32, device=x.device)
-    g = {"dx": torch.empty_like(x), "dw": torch.empty((Dd, W), **f32)}
+    win = (Bsz, Dd, W - 1)
+    if w.dim() != 2:
+        w = w.reshape(Dd, W)
+    if not x.is_contiguous():
+        x = x.contiguous()
+    g = {"dx": torch.empty_like(x), "dw": torch.empty((Dd, W), dtype=f32, device=x.device)}
     if bias is not None:
-        g["dbias"] = torch.empty((Dd,), **f32)
+        g["dbias"] = torch.empty((Dd,), dtype=f32, device=x.device)
     if want_dconv_init:
-        g["dconv_init"] = torch.empty((Bsz, Dd, W - 1), **f32)
-    pr = ss_conv_problem(Bsz, Dd, L, W, _IO[io], 1 if silu else 0, 0)
-    workspace, wsz = _scratch(workspace, lib.ss_conv1d_bwd_workspace_size(ctypes.byref(pr)), x.device)
-    win = (lambda t: _ptr(t) if W > 1 else None)
-    _launch(x.device, lib.ss_conv1d_bwd, ctypes.byref(pr), _ptr(x), _ptr(w), _ptr(bias), _ptr(seq_idx),
-            win(conv_init), _ptr(dout), win(dconv_final), _ptr(g["dx"]), _ptr(g["dw"]), _ptr(g.get("dbias")),
-            win(g.get("dconv_init")), _ptr(workspace), wsz)
+        g["dconv_init"] = torch.empty(win, dtype=f32, device=x.device)
+    pr, wsz = _problem(ss_conv_problem, "ss_conv1d_bwd_workspace_size", (), Bsz, Dd, L, W, _IO[io], 1 if silu else 0, 0)
+    if wsz:
+        workspace, wa, wsz = _scratch(workspace, wsz, dev)
+    else:
+        wa = None
+    args = [_in(x, io, "x", (Bsz, Dd, L), dev, keep), _in(w, f32, "w", (Dd, W), dev, keep),
+            _in(bias, f32, "bias", (Dd,), dev, keep), _in(seq_idx, torch.int32, "seq_idx", (Bsz, L), dev, keep),
+            _in(conv_init, f32, "conv_init", win, dev, keep), _in(dout, io, "dout", (Bsz, Dd, L), dev, keep),
+            _in(dconv_final, f32, "dconv_final", win, dev, keep)]
+    if W == 1:  # windows of no entries
+        args[4] = args[6] = None
+    _launch(dev, lib.ss_conv1d_bwd, pr, *args, g["dx"].data_ptr(), g["dw"].data_ptr(), _ptr_of(g, "dbias"),
+            _ptr_of(g, "dconv_init") if W > 1 else None, wa, wsz)
     return g
 
 
@@ -707,49 +754,39 @@ def ssd_bwd(x, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, dt_softplus=True
     io = x.dtype
     if io not in (torch.float16, torch.bfloat16):
         raise TypeError("ssd_bwd takes fp16 or bf16 data, got %s" % io)
+    dev, keep, f32 = _device(x), [], torch.float32
     Bsz, L, Hn, P = x.shape
     G, N = Bm.shape[2], Bm.shape[3]
-    x = _prep(x, io, "x")
-    dy = _prep(dy, io, "dy", (Bsz, L, Hn, P))
-    dt = _prep(dt, io, "dt", (Bsz, L, Hn))
-    Bm = _prep(Bm, io, "Bm", (Bsz, L, G, N))
-    Cm = _prep(Cm, io, "Cm", (Bsz, L, G, N))
-    z = _prep(z, io, "z", (Bsz, L, Hn, P))
-    A = _prep(A, torch.float32, "A", (Hn,))
-    D = _prep(D, torch.float32, "D", (Hn,))
-    dt_bias = _prep(dt_bias, torch.float32, "dt_bias", (Hn,))
-    h0 = _prep(h0, torch.float32, "h0", (Bsz, Hn, P, N))
-    dfinal = _prep(dfinal, torch.float32, "dfinal", (Bsz, Hn, P, N))
-    seq_idx = _prep(seq_idx, torch.int32, "seq_idx", (Bsz, L))
-    _on(x.device, dy, dt, Bm, Cm, z, A, D, dt_bias, h0, dfinal, seq_idx, workspace)
-    pr = ss_ssd_problem(Bsz, L, Hn, G, P, N, _IO[io], 1 if dt_softplus else 0)
-    wsz = lib.ss_ssd_bwd_workspace_size(ctypes.byref(pr), 0 if z is None else 1)
+    xs, bs, hs, vs = (Bsz, L, Hn, P), (Bsz, L, G, N), (Bsz, Hn, P, N), (Hn,)
+    pr, wsz = _problem(ss_ssd_problem, "ss_ssd_bwd_workspace_size", (0 if z is None else 1,), Bsz, L, Hn, G, P, N,
+                       _IO[io], 1 if dt_softplus else 0)
     if wsz == 0:
         raise RuntimeError("ss_ssd_bwd: unsupported problem (headdim must be 64, dstate 32/64/96/128, "
                            "ngroups dividing nheads, sizes within the launch limits)")
-    f32 = dict(dtype=torch.float32, device=x.device)
-    g = {"dx": torch.empty_like(x), "ddt": torch.empty_like(dt), "dA": torch.empty((Hn,), **f32),
-         "dB": torch.empty_like(Bm), "dC": torch.empty_like(Cm)}
+    args = [_in(x, io, "x", xs, dev, keep), _in(dt, io, "dt", (Bsz, L, Hn), dev, keep), _in(A, f32, "A", vs, dev, keep),
+            _in(Bm, io, "Bm", bs, dev, keep), _in(Cm, io, "Cm", bs, dev, keep), _in(D, f32, "D", vs, dev, keep),
+            _in(z, io, "z", xs, dev, keep), _in(dt_bias, f32, "dt_bias", vs, dev, keep),
+            _in(seq_idx, torch.int32, "seq_idx", (Bsz, L), dev, keep), _in(h0, f32, "h0", hs, dev, keep),
+            _in(dy, io, "dy", xs, dev, keep), _in(dfinal, f32, "dfinal", hs, dev, keep)]
+    new = (lambda shape, dtype: torch.empty(shape, dtype=dtype, device=_DEVICES[dev]))
+    g = {"dx": new(xs, io), "ddt": new((Bsz, L, Hn), io), "dA": new(vs, f32), "dB": new(bs, io), "dC": new(bs, io)}
     if D is not None:
-        g["dD"] = torch.empty((Hn,), **f32)
+        g["dD"] = new(vs, f32)
     if z is not None:
-        g["dz"] = torch.empty_like(z)
+        g["dz"] = new(xs, io)
     if dt_bias is not None:
-        g["ddt_bias"] = torch.empty((Hn,), **f32)
+        g["ddt_bias"] = new(vs, f32)
     if want_dh0:
-        g["dh0"] = torch.empty((Bsz, Hn, P, N), **f32)
-    workspace, wsz = _scratch(workspace, wsz, x.device)
-    _launch(x.device, lib.ss_ssd_bwd, ctypes.byref(pr), _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D),
-            _ptr(z), _ptr(dt_bias), _ptr(seq_idx), _ptr(h0), _ptr(dy), _ptr(dfinal), _ptr(g["dx"]), _ptr(g["ddt"]),
-            _ptr(g["dA"]), _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g.get("dD")), _ptr(g.get("dz")),
-            _ptr(g.get("ddt_bias")), _ptr(g.get("dh0")), _ptr(workspace), wsz)
+        g["dh0"] = new(hs, f32)
+    workspace, wa, wsz = _scratch(workspace, wsz, dev)
+    _launch(dev, lib.ss_ssd_bwd, pr, *args, *(_ptr_of(g, k) for k in ("dx", "ddt", "dA", "dB", "dC", "dD", "dz",
+                                                                     "ddt_bias", "dh0")), wa, wsz)
     return g
 
 
-def _step_problem(xbc, state, w, ngroups, xs, zs, ds, dt_softplus):
-    nslots, Hn, P, N = state.shape
-    return ss_ssd_step_problem(xbc.shape[0], nslots, Hn, ngroups, xs, zs, ds, P, N, w.shape[-1], _IO[xbc.dtype],
-                               1 if dt_softplus else 0, 0)
+def _ptr_of(g, name):
+    t = g.get(name)
+    return None if t is None else t.data_ptr()
 
 
 def ssd_step(xbc, dt, A, conv_w, conv_state, state, ngroups=1, conv_bias=None, D=None, z=None, dt_bias=None,
@@ -764,27 +801,26 @@ def ssd_step(xbc, dt, A, conv_w, conv_state, state, ngroups=1, conv_bias=None, D
     io = xbc.dtype
     if io not in (torch.float16, torch.bfloat16):
         raise TypeError("ssd_step takes fp16 or bf16 data, got %s" % io)
+    dev, keep, f32 = _device(xbc), [], torch.float32
     n = xbc.shape[0]
     nslots, Hn, P, N = state.shape
     ch, W = Hn * P + 2 * ngroups * N, conv_w.shape[-1]
-    xbc, xs = _rows(xbc, io, "xbc", (n, ch), vector=False)
-    dt, ds = _rows(dt, io, "dt", (n, Hn), vector=False)
-    z, zs = _rows(z, io, "z", (n, Hn, P), vector=False)
-    A = _prep(A, torch.float32, "A", (Hn,))
-    D = _prep(D, torch.float32, "D", (Hn,))
-    dt_bias = _prep(dt_bias, torch.float32, "dt_bias", (Hn,))
-    conv_w = _prep(conv_w.reshape(ch, W), torch.float32, "conv_w", (ch, W))
-    conv_bias = _prep(conv_bias, torch.float32, "conv_bias", (ch,))
-    slots = _prep(slots, torch.int32, "slots", (n,))
-    conv_state = _inplace(conv_state, torch.float32, "conv_state", (nslots, ch, W - 1))
-    state = _inplace(state, torch.float32, "state", (nslots, Hn, P, N))
-    y = torch.empty((n, Hn, P), dtype=io, device=xbc.device) if y is None else _inplace(y, io, "y", (n, Hn, P))
-    _on(xbc.device, dt, z, A, D, dt_bias, conv_w, conv_bias, slots, conv_state, state, y, workspace)
-    pr = _step_problem(xbc, state, conv_w, ngroups, xs, zs, ds, dt_softplus)
-    workspace, wsz = _scratch(workspace, lib.ss_ssd_step_workspace_size(ctypes.byref(pr)), xbc.device)
-    _launch(xbc.device, lib.ss_ssd_step, ctypes.byref(pr), _ptr(xbc), _ptr(dt), _ptr(A), _ptr(conv_w),
-            _ptr(conv_bias), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(slots), _ptr(conv_state) if W > 1 else None,
-            _ptr(state), _ptr(y), _ptr(workspace), wsz)
+    if conv_w.dim() != 2:
+        conv_w = conv_w.reshape(ch, W)
+    if y is None:
+        y = torch.empty((n, Hn, P), dtype=io, device=xbc.device)
+    xa, xs = _rows(xbc, io, "xbc", (n, ch), dev, keep, False)
+    da, ds = _rows(dt, io, "dt", (n, Hn), dev, keep, False)
+    za, zs = _rows(z, io, "z", (n, Hn, P), dev, keep, False)
+    st = _inplace(conv_state, f32, "conv_state", (nslots, ch, W - 1), dev)
+    pr, wsz = _problem(ss_ssd_step_problem, "ss_ssd_step_workspace_size", (), n, nslots, Hn, ngroups, xs, zs, ds, P, N,
+                       W, _IO[io], 1 if dt_softplus else 0, 0)
+    workspace, wa, wsz = _scratch(workspace, wsz, dev)
+    _launch(dev, lib.ss_ssd_step, pr, xa, da, _in(A, f32, "A", (Hn,), dev, keep),
+            _in(conv_w, f32, "conv_w", (ch, W), dev, keep), _in(conv_bias, f32, "conv_bias", (ch,), dev, keep),
+            _in(D, f32, "D", (Hn,), dev, keep), za, _in(dt_bias, f32, "dt_bias", (Hn,), dev, keep),
+            _in(slots, torch.int32, "slots", (n,), dev, keep), st if W > 1 else None,
+            _inplace(state, f32, "state", (nslots, Hn, P, N), dev), _inplace(y, io, "y", (n, Hn, P), dev), wa, wsz)
     return y
 
 
@@ -799,34 +835,28 @@ class SsdStepCall:
         io = xbc.dtype
         if io not in (torch.float16, torch.bfloat16):
             raise TypeError("ssd_step takes fp16 or bf16 data, got %s" % io)
+        dev, keep, f32 = _device(xbc), [], torch.float32
         n = xbc.shape[0]
         nslots, Hn, P, N = state.shape
         ch, W = Hn * P + 2 * ngroups * N, conv_w.shape[-1]
-        strides = []
-        for t, name, shape in ((xbc, "xbc", (n, ch)), (z, "z", (n, Hn, P)), (dt, "dt", (n, Hn))):
-            same, st = _rows(t, io, name, shape, vector=False)
-            if same is not t:
-                raise ValueError("the rows of %s must lie whole, at most 2^21 elements apart" % name)
-            strides.append(st)
-        for t, dtype, name, shape in ((A, torch.float32, "A", (Hn,)), (D, torch.float32, "D", (Hn,)),
-                                      (dt_bias, torch.float32, "dt_bias", (Hn,)),
-                                      (conv_w, torch.float32, "conv_w", (ch, W)),
-                                      (conv_bias, torch.float32, "conv_bias", (ch,)),
-                                      (slots, torch.int32, "slots", (n,)),
-                                      (conv_state, torch.float32, "conv_state", (nslots, ch, W - 1)),
-                                      (state, torch.float32, "state", (nslots, Hn, P, N)), (y, io, "y", (n, Hn, P))):
-            _inplace(t, dtype, name, shape)
+        (xa, xs), (za, zs), (da, ds) = (_rows(t, io, name, shape, dev, keep, False) for t, name, shape in
+                                        ((xbc, "xbc", (n, ch)), (z, "z", (n, Hn, P)), (dt, "dt", (n, Hn))))
+        if keep:
+            raise ValueError("the rows of xbc, z and dt must lie whole, at most 2^21 elements apart")
         if y is None:
             raise ValueError("SsdStepCall needs its output y")
-        _on(xbc.device, dt, z, A, D, dt_bias, conv_w, conv_bias, slots, conv_state, state, y)
-        self.pr = _step_problem(xbc, state, conv_w, ngroups, *strides, dt_softplus)
-        self.device = xbc.device
-        self.ws, wsz = _scratch(None, lib.ss_ssd_step_workspace_size(ctypes.byref(self.pr)), xbc.device)
+        at = [_inplace(t, dtype, name, shape, dev) for t, dtype, name, shape in (
+            (A, f32, "A", (Hn,)), (conv_w, f32, "conv_w", (ch, W)), (conv_bias, f32, "conv_bias", (ch,)),
+            (D, f32, "D", (Hn,)), (dt_bias, f32, "dt_bias", (Hn,)), (slots, torch.int32, "slots", (n,)),
+            (conv_state, f32, "conv_state", (nslots, ch, W - 1)), (state, f32, "state", (nslots, Hn, P, N)),
+            (y, io, "y", (n, Hn, P)))]
+        self.pr, wsz = _problem(ss_ssd_step_problem, "ss_ssd_step_workspace_size", (), n, nslots, Hn, ngroups, xs, zs,
+                                ds, P, N, W, _IO[io], 1 if dt_softplus else 0, 0)
+        self.ws, wa, wsz = _scratch(None, wsz, dev)
         self.keep = (xbc, dt, A, conv_w, conv_bias, D, z, dt_bias, slots, conv_state, state, y)
         st = stream if stream is not None else torch.cuda.current_stream(xbc.device)
-        self.args = (ctypes.byref(self.pr), _ptr(xbc), _ptr(dt), _ptr(A), _ptr(conv_w), _ptr(conv_bias), _ptr(D),
-                     _ptr(z), _ptr(dt_bias), _ptr(slots), _ptr(conv_state) if W > 1 else None, _ptr(state), _ptr(y),
-                     _ptr(self.ws), wsz, ctypes.c_void_p(st.cuda_stream))
+        self.args = (self.pr, xa, da, *at[:4], za, *at[4:6], at[6] if W > 1 else None, *at[7:], wa, wsz,
+                     ctypes.c_void_p(st.cuda_stream))
         self.fn = lib.ss_ssd_step
 
     def __call__(self):
