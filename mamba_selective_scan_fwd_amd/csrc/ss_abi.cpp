@@ -584,7 +584,7 @@ ss_status check_ssd_bwd(const ss_ssd_problem* p) {
   const ss_status s = check_ssd(p);
   if (s != SS_OK) return s;
   const double places = (double)p->batch * (double)((p->seqlen + kSsdChunk - 1) / kSsdChunk);
-  if (places * (2.0 * (double)p->nheads + 8.0 * (double)p->ngroups) > (double)kMaxGrid) return SS_ERR_BAD_SHAPE;
+  if (places * (2.0 * (double)p->nheads + 10.0 * (double)p->ngroups) > (double)kMaxGrid) return SS_ERR_BAD_SHAPE;
   if ((double)p->batch * (double)p->nheads * (p->dstate / 16) > (double)kMaxGrid) return SS_ERR_BAD_SHAPE;
   return SS_OK;
 }
@@ -597,7 +597,8 @@ struct SsdBwdLayout {
     total += align256(bytes);
     return at;
   }
-  size_t E, R, decay, dot, cb, bc, delta, cs, cl, seg, rowin, colin, row, col, e, out, xg, xd, span, part, x[2], g[3], b[2], c[2];
+  size_t E, R, decay, dot, cb, bc, delta, cs, cl, from, to, wc, wb, xd, e, r, seg, prow, pcol, S, part;
+  size_t x[2], g[3], b[2], c[2];
 };
 SsdBwdLayout ssd_bwd_layout(const ss_ssd_problem* p, bool gated) {
   const bool f16 = p->io_dtype == SS_F16;
@@ -609,9 +610,11 @@ SsdBwdLayout ssd_bwd_layout(const ss_ssd_problem* p, bool gated) {
   SsdBwdLayout l;
   l.E = l.take(st); l.R = l.take(st); l.decay = l.take(ph * 4); l.dot = l.take(ph * (size_t)p->dstate);
   l.bc = l.take(cb); l.cb = l.take(gated ? cb : 0);
-  l.delta = l.take(q); l.cs = l.take(q); l.cl = l.take(q); l.seg = l.take(places * 256 * 4);
-  l.rowin = l.take(4 * q); l.colin = l.take(4 * q); l.row = l.take(2 * q); l.col = l.take(2 * q);
-  l.e = l.take(2 * q); l.out = l.take(2 * q); l.xg = l.take(2 * q); l.xd = l.take(2 * q); l.span = l.take(ph * 32 * 4);
+  l.delta = l.take(q); l.cs = l.take(q); l.cl = l.take(q); l.from = l.take(q); l.to = l.take(q);
+  l.wc = l.take(q); l.wb = l.take(q); l.xd = l.take(q); l.e = l.take(2 * q); l.r = l.take(2 * q);
+  l.seg = l.take(places * 256 * 4);
+  l.prow = l.take(ph * 10 * 64 * 4); l.pcol = l.take(ph * 10 * 64 * 4);
+  l.S = l.take(places * (size_t)p->ngroups * 10 * (64 * 64 * 2) * 4);
   l.part = l.take(ph * 3 * 4);
   for (int i = 0; i < 3; ++i) l.g[i] = l.take(gated || (f16 && i < 2) ? xb : 0);
   for (int i = 0; i < 2; ++i) {
@@ -675,12 +678,12 @@ ss_status ss_ssd_bwd(const ss_ssd_problem* p, const void* x, const void* dt, con
   planes(parts, l.b, Bm, k.bp);
   planes(parts, l.c, Cm, k.cp);
   k.ws_E = f32_at(l.E); k.ws_R = f32_at(l.R); k.ws_decay = f32_at(l.decay); k.ws_dot = f32_at(l.dot);
-  k.ws_cb = f32_at(l.cb); k.ws_bc = f32_at(l.bc); k.ws_delta = f32_at(l.delta); k.ws_cs = f32_at(l.cs); k.ws_cl = f32_at(l.cl);
+  k.ws_cb = f32_at(l.cb); k.ws_bc = f32_at(l.bc); k.ws_delta = f32_at(l.delta);
+  k.ws_cs = f32_at(l.cs); k.ws_cl = f32_at(l.cl); k.ws_from = f32_at(l.from); k.ws_to = f32_at(l.to);
+  k.ws_wc = f32_at(l.wc); k.ws_wb = f32_at(l.wb); k.ws_xd = f32_at(l.xd); k.ws_e = f32_at(l.e); k.ws_r = f32_at(l.r);
   k.ws_seg = reinterpret_cast<int32_t*>(ws + l.seg);
-  k.ws_rowin = reinterpret_cast<double*>(ws + l.rowin); k.ws_colin = reinterpret_cast<double*>(ws + l.colin);
-  k.ws_e = f32_at(l.e); k.ws_span = f32_at(l.span);
-  k.ws_row = f32_at(l.row); k.ws_col = f32_at(l.col); k.ws_out = f32_at(l.out); k.ws_xg = f32_at(l.xg);
-  k.ws_xd = f32_at(l.xd); k.ws_part = f32_at(l.part);
+  k.ws_prow = f32_at(l.prow); k.ws_pcol = f32_at(l.pcol); k.ws_S = reinterpret_cast<uint32_t*>(ws + l.S);
+  k.ws_part = f32_at(l.part);
   k.batch = p->batch; k.seqlen = p->seqlen;
   k.nheads = (int32_t)p->nheads; k.ngroups = (int32_t)p->ngroups; k.dstate = p->dstate;
   k.nchunks = (int32_t)((p->seqlen + kSsdChunk - 1) / kSsdChunk);

@@ -213,20 +213,21 @@ struct SsdBwdParams {
   float* ws_dot;             // (places, nheads, dstate / 4): parts of decay <R, E>
   float* ws_cb;              // (places, ngroups, 256 * 256): C B^T in operand order (gated only)
   float* ws_bc;              // B C^T in operand order
-  float* ws_delta;           // (places, nheads, 256): Delta
-  float* ws_cs;              // (places, nheads, 256): Delta A summed from the start of each 64 steps,
+  // (places, nheads, 256) each:
+  float* ws_delta;           // Delta
+  float* ws_cs;              // Delta A summed from the start of each 64 steps,
   float* ws_cl;              // and what that float leaves of the sum
-  int32_t* ws_seg;           // (places, 256): document starts at or before each step (with seq_idx)
-  // (2, places, nheads, 256), one half per half of a workgroup (bwd_group); W, e, r as there:
-  double* ws_rowin;          // W of a step's row with its own 64 steps,
-  double* ws_colin;          // of its column with them,
-  float* ws_row;             // of its row with earlier 64s,
-  float* ws_col;             // of its column with later 64s,
-  float* ws_e;               // e
-  float* ws_out;             // r
-  float* ws_xg;              // x . G B
+  float* ws_from;            // exp(that sum),
+  float* ws_to;              // exp(the sum behind a step to the end of its 64)
+  float* ws_wc;              // exp(the sum from the chunk's start), 0 from the first document start on
+  float* ws_wb;              // exp(the sum to the chunk's end), 0 before the last one
   float* ws_xd;              // x . g
-  float* ws_span;            // (places, nheads, 4, 8): parts of W with whole 64s between
+  float* ws_e;               // (2, places, nheads, 256), per half of the states: e
+  float* ws_r;               // and r, without Delta
+  int32_t* ws_seg;           // (places, 256): document starts at or before each step (with seq_idx)
+  float* ws_prow;            // (places, nheads, 10, 64), per pair of 64s: rows' sums of W, or the pairs around
+  float* ws_pcol;            // and columns' sums without Delta
+  uint32_t* ws_S;            // (places, ngroups, 10, 64 * 64 * 2): S as operands of dC and dB, two bf16 parts
   float* ws_part;            // (places, nheads, 3): parts of dA, ddt_bias, dD
   int64_t batch, seqlen;
   int32_t nheads, ngroups, dstate, nchunks;

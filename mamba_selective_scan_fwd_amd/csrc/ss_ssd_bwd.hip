@@ -21,20 +21,21 @@
 // r_j = Delta_j exp(cs_last - cs_j) B_j . R^T x_j,
 //   da_t = sum_{j < t <= i} W_ij + sum_{i>=t} e_i + sum_{j<t} r_j + exp(cs_last) <R, E>.
 // The pairs around a step t of a piece k of 64 steps are summed as
-//   i and j in k:         sum_{i>=t} (sum_{j<i} W_ij - sum_{m>i} W_mi), over k alone,
+//   i and j in k:         sum_{i>=t} sum_{j<t} W_ij, rows' sums first,
 //   i in k, j before k:   sum_{i>=t} sum_j W_ij;  j in k, i behind: sum_{j<t} sum_i W_ij,
-//   i behind k, j before: one number for the piece.
-// Only the first has terms that cancel (pairs that do not span t), and its
-// errors would add up over the steps: both of its sums take the same products
-// in 64 bits.  Kernels:
+//   i behind k, j before: one number for the piece,
+// so that no terms cancel (sum_{i>=t} (row_i - col_i), shorter, loses what its
+// errors add up to over the steps: 1e-5 of dA over 600 steps, 1e-7 this way).
+// Kernels:
 //   bwd_planes   (fp16 or gated) the operands' planes of bf16 parts, g among them
 //   bwd_state    per (chunk, head): what a chunk adds to E and to R; further
 //                workgroups: B C^T (and C B^T if gated) per (chunk, group)
 //   bwd_pass     per (row, head, 1024 elements): E of every chunk, then R and
 //                <R, E> backwards, dh0
 //   bwd_scan     per (chunk, head): G_j B_j, dx; if gated another one rebuilds y for dz
-//   bwd_group    per (chunk, group, 64 rows, dC or dB): all heads of the group,
-//                S and its sums, dC or dB
+//   bwd_pair     per (chunk, group, pair of pieces of 64): all heads of the group, S
+//                and the sums of W
+//   bwd_out      per (chunk, group, dC or dB, half the states): dC or dB, e or r
 //   bwd_delta    per (chunk, head): da, ddt, and the chunk's part of dA, ddt_bias, dD
 //   bwd_sum      per head: dA, ddt_bias, dD
 // No atomics: every sum has a fixed order.  Computed operands are multiplied
@@ -226,16 +227,22 @@ __device__ __forceinline__ void state_role(const SsdBwdParams& p, int place, int
     const int64_t at = ((int64_t)place * p.nheads + h) * kQ + tid;
     float w;
     if constexpr (R) {
+      const float behind = (__shfl(v, 63, 64) - v) + (__shfl(low, 63, 64) - low);
       p.ws_cs[at] = v;
       p.ws_cl[at] = low;
+      p.ws_from[at] = exp2_hw(v * kLog2e);
+      p.ws_to[at] = exp2_hw(behind * kLog2e);
       for (int k = 0; k < wave; ++k) v += sWave[k];
       w = tid < first ? exp2_hw(v * kLog2e) : 0.0f;
+      p.ws_wc[at] = w;
     } else {
       p.ws_delta[at] = delta;
       float behind = __shfl_down(v, 1, 64);
       if (lane == 63) behind = 0.0f;
       for (int k = 3; k > wave; --k) behind += sWave[k];
-      w = seg == starts ? exp2_hw(behind * kLog2e) * delta : 0.0f;
+      w = seg == starts ? exp2_hw(behind * kLog2e) : 0.0f;
+      p.ws_wb[at] = w;
+      w *= delta;
       if (p.seq_idx && h == 0) p.ws_seg[(int64_t)place * kQ + tid] = seg;
       if (tid == 0)
         p.ws_decay[(int64_t)place * p.nheads + h] =
@@ -651,351 +658,488 @@ __global__ void __launch_bounds__(kScanThreads, MODE == 0 ? 4 : 2) bwd_scan_kern
   }
 }
 
-// ---- dC and dB -------------------------------------------------------------------------
-// Workgroup = (chunk, group, 64 rows f, dC or dB), 512 threads, all heads of the
-// group in turn; with the other rows s of the chunk (dC: s <= f, dB: s >= f),
-//   dC: f = i, s = j: F = g, O = x, K = E, v = C, u = B, w_f = exp(cs_f)
-//   dB: f = j, s = i: F = x, O = g, K = R, v = B, u = C, w_f = Delta_f exp(cs_last - cs_f)
-// per head: t_f[n] = w_f sum_p K[p][n] F_f[p], added up over the heads;
-// v_f . t_f (e or r); S_fs from O_s . F_f, added up over the heads in
-// registers, and its row of W (row or col); after the heads, sum_s S_fs u_s.
-// Wave w has the row tile w % 4; of the states and of every piece's four s
-// tiles, waves 0-3 have the first half and waves 4-7 the second.  Both halves'
-// sums of a row are left apart (bwd_delta adds them); the product with u joins
-// them through LDS.  S is built with s along a lane's 4 values, and enters the
-// last product as it is: a k-step's 32 steps are taken in the order in which
-// two of its tiles hold them (u's fragments are read in that order too).
-// dB's sums leave out Delta_f, so that x_f . G_f B_f (what dDelta_f takes
-// directly) comes from the same numbers, diagonal included, undivided.
-constexpr int kGroupThreads = 512;
-// O in LDS: rows of 64 channels, their 16-byte pieces swapped by the row, so
-// that 8 rows' pieces of one column lie in different banks
-__device__ __forceinline__ int o_off(int row, int col) { return row * kP + 8 * ((col >> 3) ^ (row & 7)) + (col & 7); }
-template <int MODE, int N, bool DB>
-__global__ void __launch_bounds__(kGroupThreads, 2) bwd_group_kernel(SsdBwdParams p) {
+// ---- S and the sums of W -----------------------------------------------------------------
+// Workgroup = (chunk, group, pair of 64-step pieces ib >= jb), all heads of the
+// group in turn; wave w has the rows i of tile w of ib and all columns j of jb,
+// lane l the row i = l % 16 and the columns 16 t + 4 (l / 16) + r: S^T is built
+// as x_j . g_i (A = x from LDS, B = g from memory) and summed over the heads in
+// registers.  The columns' x and vectors of the next head are on their way
+// while this head is worked on, two buffers in turn, one barrier per head.
+// Of W = (C_i . B_j) S_ij it leaves, per head,
+//   ib > jb: its sums over j of every row, and over i of every column, the
+//            latter without Delta_j (x . G B takes those);
+//   ib = jb: the columns' sums too (i >= j), and for every j the sum over i > j
+//            of the row's sums up to j, sum_{i>j} sum_{m<=j} W_im: the pairs
+//            around step j + 1, formed without terms that cancel.
+// A column's sum over the 16 lanes of a row tile is a halving exchange (45
+// instructions for 16 columns); the waves' parts meet in LDS once per batch of
+// heads.  The decay between two pieces is a factor per row, one per column and
+// one for the pieces between; inside a piece it is the exp of a difference, of
+// sums kept as two floats.
+constexpr int kBatch = 16;
+constexpr int kPairs = 10;
+__device__ __forceinline__ int pair_of(int ib, int jb) { return ib * (ib + 1) / 2 + jb; }
+// rows of 64 channels in LDS, their 16-byte pieces swapped by the row, so that
+// 8 rows' pieces of one column lie in different banks
+__device__ __forceinline__ int row64_off(int row, int col) {
+  return row * kP + 8 * ((col >> 3) ^ (row & 7)) + (col & 7);
+}
+
+// 16 values per lane summed over the 16 lanes of a DPP row: lane l of the row
+// receives the sum of value l.  In each of four steps a lane keeps the half of
+// its values that one bit of l names and adds its partner's; the partners (8
+// away, mirrored in 8, 2 away, 1 away) differ in that bit and in no earlier one.
+template <int CTRL>
+__device__ __forceinline__ float half_sum(float a, float b, bool upper) {
+  const float keep = upper ? b : a, send = upper ? a : b;
+  return keep + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(send), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float transpose_sum(const f32x4 (&v)[4]) {
+  const int l = threadIdx.x % 16;
+  float a[8], b[4], c[2];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) a[k] = half_sum<0x128>(v[k / 4][k % 4], v[2 + k / 4][k % 4], l & 8);  // row_ror:8
+#pragma unroll
+  for (int k = 0; k < 4; ++k) b[k] = half_sum<0x141>(a[k], a[4 + k], l & 4);                        // row_half_mirror
+#pragma unroll
+  for (int k = 0; k < 2; ++k) c[k] = half_sum<0x4E>(b[k], b[2 + k], l & 2);                         // quad_perm ^2
+  return half_sum<0xB1>(c[0], c[1], l & 1);                                                         // quad_perm ^1
+}
+
+template <int MODE>
+struct PairLds {
+  union {
+    float part[kBatch][2][4][64];  // [head][columns' sums, pairs around][wave][column]
+    float S[64 * 65];              // after the heads
+  };
+  __attribute__((aligned(16))) uint16_t x[2][data_parts<MODE>()][kJB * kP];
+  __attribute__((aligned(16))) float vec[2][3][kJB];  // Delta_j; the columns' factors, or their sums of Delta A
+};
+
+template <int MODE, int N, bool DIAG>
+__device__ __forceinline__ void pair_role(const SsdBwdParams& p, const Chunk& q, int g, int ib, int jb,
+                                          PairLds<MODE>& lds) {
   constexpr int IO = io_of<MODE>();
-  constexpr int FP = DB ? data_parts<MODE>() : g_parts<MODE>(), OP = DB ? g_parts<MODE>() : data_parts<MODE>();
-  constexpr int UP = data_parts<MODE>();
-  constexpr int NT = N / 32;  // state tiles of a wave
-  constexpr size_t kOBytes = (size_t)OP * kQ * kP * 2, kKBytes = (size_t)3 * kP * N * 2;
-  constexpr size_t kUBytes = (size_t)UP * kJB * N * 2, kJoin = (size_t)4 * (N / 16) * 64 * 16;
-  constexpr size_t kA = kOBytes + kKBytes, kB = kUBytes > kJoin ? kUBytes : kJoin;
-  __shared__ __attribute__((aligned(16))) unsigned char sMem[kA > kB ? kA : kB];
-  __shared__ __attribute__((aligned(16))) float sCs[kQ], sCl[kQ];  // Delta A from the piece's first step, two floats
-  __shared__ __attribute__((aligned(16))) float sCol[kQ];    // an s row's factor
-  __shared__ __attribute__((aligned(16))) float sDelta[kQ];
-  __shared__ float sBehind[kQ];                              // Delta A behind a row to its piece's end
-  __shared__ __attribute__((aligned(16))) int sSeg[kQ];
-  __shared__ float sTot[4];
-  uint16_t* sO = reinterpret_cast<uint16_t*>(sMem);                 // [part][s][o_off]
-  uint16_t* sK = reinterpret_cast<uint16_t*>(sMem + kOBytes);       // [part][slice][64 p x 32 n], time-major tiles
-  uint16_t* sU = reinterpret_cast<uint16_t*>(sMem);                 // after the heads: [part][slice][64 s x 32 n]
-  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, quad = lane / 16;
-  const int rt = wave % 4, half = wave / 4;
-  const int lb = (int)xcd_logical_block();
-  const int rb = lb % 4, g = (lb / 4) % p.ngroups;
-  const Chunk q = chunk_of(p, lb / (4 * p.ngroups));
-  const int rows = q.rows, f0 = kJB * rb;
-  if (f0 >= rows) return;
-  const int f = f0 + 16 * rt + lane % 16;  // this lane's row
-  const int lastp = (rows - 1) / kJB;
-  const int ob0 = DB ? rb : 0, ob1 = DB ? lastp : rb;  // pieces of s
+  constexpr int GP = g_parts<MODE>(), XP = data_parts<MODE>();
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, quad = lane / 16, l16 = lane % 16;
+  const int rows = q.rows, pr = pair_of(ib, jb);
   const int hpg = p.nheads / p.ngroups;
   const int64_t xrow = (int64_t)p.nheads * kP, vrow = (int64_t)p.ngroups * N;
-  const auto vv = plane_view(static_cast<const uint16_t*>(DB ? p.Bm : p.Cm), q.row0, vrow, g * N, rows);
-  const auto uv = plane_view(static_cast<const uint16_t*>(DB ? p.Cm : p.Bm), q.row0, vrow, g * N, rows);
+  const int il = kJB * ib + 16 * wave + l16, jl = 4 * quad, j0 = kJB * jb + jl;  // columns j0 + 16 t + r
 
-  // u_s . v_f of the wave's tiles (the same for every head); v_f of its states
-  f32x4 cb[4][2];
+  // C_i . B_j, the same for every head
+  f32x4 cb[4];
   {
-    u32x4v vq[N / 32];
+    const auto bv = plane_view(static_cast<const uint16_t*>(p.Bm), q.row0, vrow, g * N, rows);
+    const auto cv = plane_view(static_cast<const uint16_t*>(p.Cm), q.row0, vrow, g * N, rows);
 #pragma unroll
-    for (int ks = 0; ks < N / 32; ++ks) vq[ks] = vload16(vv, (uint32_t)(f * vrow * 2 + (32 * ks + 8 * quad) * 2));
+    for (int t = 0; t < 4; ++t) cb[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int ob = 0; ob < 4; ++ob)
+    for (int ks = 0; ks < N / 32; ++ks) {
+      const auto c = as_vec<IO>(vload16(cv, (uint32_t)(il * vrow * 2 + (32 * ks + 8 * quad) * 2)));
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        f32x4 a = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (ob >= ob0 && ob <= ob1) {
-          const int s = kJB * ob + 16 * (2 * half + t) + lane % 16;
-#pragma unroll
-          for (int ks = 0; ks < N / 32; ++ks)
-            a = mfma_t<IO>::run(as_vec<IO>(vload16(uv, (uint32_t)(s * vrow * 2 + (32 * ks + 8 * quad) * 2))),
-                                as_vec<IO>(vq[ks]), a);
-        }
-        cb[ob][t] = a;
-      }
+      for (int t = 0; t < 4; ++t)
+        cb[t] = mfma_t<IO>::run(
+            as_vec<IO>(vload16(bv, (uint32_t)((kJB * jb + 16 * t + l16) * vrow * 2 + (32 * ks + 8 * quad) * 2))), c, cb[t]);
+    }
   }
-  uint2 vn[NT];
+  uint32_t same = 0xffffu;  // bit 4 t + r: column j of tile t counts for row i
+  if (p.seq_idx) {
+    const int32_t* seg = p.ws_seg + (int64_t)q.place * kQ;
+    const int si = seg[il];
+    same = 0u;
 #pragma unroll
-  for (int t = 0; t < NT; ++t) vn[t] = vload8(vv, (uint32_t)(f * vrow * 2 + (16 * (NT * half + t) + 4 * quad) * 2));
-  if (p.seq_idx && tid < kQ) sSeg[tid] = p.ws_seg[(int64_t)q.place * kQ + tid];
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) same |= (uint32_t)(seg[j0 + 16 * t + r] == si) << (4 * t + r);
+  }
+  if constexpr (DIAG) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (j0 + 16 * t + r > il) same &= ~(1u << (4 * t + r));
+  }
+  f32x4 S[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) S[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  f32x4 S[4][2], tot[NT];
+  // a head's operands on their way: x of the columns (row tid / 8 + 32 k, channels
+  // 8 (tid % 8) ..), one vector element, g and the factors of this lane's row
+  u32x4v xr[XP][2], gf[GP][2];
+  float vr = 0.0f, fi, li = 0.0f, between = 0.0f;
+  auto load_head = [&](int h) {
+    const int64_t at = ((int64_t)q.place * p.nheads + h) * kQ;
 #pragma unroll
-  for (int ob = 0; ob < 4; ++ob)
+    for (int i = 0; i < XP; ++i) {
+      const auto xv = plane_view(p.xp[i], q.row0, xrow, h * kP, rows);
 #pragma unroll
-    for (int t = 0; t < 2; ++t) S[ob][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int k = 0; k < 2; ++k)
+        xr[i][k] = vload16(xv, (uint32_t)((kJB * jb + tid / 8 + 32 * k) * xrow * 2 + (tid % 8) * 16));
+    }
+    const float* vec = wave == 0 ? p.ws_delta : wave == 1 ? (DIAG ? p.ws_cs : p.ws_to) : p.ws_cl;
+    if (wave < (DIAG ? 3 : 2)) vr = vec[at + kJB * jb + lane];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) tot[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < GP; ++i) {
+      const auto gv = plane_view(p.gp[i], q.row0, xrow, h * kP, rows);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) gf[i][ks] = vload16(gv, (uint32_t)(il * xrow * 2 + (32 * ks + 8 * quad) * 2));
+    }
+    fi = (DIAG ? p.ws_cs : p.ws_from)[at + il];
+    if constexpr (DIAG) {
+      li = p.ws_cl[at + il];
+    } else {
+      between = 0.0f;
+      for (int k = jb + 1; k < ib; ++k) between += p.ws_cs[at + kJB * k + kJB - 1];
+    }
+  };
+  load_head(g * hpg);
+  int turn = 0;
+  for (int h0 = 0; h0 < hpg; h0 += kBatch) {
+    const int nb = hpg - h0 < kBatch ? hpg - h0 : kBatch;
+    for (int hb = 0; hb < nb; ++hb, turn ^= 1) {
+      const int h = g * hpg + h0 + hb;
+      const int64_t ph = (int64_t)q.place * p.nheads + h;
+#pragma unroll
+      for (int i = 0; i < XP; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          *reinterpret_cast<u32x4v*>(&lds.x[turn][i][row64_off(tid / 8 + 32 * k, 8 * (tid % 8))]) = xr[i][k];
+      if (wave < (DIAG ? 3 : 2)) lds.vec[turn][wave][lane] = vr;
+      __syncthreads();
+      f32x4 a[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) a[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int j = XP - 1; j >= 0; --j) {
+          bf16x8 xf[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+            xf[t] = bfv(*reinterpret_cast<const u32x4v*>(&lds.x[turn][j][row64_off(16 * t + l16, 32 * ks + 8 * quad)]));
+#pragma unroll
+          for (int i = GP - 1; i >= 0; --i)
+            if (i + j <= 2)
+#pragma unroll
+              for (int t = 0; t < 4; ++t) a[t] = BF::run(xf[t], bfv(gf[i][ks]), a[t]);
+        }
+      const float f = DIAG ? fi : fi * exp2_hw(between * kLog2e), l = li;
+      if (h + 1 < (g + 1) * hpg) load_head(h + 1);
+      float xd = 0.0f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const f32x4 ej = *reinterpret_cast<const f32x4*>(&lds.vec[turn][1][jl + 16 * t]);
+        if constexpr (DIAG) {
+          const f32x4 lj = *reinterpret_cast<const f32x4*>(&lds.vec[turn][2][jl + 16 * t]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if (t == wave) xd = j0 + 16 * t + r == il ? a[t][r] : xd;
+            const float e = exp2_hw(((f - ej[r]) + (l - lj[r])) * kLog2e);
+            a[t][r] = (same >> (4 * t + r)) & 1u ? a[t][r] * e : 0.0f;
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) a[t][r] *= ej[r] * f;
+          if (p.seq_idx) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) a[t][r] = (same >> (4 * t + r)) & 1u ? a[t][r] : 0.0f;
+          }
+        }
+      }
+      // a: S_ij without Delta_j
+      f32x4 W[4];
+      float row = 0.0f, base = 0.0f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const f32x4 dj = *reinterpret_cast<const f32x4*>(&lds.vec[turn][0][jl + 16 * t]);
+        f32x4 v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          S[t][r] = fmaf(a[t][r], dj[r], S[t][r]);
+          W[t][r] = cb[t][r] * a[t][r];
+          if constexpr (DIAG) {
+            v[r] = r ? fmaf(W[t][r], dj[r], v[r - 1]) : W[t][0] * dj[0];
+          } else {
+            row = fmaf(W[t][r], dj[r], row);
+          }
+        }
+        if constexpr (DIAG) {
+          // the row's sums up to each j: inside a lane's 4 columns, over the quads
+          // of a tile (lanes 16 apart), over the tiles
+          float s = v[3];
+          const float u1 = __shfl_up(s, 16, 64);
+          if (quad >= 1) s += u1;
+          const float u2 = __shfl_up(s, 32, 64);
+          if (quad >= 2) s += u2;
+          const float before = base + (s - v[3]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) a[t][r] = il > j0 + 16 * t + r ? v[r] + before : 0.0f;
+          base += __shfl(s, 48 + l16, 64);
+        }
+      }
+      lds.part[hb][0][wave][16 * (l16 / 4) + jl + l16 % 4] = transpose_sum(W);
+      if constexpr (DIAG) {
+        lds.part[hb][1][wave][16 * (l16 / 4) + jl + l16 % 4] = transpose_sum(a);
+        if (quad == (l16 >> 2)) p.ws_xd[ph * kQ + il] = xd;
+      } else {
+        row += __shfl_xor(row, 16, 64);
+        row += __shfl_xor(row, 32, 64);
+        if (quad == 0) p.ws_prow[(ph * kPairs + pr) * kJB + 16 * wave + l16] = row;
+      }
+    }
+    __syncthreads();
+    for (int k = tid; k < nb * 64; k += 256) {
+      const int hb = k / 64, j = k % 64;
+      const auto& v = lds.part[hb];
+      const int64_t to = (((int64_t)q.place * p.nheads + g * hpg + h0 + hb) * kPairs + pr) * kJB + j;
+      p.ws_pcol[to] = (v[0][0][j] + v[0][1][j]) + (v[0][2][j] + v[0][3][j]);
+      if constexpr (DIAG) p.ws_prow[to] = (v[1][0][j] + v[1][1][j]) + (v[1][2][j] + v[1][3][j]);
+    }
+    __syncthreads();
+  }
 
-  for (int hg = 0; hg < hpg; ++hg) {
-    const int h = g * hpg + hg;
-    const int64_t ph = (int64_t)q.place * p.nheads + h;
-    u32x4v F[FP][2];
+  // S as operand fragments, two parts, for dC (a lane a row i, 8 columns) and for
+  // dB (a lane a column j, 8 rows): [dC, dB][part][tile][k-step][lane][8], where
+  // element e of a k-step's quad is step 4 quad + e of its first tile, or of its
+  // second for e >= 4
+  uint32_t* out = p.ws_S + (((int64_t)q.place * p.ngroups + g) * kPairs + pr) * (2 * kJB * kJB);
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) lds.S[(16 * wave + l16) * 65 + 16 * t + jl + r] = S[t][r];
+  __syncthreads();
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    if (side) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[t][r] = lds.S[(16 * t + jl + r) * 65 + 16 * wave + l16];
+    }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      u32x4v part[2];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t hi, lo;
+        split2(S[2 * ks + e / 2][2 * (e % 2)], S[2 * ks + e / 2][2 * (e % 2) + 1], hi, lo);
+        part[0][e] = hi;
+        part[1][e] = lo;
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        *reinterpret_cast<u32x4v*>(out + ((((side * 2 + k) * 4 + wave) * 2 + ks) * 64 + lane) * 4) = part[k];
+    }
+  }
+}
+
+template <int MODE, int N>
+__global__ void __launch_bounds__(256, MODE == 0 ? 3 : 2) bwd_pair_kernel(SsdBwdParams p) {
+  __shared__ PairLds<MODE> lds;
+  const int lb = (int)xcd_logical_block();  // the pairs of one chunk's group share an XCD's L2
+  const int pr = lb % kPairs, g = (lb / kPairs) % p.ngroups;
+  const Chunk q = chunk_of(p, lb / (kPairs * p.ngroups));
+  int ib = 0;
+  while ((ib + 1) * (ib + 2) / 2 <= pr) ++ib;
+  const int jb = pr - ib * (ib + 1) / 2;
+  if (kJB * ib >= q.rows) return;
+  if (ib == jb) pair_role<MODE, N, true>(p, q, g, ib, jb, lds);
+  else pair_role<MODE, N, false>(p, q, g, ib, jb, lds);
+}
+
+// ---- dC and dB -----------------------------------------------------------------------------
+// Workgroup = (chunk, group, dC or dB, half of the states), 512 threads, wave w
+// the rows f = 32 w .. 32 w + 31:
+//   dC: f = i: F = g, K = E, v = C, u = B, w_f = exp(cs_f), d = 1
+//   dB: f = j: F = x, K = R, v = B, u = C, w_f = exp(cs_last - cs_f), d = Delta
+//   out_f[n] = sum_h d_f w_f sum_p K[p][n] F_f[p] + sum_s S_fs u_s[n]
+// and per head v_f . (w_f K^T F_f) (e; r and x . G B's share of it, without
+// Delta).  The heads' K are staged in LDS by turns of two buffers (three parts,
+// [p][16 n] tiles read back transposed): the next head's K and F are on their
+// way while this head is multiplied, one barrier per head.  S comes as operand
+// fragments from bwd_pair, with u's pieces staged in LDS.
+constexpr int kOutThreads = 512;
+// element (row, c) of a [rows][16] tile: blocks of 4 rows swapped so that the
+// transposing reads of rows 8 apart hit different banks
+__device__ __forceinline__ int t16_off(int row, int c) { return (row ^ (((row >> 3) & 1) << 2)) * 16 + c; }
+
+template <int MODE, int N, bool DB>
+__device__ __forceinline__ void out_role(const SsdBwdParams& p, int lb, uint16_t* lds) {
+  constexpr int IO = io_of<MODE>();
+  constexpr int FP = DB ? data_parts<MODE>() : g_parts<MODE>(), UP = data_parts<MODE>();
+  constexpr int NH = N / 2, NT = NH / 16;                    // states and state tiles of the half
+  constexpr int kItems = kP * NH / 4, kPer = (kItems + kOutThreads - 1) / kOutThreads;
+  constexpr int kBuf = 3 * kP * NH;
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, quad = lane / 16, l16 = lane % 16;
+  const int half = lb & 1, g = (lb >> 1) % p.ngroups;
+  const Chunk q = chunk_of(p, (lb >> 1) / p.ngroups);
+  const int rows = q.rows, n0 = NH * half;
+  const int hpg = p.nheads / p.ngroups;
+  const int64_t xrow = (int64_t)p.nheads * kP, vrow = (int64_t)p.ngroups * N;
+  const int fr[2] = {32 * wave + l16, 32 * wave + 16 + l16};  // this lane's rows
+  const auto vv = plane_view(static_cast<const uint16_t*>(DB ? p.Bm : p.Cm), q.row0, vrow, g * N, rows);
+  uint2 vn[2][NT];
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) vn[b][t] = vload8(vv, (uint32_t)(fr[b] * vrow * 2 + (n0 + 16 * t + 4 * quad) * 2));
+  f32x4 tot[2][NT];
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) tot[b][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  f32x4 kr[kPer];
+  u32x4v F[FP][2][2];
+  float wf[2], df[2];
+  auto load_k = [&](int h) {
+    const float* K = (DB ? p.ws_R : p.ws_E) + ((int64_t)q.place * p.nheads + h) * (kP * N) + n0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int item = tid + kOutThreads * k;
+      if (kItems % kOutThreads == 0 || item < kItems)
+        kr[k] = *reinterpret_cast<const f32x4*>(K + (item / (NH / 4)) * N + 4 * (item % (NH / 4)));
+    }
+  };
+  auto load_f = [&](int h) {
 #pragma unroll
     for (int i = 0; i < FP; ++i) {
       const auto fv = plane_view(DB ? p.xp[i % 2] : p.gp[i], q.row0, xrow, h * kP, rows);
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) F[i][ks] = vload16(fv, (uint32_t)(f * xrow * 2 + (32 * ks + 8 * quad) * 2));
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+          F[i][b][ks] = vload16(fv, (uint32_t)(fr[b] * xrow * 2 + (32 * ks + 8 * quad) * 2));
     }
-    u32x4v orr[OP][4];
+    const int64_t at = ((int64_t)q.place * p.nheads + h) * kQ;
 #pragma unroll
-    for (int i = 0; i < OP; ++i) {
-      const auto ov = plane_view(DB ? p.gp[i] : p.xp[i % 2], q.row0, xrow, h * kP, rows);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (k >= ob0 && k <= ob1) orr[i][k] = vload16(ov, (uint32_t)((tid / 8 + 64 * k) * xrow * 2 + (tid % 8) * 16));
+    for (int b = 0; b < 2; ++b) {
+      wf[b] = (DB ? p.ws_wb : p.ws_wc)[at + fr[b]];
+      df[b] = DB ? p.ws_delta[at + fr[b]] : 1.0f;
     }
-    const f32x4* K = reinterpret_cast<const f32x4*>((DB ? p.ws_R : p.ws_E) + ph * (kP * N));
-    f32x4 kr[N / 32];
+  };
+  load_k(g * hpg);
+  load_f(g * hpg);
+  for (int hg = 0; hg < hpg; ++hg) {
+    const int h = g * hpg + hg;
+    uint16_t* buf = lds + (hg & 1) * kBuf;
 #pragma unroll
-    for (int k = 0; k < N / 32; ++k) kr[k] = K[tid + kGroupThreads * k];
-    float delta = 0.0f, cs = 0.0f, cl = 0.0f;
-    if (tid < kQ) {
-      delta = p.ws_delta[ph * kQ + tid];
-      cs = p.ws_cs[ph * kQ + tid];
-      cl = p.ws_cl[ph * kQ + tid];
-    }
-    __syncthreads();  // the previous head's operands are used up
-    if (tid < kQ) {
-      const float behind = (__shfl(cs, 63, 64) - cs) + (__shfl(cl, 63, 64) - cl);
-      sCs[tid] = cs;
-      sCl[tid] = cl;
-      sDelta[tid] = delta;
-      sCol[tid] = exp2_hw((DB ? cs : behind) * kLog2e);
-      sBehind[tid] = behind;
-      if (lane == 63) sTot[wave] = cs;
-    }
+    for (int k = 0; k < kPer; ++k) {
+      const int item = tid + kOutThreads * k;
+      if (kItems % kOutThreads == 0 || item < kItems) {
+        const int pr = item / (NH / 4), n = 4 * (item % (NH / 4));
+        uint32_t a[3], b[3];
+        split3(kr[k][0], kr[k][1], a);
+        split3(kr[k][2], kr[k][3], b);
+        const int at = (n / 16) * (kP * 16) + t16_off(pr, n % 16);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (k >= ob0 && k <= ob1) {
-        const int at = o_off(tid / 8 + 64 * k, 8 * (tid % 8));
-#pragma unroll
-        for (int i = 0; i < OP; ++i) *reinterpret_cast<u32x4v*>(&sO[i * kQ * kP + at]) = orr[i][k];
+        for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2*>(&buf[i * kP * NH + at]) = make_uint2(a[i], b[i]);
       }
-#pragma unroll
-    for (int k = 0; k < N / 32; ++k) {
-      const int item = 4 * (tid + kGroupThreads * k), pr = item / N, n = item % N;
-      const int at = (n / 32) * (kP * 32) + tm_off<32>(pr, n % 32);
-      uint32_t a[3], b[3];
-      split3(kr[k][0], kr[k][1], a);
-      split3(kr[k][2], kr[k][3], b);
-#pragma unroll
-      for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2*>(&sK[i * kP * N + at]) = make_uint2(a[i], b[i]);
     }
     __syncthreads();
-
-    const float csf = sCs[f], clf = sCl[f], df = sDelta[f], behind = sBehind[f];
-    const int segf = p.seq_idx ? sSeg[f] : 0;
-    // t_f and v_f . t_f
-    float wf = DB ? behind : csf;
-    if constexpr (DB) {
-      for (int k = rb + 1; k < 4; ++k) wf += sTot[k];
-    } else {
-      for (int k = 0; k < rb; ++k) wf += sTot[k];
-    }
-    wf = exp2_hw(wf * kLog2e);
-    if (p.seq_idx && segf != (DB ? sSeg[rows - 1] : 0)) wf = 0.0f;
-    float vt = 0.0f;
+    if (hg + 1 < hpg) load_k(h + 1);
+    f32x4 a[2][NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int nt = NT * half + t;  // states 16 nt ..
-      f32x4 a = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int b = 0; b < 2; ++b) a[b][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        const uint16_t* tile = sK + (nt / 2) * (kP * 32) + 32 * ks * 32;
-        const int o0 = tm_lane_off<32>(16 * (nt % 2), 0, lane), o1 = tm_lane_off<32>(16 * (nt % 2), 1, lane);
+        const int r0 = 32 * ks + 8 * quad + l16 / 4, c = 4 * (l16 % 4);
+        const int o0 = t16_off(r0, c), o1 = t16_off(r0 + 4, c);
 #pragma unroll
         for (int j = 2; j >= 0; --j) {
-          const bf16x8 kp = bfv(tm_frag(tile + j * kP * N, o0, o1));
+          const bf16x8 kp = bfv(tm_frag(buf + j * kP * NH + t * (kP * 16), o0, o1));
 #pragma unroll
           for (int i = FP - 1; i >= 0; --i)
-            if (i + j <= 2) a = BF::run(kp, bfv(F[i][ks]), a);
-        }
-      }
-      const float v[4] = {low16<IO>(vn[t].x), high16<IO>(vn[t].x), low16<IO>(vn[t].y), high16<IO>(vn[t].y)};
+            if (i + j <= 2)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        a[r] *= wf;
-        vt = fmaf(v[r], a[r], vt);
-        tot[t][r] = DB ? fmaf(df, a[r], tot[t][r]) : tot[t][r] + a[r];
+              for (int b = 0; b < 2; ++b) a[b][t] = BF::run(kp, bfv(F[i][b][ks]), a[b][t]);
+        }
       }
     }
-    // S and W
-    // W of this lane's row: inside its piece, of other pieces, and of the first
-    // one and two of them; dB: all of it without Delta_f; O_f . F_f
-    double in = 0.0;
-    float off = 0.0f, first = 0.0f, second = 0.0f, all = 0.0f, xd = 0.0f;
-    const float ef = exp2_hw((DB ? behind : csf) * kLog2e);
+    const float w[2] = {wf[0], wf[1]}, d[2] = {df[0], df[1]};
+    if (hg + 1 < hpg) load_f(h + 1);
+    const int64_t to = ((int64_t)half * p.batch * p.nchunks * p.nheads + (int64_t)q.place * p.nheads + h) * kQ;
 #pragma unroll
-    for (int ob = 0; ob < 4; ++ob) {
-      if (ob < ob0 || ob > ob1) continue;
-      const bool diag = ob == rb;
-      // across pieces: exp(cs_i) exp(behind_j) exp(pieces between), in this order
-      // for dB and dC, so that both form the same W
-      float between = 0.0f;
-      for (int k = DB ? rb + 1 : ob + 1; k < (DB ? ob : rb); ++k) between += sTot[k];
-      between = exp2_hw(between * kLog2e);
+    for (int b = 0; b < 2; ++b) {
+      float vt = 0.0f;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int st = kJB * ob + 16 * (2 * half + t);
-        f32x4 a = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          const int at = o_off(st + lane % 16, 32 * ks + 8 * quad);
-#pragma unroll
-          for (int j = OP - 1; j >= 0; --j) {
-            const bf16x8 op = bfv(*reinterpret_cast<const u32x4v*>(&sO[j * kQ * kP + at]));
-#pragma unroll
-            for (int i = FP - 1; i >= 0; --i)
-              if (i + j <= 2) a = BF::run(op, bfv(F[i][ks]), a);
-          }
-        }
-        const int s = st + 4 * quad;
-        f32x4 fac, ds;  // the decay from s to f (f to s), Delta of the pair's earlier step
-        if constexpr (DB) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) ds[r] = df;
-        } else {
-          ds = *reinterpret_cast<const f32x4*>(&sDelta[s]);
-        }
-        if (diag) {
-          const f32x4 c = *reinterpret_cast<const f32x4*>(&sCs[s]), l = *reinterpret_cast<const f32x4*>(&sCl[s]);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float from = (csf - c[r]) + (clf - l[r]);  // Delta A from s to f
-            const float v = exp2_hw((DB ? -from : from) * kLog2e);
-            fac[r] = (DB ? s + r >= f : s + r <= f) ? v : 0.0f;
-          }
-        } else {
-          fac = *reinterpret_cast<const f32x4*>(&sCol[s]);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) fac[r] = fac[r] * ef * between;
-        }
+      for (int t = 0; t < NT; ++t) {
+        const float v[4] = {low16<IO>(vn[b][t].x), high16<IO>(vn[b][t].x), low16<IO>(vn[b][t].y), high16<IO>(vn[b][t].y)};
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          float v = a[r] * fac[r];
-          if (p.seq_idx) v = sSeg[s + r] == segf ? v : 0.0f;
-          const float vd = v * ds[r];
-          S[ob][t][r] += vd;
-          if constexpr (DB) all = fmaf(cb[ob][t][r], v, all);
-          if (diag) {
-            in += s + r != f ? (double)cb[ob][t][r] * (double)vd : 0.0;
-            if constexpr (DB) xd += s + r == f ? a[r] : 0.0f;
-          } else {
-            off = fmaf(cb[ob][t][r], vd, off);
-          }
+          vt = fmaf(v[r], a[b][t][r], vt);
+          tot[b][t][r] = fmaf(DB ? w[b] * d[b] : w[b], a[b][t][r], tot[b][t][r]);
         }
       }
-      if (ob == 0) first = off;
-      if (ob == 1) second = off;
-    }
-    auto over_quads = [](float v) {
-      v += __shfl_xor(v, 16, 64);
-      return v + __shfl_xor(v, 32, 64);
-    };
-    const int64_t to = ((int64_t)half * p.batch * p.nchunks * p.nheads + ph) * kQ + f;
-    in += __shfl_xor(in, 16, 64);
-    in += __shfl_xor(in, 32, 64);
-    off = over_quads(off);
-    vt = over_quads(vt);
-    if constexpr (DB) {
-      all = over_quads(all);
-      xd = over_quads(xd);
-      if (lane < 16) {
-        p.ws_colin[to] = in;
-        p.ws_col[to] = off;
-        p.ws_out[to] = df * vt;
-        p.ws_xg[to] = all + vt;
-        p.ws_xd[to] = xd;
-      }
-    } else {
-      if (lane < 16) {
-        p.ws_rowin[to] = in;
-        p.ws_row[to] = off;
-        p.ws_e[to] = vt;
-      }
-      if (rb >= 2) {  // the pairs that a whole piece lies between
-        float v[2] = {first, rb == 3 ? second : first};
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          v[k] = row_sum(over_quads(f < rows ? v[k] : 0.0f));
-          if (lane == 0) p.ws_span[(ph * 4 + 2 * (rb - 2) + k) * 8 + wave] = v[k];
-        }
-      }
+      vt *= w[b];
+      vt += __shfl_xor(vt, 16, 64);
+      vt += __shfl_xor(vt, 32, 64);
+      if (quad == 0) (DB ? p.ws_r : p.ws_e)[to + fr[b]] = vt;
     }
   }
 
-  // ---- sum_s S_fs u_s, this wave's half of every piece, all states
-  f32x4 acc[N / 16];
-#pragma unroll
-  for (int t = 0; t < N / 16; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  // ---- sum_s S_fs u_s
   __amdgpu_buffer_rsrc_t up[UP];
 #pragma unroll
-  for (int i = 0; i < UP; ++i) up[i] = plane_view(DB ? p.cp[i] : p.bp[i], q.row0, vrow, g * N, rows);
-#pragma unroll
-  for (int ob = 0; ob < 4; ++ob) {
-    if (ob < ob0 || ob > ob1) continue;  // uniform over the workgroup
+  for (int i = 0; i < UP; ++i) up[i] = plane_view(DB ? p.cp[i] : p.bp[i], q.row0, vrow, g * N + n0, rows);
+  const uint32_t* Sw = p.ws_S + ((int64_t)q.place * p.ngroups + g) * kPairs * (2 * kJB * kJB);
+  const int fb = wave / 2;  // the piece that holds this wave's rows
+  const int lastp = (rows - 1) / kJB;
+  for (int sb = 0; sb <= lastp; ++sb) {
     __syncthreads();
-    for (int item = tid; item < kJB * N / 8; item += kGroupThreads) {
-      const int s = item / (N / 8), n = 8 * (item % (N / 8));
-      const uint32_t off = (uint32_t)((kJB * ob + s) * vrow * 2 + n * 2);
-      const int at = (n / 32) * (kJB * 32) + tm_off<32>(s, n % 32);
+    for (int item = tid; item < kJB * NH / 8; item += kOutThreads) {
+      const int s = item / (NH / 8), n = 8 * (item % (NH / 8));
+      const int at = (n / 16) * (kJB * 16) + t16_off(s, n % 16);
 #pragma unroll
-      for (int i = 0; i < UP; ++i) *reinterpret_cast<u32x4v*>(&sU[i * kJB * N + at]) = vload16(up[i], off);
+      for (int i = 0; i < UP; ++i)
+        *reinterpret_cast<u32x4v*>(&lds[i * kJB * NH + at]) = vload16(up[i], (uint32_t)((kJB * sb + s) * vrow * 2 + n * 2));
     }
     __syncthreads();
-    u32x4v sh, sl;  // S of the two tiles: the k-step's steps 4 quad + r and 16 + 4 quad + r
+    if ((DB ? sb < fb : sb > fb) || fb > lastp) continue;
+    const uint32_t* Sp = Sw + pair_of(DB ? sb : fb, DB ? fb : sb) * (2 * kJB * kJB) + (DB ? kJB * kJB : 0);
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int ks = 0; ks < 2; ++ks) {
+      u32x4v sp[2][2];  // [part][row tile]
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        uint32_t a, b;
-        split2(S[ob][t][2 * e], S[ob][t][2 * e + 1], a, b);
-        sh[2 * t + e] = a;
-        sl[2 * t + e] = b;
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          sp[k][b] = *reinterpret_cast<const u32x4v*>(Sp + (((k * 4 + 2 * (wave % 2) + b) * 2 + ks) * 64 + lane) * 4);
+      const int r0 = 32 * ks + 4 * quad + l16 / 4, c = 4 * (l16 % 4);
+      const int o0 = t16_off(r0, c), o1 = t16_off(r0 + 16, c);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const bf16x8 uh = bfv(tm_frag(lds + t * (kJB * 16), o0, o1));
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          tot[b][t] = BF::run(uh, bfv(sp[1][b]), tot[b][t]);
+          if constexpr (UP > 1)
+            tot[b][t] = BF::run(bfv(tm_frag(lds + kJB * NH + t * (kJB * 16), o0, o1)), bfv(sp[0][b]), tot[b][t]);
+          tot[b][t] = BF::run(uh, bfv(sp[0][b]), tot[b][t]);
+        }
       }
-    const int j = lane % 16;
-#pragma unroll
-    for (int t = 0; t < N / 16; ++t) {
-      const int c = 16 * (t % 2) + 4 * (j % 4);
-      const uint16_t* tile = sU + (t / 2) * (kJB * 32) + 32 * half * 32;
-      const int o0 = tm_off<32>(4 * quad + j / 4, c), o1 = tm_off<32>(16 + 4 * quad + j / 4, c);
-      const bf16x8 uh = bfv(tm_frag(tile, o0, o1));
-      acc[t] = BF::run(uh, bfv(sl), acc[t]);
-      if constexpr (UP > 1) acc[t] = BF::run(bfv(tm_frag(tile + kJB * N, o0, o1)), bfv(sh), acc[t]);
-      acc[t] = BF::run(uh, bfv(sh), acc[t]);
     }
   }
+  uint16_t* out = static_cast<uint16_t*>(DB ? p.dB : p.dC) + q.row0 * vrow + g * N + n0;
 #pragma unroll
-  for (int t = 0; t < N / 16; ++t)
-    if (t / NT == half) acc[t] += tot[t % NT];
-  __syncthreads();
-  f32x4* join = reinterpret_cast<f32x4*>(sMem);
-  if (half == 1) {
+  for (int b = 0; b < 2; ++b)
+    if (fr[b] < rows)
 #pragma unroll
-    for (int t = 0; t < N / 16; ++t) join[(rt * (N / 16) + t) * 64 + lane] = acc[t];
-  }
-  __syncthreads();
-  if (half == 0 && f < rows) {
-    uint16_t* out = static_cast<uint16_t*>(DB ? p.dB : p.dC) + (q.row0 + f) * vrow + g * N;
-#pragma unroll
-    for (int t = 0; t < N / 16; ++t) {
-      const f32x4 v = acc[t] + join[(rt * (N / 16) + t) * 64 + lane];
-      *reinterpret_cast<uint2*>(out + 16 * t + 4 * quad) = make_uint2(pack2<IO>(v[0], v[1]), pack2<IO>(v[2], v[3]));
-    }
-  }
+      for (int t = 0; t < NT; ++t)
+        *reinterpret_cast<uint2*>(out + fr[b] * vrow + 16 * t + 4 * quad) =
+            make_uint2(pack2<IO>(tot[b][t][0], tot[b][t][1]), pack2<IO>(tot[b][t][2], tot[b][t][3]));
+}
+
+template <int MODE, int N>
+__global__ void __launch_bounds__(kOutThreads, 2) bwd_out_kernel(SsdBwdParams p) {
+  constexpr int kHeads = 2 * 3 * kP * (N / 2), kSteps = data_parts<MODE>() * kJB * (N / 2);
+  __shared__ __attribute__((aligned(16))) uint16_t lds[kHeads > kSteps ? kHeads : kSteps];
+  const int lb = (int)xcd_logical_block(), n = (int)p.batch * p.nchunks * p.ngroups * 2;
+  if (lb < n) out_role<MODE, N, false>(p, lb, lds);
+  else out_role<MODE, N, true>(p, lb - n, lds);
 }
 
 // ---- da, ddt ----------------------------------------------------------------------------
@@ -1017,44 +1161,42 @@ __global__ void __launch_bounds__(256) bwd_delta_kernel(SsdBwdParams p) {
   const int h = (int)(blockIdx.x % (uint32_t)p.nheads);
   const Chunk q = chunk_of(p, (int)(blockIdx.x / (uint32_t)p.nheads));
   const int64_t ph = (int64_t)q.place * p.nheads + h, at = ph * kQ + tid;
-  const int64_t other = p.batch * p.nchunks * p.nheads * kQ;  // the second half's sums
+  const int64_t other = p.batch * p.nchunks * p.nheads * kQ;  // the second half of the states
+  const float* prow = p.ws_prow + ph * kPairs * kJB + lane;
+  const float* pcol = p.ws_pcol + ph * kPairs * kJB + lane;
+  const int lastp = (q.rows - 1) / kJB;
   const bool in = tid < q.rows;
-  double pair = 0.0;
-  float row = 0.0f, col = 0.0f, e = 0.0f, out = 0.0f, xg = 0.0f, xd = 0.0f, delta = 0.0f, raw = 0.0f;
+  float around = 0.0f, row = 0.0f, col = 0.0f, e = 0.0f, out = 0.0f, xg = 0.0f, xd = 0.0f, delta = 0.0f, raw = 0.0f;
   if (in) {
-    pair = (p.ws_rowin[at] + p.ws_rowin[other + at]) - (p.ws_colin[at] + p.ws_colin[other + at]);
-    row = p.ws_row[at] + p.ws_row[other + at];
-    col = p.ws_col[at] + p.ws_col[other + at];
-    e = p.ws_e[at] + p.ws_e[other + at];
-    out = p.ws_out[at] + p.ws_out[other + at];
-    xg = p.ws_xg[at] + p.ws_xg[other + at];
-    xd = p.ws_xd[at] + p.ws_xd[other + at];
     delta = p.ws_delta[at];
+    if (lane > 0) around = prow[pair_of(wave, wave) * kJB - 1];  // the pairs around this step
+    for (int k = 0; k < wave; ++k) row += prow[pair_of(wave, k) * kJB];
+    for (int k = wave + 1; k <= lastp; ++k) col += pcol[pair_of(k, wave) * kJB];
+    e = p.ws_e[at] + p.ws_e[other + at];
+    out = p.ws_r[at] + p.ws_r[other + at];
+    xg = (pcol[pair_of(wave, wave) * kJB] + col) + out;
+    col *= delta;
+    out *= delta;
+    xd = p.ws_xd[at];
     raw = load_io<IO>(p.dt, (q.row0 + tid) * p.nheads + h) + (p.dt_bias ? p.dt_bias[h] : 0.0f);
   }
   const int nd = p.dstate / 4;
   float dot = 0.0f;
   for (int k = lane; k < nd; k += 64) dot += p.ws_dot[ph * nd + k];
-  // the pairs around the whole piece: of rows in piece 2 with piece 0 (entries
-  // 0, 1 the same), of rows in piece 3 with piece 0 (2) and pieces 0, 1 (3)
-  if (lane < 16) {
-    const float* span = p.ws_span + ph * 32;
-    if (wave == 1 && q.rows > 2 * kJB && lane < 8) dot += span[lane];
-    if (wave == 1 && q.rows > 3 * kJB && lane >= 8) dot += span[16 + lane - 8];
-    if (wave == 2 && q.rows > 3 * kJB && lane < 8) dot += span[24 + lane];
-  }
+  // the pairs around the whole piece: rows of later pieces, columns of earlier ones
+  for (int i = wave + 1; i <= lastp; ++i)
+    if (kJB * i + lane < q.rows)
+      for (int j = 0; j < wave; ++j) dot += prow[pair_of(i, j) * kJB];
   dot = row_sum(dot);
   dot += __shfl_xor(dot, 16, 64);
   dot += __shfl_xor(dot, 32, 64);
-  // from this step on (pair, row, e), and before this step (col, out)
+  // from this step on (row, e), and before this step (col, out)
   float b = out;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
-    const double u0 = __shfl_down(pair, off, 64);
     const float u1 = __shfl_down(row, off, 64), u2 = __shfl_down(e, off, 64);
     const float v1 = __shfl_up(col, off, 64), v2 = __shfl_up(b, off, 64);
     if (lane + off < 64) {
-      pair += u0;
       row += u1;
       e += u2;
     }
@@ -1066,7 +1208,7 @@ __global__ void __launch_bounds__(256) bwd_delta_kernel(SsdBwdParams p) {
   if (lane == 0) sA[wave] = e;
   if (lane == 63) sB[wave] = b;
   __syncthreads();
-  float a = (float)pair + row;
+  float a = around + row;
   const float before = __shfl_up(col, 1, 64);
   b = __shfl_up(b, 1, 64);
   if (lane == 0) b = 0.0f;
@@ -1120,8 +1262,8 @@ hipError_t launch_n(const SsdBwdParams& p, hipStream_t st) {
   SS_LAUNCH((bwd_pass_kernel<N>), p.batch * p.nheads * (kP * N / 1024), 256);
   SS_LAUNCH((bwd_scan_kernel<MODE, N, true>), heads, kScanThreads);
   if constexpr (gate) SS_LAUNCH((bwd_scan_kernel<MODE, N, false>), heads, kScanThreads);
-  SS_LAUNCH((bwd_group_kernel<MODE, N, false>), groups, kGroupThreads);
-  SS_LAUNCH((bwd_group_kernel<MODE, N, true>), groups, kGroupThreads);
+  SS_LAUNCH((bwd_pair_kernel<MODE, N>), places * p.ngroups * kPairs, 256);
+  SS_LAUNCH((bwd_out_kernel<MODE, N>), places * p.ngroups * 4, kOutThreads);
   SS_LAUNCH((bwd_delta_kernel<io_of<MODE>()>), heads, 256);
   SS_LAUNCH(bwd_sum_kernel, p.nheads, 256);
   return hipSuccess;
