@@ -12,7 +12,7 @@
 // chunks are counted from each prompt's first row (ss_packed.h), so that no
 // chunk holds two prompts, and every prompt's state comes from and goes to
 // its slot of a pool.  Three kernels:
-//   prompt_state_kernel  per (chunk, head): S, and the decay over the chunk;
+//   prompt_state_kernel  per (chunk, a few heads): S, and the decay over the chunk;
 //                        further workgroups compute C B^T per (chunk, group);
 //   prompt_pass_kernel   per (prompt, head, 1024 elements): E of every chunk,
 //                        in the place of its S, and the final state;
@@ -28,6 +28,7 @@
 #include "ss_internal.h"
 #include "ss_mfma.h"
 #include "ss_packed.h"
+#include "ss_state.h"
 
 namespace ss {
 namespace {
@@ -44,127 +45,62 @@ __device__ __forceinline__ float step_size(const SsdPromptParams& p, float raw, 
 }
 
 // ---- pass 1: the chunks' own states, and C B^T --------------------------------
-// State workgroup = (chunk, head), 256 threads: S^T[n][p] = sum_j B_j[n] (w_j x_j[p])
-// over pieces of 64 steps staged in LDS as time-major tiles; wave w holds the
-// channels 16 w .. and all states.  w_j = exp(sum of Delta A behind j) Delta_j
-// comes from a sum that runs backwards, so that no difference of long sums
-// enters the state.
-template <int IO, int N>
-__device__ __forceinline__ void state_role(const SsdPromptParams& p, int place, int h) {
-  constexpr bool kTwo = IO == SS_F16;  // B needs a lo part
-  __shared__ __attribute__((aligned(16))) float sW[kQ];
-  __shared__ float sWave[4];
-  __shared__ __attribute__((aligned(16))) uint16_t sX[3][kJB * kP];
-  __shared__ __attribute__((aligned(16))) uint16_t sB[kTwo ? 2 : 1][N / 32][kJB * 32];
-  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+// State workgroup = (chunk, HB heads of a group): S of ss_state.h with u = x, V = B
+// and w_j = exp(sum of Delta A behind j) Delta_j, from a sum that runs backwards,
+// so that no difference of long sums enters the state.
+template <int IO, int N, int HB>
+__device__ __forceinline__ void state_role(const SsdPromptParams& p, int place, int g, int h0, int heads,
+                                           StateLds<N, HB, 1, 1, IO == SS_F16>& lds) {
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, team = tid / 256, t = tid % 256;
   const SeqChunk q = find_chunk<kLogQ>(p.cu, p.nseqs, p.tokens, place);
   if (q.chunk < 0 || q.chunk * kQ >= q.len) return;
   const int left = q.len - q.chunk * kQ, rows = left < kQ ? left : kQ;
   const int64_t row0 = q.begin + (int64_t)q.chunk * kQ;
-  const int g = h / (p.nheads / p.ngroups);
-  const int64_t xrow = p.x_stride * 2, brow = p.b_stride * 2;
-  const auto xv = rows_view(static_cast<const char*>(p.x) + row0 * xrow + h * kP * 2, xrow, rows);
-  const auto bv = rows_view(static_cast<const char*>(p.Bm) + row0 * brow + g * N * 2, brow, rows);
-  u32x4v xr[2], br[N / 32];
-  auto load_piece = [&](int j0) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) xr[k] = vload16(xv, (uint32_t)((j0 + tid / 8 + 32 * k) * xrow + (tid % 8) * 16));
-#pragma unroll
-    for (int k = 0; k < N / 32; ++k) br[k] = vload16(bv, (uint32_t)((j0 + tid / 4) * brow + k * 64 + (tid % 4) * 16));
-  };
-  load_piece(0);
-  {
-    const bool in = tid < rows;
-    const float delta = in ? step_size<IO>(p, load_io<IO>(p.dt, (row0 + tid) * p.dt_stride + h), h) : 0.0f;
-    const float da = delta * p.A[h];
-    float v = da;  // sum from this step to the end of the wave's 64
+  for (int hb = 0; hb < HB; hb += 2) {  // two heads at a time, 256 threads each
+    const int h = h0 + hb + team;
+    const bool in = t < rows && hb + team < heads;
+    const float delta = in ? step_size<IO>(p, load_io<IO>(p.dt, (row0 + t) * p.dt_stride + h), h) : 0.0f;
+    float v = in ? delta * p.A[h] : 0.0f;  // sum from this step to the end of the wave's 64
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
       const float o = __shfl_down(v, off, 64);
       if (lane + off < 64) v += o;
     }
-    if (lane == 0) sWave[wave] = v;
+    if (lane == 0) lds.wave[team][wave % 4] = v;
     __syncthreads();
     float behind = __shfl_down(v, 1, 64);
     if (lane == 63) behind = 0.0f;
-    for (int w = 3; w > wave; --w) behind += sWave[w];
-    sW[tid] = in ? exp2_hw(behind * kLog2e) * delta : 0.0f;
-    if (tid == 0)
-      p.ws_decay[(int64_t)place * p.nheads + h] = exp2_hw((sWave[0] + sWave[1] + sWave[2] + sWave[3]) * kLog2e);
-    __syncthreads();
+    const float* sum = lds.wave[team];
+    for (int w = 3; w > wave % 4; --w) behind += sum[w];
+    if (hb + team < HB) lds.w[hb + team][t] = in ? exp2_hw(behind * kLog2e) * delta : 0.0f;  // in: its head is there
+    if (t == 0 && hb + team < heads)
+      p.ws_decay[(int64_t)place * p.nheads + h] = exp2_hw((sum[0] + sum[1] + sum[2] + sum[3]) * kLog2e);
+    if (hb + 2 < HB) __syncthreads();
   }
-  const int xo[2] = {tm_lane_off<kP>(16 * wave, 0, lane), tm_lane_off<kP>(16 * wave, 1, lane)};
-  const int bo[2][2] = {{tm_lane_off<32>(0, 0, lane), tm_lane_off<32>(0, 1, lane)},
-                        {tm_lane_off<32>(16, 0, lane), tm_lane_off<32>(16, 1, lane)}};
-  f32x4 acc[N / 16];
-#pragma unroll
-  for (int t = 0; t < N / 16; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int j0 = 0; j0 < rows; j0 += kJB) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int row = tid / 8 + 32 * k;
-      const float w = sW[j0 + row];
-      u32x4v part[3];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t v[3];
-        split3(low16<IO>(xr[k][e]) * w, high16<IO>(xr[k][e]) * w, v);
-#pragma unroll
-        for (int i = 0; i < 3; ++i) part[i][e] = v[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x4v*>(&sX[i][tm_off<kP>(row, 8 * (tid % 8))]) = part[i];
-    }
-#pragma unroll
-    for (int k = 0; k < N / 32; ++k) {
-      const int at = tm_off<32>(tid / 4, 8 * (tid % 4));
-      if constexpr (kTwo) {
-        u32x4v hi, lo;
-        split8<IO>(br[k], hi, lo);
-        *reinterpret_cast<u32x4v*>(&sB[0][k][at]) = hi;
-        *reinterpret_cast<u32x4v*>(&sB[1][k][at]) = lo;
-      } else {
-        *reinterpret_cast<u32x4v*>(&sB[0][k][at]) = br[k];
-      }
-    }
-    __syncthreads();
-    if (j0 + kJB < rows) load_piece(j0 + kJB);  // lands while this piece is multiplied
-#pragma unroll
-    for (int ks = 0; ks < kJB; ks += 32) {
-      bf16x8 xp[3];  // [k = step][n = channel]
-#pragma unroll
-      for (int i = 0; i < 3; ++i) xp[i] = bfv(tm_frag(&sX[i][ks * kP], xo[0], xo[1]));
-#pragma unroll
-      for (int t = 0; t < N / 16; ++t) {
-#pragma unroll
-        for (int j = 0; j < (kTwo ? 2 : 1); ++j) {
-          const bf16x8 bp = bfv(tm_frag(&sB[j][t / 2][ks * 32], bo[t % 2][0], bo[t % 2][1]));  // [m = state][k = step]
-#pragma unroll
-          for (int i = 2 - j; i >= 0; --i) acc[t] = BF::run(bp, xp[i], acc[t]);
-        }
-      }
-    }
-    __syncthreads();
-  }
-  float* S = p.ws_state + ((int64_t)place * p.nheads + h) * (kP * N) + (16 * wave + lane % 16) * N + 4 * (lane / 16);
-#pragma unroll
-  for (int t = 0; t < N / 16; ++t) *reinterpret_cast<f32x4*>(S + 16 * t) = acc[t];
+  const int64_t xrow = p.x_stride, brow = p.b_stride;
+  const __amdgpu_buffer_rsrc_t xv[1] = {
+      rows_view(static_cast<const char*>(p.x) + (row0 * xrow + h0 * kP) * 2, xrow * 2, rows)};
+  const __amdgpu_buffer_rsrc_t bv[1] = {
+      rows_view(static_cast<const char*>(p.Bm) + (row0 * brow + g * N) * 2, brow * 2, rows)};
+  chunk_states<IO, N, HB, 1, 1, IO == SS_F16>(lds, xv, xrow, bv, brow, rows, heads,
+                                             p.ws_state + ((int64_t)place * p.nheads + h0) * (kP * N));
 }
 
-// C B^T workgroup = (chunk, group, band of 64 rows): for the band's rows i and
-// the columns j up to its end, in fp32, in the order in which the output pass
+// C B^T workgroup = (chunk, group, half of the rows): for the half's rows i and
+// the columns j up to the end of i's piece of 64, in fp32, in the order in which the output pass
 // reads its operands: element (i, j) of row tile it = i / 16 and k-step
 // kt = j / 32 is float j % 8 of lane i % 16 + 16 ((j % 32) / 8), 8 floats a
 // lane, so that pass reads whole contiguous kilobytes.  Wave w has row tile
-// 4 band + w; the product is built transposed (B C^T), so that a lane holds 4
+// 8 half + w; the product is built transposed (B C^T), so that a lane holds 4
 // consecutive columns of one row.
 template <int IO, int N>
-__device__ __forceinline__ void cb_role(const SsdPromptParams& p, int place, int g, int band) {
+__device__ __forceinline__ void cb_role(const SsdPromptParams& p, int place, int g, int half) {
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const SeqChunk q = find_chunk<kLogQ>(p.cu, p.nseqs, p.tokens, place);
   if (q.chunk < 0 || q.chunk * kQ >= q.len) return;
   const int left = q.len - q.chunk * kQ, rows = left < kQ ? left : kQ;
-  const int it = 4 * band + wave;
+  const int it = 8 * half + wave;
   if (16 * it >= rows) return;
   const int64_t row0 = q.begin + (int64_t)q.chunk * kQ;
   const int64_t brow = p.b_stride * 2, crow = p.c_stride * 2;
@@ -175,7 +111,7 @@ __device__ __forceinline__ void cb_role(const SsdPromptParams& p, int place, int
   for (int ks = 0; ks < N / 32; ++ks)
     c[ks] = vload16(cv, (uint32_t)((16 * it + lane % 16) * crow + (32 * ks + 8 * (lane / 16)) * 2));
   float* CB = p.ws_cb + ((int64_t)place * p.ngroups + g) * (kQ * kQ);
-  for (int jt = 0; jt < 4 * band + 4; ++jt) {
+  for (int jt = 0; jt < 4 * (it / 4) + 4; ++jt) {
     f32x4 acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int ks = 0; ks < N / 32; ++ks) {
@@ -187,15 +123,19 @@ __device__ __forceinline__ void cb_role(const SsdPromptParams& p, int place, int
   }
 }
 
-template <int IO, int N>
-__global__ void __launch_bounds__(256) prompt_state_kernel(SsdPromptParams p) {
-  const int states = p.chunks * p.nheads;
+template <int IO, int N, int HB>
+__global__ void __launch_bounds__(kStateThreads, IO == SS_F16 ? 2 : 4) prompt_state_kernel(SsdPromptParams p) {
+  __shared__ StateLds<N, HB, 1, 1, IO == SS_F16> lds;
+  const int hpg = p.nheads / p.ngroups, parts = (hpg + HB - 1) / HB;  // workgroups of a (chunk, group)
+  const int states = p.chunks * p.ngroups * parts;
   const int lb = (int)xcd_logical_block();
   if (lb < states) {
-    state_role<IO, N>(p, lb / p.nheads, lb % p.nheads);
+    const int part = lb % parts, g = (lb / parts) % p.ngroups, place = lb / (parts * p.ngroups);
+    const int left = hpg - part * HB;
+    state_role<IO, N, HB>(p, place, g, g * hpg + part * HB, left < HB ? left : HB, lds);
   } else {
     const int r = lb - states;
-    cb_role<IO, N>(p, r / (4 * p.ngroups), (r / 4) % p.ngroups, r % 4);
+    cb_role<IO, N>(p, r / (2 * p.ngroups), (r / 2) % p.ngroups, r % 2);
   }
 }
 
@@ -361,11 +301,13 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
       const bf16x8 eh = bfv(*reinterpret_cast<const u32x4v*>(&sE[0][at]));
       const bf16x8 el = bfv(*reinterpret_cast<const u32x4v*>(&sE[1][at]));
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        acc[b][pt] = BF::run(el, bfv(ch[b]), acc[b][pt]);
-        if constexpr (kTwo) acc[b][pt] = BF::run(eh, bfv(cl[b]), acc[b][pt]);
-        acc[b][pt] = BF::run(eh, bfv(ch[b]), acc[b][pt]);
+      for (int b = 0; b < 2; ++b) acc[b][pt] = BF::run(el, bfv(ch[b]), acc[b][pt]);
+      if constexpr (kTwo) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) acc[b][pt] = BF::run(eh, bfv(cl[b]), acc[b][pt]);
       }
+#pragma unroll
+      for (int b = 0; b < 2; ++b) acc[b][pt] = BF::run(eh, bfv(ch[b]), acc[b][pt]);
     }
   }
 #pragma unroll
@@ -412,6 +354,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
       const float ei = exp2_hw(between * kLog2e);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
+        if (ks == 1 && diag && blk[b] % 2 == 0) continue;  // columns behind all of the block's rows
         const int j0 = jb + 32 * ks + 8 * (lane / 16);
         float m[8];
         if (diag) {
@@ -437,17 +380,21 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
           mh[e] = a;
           ml[e] = c;
         }
+        bf16x8 xa[kTwo ? 2 : 1][4];  // A[m = p][k = step] = x^T, from the time-major tile
 #pragma unroll
-        for (int pt = 0; pt < 4; ++pt) {  // A[m = p][k = step] = x^T, from the time-major tile
-          const int o0 = tm_lane_off<kP>(16 * pt, 0, lane), o1 = tm_lane_off<kP>(16 * pt, 1, lane);
-          const bf16x8 xh = bfv(tm_frag(&sX[0][(jb + 32 * ks) * kP], o0, o1));
-          acc[b][pt] = BF::run(xh, bfv(ml), acc[b][pt]);
-          if constexpr (kTwo) {
-            const bf16x8 xl = bfv(tm_frag(&sX[kTwo ? 1 : 0][(jb + 32 * ks) * kP], o0, o1));
-            acc[b][pt] = BF::run(xl, bfv(mh), acc[b][pt]);
-          }
-          acc[b][pt] = BF::run(xh, bfv(mh), acc[b][pt]);
+        for (int i = 0; i < (kTwo ? 2 : 1); ++i)
+#pragma unroll
+          for (int pt = 0; pt < 4; ++pt)
+            xa[i][pt] = bfv(tm_frag(&sX[i][(jb + 32 * ks) * kP], tm_lane_off<kP>(16 * pt, 0, lane),
+                                    tm_lane_off<kP>(16 * pt, 1, lane)));
+#pragma unroll
+        for (int pt = 0; pt < 4; ++pt) acc[b][pt] = BF::run(xa[0][pt], bfv(ml), acc[b][pt]);
+        if constexpr (kTwo) {
+#pragma unroll
+          for (int pt = 0; pt < 4; ++pt) acc[b][pt] = BF::run(xa[kTwo ? 1 : 0][pt], bfv(mh), acc[b][pt]);
         }
+#pragma unroll
+        for (int pt = 0; pt < 4; ++pt) acc[b][pt] = BF::run(xa[0][pt], bfv(mh), acc[b][pt]);
       }
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
@@ -485,11 +432,21 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
   }
 }
 
+template <int IO, int N, int HB>
+void launch_state(const SsdPromptParams& p, hipStream_t st) {
+  const uint32_t parts = (uint32_t)((p.nheads / p.ngroups + HB - 1) / HB);
+  hipLaunchKernelGGL((prompt_state_kernel<IO, N, HB>), dim3((uint32_t)p.chunks * (uint32_t)p.ngroups * (parts + 2)),
+                     dim3(kStateThreads), 0, st, p);
+}
 template <int IO, int N>
 hipError_t launch_prompt_n(const SsdPromptParams& p, hipStream_t st) {
   const uint32_t chunks = (uint32_t)p.chunks, heads = (uint32_t)p.nheads;
-  hipLaunchKernelGGL((prompt_state_kernel<IO, N>), dim3(chunks * heads + chunks * (uint32_t)p.ngroups * 4), dim3(256), 0,
-                     st, p);
+  switch (state_heads((int64_t)p.chunks * p.ngroups, p.nheads / p.ngroups, device_cus())) {
+    case 1: launch_state<IO, N, 1>(p, st); break;
+    case 2: launch_state<IO, N, 2>(p, st); break;
+    case 3: launch_state<IO, N, 3>(p, st); break;
+    default: launch_state<IO, N, 4>(p, st); break;
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((prompt_pass_kernel<N>), dim3((uint32_t)p.nseqs * heads * (kP * N / 1024)), dim3(256), 0, st, p);

@@ -45,6 +45,7 @@
 #include "ss_device.h"
 #include "ss_internal.h"
 #include "ss_mfma.h"
+#include "ss_state.h"
 
 namespace ss {
 namespace {
@@ -130,79 +131,53 @@ __global__ void __launch_bounds__(256) bwd_planes_kernel(PlaneJobs a) {
 }
 
 // ---- what a chunk adds to E and to R ------------------------------------------------
-// As prompt_state_kernel: out^T[n][p] = sum_t V_t[n] (w_t u_t[p]), pieces of 64
-// steps staged in LDS as time-major tiles, wave w holding channels 16 w ...
+// Workgroup = (chunk, HB heads of a group, E or R), the sums of ss_state.h:
 // E: u = x, V = B, w_j = exp(sum of Delta A behind j) Delta_j, from the last
 // document start on; R: u = g, V = C, w_i = exp(cs_i), before the first start.
-template <int MODE, int N>
-struct StateLds {
-  __attribute__((aligned(16))) float w[kQ];
-  float wave[4];
-  int first[4], count[4];
-  __attribute__((aligned(16))) uint16_t u[3][kJB * kP];
-  __attribute__((aligned(16))) uint16_t v[data_parts<MODE>()][N / 32][kJB * 32];
-};
-template <int MODE, int N, bool R>
-__device__ __forceinline__ void state_role(const SsdBwdParams& p, int place, int h, StateLds<MODE, N>& lds) {
+template <int MODE, int N, int HB, bool R>
+using StateOf = StateLds<N, HB, R ? g_parts<MODE>() : data_parts<MODE>(), data_parts<MODE>(), false>;
+
+template <int MODE, int N, int HB, bool R>
+__device__ __forceinline__ void state_role(const SsdBwdParams& p, int place, int g, int h0, int heads,
+                                           StateOf<MODE, N, HB, R>& lds) {
   constexpr int UP = R ? g_parts<MODE>() : data_parts<MODE>(), VP = data_parts<MODE>();
   constexpr int IO = io_of<MODE>();
-  auto& sW = lds.w;
-  auto& sWave = lds.wave;
-  auto& sFirst = lds.first;
-  auto& sCount = lds.count;
-  auto& sU = lds.u;
-  auto& sV = lds.v;
-  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  const int tid = threadIdx.x, lane = tid % 64, team = tid / 256, t = tid % 256, wave = t / 64;
   const Chunk q = chunk_of(p, place);
-  const int g = h / (p.nheads / p.ngroups);
-  const int64_t urow = (int64_t)p.nheads * kP, vrow = (int64_t)p.ngroups * N;
-  __amdgpu_buffer_rsrc_t uv[UP], vv[VP];
-#pragma unroll
-  for (int i = 0; i < UP; ++i) uv[i] = plane_view(R ? p.gp[i] : p.xp[i % 2], q.row0, urow, h * kP, q.rows);
-#pragma unroll
-  for (int i = 0; i < VP; ++i) vv[i] = plane_view(R ? p.cp[i] : p.bp[i], q.row0, vrow, g * N, q.rows);
-  u32x4v ur[UP][2], vr[VP][N / 32];
-  auto load_piece = [&](int j0) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t off = (uint32_t)((j0 + tid / 8 + 32 * k) * urow * 2 + (tid % 8) * 16);
-#pragma unroll
-      for (int i = 0; i < UP; ++i) ur[i][k] = vload16(uv[i], off);
+  // documents: starts at or before each step of the chunk
+  int seg = 0, starts = 0, first = kQ;
+  if (p.seq_idx) {
+    const int64_t at = q.row0 + t;
+    const bool st = t < q.rows && at % p.seqlen != 0 && p.seq_idx[at] != p.seq_idx[at - 1];
+    const uint64_t m = __builtin_amdgcn_ballot_w64(st);
+    if (lane == 0 && team == 0) {
+      lds.count[wave] = (int)__builtin_popcountll(m);
+      lds.first[wave] = m ? 64 * wave + (int)__builtin_ctzll(m) : kQ;
     }
+    seg = (int)__builtin_popcountll(m & (lane == 63 ? ~0ull : (2ull << lane) - 1));
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) seg += lds.count[w];
+    starts = lds.count[0] + lds.count[1] + lds.count[2] + lds.count[3];
+    first = min(min(lds.first[0], lds.first[1]), min(lds.first[2], lds.first[3]));
+    if (!R && h0 == 0 && team == 0) p.ws_seg[(int64_t)place * kQ + t] = seg;
+  }
 #pragma unroll
-    for (int k = 0; k < N / 32; ++k) {
-      const uint32_t off = (uint32_t)((j0 + tid / 4) * vrow * 2 + k * 64 + (tid % 4) * 16);
-#pragma unroll
-      for (int i = 0; i < VP; ++i) vr[i][k] = vload16(vv[i], off);
-    }
-  };
-  load_piece(0);
-  {
-    const bool in = tid < q.rows;
+  for (int hb = 0; hb < HB; hb += 2) {  // two heads at a time, 256 threads each
+    const int h = h0 + hb + team;
+    const bool mine = hb + team < heads, in = mine && t < q.rows;
     float delta = 0.0f;
     if (in) {
-      const float xd = load_io<IO>(p.dt, (q.row0 + tid) * p.nheads + h) + (p.dt_bias ? p.dt_bias[h] : 0.0f);
+      const float xd = load_io<IO>(p.dt, (q.row0 + t) * p.nheads + h) + (p.dt_bias ? p.dt_bias[h] : 0.0f);
       delta = p.softplus ? softplus_f(xd) : xd;
     }
-    // documents: starts at or before each step of the chunk
-    int seg = 0, starts = 0, first = kQ;
-    if (p.seq_idx) {
-      const int64_t t = q.row0 + tid;
-      const bool st = in && t % p.seqlen != 0 && p.seq_idx[t] != p.seq_idx[t - 1];
-      const uint64_t m = __builtin_amdgcn_ballot_w64(st);
-      if (lane == 0) {
-        sCount[wave] = (int)__builtin_popcountll(m);
-        sFirst[wave] = m ? 64 * wave + (int)__builtin_ctzll(m) : kQ;
-      }
-      seg = (int)__builtin_popcountll(m & (lane == 63 ? ~0ull : (2ull << lane) - 1));
-    }
+    const float A = mine ? p.A[h] : 0.0f;
     // R: the sum up to this step in the wave's 64; E: from this step on.  The
     // former's differences decide the weights of neighbouring steps, whose
     // exponents are small where the sums are not: it is formed in 64 bits and
     // kept as two floats.
-    float v = delta * p.A[h], low = 0.0f;
+    float v = delta * A, low = 0.0f;
     if constexpr (R) {
-      double c = (double)delta * (double)p.A[h];
+      double c = (double)delta * (double)A;
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
         const double o = __shfl_up(c, off, 64);
@@ -217,106 +192,56 @@ __device__ __forceinline__ void state_role(const SsdBwdParams& p, int place, int
         if (lane + off < 64) v += o;
       }
     }
-    if (lane == (R ? 63 : 0)) sWave[wave] = v;
+    float* sum = lds.wave[team];
+    if (lane == (R ? 63 : 0)) sum[wave] = v;
     __syncthreads();
-    if (p.seq_idx) {
-      for (int w = 0; w < wave; ++w) seg += sCount[w];
-      starts = sCount[0] + sCount[1] + sCount[2] + sCount[3];
-      first = min(min(sFirst[0], sFirst[1]), min(sFirst[2], sFirst[3]));
-    }
-    const int64_t at = ((int64_t)place * p.nheads + h) * kQ + tid;
-    float w;
-    if constexpr (R) {
-      const float behind = (__shfl(v, 63, 64) - v) + (__shfl(low, 63, 64) - low);
-      p.ws_cs[at] = v;
-      p.ws_cl[at] = low;
-      p.ws_from[at] = exp2_hw(v * kLog2e);
-      p.ws_to[at] = exp2_hw(behind * kLog2e);
-      for (int k = 0; k < wave; ++k) v += sWave[k];
-      w = tid < first ? exp2_hw(v * kLog2e) : 0.0f;
-      p.ws_wc[at] = w;
-    } else {
-      p.ws_delta[at] = delta;
-      float behind = __shfl_down(v, 1, 64);
-      if (lane == 63) behind = 0.0f;
-      for (int k = 3; k > wave; --k) behind += sWave[k];
-      w = seg == starts ? exp2_hw(behind * kLog2e) : 0.0f;
-      p.ws_wb[at] = w;
-      w *= delta;
-      if (p.seq_idx && h == 0) p.ws_seg[(int64_t)place * kQ + tid] = seg;
-      if (tid == 0)
-        p.ws_decay[(int64_t)place * p.nheads + h] =
-            starts ? 0.0f : exp2_hw((sWave[0] + sWave[1] + sWave[2] + sWave[3]) * kLog2e);
-    }
-    sW[tid] = in ? w : 0.0f;
-    __syncthreads();
-  }
-  const int uo[2] = {tm_lane_off<kP>(16 * wave, 0, lane), tm_lane_off<kP>(16 * wave, 1, lane)};
-  const int vo[2][2] = {{tm_lane_off<32>(0, 0, lane), tm_lane_off<32>(0, 1, lane)},
-                        {tm_lane_off<32>(16, 0, lane), tm_lane_off<32>(16, 1, lane)}};
-  f32x4 acc[N / 16];
-#pragma unroll
-  for (int t = 0; t < N / 16; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int j0 = 0; j0 < q.rows; j0 += kJB) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int row = tid / 8 + 32 * k;
-      const float w = sW[j0 + row];
-      u32x4v part[3];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float a = lo_f(ur[UP - 1][k][e]), b = hi_f(ur[UP - 1][k][e]);
-#pragma unroll
-        for (int i = UP - 2; i >= 0; --i) {
-          a += lo_f(ur[i][k][e]);
-          b += hi_f(ur[i][k][e]);
-        }
-        uint32_t v[3];
-        split3(a * w, b * w, v);
-#pragma unroll
-        for (int i = 0; i < 3; ++i) part[i][e] = v[i];
+    const int64_t at = ((int64_t)place * p.nheads + h) * kQ + t;
+    float w = 0.0f;
+    if (mine) {
+      if constexpr (R) {
+        const float behind = (__shfl(v, 63, 64) - v) + (__shfl(low, 63, 64) - low);
+        p.ws_cs[at] = v;
+        p.ws_cl[at] = low;
+        p.ws_from[at] = exp2_hw(v * kLog2e);
+        p.ws_to[at] = exp2_hw(behind * kLog2e);
+        for (int k = 0; k < wave; ++k) v += sum[k];
+        w = t < first ? exp2_hw(v * kLog2e) : 0.0f;
+        p.ws_wc[at] = w;
+      } else {
+        p.ws_delta[at] = delta;
+        float behind = __shfl_down(v, 1, 64);
+        if (lane == 63) behind = 0.0f;
+        for (int k = 3; k > wave; --k) behind += sum[k];
+        w = seg == starts ? exp2_hw(behind * kLog2e) : 0.0f;
+        p.ws_wb[at] = w;
+        w *= delta;
+        if (t == 0)
+          p.ws_decay[(int64_t)place * p.nheads + h] =
+              starts ? 0.0f : exp2_hw((sum[0] + sum[1] + sum[2] + sum[3]) * kLog2e);
       }
-#pragma unroll
-      for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x4v*>(&sU[i][tm_off<kP>(row, 8 * (tid % 8))]) = part[i];
     }
-#pragma unroll
-    for (int k = 0; k < N / 32; ++k)
-#pragma unroll
-      for (int i = 0; i < VP; ++i)
-        *reinterpret_cast<u32x4v*>(&sV[i][k][tm_off<32>(tid / 4, 8 * (tid % 4))]) = vr[i][k];
-    __syncthreads();
-    if (j0 + kJB < q.rows) load_piece(j0 + kJB);  // lands while this piece is multiplied
-#pragma unroll
-    for (int ks = 0; ks < kJB; ks += 32) {
-      bf16x8 up[3];
-#pragma unroll
-      for (int i = 0; i < 3; ++i) up[i] = bfv(tm_frag(&sU[i][ks * kP], uo[0], uo[1]));
-#pragma unroll
-      for (int t = 0; t < N / 16; ++t)
-#pragma unroll
-        for (int j = 0; j < VP; ++j) {
-          const bf16x8 vp = bfv(tm_frag(&sV[j][t / 2][ks * 32], vo[t % 2][0], vo[t % 2][1]));
-#pragma unroll
-          for (int i = 2 - j; i >= 0; --i) acc[t] = BF::run(vp, up[i], acc[t]);
-        }
-    }
-    __syncthreads();
+    if (hb + team < HB) lds.w[hb + team][t] = in ? w : 0.0f;
+    if (hb + 2 < HB) __syncthreads();
   }
-  float* S = (R ? p.ws_R : p.ws_E) + ((int64_t)place * p.nheads + h) * (kP * N) + (16 * wave + lane % 16) * N +
-             4 * (lane / 16);
+  const int64_t urow = (int64_t)p.nheads * kP, vrow = (int64_t)p.ngroups * N;
+  __amdgpu_buffer_rsrc_t uv[UP], vv[VP];
 #pragma unroll
-  for (int t = 0; t < N / 16; ++t) *reinterpret_cast<f32x4*>(S + 16 * t) = acc[t];
+  for (int i = 0; i < UP; ++i) uv[i] = plane_view(R ? p.gp[i] : p.xp[i % 2], q.row0, urow, h0 * kP, q.rows);
+#pragma unroll
+  for (int i = 0; i < VP; ++i) vv[i] = plane_view(R ? p.cp[i] : p.bp[i], q.row0, vrow, g * N, q.rows);
+  chunk_states<IO, N, HB, UP, VP, false>(lds, uv, urow, vv, vrow, q.rows, heads,
+                                         (R ? p.ws_R : p.ws_E) + ((int64_t)place * p.nheads + h0) * (kP * N));
 }
 
 // C B^T (REV false: rows i of C, columns j of B up to the row's piece) or B C^T
 // (REV true: rows j of B, columns i of C from the row's piece to the last) of a
 // chunk in operand order, fp32; rows past the chunk come out as zeros.
 template <int MODE, int N, bool REV>
-__device__ __forceinline__ void cb_role(const SsdBwdParams& p, int place, int g, int band) {
+__device__ __forceinline__ void cb_role(const SsdBwdParams& p, int place, int g, int half) {
   constexpr int IO = io_of<MODE>();
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const Chunk q = chunk_of(p, place);
-  const int it = 4 * band + wave;
+  const int it = 8 * half + wave, piece = it / 4;
   if (16 * it >= q.rows) return;
   const int64_t row = (int64_t)p.ngroups * N;
   const auto bv = plane_view(static_cast<const uint16_t*>(REV ? p.Cm : p.Bm), q.row0, row, g * N, q.rows);
@@ -326,8 +251,8 @@ __device__ __forceinline__ void cb_role(const SsdBwdParams& p, int place, int g,
   for (int ks = 0; ks < N / 32; ++ks)
     c[ks] = vload16(cv, (uint32_t)((16 * it + lane % 16) * row * 2 + (32 * ks + 8 * (lane / 16)) * 2));
   float* CB = (REV ? p.ws_bc : p.ws_cb) + ((int64_t)place * p.ngroups + g) * (kQ * kQ);
-  const int j1 = REV ? 4 * ((q.rows + kJB - 1) / kJB) : 4 * band + 4;
-  for (int jt = REV ? 4 * band : 0; jt < j1; ++jt) {
+  const int j1 = REV ? 4 * ((q.rows + kJB - 1) / kJB) : 4 * piece + 4;
+  for (int jt = REV ? 4 * piece : 0; jt < j1; ++jt) {
     f32x4 acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int ks = 0; ks < N / 32; ++ks) {
@@ -339,22 +264,28 @@ __device__ __forceinline__ void cb_role(const SsdBwdParams& p, int place, int g,
   }
 }
 
-template <int MODE, int N>
-__global__ void __launch_bounds__(256) bwd_state_kernel(SsdBwdParams p) {
-  __shared__ StateLds<MODE, N> lds;
-  const int places = (int)p.batch * p.nchunks, states = places * p.nheads, cbs = places * p.ngroups * 4;
+template <int MODE, int N, int HB>
+__global__ void __launch_bounds__(kStateThreads, MODE == 0 ? 4 : 2) bwd_state_kernel(SsdBwdParams p) {
+  __shared__ union {
+    StateOf<MODE, N, HB, false> e;
+    StateOf<MODE, N, HB, true> r;
+  } lds;
+  const int places = (int)p.batch * p.nchunks, cbs = places * p.ngroups * 2;
+  const int hpg = p.nheads / p.ngroups, parts = (hpg + HB - 1) / HB;  // workgroups of a (chunk, group) and role
+  const int states = places * p.ngroups * parts * 2;
   int lb = (int)xcd_logical_block();
-  if (lb < 2 * states) {
-    const int place = lb / (2 * p.nheads), r = lb - place * 2 * p.nheads;
-    if (r < p.nheads) state_role<MODE, N, false>(p, place, r, lds);
-    else state_role<MODE, N, true>(p, place, r - p.nheads, lds);
+  if (lb < states) {
+    const int part = (lb >> 1) % parts, g = ((lb >> 1) / parts) % p.ngroups, place = (lb >> 1) / (parts * p.ngroups);
+    const int left = hpg - part * HB, heads = left < HB ? left : HB, h0 = g * hpg + part * HB;
+    if (lb & 1) state_role<MODE, N, HB, true>(p, place, g, h0, heads, lds.r);
+    else state_role<MODE, N, HB, false>(p, place, g, h0, heads, lds.e);
   } else {
-    lb -= 2 * states;
+    lb -= states;
     if (lb < cbs) {
-      cb_role<MODE, N, true>(p, lb / (4 * p.ngroups), (lb / 4) % p.ngroups, lb % 4);
+      cb_role<MODE, N, true>(p, lb / (2 * p.ngroups), (lb / 2) % p.ngroups, lb % 2);
     } else {
       lb -= cbs;
-      cb_role<MODE, N, false>(p, lb / (4 * p.ngroups), (lb / 4) % p.ngroups, lb % 4);
+      cb_role<MODE, N, false>(p, lb / (2 * p.ngroups), (lb / 2) % p.ngroups, lb % 2);
     }
   }
 }
@@ -531,11 +462,13 @@ __global__ void __launch_bounds__(kScanThreads, MODE == 0 ? 4 : 2) bwd_scan_kern
       const bf16x8 kh = bfv(*reinterpret_cast<const u32x4v*>(&sK[0][at]));
       const bf16x8 kl = bfv(*reinterpret_cast<const u32x4v*>(&sK[1][at]));
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        acc[b][pt] = BF::run(kl, bfv(vf[0][b][ks]), acc[b][pt]);
-        if constexpr (VP > 1) acc[b][pt] = BF::run(kh, bfv(vf[VP - 1][b][ks]), acc[b][pt]);
-        acc[b][pt] = BF::run(kh, bfv(vf[0][b][ks]), acc[b][pt]);
+      for (int b = 0; b < 2; ++b) acc[b][pt] = BF::run(kl, bfv(vf[0][b][ks]), acc[b][pt]);
+      if constexpr (VP > 1) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) acc[b][pt] = BF::run(kh, bfv(vf[VP - 1][b][ks]), acc[b][pt]);
       }
+#pragma unroll
+      for (int b = 0; b < 2; ++b) acc[b][pt] = BF::run(kh, bfv(vf[0][b][ks]), acc[b][pt]);
     }
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
@@ -580,6 +513,8 @@ __global__ void __launch_bounds__(kScanThreads, MODE == 0 ? 4 : 2) bwd_scan_kern
       const float fo = exp2_hw(arg * kLog2e);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
+        // steps all behind (REV: before) the block's rows
+        if (diag && ks == (REV ? 0 : 1) && blk[b] % 2 == (REV ? 1 : 0)) continue;
         const int s = kJB * sp + 32 * ks + 8 * (lane / 16);
         float m[8];
         if (diag) {
@@ -610,17 +545,21 @@ __global__ void __launch_bounds__(kScanThreads, MODE == 0 ? 4 : 2) bwd_scan_kern
           mh[e] = a;
           ml[e] = c;
         }
+        bf16x8 ua[UP][4];
 #pragma unroll
-        for (int pt = 0; pt < 4; ++pt) {
-          const int o0 = tm_lane_off<kP>(16 * pt, 0, lane), o1 = tm_lane_off<kP>(16 * pt, 1, lane);
-          const bf16x8 a = bfv(tm_frag(&sU[0][(kJB * sp + 32 * ks) * kP], o0, o1));
-          acc[b][pt] = BF::run(a, bfv(ml), acc[b][pt]);
-          if constexpr (UP > 1) {
-            const bf16x8 a2 = bfv(tm_frag(&sU[UP - 1][(kJB * sp + 32 * ks) * kP], o0, o1));
-            acc[b][pt] = BF::run(a2, bfv(mh), acc[b][pt]);
-          }
-          acc[b][pt] = BF::run(a, bfv(mh), acc[b][pt]);
+        for (int i = 0; i < UP; ++i)
+#pragma unroll
+          for (int pt = 0; pt < 4; ++pt)
+            ua[i][pt] = bfv(tm_frag(&sU[i][(kJB * sp + 32 * ks) * kP], tm_lane_off<kP>(16 * pt, 0, lane),
+                                    tm_lane_off<kP>(16 * pt, 1, lane)));
+#pragma unroll
+        for (int pt = 0; pt < 4; ++pt) acc[b][pt] = BF::run(ua[0][pt], bfv(ml), acc[b][pt]);
+        if constexpr (UP > 1) {
+#pragma unroll
+          for (int pt = 0; pt < 4; ++pt) acc[b][pt] = BF::run(ua[UP - 1][pt], bfv(mh), acc[b][pt]);
         }
+#pragma unroll
+        for (int pt = 0; pt < 4; ++pt) acc[b][pt] = BF::run(ua[0][pt], bfv(mh), acc[b][pt]);
       }
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
@@ -766,8 +705,8 @@ __device__ __forceinline__ void pair_role(const SsdBwdParams& p, const Chunk& q,
 
   // a head's operands on their way: x of the columns (row tid / 8 + 32 k, channels
   // 8 (tid % 8) ..), one vector element, g and the factors of this lane's row
-  u32x4v xr[XP][2], gf[GP][2];
-  float vr = 0.0f, fi, li = 0.0f, between = 0.0f;
+  u32x4v xr[XP][2], gn[GP][2];
+  float vr = 0.0f, fn, ln = 0.0f, mid[2] = {0.0f, 0.0f};
   auto load_head = [&](int h) {
     const int64_t at = ((int64_t)q.place * p.nheads + h) * kQ;
 #pragma unroll
@@ -783,14 +722,15 @@ __device__ __forceinline__ void pair_role(const SsdBwdParams& p, const Chunk& q,
     for (int i = 0; i < GP; ++i) {
       const auto gv = plane_view(p.gp[i], q.row0, xrow, h * kP, rows);
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) gf[i][ks] = vload16(gv, (uint32_t)(il * xrow * 2 + (32 * ks + 8 * quad) * 2));
+      for (int ks = 0; ks < 2; ++ks) gn[i][ks] = vload16(gv, (uint32_t)(il * xrow * 2 + (32 * ks + 8 * quad) * 2));
     }
-    fi = (DIAG ? p.ws_cs : p.ws_from)[at + il];
+    fn = (DIAG ? p.ws_cs : p.ws_from)[at + il];
     if constexpr (DIAG) {
-      li = p.ws_cl[at + il];
-    } else {
-      between = 0.0f;
-      for (int k = jb + 1; k < ib; ++k) between += p.ws_cs[at + kJB * k + kJB - 1];
+      ln = p.ws_cl[at + il];
+    } else {  // the sums over the pieces between
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (jb + 1 + k < ib) mid[k] = p.ws_cs[at + kJB * (jb + 1 + k) + kJB - 1];
     }
   };
   load_head(g * hpg);
@@ -806,6 +746,13 @@ __device__ __forceinline__ void pair_role(const SsdBwdParams& p, const Chunk& q,
         for (int k = 0; k < 2; ++k)
           *reinterpret_cast<u32x4v*>(&lds.x[turn][i][row64_off(tid / 8 + 32 * k, 8 * (tid % 8))]) = xr[i][k];
       if (wave < (DIAG ? 3 : 2)) lds.vec[turn][wave][lane] = vr;
+      u32x4v gf[GP][2];
+#pragma unroll
+      for (int i = 0; i < GP; ++i)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) gf[i][ks] = gn[i][ks];
+      const float f = DIAG ? fn : fn * exp2_hw((mid[0] + mid[1]) * kLog2e), l = ln;
+      if (h + 1 < (g + 1) * hpg) load_head(h + 1);
       __syncthreads();
       f32x4 a[4];
 #pragma unroll
@@ -824,8 +771,6 @@ __device__ __forceinline__ void pair_role(const SsdBwdParams& p, const Chunk& q,
 #pragma unroll
               for (int t = 0; t < 4; ++t) a[t] = BF::run(xf[t], bfv(gf[i][ks]), a[t]);
         }
-      const float f = DIAG ? fi : fi * exp2_hw(between * kLog2e), l = li;
-      if (h + 1 < (g + 1) * hpg) load_head(h + 1);
       float xd = 0.0f;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
@@ -1019,11 +964,7 @@ __device__ __forceinline__ void out_role(const SsdBwdParams& p, int lb, uint16_t
       df[b] = DB ? p.ws_delta[at + fr[b]] : 1.0f;
     }
   };
-  load_k(g * hpg);
-  load_f(g * hpg);
-  for (int hg = 0; hg < hpg; ++hg) {
-    const int h = g * hpg + hg;
-    uint16_t* buf = lds + (hg & 1) * kBuf;
+  auto stage_k = [&](uint16_t* buf) {
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const int item = tid + kOutThreads * k;
@@ -1037,30 +978,44 @@ __device__ __forceinline__ void out_role(const SsdBwdParams& p, int lb, uint16_t
         for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2*>(&buf[i * kP * NH + at]) = make_uint2(a[i], b[i]);
       }
     }
+  };
+  load_k(g * hpg);
+  load_f(g * hpg);
+  stage_k(lds);
+  if (hpg > 1) load_k(g * hpg + 1);
+  for (int hg = 0; hg < hpg; ++hg) {
+    const int h = g * hpg + hg;
+    const uint16_t* buf = lds + (hg & 1) * kBuf;
     __syncthreads();
-    if (hg + 1 < hpg) load_k(h + 1);
     f32x4 a[2][NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int b = 0; b < 2; ++b) a[b][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        const int r0 = 32 * ks + 8 * quad + l16 / 4, c = 4 * (l16 % 4);
-        const int o0 = t16_off(r0, c), o1 = t16_off(r0 + 4, c);
+    for (int ks = 0; ks < 2; ++ks) {
+      const int r0 = 32 * ks + 8 * quad + l16 / 4, c = 4 * (l16 % 4);
+      const int o0 = t16_off(r0, c), o1 = t16_off(r0 + 4, c);
 #pragma unroll
-        for (int j = 2; j >= 0; --j) {
-          const bf16x8 kp = bfv(tm_frag(buf + j * kP * NH + t * (kP * 16), o0, o1));
+      for (int j = 2; j >= 0; --j) {
+        bf16x8 kp[NT];
 #pragma unroll
-          for (int i = FP - 1; i >= 0; --i)
-            if (i + j <= 2)
+        for (int t = 0; t < NT; ++t) kp[t] = bfv(tm_frag(buf + j * kP * NH + t * (kP * 16), o0, o1));
 #pragma unroll
-              for (int b = 0; b < 2; ++b) a[b][t] = BF::run(kp, bfv(F[i][b][ks]), a[b][t]);
-        }
+        for (int i = FP - 1; i >= 0; --i)
+          if (i + j <= 2)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int b = 0; b < 2; ++b) a[b][t] = BF::run(kp[t], bfv(F[i][b][ks]), a[b][t]);
       }
     }
     const float w[2] = {wf[0], wf[1]}, d[2] = {df[0], df[1]};
-    if (hg + 1 < hpg) load_f(h + 1);
+    if (hg + 1 < hpg) {  // the next head's K into the other buffer, the one after on its way
+      load_f(h + 1);
+      stage_k(lds + ((hg + 1) & 1) * kBuf);
+      if (hg + 2 < hpg) load_k(h + 2);
+    }
     const int64_t to = ((int64_t)half * p.batch * p.nchunks * p.nheads + (int64_t)q.place * p.nheads + h) * kQ;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
@@ -1254,11 +1209,24 @@ __global__ void __launch_bounds__(256) bwd_sum_kernel(SsdBwdParams p) {
     if (e_ != hipSuccess) return e_;                                    \
   } while (0)
 
+template <int MODE, int N, int HB>
+hipError_t launch_state(const SsdBwdParams& p, hipStream_t st) {
+  const int64_t groups = p.batch * p.nchunks * p.ngroups, parts = (p.nheads / p.ngroups + HB - 1) / HB;
+  SS_LAUNCH((bwd_state_kernel<MODE, N, HB>), groups * (2 * parts + (MODE % 2 ? 4 : 2)), kStateThreads);
+  return hipSuccess;
+}
 template <int MODE, int N>
 hipError_t launch_n(const SsdBwdParams& p, hipStream_t st) {
-  const int64_t places = p.batch * p.nchunks, heads = places * p.nheads, groups = places * p.ngroups * 4;
+  const int64_t places = p.batch * p.nchunks, heads = places * p.nheads;
   constexpr bool gate = MODE % 2 != 0;
-  SS_LAUNCH((bwd_state_kernel<MODE, N>), 2 * heads + groups * (gate ? 2 : 1), 256);
+  hipError_t e;
+  switch (state_heads(2 * places * p.ngroups, p.nheads / p.ngroups, device_cus())) {
+    case 1: e = launch_state<MODE, N, 1>(p, st); break;
+    case 2: e = launch_state<MODE, N, 2>(p, st); break;
+    case 3: e = launch_state<MODE, N, 3>(p, st); break;
+    default: e = launch_state<MODE, N, 4>(p, st); break;
+  }
+  if (e != hipSuccess) return e;
   SS_LAUNCH((bwd_pass_kernel<N>), p.batch * p.nheads * (kP * N / 1024), 256);
   SS_LAUNCH((bwd_scan_kernel<MODE, N, true>), heads, kScanThreads);
   if constexpr (gate) SS_LAUNCH((bwd_scan_kernel<MODE, N, false>), heads, kScanThreads);
