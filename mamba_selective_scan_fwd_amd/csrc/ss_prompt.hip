@@ -111,13 +111,19 @@ __device__ __forceinline__ void cb_role(const SsdPromptParams& p, int place, int
   for (int ks = 0; ks < N / 32; ++ks)
     c[ks] = vload16(cv, (uint32_t)((16 * it + lane % 16) * crow + (32 * ks + 8 * (lane / 16)) * 2));
   float* CB = p.ws_cb + ((int64_t)place * p.ngroups + g) * (kQ * kQ);
-  for (int jt = 0; jt < 4 * (it / 4) + 4; ++jt) {
+  u32x4v b[N / 32];
+  auto load_b = [&](int jt) {
+#pragma unroll
+    for (int ks = 0; ks < N / 32; ++ks)
+      b[ks] = vload16(bv, (uint32_t)((16 * jt + lane % 16) * brow + (32 * ks + 8 * (lane / 16)) * 2));
+  };
+  load_b(0);
+  const int j1 = 4 * (it / 4) + 4;
+  for (int jt = 0; jt < j1; ++jt) {
     f32x4 acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int ks = 0; ks < N / 32; ++ks) {
-      const u32x4v b = vload16(bv, (uint32_t)((16 * jt + lane % 16) * brow + (32 * ks + 8 * (lane / 16)) * 2));
-      acc = mfma_t<IO>::run(as_vec<IO>(b), as_vec<IO>(c[ks]), acc);
-    }
+    for (int ks = 0; ks < N / 32; ++ks) acc = mfma_t<IO>::run(as_vec<IO>(b[ks]), as_vec<IO>(c[ks]), acc);
+    if (jt + 1 < j1) load_b(jt + 1);
     const int to = lane % 16 + 16 * (2 * (jt & 1) + lane / 32);
     *reinterpret_cast<f32x4*>(CB + cb_at(it, jt / 2) + to * 8 + 4 * ((lane / 16) & 1)) = acc;
   }
@@ -126,16 +132,16 @@ __device__ __forceinline__ void cb_role(const SsdPromptParams& p, int place, int
 template <int IO, int N, int HB>
 __global__ void __launch_bounds__(kStateThreads, IO == SS_F16 ? 2 : 4) prompt_state_kernel(SsdPromptParams p) {
   __shared__ StateLds<N, HB, 1, 1, IO == SS_F16> lds;
-  const int hpg = p.nheads / p.ngroups, parts = (hpg + HB - 1) / HB;  // workgroups of a (chunk, group)
-  const int states = p.chunks * p.ngroups * parts;
-  const int lb = (int)xcd_logical_block();
-  if (lb < states) {
-    const int part = lb % parts, g = (lb / parts) % p.ngroups, place = lb / (parts * p.ngroups);
-    const int left = hpg - part * HB;
-    state_role<IO, N, HB>(p, place, g, g * hpg + part * HB, left < HB ? left : HB, lds);
+  // a (chunk, group) has 2 workgroups for C B^T, which take longest, then `parts`
+  // for the states, all on one XCD
+  const int hpg = p.nheads / p.ngroups, parts = (hpg + HB - 1) / HB;
+  const int lb = (int)xcd_logical_block(), r = lb % (parts + 2), g = (lb / (parts + 2)) % p.ngroups;
+  const int place = lb / (parts + 2) / p.ngroups;
+  if (r < 2) {
+    cb_role<IO, N>(p, place, g, 1 - r);
   } else {
-    const int r = lb - states;
-    cb_role<IO, N>(p, r / (2 * p.ngroups), (r / 2) % p.ngroups, r % 2);
+    const int h = (r - 2) * HB, left = hpg - h;
+    state_role<IO, N, HB>(p, place, g, g * hpg + h, left < HB ? left : HB, lds);
   }
 }
 

@@ -252,13 +252,18 @@ __device__ __forceinline__ void cb_role(const SsdBwdParams& p, int place, int g,
     c[ks] = vload16(cv, (uint32_t)((16 * it + lane % 16) * row * 2 + (32 * ks + 8 * (lane / 16)) * 2));
   float* CB = (REV ? p.ws_bc : p.ws_cb) + ((int64_t)place * p.ngroups + g) * (kQ * kQ);
   const int j1 = REV ? 4 * ((q.rows + kJB - 1) / kJB) : 4 * piece + 4;
+  u32x4v b[N / 32];
+  auto load_b = [&](int jt) {
+#pragma unroll
+    for (int ks = 0; ks < N / 32; ++ks)
+      b[ks] = vload16(bv, (uint32_t)((16 * jt + lane % 16) * row * 2 + (32 * ks + 8 * (lane / 16)) * 2));
+  };
+  load_b(REV ? 4 * piece : 0);
   for (int jt = REV ? 4 * piece : 0; jt < j1; ++jt) {
     f32x4 acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int ks = 0; ks < N / 32; ++ks) {
-      const u32x4v b = vload16(bv, (uint32_t)((16 * jt + lane % 16) * row * 2 + (32 * ks + 8 * (lane / 16)) * 2));
-      acc = mfma_t<IO>::run(as_vec<IO>(b), as_vec<IO>(c[ks]), acc);
-    }
+    for (int ks = 0; ks < N / 32; ++ks) acc = mfma_t<IO>::run(as_vec<IO>(b[ks]), as_vec<IO>(c[ks]), acc);
+    if (jt + 1 < j1) load_b(jt + 1);
     const int to = lane % 16 + 16 * (2 * (jt & 1) + lane / 32);
     *reinterpret_cast<f32x4*>(CB + cb_at(it, jt / 2) + to * 8 + 4 * ((lane / 16) & 1)) = acc;
   }
@@ -270,23 +275,19 @@ __global__ void __launch_bounds__(kStateThreads, MODE == 0 ? 4 : 2) bwd_state_ke
     StateOf<MODE, N, HB, false> e;
     StateOf<MODE, N, HB, true> r;
   } lds;
-  const int places = (int)p.batch * p.nchunks, cbs = places * p.ngroups * 2;
-  const int hpg = p.nheads / p.ngroups, parts = (hpg + HB - 1) / HB;  // workgroups of a (chunk, group) and role
-  const int states = places * p.ngroups * parts * 2;
-  int lb = (int)xcd_logical_block();
-  if (lb < states) {
-    const int part = (lb >> 1) % parts, g = ((lb >> 1) / parts) % p.ngroups, place = (lb >> 1) / (parts * p.ngroups);
-    const int left = hpg - part * HB, heads = left < HB ? left : HB, h0 = g * hpg + part * HB;
-    if (lb & 1) state_role<MODE, N, HB, true>(p, place, g, h0, heads, lds.r);
-    else state_role<MODE, N, HB, false>(p, place, g, h0, heads, lds.e);
+  // a (chunk, group) has 2 workgroups for B C^T and, if gated, 2 for C B^T, which
+  // take longest, then 2 * parts for the states, all on one XCD
+  constexpr int kCb = MODE % 2 ? 4 : 2;
+  const int hpg = p.nheads / p.ngroups, parts = (hpg + HB - 1) / HB, per = kCb + 2 * parts;
+  const int lb = (int)xcd_logical_block(), r = lb % per, g = (lb / per) % p.ngroups, place = lb / per / p.ngroups;
+  if (r < 2) {
+    cb_role<MODE, N, true>(p, place, g, r);
+  } else if (r < kCb) {
+    cb_role<MODE, N, false>(p, place, g, 1 - r % 2);
   } else {
-    lb -= states;
-    if (lb < cbs) {
-      cb_role<MODE, N, true>(p, lb / (2 * p.ngroups), (lb / 2) % p.ngroups, lb % 2);
-    } else {
-      lb -= cbs;
-      cb_role<MODE, N, false>(p, lb / (2 * p.ngroups), (lb / 2) % p.ngroups, lb % 2);
-    }
+    const int h = (r - kCb) / 2 * HB, left = hpg - h, heads = left < HB ? left : HB;
+    if (r & 1) state_role<MODE, N, HB, true>(p, place, g, g * hpg + h, heads, lds.r);
+    else state_role<MODE, N, HB, false>(p, place, g, g * hpg + h, heads, lds.e);
   }
 }
 
@@ -1212,7 +1213,7 @@ __global__ void __launch_bounds__(256) bwd_sum_kernel(SsdBwdParams p) {
 template <int MODE, int N, int HB>
 hipError_t launch_state(const SsdBwdParams& p, hipStream_t st) {
   const int64_t groups = p.batch * p.nchunks * p.ngroups, parts = (p.nheads / p.ngroups + HB - 1) / HB;
-  SS_LAUNCH((bwd_state_kernel<MODE, N, HB>), groups * (2 * parts + (MODE % 2 ? 4 : 2)), kStateThreads);
+  SS_LAUNCH((bwd_state_kernel<MODE, N, HB>), groups * ((MODE % 2 ? 4 : 2) + 2 * parts), kStateThreads);
   return hipSuccess;
 }
 template <int MODE, int N>
