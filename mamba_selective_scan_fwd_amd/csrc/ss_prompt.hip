@@ -147,11 +147,11 @@ __global__ void __launch_bounds__(kStateThreads, IO == SS_F16 ? 2 : 4) prompt_st
 
 // ---- pass 2: the states between the chunks -----------------------------------------
 // Workgroup = (prompt, head, 1024 elements), a thread 4 elements: E <- the
-// slot's state (or 0); per chunk, S <- E in memory and E <- decay E + S.  Four
-// chunks' S are loaded ahead.
-template <int N>
+// slot's state (or 0); per chunk, S <- E in memory and E <- decay E + S.  AHEAD
+// chunks' S are loaded ahead; a chunk's view is empty behind the last one.
+template <int N, int AHEAD>
 __global__ void __launch_bounds__(256) prompt_pass_kernel(SsdPromptParams p) {
-  constexpr int kParts = kP * N / 1024, kAhead = 4;
+  constexpr int kParts = kP * N / 1024;
   const int part = (int)(blockIdx.x % kParts);
   const int h = (int)((blockIdx.x / kParts) % (uint32_t)p.nheads);
   const int s = (int)(blockIdx.x / kParts / (uint32_t)p.nheads);
@@ -163,33 +163,45 @@ __global__ void __launch_bounds__(256) prompt_pass_kernel(SsdPromptParams p) {
   f32x4* state = reinterpret_cast<f32x4*>(p.state + ((int64_t)(slot < 0 ? 0 : slot) * p.nheads + h) * (kP * N) + e);
   f32x4 E = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   if (slot >= 0 && p.has_state && p.has_state[s] != 0) E = *state;
-  float* ws = p.ws_state + ((int64_t)first * p.nheads + h) * (kP * N) + e;
+  float* ws = p.ws_state + ((int64_t)first * p.nheads + h) * (kP * N);
   const float* dec = p.ws_decay + (int64_t)first * p.nheads + h;
   const int64_t step = (int64_t)p.nheads * (kP * N);
-  f32x4 S[kAhead];
-  float d[kAhead];
+  // chunk c's state, empty behind the last: what is out of range reads 0 and is not written
+  auto at = [&](int c) { return make_rsrc(ws + c * step, c < n ? (uint32_t)(kP * N * 4) : 0u); };
+  f32x4 S[AHEAD];
+  float d[AHEAD];
+  auto load = [&](int k, int c) {
+    if (AHEAD == 4 && c >= n) return;  // short prompts: most of the loads ahead are behind the end
+    S[k] = __builtin_bit_cast(f32x4, vload16(at(c), (uint32_t)(e * 4)));
+    d[k] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+        make_rsrc(dec + (int64_t)c * p.nheads, c < n ? 4u : 0u), 0, 0, 0));
+  };
 #pragma unroll
-  for (int k = 0; k < kAhead; ++k)
-    if (k < n) {
-      S[k] = *reinterpret_cast<const f32x4*>(ws + k * step);
-      d[k] = dec[(int64_t)k * p.nheads];
-    }
-  for (int c = 0; c < n; c += kAhead) {
+  for (int k = 0; k < AHEAD; ++k) load(k, k);
+  for (int c = 0; c < n; c += AHEAD) {
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
+    for (int k = 0; k < AHEAD; ++k) {
+      if (k && k % 4 == 0 && c + k >= n) break;
+      const f32x4 own = S[k];
+      const float decay = d[k];
+      load(k, c + k + AHEAD);
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4v, E), at(c + k), (uint32_t)(e * 4), 0, 0);
       if (c + k < n) {
-        const f32x4 own = S[k];
-        const float decay = d[k];
-        if (c + k + kAhead < n) {
-          S[k] = *reinterpret_cast<const f32x4*>(ws + (c + k + kAhead) * step);
-          d[k] = dec[(int64_t)(c + k + kAhead) * p.nheads];
-        }
-        *reinterpret_cast<f32x4*>(ws + (c + k) * step) = E;
 #pragma unroll
         for (int i = 0; i < 4; ++i) E[i] = fmaf(decay, E[i], own[i]);
       }
+    }
   }
   if (slot >= 0) *state = E;
+}
+
+// Sixteen chunks ahead where a few long prompts leave the CUs few workgroups:
+// one prompt of 32769 tokens, 24 heads, state 64 (96 workgroups, 129 chunks)
+// takes 20.9 us with 16 against 46.3 us with 4 (4.9 and 2.2 TB/s), while 24
+// ragged prompts of 16384 tokens, state 128 (4608 workgroups) take 31.8 us
+// against 24.6 us: there the loads behind a prompt's end are what is left.
+bool pass_deep(int64_t workgroups, int64_t chunks, int64_t nseqs) {
+  return workgroups <= 4 * (int64_t)device_cus() && chunks >= 8 * nseqs;
 }
 
 // ---- pass 3: outputs of a chunk ------------------------------------------------------
@@ -202,7 +214,11 @@ __global__ void __launch_bounds__(256) prompt_pass_kernel(SsdPromptParams p) {
 // cs is kept as its sum inside a piece of 64 steps (sCs) and the sums over
 // whole pieces (sTot): pairs inside a piece take a difference of the former, a
 // pair across pieces two factors, exp(cs_i - end of j's piece) and
-// exp(end of j's piece - cs_j), one exp per row and one per column.
+// exp(end of j's piece - cs_j), one exp per row and one per column.  fp16's lo
+// part of x takes E's place once E C^T is done, so that two workgroups share a
+// CU (one prompt of 32769 tokens: 137 -> 122 us).  Several heads one after the
+// other in a workgroup, the next one's loads ahead, leave one workgroup to a CU
+// and take longer (24 ragged prompts: 160 us against 95).
 constexpr int kScanThreads = 512;
 template <int IO, int N>
 __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptParams p) {
@@ -212,8 +228,10 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
   __shared__ __attribute__((aligned(16))) float sCs[kQ];   // Delta A summed from the piece's first step
   __shared__ __attribute__((aligned(16))) float sWp[kQ];   // exp(piece's end - cs_j) Delta_j
   __shared__ float sTot[4];
-  __shared__ __attribute__((aligned(16))) uint16_t sX[kTwo ? 2 : 1][kQ * kP];
-  __shared__ __attribute__((aligned(16))) uint16_t sE[2][kP * kHS];
+  __shared__ __attribute__((aligned(16))) uint16_t sX0[kQ * kP];
+  __shared__ __attribute__((aligned(16))) uint16_t sU[kTwo && 2 * kP * kHS < kQ * kP ? kQ * kP : 2 * kP * kHS];
+  uint16_t* const sX[2] = {sX0, sU};
+  uint16_t* const sE[2] = {sU, sU + kP * kHS};
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
   const int lb = (int)xcd_logical_block();  // the heads of one chunk share its C and CB in an XCD's L2
   const int h = lb % p.nheads, place = lb / p.nheads;
@@ -228,6 +246,8 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
   const int ir[2] = {32 * blk[0] + 16 * half, 32 * blk[1] + 16 * half};  // first row of each block
 
   // ---- prologue: every operand's load, then the sums, then LDS
+  const auto dv = rows_view(static_cast<const char*>(p.dt) + (row0 * p.dt_stride + h) * 2, p.dt_stride * 2, rows);
+  const raw_t<IO> dr = bload<IO>(dv, tid < kQ ? (uint32_t)(tid * p.dt_stride * 2) : kOffNone);
   const auto xv = rows_view(static_cast<const char*>(p.x) + row0 * xrow + h * kP * 2, xrow, rows);
   u32x4v xr[4];
 #pragma unroll
@@ -236,8 +256,6 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
   f32x4 er[N / 32];
 #pragma unroll
   for (int k = 0; k < N / 32; ++k) er[k] = E[tid + kScanThreads * k];
-  const bool in = tid < rows;
-  const float delta = in ? step_size<IO>(p, load_io<IO>(p.dt, (row0 + tid) * p.dt_stride + h), h) : 0.0f;
   const auto cv = rows_view(static_cast<const char*>(p.Cm) + row0 * crow + g * N * 2, crow, rows);
   u32x4v cf[2][N / 32];
 #pragma unroll
@@ -246,6 +264,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
     for (int ks = 0; ks < N / 32; ++ks)
       cf[b][ks] = vload16(cv, (uint32_t)((ir[b] + lane % 16) * crow + (32 * ks + 8 * (lane / 16)) * 2));
   if (tid < kQ) {
+    const float delta = tid < rows ? step_size<IO>(p, bits_f32<IO>(dr), h) : 0.0f;
     float v = delta * p.A[h];
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -265,7 +284,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
       u32x4v hi, lo;
       split8<IO>(xr[k], hi, lo);
       *reinterpret_cast<u32x4v*>(&sX[0][at]) = hi;
-      *reinterpret_cast<u32x4v*>(&sX[kTwo ? 1 : 0][at]) = lo;
+      xr[k] = lo;
     } else {
       *reinterpret_cast<u32x4v*>(&sX[0][at]) = xr[k];
     }
@@ -322,6 +341,14 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
     const float sc = exp2_hw((sCs[ir[b] + lane % 16] + bf) * kLog2e);
 #pragma unroll
     for (int pt = 0; pt < 4; ++pt) acc[b][pt] *= sc;
+  }
+
+  if constexpr (kTwo) {
+    __syncthreads();  // E is used up
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      *reinterpret_cast<u32x4v*>(&sX[1][tm_off<kP>(tid / 8 + 64 * k, 8 * (tid % 8))]) = xr[k];
+    __syncthreads();
   }
 
   // ---- Y_diag += x^T M^T, piece by piece
@@ -455,7 +482,11 @@ hipError_t launch_prompt_n(const SsdPromptParams& p, hipStream_t st) {
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((prompt_pass_kernel<N>), dim3((uint32_t)p.nseqs * heads * (kP * N / 1024)), dim3(256), 0, st, p);
+  const uint32_t pass = (uint32_t)p.nseqs * heads * (kP * N / 1024);
+  if (pass_deep(pass, p.chunks, p.nseqs))
+    hipLaunchKernelGGL((prompt_pass_kernel<N, 16>), dim3(pass), dim3(256), 0, st, p);
+  else
+    hipLaunchKernelGGL((prompt_pass_kernel<N, 4>), dim3(pass), dim3(256), 0, st, p);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((prompt_scan_kernel<IO, N>), dim3(chunks * heads), dim3(kScanThreads), 0, st, p);

@@ -203,6 +203,17 @@ def test_ssd_prompt_long():
     _ssd_check(q, 2, 1, 64, y, state)
 
 
+@pytest.mark.parametrize("io", ["bf16", "f16"])
+def test_ssd_prompt_long_among_short(io):
+    """A long prompt between an empty and two short ones, on average long: chunk numbers on both sides of 16."""
+    ss = _ss()
+    for lens in ([100, 9 * 1024, 0, 300], [0, 16 * 256, 16 * 256 + 1, 15 * 256]):
+        q = _ssd_problem(lens, 2, 1, 32, io, seed=len(lens) + lens[0])
+        y = torch.zeros(sum(lens), 2, 64, dtype=DT[io], device="cuda")
+        state = _ssd_run(ss, q, 2, 1, 32, y)
+        _ssd_check(q, 2, 1, 32, y, state)
+
+
 def test_ssd_prompt_strong_and_no_decay():
     """Steps that forget everything (the weights underflow) and steps that change nothing (Delta = 0)."""
     ss = _ss()
