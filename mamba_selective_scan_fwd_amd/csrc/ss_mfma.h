@@ -90,6 +90,35 @@ __device__ __forceinline__ u32x4v tm_frag(const uint16_t* at, int off_lo, int of
   return __builtin_bit_cast(u32x4v, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
+// ---- sums over the four 16-lane rows of a wave ---------------------------------
+// v_permlane16_swap of a value with itself leaves rows (0, 0, 2, 2) and (1, 1, 3, 3),
+// v_permlane32_swap the halves (0, 0) and (1, 1): sums across rows without LDS.
+__device__ __forceinline__ void swap_rows(float v, float& even, float& odd) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  even = __uint_as_float(r[0]);
+  odd = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ void swap_halves(float v, float& low, float& high) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  low = __uint_as_float(r[0]);
+  high = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float quad_sum(float v) {  // of the lanes l % 16 of all rows
+  float a, b;
+  swap_rows(v, a, b);
+  swap_halves(a + b, a, b);
+  return a + b;
+}
+struct QuadSums {
+  float before, all;  // the rows before this lane's, and all four
+};
+__device__ __forceinline__ QuadSums quad_sums(float v) {
+  float even, odd, low, high;
+  swap_rows(v, even, odd);
+  swap_halves(even + odd, low, high);
+  return {(threadIdx.x & 16 ? even : 0.0f) + (threadIdx.x & 32 ? low : 0.0f), low + high};
+}
+
 // ---- operands as sums of bf16 values -------------------------------------------
 // A computed operand v is split into bf16 parts, each the rounding of what the
 // parts before it leave: |v - p0 - p1| <= 2^-18 |v|, |v - p0 - p1 - p2| <= 2^-27

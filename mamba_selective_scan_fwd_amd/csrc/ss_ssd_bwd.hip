@@ -704,11 +704,14 @@ __device__ __forceinline__ void pair_role(const SsdBwdParams& p, const Chunk& q,
 #pragma unroll
   for (int t = 0; t < 4; ++t) S[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // a head's operands on their way: x of the columns (row tid / 8 + 32 k, channels
-  // 8 (tid % 8) ..), one vector element, g and the factors of this lane's row
-  u32x4v xr[XP][2], gn[GP][2];
+  // a head's operands on their way: x of the columns (row tid / 8 + 32 k,
+  // channels 8 (tid % 8) ..), one vector element, the factors of this lane's row, and
+  // its g, of which two heads' take turns
+  u32x4v xr[XP][2], gf[2][GP][2];
   float vr = 0.0f, fn, ln = 0.0f, mid[2] = {0.0f, 0.0f};
-  auto load_head = [&](int h) {
+  const int uwave = uniform(wave);
+  const float* const vec = uwave == 0 ? p.ws_delta : uwave == 1 ? (DIAG ? p.ws_cs : p.ws_to) : p.ws_cl;
+  auto load_x = [&](int h) {
     const int64_t at = ((int64_t)q.place * p.nheads + h) * kQ;
 #pragma unroll
     for (int i = 0; i < XP; ++i) {
@@ -717,14 +720,7 @@ __device__ __forceinline__ void pair_role(const SsdBwdParams& p, const Chunk& q,
       for (int k = 0; k < 2; ++k)
         xr[i][k] = vload16(xv, (uint32_t)((kJB * jb + tid / 8 + 32 * k) * xrow * 2 + (tid % 8) * 16));
     }
-    const float* vec = wave == 0 ? p.ws_delta : wave == 1 ? (DIAG ? p.ws_cs : p.ws_to) : p.ws_cl;
-    if (wave < (DIAG ? 3 : 2)) vr = vec[at + kJB * jb + lane];
-#pragma unroll
-    for (int i = 0; i < GP; ++i) {
-      const auto gv = plane_view(p.gp[i], q.row0, xrow, h * kP, rows);
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) gn[i][ks] = vload16(gv, (uint32_t)(il * xrow * 2 + (32 * ks + 8 * quad) * 2));
-    }
+    if (uwave < (DIAG ? 3 : 2)) vr = vec[at + kJB * jb + lane];
     fn = (DIAG ? p.ws_cs : p.ws_from)[at + il];
     if constexpr (DIAG) {
       ln = p.ws_cl[at + il];
@@ -734,26 +730,36 @@ __device__ __forceinline__ void pair_role(const SsdBwdParams& p, const Chunk& q,
         if (jb + 1 + k < ib) mid[k] = p.ws_cs[at + kJB * (jb + 1 + k) + kJB - 1];
     }
   };
-  load_head(g * hpg);
-  int turn = 0;
+  auto load_g = [&](int u, int h) {
+#pragma unroll
+    for (int i = 0; i < GP; ++i) {
+      const auto gv = plane_view(p.gp[i], q.row0, xrow, h * kP, rows);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) gf[u][i][ks] = vload16(gv, (uint32_t)(il * xrow * 2 + (32 * ks + 8 * quad) * 2));
+    }
+  };
+  const int hend = (g + 1) * hpg;
+  load_x(g * hpg);
+  load_g(0, g * hpg);
   for (int h0 = 0; h0 < hpg; h0 += kBatch) {
     const int nb = hpg - h0 < kBatch ? hpg - h0 : kBatch;
-    for (int hb = 0; hb < nb; ++hb, turn ^= 1) {
-      const int h = g * hpg + h0 + hb;
+    for (int hb0 = 0; hb0 < nb; hb0 += 2)
+#pragma unroll
+    for (int turn = 0; turn < 2; ++turn) {
+      const int hb = hb0 + turn, h = g * hpg + h0 + hb;
+      if (hb >= nb) break;
       const int64_t ph = (int64_t)q.place * p.nheads + h;
 #pragma unroll
       for (int i = 0; i < XP; ++i)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           *reinterpret_cast<u32x4v*>(&lds.x[turn][i][row64_off(tid / 8 + 32 * k, 8 * (tid % 8))]) = xr[i][k];
-      if (wave < (DIAG ? 3 : 2)) lds.vec[turn][wave][lane] = vr;
-      u32x4v gf[GP][2];
-#pragma unroll
-      for (int i = 0; i < GP; ++i)
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) gf[i][ks] = gn[i][ks];
+      if (uwave < (DIAG ? 3 : 2)) lds.vec[turn][wave][lane] = vr;
       const float f = DIAG ? fn : fn * exp2_hw((mid[0] + mid[1]) * kLog2e), l = ln;
-      if (h + 1 < (g + 1) * hpg) load_head(h + 1);
+      if (h + 1 < hend) {
+        load_x(h + 1);
+        load_g(1 - turn, h + 1);
+      }
       __syncthreads();
       f32x4 a[4];
 #pragma unroll
@@ -770,7 +776,7 @@ __device__ __forceinline__ void pair_role(const SsdBwdParams& p, const Chunk& q,
           for (int i = GP - 1; i >= 0; --i)
             if (i + j <= 2)
 #pragma unroll
-              for (int t = 0; t < 4; ++t) a[t] = BF::run(xf[t], bfv(gf[i][ks]), a[t]);
+              for (int t = 0; t < 4; ++t) a[t] = BF::run(xf[t], bfv(gf[turn][i][ks]), a[t]);
         }
       float xd = 0.0f;
 #pragma unroll
@@ -813,15 +819,11 @@ __device__ __forceinline__ void pair_role(const SsdBwdParams& p, const Chunk& q,
         if constexpr (DIAG) {
           // the row's sums up to each j: inside a lane's 4 columns, over the quads
           // of a tile (lanes 16 apart), over the tiles
-          float s = v[3];
-          const float u1 = __shfl_up(s, 16, 64);
-          if (quad >= 1) s += u1;
-          const float u2 = __shfl_up(s, 32, 64);
-          if (quad >= 2) s += u2;
-          const float before = base + (s - v[3]);
+          const QuadSums s = quad_sums(v[3]);
+          const float before = base + s.before;
 #pragma unroll
           for (int r = 0; r < 4; ++r) a[t][r] = il > j0 + 16 * t + r ? v[r] + before : 0.0f;
-          base += __shfl(s, 48 + l16, 64);
+          base += s.all;
         }
       }
       lds.part[hb][0][wave][16 * (l16 / 4) + jl + l16 % 4] = transpose_sum(W);
@@ -829,8 +831,7 @@ __device__ __forceinline__ void pair_role(const SsdBwdParams& p, const Chunk& q,
         lds.part[hb][1][wave][16 * (l16 / 4) + jl + l16 % 4] = transpose_sum(a);
         if (quad == (l16 >> 2)) p.ws_xd[ph * kQ + il] = xd;
       } else {
-        row += __shfl_xor(row, 16, 64);
-        row += __shfl_xor(row, 32, 64);
+        row = quad_sum(row);
         if (quad == 0) p.ws_prow[(ph * kPairs + pr) * kJB + 16 * wave + l16] = row;
       }
     }
@@ -895,8 +896,8 @@ __global__ void __launch_bounds__(256, MODE == 0 ? 3 : 2) bwd_pair_kernel(SsdBwd
 }
 
 // ---- dC and dB -----------------------------------------------------------------------------
-// Workgroup = (chunk, group, dC or dB, half of the states), 512 threads, wave w
-// the rows f = 32 w .. 32 w + 31:
+// Workgroup = (chunk, group, dC or dB, half of the rows, half of the states), 256
+// threads, wave w the rows f = 32 w .. 32 w + 31 of the half:
 //   dC: f = i: F = g, K = E, v = C, u = B, w_f = exp(cs_f), d = 1
 //   dB: f = j: F = x, K = R, v = B, u = C, w_f = exp(cs_last - cs_f), d = Delta
 //   out_f[n] = sum_h d_f w_f sum_p K[p][n] F_f[p] + sum_s S_fs u_s[n]
@@ -905,7 +906,7 @@ __global__ void __launch_bounds__(256, MODE == 0 ? 3 : 2) bwd_pair_kernel(SsdBwd
 // [p][16 n] tiles read back transposed): the next head's K and F are on their
 // way while this head is multiplied, one barrier per head.  S comes as operand
 // fragments from bwd_pair, with u's pieces staged in LDS.
-constexpr int kOutThreads = 512;
+constexpr int kOutThreads = 256;
 // element (row, c) of a [rows][16] tile: blocks of 4 rows swapped so that the
 // transposing reads of rows 8 apart hit different banks
 __device__ __forceinline__ int t16_off(int row, int c) { return (row ^ (((row >> 3) & 1) << 2)) * 16 + c; }
@@ -918,12 +919,13 @@ __device__ __forceinline__ void out_role(const SsdBwdParams& p, int lb, uint16_t
   constexpr int kItems = kP * NH / 4, kPer = (kItems + kOutThreads - 1) / kOutThreads;
   constexpr int kBuf = 3 * kP * NH;
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, quad = lane / 16, l16 = lane % 16;
-  const int half = lb & 1, g = (lb >> 1) % p.ngroups;
-  const Chunk q = chunk_of(p, (lb >> 1) / p.ngroups);
-  const int rows = q.rows, n0 = NH * half;
+  const int half = lb & 1, upper = (lb >> 1) & 1, g = (lb >> 2) % p.ngroups;
+  const Chunk q = chunk_of(p, (lb >> 2) / p.ngroups);
+  const int rows = q.rows, n0 = NH * half, f0 = kQ / 2 * upper;
+  if (f0 >= rows) return;
   const int hpg = p.nheads / p.ngroups;
   const int64_t xrow = (int64_t)p.nheads * kP, vrow = (int64_t)p.ngroups * N;
-  const int fr[2] = {32 * wave + l16, 32 * wave + 16 + l16};  // this lane's rows
+  const int fr[2] = {f0 + 32 * wave + l16, f0 + 32 * wave + 16 + l16};  // this lane's rows
   const auto vv = plane_view(static_cast<const uint16_t*>(DB ? p.Bm : p.Cm), q.row0, vrow, g * N, rows);
   uint2 vn[2][NT];
 #pragma unroll
@@ -937,8 +939,8 @@ __device__ __forceinline__ void out_role(const SsdBwdParams& p, int lb, uint16_t
     for (int t = 0; t < NT; ++t) tot[b][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
   f32x4 kr[kPer];
-  u32x4v F[FP][2][2];
-  float wf[2], df[2];
+  u32x4v F[2][FP][2][2];  // two heads' in turn
+  float wf[2][2], df[2][2];
   auto load_k = [&](int h) {
     const float* K = (DB ? p.ws_R : p.ws_E) + ((int64_t)q.place * p.nheads + h) * (kP * N) + n0;
 #pragma unroll
@@ -948,7 +950,7 @@ __device__ __forceinline__ void out_role(const SsdBwdParams& p, int lb, uint16_t
         kr[k] = *reinterpret_cast<const f32x4*>(K + (item / (NH / 4)) * N + 4 * (item % (NH / 4)));
     }
   };
-  auto load_f = [&](int h) {
+  auto load_f = [&](int u, int h) {
 #pragma unroll
     for (int i = 0; i < FP; ++i) {
       const auto fv = plane_view(DB ? p.xp[i % 2] : p.gp[i], q.row0, xrow, h * kP, rows);
@@ -956,13 +958,13 @@ __device__ __forceinline__ void out_role(const SsdBwdParams& p, int lb, uint16_t
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
-          F[i][b][ks] = vload16(fv, (uint32_t)(fr[b] * xrow * 2 + (32 * ks + 8 * quad) * 2));
+          F[u][i][b][ks] = vload16(fv, (uint32_t)(fr[b] * xrow * 2 + (32 * ks + 8 * quad) * 2));
     }
     const int64_t at = ((int64_t)q.place * p.nheads + h) * kQ;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      wf[b] = (DB ? p.ws_wb : p.ws_wc)[at + fr[b]];
-      df[b] = DB ? p.ws_delta[at + fr[b]] : 1.0f;
+      wf[u][b] = (DB ? p.ws_wb : p.ws_wc)[at + fr[b]];
+      df[u][b] = DB ? p.ws_delta[at + fr[b]] : 1.0f;
     }
   };
   auto stage_k = [&](uint16_t* buf) {
@@ -981,12 +983,16 @@ __device__ __forceinline__ void out_role(const SsdBwdParams& p, int lb, uint16_t
     }
   };
   load_k(g * hpg);
-  load_f(g * hpg);
+  load_f(0, g * hpg);
   stage_k(lds);
   if (hpg > 1) load_k(g * hpg + 1);
-  for (int hg = 0; hg < hpg; ++hg) {
-    const int h = g * hpg + hg;
-    const uint16_t* buf = lds + (hg & 1) * kBuf;
+  for (int hg0 = 0; hg0 < hpg; hg0 += 2)
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int hg = hg0 + u, h = g * hpg + hg;
+    if (hg >= hpg) break;
+    const uint16_t* buf = lds + u * kBuf;
+    if (hg + 1 < hpg) load_f(1 - u, h + 1);
     __syncthreads();
     f32x4 a[2][NT];
 #pragma unroll
@@ -1008,13 +1014,11 @@ __device__ __forceinline__ void out_role(const SsdBwdParams& p, int lb, uint16_t
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-              for (int b = 0; b < 2; ++b) a[b][t] = BF::run(kp[t], bfv(F[i][b][ks]), a[b][t]);
+              for (int b = 0; b < 2; ++b) a[b][t] = BF::run(kp[t], bfv(F[u][i][b][ks]), a[b][t]);
       }
     }
-    const float w[2] = {wf[0], wf[1]}, d[2] = {df[0], df[1]};
     if (hg + 1 < hpg) {  // the next head's K into the other buffer, the one after on its way
-      load_f(h + 1);
-      stage_k(lds + ((hg + 1) & 1) * kBuf);
+      stage_k(lds + (1 - u) * kBuf);
       if (hg + 2 < hpg) load_k(h + 2);
     }
     const int64_t to = ((int64_t)half * p.batch * p.nchunks * p.nheads + (int64_t)q.place * p.nheads + h) * kQ;
@@ -1027,12 +1031,10 @@ __device__ __forceinline__ void out_role(const SsdBwdParams& p, int lb, uint16_t
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           vt = fmaf(v[r], a[b][t][r], vt);
-          tot[b][t][r] = fmaf(DB ? w[b] * d[b] : w[b], a[b][t][r], tot[b][t][r]);
+          tot[b][t][r] = fmaf(DB ? wf[u][b] * df[u][b] : wf[u][b], a[b][t][r], tot[b][t][r]);
         }
       }
-      vt *= w[b];
-      vt += __shfl_xor(vt, 16, 64);
-      vt += __shfl_xor(vt, 32, 64);
+      vt = quad_sum(vt * wf[u][b]);
       if (quad == 0) (DB ? p.ws_r : p.ws_e)[to + fr[b]] = vt;
     }
   }
@@ -1042,28 +1044,49 @@ __device__ __forceinline__ void out_role(const SsdBwdParams& p, int lb, uint16_t
 #pragma unroll
   for (int i = 0; i < UP; ++i) up[i] = plane_view(DB ? p.cp[i] : p.bp[i], q.row0, vrow, g * N + n0, rows);
   const uint32_t* Sw = p.ws_S + ((int64_t)q.place * p.ngroups + g) * kPairs * (2 * kJB * kJB);
-  const int fb = wave / 2;  // the piece that holds this wave's rows
-  const int lastp = (rows - 1) / kJB;
-  for (int sb = 0; sb <= lastp; ++sb) {
-    __syncthreads();
-    for (int item = tid; item < kJB * NH / 8; item += kOutThreads) {
-      const int s = item / (NH / 8), n = 8 * (item % (NH / 8));
-      const int at = (n / 16) * (kJB * 16) + t16_off(s, n % 16);
+  const int fb = 2 * upper + wave / 2;  // the piece that holds this wave's rows
+  const int lastp = (rows - 1) / kJB, fend = 2 * upper + 1 < lastp ? 2 * upper + 1 : lastp;
+  const int s0 = DB ? 2 * upper : 0, s1 = DB ? lastp : fend;  // the pieces that any of the rows meets
+  constexpr int kUItems = kJB * NH / 8, kU = (kUItems + kOutThreads - 1) / kOutThreads;
+  u32x4v ur[UP][kU];  // the next piece of u on its way
+  auto load_u = [&](int sb) {
 #pragma unroll
-      for (int i = 0; i < UP; ++i)
-        *reinterpret_cast<u32x4v*>(&lds[i * kJB * NH + at]) = vload16(up[i], (uint32_t)((kJB * sb + s) * vrow * 2 + n * 2));
+    for (int k = 0; k < kU; ++k) {
+      const int item = tid + kOutThreads * k;
+      const uint32_t at = (uint32_t)((kJB * sb + item / (NH / 8)) * vrow * 2 + 16 * (item % (NH / 8)));
+#pragma unroll
+      for (int i = 0; i < UP; ++i) ur[i][k] = vload16(up[i], item < kUItems ? at : kOffNone);
+    }
+  };
+  load_u(s0);
+  for (int sb = s0; sb <= s1; ++sb) {
+    const bool mine = fb <= lastp && (DB ? sb >= fb : sb <= fb);
+    const uint32_t* Sp = Sw + (mine ? pair_of(DB ? sb : fb, DB ? fb : sb) : 0) * (2 * kJB * kJB) + (DB ? kJB * kJB : 0);
+    u32x4v sp[2][2][2];  // [k-step][part][row tile]
+    if (mine) {
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            sp[ks][k][b] =
+                *reinterpret_cast<const u32x4v*>(Sp + (((k * 4 + 2 * (wave % 2) + b) * 2 + ks) * 64 + lane) * 4);
     }
     __syncthreads();
-    if ((DB ? sb < fb : sb > fb) || fb > lastp) continue;
-    const uint32_t* Sp = Sw + pair_of(DB ? sb : fb, DB ? fb : sb) * (2 * kJB * kJB) + (DB ? kJB * kJB : 0);
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      const int item = tid + kOutThreads * k, s = item / (NH / 8), n = 8 * (item % (NH / 8));
+      const int at = (n / 16) * (kJB * 16) + t16_off(s, n % 16);
+      if (kUItems % kOutThreads == 0 || item < kUItems)
+#pragma unroll
+        for (int i = 0; i < UP; ++i) *reinterpret_cast<u32x4v*>(&lds[i * kJB * NH + at]) = ur[i][k];
+    }
+    __syncthreads();
+    if (sb < s1) load_u(sb + 1);
+    if (!mine) continue;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      u32x4v sp[2][2];  // [part][row tile]
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-          sp[k][b] = *reinterpret_cast<const u32x4v*>(Sp + (((k * 4 + 2 * (wave % 2) + b) * 2 + ks) * 64 + lane) * 4);
       const int r0 = 32 * ks + 4 * quad + l16 / 4, c = 4 * (l16 % 4);
       const int o0 = t16_off(r0, c), o1 = t16_off(r0 + 16, c);
 #pragma unroll
@@ -1071,10 +1094,10 @@ __device__ __forceinline__ void out_role(const SsdBwdParams& p, int lb, uint16_t
         const bf16x8 uh = bfv(tm_frag(lds + t * (kJB * 16), o0, o1));
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          tot[b][t] = BF::run(uh, bfv(sp[1][b]), tot[b][t]);
+          tot[b][t] = BF::run(uh, bfv(sp[ks][1][b]), tot[b][t]);
           if constexpr (UP > 1)
-            tot[b][t] = BF::run(bfv(tm_frag(lds + kJB * NH + t * (kJB * 16), o0, o1)), bfv(sp[0][b]), tot[b][t]);
-          tot[b][t] = BF::run(uh, bfv(sp[0][b]), tot[b][t]);
+            tot[b][t] = BF::run(bfv(tm_frag(lds + kJB * NH + t * (kJB * 16), o0, o1)), bfv(sp[ks][0][b]), tot[b][t]);
+          tot[b][t] = BF::run(uh, bfv(sp[ks][0][b]), tot[b][t]);
         }
       }
     }
@@ -1093,7 +1116,7 @@ template <int MODE, int N>
 __global__ void __launch_bounds__(kOutThreads, 2) bwd_out_kernel(SsdBwdParams p) {
   constexpr int kHeads = 2 * 3 * kP * (N / 2), kSteps = data_parts<MODE>() * kJB * (N / 2);
   __shared__ __attribute__((aligned(16))) uint16_t lds[kHeads > kSteps ? kHeads : kSteps];
-  const int lb = (int)xcd_logical_block(), n = (int)p.batch * p.nchunks * p.ngroups * 2;
+  const int lb = (int)xcd_logical_block(), n = (int)p.batch * p.nchunks * p.ngroups * 4;
   if (lb < n) out_role<MODE, N, false>(p, lb, lds);
   else out_role<MODE, N, true>(p, lb - n, lds);
 }
@@ -1232,7 +1255,7 @@ hipError_t launch_n(const SsdBwdParams& p, hipStream_t st) {
   SS_LAUNCH((bwd_scan_kernel<MODE, N, true>), heads, kScanThreads);
   if constexpr (gate) SS_LAUNCH((bwd_scan_kernel<MODE, N, false>), heads, kScanThreads);
   SS_LAUNCH((bwd_pair_kernel<MODE, N>), places * p.ngroups * kPairs, 256);
-  SS_LAUNCH((bwd_out_kernel<MODE, N>), places * p.ngroups * 4, kOutThreads);
+  SS_LAUNCH((bwd_out_kernel<MODE, N>), places * p.ngroups * 8, kOutThreads);
   SS_LAUNCH((bwd_delta_kernel<io_of<MODE>()>), heads, 256);
   SS_LAUNCH(bwd_sum_kernel, p.nheads, 256);
   return hipSuccess;
