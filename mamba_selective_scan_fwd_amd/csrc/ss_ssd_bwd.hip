@@ -884,12 +884,24 @@ __device__ __forceinline__ void pair_role(const SsdBwdParams& p, const Chunk& q,
 template <int MODE, int N>
 __global__ void __launch_bounds__(256, MODE == 0 ? 3 : 2) bwd_pair_kernel(SsdBwdParams p) {
   __shared__ PairLds<MODE> lds;
-  const int lb = (int)xcd_logical_block();  // the pairs of one chunk's group share an XCD's L2
-  const int pr = lb % kPairs, g = (lb / kPairs) % p.ngroups;
-  const Chunk q = chunk_of(p, lb / (kPairs * p.ngroups));
-  int ib = 0;
-  while ((ib + 1) * (ib + 2) / 2 <= pr) ++ib;
-  const int jb = pr - ib * (ib + 1) / 2;
+  // the pairs of one chunk's group share an XCD's L2, and of an XCD's pairs the
+  // ib = jb ones, which take longest, come first
+  const int units = (int)p.batch * p.nchunks * p.ngroups, xcd = (int)(blockIdx.x % 8u);
+  const int u0 = (int)((int64_t)units * xcd / 8), n = (int)((int64_t)units * (xcd + 1) / 8) - u0;
+  int l = (int)(blockIdx.x / 8u), ib, jb, unit;
+  if (l < 4 * n) {
+    unit = u0 + l / 4;
+    ib = jb = l % 4;
+  } else {
+    l -= 4 * n;
+    if (l >= 6 * n) return;
+    unit = u0 + l / 6;
+    l %= 6;
+    ib = l < 1 ? 1 : l < 3 ? 2 : 3;
+    jb = l - ib * (ib - 1) / 2;
+  }
+  const int g = unit % p.ngroups;
+  const Chunk q = chunk_of(p, unit / p.ngroups);
   if (kJB * ib >= q.rows) return;
   if (ib == jb) pair_role<MODE, N, true>(p, q, g, ib, jb, lds);
   else pair_role<MODE, N, false>(p, q, g, ib, jb, lds);
@@ -1254,7 +1266,7 @@ hipError_t launch_n(const SsdBwdParams& p, hipStream_t st) {
   SS_LAUNCH((bwd_pass_kernel<N>), p.batch * p.nheads * (kP * N / 1024), 256);
   SS_LAUNCH((bwd_scan_kernel<MODE, N, true>), heads, kScanThreads);
   if constexpr (gate) SS_LAUNCH((bwd_scan_kernel<MODE, N, false>), heads, kScanThreads);
-  SS_LAUNCH((bwd_pair_kernel<MODE, N>), places * p.ngroups * kPairs, 256);
+  SS_LAUNCH((bwd_pair_kernel<MODE, N>), (places * p.ngroups + 7) / 8 * (8 * kPairs), 256);
   SS_LAUNCH((bwd_out_kernel<MODE, N>), places * p.ngroups * 8, kOutThreads);
   SS_LAUNCH((bwd_delta_kernel<io_of<MODE>()>), heads, 256);
   SS_LAUNCH(bwd_sum_kernel, p.nheads, 256);
