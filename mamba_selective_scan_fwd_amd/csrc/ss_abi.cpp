@@ -601,36 +601,35 @@ struct SsdBwdLayout {
   }
   size_t E, R, decay, dot, cb, bc, delta, cs, cl, from, to, wc, wb, xd, e, r, seg, prow, pcol, S, part;
   size_t x[2], g[3], b[2], c[2];
+  SsdBwdLayout(const ss_ssd_problem* p, bool gated);
 };
-SsdBwdLayout ssd_bwd_layout(const ss_ssd_problem* p, bool gated) {
+SsdBwdLayout::SsdBwdLayout(const ss_ssd_problem* p, bool gated) {
   const bool f16 = p->io_dtype == SS_F16;
   const size_t places = (size_t)(p->batch * ((p->seqlen + kSsdChunk - 1) / kSsdChunk));
   const size_t ph = places * (size_t)p->nheads, st = ph * (size_t)(64 * p->dstate) * 4, q = ph * 256 * 4;
-  const size_t cb = places * (size_t)p->ngroups * (256 * 256) * 4;
+  const size_t square = places * (size_t)p->ngroups * (256 * 256) * 4;
   const size_t rows = (size_t)(p->batch * p->seqlen);
   const size_t xb = rows * (size_t)p->nheads * 64 * 2, vb = rows * (size_t)(p->ngroups * p->dstate) * 2;
-  SsdBwdLayout l;
-  l.E = l.take(st); l.R = l.take(st); l.decay = l.take(ph * 4); l.dot = l.take(ph * (size_t)p->dstate);
-  l.bc = l.take(cb); l.cb = l.take(gated ? cb : 0);
-  l.delta = l.take(q); l.cs = l.take(q); l.cl = l.take(q); l.from = l.take(q); l.to = l.take(q);
-  l.wc = l.take(q); l.wb = l.take(q); l.xd = l.take(q); l.e = l.take(2 * q); l.r = l.take(2 * q);
-  l.seg = l.take(places * 256 * 4);
-  l.prow = l.take(ph * 10 * 64 * 4); l.pcol = l.take(ph * 10 * 64 * 4);
-  l.S = l.take(places * (size_t)p->ngroups * 10 * (64 * 64 * 2) * 4);
-  l.part = l.take(ph * 3 * 4);
-  for (int i = 0; i < 3; ++i) l.g[i] = l.take(gated || (f16 && i < 2) ? xb : 0);
+  E = take(st); R = take(st); decay = take(ph * 4); dot = take(ph * (size_t)p->dstate);
+  bc = take(square); cb = take(gated ? square : 0);
+  delta = take(q); cs = take(q); cl = take(q); from = take(q); to = take(q);
+  wc = take(q); wb = take(q); xd = take(q); e = take(2 * q); r = take(2 * q);
+  seg = take(places * 256 * 4);
+  prow = take(ph * 10 * 64 * 4); pcol = take(ph * 10 * 64 * 4);
+  S = take(places * (size_t)p->ngroups * 10 * (64 * 64 * 2) * 4);
+  part = take(ph * 3 * 4);
+  for (int i = 0; i < 3; ++i) g[i] = take(gated || (f16 && i < 2) ? xb : 0);
   for (int i = 0; i < 2; ++i) {
-    l.x[i] = l.take(f16 ? xb : 0);
-    l.b[i] = l.take(f16 ? vb : 0);
-    l.c[i] = l.take(f16 ? vb : 0);
+    x[i] = take(f16 ? xb : 0);
+    b[i] = take(f16 ? vb : 0);
+    c[i] = take(f16 ? vb : 0);
   }
-  return l;
 }
 }  // namespace
 
 size_t ss_ssd_bwd_workspace_size(const ss_ssd_problem* p, int32_t gated) {
   if (check_ssd_bwd(p) != SS_OK) return 0;
-  return ssd_bwd_layout(p, gated != 0).total;
+  return SsdBwdLayout(p, gated != 0).total;
 }
 
 ss_status ss_ssd_bwd(const ss_ssd_problem* p, const void* x, const void* dt, const float* A, const void* Bm,
@@ -648,7 +647,7 @@ ss_status ss_ssd_bwd(const ss_ssd_problem* p, const void* x, const void* dt, con
                         dD, dz, ddt_bias, dh0, workspace};
   for (const void* q : ptrs)
     if (q && !aligned(q)) return SS_ERR_MISALIGNED;
-  const SsdBwdLayout l = ssd_bwd_layout(p, z != nullptr);
+  const SsdBwdLayout l(p, z != nullptr);
   if (!workspace || workspace_bytes < l.total) return SS_ERR_UNSUPPORTED;
   {
     const size_t rows = (size_t)(p->batch * p->seqlen);

@@ -12,6 +12,7 @@ import functools
 import os
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libss.so")
@@ -630,8 +631,8 @@ def _scratch(workspace, nbytes, dev):
             return None, None, 0
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=_DEVICES[dev])
         return workspace, workspace.data_ptr(), nbytes
-    if workspace.get_device() != dev:
-        raise ValueError("the workspace must be on cuda:%d" % dev)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("the workspace must be a contiguous tensor on cuda:%d" % dev)
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -827,7 +828,9 @@ def ssd_step(xbc, dt, A, conv_w, conv_state, state, ngroups=1, conv_bias=None, D
 class SsdStepCall:
     """ssd_step validated once and replayed with one C call per launch (the serving pattern of StepCall:
     preallocated token, slot and output buffers refilled in place; the tensors must stay alive and
-    unmoved).  Takes its operands as they are: rows whole, weights contiguous."""
+    unmoved).  Takes its operands as they are: rows whole, weights contiguous.  Its launches go to the
+    stream it was made with or for, so one that a graph captures is made with the capturing stream, and
+    are ordered by it: it owns its workspace, two of them may run at once on slots of their own."""
 
     def __init__(self, xbc, dt, A, conv_w, conv_state, state, y, ngroups=1, conv_bias=None, D=None, z=None,
                  dt_bias=None, dt_softplus=True, slots=None, stream=None):
@@ -857,10 +860,14 @@ class SsdStepCall:
         st = stream if stream is not None else torch.cuda.current_stream(xbc.device)
         self.args = (self.pr, xa, da, *at[:4], za, *at[4:6], at[6] if W > 1 else None, *at[7:], wa, wsz,
                      ctypes.c_void_p(st.cuda_stream))
-        self.fn = lib.ss_ssd_step
+        self.fn, self.dev = lib.ss_ssd_step, dev
 
     def __call__(self):
-        status = self.fn(*self.args)
+        if torch.cuda.current_device() == self.dev:
+            status = self.fn(*self.args)
+        else:
+            with torch.cuda.device(self.dev):
+                status = self.fn(*self.args)
         if status != 0:
             _check(status)
 
@@ -956,6 +963,7 @@ class Conv1dFn(torch.autograd.Function):
         return conv1d(x, w, bias, silu=silu, seq_idx=seq_idx, conv_init=conv_init, return_final=return_final)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout, dfinal=None):
         x, w, bias, seq_idx, conv_init = ctx.saved_tensors
         g = conv1d_bwd(x, w, dout.contiguous(), bias=bias, silu=ctx.silu, seq_idx=seq_idx, conv_init=conv_init,
@@ -965,7 +973,9 @@ class Conv1dFn(torch.autograd.Function):
 
 
 def conv1d_fn(x, w, bias=None, silu=True, seq_idx=None, conv_init=None, return_final=False):
-    """conv1d, differentiable: out, or (out, conv_final) with return_final."""
+    """conv1d, differentiable once: out, or (out, conv_final) with return_final.  To capture it in a
+    graph, capture the forward with its backward, and drop the outputs of eager passes over the same
+    leaves before: while one lives, the leaves' gradients are accumulated on that pass's stream."""
     return Conv1dFn.apply(x, w, bias, silu, seq_idx, conv_init, return_final)
 
 
@@ -982,6 +992,7 @@ class SsdScanFn(torch.autograd.Function):
                        return_final_state=return_final_state, seq_idx=seq_idx)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dfinal=None):
         x, dt, A, Bm, Cm, D, z, dt_bias, seq_idx, h0 = ctx.saved_tensors
         g = ssd_bwd(x, dt, A, Bm, Cm, dy.contiguous(), D=D, z=z, dt_bias=dt_bias, dt_softplus=ctx.dt_softplus,
@@ -992,5 +1003,6 @@ class SsdScanFn(torch.autograd.Function):
 
 def ssd_scan_fn(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, dt_softplus=True, seq_idx=None, h0=None,
                 return_final_state=False):
-    """ssd_fwd, differentiable: y, or (y, final_state) with return_final_state."""
+    """ssd_fwd, differentiable once: y, or (y, final_state) with return_final_state.  In a captured
+    graph as conv1d_fn."""
     return SsdScanFn.apply(x, dt, A, Bm, Cm, D, z, dt_bias, dt_softplus, seq_idx, h0, return_final_state)

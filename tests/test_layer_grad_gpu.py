@@ -329,3 +329,63 @@ def test_gradients_repeat_on_streams_and_in_graphs():
             assert same(caught[0], want[0])
         run[k % 3]()
         torch.cuda.synchronize()
+
+
+def test_training_step_captured_and_replayed():
+    """Forward and backward of both operators through autograd inside one graph: every replay leaves the gradients
+    that an eager pass over other leaves of the same values gives, new inputs among them."""
+    ss = _ss()
+    Bsz, L, H, N = 2, 270, 2, 32
+    ch = H * 64 + 2 * N
+    q = {k: v.cuda() for k, v in _ssd(Bsz, L, H, 1, N, "bf16", seed=31).items()}
+    c = {k: v.cuda() for k, v in _conv(Bsz, ch, L, 4, "bf16", seed=32).items()}
+
+    def leaves():
+        return [c[k].clone().requires_grad_() for k in ("x", "w", "bias")] + [q["A"].clone().requires_grad_()]
+
+    def step(x, w, b, A):
+        tm = ss.conv1d_fn(x, w, b).transpose(1, 2)
+        sx, sB, sC = (v.reshape(Bsz, L, -1, n) for v, n in zip(tm.split([H * 64, N, N], 2), (64, N, N)))
+        y = ss.ssd_scan_fn(sx, q["dt"], A, sB, sC, D=q["D"], dt_bias=q["dt_bias"])
+        y.backward(q["dy"])
+
+    def eager(x):
+        v = leaves()
+        with torch.no_grad():
+            v[0].copy_(x)
+        step(*v)
+        return [t.grad for t in v]
+
+    inputs = [c["x"].clone(), c["x"].flip(2).contiguous(), c["x"].clone()]
+    want = [eager(x) for x in inputs]
+    torch.cuda.synchronize()
+    mine = leaves()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(*mine)
+    for x, w in zip(inputs, want):
+        with torch.no_grad():
+            mine[0].copy_(x)
+        graph.replay()
+        eager(x)
+        torch.cuda.synchronize()
+        assert all(torch.equal(t.grad, v) for t, v in zip(mine, w))
+
+
+def test_second_derivatives_and_strided_workspaces_are_refused():
+    ss = _ss()
+    c = {k: v.cuda() for k, v in _conv(1, 8, 40, 4, "f32", seed=33).items()}
+    x = c["x"].requires_grad_()
+    (dx,) = torch.autograd.grad(ss.conv1d_fn(x, c["w"], c["bias"]).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        dx.sum().backward()
+    q = {k: v.cuda() for k, v in _ssd(1, 40, 2, 1, 32, "bf16", seed=34).items()}
+    x = q["x"].requires_grad_()
+    (dx,) = torch.autograd.grad(ss.ssd_scan_fn(x, q["dt"], q["A"], q["Bm"], q["Cm"]).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        dx.sum().backward()
+    room = torch.empty(1 << 25, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError):
+        ss.ssd_bwd(q["x"].detach(), q["dt"], q["A"], q["Bm"], q["Cm"], q["dy"], workspace=room[::2])
+    with pytest.raises(ValueError):
+        ss.ssd_bwd(q["x"].detach(), q["dt"], q["A"], q["Bm"], q["Cm"], q["dy"], workspace=room.cpu())
