@@ -586,8 +586,10 @@ ss_status check_ssd_bwd(const ss_ssd_problem* p) {
   const ss_status s = check_ssd(p);
   if (s != SS_OK) return s;
   const double places = (double)p->batch * (double)((p->seqlen + kSsdChunk - 1) / kSsdChunk);
-  if (places * (2.0 * (double)p->nheads + 10.0 * (double)p->ngroups) > (double)kMaxGrid) return SS_ERR_BAD_SHAPE;
-  if ((double)p->batch * (double)p->nheads * (p->dstate / 16) > (double)kMaxGrid) return SS_ERR_BAD_SHAPE;
+  // the pass and the pairs share a launch, each rounded up to the XCDs
+  if (places * (2.0 * (double)p->nheads + 10.0 * (double)p->ngroups) +
+          (double)p->batch * (double)p->nheads * (p->dstate / 16) + 88.0 > (double)kMaxGrid)
+    return SS_ERR_BAD_SHAPE;
   return SS_OK;
 }
 // the workspace of the SSD's backward: one piece after the other, each on a

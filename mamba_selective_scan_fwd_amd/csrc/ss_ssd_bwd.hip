@@ -295,11 +295,11 @@ __global__ void __launch_bounds__(kStateThreads, MODE == 0 ? 4 : 2) bwd_state_ke
 // Workgroup = (batch row, head, 1024 elements), a thread 4 elements.  <R, E> of a
 // chunk: each wave leaves the sum of its 256 elements.
 template <int N>
-__global__ void __launch_bounds__(256) bwd_pass_kernel(SsdBwdParams p) {
+__device__ __forceinline__ void pass_role(const SsdBwdParams& p, uint32_t block) {
   constexpr int kParts = kP * N / 1024, kAhead = 4;
-  const int part = (int)(blockIdx.x % kParts);
-  const int h = (int)((blockIdx.x / kParts) % (uint32_t)p.nheads);
-  const int64_t b = blockIdx.x / kParts / (uint32_t)p.nheads;
+  const int part = (int)(block % kParts);
+  const int h = (int)((block / kParts) % (uint32_t)p.nheads);
+  const int64_t b = block / kParts / (uint32_t)p.nheads;
   const int e = part * 1024 + 4 * (int)threadIdx.x, n = p.nchunks;
   const int64_t first = b * n * p.nheads + h, step = (int64_t)p.nheads * (kP * N);
   const float* dec = p.ws_decay + first;
@@ -881,14 +881,34 @@ __device__ __forceinline__ void pair_role(const SsdBwdParams& p, const Chunk& q,
   }
 }
 
+// The pass between the chunks' states and the pairs need nothing of each other;
+// the former waits for memory, the latter computes, so they share a launch, the
+// pairs' workgroups first, which live longer (bench layer: 75 us; 94 us as two
+// launches, 98 us with one's eight workgroups, one on each XCD, after the
+// other's eight, 103 us with the pass first).
+inline uint32_t pass_octets(const SsdBwdParams& p) {
+  return (uint32_t)((p.batch * p.nheads * (kP * p.dstate / 1024) + 7) / 8);
+}
+inline uint32_t pair_octets(const SsdBwdParams& p) {
+  return (uint32_t)((p.batch * p.nchunks * p.ngroups + 7) / 8 * kPairs);
+}
 template <int MODE, int N>
-__global__ void __launch_bounds__(256, MODE == 0 ? 3 : 2) bwd_pair_kernel(SsdBwdParams p) {
+__global__ void __launch_bounds__(256, MODE == 0 ? 3 : 2)
+    bwd_pass_pair_kernel(SsdBwdParams p, uint32_t passes, uint32_t pairs) {
   __shared__ PairLds<MODE> lds;
+  uint32_t octet = blockIdx.x / 8u;
+  const bool pass = octet >= pairs;
+  octet = pass ? octet - pairs : octet;
+  if (pass) {
+    const uint32_t block = octet * 8u + blockIdx.x % 8u;
+    if (block < (uint32_t)(p.batch * p.nheads * (kP * N / 1024))) pass_role<N>(p, block);
+    return;
+  }
   // the pairs of one chunk's group share an XCD's L2, and of an XCD's pairs the
   // ib = jb ones, which take longest, come first
   const int units = (int)p.batch * p.nchunks * p.ngroups, xcd = (int)(blockIdx.x % 8u);
   const int u0 = (int)((int64_t)units * xcd / 8), n = (int)((int64_t)units * (xcd + 1) / 8) - u0;
-  int l = (int)(blockIdx.x / 8u), ib, jb, unit;
+  int l = (int)octet, ib, jb, unit;
   if (l < 4 * n) {
     unit = u0 + l / 4;
     ib = jb = l % 4;
@@ -1263,10 +1283,12 @@ hipError_t launch_n(const SsdBwdParams& p, hipStream_t st) {
     default: e = launch_state<MODE, N, 4>(p, st); break;
   }
   if (e != hipSuccess) return e;
-  SS_LAUNCH((bwd_pass_kernel<N>), p.batch * p.nheads * (kP * N / 1024), 256);
+  const uint32_t passes = pass_octets(p), pairs = pair_octets(p);
+  hipLaunchKernelGGL((bwd_pass_pair_kernel<MODE, N>), dim3(8u * (passes + pairs)), dim3(256), 0, st, p, passes, pairs);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
   SS_LAUNCH((bwd_scan_kernel<MODE, N, true>), heads, kScanThreads);
   if constexpr (gate) SS_LAUNCH((bwd_scan_kernel<MODE, N, false>), heads, kScanThreads);
-  SS_LAUNCH((bwd_pair_kernel<MODE, N>), (places * p.ngroups + 7) / 8 * (8 * kPairs), 256);
   SS_LAUNCH((bwd_out_kernel<MODE, N>), places * p.ngroups * 8, kOutThreads);
   SS_LAUNCH((bwd_delta_kernel<io_of<MODE>()>), heads, 256);
   SS_LAUNCH(bwd_sum_kernel, p.nheads, 256);
