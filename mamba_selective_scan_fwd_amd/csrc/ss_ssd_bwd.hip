@@ -368,29 +368,37 @@ __device__ __forceinline__ void pass_role(const SsdBwdParams& p, uint32_t block)
   if (p.dh0) *reinterpret_cast<f32x4*>(p.dh0 + row) = Rg;
 }
 
-// ---- dx (REV), or y for dz --------------------------------------------------------------
+// ---- dx (rev), or y for dz --------------------------------------------------------------
 // Workgroup = (chunk, head), 512 threads, laid out as prompt_scan_kernel: out
 // rows o, source rows s, out^T[p][o] = sum_s u_s[p] M[o][s] + f_o sum_n K[p][n] v_o[n].
-//   REV:  s >= o, u = g, M = exp(cs_s - cs_o) (C_s . B_o),         K = R, v = B, f = exp(cs_last - cs_o)
+//   rev:  s >= o, u = g, M = exp(cs_s - cs_o) (C_s . B_o),         K = R, v = B, f = exp(cs_last - cs_o)
 //   else: s <= o, u = x, M = exp(cs_o - cs_s) Delta_s (C_o . B_s), K = E, v = C, f = exp(cs_o)
 // A pair in different pieces of 64 takes a factor per row and one per column,
 // both through the piece's end, a pair inside a piece the exp of a difference.
 constexpr int kScanThreads = 512;
-template <int MODE, int N, bool REV>
-__global__ void __launch_bounds__(kScanThreads, MODE == 0 ? 4 : 2) bwd_scan_kernel(SsdBwdParams p) {
+// Where z is given, workgroups of both take turns in one launch; u's second part
+// takes K's place once K is used up, so that two workgroups share a CU (gated
+// fp16, B = 2, L = 1001, 8 heads, state 64: the gradients take 77 us, 86 us with
+// two launches; B = 4, L = 2048, 24 heads: 296 against 298 us).
+template <int MODE, int N>
+__global__ void __launch_bounds__(kScanThreads, 4) bwd_scan_kernel(SsdBwdParams p) {
   constexpr int IO = io_of<MODE>();
   // two parts at the most: dx and dz are rounded to 16 bits
-  constexpr int UP = REV ? (g_parts<MODE>() > 1 ? 2 : 1) : data_parts<MODE>(), VP = data_parts<MODE>();
+  constexpr int UP = g_parts<MODE>() > 1 ? 2 : 1, VP = data_parts<MODE>();
   constexpr int kHS = N + 8;
   __shared__ __attribute__((aligned(16))) float sDelta[kQ];
   __shared__ __attribute__((aligned(16))) float sCs[kQ];   // Delta A summed from the piece's first step
   __shared__ __attribute__((aligned(16))) float sCol[kQ];  // a source row's factor
   __shared__ __attribute__((aligned(16))) int sSeg[kQ];
   __shared__ float sTot[4];
-  __shared__ __attribute__((aligned(16))) uint16_t sU[UP][kQ * kP];
-  __shared__ __attribute__((aligned(16))) uint16_t sK[2][kP * kHS];
+  __shared__ __attribute__((aligned(16))) uint16_t u0[kQ * kP];
+  __shared__ __attribute__((aligned(16))) uint16_t ku[UP > 1 && 2 * kP * kHS < kQ * kP ? kQ * kP : 2 * kP * kHS];
+  uint16_t* const sU[2] = {u0, ku};
+  uint16_t* const sK[2] = {ku, ku + kP * kHS};
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
-  const int lb = (int)xcd_logical_block();  // the heads of one chunk share its B, C and C B^T in an XCD's L2
+  const int all = (int)xcd_logical_block();  // the heads of one chunk share its B, C and C B^T in an XCD's L2
+  const int lb = MODE % 2 ? all >> 1 : all;
+  const bool rev = MODE % 2 ? all & 1 : true;
   const int h = lb % p.nheads;
   const Chunk q = chunk_of(p, lb / p.nheads);
   const int rows = q.rows, g = h / (p.nheads / p.ngroups);
@@ -404,19 +412,19 @@ __global__ void __launch_bounds__(kScanThreads, MODE == 0 ? 4 : 2) bwd_scan_kern
   u32x4v ur[UP][4];
 #pragma unroll
   for (int i = 0; i < UP; ++i) {
-    const auto uv = plane_view(REV ? p.gp[i] : p.xp[i], q.row0, xrow, h * kP, rows);
+    const auto uv = plane_view(rev ? p.gp[i] : i < data_parts<MODE>() ? p.xp[i] : nullptr, q.row0, xrow, h * kP, rows);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       ur[i][k] = vload16(uv, (uint32_t)((tid / 8 + 64 * k) * xrow * 2 + (tid % 8) * 16));
   }
-  const f32x4* K = reinterpret_cast<const f32x4*>((REV ? p.ws_R : p.ws_E) + ph * (kP * N));
+  const f32x4* K = reinterpret_cast<const f32x4*>((rev ? p.ws_R : p.ws_E) + ph * (kP * N));
   f32x4 kr[N / 32];
 #pragma unroll
   for (int k = 0; k < N / 32; ++k) kr[k] = K[tid + kScanThreads * k];
   u32x4v vf[VP][2][N / 32];
 #pragma unroll
   for (int i = 0; i < VP; ++i) {
-    const auto vv = plane_view(REV ? p.bp[i] : p.cp[i], q.row0, vrow, g * N, rows);
+    const auto vv = plane_view(rev ? p.bp[i] : p.cp[i], q.row0, vrow, g * N, rows);
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -428,15 +436,13 @@ __global__ void __launch_bounds__(kScanThreads, MODE == 0 ? 4 : 2) bwd_scan_kern
     const float tot = __shfl(cs, 63, 64);
     sDelta[tid] = delta;
     sCs[tid] = cs;
-    sCol[tid] = REV ? exp2_hw(cs * kLog2e) : exp2_hw((tot - cs) * kLog2e) * delta;
+    sCol[tid] = rev ? exp2_hw(cs * kLog2e) : exp2_hw((tot - cs) * kLog2e) * delta;
     if (lane == 63) sTot[wave] = cs;
     if (p.seq_idx) sSeg[tid] = p.ws_seg[(int64_t)q.place * kQ + tid];
   }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int at = tm_off<kP>(tid / 8 + 64 * k, 8 * (tid % 8));
-#pragma unroll
-    for (int i = 0; i < UP; ++i) *reinterpret_cast<u32x4v*>(&sU[i][at]) = ur[i][k];
+    *reinterpret_cast<u32x4v*>(&sU[0][tm_off<kP>(tid / 8 + 64 * k, 8 * (tid % 8))]) = ur[0][k];
   }
 #pragma unroll
   for (int k = 0; k < N / 32; ++k) {
@@ -474,19 +480,27 @@ __global__ void __launch_bounds__(kScanThreads, MODE == 0 ? 4 : 2) bwd_scan_kern
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     const int o = orow[b] + lane % 16, piece = blk[b] / 2;
-    float arg = REV ? sTot[piece] - sCs[o] : sCs[o];
-    if constexpr (REV) {
+    float arg = rev ? sTot[piece] - sCs[o] : sCs[o];
+    if (rev) {
       for (int k = piece + 1; k < 4; ++k) arg += sTot[k];
     } else {
       for (int k = 0; k < piece; ++k) arg += sTot[k];
     }
     float f = exp2_hw(arg * kLog2e);
-    if (p.seq_idx && sSeg[o] != (REV ? sSeg[rows - 1] : 0)) f = 0.0f;
+    if (p.seq_idx && sSeg[o] != (rev ? sSeg[rows - 1] : 0)) f = 0.0f;
 #pragma unroll
     for (int pt = 0; pt < 4; ++pt) acc[b][pt] *= f;
   }
 
-  const float* CB = (REV ? p.ws_bc : p.ws_cb) + ((int64_t)q.place * p.ngroups + g) * (kQ * kQ);
+  if constexpr (UP > 1) {
+    __syncthreads();  // K is used up
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      *reinterpret_cast<u32x4v*>(&sU[1][tm_off<kP>(tid / 8 + 64 * k, 8 * (tid % 8))]) = ur[UP - 1][k];
+    __syncthreads();
+  }
+
+  const float* CB = (rev ? p.ws_bc : p.ws_cb) + ((int64_t)q.place * p.ngroups + g) * (kQ * kQ);
   const float Dh = p.D ? p.D[h] : 0.0f;
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
@@ -495,7 +509,7 @@ __global__ void __launch_bounds__(kScanThreads, MODE == 0 ? 4 : 2) bwd_scan_kern
     const float cso = sCs[o], tot = sTot[piece];
     const int sego = p.seq_idx ? sSeg[o] : 0;
     const float* cb = CB + cb_at(orow[b] / 16, 0) + lane * 8;
-    const int s0 = REV ? piece : 0, s1 = REV ? lastp : piece;
+    const int s0 = rev ? piece : 0, s1 = rev ? lastp : piece;
     f32x4 cur[2][2], nxt[2][2];
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
@@ -509,13 +523,13 @@ __global__ void __launch_bounds__(kScanThreads, MODE == 0 ? 4 : 2) bwd_scan_kern
           for (int e = 0; e < 2; ++e) nxt[ks][e] = *reinterpret_cast<const f32x4*>(cb + (2 * sp + 2 + ks) * 512 + 4 * e);
       }
       const bool diag = sp == piece;
-      float arg = REV ? tot - cso : cso;  // Delta A between this row and the source piece's end towards it
-      for (int k = REV ? piece + 1 : sp + 1; k < (REV ? sp : piece); ++k) arg += sTot[k];
+      float arg = rev ? tot - cso : cso;  // Delta A between this row and the source piece's end towards it
+      for (int k = rev ? piece + 1 : sp + 1; k < (rev ? sp : piece); ++k) arg += sTot[k];
       const float fo = exp2_hw(arg * kLog2e);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        // steps all behind (REV: before) the block's rows
-        if (diag && ks == (REV ? 0 : 1) && blk[b] % 2 == (REV ? 1 : 0)) continue;
+        // steps all behind (rev: before) the block's rows
+        if (diag && ks == (rev ? 0 : 1) && blk[b] % 2 == (rev ? 1 : 0)) continue;
         const int s = kJB * sp + 32 * ks + 8 * (lane / 16);
         float m[8];
         if (diag) {
@@ -525,9 +539,9 @@ __global__ void __launch_bounds__(kScanThreads, MODE == 0 ? 4 : 2) bwd_scan_kern
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float css = e < 4 ? c0[e & 3] : c1[e & 3];
-            float v = cur[ks][e / 4][e & 3] * exp2_hw((REV ? css - cso : cso - css) * kLog2e);
-            if constexpr (!REV) v *= e < 4 ? d0[e & 3] : d1[e & 3];
-            m[e] = (REV ? s + e >= o : s + e <= o) ? v : 0.0f;
+            float v = cur[ks][e / 4][e & 3] * exp2_hw((rev ? css - cso : cso - css) * kLog2e);
+            if (!rev) v *= e < 4 ? d0[e & 3] : d1[e & 3];
+            m[e] = (rev ? s + e >= o : s + e <= o) ? v : 0.0f;
           }
         } else {
           const f32x4 w0 = *reinterpret_cast<const f32x4*>(&sCol[s]), w1 = *reinterpret_cast<const f32x4*>(&sCol[s + 4]);
@@ -578,7 +592,7 @@ __global__ void __launch_bounds__(kScanThreads, MODE == 0 ? 4 : 2) bwd_scan_kern
       for (int i = 0; i < UP; ++i) uw[i] = *reinterpret_cast<const uint2*>(&sU[i][tm_off<kP>(o, p0)]);
       float u[4], r[4];  // of row o: g, or x
       join4<UP>(uw, u);
-      if constexpr (REV) {
+      if (rev) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) r[e] = fmaf(Dh, u[e], delta * acc[b][pt][e]);
       } else {
@@ -592,7 +606,7 @@ __global__ void __launch_bounds__(kScanThreads, MODE == 0 ? 4 : 2) bwd_scan_kern
           r[e] = dy[e] * fmaf(Dh, u[e], acc[b][pt][e]) * (sg * fmaf(z[e], 1.0f - sg, 1.0f));
         }
       }
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(REV ? p.dx : p.dz) + out + p0) =
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(rev ? p.dx : p.dz) + out + p0) =
           make_uint2(pack2<IO>(r[0], r[1]), pack2<IO>(r[2], r[3]));
     }
   }
@@ -1287,8 +1301,7 @@ hipError_t launch_n(const SsdBwdParams& p, hipStream_t st) {
   hipLaunchKernelGGL((bwd_pass_pair_kernel<MODE, N>), dim3(8u * (passes + pairs)), dim3(256), 0, st, p, passes, pairs);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  SS_LAUNCH((bwd_scan_kernel<MODE, N, true>), heads, kScanThreads);
-  if constexpr (gate) SS_LAUNCH((bwd_scan_kernel<MODE, N, false>), heads, kScanThreads);
+  SS_LAUNCH((bwd_scan_kernel<MODE, N>), gate ? 2 * heads : heads, kScanThreads);
   SS_LAUNCH((bwd_out_kernel<MODE, N>), places * p.ngroups * 8, kOutThreads);
   SS_LAUNCH((bwd_delta_kernel<io_of<MODE>()>), heads, 256);
   SS_LAUNCH(bwd_sum_kernel, p.nheads, 256);
