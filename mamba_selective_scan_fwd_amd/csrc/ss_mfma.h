@@ -58,6 +58,10 @@ __device__ __forceinline__ u32x4v vload16(__amdgpu_buffer_rsrc_t r, uint32_t off
 __device__ __forceinline__ uint2 vload8(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
 }
+__device__ __forceinline__ void vstore8(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t a, uint32_t b) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  __builtin_amdgcn_raw_buffer_store_b64(u32x2{a, b}, r, off, 0, 0);
+}
 
 // Time-major tiles in LDS (row = step, W 16-bit columns, 16-byte chunks of a
 // row rotated by (row / 4) so that both the row writes and the transposing

@@ -216,9 +216,15 @@ bool pass_deep(int64_t workgroups, int64_t chunks, int64_t nseqs) {
 // pair across pieces two factors, exp(cs_i - end of j's piece) and
 // exp(end of j's piece - cs_j), one exp per row and one per column.  fp16's lo
 // part of x takes E's place once E C^T is done, so that two workgroups share a
-// CU (one prompt of 32769 tokens: 137 -> 122 us).  Several heads one after the
-// other in a workgroup, the next one's loads ahead, leave one workgroup to a CU
-// and take longer (24 ragged prompts: 160 us against 95).
+// CU (one prompt of 32769 tokens: 122 us, 137 us with one).  C B^T and y go
+// through range-checked views, whose addresses take one register, and the gate
+// is loaded in the place of a next piece behind the last: nothing is spilled at
+// two workgroups to a CU (88 and 115 us; 94 and 122 us with 8 and 12 registers
+// spilled, whose stores went to HBM).  Of the 88 us, the loads, E's staging and
+// the stores alone take about 52, near what their 230 MB need, and the products
+// do not hide behind them.  Several heads one after the other in a workgroup,
+// the next one's loads ahead, leave one workgroup to a CU and take longer (24
+// ragged prompts: 160 us against 95).
 constexpr int kScanThreads = 512;
 template <int IO, int N>
 __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptParams p) {
@@ -352,7 +358,8 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
   }
 
   // ---- Y_diag += x^T M^T, piece by piece
-  const float* CB = p.ws_cb + ((int64_t)place * p.ngroups + g) * (kQ * kQ);
+  const auto cbv = make_rsrc(p.ws_cb + ((int64_t)place * p.ngroups + g) * (kQ * kQ), kQ * kQ * 4);
+  const auto yv = rows_view(static_cast<char*>(p.y) + (row0 * p.nheads + h) * (kP * 2), (int64_t)p.nheads * (kP * 2), rows);
   const auto zv = rows_view(p.z ? static_cast<const char*>(p.z) + row0 * p.z_stride * 2 + h * kP * 2 : nullptr,
                             p.z_stride * 2, rows);
   const float Dh = p.D ? p.D[h] : 0.0f;
@@ -362,16 +369,13 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
     const int i = ir[b] + lane % 16;  // this lane's row
     const int dpiece = blk[b] / 2;    // the piece that holds it
     const float csi = sCs[i];
-    const float* cb = CB + cb_at(ir[b] / 16, 0) + lane * 8;
+    const uint32_t cb = (uint32_t)(cb_at(ir[b] / 16, 0) + lane * 8) * 4u;
     uint2 zr[4];
-#pragma unroll
-    for (int pt = 0; pt < 4; ++pt)
-      zr[pt] = vload8(zv, (uint32_t)(i * p.z_stride * 2 + (16 * pt + 4 * (lane / 16)) * 2));
     f32x4 cur[2][2], nxt[2][2];
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) cur[ks][e] = *reinterpret_cast<const f32x4*>(cb + ks * 512 + 4 * e);
+      for (int e = 0; e < 2; ++e) cur[ks][e] = __builtin_bit_cast(f32x4, vload16(cbv, cb + ks * 2048 + 16 * e));
     for (int piece = 0; piece <= dpiece; ++piece) {
       const int jb = kJB * piece;
       if (piece < dpiece) {
@@ -379,7 +383,11 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
         for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            nxt[ks][e] = *reinterpret_cast<const f32x4*>(cb + (2 * piece + 2 + ks) * 512 + 4 * e);
+            nxt[ks][e] = __builtin_bit_cast(f32x4, vload16(cbv, cb + (2 * piece + 2 + ks) * 2048 + 16 * e));
+      } else {  // the last piece: the gate instead
+#pragma unroll
+        for (int pt = 0; pt < 4; ++pt)
+          zr[pt] = vload8(zv, (uint32_t)(i * p.z_stride * 2 + (16 * pt + 4 * (lane / 16)) * 2));
       }
       const bool diag = piece == dpiece;
       float between = csi;  // Delta A from the end of this piece to row i
@@ -434,9 +442,8 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
 #pragma unroll
         for (int e = 0; e < 2; ++e) cur[ks][e] = nxt[ks][e];
     }
-    // ---- D skip, gate, store
-    if (i < rows) {
-      char* y = static_cast<char*>(p.y) + ((row0 + i) * p.nheads + h) * (int64_t)(kP * 2);
+    // ---- D skip, gate, store (rows past the chunk are dropped by the range check)
+    {
 #pragma unroll
       for (int pt = 0; pt < 4; ++pt) {
         const int p0 = 16 * pt + 4 * (lane / 16);
@@ -459,7 +466,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
           o[2] *= silu_f(low16<IO>(zr[pt].y));
           o[3] *= silu_f(high16<IO>(zr[pt].y));
         }
-        *reinterpret_cast<uint2*>(y + p0 * 2) = make_uint2(pack2<IO>(o[0], o[1]), pack2<IO>(o[2], o[3]));
+        vstore8(yv, (uint32_t)(i * p.nheads * (kP * 2) + p0 * 2), pack2<IO>(o[0], o[1]), pack2<IO>(o[2], o[3]));
       }
     }
   }
