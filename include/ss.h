@@ -441,8 +441,8 @@ ss_status ss_ssd_bwd(const ss_ssd_problem *p, const void *x, const void *dt, con
  *   out[t,d] = silu(bias[d] + sum_{k<W} w[d,k] * x[t-W+1+k,d]),
  * the inputs before a sequence's first row being its slot's window, or zeros.
  *   x, out : (tokens, dim) io dtype (fp32, fp16 or bf16), rows x_stride /
- *            out_stride apart; aligned to the element.  16-byte aligned rows
- *            of whole 16-byte vectors run faster.
+ *            out_stride apart; aligned to the element.  16-bit rows of an
+ *            even length on 4-byte boundaries run faster.
  *   w      : (dim, W) fp32; bias: (dim) fp32 or NULL, as in ss_conv1d_fwd.
  *   conv_state : afterwards every sequence's slot holds its last W-1 inputs
  *            (oldest first; of the window before where it is shorter).  May be

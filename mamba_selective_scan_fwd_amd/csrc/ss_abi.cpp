@@ -796,8 +796,8 @@ ss_status ss_conv1d_prompt(const ss_conv_prompt_problem* p, const void* x, const
   k.conv_state = conv_state; k.out = out;
   k.x_stride = p->x_stride; k.out_stride = p->out_stride;
   k.tokens = (int32_t)p->tokens; k.nseqs = (int32_t)p->nseqs; k.dim = (int32_t)p->dim; k.nslots = (int32_t)p->nslots;
-  k.vec = aligned(x) && aligned(out) && (p->dim * e) % 16 == 0 && (p->x_stride * e) % 16 == 0 &&
-          (p->out_stride * e) % 16 == 0;
+  k.pairs = e == 2 && aligned_to(x, 4) && aligned_to(out, 4) && p->dim % 2 == 0 && p->x_stride % 2 == 0 &&
+            p->out_stride % 2 == 0;
   return from_hip(ss::launch_conv_prompt(k, static_cast<hipStream_t>(stream)));
 }
 

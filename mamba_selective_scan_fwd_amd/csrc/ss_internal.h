@@ -238,7 +238,7 @@ struct ConvPromptParams {
   int32_t io;
   int32_t width;
   int32_t silu;
-  bool vec;                  // 16-byte rows of channels (see conv1d_prompt_kernel)
+  bool pairs;                // 16-bit channels in pairs on 4-byte boundaries (see conv1d_prompt_kernel)
   const void* x;             // (tokens, dim), rows x_stride apart
   const float* w;            // (dim, W)
   const float* bias;         // (dim) or null

@@ -484,8 +484,7 @@ hipError_t launch_prompt_n(const SsdPromptParams& p, hipStream_t st) {
   switch (state_heads((int64_t)p.chunks * p.ngroups, p.nheads / p.ngroups, device_cus())) {
     case 1: launch_state<IO, N, 1>(p, st); break;
     case 2: launch_state<IO, N, 2>(p, st); break;
-    case 3: launch_state<IO, N, 3>(p, st); break;
-    default: launch_state<IO, N, 4>(p, st); break;
+    default: launch_state<IO, N, 3>(p, st); break;
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

@@ -17,42 +17,33 @@ namespace {
 
 // ---- causal conv1d + SiLU of packed prompts ---------------------------------
 // A streaming stencil, bound by HBM.  A wave takes a chunk of 16 rows of one
-// sequence and 64 vectors of VEC channels (16 bytes; VEC = 1 where the channels
-// or a row's start do not allow 16-byte access); a lane loads its 16 rows and
-// the W - 1 rows before them at once, each row's 16-byte pieces adjacent over the
-// lanes, and walks down the rows.  A workgroup's four waves have the same
-// channels of four chunks in a row, so that they share the weights (40 floats a
-// lane at W = 4) and the rows before a chunk in L1 (37 ragged prompts, 16,021
-// rows of 5376 fp16 channels: 86 us, 97 us with neighbouring channels instead).
+// sequence and 64 times 4 bytes of channels (two 16-bit ones, which need 4-byte
+// rows, or one); a lane loads its 16 rows and the W - 1 rows before them at once
+// and walks down the rows.  Four bytes a lane, not more: with 16 the weights and
+// rows take 142 registers and a quarter of the waves (37 ragged prompts, 16,021
+// rows of 5376 fp16 channels: 74 us, 78 with 8 bytes a lane, 86 with 16; fp32
+// 139 against 142; one prompt of 2048 rows of 1792 channels 6.0, 7.4 and 10.0
+// us), with 2 bytes the large sizes take 75 us; chunks of 8 and 32 rows take 75
+// and 76 us.  74 us are 4.75 TB/s.  A workgroup's four waves have
+// the same channels of four chunks in a row, so that they share the weights and
+// the rows before a chunk in L1.
 // The chunk that holds a sequence's first rows reads the slot's window and,
 // having read it, writes the new one: no other wave touches these channels of
 // the slot, so the update is in place.
 constexpr int kLogRows = 4;
 constexpr int kRows = 1 << kLogRows;
 
-template <int IO, int VEC> struct row_vec;  // the raw bits of VEC channels
-template <int VEC> struct row_vec<SS_F32, VEC> { uint32_t v[VEC]; };
-template <int VEC> struct row_vec<SS_F16, VEC> { uint32_t v[(VEC + 1) / 2]; };
-template <int VEC> struct row_vec<SS_BF16, VEC> { uint32_t v[(VEC + 1) / 2]; };
-
 template <int IO, int VEC>
-__device__ __forceinline__ row_vec<IO, VEC> load_row(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  row_vec<IO, VEC> a;
-  if constexpr (VEC == 1) {
-    a.v[0] = bload<IO>(r, off);
-  } else {
-    const auto b = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a.v[i] = b[i];
-  }
-  return a;
+__device__ __forceinline__ uint32_t load_row(__amdgpu_buffer_rsrc_t r, uint32_t off) {  // the raw bits of VEC channels
+  if constexpr (VEC == 1) return bload<IO>(r, off);
+  else return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
 }
-template <int IO, int VEC>
-__device__ __forceinline__ float channel(const row_vec<IO, VEC>& a, int e) {
+template <int IO>
+__device__ __forceinline__ float channel(uint32_t a, int e) {
   if constexpr (IO == SS_F32)
-    return __uint_as_float(a.v[e]);
+    return __uint_as_float(a);
   else
-    return bits_f32<IO>((raw_t<IO>)((a.v[e / 2] >> (16 * (e % 2))) & 0xffffu));
+    return bits_f32<IO>((raw_t<IO>)((a >> (16 * e)) & 0xffffu));
 }
 
 template <int IO, int W, int VEC>
@@ -75,7 +66,7 @@ __global__ void __launch_bounds__(256) conv1d_prompt_kernel(ConvPromptParams p) 
   const auto xv = make_rsrc(static_cast<const char*>(p.x) + row0 * p.x_stride * s,
                             rows > 0 ? (uint32_t)(((rows - 1) * p.x_stride + p.dim) * s) : 0u);
   const uint32_t co = (uint32_t)(c0 * s), rb = (uint32_t)(p.x_stride * s);
-  row_vec<IO, VEC> cur[kRows];
+  uint32_t cur[kRows];
 #pragma unroll
   for (int r = 0; r < kRows; ++r) cur[r] = load_row<IO, VEC>(xv, r < rows ? r * rb + co : kOffNone);
 
@@ -93,9 +84,9 @@ __global__ void __launch_bounds__(256) conv1d_prompt_kernel(ConvPromptParams p) 
                                 (uint32_t)(((W - 2) * p.x_stride + p.dim) * s));
 #pragma unroll
       for (int k = 0; k < W - 1; ++k) {
-        const row_vec<IO, VEC> a = load_row<IO, VEC>(hv, k * rb + co);
+        const uint32_t a = load_row<IO, VEC>(hv, k * rb + co);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) prev[k][e] = channel<IO, VEC>(a, e);
+        for (int e = 0; e < VEC; ++e) prev[k][e] = channel<IO>(a, e);
       }
     } else {
       const int slot = uniform(slot_of(p.slots, q.seq, p.nslots));
@@ -115,9 +106,9 @@ __global__ void __launch_bounds__(256) conv1d_prompt_kernel(ConvPromptParams p) 
           float v[VEC];
           if (r >= 0) {
             const auto one = make_rsrc(xs + r * p.x_stride * s, (uint32_t)(p.dim * s));
-            const row_vec<IO, VEC> a = load_row<IO, VEC>(one, co);
+            const uint32_t a = load_row<IO, VEC>(one, co);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) v[e] = channel<IO, VEC>(a, e);
+            for (int e = 0; e < VEC; ++e) v[e] = channel<IO>(a, e);
           } else {
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
@@ -142,7 +133,7 @@ __global__ void __launch_bounds__(256) conv1d_prompt_kernel(ConvPromptParams p) 
   for (int r = 0; r < kRows; ++r) {
     float x[VEC], y[VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) x[e] = channel<IO, VEC>(cur[r], e);
+    for (int e = 0; e < VEC; ++e) x[e] = channel<IO>(cur[r], e);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       float pre = bias[e];
@@ -163,17 +154,9 @@ __global__ void __launch_bounds__(256) conv1d_prompt_kernel(ConvPromptParams p) 
     if constexpr (VEC == 1) {
       bstore<IO>(ov, at, y[0]);
     } else {
-      typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-      u32x4 o;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (IO == SS_F32)
-          o[i] = __float_as_uint(y[i]);
-        else
-          o[i] = (uint32_t)__builtin_bit_cast(uint16_t, from_f32<IO>(y[2 * i])) |
-                 ((uint32_t)__builtin_bit_cast(uint16_t, from_f32<IO>(y[2 * i + 1])) << 16);
-      }
-      __builtin_amdgcn_raw_buffer_store_b128(o, ov, at, 0, 0);
+      const uint32_t o = (uint32_t)__builtin_bit_cast(uint16_t, from_f32<IO>(y[0])) |
+                         ((uint32_t)__builtin_bit_cast(uint16_t, from_f32<IO>(y[VEC - 1])) << 16);
+      __builtin_amdgcn_raw_buffer_store_b32(o, ov, at, 0, 0);
     }
   }
 }
@@ -186,7 +169,9 @@ hipError_t launch_conv_prompt_vec(const ConvPromptParams& p, hipStream_t st) {
 }
 template <int IO, int W>
 hipError_t launch_conv_prompt_w(const ConvPromptParams& p, hipStream_t st) {
-  return p.vec ? launch_conv_prompt_vec<IO, W, IO == SS_F32 ? 4 : 8>(p, st) : launch_conv_prompt_vec<IO, W, 1>(p, st);
+  if constexpr (IO != SS_F32)
+    if (p.pairs) return launch_conv_prompt_vec<IO, W, 2>(p, st);
+  return launch_conv_prompt_vec<IO, W, 1>(p, st);
 }
 template <int IO>
 hipError_t launch_conv_prompt_io(const ConvPromptParams& p, hipStream_t st) {

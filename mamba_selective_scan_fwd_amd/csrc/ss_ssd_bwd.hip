@@ -1293,8 +1293,7 @@ hipError_t launch_n(const SsdBwdParams& p, hipStream_t st) {
   switch (state_heads(2 * places * p.ngroups, p.nheads / p.ngroups, device_cus())) {
     case 1: e = launch_state<MODE, N, 1>(p, st); break;
     case 2: e = launch_state<MODE, N, 2>(p, st); break;
-    case 3: e = launch_state<MODE, N, 3>(p, st); break;
-    default: e = launch_state<MODE, N, 4>(p, st); break;
+    default: e = launch_state<MODE, N, 3>(p, st); break;
   }
   if (e != hipSuccess) return e;
   const uint32_t passes = pass_octets(p), pairs = pair_octets(p);
