@@ -572,12 +572,14 @@ def _rows(t, dtype, name, shape, dev, keep, vector=True):
         return None, 0
     if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         _refuse(t, dtype, name, shape, dev)
-    strides = t.stride()
-    size, whole = 1, True
-    for k in range(len(shape) - 1, 0, -1):
-        whole = whole and (strides[k] == size or shape[k] == 1)
-        size *= shape[k]
-    stride, at = strides[0] if shape[0] > 1 else size, t.data_ptr()
+    strides, at = t.stride(), t.data_ptr()
+    if len(shape) == 2:
+        size = shape[1]
+        whole = strides[1] == 1 or size == 1
+    else:
+        size = shape[1] * shape[2]
+        whole = (strides[2] == 1 or shape[2] == 1) and (strides[1] == shape[2] or shape[1] == 1)
+    stride = strides[0] if shape[0] > 1 else size
     if not whole or stride < size or stride > 1 << 21 or (vector and (at & 15 or stride * t.element_size() & 15)):
         t, stride = t.contiguous(), size
         if vector and t.data_ptr() & 15:
@@ -615,7 +617,7 @@ def _problem(kind, size, sizes, *fields):
 def _launch(dev, fn, problem, *args):
     """The C call on the current stream of the tensors' device, whichever device is current."""
     stream = torch._C._cuda_getCurrentRawStream(dev)  # torch.cuda.current_stream(dev).cuda_stream, 1 us sooner
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         status = fn(problem, *args, stream)
     else:
         with torch.cuda.device(dev):
@@ -662,7 +664,7 @@ def conv1d_prompt(x, w, cu_seqlens, conv_state, bias=None, silu=True, slots=None
     if w.dim() != 2:
         w = w.reshape(Dd, W)
     if out is None:
-        out = torch.empty((T, Dd), dtype=io, device=x.device)
+        out = x.new_empty((T, Dd))
     xa, xs = _rows(x, io, "x", (T, Dd), dev, keep, False)
     oa, os_ = _rows(out, io, "out", (T, Dd), dev, [], False)
     if oa != out.data_ptr():
@@ -691,7 +693,7 @@ def ssd_prompt(x, dt, A, Bm, Cm, cu_seqlens, state, D=None, z=None, dt_bias=None
     _, G, N = Bm.shape
     S, nslots = cu_seqlens.numel() - 1, state.shape[0]
     if y is None:
-        y = torch.empty((T, Hn, P), dtype=io, device=x.device)
+        y = x.new_empty((T, Hn, P))
     xa, xs = _rows(x, io, "x", (T, Hn, P), dev, keep)
     za, zs = _rows(z, io, "z", (T, Hn, P), dev, keep)
     ba, bs = _rows(Bm, io, "Bm", (T, G, N), dev, keep)
@@ -809,7 +811,7 @@ def ssd_step(xbc, dt, A, conv_w, conv_state, state, ngroups=1, conv_bias=None, D
     if conv_w.dim() != 2:
         conv_w = conv_w.reshape(ch, W)
     if y is None:
-        y = torch.empty((n, Hn, P), dtype=io, device=xbc.device)
+        y = xbc.new_empty((n, Hn, P))
     xa, xs = _rows(xbc, io, "xbc", (n, ch), dev, keep, False)
     da, ds = _rows(dt, io, "dt", (n, Hn), dev, keep, False)
     za, zs = _rows(z, io, "z", (n, Hn, P), dev, keep, False)
@@ -863,7 +865,7 @@ class SsdStepCall:
         self.fn, self.dev = lib.ss_ssd_step, dev
 
     def __call__(self):
-        if torch.cuda.current_device() == self.dev:
+        if torch._C._cuda_getDevice() == self.dev:
             status = self.fn(*self.args)
         else:
             with torch.cuda.device(self.dev):
