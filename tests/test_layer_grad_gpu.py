@@ -389,3 +389,25 @@ def test_second_derivatives_and_strided_workspaces_are_refused():
         ss.ssd_bwd(q["x"].detach(), q["dt"], q["A"], q["Bm"], q["Cm"], q["dy"], workspace=room[::2])
     with pytest.raises(ValueError):
         ss.ssd_bwd(q["x"].detach(), q["dt"], q["A"], q["Bm"], q["Cm"], q["dy"], workspace=room.cpu())
+
+
+@pytest.mark.parametrize("L", [3, 8, 9, 16, 21, 4096])
+def test_conv_bwd_values_that_are_not_finite_stay_in_their_reach(L):
+    """An infinity or NaN in x at one step of one row reaches the gradients of the steps that its window meets, its
+    channel's dw and dbias, and nothing else."""
+    ss = _ss()
+    W, D = 4, 4
+    q = _conv(2, D, L, W, "f32", seed=L)
+    g = {k: v.cuda() for k, v in q.items()}
+    clean = ss.conv1d_bwd(**g)
+    for t in sorted({0, L // 2, max(L - 4, 0), L - 1}):
+        for bad in (float("inf"), float("nan")):
+            x = g["x"].clone()
+            x[1, 2, t] = bad
+            got = ss.conv1d_bwd(**dict(g, x=x))
+            far = torch.ones(2, D, L, dtype=torch.bool, device="cuda")
+            far[1, 2, max(t - (W - 1), 0):t + W] = False       # dpre of steps t .. t + W - 1, dx W - 1 before them
+            assert torch.equal(got["dx"][far], clean["dx"][far]), (t, bad)
+            others = [0, 1, 3]
+            assert torch.equal(got["dw"][others], clean["dw"][others])
+            assert torch.equal(got["dbias"][others], clean["dbias"][others])
