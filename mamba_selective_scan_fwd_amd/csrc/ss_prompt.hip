@@ -18,7 +18,12 @@
 //                        in the place of its S, and the final state;
 //   prompt_scan_kernel   per (chunk, head): Y, skip, gate.
 // All chunks of a prompt run at once, whatever its length; only the
-// element-wise pass walks them in order.
+// element-wise pass walks them in order.  24 ragged prompts of 16384 tokens (24
+// heads, state 128, bf16, gate): 50, 25 and 88 us; one prompt of 32769 tokens
+// (state 64, fp16): 68, 21 and 115-125 us.  Of the bytes, 4 times the fp32 states
+// (276 MB of the first) are the price of the chunks' independence: a walk over the
+// chunks inside a workgroup, as in ss_ssd.hip, has no such traffic and as many
+// workgroups as prompts have heads.
 //
 // Precision: products of 16-bit inputs run on the matrix cores as they are.
 // Computed operands are multiplied as sums of bf16 parts (ss_mfma.h): the

@@ -30,14 +30,21 @@
 //   bwd_planes   (fp16 or gated) the operands' planes of bf16 parts, g among them
 //   bwd_state    per (chunk, head): what a chunk adds to E and to R; further
 //                workgroups: B C^T (and C B^T if gated) per (chunk, group)
-//   bwd_pass     per (row, head, 1024 elements): E of every chunk, then R and
+//   bwd_pass_pair, two kinds of workgroups:
+//     pass       per (row, head, 1024 elements): E of every chunk, then R and
 //                <R, E> backwards, dh0
-//   bwd_scan     per (chunk, head): G_j B_j, dx; if gated another one rebuilds y for dz
-//   bwd_pair     per (chunk, group, pair of pieces of 64): all heads of the group, S
+//     pair       per (chunk, group, pair of pieces of 64): all heads of the group, S
 //                and the sums of W
-//   bwd_out      per (chunk, group, dC or dB, half the states): dC or dB, e or r
+//   bwd_scan     per (chunk, head): G_j B_j, dx; if gated, others rebuild y for dz
+//   bwd_out      per (chunk, group, dC or dB, half the rows, half the states): dC or
+//                dB, e or r
 //   bwd_delta    per (chunk, head): da, ddt, and the chunk's part of dA, ddt_bias, dD
 //   bwd_sum      per head: dA, ddt_bias, dD
+// At the bench layer (B = 8, L = 2048, 24 heads, state 128, bf16) state, pass_pair,
+// scan, out, delta and sum take 68, 75, 56, 67, 11 and 5 us, of which the bytes they
+// move need 48, 80, 35, 53, 6 and 0 at 4.9 TB/s (E, R and S are read back partly
+// from the last level cache); at two workgroups or less to a CU, their loads,
+// products and LDS phases hide each other only in part.
 // No atomics: every sum has a fixed order.  Computed operands are multiplied
 // as sums of bf16 parts (ss_mfma.h), three where the result stays in fp32 (E,
 // R, t and S's products, which dA, ddt_bias, dD and dh0 sum up), two where it
@@ -949,9 +956,17 @@ __global__ void __launch_bounds__(256, MODE == 0 ? 3 : 2)
 //   out_f[n] = sum_h d_f w_f sum_p K[p][n] F_f[p] + sum_s S_fs u_s[n]
 // and per head v_f . (w_f K^T F_f) (e; r and x . G B's share of it, without
 // Delta).  The heads' K are staged in LDS by turns of two buffers (three parts,
-// [p][16 n] tiles read back transposed): the next head's K and F are on their
-// way while this head is multiplied, one barrier per head.  S comes as operand
-// fragments from bwd_pair, with u's pieces staged in LDS.
+// [p][16 n] tiles read back transposed): the K of the head after the next is on
+// its way while this head is multiplied, the next one's F while its K is staged,
+// one barrier per head.  S comes as operand fragments from bwd_pair, with u's
+// pieces staged in LDS.
+// Bound by HBM and the phases' waits: at the bench layer 68 us for 259 MB (E, R, x
+// and g; the halves' second reads are the L2's), the matrix units busy for a
+// quarter of it.  Two registers sets for F, so that it is loaded a multiplication
+// earlier, take 72 us (gated bf16 at state 128, where they spill: 641 against 599
+// us of the whole); 32 states a workgroup, which read x and g twice as often, 78
+// us; all rows in one workgroup of 512 threads 67 us, and 23.5 against 14.1 us
+// where a few chunks (B = 2, L = 1001, 8 heads) leave CUs idle.
 constexpr int kOutThreads = 256;
 // element (row, c) of a [rows][16] tile: blocks of 4 rows swapped so that the
 // transposing reads of rows 8 apart hit different banks
@@ -985,8 +1000,8 @@ __device__ __forceinline__ void out_role(const SsdBwdParams& p, int lb, uint16_t
     for (int t = 0; t < NT; ++t) tot[b][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
   f32x4 kr[kPer];
-  u32x4v F[2][FP][2][2];  // two heads' in turn
-  float wf[2][2], df[2][2];
+  u32x4v F[FP][2][2];
+  float wf[2], df[2];
   auto load_k = [&](int h) {
     const float* K = (DB ? p.ws_R : p.ws_E) + ((int64_t)q.place * p.nheads + h) * (kP * N) + n0;
 #pragma unroll
@@ -996,7 +1011,7 @@ __device__ __forceinline__ void out_role(const SsdBwdParams& p, int lb, uint16_t
         kr[k] = *reinterpret_cast<const f32x4*>(K + (item / (NH / 4)) * N + 4 * (item % (NH / 4)));
     }
   };
-  auto load_f = [&](int u, int h) {
+  auto load_f = [&](int h) {
 #pragma unroll
     for (int i = 0; i < FP; ++i) {
       const auto fv = plane_view(DB ? p.xp[i % 2] : p.gp[i], q.row0, xrow, h * kP, rows);
@@ -1004,13 +1019,13 @@ __device__ __forceinline__ void out_role(const SsdBwdParams& p, int lb, uint16_t
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
-          F[u][i][b][ks] = vload16(fv, (uint32_t)(fr[b] * xrow * 2 + (32 * ks + 8 * quad) * 2));
+          F[i][b][ks] = vload16(fv, (uint32_t)(fr[b] * xrow * 2 + (32 * ks + 8 * quad) * 2));
     }
     const int64_t at = ((int64_t)q.place * p.nheads + h) * kQ;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      wf[u][b] = (DB ? p.ws_wb : p.ws_wc)[at + fr[b]];
-      df[u][b] = DB ? p.ws_delta[at + fr[b]] : 1.0f;
+      wf[b] = (DB ? p.ws_wb : p.ws_wc)[at + fr[b]];
+      df[b] = DB ? p.ws_delta[at + fr[b]] : 1.0f;
     }
   };
   auto stage_k = [&](uint16_t* buf) {
@@ -1029,7 +1044,7 @@ __device__ __forceinline__ void out_role(const SsdBwdParams& p, int lb, uint16_t
     }
   };
   load_k(g * hpg);
-  load_f(0, g * hpg);
+  load_f(g * hpg);
   stage_k(lds);
   if (hpg > 1) load_k(g * hpg + 1);
   for (int hg0 = 0; hg0 < hpg; hg0 += 2)
@@ -1038,7 +1053,6 @@ __device__ __forceinline__ void out_role(const SsdBwdParams& p, int lb, uint16_t
     const int hg = hg0 + u, h = g * hpg + hg;
     if (hg >= hpg) break;
     const uint16_t* buf = lds + u * kBuf;
-    if (hg + 1 < hpg) load_f(1 - u, h + 1);
     __syncthreads();
     f32x4 a[2][NT];
 #pragma unroll
@@ -1060,10 +1074,12 @@ __device__ __forceinline__ void out_role(const SsdBwdParams& p, int lb, uint16_t
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-              for (int b = 0; b < 2; ++b) a[b][t] = BF::run(kp[t], bfv(F[u][i][b][ks]), a[b][t]);
+              for (int b = 0; b < 2; ++b) a[b][t] = BF::run(kp[t], bfv(F[i][b][ks]), a[b][t]);
       }
     }
+    const float w[2] = {wf[0], wf[1]}, d[2] = {df[0], df[1]};
     if (hg + 1 < hpg) {  // the next head's K into the other buffer, the one after on its way
+      load_f(h + 1);
       stage_k(lds + (1 - u) * kBuf);
       if (hg + 2 < hpg) load_k(h + 2);
     }
@@ -1077,10 +1093,10 @@ __device__ __forceinline__ void out_role(const SsdBwdParams& p, int lb, uint16_t
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           vt = fmaf(v[r], a[b][t][r], vt);
-          tot[b][t][r] = fmaf(DB ? wf[u][b] * df[u][b] : wf[u][b], a[b][t][r], tot[b][t][r]);
+          tot[b][t][r] = fmaf(DB ? w[b] * d[b] : w[b], a[b][t][r], tot[b][t][r]);
         }
       }
-      vt = quad_sum(vt * wf[u][b]);
+      vt = quad_sum(vt * w[b]);
       if (quad == 0) (DB ? p.ws_r : p.ws_e)[to + fr[b]] = vt;
     }
   }
