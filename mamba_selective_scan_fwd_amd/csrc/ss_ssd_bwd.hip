@@ -962,7 +962,7 @@ __global__ void __launch_bounds__(256, MODE == 0 ? 3 : 2)
 // pieces staged in LDS.
 // Bound by HBM and the phases' waits: at the bench layer 68 us for 259 MB (E, R, x
 // and g; the halves' second reads are the L2's), the matrix units busy for a
-// quarter of it.  Two registers sets for F, so that it is loaded a multiplication
+// quarter of it.  Two register sets for F, so that it is loaded a multiplication
 // earlier, take 72 us (gated bf16 at state 128, where they spill: 641 against 599
 // us of the whole); 32 states a workgroup, which read x and g twice as often, 78
 // us; all rows in one workgroup of 512 threads 67 us, and 23.5 against 14.1 us
