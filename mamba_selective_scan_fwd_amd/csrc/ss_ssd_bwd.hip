@@ -236,8 +236,14 @@ __device__ __forceinline__ void state_role(const SsdBwdParams& p, int place, int
   for (int i = 0; i < UP; ++i) uv[i] = plane_view(R ? p.gp[i] : p.xp[i % 2], q.row0, urow, h0 * kP, q.rows);
 #pragma unroll
   for (int i = 0; i < VP; ++i) vv[i] = plane_view(R ? p.cp[i] : p.bp[i], q.row0, vrow, g * N, q.rows);
-  chunk_states<IO, N, HB, UP, VP, false>(lds, uv, urow, vv, vrow, q.rows, heads,
-                                         (R ? p.ws_R : p.ws_E) + ((int64_t)place * p.nheads + h0) * (kP * N));
+  float* const base = R ? p.ws_R : p.ws_E;
+  const int nheads = p.nheads;
+  chunk_states<IO, N, HB, UP, VP, false>(
+      lds, uv, urow, vv, vrow, q.rows, heads, [=](int hb, int at, const f32x4 (&v)[N / 32]) {
+        float* out = base + ((int64_t)place * nheads + h0 + hb) * (kP * N) + at;
+#pragma unroll
+        for (int t = 0; t < N / 32; ++t) *reinterpret_cast<f32x4*>(out + 16 * t) = v[t];
+      });
 }
 
 // C B^T (REV false: rows i of C, columns j of B up to the row's piece) or B C^T

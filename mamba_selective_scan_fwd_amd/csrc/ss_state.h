@@ -27,6 +27,7 @@ template <int N, int HB, int UP, int VP, bool SPLIT>
 struct StateLds {
   float w[HB][256];
   float wave[2][4];
+  float decay[HB];
   int first[4], count[4];
   __attribute__((aligned(16))) uint16_t u[2][3][kStatePiece * 64];
   __attribute__((aligned(16))) uint16_t v[SPLIT ? 2 : VP][N / 32][kStatePiece * 32];
@@ -35,11 +36,12 @@ struct StateLds {
 // uv, vv: views of the planes from the chunk's first row on (rows past it read as
 // zeros); the heads' columns start 64 channels apart.  w (LDS) is 0 for rows
 // past the chunk and for the heads past `heads`, which are worked on (what their
-// columns hold, or zeros, times 0) and not stored.  out: the first head's (64, N), the next 64 * N on.
-template <int IO, int N, int HB, int UP, int VP, bool SPLIT>
+// columns hold, or zeros, times 0) and not stored.  store(hb, at, v) takes NT
+// pieces of 4 elements of head hb's (64, N) at at, at + 16 ..
+template <int IO, int N, int HB, int UP, int VP, bool SPLIT, class Store>
 __device__ __forceinline__ void chunk_states(StateLds<N, HB, UP, VP, SPLIT>& lds, const __amdgpu_buffer_rsrc_t (&uv)[UP],
                                              int64_t urow, const __amdgpu_buffer_rsrc_t (&vv)[VP], int64_t vrow,
-                                             int rows, int heads, float* out) {
+                                             int rows, int heads, Store store) {
   constexpr int NT = N / 32;  // state tiles of a wave
   constexpr int kV = SPLIT ? 2 : VP, kVItems = kStatePiece * N / 8, kVPer = (kVItems + kStateThreads - 1) / kStateThreads;
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, pt = wave % 4, nh = wave / 4;
@@ -161,11 +163,7 @@ __device__ __forceinline__ void chunk_states(StateLds<N, HB, UP, VP, SPLIT>& lds
   }
 #pragma unroll
   for (int hb = 0; hb < HB; ++hb)
-    if (hb < heads) {
-      float* o = out + (int64_t)hb * (64 * N) + (16 * pt + lane % 16) * N + 16 * NT * nh + 4 * (lane / 16);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(o + 16 * t) = acc[hb][t];
-    }
+    if (hb < heads) store(hb, (16 * pt + lane % 16) * N + 16 * NT * nh + 4 * (lane / 16), acc[hb]);
 }
 
 // Heads per workgroup: of 1, 2 and 3 the one for which the workgroups' rounds

@@ -214,6 +214,52 @@ def test_ssd_prompt_long_among_short(io):
         _ssd_check(q, 2, 1, 32, y, state)
 
 
+@pytest.mark.parametrize("lens", [[256], [255, 1], [0, 100, 0], [256, 257, 0, 1], [0, 0]])
+def test_ssd_prompt_one_chunk_or_none(lens):
+    """Prompts of one chunk, of none and of two, carried and not, with and without a slot: the states in the slots
+    and every output, and the slots that no prompt names stay as they were."""
+    ss = _ss()
+    H, G, N = 3, 1, 64
+    q = _ssd_problem(lens, H, G, N, "bf16", seed=41 + len(lens) + lens[0])
+    T = max(sum(lens), 1)
+    if sum(lens) == 0:                                   # a row of no prompt
+        q = _ssd_problem([1], H, G, N, "bf16", seed=40)
+        q["cu"] = torch.zeros(len(lens) + 1, dtype=torch.int32)
+    S = len(lens)
+    g = {k: v.cuda() for k, v in q.items()}
+    g.update(zip(("x", "Bm", "Cm"), _parts(g["row"], H, G, N)))
+    pool = torch.randn(2 * S + 2, H, 64, N, generator=torch.Generator().manual_seed(5)).cuda()
+    for use in (True, False):
+        slots = torch.tensor([2 * k + 1 if k != 1 else -1 for k in range(S)], dtype=torch.int32, device="cuda")
+        has = torch.full((S,), int(use), dtype=torch.int32, device="cuda")
+        state = pool.clone()
+        y = torch.zeros(T, H, 64, dtype=torch.bfloat16, device="cuda")
+        ss.ssd_prompt(g["x"], g["dt"], g["A"], g["Bm"], g["Cm"], g["cu"], state, D=g.get("D"), z=g.get("z"),
+                      dt_bias=g["bias"], slots=slots, has_state=has, y=y)
+        torch.cuda.synchronize()
+        at = 0
+        for k, n in enumerate(lens):
+            slot = int(slots[k])
+            if n:                                        # the same prompt alone, in a pool of its own
+                one = pool[slot:slot + 1].clone() if slot >= 0 and use else torch.zeros_like(pool[:1])
+                cut = lambda v: g[v][at:at + n].contiguous() if v in g else None
+                yk = torch.zeros(n, H, 64, dtype=torch.bfloat16, device="cuda")
+                ss.ssd_prompt(cut("x"), cut("dt"), g["A"], cut("Bm"), cut("Cm"),
+                              torch.tensor([0, n], dtype=torch.int32, device="cuda"), one, D=g.get("D"), z=cut("z"),
+                              dt_bias=g["bias"], has_state=torch.ones(1, dtype=torch.int32, device="cuda"),
+                              y=yk)
+                assert torch.equal(y[at:at + n], yk), (k, n)
+                if slot >= 0:
+                    assert torch.equal(state[slot], one[0]), (k, n)
+            elif slot >= 0:
+                assert torch.equal(state[slot], pool[slot] if use else torch.zeros_like(pool[slot])), k
+            at += n
+        named = {int(v) for v in slots if v >= 0}
+        for k in range(pool.shape[0]):
+            if k not in named:
+                assert torch.equal(state[k], pool[k])
+
+
 def test_ssd_prompt_strong_and_no_decay():
     """Steps that forget everything (the weights underflow) and steps that change nothing (Delta = 0)."""
     ss = _ss()
