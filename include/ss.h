@@ -304,7 +304,8 @@ ss_status ss_conv1d_step(const ss_conv_problem *p, const void *x_t, const float 
  *   dconv_init  : optional (batch, dim, W-1) fp32 output, the gradient w.r.t.
  *                 the inputs before t = 0 (also where conv_init is NULL)
  *   workspace   : ss_conv1d_bwd_workspace_size() bytes (NULL when that is 0);
- *                 its contents on entry do not matter
+ *                 its contents on entry do not matter; calls that share one
+ *                 must be ordered by the caller
  * Every output is overwritten; sums have a fixed order.  Returns
  * SS_ERR_NULL_ARG when dbias and bias are not given together,
  * SS_ERR_UNSUPPORTED when the workspace is missing or too small or when an
@@ -385,7 +386,8 @@ ss_status ss_ssd_fwd(const ss_ssd_problem *p, const void *x, const void *dt, con
  *   dh0     : optional (batch, nheads, 64, dstate) fp32 output, the gradient
  *             w.r.t. the initial state (also where h0 is NULL)
  *   workspace : ss_ssd_bwd_workspace_size(p, z is given) bytes; its contents on
- *             entry do not matter
+ *             entry do not matter; calls that share one must be ordered by the
+ *             caller
  * dz is given iff z is, dD iff D, ddt_bias iff dt_bias (SS_ERR_NULL_ARG).
  * Every output is overwritten; sums have a fixed order.  Computed operands are
  * multiplied as sums of bf16 parts and states kept in fp32, so that

@@ -72,6 +72,29 @@ def test_conv_prompt(io, dim, wide):
     _conv_check(q, out, g["state"], fill=7.0)       # rows of no sequence stay as they were
 
 
+@pytest.mark.parametrize("io", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("start,wide", [(1, 9), (2, 8), (3, 12), (0, 1)])
+def test_conv_prompt_rows_at_any_element(io, start, wide):
+    """Rows that begin and lie at odd elements give what whole rows give, bit for bit, and nothing beside them is
+    written."""
+    ss = _ss()
+    q = _conv_problem([20, 0, 3, 40], 66, 4, io, seed=start)
+    g = {k: v.cuda() for k, v in q.items()}
+    T = q["x"].shape[0]
+    args = (g["w"], g["cu"])
+    kw = dict(bias=g["b"], slots=g["slots"], has_state=g["has"])
+    a, b = g["state"].clone(), g["state"].clone()
+    want = ss.conv1d_prompt(g["x"].contiguous(), *args, a, **kw)
+    src = torch.full((T, 66 + wide), 7.0, dtype=DT[io], device="cuda")
+    src[:, start:start + 66] = g["x"]
+    dst = torch.full((T, 66 + wide), 5.0, dtype=DT[io], device="cuda")
+    ss.conv1d_prompt(src[:, start:start + 66], *args, b, out=dst[:, start:start + 66], **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(dst[:, start:start + 66], want) and torch.equal(a, b)
+    dst[:, start:start + 66] = 5.0
+    assert bool((dst == 5.0).all())
+
+
 @pytest.mark.parametrize("W", [1, 2, 3, 4])
 def test_conv_prompt_options(W):
     ss = _ss()
