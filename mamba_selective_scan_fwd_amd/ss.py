@@ -727,11 +727,11 @@ def conv1d_bwd(x, w, dout, bias=None, silu=True, seq_idx=None, conv_init=None, d
         w = w.reshape(Dd, W)
     if not x.is_contiguous():
         x = x.contiguous()
-    g = {"dx": torch.empty_like(x), "dw": torch.empty((Dd, W), dtype=f32, device=x.device)}
+    g = {"dx": torch.empty_like(x), "dw": _like(w)}
     if bias is not None:
-        g["dbias"] = torch.empty((Dd,), dtype=f32, device=x.device)
+        g["dbias"] = _like(bias)
     if want_dconv_init:
-        g["dconv_init"] = torch.empty(win, dtype=f32, device=x.device)
+        g["dconv_init"] = _like(conv_init) if conv_init is not None else x.new_empty(win, dtype=f32)
     pr, wsz = _problem(ss_conv_problem, "ss_conv1d_bwd_workspace_size", (), Bsz, Dd, L, W, _IO[io], 1 if silu else 0, 0)
     if wsz:
         workspace, wa, wsz = _scratch(workspace, wsz, dev)
@@ -771,20 +771,24 @@ def ssd_bwd(x, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, dt_softplus=True
             _in(z, io, "z", xs, dev, keep), _in(dt_bias, f32, "dt_bias", vs, dev, keep),
             _in(seq_idx, torch.int32, "seq_idx", (Bsz, L), dev, keep), _in(h0, f32, "h0", hs, dev, keep),
             _in(dy, io, "dy", xs, dev, keep), _in(dfinal, f32, "dfinal", hs, dev, keep)]
-    new = (lambda shape, dtype: torch.empty(shape, dtype=dtype, device=_DEVICES[dev]))
-    g = {"dx": new(xs, io), "ddt": new((Bsz, L, Hn), io), "dA": new(vs, f32), "dB": new(bs, io), "dC": new(bs, io)}
+    g = {"dx": _like(x), "ddt": _like(dt), "dA": _like(A), "dB": _like(Bm), "dC": _like(Cm)}
     if D is not None:
-        g["dD"] = new(vs, f32)
+        g["dD"] = _like(D)
     if z is not None:
-        g["dz"] = new(xs, io)
+        g["dz"] = _like(z)
     if dt_bias is not None:
-        g["ddt_bias"] = new(vs, f32)
+        g["ddt_bias"] = _like(dt_bias)
     if want_dh0:
-        g["dh0"] = new(hs, f32)
+        g["dh0"] = _like(h0) if h0 is not None else x.new_empty(hs, dtype=f32)
     workspace, wa, wsz = _scratch(workspace, wsz, dev)
     _launch(dev, lib.ss_ssd_bwd, pr, *args, *(_ptr_of(g, k) for k in ("dx", "ddt", "dA", "dB", "dC", "dD", "dz",
                                                                      "ddt_bias", "dh0")), wa, wsz)
     return g
+
+
+def _like(t):
+    """A contiguous tensor of t's shape, type and device, for its gradient."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 def _ptr_of(g, name):
