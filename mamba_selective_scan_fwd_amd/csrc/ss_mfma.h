@@ -8,6 +8,7 @@
 #pragma once
 
 #include "ss_device.h"
+#include "ss_view.h"
 
 namespace ss {
 
@@ -166,10 +167,11 @@ __device__ __forceinline__ void split8(u32x4v w, u32x4v& hi, u32x4v& lo) {
 __device__ __forceinline__ bf16x8 bfv(u32x4v w) { return as_vec<SS_BF16>(w); }
 
 // The rows of a chunk of an operand: `at` points at its first row's columns
-// (wave-uniform), rows are `row` bytes apart, and rows from `rows` on read as
-// zeros through the range check.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_view(const void* at, int64_t row, int rows) {
-  return make_rsrc(at, at ? (uint32_t)(rows * row) : 0u);
+// (wave-uniform), `cols` bytes a row, rows are `row` bytes apart; rows from
+// `rows` on, and in the last one what follows its columns, read as zeros
+// through the range check.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_view(const void* at, int64_t row, int rows, int64_t cols) {
+  return make_rsrc(at, at ? view_bytes(row, rows, cols) : 0u);
 }
 
 // C B^T tiles in operand order: element (i, j) of row tile it = i / 16 and

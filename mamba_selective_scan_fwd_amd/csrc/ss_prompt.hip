@@ -98,9 +98,9 @@ __device__ __forceinline__ void state_role(const SsdPromptParams& p, int place, 
   }
   const int64_t xrow = p.x_stride, brow = p.b_stride;
   const __amdgpu_buffer_rsrc_t xv[1] = {
-      rows_view(static_cast<const char*>(p.x) + (row0 * xrow + h0 * kP) * 2, xrow * 2, rows)};
+      rows_view(static_cast<const char*>(p.x) + (row0 * xrow + h0 * kP) * 2, xrow * 2, rows, heads * (kP * 2))};
   const __amdgpu_buffer_rsrc_t bv[1] = {
-      rows_view(static_cast<const char*>(p.Bm) + (row0 * brow + g * N) * 2, brow * 2, rows)};
+      rows_view(static_cast<const char*>(p.Bm) + (row0 * brow + g * N) * 2, brow * 2, rows, N * 2)};
   float* ws = p.ws_state + ((int64_t)place * p.nheads + h0) * (kP * N);
   chunk_states<IO, N, HB, 1, 1, IO == SS_F16>(
       lds, xv, xrow, bv, brow, rows, heads, [&](int hb, int at, const f32x4 (&S)[N / 32]) {
@@ -140,8 +140,8 @@ __device__ __forceinline__ void cb_role(const SsdPromptParams& p, int place, int
   if (16 * it >= rows) return;
   const int64_t row0 = q.begin + (int64_t)q.chunk * kQ;
   const int64_t brow = p.b_stride * 2, crow = p.c_stride * 2;
-  const auto bv = rows_view(static_cast<const char*>(p.Bm) + row0 * brow + g * N * 2, brow, rows);
-  const auto cv = rows_view(static_cast<const char*>(p.Cm) + row0 * crow + g * N * 2, crow, rows);
+  const auto bv = rows_view(static_cast<const char*>(p.Bm) + row0 * brow + g * N * 2, brow, rows, N * 2);
+  const auto cv = rows_view(static_cast<const char*>(p.Cm) + row0 * crow + g * N * 2, crow, rows, N * 2);
   u32x4v c[N / 32];
 #pragma unroll
   for (int ks = 0; ks < N / 32; ++ks)
@@ -289,9 +289,9 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
   const int ir[2] = {32 * blk[0] + 16 * half, 32 * blk[1] + 16 * half};  // first row of each block
 
   // ---- prologue: every operand's load, then the sums, then LDS
-  const auto dv = rows_view(static_cast<const char*>(p.dt) + (row0 * p.dt_stride + h) * 2, p.dt_stride * 2, rows);
+  const auto dv = rows_view(static_cast<const char*>(p.dt) + (row0 * p.dt_stride + h) * 2, p.dt_stride * 2, rows, 2);
   const raw_t<IO> dr = bload<IO>(dv, tid < kQ ? (uint32_t)(tid * p.dt_stride * 2) : kOffNone);
-  const auto xv = rows_view(static_cast<const char*>(p.x) + row0 * xrow + h * kP * 2, xrow, rows);
+  const auto xv = rows_view(static_cast<const char*>(p.x) + row0 * xrow + h * kP * 2, xrow, rows, kP * 2);
   u32x4v xr[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) xr[k] = vload16(xv, (uint32_t)((tid / 8 + 64 * k) * xrow + (tid % 8) * 16));
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
   f32x4 er[N / 32];
 #pragma unroll
   for (int k = 0; k < N / 32; ++k) er[k] = E[tid + kScanThreads * k];
-  const auto cv = rows_view(static_cast<const char*>(p.Cm) + row0 * crow + g * N * 2, crow, rows);
+  const auto cv = rows_view(static_cast<const char*>(p.Cm) + row0 * crow + g * N * 2, crow, rows, N * 2);
   u32x4v cf[2][N / 32];
 #pragma unroll
   for (int b = 0; b < 2; ++b)
@@ -396,9 +396,10 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
 
   // ---- Y_diag += x^T M^T, piece by piece
   const auto cbv = make_rsrc(p.ws_cb + ((int64_t)place * p.ngroups + g) * (kQ * kQ), kQ * kQ * 4);
-  const auto yv = rows_view(static_cast<char*>(p.y) + (row0 * p.nheads + h) * (kP * 2), (int64_t)p.nheads * (kP * 2), rows);
+  const auto yv = rows_view(static_cast<char*>(p.y) + (row0 * p.nheads + h) * (kP * 2), (int64_t)p.nheads * (kP * 2), rows,
+                            kP * 2);
   const auto zv = rows_view(p.z ? static_cast<const char*>(p.z) + row0 * p.z_stride * 2 + h * kP * 2 : nullptr,
-                            p.z_stride * 2, rows);
+                            p.z_stride * 2, rows, kP * 2);
   const float Dh = p.D ? p.D[h] : 0.0f;
 #pragma unroll
   for (int b = 0; b < 2; ++b) {

@@ -79,10 +79,10 @@ __device__ __forceinline__ Chunk chunk_of(const SsdBwdParams& p, int place) {
   q.row0 = b * p.seqlen + (int64_t)c * kQ;
   return q;
 }
-// a plane's view from a chunk's first row on
+// a view of `cols` columns of a plane, from a chunk's first row on
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t plane_view(const uint16_t* at, int64_t row0, int64_t row, int col,
-                                                             int rows) {
-  return rows_view(at ? at + row0 * row + col : nullptr, row * 2, rows);
+                                                             int cols, int rows) {
+  return rows_view(at ? at + row0 * row + col : nullptr, row * 2, rows, cols * 2);
 }
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -233,9 +233,9 @@ __device__ __forceinline__ void state_role(const SsdBwdParams& p, int place, int
   const int64_t urow = (int64_t)p.nheads * kP, vrow = (int64_t)p.ngroups * N;
   __amdgpu_buffer_rsrc_t uv[UP], vv[VP];
 #pragma unroll
-  for (int i = 0; i < UP; ++i) uv[i] = plane_view(R ? p.gp[i] : p.xp[i % 2], q.row0, urow, h0 * kP, q.rows);
+  for (int i = 0; i < UP; ++i) uv[i] = plane_view(R ? p.gp[i] : p.xp[i % 2], q.row0, urow, h0 * kP, heads * kP, q.rows);
 #pragma unroll
-  for (int i = 0; i < VP; ++i) vv[i] = plane_view(R ? p.cp[i] : p.bp[i], q.row0, vrow, g * N, q.rows);
+  for (int i = 0; i < VP; ++i) vv[i] = plane_view(R ? p.cp[i] : p.bp[i], q.row0, vrow, g * N, N, q.rows);
   float* const base = R ? p.ws_R : p.ws_E;
   const int nheads = p.nheads;
   chunk_states<IO, N, HB, UP, VP, false>(
@@ -257,8 +257,8 @@ __device__ __forceinline__ void cb_role(const SsdBwdParams& p, int place, int g,
   const int it = 8 * half + wave, piece = it / 4;
   if (16 * it >= q.rows) return;
   const int64_t row = (int64_t)p.ngroups * N;
-  const auto bv = plane_view(static_cast<const uint16_t*>(REV ? p.Cm : p.Bm), q.row0, row, g * N, q.rows);
-  const auto cv = plane_view(static_cast<const uint16_t*>(REV ? p.Bm : p.Cm), q.row0, row, g * N, q.rows);
+  const auto bv = plane_view(static_cast<const uint16_t*>(REV ? p.Cm : p.Bm), q.row0, row, g * N, N, q.rows);
+  const auto cv = plane_view(static_cast<const uint16_t*>(REV ? p.Bm : p.Cm), q.row0, row, g * N, N, q.rows);
   u32x4v c[N / 32];
 #pragma unroll
   for (int ks = 0; ks < N / 32; ++ks)
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) bwd_scan_kernel(SsdBwdParams 
   u32x4v ur[UP][4];
 #pragma unroll
   for (int i = 0; i < UP; ++i) {
-    const auto uv = plane_view(rev ? p.gp[i] : i < data_parts<MODE>() ? p.xp[i] : nullptr, q.row0, xrow, h * kP, rows);
+    const auto uv = plane_view(rev ? p.gp[i] : i < data_parts<MODE>() ? p.xp[i] : nullptr, q.row0, xrow, h * kP, kP, rows);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       ur[i][k] = vload16(uv, (uint32_t)((tid / 8 + 64 * k) * xrow * 2 + (tid % 8) * 16));
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) bwd_scan_kernel(SsdBwdParams 
   u32x4v vf[VP][2][N / 32];
 #pragma unroll
   for (int i = 0; i < VP; ++i) {
-    const auto vv = plane_view(rev ? p.bp[i] : p.cp[i], q.row0, vrow, g * N, rows);
+    const auto vv = plane_view(rev ? p.bp[i] : p.cp[i], q.row0, vrow, g * N, N, rows);
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -697,8 +697,8 @@ __device__ __forceinline__ void pair_role(const SsdBwdParams& p, const Chunk& q,
   // C_i . B_j, the same for every head
   f32x4 cb[4];
   {
-    const auto bv = plane_view(static_cast<const uint16_t*>(p.Bm), q.row0, vrow, g * N, rows);
-    const auto cv = plane_view(static_cast<const uint16_t*>(p.Cm), q.row0, vrow, g * N, rows);
+    const auto bv = plane_view(static_cast<const uint16_t*>(p.Bm), q.row0, vrow, g * N, N, rows);
+    const auto cv = plane_view(static_cast<const uint16_t*>(p.Cm), q.row0, vrow, g * N, N, rows);
 #pragma unroll
     for (int t = 0; t < 4; ++t) cb[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -742,7 +742,7 @@ __device__ __forceinline__ void pair_role(const SsdBwdParams& p, const Chunk& q,
     const int64_t at = ((int64_t)q.place * p.nheads + h) * kQ;
 #pragma unroll
     for (int i = 0; i < XP; ++i) {
-      const auto xv = plane_view(p.xp[i], q.row0, xrow, h * kP, rows);
+      const auto xv = plane_view(p.xp[i], q.row0, xrow, h * kP, kP, rows);
 #pragma unroll
       for (int k = 0; k < 2; ++k)
         xr[i][k] = vload16(xv, (uint32_t)((kJB * jb + tid / 8 + 32 * k) * xrow * 2 + (tid % 8) * 16));
@@ -760,7 +760,7 @@ __device__ __forceinline__ void pair_role(const SsdBwdParams& p, const Chunk& q,
   auto load_g = [&](int u, int h) {
 #pragma unroll
     for (int i = 0; i < GP; ++i) {
-      const auto gv = plane_view(p.gp[i], q.row0, xrow, h * kP, rows);
+      const auto gv = plane_view(p.gp[i], q.row0, xrow, h * kP, kP, rows);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) gf[u][i][ks] = vload16(gv, (uint32_t)(il * xrow * 2 + (32 * ks + 8 * quad) * 2));
     }
@@ -993,7 +993,7 @@ __device__ __forceinline__ void out_role(const SsdBwdParams& p, int lb, uint16_t
   const int hpg = p.nheads / p.ngroups;
   const int64_t xrow = (int64_t)p.nheads * kP, vrow = (int64_t)p.ngroups * N;
   const int fr[2] = {f0 + 32 * wave + l16, f0 + 32 * wave + 16 + l16};  // this lane's rows
-  const auto vv = plane_view(static_cast<const uint16_t*>(DB ? p.Bm : p.Cm), q.row0, vrow, g * N, rows);
+  const auto vv = plane_view(static_cast<const uint16_t*>(DB ? p.Bm : p.Cm), q.row0, vrow, g * N, N, rows);
   uint2 vn[2][NT];
 #pragma unroll
   for (int b = 0; b < 2; ++b)
@@ -1020,7 +1020,7 @@ __device__ __forceinline__ void out_role(const SsdBwdParams& p, int lb, uint16_t
   auto load_f = [&](int h) {
 #pragma unroll
     for (int i = 0; i < FP; ++i) {
-      const auto fv = plane_view(DB ? p.xp[i % 2] : p.gp[i], q.row0, xrow, h * kP, rows);
+      const auto fv = plane_view(DB ? p.xp[i % 2] : p.gp[i], q.row0, xrow, h * kP, kP, rows);
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -1110,7 +1110,7 @@ __device__ __forceinline__ void out_role(const SsdBwdParams& p, int lb, uint16_t
   // ---- sum_s S_fs u_s
   __amdgpu_buffer_rsrc_t up[UP];
 #pragma unroll
-  for (int i = 0; i < UP; ++i) up[i] = plane_view(DB ? p.cp[i] : p.bp[i], q.row0, vrow, g * N + n0, rows);
+  for (int i = 0; i < UP; ++i) up[i] = plane_view(DB ? p.cp[i] : p.bp[i], q.row0, vrow, g * N + n0, NH, rows);
   const uint32_t* Sw = p.ws_S + ((int64_t)q.place * p.ngroups + g) * kPairs * (2 * kJB * kJB);
   const int fb = 2 * upper + wave / 2;  // the piece that holds this wave's rows
   const int lastp = (rows - 1) / kJB, fend = 2 * upper + 1 < lastp ? 2 * upper + 1 : lastp;

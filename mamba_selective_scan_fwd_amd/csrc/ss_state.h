@@ -34,9 +34,11 @@ struct StateLds {
 };
 
 // uv, vv: views of the planes from the chunk's first row on (rows past it read as
-// zeros); the heads' columns start 64 channels apart.  w (LDS) is 0 for rows
-// past the chunk and for the heads past `heads`, which are worked on (what their
-// columns hold, or zeros, times 0) and not stored.  store(hb, at, v) takes NT
+// zeros); the heads' columns start 64 channels apart.  uv ends with the columns of
+// the last of `heads` in the last row.  Heads past `heads` are worked on and not
+// stored: w (LDS) is 0 for them, as for rows past the chunk, and their u is what
+// follows in the same plane, the next row's columns, or zeros behind the view's
+// end.  store(hb, at, v) takes NT
 // pieces of 4 elements of head hb's (64, N) at at, at + 16 ..
 template <int IO, int N, int HB, int UP, int VP, bool SPLIT, class Store>
 __device__ __forceinline__ void chunk_states(StateLds<N, HB, UP, VP, SPLIT>& lds, const __amdgpu_buffer_rsrc_t (&uv)[UP],
