@@ -9,7 +9,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libss.so")
 SOURCES = ["ss_fwd.hip", "ss_bwd.hip", "ss_conv.hip", "ss_conv_bwd.hip", "ss_ssd.hip", "ss_ssd_bwd.hip", "ss_prompt.hip",
            "ss_serve.hip", "ss_probe.hip", "ss_noalloc.hip", "ss_abi.cpp"]
-HEADERS = ["ss_device.h", "ss_internal.h", "ss_mfma.h", "ss_packed.h", "ss_state.h",
+HEADERS = ["ss_device.h", "ss_internal.h", "ss_mfma.h", "ss_packed.h", "ss_plan.h", "ss_state.h",
            "ss_view.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

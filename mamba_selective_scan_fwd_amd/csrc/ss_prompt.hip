@@ -232,15 +232,6 @@ __global__ void __launch_bounds__(256) prompt_pass_kernel(SsdPromptParams p) {
   if (slot >= 0) *state = E;
 }
 
-// Sixteen chunks ahead where a few long prompts leave the CUs few workgroups:
-// one prompt of 32769 tokens, 24 heads, state 64 (96 workgroups, 129 chunks)
-// takes 20.9 us with 16 against 46.3 us with 4 (4.9 and 2.2 TB/s), while 24
-// ragged prompts of 16384 tokens, state 128 (4608 workgroups) take 31.8 us
-// against 24.6 us: there the loads behind a prompt's end are what is left.
-bool pass_deep(int64_t workgroups, int64_t chunks, int64_t nseqs) {
-  return workgroups <= 4 * (int64_t)device_cus() && chunks >= 8 * nseqs;
-}
-
 // ---- pass 3: outputs of a chunk ------------------------------------------------------
 // Workgroup = (chunk, head), 512 threads.  Y is built transposed, Y^T[p][i], so
 // that a lane ends with 4 consecutive channels of one step i.  The chunk's 256
@@ -530,7 +521,7 @@ hipError_t launch_prompt_n(const SsdPromptParams& p, hipStream_t st) {
   // 15.6 us without the launch, 17.9 us with it
   const uint32_t pass = p.tokens <= kQ ? 0 : (uint32_t)p.nseqs * heads * (kP * N / 1024);
   if (pass == 0) {
-  } else if (pass_deep(pass, p.chunks, p.nseqs))
+  } else if (pass_ahead(pass, p.chunks, p.nseqs, device_cus()) == 16)
     hipLaunchKernelGGL((prompt_pass_kernel<N, 16>), dim3(pass), dim3(256), 0, st, p);
   else
     hipLaunchKernelGGL((prompt_pass_kernel<N, 4>), dim3(pass), dim3(256), 0, st, p);

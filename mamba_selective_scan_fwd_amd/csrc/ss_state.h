@@ -15,6 +15,7 @@
 #pragma once
 
 #include "ss_mfma.h"
+#include "ss_plan.h"
 
 namespace ss {
 
@@ -166,26 +167,6 @@ __device__ __forceinline__ void chunk_states(StateLds<N, HB, UP, VP, SPLIT>& lds
 #pragma unroll
   for (int hb = 0; hb < HB; ++hb)
     if (hb < heads) store(hb, (16 * pt + lane % 16) * N + 16 * NT * nh + 4 * (lane / 16), acc[hb]);
-}
-
-// Heads per workgroup: of 1, 2 and 3 the one for which the workgroups' rounds
-// over 2 per CU take the least time, a workgroup's being its heads and two
-// heads' worth of its own (the weights, V, the first loads).  With 1, 2 and 3: 24
-// ragged prompts of 16384 tokens, 24 heads, state 128: 60, 50, 50 us; five prompts
-// of 131 tokens: 6.7, 8.4, 10.7 us; one of 32769 tokens, state 64, fp16: 83, 68,
-// 68 us (4 spills registers at state 128: 66 us for the first).
-inline int state_heads(int64_t chunk_groups, int64_t heads_per_group, int64_t cus) {
-  int best = 1;
-  int64_t cost = -1;
-  for (int hb = 1; hb <= 3; ++hb) {
-    const int64_t wgs = chunk_groups * ((heads_per_group + hb - 1) / hb);
-    const int64_t c = (wgs + 2 * cus - 1) / (2 * cus) * (hb + 2);
-    if (cost < 0 || c <= cost) {
-      cost = c;
-      best = hb;
-    }
-  }
-  return best;
 }
 
 }  // namespace ss
