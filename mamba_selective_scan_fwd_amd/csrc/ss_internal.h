@@ -215,12 +215,12 @@ struct SsdBwdParams {
   float* ws_bc;              // B C^T in operand order
   // (places, nheads, 256) each:
   float* ws_delta;           // Delta
-  float* ws_cs;              // Delta A summed from the start of each 64 steps,
-  float* ws_cl;              // and what that float leaves of the sum
-  float* ws_from;            // exp(that sum),
-  float* ws_to;              // exp(the sum behind a step to the end of its 64)
-  float* ws_wc;              // exp(the sum from the chunk's start), 0 from the first document start on
-  float* ws_wb;              // exp(the sum to the chunk's end), 0 before the last one
+  float* ws_cs;              // log2 of the decay from the start of each 64 steps (sums of Delta A),
+  float* ws_cl;              // and what that float leaves of it
+  float* ws_from;            // that decay,
+  float* ws_to;              // the decay behind a step to the end of its 64,
+  float* ws_wc;              // the decay from the chunk's start, 0 from the first document start on,
+  float* ws_wb;              // and to the chunk's end, 0 before the last one
   float* ws_xd;              // x . g
   float* ws_e;               // (2, places, nheads, 256), per half of the states: e
   float* ws_r;               // and r, without Delta

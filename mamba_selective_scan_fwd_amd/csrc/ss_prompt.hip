@@ -239,16 +239,17 @@ __global__ void __launch_bounds__(256) prompt_pass_kernel(SsdPromptParams p) {
 // blocks w and 7 - w, so that every wave does the same causal work:
 //   Y^T = E C^T scaled by exp(cs_i)  +  x^T M^T,
 // M[i][j] = CB[i][j] exp(cs_i - cs_j) Delta_j for j <= i, built in registers.
-// cs is kept as its sum inside a piece of 64 steps (sCs) and the sums over
-// whole pieces (sTot): pairs inside a piece take a difference of the former, a
+// cs is kept as its sum inside a piece of 64 steps (sCs; what the float leaves goes
+// into sRow and the columns' factors) and the sums over whole pieces (sTot), in
+// powers of two: pairs inside a piece take a difference of the former, a
 // pair across pieces two factors, exp(cs_i - end of j's piece) and
 // exp(end of j's piece - cs_j), one exp per row and one per column.  fp16's lo
 // part of x takes E's place once E C^T is done, so that two workgroups share a
 // CU (one prompt of 32769 tokens: 122 us, 137 us with one).  C B^T and y go
 // through range-checked views, whose addresses take one register, and the gate
-// is loaded in the place of a next piece behind the last: nothing is spilled at
-// two workgroups to a CU (88 and 115 us; 94 and 122 us with 8 and 12 registers
-// spilled, whose stores went to HBM).  Of the 88 us, the loads, E's staging and
+// is loaded in the place of a next piece behind the last: at two workgroups to a
+// CU nothing is spilled, but 4 registers of bf16 at states below 128 (88 and 118 us;
+// 94 and 122 us with 8 and 12 registers spilled, whose stores went to HBM).  Of the 88 us, the loads, E's staging and
 // the stores alone take about 52, near what their 230 MB need, and the products
 // do not hide behind them.  Several heads one after the other in a workgroup,
 // the next one's loads ahead, leave one workgroup to a CU and take longer (24
@@ -258,8 +259,9 @@ template <int IO, int N>
 __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptParams p) {
   constexpr bool kTwo = IO == SS_F16;  // x and C need a lo part
   constexpr int kHS = N + 8;           // row stride of E in LDS: 16 rows' fragments in different banks
-  __shared__ __attribute__((aligned(16))) float sDelta[kQ];
-  __shared__ __attribute__((aligned(16))) float sCs[kQ];   // Delta A summed from the piece's first step
+  __shared__ __attribute__((aligned(16))) float sCs[kQ];   // log2 of the decay from the piece's first step,
+  __shared__ float sRow[kQ];                               // 2^lo, lo what that float leaves of it (step_log2),
+  __shared__ __attribute__((aligned(16))) float sOwn[kQ];  // and 2^-lo_j Delta_j
   __shared__ __attribute__((aligned(16))) float sWp[kQ];   // exp(piece's end - cs_j) Delta_j
   __shared__ float sTot[4];
   __shared__ __attribute__((aligned(16))) uint16_t sX0[kQ * kP];
@@ -299,17 +301,13 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
       cf[b][ks] = vload16(cv, (uint32_t)((ir[b] + lane % 16) * crow + (32 * ks + 8 * (lane / 16)) * 2));
   if (tid < kQ) {
     const float delta = tid < rows ? step_size<IO>(p, bits_f32<IO>(dr), h) : 0.0f;
-    float v = delta * p.A[h];
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const float o = __shfl_up(v, off, 64);
-      if (lane >= off) v += o;
-    }
-    const float tot = __shfl(v, 63, 64);
-    sDelta[tid] = delta;
-    sCs[tid] = v;
-    sWp[tid] = exp2_hw((tot - v) * kLog2e) * delta;
-    if (lane == 63) sTot[wave] = v;
+    const double sum = scan_up(step_log2(delta, p.A[h]));
+    const float hi = (float)sum, lo = (float)(sum - (double)hi);
+    sCs[tid] = hi;
+    sRow[tid] = exp2_hw(lo);
+    sOwn[tid] = exp2_hw(-lo) * delta;
+    sWp[tid] = exp2_hw((float)(__shfl(sum, 63, 64) - sum)) * delta;
+    if (lane == 63) sTot[wave] = hi;
   }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -372,7 +370,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     const float bf = blk[b] / 2 == 0 ? before[0] : blk[b] / 2 == 1 ? before[1] : blk[b] / 2 == 2 ? before[2] : before[3];
-    const float sc = exp2_hw((sCs[ir[b] + lane % 16] + bf) * kLog2e);
+    const float sc = exp2_hw(sCs[ir[b] + lane % 16] + bf);
 #pragma unroll
     for (int pt = 0; pt < 4; ++pt) acc[b][pt] *= sc;
   }
@@ -419,9 +417,9 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
           zr[pt] = vload8(zv, (uint32_t)(i * p.z_stride * 2 + (16 * pt + 4 * (lane / 16)) * 2));
       }
       const bool diag = piece == dpiece;
-      float between = csi;  // Delta A from the end of this piece to row i
+      float between = csi;  // log2 of the decay from the end of this piece to row i
       for (int k = piece + 1; k < dpiece; ++k) between += sTot[k];
-      const float ei = exp2_hw(between * kLog2e);
+      const float ei = exp2_hw(between);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         if (ks == 1 && diag && blk[b] % 2 == 0) continue;  // columns behind all of the block's rows
@@ -429,12 +427,11 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
         float m[8];
         if (diag) {
           const f32x4 c0 = *reinterpret_cast<const f32x4*>(&sCs[j0]), c1 = *reinterpret_cast<const f32x4*>(&sCs[j0 + 4]);
-          const f32x4 d0 = *reinterpret_cast<const f32x4*>(&sDelta[j0]),
-                      d1 = *reinterpret_cast<const f32x4*>(&sDelta[j0 + 4]);
+          const f32x4 d0 = *reinterpret_cast<const f32x4*>(&sOwn[j0]), d1 = *reinterpret_cast<const f32x4*>(&sOwn[j0 + 4]);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float csj = e < 4 ? c0[e & 3] : c1[e & 3], dj = e < 4 ? d0[e & 3] : d1[e & 3];
-            const float v = cur[ks][e / 4][e & 3] * exp2_hw((csi - csj) * kLog2e) * dj;
+            const float v = cur[ks][e / 4][e & 3] * exp2_hw(csi - csj) * dj;
             m[e] = j0 + e <= i ? v : 0.0f;
           }
         } else {
@@ -473,6 +470,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
     }
     // ---- D skip, gate, store (rows past the chunk are dropped by the range check)
     {
+      const float row = sRow[i];
 #pragma unroll
       for (int pt = 0; pt < 4; ++pt) {
         const int p0 = 16 * pt + 4 * (lane / 16);
@@ -488,7 +486,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptP
         }
         float o[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) o[r] = fmaf(Dh, x[r], acc[b][pt][r]);
+        for (int r = 0; r < 4; ++r) o[r] = fmaf(Dh, x[r], row * acc[b][pt][r]);
         if (p.z) {
           o[0] *= silu_f(low16<IO>(zr[pt].x));
           o[1] *= silu_f(high16<IO>(zr[pt].x));

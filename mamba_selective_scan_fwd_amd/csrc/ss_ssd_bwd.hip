@@ -178,18 +178,11 @@ __device__ __forceinline__ void state_role(const SsdBwdParams& p, int place, int
       delta = p.softplus ? softplus_f(xd) : xd;
     }
     const float A = mine ? p.A[h] : 0.0f;
-    // R: the sum up to this step in the wave's 64; E: from this step on.  The
-    // former's differences decide the weights of neighbouring steps, whose
-    // exponents are small where the sums are not: it is formed in 64 bits and
-    // kept as two floats.
+    // R: the sum up to this step in the wave's 64, a power of two in two floats
+    // (step_log2); E: of Delta A from this step on.
     float v = delta * A, low = 0.0f;
     if constexpr (R) {
-      double c = (double)delta * (double)A;
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const double o = __shfl_up(c, off, 64);
-        if (lane >= off) c += o;
-      }
+      const double c = scan_up(step_log2(delta, A));
       v = (float)c;
       low = (float)(c - (double)v);
     } else {
@@ -209,10 +202,10 @@ __device__ __forceinline__ void state_role(const SsdBwdParams& p, int place, int
         const float behind = (__shfl(v, 63, 64) - v) + (__shfl(low, 63, 64) - low);
         p.ws_cs[at] = v;
         p.ws_cl[at] = low;
-        p.ws_from[at] = exp2_hw(v * kLog2e);
-        p.ws_to[at] = exp2_hw(behind * kLog2e);
+        p.ws_from[at] = exp2_hw(v);
+        p.ws_to[at] = exp2_hw(behind);
         for (int k = 0; k < wave; ++k) v += sum[k];
-        w = t < first ? exp2_hw(v * kLog2e) : 0.0f;
+        w = t < first ? exp2_hw(v) : 0.0f;
         p.ws_wc[at] = w;
       } else {
         p.ws_delta[at] = delta;
@@ -399,11 +392,13 @@ __global__ void __launch_bounds__(kScanThreads, 4) bwd_scan_kernel(SsdBwdParams 
   // two parts at the most: dx and dz are rounded to 16 bits
   constexpr int UP = g_parts<MODE>() > 1 ? 2 : 1, VP = data_parts<MODE>();
   constexpr int kHS = N + 8;
-  __shared__ __attribute__((aligned(16))) float sDelta[kQ];
-  __shared__ __attribute__((aligned(16))) float sCs[kQ];   // Delta A summed from the piece's first step
-  __shared__ __attribute__((aligned(16))) float sCol[kQ];  // a source row's factor
+  __shared__ __attribute__((aligned(16))) float sCs[kQ];   // log2 of the decay from the piece's first step
+  __shared__ __attribute__((aligned(16))) float sCol[kQ];  // a source row's factor in other pieces
+  // of lo, what that float leaves of the sum (step_log2):
+  __shared__ __attribute__((aligned(16))) float sOwn[kQ];  // a source row's factor in its own piece: 2^lo, or 2^-lo Delta
+  __shared__ float sRow[kQ];                               // an out row's at the end: 2^-lo Delta, or 2^lo
   __shared__ __attribute__((aligned(16))) int sSeg[kQ];
-  __shared__ float sTot[4];
+  __shared__ float sTot[4], sTotLo[4];
   __shared__ __attribute__((aligned(16))) uint16_t u0[kQ * kP];
   __shared__ __attribute__((aligned(16))) uint16_t ku[UP > 1 && 2 * kP * kHS < kQ * kP ? kQ * kP : 2 * kP * kHS];
   uint16_t* const sU[2] = {u0, ku};
@@ -445,12 +440,17 @@ __global__ void __launch_bounds__(kScanThreads, 4) bwd_scan_kernel(SsdBwdParams 
         vf[i][b][ks] = vload16(vv, (uint32_t)((orow[b] + lane % 16) * vrow * 2 + (32 * ks + 8 * (lane / 16)) * 2));
   }
   if (tid < kQ) {
-    const float delta = p.ws_delta[ph * kQ + tid], cs = p.ws_cs[ph * kQ + tid];
-    const float tot = __shfl(cs, 63, 64);
-    sDelta[tid] = delta;
+    const float delta = p.ws_delta[ph * kQ + tid], cs = p.ws_cs[ph * kQ + tid], lo = p.ws_cl[ph * kQ + tid];
+    const float col = (rev ? p.ws_from : p.ws_to)[ph * kQ + tid];
+    const float up = exp2_hw(lo), down = exp2_hw(-lo) * delta;
     sCs[tid] = cs;
-    sCol[tid] = rev ? exp2_hw(cs * kLog2e) : exp2_hw((tot - cs) * kLog2e) * delta;
-    if (lane == 63) sTot[wave] = cs;
+    sCol[tid] = rev ? col : col * delta;
+    sOwn[tid] = rev ? up : down;
+    sRow[tid] = rev ? down : up;
+    if (lane == 63) {
+      sTot[wave] = cs;
+      sTotLo[wave] = lo;
+    }
     if (p.seq_idx) sSeg[tid] = p.ws_seg[(int64_t)q.place * kQ + tid];
   }
 #pragma unroll
@@ -493,13 +493,13 @@ __global__ void __launch_bounds__(kScanThreads, 4) bwd_scan_kernel(SsdBwdParams 
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     const int o = orow[b] + lane % 16, piece = blk[b] / 2;
-    float arg = rev ? sTot[piece] - sCs[o] : sCs[o];
+    float arg = rev ? (sTot[piece] - sCs[o]) + sTotLo[piece] : sCs[o];
     if (rev) {
       for (int k = piece + 1; k < 4; ++k) arg += sTot[k];
     } else {
       for (int k = 0; k < piece; ++k) arg += sTot[k];
     }
-    float f = exp2_hw(arg * kLog2e);
+    float f = exp2_hw(arg);
     if (p.seq_idx && sSeg[o] != (rev ? sSeg[rows - 1] : 0)) f = 0.0f;
 #pragma unroll
     for (int pt = 0; pt < 4; ++pt) acc[b][pt] *= f;
@@ -519,7 +519,8 @@ __global__ void __launch_bounds__(kScanThreads, 4) bwd_scan_kernel(SsdBwdParams 
   for (int b = 0; b < 2; ++b) {
     if (orow[b] >= rows) continue;
     const int o = orow[b] + lane % 16, piece = blk[b] / 2;
-    const float cso = sCs[o], tot = sTot[piece];
+    const float cso = sCs[o];
+    const float base = rev ? (sTot[piece] - cso) + sTotLo[piece] : cso;  // log2 of the decay from or to the piece's end
     const int sego = p.seq_idx ? sSeg[o] : 0;
     const float* cb = CB + cb_at(orow[b] / 16, 0) + lane * 8;
     const int s0 = rev ? piece : 0, s1 = rev ? lastp : piece;
@@ -536,9 +537,9 @@ __global__ void __launch_bounds__(kScanThreads, 4) bwd_scan_kernel(SsdBwdParams 
           for (int e = 0; e < 2; ++e) nxt[ks][e] = *reinterpret_cast<const f32x4*>(cb + (2 * sp + 2 + ks) * 512 + 4 * e);
       }
       const bool diag = sp == piece;
-      float arg = rev ? tot - cso : cso;  // Delta A between this row and the source piece's end towards it
+      float arg = base;  // log2 of the decay between this row and the source piece's end towards it
       for (int k = rev ? piece + 1 : sp + 1; k < (rev ? sp : piece); ++k) arg += sTot[k];
-      const float fo = exp2_hw(arg * kLog2e);
+      const float fo = exp2_hw(arg);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         // steps all behind (rev: before) the block's rows
@@ -547,13 +548,12 @@ __global__ void __launch_bounds__(kScanThreads, 4) bwd_scan_kernel(SsdBwdParams 
         float m[8];
         if (diag) {
           const f32x4 c0 = *reinterpret_cast<const f32x4*>(&sCs[s]), c1 = *reinterpret_cast<const f32x4*>(&sCs[s + 4]);
-          const f32x4 d0 = *reinterpret_cast<const f32x4*>(&sDelta[s]),
-                      d1 = *reinterpret_cast<const f32x4*>(&sDelta[s + 4]);
+          const f32x4 d0 = *reinterpret_cast<const f32x4*>(&sOwn[s]), d1 = *reinterpret_cast<const f32x4*>(&sOwn[s + 4]);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float css = e < 4 ? c0[e & 3] : c1[e & 3];
-            float v = cur[ks][e / 4][e & 3] * exp2_hw((rev ? css - cso : cso - css) * kLog2e);
-            if (!rev) v *= e < 4 ? d0[e & 3] : d1[e & 3];
+            const float v = cur[ks][e / 4][e & 3] * exp2_hw(rev ? css - cso : cso - css) *
+                            (e < 4 ? d0[e & 3] : d1[e & 3]);
             m[e] = (rev ? s + e >= o : s + e <= o) ? v : 0.0f;
           }
         } else {
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) bwd_scan_kernel(SsdBwdParams 
     }
     const int64_t out = (q.row0 + o) * xrow + h * kP;
     if (o >= rows) continue;
-    const float delta = sDelta[o];
+    const float row = sRow[o];
 #pragma unroll
     for (int pt = 0; pt < 4; ++pt) {
       const int p0 = 16 * pt + 4 * (lane / 16);
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) bwd_scan_kernel(SsdBwdParams 
       join4<UP>(uw, u);
       if (rev) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r[e] = fmaf(Dh, u[e], delta * acc[b][pt][e]);
+        for (int e = 0; e < 4; ++e) r[e] = fmaf(Dh, u[e], row * acc[b][pt][e]);
       } else {
         const uint2 zw = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.z) + out + p0);
         const uint2 dw = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.dy) + out + p0);
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) bwd_scan_kernel(SsdBwdParams 
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float sg = sigmoid_f(z[e]);
-          r[e] = dy[e] * fmaf(Dh, u[e], acc[b][pt][e]) * (sg * fmaf(z[e], 1.0f - sg, 1.0f));
+          r[e] = dy[e] * fmaf(Dh, u[e], row * acc[b][pt][e]) * (sg * fmaf(z[e], 1.0f - sg, 1.0f));
         }
       }
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(rev ? p.dx : p.dz) + out + p0) =
@@ -680,7 +680,7 @@ struct PairLds {
     float S[64 * 65];              // after the heads
   };
   __attribute__((aligned(16))) uint16_t x[2][data_parts<MODE>()][kJB * kP];
-  __attribute__((aligned(16))) float vec[2][3][kJB];  // Delta_j; the columns' factors, or their sums of Delta A
+  __attribute__((aligned(16))) float vec[2][3][kJB];  // Delta_j; the columns' factors, or their sums (step_log2)
 };
 
 template <int MODE, int N, bool DIAG>
@@ -782,7 +782,7 @@ __device__ __forceinline__ void pair_role(const SsdBwdParams& p, const Chunk& q,
         for (int k = 0; k < 2; ++k)
           *reinterpret_cast<u32x4v*>(&lds.x[turn][i][row64_off(tid / 8 + 32 * k, 8 * (tid % 8))]) = xr[i][k];
       if (uwave < (DIAG ? 3 : 2)) lds.vec[turn][wave][lane] = vr;
-      const float f = DIAG ? fn : fn * exp2_hw((mid[0] + mid[1]) * kLog2e), l = ln;
+      const float f = DIAG ? fn : fn * exp2_hw(mid[0] + mid[1]), l = ln;
       if (h + 1 < hend) {
         load_x(h + 1);
         load_g(1 - turn, h + 1);
@@ -814,7 +814,7 @@ __device__ __forceinline__ void pair_role(const SsdBwdParams& p, const Chunk& q,
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             if (t == wave) xd = j0 + 16 * t + r == il ? a[t][r] : xd;
-            const float e = exp2_hw(((f - ej[r]) + (l - lj[r])) * kLog2e);
+            const float e = exp2_hw((f - ej[r]) + (l - lj[r]));
             a[t][r] = (same >> (4 * t + r)) & 1u ? a[t][r] * e : 0.0f;
           }
         } else {

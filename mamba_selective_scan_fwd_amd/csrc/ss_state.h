@@ -19,6 +19,33 @@
 
 namespace ss {
 
+// ---- decays inside a chunk ----------------------------------------------------------
+// exp(Delta_t A) as a power of two, in 64 bits.  The weight of step j in step i is
+// 2 to the difference of two running sums of these over up to 64 steps: after
+// steps that forget everything the sums are large where the difference between
+// neighbours is small, and its error is the sums' own.  One float leaves 2^-24 of
+// the sum (32 steps of Delta A = -320 and 32 small ones: weights near 1 off by
+// 2e-3); the sums are formed in 64 bits and kept as two floats hi + lo.  The scans
+// take a pair's exponent from hi alone and lo as factors 2^lo, of the column with
+// what else scales it and of the row at the end, so that a pair costs no more.
+// Beyond +-2^20 a decay is 0 or infinite in every product that fp32 holds; the
+// bound keeps lo within 2, and its power finite.
+__device__ __forceinline__ double step_log2(float delta, float A) {
+  constexpr double kMost = 1048576.0;
+  const double v = (double)delta * (double)A * 1.4426950408889634074;
+  return v < -kMost ? -kMost : v > kMost ? kMost : v;
+}
+// sum of v over this lane and those before it
+__device__ __forceinline__ double scan_up(double v) {
+  const int lane = threadIdx.x % 64;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const double o = __shfl_up(v, off, 64);
+    if (lane >= off) v += o;
+  }
+  return v;
+}
+
 constexpr int kStateThreads = 512;
 constexpr int kStatePiece = 64;
 
