@@ -134,17 +134,22 @@ __global__ void __launch_bounds__(kBwdThreads) conv1d_bwd_kernel(ConvBwdParams p
         const float s = sigmoid_f(pre);
         g *= s * fmaf(pre, 1.0f - s, 1.0f);
       }
-      // Steps behind the row's end: dout is 0 there, and where pre is not finite, so is
-      // pre of the last step, whose dpre reaches the same dx; of documents, their ids
-      // do not say so much.
-      dpre[e] = !SEQ || t0 + e < L ? g : 0.0f;
-      if (e < kPer) {
-        db += dpre[e];
+      dpre[e] = g;
+    }
+    // Steps behind the row's end have no gradient, whatever their pre is: other
+    // weights meet the last inputs there, and it may be infinite where the row's own
+    // are not.
+    if (t0 + kPer + W - 1 > L) {
 #pragma unroll
-        for (int k = 0; k < W; ++k) {
-          const int i = 4 + e - (W - 1) + k;
-          dw[k] = fmaf(dpre[e], k == W - 1 || meets(i, 4 + e) ? x[i] : 0.0f, dw[k]);
-        }
+      for (int e = 0; e < kPer + W - 1; ++e) dpre[e] = t0 + e < L ? dpre[e] : 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      db += dpre[e];
+#pragma unroll
+      for (int k = 0; k < W; ++k) {
+        const int i = 4 + e - (W - 1) + k;
+        dw[k] = fmaf(dpre[e], k == W - 1 || meets(i, 4 + e) ? x[i] : 0.0f, dw[k]);
       }
     }
     float dx[kPer];
