@@ -861,9 +861,11 @@ class SsdStepCall:
             (y, io, "y", (n, Hn, P)))]
         self.pr, wsz = _problem(ss_ssd_step_problem, "ss_ssd_step_workspace_size", (), n, nslots, Hn, ngroups, xs, zs,
                                 ds, P, N, W, _IO[io], 1 if dt_softplus else 0, 0)
-        self.ws, wa, wsz = _scratch(None, wsz, dev)
-        self.keep = (xbc, dt, A, conv_w, conv_bias, D, z, dt_bias, slots, conv_state, state, y)
         st = stream if stream is not None else torch.cuda.current_stream(xbc.device)
+        # the allocator hands memory out, and takes it back, in the order of the stream that is current then
+        with torch.cuda.stream(st):
+            self.ws, wa, wsz = _scratch(None, wsz, dev)
+        self.keep = (xbc, dt, A, conv_w, conv_bias, D, z, dt_bias, slots, conv_state, state, y)
         self.args = (self.pr, xa, da, *at[:4], za, *at[4:6], at[6] if W > 1 else None, *at[7:], wa, wsz,
                      ctypes.c_void_p(st.cuda_stream))
         self.fn, self.dev = lib.ss_ssd_step, dev
