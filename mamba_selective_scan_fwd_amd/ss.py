@@ -264,9 +264,11 @@ class FwdCall:
             raise ValueError("FwdCall needs its output y")
         self.pr = problem(Bsz, Dd, N, L, io, delta_softplus)
         wsz = lib.ss_fwd_workspace_size(ctypes.byref(self.pr))
-        self.ws = torch.empty((wsz + 3) // 4, dtype=torch.float32, device=u.device) if wsz else None
-        self.keep = (u, delta, A, Bm, Cm, D, z, delta_bias, lengths, seq_idx, h0, y, last_state, ckpt, self.ws)
         st = stream if stream is not None else torch.cuda.current_stream(u.device)
+        # the allocator hands memory out, and takes it back, in the order of the stream that is current then
+        with torch.cuda.stream(st):
+            self.ws = torch.empty((wsz + 3) // 4, dtype=torch.float32, device=u.device) if wsz else None
+        self.keep = (u, delta, A, Bm, Cm, D, z, delta_bias, lengths, seq_idx, h0, y, last_state, ckpt, self.ws)
         self.args = (ctypes.byref(self.pr), _ptr(u), _ptr(delta), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z),
                      _ptr(delta_bias), _ptr(lengths), _ptr(seq_idx), _ptr(h0), _ptr(y), _ptr(last_state),
                      _ptr(ckpt), _ptr(self.ws), wsz,

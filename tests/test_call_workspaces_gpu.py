@@ -35,3 +35,21 @@ def test_step_call_workspace_is_its_streams():
     ss.SsdStepCall(y=want, **b)()
     torch.cuda.synchronize()
     assert torch.equal(y, want) and torch.equal(a["state"], b["state"])
+
+
+def test_forward_call_workspace_is_its_streams():
+    ss = _ss()
+    t = lambda *s: torch.randn(*s, device="cuda")
+    u, delta, B, C, A = t(1, 32, 4096), t(1, 32, 4096), t(1, 16, 4096), t(1, 16, 4096), -torch.rand(32, 16, device="cuda")
+    y = torch.zeros_like(u)
+    side = torch.cuda.Stream()
+    call = ss.FwdCall(u, delta, A, B, C, y=y, stream=side)      # few channels: time is split, over a workspace
+    assert _stream_of(call.ws) == side.cuda_stream
+    side.wait_stream(torch.cuda.current_stream())
+    call()
+    del call
+    side.synchronize()
+    want = torch.empty_like(u)
+    ss.FwdCall(u, delta, A, B, C, y=want)()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
