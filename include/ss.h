@@ -426,14 +426,18 @@ ss_status ss_ssd_bwd(const ss_ssd_problem *p, const void *x, const void *dt, con
  *                slot: such a sequence starts from zero and keeps no state;
  *                such a row of a step is not computed and its output stays as
  *                it was (padding of a captured batch).  No two may name the
- *                same slot: which of them it then holds is not specified.
+ *                same slot: what it then holds, and what those that continue
+ *                from it give, is not specified (not always what one of them
+ *                alone would).
  *   has_state  : device int32[nseqs]; nonzero: the sequence continues from its
  *                slot's state; zero (NULL: all): it starts from zero, whatever
  *                the slot holds.
  * Rows may lie further apart than they are long (strides in elements, at most
  * 2^21), so that the parts of a projection's output rows are taken as they
- * lie.  No output may share a byte with any other buffer, slots' pools among
- * them (SS_ERR_UNSUPPORTED).  Nothing is kept between calls but the pools;
+ * lie.  No output's range, from its first byte to the last of its last row, may
+ * meet that of any other buffer, slots' pools among them (SS_ERR_UNSUPPORTED):
+ * an input and an output cannot be columns of the same rows.  Nothing is kept
+ * between calls but the pools;
  * calls that use the same slots or the same workspace must be ordered by the
  * caller.  1 <= tokens <= 2^30, 1 <= nseqs <= 2^20.
  */
