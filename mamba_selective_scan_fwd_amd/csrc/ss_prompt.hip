@@ -249,11 +249,11 @@ __global__ void __launch_bounds__(256) prompt_pass_kernel(SsdPromptParams p) {
 // through range-checked views, whose addresses take one register, and the gate
 // is loaded in the place of a next piece behind the last: at two workgroups to a
 // CU nothing is spilled, but 4 registers of bf16 at states below 128 (88 and 118 us;
-// 94 and 122 us with 8 and 12 registers spilled, whose stores went to HBM).  Of the 88 us, the loads, E's staging and
-// the stores alone take about 52, near what their 230 MB need, and the products
-// do not hide behind them.  Several heads one after the other in a workgroup,
-// the next one's loads ahead, leave one workgroup to a CU and take longer (24
-// ragged prompts: 160 us against 95).
+// 94 and 122 us with 8 and 12 registers spilled, whose stores went to HBM).  Of
+// the 88 us, the loads, E's staging and the stores alone take about 52, near what
+// their 230 MB need, and the products do not hide behind them.  Several heads one
+// after the other in a workgroup, the next one's loads ahead, leave one workgroup
+// to a CU and take longer (24 ragged prompts: 160 us against 95).
 constexpr int kScanThreads = 512;
 template <int IO, int N>
 __global__ void __launch_bounds__(kScanThreads, 4) prompt_scan_kernel(SsdPromptParams p) {

@@ -28,8 +28,8 @@
 // errors add up to over the steps: 1e-5 of dA over 600 steps, 1e-7 this way).
 // Kernels:
 //   bwd_planes   (fp16 or gated) the operands' planes of bf16 parts, g among them
-//   bwd_state    per (chunk, head): what a chunk adds to E and to R; further
-//                workgroups: B C^T (and C B^T if gated) per (chunk, group)
+//   bwd_state    per (chunk, one to three heads of a group, E or R): what a chunk adds
+//                to E and to R; further workgroups: B C^T (and C B^T if gated) per (chunk, group)
 //   bwd_pass_pair, two kinds of workgroups:
 //     pass       per (row, head, 1024 elements): E of every chunk, then R and
 //                <R, E> backwards, dh0
@@ -380,7 +380,8 @@ __device__ __forceinline__ void pass_role(const SsdBwdParams& p, uint32_t block)
 //   rev:  s >= o, u = g, M = exp(cs_s - cs_o) (C_s . B_o),         K = R, v = B, f = exp(cs_last - cs_o)
 //   else: s <= o, u = x, M = exp(cs_o - cs_s) Delta_s (C_o . B_s), K = E, v = C, f = exp(cs_o)
 // A pair in different pieces of 64 takes a factor per row and one per column,
-// both through the piece's end, a pair inside a piece the exp of a difference.
+// both through the piece's end, a pair inside a piece the exp of a difference (of
+// sums in two floats: step_log2).
 constexpr int kScanThreads = 512;
 // Where z is given, workgroups of both take turns in one launch; u's second part
 // takes K's place once K is used up, so that two workgroups share a CU (gated

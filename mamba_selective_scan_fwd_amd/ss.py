@@ -715,8 +715,9 @@ def ssd_prompt(x, dt, A, Bm, Cm, cu_seqlens, state, D=None, z=None, dt_bias=None
 def conv1d_bwd(x, w, dout, bias=None, silu=True, seq_idx=None, conv_init=None, dconv_final=None,
                want_dconv_init=False, workspace=None):
     """Gradients of conv1d for the loss sum(dout * out) + sum(dconv_final * conv_final); x, w, bias,
-    silu, seq_idx and conv_init as given to it.  Returns a dict: dx (B, D, L) in x's dtype, dw (D, W)
-    and dbias (D,) (with bias) fp32, dconv_init (B, D, W-1) fp32 when want_dconv_init."""
+    silu, seq_idx and conv_init as given to it; what is not contiguous is copied.  Returns a dict: dx
+    (B, D, L) in x's dtype, dw (D, W) and dbias (D,) (with bias) fp32, dconv_init (B, D, W-1) fp32 when
+    want_dconv_init."""
     lib = load_library()
     io = x.dtype
     if io not in _IO:
@@ -753,7 +754,7 @@ def conv1d_bwd(x, w, dout, bias=None, silu=True, seq_idx=None, conv_init=None, d
 def ssd_bwd(x, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, dt_softplus=True, seq_idx=None, h0=None,
             dfinal=None, want_dh0=False, workspace=None):
     """Gradients of ssd_fwd for the loss sum(dy * y) + sum(dfinal * final_state); the inputs as given to
-    it (nothing else of the forward is needed).  Returns a dict: dx, ddt, dB, dC and dz (with z) in the
+    it (nothing else of the forward is needed); what is not contiguous is copied.  Returns a dict: dx, ddt, dB, dC and dz (with z) in the
     data's dtype, dA, dD (with D) and ddt_bias (with dt_bias) fp32, dh0 fp32 when want_dh0."""
     lib = load_library()
     io = x.dtype
@@ -983,7 +984,8 @@ class Conv1dFn(torch.autograd.Function):
 
 
 def conv1d_fn(x, w, bias=None, silu=True, seq_idx=None, conv_init=None, return_final=False):
-    """conv1d, differentiable once: out, or (out, conv_final) with return_final.  To capture it in a
+    """conv1d, differentiable once: out, or (out, conv_final) with return_final.  Its backward computes
+    the gradients of x, w and bias together, whichever are asked for.  To capture it in a
     graph, capture the forward with its backward, and drop the outputs of eager passes over the same
     leaves before: while one lives, the leaves' gradients are accumulated on that pass's stream."""
     return Conv1dFn.apply(x, w, bias, silu, seq_idx, conv_init, return_final)
@@ -1013,6 +1015,7 @@ class SsdScanFn(torch.autograd.Function):
 
 def ssd_scan_fn(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, dt_softplus=True, seq_idx=None, h0=None,
                 return_final_state=False):
-    """ssd_fwd, differentiable once: y, or (y, final_state) with return_final_state.  In a captured
+    """ssd_fwd, differentiable once: y, or (y, final_state) with return_final_state.  Its backward
+    computes the gradients of all inputs but h0 together, whichever are asked for.  In a captured
     graph as conv1d_fn."""
     return SsdScanFn.apply(x, dt, A, Bm, Cm, D, z, dt_bias, dt_softplus, seq_idx, h0, return_final_state)
