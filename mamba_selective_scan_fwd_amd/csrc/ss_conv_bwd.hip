@@ -11,7 +11,7 @@
 // it holds.  pre is rebuilt from x.
 //
 // A streaming stencil (x, dout and dx once each), bound by HBM and by the vector
-// units about alike (8 x 1536 rows of 2048 bf16 steps: 36 us, 4.2 TB/s, the
+// units about alike (8 x 1536 rows of 2048 bf16 steps: 37 us, 4.1 TB/s, the
 // latter busy for three quarters of it; 16 steps a thread, which rebuild less,
 // take 39): a thread
 // covers 8 consecutive steps of one row, takes 4 inputs before and 4 inputs

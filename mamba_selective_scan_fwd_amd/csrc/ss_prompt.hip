@@ -20,7 +20,7 @@
 // All chunks of a prompt run at once, whatever its length; only the
 // element-wise pass walks them in order.  24 ragged prompts of 16384 tokens (24
 // heads, state 128, bf16, gate): 50, 25 and 88 us; one prompt of 32769 tokens
-// (state 64, fp16): 68, 21 and 115-125 us.  Of the bytes, 4 times the fp32 states
+// (state 64, fp16): 68-72, 21 and 118-126 us.  Of the bytes, 4 times the fp32 states
 // (276 MB of the first) are the price of the chunks' independence: a walk over the
 // chunks inside a workgroup, as in ss_ssd.hip, has no such traffic and as many
 // workgroups as prompts have heads.
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(256) prompt_pass_kernel(SsdPromptParams p) {
 // CU (one prompt of 32769 tokens: 122 us, 137 us with one).  C B^T and y go
 // through range-checked views, whose addresses take one register, and the gate
 // is loaded in the place of a next piece behind the last: at two workgroups to a
-// CU nothing is spilled, but 4 registers of bf16 at states below 128 (88 and 118 us;
+// CU nothing is spilled, but 4 registers of bf16 at states below 128 (87 and 118-126 us;
 // 94 and 122 us with 8 and 12 registers spilled, whose stores went to HBM).  Of
 // the 88 us, the loads, E's staging and the stores alone take about 52, near what
 // their 230 MB need, and the products do not hide behind them.  Several heads one

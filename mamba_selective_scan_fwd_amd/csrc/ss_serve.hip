@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(256) ssd_step_conv_kernel(SsdStepParams p) {
 
 // Workgroup = (row, head): the head's 64 x N state is one contiguous slab,
 // read and written once, which is what bounds the kernel (HBM: 61 requests of 24
-// heads, state 128: 15.4 us, 6.2 TB/s, part of it from the last level cache; 201
+// heads, state 128: 15.4-17 us, 5.7-6.2 TB/s, part of it from the last level cache; 201
 // of 80 heads, state 64: 104 us, 5.2 TB/s).  8 lanes share
 // a row p of the state, lane j of them holding the 4 states 4 j + 32 m ..: a
 // load instruction covers whole 128-byte lines of 8 rows, every load is issued
