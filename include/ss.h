@@ -553,6 +553,182 @@ ss_status ss_ssd_step(const ss_ssd_step_problem *p, const void *xbc, const void 
                       const float *dt_bias, const int32_t *slots, float *conv_state, float *state,
                       void *y, void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * ---- linear attention with a decay for each head --------------------------------
+ * The constant-decay relative of the SSD ("Mamba", "Deep dive: Mamba-2 and
+ * state-space duality": the chunked, attention-like form of a scan and its
+ * recurrent form), per head h with a = exp(log_decay[h]), kv head g =
+ * h / (nheads / kv_heads), and a state H (dv x dk):
+ *   H_t = a H_{t-1} + v_t k_t^T,   y_t = scale * H_t q_t.
+ *   q       : (tokens, nheads, dk)    io dtype (fp16 or bf16), tokens q_stride apart
+ *   k, v    : (tokens, kv_heads, dk / dv)  io dtype, tokens k_stride / v_stride apart
+ *   log_decay : (nheads) fp32, at most 0 (larger ones make the state grow, and
+ *             may overflow)
+ *   y       : (tokens, nheads, dv) io dtype, without gaps
+ *   states  : (.., nheads, dv, dk) fp32
+ * dk and dv are 64 or 128 each; strides are multiples of 8 and at most 2^21; every
+ * pointer is 16-byte aligned.  Computed operands are multiplied as sums of bf16
+ * parts and states kept in fp32, so that states carry nearly fp32's error, and y and
+ * the gradients before their rounding too.  A value that is not finite spreads
+ * to other rows of the same 64-row chunk of its sequence, earlier ones among
+ * them, and to the rows behind it, and to no other sequence.
+ * `packed` nonzero: the rows of sequence s are cu_seqlens[s] .. cu_seqlens[s+1]-1,
+ * as declared with the serving calls above (a device array, clamped to
+ * 0 .. tokens, sequences may be empty); zero: cu_seqlens is NULL, tokens is a
+ * multiple of nseqs and every sequence has tokens / nseqs rows.
+ * The workspace is needed where the sequences are too few to fill the GPU and
+ * are walked in segments: per segment, a state of every head (the backward's: of
+ * every head three, and with shared heads their parts of dk and dv in fp32).  Its
+ * size goes by sizes alone (0: none is needed, NULL); its contents on entry do not
+ * matter, and calls that share one must be ordered by the caller.
+ */
+typedef struct ss_linattn_problem {
+    int64_t tokens;       /* rows of q, k, v and y */
+    int64_t nseqs;        /* ignored by ss_linattn_step */
+    int64_t nslots;       /* ss_linattn_prompt and ss_linattn_step */
+    int64_t nheads;       /* at most 2^14 */
+    int64_t kv_heads;     /* divides nheads */
+    int64_t q_stride;     /* elements between tokens */
+    int64_t k_stride;
+    int64_t v_stride;
+    int32_t dk;           /* 64 or 128 */
+    int32_t dv;           /* 64 or 128 */
+    int32_t io_dtype;     /* SS_F16 or SS_BF16 */
+    int32_t packed;       /* 1: cu_seqlens is given, 0: sequences of one length */
+    float scale;
+    int32_t reserved;     /* must be 0 */
+} ss_linattn_problem;
+
+size_t ss_linattn_workspace_size(const ss_linattn_problem *p);
+size_t ss_linattn_bwd_workspace_size(const ss_linattn_problem *p);
+
+/*
+ * Forward for training.  h0 (NULL: zeros) and final_state (NULL: not wanted):
+ * (nseqs, nheads, dv, dk) fp32.  Rows of no sequence get y = 0.  No output or
+ * workspace may overlap any other buffer (SS_ERR_UNSUPPORTED).
+ */
+ss_status ss_linattn_fwd(const ss_linattn_problem *p, const void *q, const void *k, const void *v,
+                         const float *log_decay, const int32_t *cu_seqlens, const float *h0, void *y,
+                         float *final_state, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of ss_linattn_fwd for the loss sum(dy * y) + sum(dfinal *
+ * final_state); p and the inputs are the forward's, and nothing else of it is
+ * needed.  log_decay is a constant of the layer and has no gradient.
+ *   dy      : (tokens, nheads, dv) io dtype, without gaps
+ *   dfinal  : optional, like final_state (NULL: zero)
+ *   dq      : (tokens, nheads, dk), dk (tokens, kv_heads, dk), dv (tokens,
+ *             kv_heads, dv) io dtype, without gaps; a shared head's are summed
+ *             over its heads in fp32; 0 in rows of no sequence
+ *   dh0     : optional, like h0, also where h0 is NULL
+ * Every output is overwritten; sums have a fixed order.
+ */
+ss_status ss_linattn_bwd(const ss_linattn_problem *p, const void *q, const void *k, const void *v,
+                         const float *log_decay, const int32_t *cu_seqlens, const float *h0, const void *dy,
+                         const float *dfinal, void *dq, void *dk, void *dv, float *dh0, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/*
+ * Packed prompts, each from and into its slot's state: cu_seqlens, slots,
+ * has_state and rows of no sequence (left as they were) as in ss_ssd_prompt.
+ *   state : (nslots, nheads, dv, dk) fp32, updated in place
+ */
+ss_status ss_linattn_prompt(const ss_linattn_problem *p, const void *q, const void *k, const void *v,
+                            const float *log_decay, const int32_t *cu_seqlens, const int32_t *slots,
+                            const int32_t *has_state, float *state, void *y, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/*
+ * One token of p->tokens requests, in fp32 over state slots: slots as in
+ * ss_ssd_step (a row without one is not computed, its y stays as it was).  q, k
+ * and v are aligned to the element, their strides any.
+ */
+ss_status ss_linattn_step(const ss_linattn_problem *p, const void *q, const void *k, const void *v,
+                          const float *log_decay, const int32_t *slots, float *state, void *y, void *stream);
+
+/*
+ * ---- grouped norm of a token's channels, with a gate or an activation ----------------
+ * What stands between a layer's scan and its output projection: per row and
+ * group of n = channels / ngroups neighbouring channels, with u = x, or
+ * x * silu(z) (SS_NORM_GATE_FIRST):
+ *   m = mean(u) (0 unless `center`),  o = (u - m) / sqrt(mean((u - m)^2) + eps) * weight + bias,
+ *   y = o, silu(o) (SS_NORM_SILU) or o * silu(z) (SS_NORM_GATE).
+ * Mamba-2's gated norm is SS_NORM_GATE_FIRST without centring; linear attention's, a
+ * group a head, is centred with SS_NORM_GATE.
+ *   x, z, y : (rows, channels) io dtype (fp32, fp16 or bf16), rows *_stride elements
+ *             apart; z is given iff the mode has a gate
+ *   weight, bias : (channels) fp32, each may be NULL (1, 0); 16-byte aligned
+ * Sums and norms are in fp32.  Data pointers are aligned to the element; groups of a
+ * multiple of 4 (fp32) or 8 (16-bit) channels, in rows on 16-byte boundaries, run
+ * fastest.  No output may overlap any other buffer (SS_ERR_UNSUPPORTED), nor may its
+ * range of strided rows meet another's.  rows <= 2^30, channels and strides <= 2^21.
+ */
+typedef enum ss_norm_mode {
+    SS_NORM_PLAIN = 0,
+    SS_NORM_SILU = 1,
+    SS_NORM_GATE = 2,
+    SS_NORM_GATE_FIRST = 3
+} ss_norm_mode;
+
+typedef struct ss_norm_problem {
+    int64_t rows;
+    int64_t channels;
+    int64_t ngroups;      /* divides channels */
+    int64_t x_stride;
+    int64_t z_stride;     /* ignored without a gate */
+    int64_t y_stride;     /* ss_group_norm */
+    int64_t dy_stride;    /* ss_group_norm_bwd */
+    float eps;            /* >= 0 */
+    int32_t io_dtype;
+    int32_t mode;         /* ss_norm_mode */
+    int32_t center;       /* nonzero: the mean is subtracted */
+} ss_norm_problem;
+
+ss_status ss_group_norm(const ss_norm_problem *p, const void *x, const float *weight, const float *bias,
+                        const void *z, void *y, void *stream);
+
+/*
+ * Gradients of ss_group_norm for the loss sum(dy * y); the inputs are the
+ * forward's, nothing else of it is needed.
+ *   dx, dz  : (rows, channels) io dtype, without gaps; dz iff z
+ *   dweight, dbias : (channels) fp32, given iff weight, bias are; summed over the
+ *             rows in a fixed order
+ *   workspace : ss_group_norm_bwd_workspace_size() bytes; its contents on entry
+ *             do not matter; calls that share one must be ordered by the caller
+ */
+size_t ss_group_norm_bwd_workspace_size(const ss_norm_problem *p);
+
+ss_status ss_group_norm_bwd(const ss_norm_problem *p, const void *x, const float *weight, const float *bias,
+                            const void *z, const void *dy, void *dx, float *dweight, float *dbias, void *dz,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * ---- the maps of a serving batch ---------------------------------------------------------
+ * What the serving calls take of a batch, from its requests on the device.
+ * Request i has new_tokens[i] rows to run, seen[i] tokens behind it and slots[i];
+ * one without a slot (negative) or without new tokens is idle.  A request with one
+ * new token and seen > 0 is a step, any other a prompt.  The batch's rows are the
+ * steps' in the requests' order, one each, then the prompts' in that order, at most
+ * `tokens` in all: the prompt that reaches that end is cut, what comes behind
+ * it has no rows in this batch.
+ *   rows, taken   : (requests) the request's first row (-1: none) and its rows
+ *   step_slots    : (requests) the slot of row i if that is a step, else -1: with
+ *                   the first rows of a batch, the slots of ss_ssd_step or
+ *                   ss_linattn_step
+ *   cu_seqlens    : (requests + 1), prompt_slots, has_state : (requests) of the
+ *                   prompts that have rows, as ss_conv1d_prompt, ss_ssd_prompt and
+ *                   ss_linattn_prompt take them; behind the last prompt empty
+ *                   sequences without a slot (-1, 0)
+ *   row_request, row_position : (tokens) a row's request, and its token's
+ *                   position in it (seen + ..); -1 behind the last row
+ * All int32, 16-byte aligned; seen below 0 counts as 0.  requests <= 2^20,
+ * tokens <= 2^30.
+ */
+ss_status ss_pack_requests(int64_t requests, int64_t tokens, const int32_t *new_tokens, const int32_t *slots,
+                           const int32_t *seen, int32_t *rows, int32_t *taken, int32_t *step_slots,
+                           int32_t *cu_seqlens, int32_t *prompt_slots, int32_t *has_state, int32_t *row_request,
+                           int32_t *row_position, void *stream);
+
 /* Number of floats of the checkpoint buffer: batch*dim*ceil(seqlen/64)*dstate (0 if invalid). */
 size_t ss_ckpt_count(const ss_problem *p);
 

@@ -8,7 +8,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libss.so")
 SOURCES = ["ss_fwd.hip", "ss_bwd.hip", "ss_conv.hip", "ss_conv_bwd.hip", "ss_ssd.hip", "ss_ssd_bwd.hip", "ss_prompt.hip",
-           "ss_serve.hip", "ss_probe.hip", "ss_noalloc.hip", "ss_abi.cpp"]
+           "ss_serve.hip", "ss_linattn.hip", "ss_norm.hip", "ss_pack.hip", "ss_probe.hip", "ss_noalloc.hip", "ss_abi.cpp"]
 HEADERS = ["ss_device.h", "ss_internal.h", "ss_mfma.h", "ss_packed.h", "ss_plan.h", "ss_state.h",
            "ss_view.h"]
 

@@ -8,6 +8,7 @@
 
 #include "../../include/ss.h"
 #include "ss_internal.h"
+#include "ss_plan.h"
 
 namespace {
 
@@ -895,6 +896,371 @@ ss_status ss_ssd_step(const ss_ssd_step_problem* p, const void* xbc, const void*
   k.rows = (int32_t)p->rows; k.nslots = (int32_t)p->nslots; k.nheads = (int32_t)p->nheads;
   k.ngroups = (int32_t)p->ngroups; k.dstate = p->dstate; k.channels = (int32_t)ch;
   return from_hip(ss::launch_ssd_step(k, static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+// ---- linear attention -----------------------------------------------------------------
+ss_status check_linattn_heads(const ss_linattn_problem* p) {
+  if (!p) return SS_ERR_NULL_ARG;
+  if (p->nheads < 1 || p->kv_heads < 1) return SS_ERR_BAD_SHAPE;
+  if (p->io_dtype != SS_F16 && p->io_dtype != SS_BF16) return SS_ERR_BAD_DTYPE;
+  if ((p->dk != 64 && p->dk != 128) || (p->dv != 64 && p->dv != 128)) return SS_ERR_UNSUPPORTED;
+  if (p->nheads > kMaxStride / 128 || p->nheads % p->kv_heads != 0 || (p->packed != 0 && p->packed != 1) || p->reserved != 0)
+    return SS_ERR_UNSUPPORTED;
+  if (p->tokens < 1 || p->tokens > kMaxTokens) return SS_ERR_BAD_SHAPE;
+  const int64_t strides[] = {p->q_stride, p->k_stride, p->v_stride};
+  const int64_t rows[] = {p->nheads * p->dk, p->kv_heads * p->dk, p->kv_heads * p->dv};
+  for (int i = 0; i < 3; ++i)
+    if (strides[i] < rows[i] || strides[i] > kMaxStride) return SS_ERR_BAD_SHAPE;
+  return SS_OK;
+}
+struct LinPlan {
+  int logq;
+  int64_t places;
+  size_t states, parts, total;  // bytes of the segments' states, and where the shared heads' parts begin
+};
+// `jobs` walks of every head: one forward, three backward
+ss_status plan_linattn(const ss_linattn_problem* p, int jobs, LinPlan* plan) {
+  const ss_status s = check_linattn_heads(p);
+  if (s != SS_OK) return s;
+  if (p->nseqs < 1 || p->nseqs > kMaxSeqs) return SS_ERR_BAD_SHAPE;
+  if (!p->packed && p->tokens % p->nseqs != 0) return SS_ERR_BAD_SHAPE;
+  if (p->q_stride % 8 || p->k_stride % 8 || p->v_stride % 8) return SS_ERR_MISALIGNED;
+  const int64_t longest = p->packed ? p->tokens : p->tokens / p->nseqs, walks = p->nheads * jobs;
+  LinPlan l{};
+  l.logq = ss::lin_segments(p->tokens, p->nseqs, longest, walks, 256);
+  l.places = p->packed ? (p->tokens >> l.logq) + p->nseqs
+                       : p->nseqs * ((longest + ((int64_t)1 << l.logq) - 1) >> l.logq);
+  if (l.places * walks > kMaxGrid || p->nseqs * walks * (p->dk * p->dv / 1024) > kMaxGrid) return SS_ERR_BAD_SHAPE;
+  if (jobs > 1 && p->tokens * p->nheads > kMaxGrid * 8) return SS_ERR_BAD_SHAPE;  // the shared heads' sums
+  l.states = l.logq == ss::kLinWhole ? 0 : align256((size_t)(l.places * walks) * (size_t)(p->dk * p->dv) * 4);
+  l.parts = l.states;
+  l.total = l.parts + (jobs > 1 && p->kv_heads != p->nheads
+                           ? align256((size_t)(p->tokens * p->nheads) * (size_t)(p->dk + p->dv) * 4) : 0);
+  *plan = l;
+  return SS_OK;
+}
+struct LinSpans {  // bytes of the operands
+  size_t q, k, v, y, state, heads;
+  explicit LinSpans(const ss_linattn_problem* p)
+      : q(rows_bytes(p->tokens, p->q_stride, p->nheads * p->dk, 2)),
+        k(rows_bytes(p->tokens, p->k_stride, p->kv_heads * p->dk, 2)),
+        v(rows_bytes(p->tokens, p->v_stride, p->kv_heads * p->dv, 2)),
+        y((size_t)(p->tokens * p->nheads * p->dv) * 2),
+        state((size_t)(p->nheads * p->dk * p->dv) * 4),
+        heads((size_t)p->nheads * 4) {}
+};
+ss::LinParams linattn_params(const ss_linattn_problem* p, const LinPlan& l, const float* log_decay,
+                             const int32_t* cu, void* workspace) {
+  ss::LinParams k{};
+  k.io = p->io_dtype;
+  k.log_decay = log_decay;
+  k.cu = cu;
+  k.split = l.logq != ss::kLinWhole;
+  k.ws = static_cast<float*>(workspace);
+  k.tokens = (int32_t)p->tokens; k.nseqs = (int32_t)p->nseqs;
+  k.heads = (int32_t)p->nheads; k.share = (int32_t)(p->nheads / p->kv_heads);
+  k.logq = l.logq; k.places = (int32_t)l.places;
+  return k;
+}
+ss::LinWalk linattn_forward(const ss_linattn_problem* p, const void* q, const void* k, const void* v,
+                            const float* init, void* y, float* fin) {
+  ss::LinWalk w{};
+  w.a = q; w.b = k; w.c = v;
+  w.a_stride = p->q_stride; w.b_stride = p->k_stride; w.c_stride = p->v_stride;
+  w.b_kv = w.c_kv = 1;
+  w.dc = p->dk; w.dout = p->dv; w.c_inner = 1;
+  w.out = y; w.init = init; w.fin = fin;
+  w.m_scale = w.e_scale = p->scale;
+  w.u_scale = 1.0f;
+  return w;
+}
+}  // namespace
+
+size_t ss_linattn_workspace_size(const ss_linattn_problem* p) {
+  LinPlan l;
+  return plan_linattn(p, 1, &l) == SS_OK ? l.total : 0;
+}
+
+size_t ss_linattn_bwd_workspace_size(const ss_linattn_problem* p) {
+  LinPlan l;
+  return plan_linattn(p, 3, &l) == SS_OK ? l.total : 0;
+}
+
+ss_status ss_linattn_fwd(const ss_linattn_problem* p, const void* q, const void* k, const void* v,
+                         const float* log_decay, const int32_t* cu_seqlens, const float* h0, void* y,
+                         float* final_state, void* workspace, size_t workspace_bytes, void* stream) {
+  LinPlan l;
+  const ss_status s = plan_linattn(p, 1, &l);
+  if (s != SS_OK) return s;
+  if (!q || !k || !v || !log_decay || !y || (cu_seqlens != nullptr) != (p->packed != 0)) return SS_ERR_NULL_ARG;
+  const void* ptrs[] = {q, k, v, log_decay, cu_seqlens, h0, y, final_state, workspace};
+  for (const void* a : ptrs)
+    if (a && !aligned(a)) return SS_ERR_MISALIGNED;
+  if (l.total && (!workspace || workspace_bytes < l.total)) return SS_ERR_UNSUPPORTED;
+  {
+    const LinSpans n(p);
+    const size_t st = n.state * (size_t)p->nseqs;
+    const Span in[] = {{q, n.q}, {k, n.k}, {v, n.v}, {log_decay, n.heads}, {cu_seqlens, (size_t)p->nseqs * 4 + 4}, {h0, st}};
+    const Span outs[] = {{y, n.y}, {final_state, st}, {l.total ? workspace : nullptr, l.total}};
+    if (conflict(in, outs)) return SS_ERR_UNSUPPORTED;
+  }
+  ss::LinParams k_ = linattn_params(p, l, log_decay, cu_seqlens, workspace);
+  k_.zero_rest = 1;
+  k_.jobs = 1;
+  k_.job[0] = linattn_forward(p, q, k, v, h0, y, final_state);
+  return from_hip(ss::launch_linattn(k_, static_cast<hipStream_t>(stream)));
+}
+
+ss_status ss_linattn_prompt(const ss_linattn_problem* p, const void* q, const void* k, const void* v,
+                            const float* log_decay, const int32_t* cu_seqlens, const int32_t* slots,
+                            const int32_t* has_state, float* state, void* y, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  LinPlan l;
+  const ss_status s = plan_linattn(p, 1, &l);
+  if (s != SS_OK) return s;
+  if (p->nslots < 1 || p->nslots > kMaxSlots) return SS_ERR_BAD_SHAPE;
+  if (!q || !k || !v || !log_decay || !cu_seqlens || !p->packed || !state || !y) return SS_ERR_NULL_ARG;
+  const void* ptrs[] = {q, k, v, log_decay, cu_seqlens, slots, has_state, state, y, workspace};
+  for (const void* a : ptrs)
+    if (a && !aligned(a)) return SS_ERR_MISALIGNED;
+  if (!slots && p->nslots < p->nseqs) return SS_ERR_UNSUPPORTED;
+  if (l.total && (!workspace || workspace_bytes < l.total)) return SS_ERR_UNSUPPORTED;
+  {
+    const LinSpans n(p);
+    const size_t ib = (size_t)p->nseqs * 4;
+    const Span in[] = {{q, n.q}, {k, n.k}, {v, n.v}, {log_decay, n.heads}, {cu_seqlens, ib + 4}, {slots, ib}, {has_state, ib}};
+    const Span outs[] = {{y, n.y}, {state, n.state * (size_t)p->nslots}, {l.total ? workspace : nullptr, l.total}};
+    if (conflict(in, outs)) return SS_ERR_UNSUPPORTED;
+  }
+  ss::LinParams k_ = linattn_params(p, l, log_decay, cu_seqlens, workspace);
+  k_.pool = 1;
+  k_.slots = slots; k_.has_state = has_state; k_.nslots = (int32_t)p->nslots;
+  k_.jobs = 1;
+  k_.job[0] = linattn_forward(p, q, k, v, state, y, state);
+  return from_hip(ss::launch_linattn(k_, static_cast<hipStream_t>(stream)));
+}
+
+ss_status ss_linattn_bwd(const ss_linattn_problem* p, const void* q, const void* k, const void* v,
+                         const float* log_decay, const int32_t* cu_seqlens, const float* h0, const void* dy,
+                         const float* dfinal, void* dq, void* dk, void* dv, float* dh0, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  LinPlan l;
+  const ss_status s = plan_linattn(p, 3, &l);
+  if (s != SS_OK) return s;
+  if (!q || !k || !v || !log_decay || !dy || !dq || !dk || !dv || (cu_seqlens != nullptr) != (p->packed != 0))
+    return SS_ERR_NULL_ARG;
+  const void* ptrs[] = {q, k, v, log_decay, cu_seqlens, h0, dy, dfinal, dq, dk, dv, dh0, workspace};
+  for (const void* a : ptrs)
+    if (a && !aligned(a)) return SS_ERR_MISALIGNED;
+  if (l.total && (!workspace || workspace_bytes < l.total)) return SS_ERR_UNSUPPORTED;
+  const size_t kb = (size_t)(p->tokens * p->kv_heads) * 2;
+  {
+    const LinSpans n(p);
+    const size_t st = n.state * (size_t)p->nseqs;
+    const Span in[] = {{q, n.q}, {k, n.k}, {v, n.v}, {log_decay, n.heads}, {cu_seqlens, (size_t)p->nseqs * 4 + 4},
+                       {h0, st}, {dy, n.y}, {dfinal, st}};
+    const Span outs[] = {{dq, (size_t)(p->tokens * p->nheads * p->dk) * 2}, {dk, kb * (size_t)p->dk}, {dv, kb * (size_t)p->dv},
+                         {dh0, st}, {l.total ? workspace : nullptr, l.total}};
+    if (conflict(in, outs)) return SS_ERR_UNSUPPORTED;
+  }
+  ss::LinParams k_ = linattn_params(p, l, log_decay, cu_seqlens, workspace);
+  k_.zero_rest = 1;
+  k_.jobs = 3;
+  const int64_t dys = p->nheads * p->dv;
+  const bool shared = p->kv_heads != p->nheads;
+  float* parts = shared ? reinterpret_cast<float*>(static_cast<char*>(workspace) + l.parts) : nullptr;
+  ss::LinWalk& a = k_.job[0];  // dq
+  a.a = dy; a.b = v; a.c = k;
+  a.a_stride = dys; a.b_stride = p->v_stride; a.c_stride = p->k_stride;
+  a.b_kv = a.c_kv = 1;
+  a.dc = p->dv; a.dout = p->dk;
+  a.out = dq; a.init = h0;
+  a.m_scale = a.e_scale = p->scale;
+  a.u_scale = 1.0f;
+  ss::LinWalk& b = k_.job[1];  // dk
+  b.a = v; b.b = dy; b.c = q;
+  b.a_stride = p->v_stride; b.b_stride = dys; b.c_stride = p->q_stride;
+  b.a_kv = 1;
+  b.dc = p->dv; b.dout = p->dk; b.rev = 1;
+  b.out = shared ? parts : dk;
+  b.sum = shared ? dk : nullptr;
+  b.init = dfinal;
+  b.m_scale = b.u_scale = p->scale;
+  b.e_scale = 1.0f;
+  ss::LinWalk& c = k_.job[2];  // dv, and dh0, the G that its walk ends with
+  c.a = k; c.b = q; c.c = dy;
+  c.a_stride = p->k_stride; c.b_stride = p->q_stride; c.c_stride = dys;
+  c.a_kv = 1;
+  c.dc = p->dk; c.dout = p->dv; c.rev = 1; c.c_inner = 1;
+  c.out = shared ? parts + (size_t)(p->tokens * p->nheads) * (size_t)p->dk : dv;
+  c.sum = shared ? dv : nullptr;
+  c.init = dfinal; c.fin = dh0;
+  c.m_scale = c.u_scale = p->scale;
+  c.e_scale = 1.0f;
+  return from_hip(ss::launch_linattn(k_, static_cast<hipStream_t>(stream)));
+}
+
+ss_status ss_linattn_step(const ss_linattn_problem* p, const void* q, const void* k, const void* v,
+                          const float* log_decay, const int32_t* slots, float* state, void* y, void* stream) {
+  const ss_status s = check_linattn_heads(p);
+  if (s != SS_OK) return s;
+  if (p->tokens > kMaxSeqs || p->nslots < 1 || p->nslots > kMaxSlots) return SS_ERR_BAD_SHAPE;
+  if (p->tokens * p->nheads * (p->dk * p->dv / 1024) > kMaxGrid) return SS_ERR_BAD_SHAPE;
+  if (!q || !k || !v || !log_decay || !state || !y) return SS_ERR_NULL_ARG;
+  const void* ptrs[] = {log_decay, slots, state, y};
+  for (const void* a : ptrs)
+    if (a && !aligned(a)) return SS_ERR_MISALIGNED;
+  if (!aligned_to(q, 2) || !aligned_to(k, 2) || !aligned_to(v, 2)) return SS_ERR_MISALIGNED;
+  if (!slots && p->nslots < p->tokens) return SS_ERR_UNSUPPORTED;
+  {
+    const LinSpans n(p);
+    const Span in[] = {{q, n.q}, {k, n.k}, {v, n.v}, {log_decay, n.heads}, {slots, (size_t)p->tokens * 4}};
+    const Span outs[] = {{y, n.y}, {state, n.state * (size_t)p->nslots}};
+    if (conflict(in, outs)) return SS_ERR_UNSUPPORTED;
+  }
+  ss::LinStepParams k_{};
+  k_.io = p->io_dtype;
+  k_.q = q; k_.k = k; k_.v = v; k_.log_decay = log_decay; k_.slots = slots; k_.state = state; k_.y = y;
+  k_.q_stride = p->q_stride; k_.k_stride = p->k_stride; k_.v_stride = p->v_stride;
+  k_.scale = p->scale;
+  k_.rows = (int32_t)p->tokens; k_.nslots = (int32_t)p->nslots; k_.heads = (int32_t)p->nheads;
+  k_.share = (int32_t)(p->nheads / p->kv_heads); k_.dk = p->dk; k_.dv = p->dv;
+  return from_hip(ss::launch_linattn_step(k_, static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+// ---- grouped norm -----------------------------------------------------------------------
+ss_status check_norm(const ss_norm_problem* p) {
+  if (!p) return SS_ERR_NULL_ARG;
+  if (p->rows < 1 || p->channels < 1 || p->ngroups < 1 || p->rows > kMaxTokens || p->channels > kMaxStride)
+    return SS_ERR_BAD_SHAPE;
+  if (p->io_dtype != SS_F32 && p->io_dtype != SS_F16 && p->io_dtype != SS_BF16) return SS_ERR_BAD_DTYPE;
+  if (p->channels % p->ngroups != 0) return SS_ERR_UNSUPPORTED;
+  if (p->mode < SS_NORM_PLAIN || p->mode > SS_NORM_GATE_FIRST || !(p->eps >= 0.0f)) return SS_ERR_UNSUPPORTED;
+  if (p->x_stride < p->channels || p->x_stride > kMaxStride) return SS_ERR_BAD_SHAPE;
+  return SS_OK;
+}
+// workgroups over the rows: enough to fill the GPU; the backward's each leave sums behind
+void norm_layout(const ss_norm_problem* p, int vec, bool bwd, ss::NormParams* k) {
+  const int size = (int)(p->channels / p->ngroups), nvec = size / vec;
+  int lanes = 1;
+  while (lanes < nvec && lanes < 1024) lanes *= 2;
+  const int slots = lanes >= 256 ? 1 : 256 / lanes;
+  k->io = p->io_dtype; k->mode = p->mode; k->center = p->center != 0; k->eps = p->eps;
+  k->rows = p->rows; k->groups = (int)p->ngroups; k->size = size; k->vec = vec; k->lanes = lanes;
+  k->block_groups = p->ngroups < slots ? (int)p->ngroups : slots;
+  k->row_lanes = slots / k->block_groups;
+  k->blocks = (int)((p->ngroups + k->block_groups - 1) / k->block_groups);
+  const int64_t most = bwd ? 1024 : 4096, rows = (p->rows + k->row_lanes - 1) / k->row_lanes;
+  const int64_t want = most / k->blocks > 0 ? most / k->blocks : 1;
+  k->row_blocks = (int)(rows < want ? rows : want);
+}
+// the widest vector that sizes allow: the workspace is by sizes alone
+int norm_vec(const ss_norm_problem* p, bool aligned_rows) {
+  const int64_t size = p->channels / p->ngroups;
+  if (!aligned_rows) return 1;
+  if (p->io_dtype == SS_F32) return size % 4 == 0 ? 4 : 1;
+  return size % 8 == 0 ? 8 : size % 4 == 0 ? 4 : 1;
+}
+}  // namespace
+
+size_t ss_group_norm_bwd_workspace_size(const ss_norm_problem* p) {
+  if (check_norm(p) != SS_OK) return 0;
+  return (size_t)(p->rows < 1024 ? p->rows : 1024) * (size_t)p->channels * 8;
+}
+
+ss_status ss_group_norm(const ss_norm_problem* p, const void* x, const float* weight, const float* bias, const void* z,
+                        void* y, void* stream) {
+  const ss_status s = check_norm(p);
+  if (s != SS_OK) return s;
+  const bool gated = p->mode == SS_NORM_GATE || p->mode == SS_NORM_GATE_FIRST;
+  if (!x || !y || gated != (z != nullptr)) return SS_ERR_NULL_ARG;
+  if (p->y_stride < p->channels || p->y_stride > kMaxStride) return SS_ERR_BAD_SHAPE;
+  if (gated && (p->z_stride < p->channels || p->z_stride > kMaxStride)) return SS_ERR_BAD_SHAPE;
+  const int64_t e = elem_size(p->io_dtype);
+  if (!aligned_to(x, e) || !aligned_to(z, e) || !aligned_to(y, e)) return SS_ERR_MISALIGNED;
+  if ((weight && !aligned(weight)) || (bias && !aligned(bias))) return SS_ERR_MISALIGNED;
+  {
+    const size_t wb = (size_t)p->channels * 4;
+    const Span in[] = {{x, rows_bytes(p->rows, p->x_stride, p->channels, e)},
+                       {z, rows_bytes(p->rows, gated ? p->z_stride : p->channels, p->channels, e)},
+                       {weight, wb}, {bias, wb}};
+    const Span outs[] = {{y, rows_bytes(p->rows, p->y_stride, p->channels, e)}};
+    if (conflict(in, outs)) return SS_ERR_UNSUPPORTED;
+  }
+  ss::NormParams k{};
+  int vec = norm_vec(p, true);
+  const int64_t vb = vec * e;
+  if (!aligned_to(x, vb) || !aligned_to(z, vb) || !aligned_to(y, vb) || p->x_stride % vec || p->y_stride % vec ||
+      (gated && p->z_stride % vec))
+    vec = 1;
+  norm_layout(p, vec, false, &k);
+  k.x = x; k.z = z; k.w = weight; k.b = bias; k.y = y;
+  k.x_stride = p->x_stride; k.z_stride = p->z_stride; k.y_stride = p->y_stride;
+  return from_hip(ss::launch_group_norm(k, static_cast<hipStream_t>(stream)));
+}
+
+ss_status ss_group_norm_bwd(const ss_norm_problem* p, const void* x, const float* weight, const float* bias,
+                            const void* z, const void* dy, void* dx, float* dweight, float* dbias, void* dz,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  const ss_status s = check_norm(p);
+  if (s != SS_OK) return s;
+  const bool gated = p->mode == SS_NORM_GATE || p->mode == SS_NORM_GATE_FIRST;
+  if (!x || !dy || !dx || gated != (z != nullptr) || gated != (dz != nullptr)) return SS_ERR_NULL_ARG;
+  if ((weight != nullptr) != (dweight != nullptr) || (bias != nullptr) != (dbias != nullptr)) return SS_ERR_NULL_ARG;
+  if (p->dy_stride < p->channels || p->dy_stride > kMaxStride) return SS_ERR_BAD_SHAPE;
+  if (gated && (p->z_stride < p->channels || p->z_stride > kMaxStride)) return SS_ERR_BAD_SHAPE;
+  const int64_t e = elem_size(p->io_dtype);
+  if (!aligned_to(x, e) || !aligned_to(z, e) || !aligned_to(dy, e) || !aligned_to(dx, e) || !aligned_to(dz, e))
+    return SS_ERR_MISALIGNED;
+  const void* ptrs[] = {weight, bias, dweight, dbias, workspace};
+  for (const void* a : ptrs)
+    if (a && !aligned(a)) return SS_ERR_MISALIGNED;
+  const size_t need = ss_group_norm_bwd_workspace_size(p);
+  if (!workspace || workspace_bytes < need) return SS_ERR_UNSUPPORTED;
+  {
+    const size_t wb = (size_t)p->channels * 4, xb = (size_t)(p->rows * p->channels * e);
+    const Span in[] = {{x, rows_bytes(p->rows, p->x_stride, p->channels, e)},
+                       {z, rows_bytes(p->rows, gated ? p->z_stride : p->channels, p->channels, e)},
+                       {dy, rows_bytes(p->rows, p->dy_stride, p->channels, e)}, {weight, wb}, {bias, wb}};
+    const Span outs[] = {{dx, xb}, {dz, xb}, {dweight, wb}, {dbias, wb}, {workspace, need}};
+    if (conflict(in, outs)) return SS_ERR_UNSUPPORTED;
+  }
+  ss::NormParams k{};
+  int vec = norm_vec(p, true);
+  const int64_t vb = vec * e;
+  if (!aligned_to(x, vb) || !aligned_to(z, vb) || !aligned_to(dy, vb) || !aligned_to(dx, vb) || !aligned_to(dz, vb) ||
+      p->x_stride % vec || p->dy_stride % vec || (gated && p->z_stride % vec))
+    vec = 1;
+  norm_layout(p, vec, true, &k);
+  k.x = x; k.z = z; k.dy = dy; k.w = weight; k.b = bias; k.dx = dx; k.dz = dz; k.dw = dweight; k.db = dbias;
+  k.x_stride = p->x_stride; k.z_stride = p->z_stride; k.dy_stride = p->dy_stride;
+  k.ws = static_cast<float*>(workspace);
+  return from_hip(ss::launch_group_norm(k, static_cast<hipStream_t>(stream)));
+}
+
+ss_status ss_pack_requests(int64_t requests, int64_t tokens, const int32_t* new_tokens, const int32_t* slots,
+                           const int32_t* seen, int32_t* rows, int32_t* taken, int32_t* step_slots,
+                           int32_t* cu_seqlens, int32_t* prompt_slots, int32_t* has_state, int32_t* row_request,
+                           int32_t* row_position, void* stream) {
+  if (requests < 1 || tokens < 1 || requests > kMaxSeqs || tokens > kMaxTokens) return SS_ERR_BAD_SHAPE;
+  const size_t n = (size_t)requests * 4, t = (size_t)tokens * 4;
+  const Span in[] = {{new_tokens, n}, {slots, n}, {seen, n}};
+  const Span outs[] = {{rows, n}, {taken, n}, {step_slots, n}, {cu_seqlens, n + 4}, {prompt_slots, n}, {has_state, n},
+                       {row_request, t}, {row_position, t}};
+  for (const Span& a : in) {
+    if (!a.ptr) return SS_ERR_NULL_ARG;
+    if (!aligned(a.ptr)) return SS_ERR_MISALIGNED;
+  }
+  for (const Span& a : outs) {
+    if (!a.ptr) return SS_ERR_NULL_ARG;
+    if (!aligned(a.ptr)) return SS_ERR_MISALIGNED;
+  }
+  if (conflict(in, outs)) return SS_ERR_UNSUPPORTED;
+  ss::PackParams k{new_tokens, slots, seen, rows, taken, step_slots, cu_seqlens, prompt_slots, has_state, row_request,
+                   row_position, (int32_t)requests, (int32_t)tokens};
+  return from_hip(ss::launch_pack(k, static_cast<hipStream_t>(stream)));
 }
 
 ss_status ss_copy_probe(const void* src, void* dst, size_t bytes, void* stream) {

@@ -296,12 +296,83 @@ struct SsdPromptParams {
   int32_t chunks;            // chunk places: tokens / 256 + nseqs
 };
 
+// One walk of the linear attention kernel over the rows of every sequence (ss_linattn.hip).
+struct LinWalk {
+  const void *a, *b, *c;     // (tokens, heads or shared heads, dc), the same, and (.., dout); rows *_stride elements apart
+  int64_t a_stride, b_stride, c_stride;
+  int32_t a_kv, b_kv, c_kv;  // its heads are the shared ones
+  int32_t dc, dout;
+  int32_t rev;               // from the last row
+  int32_t c_inner;           // states lie (dout, dc) in memory
+  void* out;                 // (tokens, heads, dout), I/O dtype; fp32 if sum
+  void* sum;                 // where the shared heads' sums of out go, or null
+  const float* init;         // (sequences or slots, heads, dv, dk) or null
+  float* fin;                // like init, or null
+  float m_scale, e_scale, u_scale;  // of the pairs inside a chunk, of the state in the rows, of the rows in the state
+};
+
+struct LinParams {
+  int32_t io;
+  LinWalk job[3];
+  int32_t jobs;              // walks
+  int32_t job0, njobs;       // those of a launch
+  const float* log_decay;    // (heads)
+  const int32_t* cu;         // (nseqs + 1) or null: sequences of tokens / nseqs rows
+  const int32_t* slots;      // with pool: (nseqs) or null, sequence s has slot s
+  const int32_t* has_state;  // with pool: (nseqs) or null, none has
+  int32_t pool;              // states lie in slots, else by sequence
+  int32_t zero_rest;         // rows of no sequence get outputs of zero
+  int32_t split;             // this launch computes the segments' own states
+  float* ws;                 // (places, jobs, heads, dk * dv): a segment's own state, then the state that enters it
+  int32_t tokens, nseqs, nslots, heads, share;  // share: heads to a key and value
+  int32_t logq;              // a segment has 2^logq rows
+  int32_t places;
+};
+
+struct LinStepParams {
+  int32_t io;
+  const void *q, *k, *v;     // (rows, heads, dk), (rows, heads / share, dk), (rows, heads / share, dv)
+  const float* log_decay;
+  const int32_t* slots;      // (rows) or null: row r has slot r
+  float* state;              // (nslots, heads, dv, dk)
+  void* y;                   // (rows, heads, dv)
+  int64_t q_stride, k_stride, v_stride;
+  float scale;
+  int32_t rows, nslots, heads, share, dk, dv;
+};
+
+// A workgroup: block_groups groups of row_lanes rows, `lanes` threads a group.
+struct NormParams {
+  int32_t io;
+  int32_t mode;              // ss_norm_mode
+  int32_t center;
+  const void *x, *z, *dy;    // (rows, groups * size), rows *_stride elements apart; dy: gradients are asked for
+  const float *w, *b;        // (groups * size) or null
+  void *y, *dx, *dz;         // dx, dz without gaps
+  float *dw, *db;            // or null
+  float* ws;                 // (row_blocks, 2, groups * size): sums of dw and db
+  int64_t x_stride, z_stride, dy_stride, y_stride, rows;
+  float eps;
+  int32_t groups, size, vec, lanes, block_groups, row_lanes;
+  int32_t blocks, row_blocks;  // workgroups over the groups and over the rows
+};
+
+struct PackParams {
+  const int32_t *new_tokens, *slots, *seen;  // (requests)
+  int32_t *rows, *taken, *step_slots, *cu, *prompt_slots, *has_state, *row_request, *row_position;
+  int32_t requests, tokens;
+};
+
 int64_t conv_bwd_units(int64_t batch, int64_t seqlen);
 hipError_t launch_conv_bwd(const ConvBwdParams& p, hipStream_t st);
 hipError_t launch_ssd_bwd(int32_t io, const SsdBwdParams& p, hipStream_t st);
 hipError_t launch_conv_prompt(const ConvPromptParams& p, hipStream_t st);
 hipError_t launch_ssd_step(const SsdStepParams& p, hipStream_t st);
 hipError_t launch_ssd_prompt(const SsdPromptParams& p, hipStream_t st);
+hipError_t launch_linattn(const LinParams& p, hipStream_t st);
+hipError_t launch_linattn_step(const LinStepParams& p, hipStream_t st);
+hipError_t launch_group_norm(const NormParams& p, hipStream_t st);
+hipError_t launch_pack(const PackParams& p, hipStream_t st);
 hipError_t launch_fwd(const FwdParams& p, int64_t nchunks, hipStream_t st);
 int64_t device_cus();
 hipError_t launch_ssd(const SsdParams& p, hipStream_t st);

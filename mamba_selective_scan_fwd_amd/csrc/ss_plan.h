@@ -37,4 +37,15 @@ inline int pass_ahead(int64_t workgroups, int64_t chunks, int64_t nseqs, int64_t
   return workgroups <= 4 * cus && chunks >= 8 * nseqs ? 16 : 4;
 }
 
+// Rows of the segments, 2^this, in which linear attention walks its sequences: the
+// longest that give two workgroups to a CU (a sequence of `longest` rows at the
+// most, all of them `tokens`), 128 at the least; kLinWhole where that splits none.
+constexpr int kLinWhole = 30;
+inline int lin_segments(int64_t tokens, int64_t nseqs, int64_t longest, int64_t walks, int64_t cus) {
+  if (nseqs * longest == tokens && nseqs * walks >= cus) return kLinWhole;  // all alike, and enough of them
+  int logq = 7;
+  while (logq < kLinWhole && (tokens >> (logq + 1)) * walks >= 2 * cus) ++logq;
+  return ((int64_t)1 << logq) >= longest ? kLinWhole : logq;
+}
+
 }  // namespace ss

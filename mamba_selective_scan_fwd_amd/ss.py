@@ -62,6 +62,21 @@ class ss_ssd_step_problem(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class ss_linattn_problem(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("nseqs", ctypes.c_int64), ("nslots", ctypes.c_int64),
+                ("nheads", ctypes.c_int64), ("kv_heads", ctypes.c_int64), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("dk", ctypes.c_int32),
+                ("dv", ctypes.c_int32), ("io_dtype", ctypes.c_int32), ("packed", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class ss_norm_problem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("channels", ctypes.c_int64), ("ngroups", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+                ("dy_stride", ctypes.c_int64), ("eps", ctypes.c_float), ("io_dtype", ctypes.c_int32),
+                ("mode", ctypes.c_int32), ("center", ctypes.c_int32)]
+
+
 _vp = ctypes.c_void_p
 _lib = None
 
@@ -70,7 +85,10 @@ EXPORTS = ("ss_fwd", "ss_fwd_step", "ss_bwd", "ss_fwd_workspace_size", "ss_fwd_w
            "ss_ckpt_count", "ss_status_str", "ss_copy_probe", "ss_alu_probe", "ss_conv1d_fwd", "ss_conv1d_step",
            "ss_ssd_fwd", "ss_ssd_workspace_size", "ss_fwd_noalloc", "ss_fwd_noalloc_max_workspace", "ss_conv1d_prompt",
            "ss_ssd_prompt", "ss_ssd_prompt_workspace_size", "ss_ssd_step", "ss_ssd_step_workspace_size",
-           "ss_ssd_bwd", "ss_ssd_bwd_workspace_size", "ss_conv1d_bwd", "ss_conv1d_bwd_workspace_size")
+           "ss_ssd_bwd", "ss_ssd_bwd_workspace_size", "ss_conv1d_bwd", "ss_conv1d_bwd_workspace_size",
+           "ss_linattn_fwd", "ss_linattn_bwd", "ss_linattn_prompt", "ss_linattn_step", "ss_linattn_workspace_size",
+           "ss_linattn_bwd_workspace_size", "ss_group_norm", "ss_group_norm_bwd", "ss_group_norm_bwd_workspace_size",
+           "ss_pack_requests")
 PROBE_KINDS = {"fma": 0, "exp": 1, "dpp_mul": 2, "scan_step": 3}
 
 
@@ -135,6 +153,28 @@ def load_library(path: str = LIB_PATH):
     lib.ss_ssd_step_workspace_size.argtypes = [TP]
     lib.ss_ssd_step.restype = ctypes.c_int
     lib.ss_ssd_step.argtypes = [TP] + [_vp] * 12 + [_vp, ctypes.c_size_t, _vp]
+    LP = ctypes.POINTER(ss_linattn_problem)
+    lib.ss_linattn_workspace_size.restype = ctypes.c_size_t
+    lib.ss_linattn_workspace_size.argtypes = [LP]
+    lib.ss_linattn_bwd_workspace_size.restype = ctypes.c_size_t
+    lib.ss_linattn_bwd_workspace_size.argtypes = [LP]
+    lib.ss_linattn_fwd.restype = ctypes.c_int
+    lib.ss_linattn_fwd.argtypes = [LP] + [_vp] * 8 + [_vp, ctypes.c_size_t, _vp]
+    lib.ss_linattn_bwd.restype = ctypes.c_int
+    lib.ss_linattn_bwd.argtypes = [LP] + [_vp] * 12 + [_vp, ctypes.c_size_t, _vp]
+    lib.ss_linattn_prompt.restype = ctypes.c_int
+    lib.ss_linattn_prompt.argtypes = [LP] + [_vp] * 9 + [_vp, ctypes.c_size_t, _vp]
+    lib.ss_linattn_step.restype = ctypes.c_int
+    lib.ss_linattn_step.argtypes = [LP] + [_vp] * 7 + [_vp]
+    NP = ctypes.POINTER(ss_norm_problem)
+    lib.ss_group_norm.restype = ctypes.c_int
+    lib.ss_group_norm.argtypes = [NP] + [_vp] * 5 + [_vp]
+    lib.ss_group_norm_bwd_workspace_size.restype = ctypes.c_size_t
+    lib.ss_group_norm_bwd_workspace_size.argtypes = [NP]
+    lib.ss_group_norm_bwd.restype = ctypes.c_int
+    lib.ss_group_norm_bwd.argtypes = [NP] + [_vp] * 9 + [_vp, ctypes.c_size_t, _vp]
+    lib.ss_pack_requests.restype = ctypes.c_int
+    lib.ss_pack_requests.argtypes = [ctypes.c_int64, ctypes.c_int64] + [_vp] * 11 + [_vp]
     lib.ss_copy_probe.restype = ctypes.c_int
     lib.ss_copy_probe.argtypes = [_vp, _vp, ctypes.c_size_t, _vp]
     lib.ss_alu_probe.restype = ctypes.c_int
@@ -883,6 +923,225 @@ class SsdStepCall:
             _check(status)
 
 
+# ---- linear attention with a decay for each head ------------------------------------
+def _heads16(t, name):
+    if t.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError("%s takes fp16 or bf16 data, got %s" % (name, t.dtype))
+    return t.dtype
+
+
+def _flat(t, name):
+    """(B * L, heads, d) of a (B, L, heads, d) tensor: the same memory where its rows lie evenly."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 4:
+        raise ValueError("%s must be a (B, L, heads, d) tensor" % name)
+    return t.flatten(0, 1)
+
+
+def _linattn(q, k, v, log_decay, cu_seqlens, scale, nseqs, nslots, size, keep, vector=True):
+    """(problem, bytes of its workspace, addresses of q, k, v, log_decay and cu_seqlens)."""
+    io, dev = q.dtype, _device(q)
+    if k.dim() != 3 or v.dim() != 3:
+        raise ValueError("k and v must have as many dimensions as q")
+    T, Hn, dk = q.shape
+    Hk, dv = v.shape[1:]
+    qa, qs = _rows(q, io, "q", (T, Hn, dk), dev, keep, vector)
+    ka, ks = _rows(k, io, "k", (T, Hk, dk), dev, keep, vector)
+    va, vs = _rows(v, io, "v", (T, Hk, dv), dev, keep, vector)
+    pr, wsz = _problem(ss_linattn_problem, size, (), T, nseqs, nslots, Hn, Hk, qs, ks, vs, dk, dv, _IO[io],
+                       0 if cu_seqlens is None else 1, dk ** -0.5 if scale is None else float(scale), 0)
+    return pr, wsz, (qa, ka, va, _in(log_decay, torch.float32, "log_decay", (Hn,), dev, keep))
+
+
+def linattn_fwd(q, k, v, log_decay, scale=None, cu_seqlens=None, h0=None, return_final_state=False, y=None,
+                workspace=None):
+    """Linear attention with a decay for each head: H <- exp(log_decay) H + v k^T, y = scale H q.  q:
+    (B, L, H, dk); k: (B, L, G, dk); v: (B, L, G, dv) in fp16 or bf16, G dividing H, dk and dv 64 or 128,
+    tokens may lie apart (slices of a projection's output); log_decay: (H,) fp32, at most 0; scale: dk^-0.5
+    unless given.  cu_seqlens: (S + 1,) int32 offsets into the B*L tokens, the documents that they hold
+    (default: every row of the batch is one; tokens of none give 0); h0: (S, H, dv, dk) fp32 (S = B without
+    cu_seqlens).  Returns y (B, L, H, dv), or (y, final_state)."""
+    lib = load_library()
+    io = _heads16(q, "linattn_fwd")
+    dev, keep, f32 = _device(q), [], torch.float32
+    B, L, Hn, dk = q.shape
+    dv = v.shape[-1]
+    S = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    pr, wsz, at = _linattn(_flat(q, "q"), _flat(k, "k"), _flat(v, "v"), log_decay, cu_seqlens, scale, S, 0,
+                           "ss_linattn_workspace_size", keep)
+    if y is None:
+        y = q.new_empty((B, L, Hn, dv))
+    fin = q.new_empty((S, Hn, dv, dk), dtype=f32) if return_final_state else None
+    wa = None
+    if wsz:
+        workspace, wa, wsz = _scratch(workspace, wsz, dev)
+    _launch(dev, lib.ss_linattn_fwd, pr, *at, _in(cu_seqlens, torch.int32, "cu_seqlens", (S + 1,), dev, keep),
+            _in(h0, f32, "h0", (S, Hn, dv, dk), dev, keep), _inplace(y, io, "y", (B, L, Hn, dv), dev),
+            None if fin is None else fin.data_ptr(), wa, wsz)
+    return (y, fin) if return_final_state else y
+
+
+def linattn_bwd(q, k, v, log_decay, dy, scale=None, cu_seqlens=None, h0=None, dfinal=None, want_dh0=False,
+                workspace=None):
+    """Gradients of linattn_fwd for the loss sum(dy * y) + sum(dfinal * final_state); the inputs as given to
+    it (nothing else of the forward is needed).  Returns a dict: dq, dk, dv in the data's dtype, dh0 fp32 when
+    want_dh0.  log_decay is a constant of the layer and has none."""
+    lib = load_library()
+    io = _heads16(q, "linattn_bwd")
+    dev, keep, f32 = _device(q), [], torch.float32
+    B, L, Hn, dk = q.shape
+    dv = v.shape[-1]
+    S = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    st = (S, Hn, dv, dk)
+    pr, wsz, at = _linattn(_flat(q, "q"), _flat(k, "k"), _flat(v, "v"), log_decay, cu_seqlens, scale, S, 0,
+                           "ss_linattn_bwd_workspace_size", keep)
+    g = {"dq": q.new_empty(q.shape), "dk": k.new_empty(k.shape), "dv": v.new_empty(v.shape)}
+    if want_dh0:
+        g["dh0"] = q.new_empty(st, dtype=f32)
+    wa = None
+    if wsz:
+        workspace, wa, wsz = _scratch(workspace, wsz, dev)
+    _launch(dev, lib.ss_linattn_bwd, pr, *at, _in(cu_seqlens, torch.int32, "cu_seqlens", (S + 1,), dev, keep),
+            _in(h0, f32, "h0", st, dev, keep), _in(dy, io, "dy", (B, L, Hn, dv), dev, keep),
+            _in(dfinal, f32, "dfinal", st, dev, keep), *(_ptr_of(g, n) for n in ("dq", "dk", "dv", "dh0")), wa, wsz)
+    return g
+
+
+def linattn_prompt(q, k, v, log_decay, cu_seqlens, state, scale=None, slots=None, has_state=None, y=None,
+                   workspace=None):
+    """linattn_fwd of packed prompts from and into state slots.  q: (T, H, dk); k: (T, G, dk); v: (T, G, dv);
+    cu_seqlens, slots, has_state as in conv1d_prompt; state: (slots, H, dv, dk) fp32, updated in place.
+    Returns y (T, H, dv); rows of no prompt are not written."""
+    lib = load_library()
+    io = _heads16(q, "linattn_prompt")
+    dev, keep, i32 = _device(q), [], torch.int32
+    T, Hn, dk = q.shape
+    dv = v.shape[-1]
+    S, nslots = cu_seqlens.numel() - 1, state.shape[0]
+    if y is None:
+        y = q.new_empty((T, Hn, dv))
+    pr, wsz, at = _linattn(q, k, v, log_decay, cu_seqlens, scale, S, nslots, "ss_linattn_workspace_size", keep)
+    wa = None
+    if wsz:
+        workspace, wa, wsz = _scratch(workspace, wsz, dev)
+    _launch(dev, lib.ss_linattn_prompt, pr, *at, _in(cu_seqlens, i32, "cu_seqlens", (S + 1,), dev, keep),
+            _in(slots, i32, "slots", (S,), dev, keep), _in(has_state, i32, "has_state", (S,), dev, keep),
+            _inplace(state, torch.float32, "state", (nslots, Hn, dv, dk), dev), _inplace(y, io, "y", (T, Hn, dv), dev),
+            wa, wsz)
+    return y
+
+
+def linattn_step(q, k, v, log_decay, state, scale=None, slots=None, y=None):
+    """One token of many requests through linear attention, over state slots.  q: (n, H, dk); k: (n, G, dk);
+    v: (n, G, dv), rows may lie apart; state: (slots, H, dv, dk) fp32, updated in place; slots as in
+    ssd_step.  Returns y (n, H, dv)."""
+    lib = load_library()
+    io = _heads16(q, "linattn_step")
+    dev, keep = _device(q), []
+    n, Hn, dk = q.shape
+    dv, nslots = v.shape[-1], state.shape[0]
+    if y is None:
+        y = q.new_empty((n, Hn, dv))
+    pr, _, at = _linattn(q, k, v, log_decay, None, scale, 1, nslots, None, keep, False)
+    _launch(dev, lib.ss_linattn_step, pr, *at, _in(slots, torch.int32, "slots", (n,), dev, keep),
+            _inplace(state, torch.float32, "state", (nslots, Hn, dv, dk), dev), _inplace(y, io, "y", (n, Hn, dv), dev))
+    return y
+
+
+# ---- grouped norm ------------------------------------------------------------------------
+def _norm(x, weight, bias, z, ngroups, eps, center, silu, gate_first, size, keep, dy=None, y=None):
+    """(problem, bytes of its workspace, addresses of x, weight, bias and z, of dy and of y)."""
+    io = x.dtype
+    if io not in _IO:
+        raise TypeError("unsupported dtype %s" % io)
+    if silu and z is not None:
+        raise ValueError("either silu or a gate z")
+    if gate_first and z is None:
+        raise ValueError("gate_first needs a gate z")
+    dev, f32, C = _device(x), torch.float32, x.shape[-1]
+    rows, n = x.shape, x.numel() // C if C else 0
+    two = (n, C)
+
+    def flat(t, name, keep):
+        if t is None:
+            return None, 0
+        if t.dtype is not io or t.shape != rows or t.get_device() != dev:
+            _refuse(t, io, name, rows, dev)
+        return _rows(t.reshape(two) if t.dim() != 2 else t, io, name, two, dev, keep, False)
+
+    xa, xs = flat(x, "x", keep)
+    za, zs = flat(z, "z", keep)
+    da, ds = flat(dy, "dy", keep)
+    ya, ys = None, 0
+    if y is not None:
+        ya, ys = flat(y, "y", [])
+        if ya != y.data_ptr():
+            raise ValueError("the rows of y must lie whole, at most 2^21 elements apart")
+    mode = 1 if silu else 0 if z is None else 3 if gate_first else 2
+    pr, wsz = _problem(ss_norm_problem, size, (), n, C, ngroups, xs, zs, ys, ds, float(eps), _IO[io], mode,
+                       1 if center else 0)
+    return pr, wsz, (xa, _in(weight, f32, "weight", (C,), dev, keep), _in(bias, f32, "bias", (C,), dev, keep), za), da, ya
+
+
+def group_norm(x, weight=None, bias=None, z=None, ngroups=1, eps=1e-5, center=True, silu=False, gate_first=False, y=None):
+    """Every token's channels normalised in ngroups groups of neighbours: x (.., C) fp32/fp16/bf16, rows may
+    lie apart; weight, bias: (C,) fp32 or None; center: subtract the group's mean; silu: SiLU of the result;
+    z: like x, a gate: the result times SiLU(z), or, gate_first, x times SiLU(z) before the norm (Mamba-2's
+    gated norm, with center=False).  Returns y, like x."""
+    lib = load_library()
+    keep = []
+    if y is None:
+        y = x.new_empty(x.shape)
+    pr, _, at, _, ya = _norm(x, weight, bias, z, ngroups, eps, center, silu, gate_first, None, keep, y=y)
+    _launch(_device(x), lib.ss_group_norm, pr, *at, ya)
+    return y
+
+
+def group_norm_bwd(x, weight, dy, bias=None, z=None, ngroups=1, eps=1e-5, center=True, silu=False, gate_first=False,
+                   workspace=None):
+    """Gradients of group_norm for the loss sum(dy * y); the inputs as given to it.  Returns a dict: dx and dz
+    (with z) in x's dtype, dweight (with weight) and dbias (with bias) fp32."""
+    lib = load_library()
+    keep, dev = [], _device(x)
+    pr, wsz, at, da, _ = _norm(x, weight, bias, z, ngroups, eps, center, silu, gate_first,
+                               "ss_group_norm_bwd_workspace_size", keep, dy=dy)
+    g = {"dx": x.new_empty(x.shape)}
+    if weight is not None:
+        g["dweight"] = x.new_empty(weight.shape, dtype=torch.float32)
+    if bias is not None:
+        g["dbias"] = x.new_empty(bias.shape, dtype=torch.float32)
+    if z is not None:
+        g["dz"] = x.new_empty(x.shape)
+    workspace, wa, wsz = _scratch(workspace, wsz, dev)
+    _launch(dev, lib.ss_group_norm_bwd, pr, *at, da, *(_ptr_of(g, n) for n in ("dx", "dweight", "dbias", "dz")), wa, wsz)
+    return g
+
+
+# ---- the maps of a serving batch ---------------------------------------------------------
+def pack_requests(new_tokens, slots, seen, tokens):
+    """What the serving calls take of a batch, from its requests, on the GPU.  new_tokens, slots, seen: (R,)
+    int32: a request's tokens to run, its slot (negative: idle) and the tokens behind it; tokens: the batch's
+    rows.  Single tokens of running requests come first, a row each, then the prompts; what does not fit is cut.
+    Returns a dict of int32 tensors: rows, taken (R,): a request's first row (-1: none) and its rows; step_slots
+    (R,): for ssd_step and linattn_step on the batch's first rows; cu_seqlens (R + 1,), prompt_slots and
+    has_state (R,): for conv1d_prompt, ssd_prompt and linattn_prompt; row_request, row_position (tokens,): a
+    row's request and its token's position (-1 behind the last row)."""
+    lib = load_library()
+    dev, keep, i32 = _device(new_tokens), [], torch.int32
+    R = new_tokens.numel()
+    at = [_in(t, i32, name, (R,), dev, keep)
+          for t, name in ((new_tokens, "new_tokens"), (slots, "slots"), (seen, "seen"))]
+    # every output on a 16-byte boundary of one allocation
+    sizes = dict(rows=R, taken=R, step_slots=R, cu_seqlens=R + 1, prompt_slots=R, has_state=R, row_request=tokens,
+                 row_position=tokens)
+    buf = new_tokens.new_empty(sum((n + 3) // 4 * 4 for n in sizes.values()))
+    out, base = {}, 0
+    for name, n in sizes.items():
+        out[name] = buf[base:base + n]
+        base += (n + 3) // 4 * 4
+    _launch(dev, lib.ss_pack_requests, R, tokens, *at, *(t.data_ptr() for t in out.values()))
+    return out
+
+
 def copy_probe(src, dst):
     """Device copy with the library's streaming copy kernel (bandwidth reference)."""
     lib = load_library()
@@ -1019,3 +1278,53 @@ def ssd_scan_fn(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, dt_softplus=True
     computes the gradients of all inputs but h0 together, whichever are asked for.  In a captured
     graph as conv1d_fn."""
     return SsdScanFn.apply(x, dt, A, Bm, Cm, D, z, dt_bias, dt_softplus, seq_idx, h0, return_final_state)
+
+
+class LinAttnFn(torch.autograd.Function):
+    """autograd wrapper: forward = ss_linattn_fwd, backward = ss_linattn_bwd (only the inputs are kept).
+    Differentiable in q, k, v and h0; with return_final_state the final state is a second output."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, log_decay, scale, cu_seqlens, h0, return_final_state):
+        ctx.save_for_backward(q, k, v, log_decay, cu_seqlens, h0)
+        ctx.scale = scale
+        return linattn_fwd(q, k, v, log_decay, scale=scale, cu_seqlens=cu_seqlens, h0=h0,
+                           return_final_state=return_final_state)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dfinal=None):
+        q, k, v, log_decay, cu_seqlens, h0 = ctx.saved_tensors
+        g = linattn_bwd(q, k, v, log_decay, dy.contiguous(), scale=ctx.scale, cu_seqlens=cu_seqlens, h0=h0,
+                        dfinal=dfinal, want_dh0=ctx.needs_input_grad[6])
+        return g["dq"], g["dk"], g["dv"], None, None, None, g.get("dh0"), None
+
+
+def linattn_fn(q, k, v, log_decay, scale=None, cu_seqlens=None, h0=None, return_final_state=False):
+    """linattn_fwd, differentiable once: y, or (y, final_state) with return_final_state.  log_decay is a
+    constant of the layer: one that requires a gradient is refused.  In a captured graph as conv1d_fn."""
+    if log_decay.requires_grad:
+        raise ValueError("log_decay has no gradient: pass it detached")
+    return LinAttnFn.apply(q, k, v, log_decay, scale, cu_seqlens, h0, return_final_state)
+
+
+class GroupNormFn(torch.autograd.Function):
+    """autograd wrapper: forward = ss_group_norm, backward = ss_group_norm_bwd (only the inputs are kept)."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, z, ngroups, eps, center, silu, gate_first):
+        ctx.save_for_backward(x, weight, bias, z)
+        ctx.how = dict(ngroups=ngroups, eps=eps, center=center, silu=silu, gate_first=gate_first)
+        return group_norm(x, weight, bias=bias, z=z, **ctx.how)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, weight, bias, z = ctx.saved_tensors
+        g = group_norm_bwd(x, weight, dy, bias=bias, z=z, **ctx.how)
+        return g["dx"], g.get("dweight"), g.get("dbias"), g.get("dz"), None, None, None, None, None
+
+
+def group_norm_fn(x, weight=None, bias=None, z=None, ngroups=1, eps=1e-5, center=True, silu=False, gate_first=False):
+    """group_norm, differentiable once in x, weight, bias and z.  In a captured graph as conv1d_fn."""
+    return GroupNormFn.apply(x, weight, bias, z, ngroups, eps, center, silu, gate_first)
