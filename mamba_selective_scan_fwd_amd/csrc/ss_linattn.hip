@@ -14,6 +14,8 @@
 // so that one kernel computes all four, and nothing of the forward is kept.  From
 // the end the state that enters a chunk is a G (no decay before the first row,
 // one more behind the last), which leaves dh0 behind.
+#include <type_traits>
+
 #include "ss_device.h"
 #include "ss_internal.h"
 #include "ss_mfma.h"
@@ -23,26 +25,43 @@ namespace ss {
 namespace {
 
 constexpr int kC = 64;  // rows of a chunk
-constexpr int kWalkThreads = 256;
 
-// 16-bit tiles of W columns in LDS, 16-byte pieces of a row exchanged by the row:
-// the 16 rows of a fragment read (16 or 8 bytes a lane) and the 4 consecutive
-// rows of a transposing read (32 bytes each) lie in different banks.
+// 16-bit tiles of W columns in LDS, the 16-byte pieces of a row exchanged by the row:
+// piece c of row r lies at c ^ x(r).  The 16 rows of a fragment read (16 or 8 bytes a
+// lane), in whichever halves they are served, and the 4 consecutive rows (32 bytes
+// each) of two of a transposing read's lane groups lie in different banks.
 template <int W>
-__device__ __forceinline__ int tile_off(int row, int col) {
+__device__ __forceinline__ constexpr int tile_x(int row) {
   static_assert(W == 64 || W == 128, "tile width");
-  const int x = W == 128 ? ((row & 3) << 1) | ((row >> 2) & 1) | (((row >> 3) & 1) << 3)
-                         : (((row >> 1) & 1) << 1) | ((row >> 2) & 1) | (((row >> 3) & 1) << 2);
-  return row * W + 8 * ((col >> 3) ^ x) + (col & 7);
+  const int q = (row >> 2) & 3, low = q >> 1, high = (q ^ (q >> 1)) & 1;  // Gray code of the row's quarter of 16
+  return W == 128 ? ((row & 3) << 1) | low | (high << 3) : (((row >> 1) & 1) << 1) | low | (high << 2);
 }
-__device__ __forceinline__ u32x4v lds16(const uint16_t* at) { return *reinterpret_cast<const u32x4v*>(at); }
-__device__ __forceinline__ uint2 lds8(const uint16_t* at) { return *reinterpret_cast<const uint2*>(at); }
-
-// rows row0 .. row0 + 31 (row0 a multiple of 16) of the columns 16 ct .. as an operand whose k axis is the row
 template <int W>
-__device__ __forceinline__ u32x4v time_frag(const uint16_t* tile, int row0, int ct, int lane) {
-  const int j = lane % 16, g = lane / 16, row = 8 * g + j / 4, col = 16 * ct + 4 * (j % 4);
-  return tm_frag(tile + row0 * W, tile_off<W>(row, col), tile_off<W>(row + 4, col));
+__device__ __forceinline__ constexpr int tile_off(int row, int col) {
+  return row * W + 8 * ((col >> 3) ^ tile_x<W>(row)) + (col & 7);
+}
+__device__ __forceinline__ u32x4v lds16(const char* at) { return *reinterpret_cast<const u32x4v*>(at); }
+__device__ __forceinline__ uint2 lds8(const char* at) { return *reinterpret_cast<const uint2*>(at); }
+
+// Where a lane's fragments lie in a tile, in bytes: other columns are another power of
+// two exclusive-or'ed in, other rows (multiples of 16) an immediate offset.
+// rows l16, the columns 32 ks + 8 (lane / 16) ..: row_frag ^ 64 ks
+template <int W>
+__device__ __forceinline__ uint32_t row_frag(int lane) { return 2 * tile_off<W>(lane % 16, 8 * (lane / 16)); }
+// rows l16, the columns 16 i + 4 (lane / 16) ..: quad_frag ^ 32 i
+template <int W>
+__device__ __forceinline__ uint32_t quad_frag(int lane) { return 2 * tile_off<W>(lane % 16, 4 * (lane / 16)); }
+// the columns 16 i .. as an operand whose k axis is the row: time_frag ^ 32 i
+template <int W>
+__device__ __forceinline__ uint32_t time_frag(int lane) {
+  return 2 * tile_off<W>(8 * (lane / 16) + lane % 16 / 4, 4 * (lane % 4));
+}
+// rows row0 .. + 31 of it
+template <int W>
+__device__ __forceinline__ u32x4v read_time_frag(const char* tile, uint32_t at, int row0) {
+  constexpr uint32_t kNext = W == 128 ? 128 : 64;  // the rows 4 further on: x differs in its highest bit
+  const uint16_t* rows = reinterpret_cast<const uint16_t*>(tile + row0 * (W * 2));
+  return tm_frag(rows, (int)(at / 2), (int)((at ^ kNext) / 2 + 4 * W));
 }
 
 // The rows that workgroup place `place` walks.
@@ -91,19 +110,47 @@ __device__ __forceinline__ void lin_states(const LinParams& p, const LinWalk& w,
 // element (c, o) of a state in memory: (dv, dk), c being the side that is contracted with a
 __device__ __forceinline__ int state_at(const LinWalk& w, int c, int o) { return w.c_inner ? o * w.dc + c : c * w.dout + o; }
 
-// exp(n g) and exp(n g) - 1; n = 0 has no decay, whatever g
-__device__ __forceinline__ double lin_power(float g, int n) { return n ? exp((double)n * (double)g) : 1.0; }
-__device__ __forceinline__ double lin_power_m1(float g, int n) { return n ? expm1((double)n * (double)g) : 0.0; }
+// exp(n g), its exponent formed in 64 bits; n = 0 has no decay, whatever g
+__device__ __forceinline__ float lin_power(float g, int n) {
+  if (n == 0) return 1.0f;
+  const double x = (double)n * (double)g * 1.4426950408889634074;
+  if (x <= -200.0) return 0.0f;  // below fp32's smallest
+  if (!(x < 200.0)) return x > 0.0 ? __builtin_inff() : (float)x;
+  const double whole = rint(x);
+  return ldexpf(exp2_hw((float)(x - whole)), (int)whole);
+}
+// exp(n g) - 1, for H <- H + (exp(n g) - 1) H: a slow decay's own rounding would add up
+// over the chunks that it takes
+__device__ __forceinline__ float lin_power_m1(float g, int n) {
+  const double x = n ? (double)n * (double)g : 0.0;
+  if (!(x > -0.25 && x < 0.25)) return (float)((double)lin_power(g, n) - 1.0);
+  double s = 1.0;  // the power series: 0.25^12 / 13! is below 2^-56
+#pragma unroll
+  for (int k = 12; k > 1; --k) s = fma(s, x * (1.0 / k), 1.0);
+  return (float)(s * x);
+}
 
 // ---- the walk ----------------------------------------------------------------------
+// Wave w has the columns o = 16 w .. of the outputs and of the state, the state as
+// accumulators.  Two workgroups share a CU.  A chunk's operands come into LDS without
+// registers in between: b, which is in use from a chunk's begin to its end, a chunk
+// ahead in one of two buffers; a, once the last chunk's is used, for the next; c, which
+// is not needed before the pairs' weights are made, at its chunk's begin.
+template <int DO> constexpr int walk_threads() { return 4 * DO; }
+constexpr int walk_waves_per_simd(int dc, int dout) { return dout == 128 ? 4 : dc == 64 ? 3 : 2; }
+// Weights by number, of rows in E' (0 .. 63), powers of a (64 .. 129) and a^rows - 1
+// of a whole chunk and of the last one (160, 161): with M they lie in the columns of
+// its first rows that no pair has, so that two workgroups have LDS's 160 KB
+constexpr int kPowers = 64, kDecays = 160;
 template <int DC, int DO, bool STATE>
 struct WalkLds {
-  float power[kC + 4];  // a^i
-  float decay[2];       // a^rows - 1 of a whole chunk and of the last one
   __attribute__((aligned(16))) uint16_t a[STATE ? 8 : kC * DC];
-  __attribute__((aligned(16))) uint16_t b[kC * DC];
-  __attribute__((aligned(16))) uint16_t c[kC * DO];
-  __attribute__((aligned(16))) uint16_t m[STATE ? 1 : 2][STATE ? 8 : kC * kC];
+  __attribute__((aligned(16))) uint16_t b[2][kC * DC];
+  __attribute__((aligned(16))) uint16_t c[STATE ? 2 : 1][kC * DO];
+  __attribute__((aligned(16))) uint16_t m[STATE ? 1 : 2][STATE ? 512 : kC * kC];
+  __device__ __forceinline__ float* weight(int i) {
+    return reinterpret_cast<float*>(&m[0][STATE ? 2 * i : tile_off<kC>(i / 16, 32 + 2 * (i % 16))]);
+  }
 };
 
 // a 16-bit fragment as bf16 parts: one, or two of fp16 data
@@ -122,13 +169,63 @@ struct Parts {
   }
 };
 
+// v as two fp16 parts, |v - hi - lo| <= 2^-22 |v| where |v| is within a factor of 2^15 of the
+// largest that its scale is taken from (2^-38 of that one below)
+__device__ __forceinline__ void split2_f16(float v0, float v1, uint32_t& hi, uint32_t& lo) {
+  hi = pack2<SS_F16>(v0, v1);
+  lo = pack2<SS_F16>(v0 - low16<SS_F16>(hi), v1 - high16<SS_F16>(hi));
+}
+// the power of two that takes a wave's largest magnitude to 2^14 .. 2^15, and its inverse
+struct Scale {
+  float to, from;
+};
+__device__ __forceinline__ Scale wave_scale(float most) {
+  most = fmaxf(most, row_ror<8>(most));
+  most = fmaxf(most, row_ror<4>(most));
+  most = fmaxf(most, row_ror<2>(most));
+  most = fmaxf(most, row_ror<1>(most));
+  float x, y;
+  swap_rows(most, x, y);
+  swap_halves(fmaxf(x, y), x, y);
+  const int e = uniform((int)(__float_as_uint(fmaxf(x, y)) >> 23) & 255);
+  const int field = 268 - e < 253 ? 268 - e : 253;
+  return {__uint_as_float((uint32_t)field << 23), __uint_as_float((uint32_t)(254 - field) << 23)};
+}
+
+// A barrier behind this wave's LDS accesses and its memory accesses but the last AHEAD
+// (they end in their order): loads ahead stay in flight through it
+template <int AHEAD>
+__device__ __forceinline__ void lds_barrier() {
+  if constexpr (AHEAD < 0) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(AHEAD) : "memory");
+}
+
+// `rows` rows of W columns into a tile: a wave's load fills 1 KB of it, 16 bytes a lane in
+// the lanes' order, so that the exchange of pieces is made on the memory's side.  Rows
+// behind the last one repeat it: no weight but 0 meets them, and their outputs go nowhere.
+template <int W, int WAVES> constexpr int tile_loads() { return kC * W / 512 / WAVES; }
+template <int W, int WAVES>
+__device__ __forceinline__ void load_tile(uint16_t* tile, const void* at, int64_t stride, int rows, bool rev, int wave, int lane) {
+  constexpr int kRows = 512 / W, kLoads = tile_loads<W, WAVES>();  // rows of a load, loads of a wave
+  const auto v = rows_view(at, stride * 2, rows, W * 2);
+#pragma unroll
+  for (int k = 0; k < kLoads; ++k) {
+    const int first = (wave * kLoads + k) * kRows, row = first + lane / (W / 8);
+    const int piece = lane % (W / 8) ^ tile_x<W>(row);
+    const int in = row < rows ? row : rows - 1;
+    const uint32_t off = (uint32_t)(rev ? rows - 1 - in : in) * (uint32_t)(stride * 2) + (uint32_t)piece * 16u;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(v, (__attribute__((address_space(3))) void*)(tile + first * W), 16, off, 0, 0, 0);
+  }
+}
+
 template <int IO, int DC, int DO, bool STATE>
-__global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) {
-  constexpr int CT = DC / 16, OT = DO / 64;  // state tiles of a wave: all of c, a quarter of o
-  constexpr int NB = DC / 32, NO = DO / 32;  // 16-byte pieces of a thread
+__global__ void __launch_bounds__(walk_threads<DO>(), walk_waves_per_simd(DC, DO)) lin_walk_kernel(LinParams p) {
+  constexpr int CT = DC / 16, WAVES = DO / 16;
+  constexpr int kPairs = (10 + WAVES - 1) / WAVES;  // 16 x 16 tiles of pairs a wave
   constexpr bool kTwo = IO == SS_F16;
   __shared__ WalkLds<DC, DO, STATE> lds;
-  const int tid = threadIdx.x, lane = tid % 64, wave = uniform(tid / 64), l16 = lane % 16, g4 = 4 * (lane / 16);
+  const int tid = threadIdx.x, wave = uniform(tid / 64);
+  int lane = tid % 64, l16 = lane % 16, g4 = 4 * (lane / 16);
   const int lb = (int)xcd_logical_block();
   const int job = p.job0 + lb % p.njobs, h = lb / p.njobs % p.heads, place = lb / p.njobs / p.heads;
   const LinWalk& w = p.job[job];
@@ -146,274 +243,303 @@ __global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) 
     }
   }
   if (!q.live || (STATE && q.last)) return;
-  const float g = p.log_decay[h];
-  const int tail = q.rows % kC;
-  if (tid < kC + 2) lds.power[tid] = (float)lin_power(g, tid);
-  if (tid >= 128 && tid < 130) lds.decay[tid - 128] = (float)lin_power_m1(g, tid == 128 ? kC : tail);
-  if constexpr (!STATE)
-    for (int k = tid; k < 2 * kC * kC / 8; k += kWalkThreads) reinterpret_cast<u32x4v*>(lds.m)[k] = u32x4v{0, 0, 0, 0};
 
-  // ---- loads of a chunk: rows t .. of the segment, in the walk's order
+  // ---- loads for the chunk that begins at row t of the segment, in the walk's order
   const bool rev = w.rev != 0;
-  u32x4v ar[STATE ? 1 : NB], br[NB], cr[NO];
-  auto load = [&](int t) {
-    const int rows = q.rows - t < kC ? q.rows - t : kC;
-    const int64_t tok = rev ? (int64_t)q.begin + q.len - (q.t0 + t + rows) : (int64_t)q.begin + q.t0 + t;
-    auto view = [&](const void* at, int64_t stride, int head, int cols) {
-      return rows_view(static_cast<const char*>(at) + (tok * stride + head * cols) * 2, stride * 2, rows, cols * 2);
-    };
-    auto off = [&](int row, int64_t stride, int col) {
-      return row < rows ? (uint32_t)(rev ? rows - 1 - row : row) * (uint32_t)(stride * 2) + (uint32_t)col * 2u : kOffNone;
-    };
-    const auto bv = view(w.b, w.b_stride, w.b_kv ? kvh : h, DC);
-    const auto cv = view(w.c, w.c_stride, w.c_kv ? kvh : h, DO);
-#pragma unroll
-    for (int k = 0; k < NB; ++k)
-      br[k] = vload16(bv, off(tid / (DC / 8) + k * (2048 / DC), w.b_stride, 8 * (tid % (DC / 8))));
-#pragma unroll
-    for (int k = 0; k < NO; ++k)
-      cr[k] = vload16(cv, off(tid / (DO / 8) + k * (2048 / DO), w.c_stride, 8 * (tid % (DO / 8))));
-    if constexpr (!STATE) {
-      const auto av = view(w.a, w.a_stride, w.a_kv ? kvh : h, DC);
-#pragma unroll
-      for (int k = 0; k < NB; ++k)
-        ar[k] = vload16(av, off(tid / (DC / 8) + k * (2048 / DC), w.a_stride, 8 * (tid % (DC / 8))));
-    }
+  auto chunk_rows = [&](int t) { return q.rows - t < kC ? q.rows - t : kC; };
+  auto chunk_tok = [&](int t, int rows) {
+    return rev ? (int64_t)q.begin + q.len - (q.t0 + t + rows) : (int64_t)q.begin + q.t0 + t;
   };
-  load(0);
+  auto chunk_at = [&](const void* base, int t, int64_t stride, int head, int cols) {
+    return static_cast<const char*>(base) + (chunk_tok(t, chunk_rows(t)) * stride + head * cols) * 2;
+  };
+  auto load_a = [&](int t) {
+    load_tile<DC, WAVES>(lds.a, chunk_at(w.a, t, w.a_stride, w.a_kv ? kvh : h, DC), w.a_stride, chunk_rows(t), rev, wave, lane);
+  };
+  auto load_b = [&](int t, int turn) {
+    load_tile<DC, WAVES>(lds.b[turn], chunk_at(w.b, t, w.b_stride, w.b_kv ? kvh : h, DC), w.b_stride, chunk_rows(t), rev, wave, lane);
+  };
+  auto load_c = [&](int t, int turn) {
+    load_tile<DO, WAVES>(lds.c[turn], chunk_at(w.c, t, w.c_stride, w.c_kv ? kvh : h, DO), w.c_stride, chunk_rows(t), rev, wave, lane);
+  };
+  if (q.rows > 0) {
+    load_b(0, 0);
+    if constexpr (STATE) load_c(0, 0);
+    else load_a(0);
+  }
+
+  const float g = p.log_decay[h];
+  const int later = rev ? 0 : 1;  // the entering state decays before its first row, or behind the last
+  auto set_weights = [&](int rows) {  // of the rows in E'
+    if (tid < kC) *lds.weight(tid) = tid < rows ? w.u_scale * lin_power(g, rows - tid - later) : 0.0f;
+  };
+  set_weights(chunk_rows(0));
+  if (tid >= 64 && tid < 64 + kC + 2) *lds.weight(kPowers + tid - 64) = lin_power(g, tid - 64);
+  if (tid >= 192 && tid < 194) *lds.weight(kDecays + tid - 192) = lin_power_m1(g, tid == 192 ? kC : q.rows % kC);
+  if constexpr (!STATE) {  // M's 16 x 16 tiles above the diagonal that are read with their neighbours
+    if (tid < 128) {
+      const int tile = tid / 32 % 2, row = tid / 2 % 16;
+      *reinterpret_cast<u32x4v*>(&lds.m[tid / 64][tile_off<kC>(32 * tile + row, 16 + 32 * tile + 8 * (tid % 2))]) = u32x4v{0, 0, 0, 0};
+    }
+  }
 
   // ---- the state that enters
   const float* init;
   float* fin;
   lin_states(p, w, q.seq, h, init, fin);
   const bool several = q.len > q.rows;  // the segments' states are in the workspace
-  float* ws = p.ws + (((int64_t)place * p.jobs + job) * p.heads + h) * (DC * DO) + wave * (CT * OT * 256) + lane * 4;
-  f32x4 H[CT][OT];  // element r: c = 16 ct + g4 + r, o = 16 (OT wave + ot) + l16
+  float* ws = p.ws + (((int64_t)place * p.jobs + job) * p.heads + h) * (DC * DO) + wave * (CT * 256) + lane * 4;
+  f32x4 H[CT];  // element r: c = 16 ct + g4 + r, o = 16 wave + l16
   bool have = !STATE && (several || init);
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct)
+  for (int ct = 0; ct < CT; ++ct) {
+    H[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (!STATE && several) {
+      H[ct] = *reinterpret_cast<const f32x4*>(ws + ct * 256);
+    } else if (have) {
+      const float* at = init + state_at(w, 16 * ct + g4, 16 * wave + l16);
+      if (w.c_inner) {
+        H[ct] = *reinterpret_cast<const f32x4*>(at);
+      } else {
 #pragma unroll
-    for (int ot = 0; ot < OT; ++ot) {
-      H[ct][ot] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      if (!STATE && several) {
-        H[ct][ot] = *reinterpret_cast<const f32x4*>(ws + (ct * OT + ot) * 256);
-      } else if (have) {
-        const float* at = init + state_at(w, 16 * ct + g4, 16 * (OT * wave + ot) + l16);
-        if (w.c_inner) {
-          H[ct][ot] = *reinterpret_cast<const f32x4*>(at);
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) H[ct][ot][r] = at[r * DO];
-        }
+        for (int r = 0; r < 4; ++r) H[ct][r] = at[r * DO];
       }
-    }
-  __syncthreads();  // the powers are there
-
-  const int later = rev ? 0 : 1;  // the entering state decays before its first row, or behind the last
-  // weights of the pairs (row t, row s <= t) of this wave's tiles, of E in row t, and of row s in E'
-  float mw[3][4], iw[4], uw[2][8];
-  int tile_t[3], tile_s[3];
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const int n = wave + 4 * i;
-    tile_t[i] = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : n < 10 ? 3 : 4;
-    tile_s[i] = n - tile_t[i] * (tile_t[i] + 1) / 2;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int d = 16 * (tile_t[i] - tile_s[i]) + l16 - g4 - r;
-      mw[i][r] = d >= 0 && d < kC ? w.m_scale * lds.power[d] : 0.0f;
     }
   }
-#pragma unroll
-  for (int tt = 0; tt < 4; ++tt) iw[tt] = w.e_scale * lds.power[16 * tt + l16 + later];
-  auto set_uw = [&](int rows) {
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int n = rows - 32 * ks - 2 * g4 - e - later;  // >= 0 for the rows that are there
-        uw[ks][e] = n >= 0 ? w.u_scale * lds.power[n] : 0.0f;
-      }
-  };
-  set_uw(kC);
+  lds_barrier<0>();  // the weights and the first chunk are there
 
-  for (int t = 0; t < q.rows; t += kC) {
-    const int rows = q.rows - t < kC ? q.rows - t : kC;
+  // weights of the pairs (row t, row s <= t) of this wave's tiles and of E in row t
+  float mw[kPairs][4], iw[4];
+  int tile_t[kPairs], tile_s[kPairs];
+  if constexpr (!STATE) {
 #pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      const int at = tile_off<DC>(tid / (DC / 8) + k * (2048 / DC), 8 * (tid % (DC / 8)));
-      *reinterpret_cast<u32x4v*>(&lds.b[at]) = br[k];
-      if constexpr (!STATE) *reinterpret_cast<u32x4v*>(&lds.a[at]) = ar[k];
+    for (int i = 0; i < kPairs; ++i) {
+      const int n = wave + WAVES * i;
+      tile_t[i] = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : n < 10 ? 3 : 4;
+      tile_s[i] = n - tile_t[i] * (tile_t[i] + 1) / 2;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int d = 16 * (tile_t[i] - tile_s[i]) + l16 - g4 - r;
+        mw[i][r] = d >= 0 && d < kC ? w.m_scale * *lds.weight(kPowers + d) : 0.0f;
+      }
     }
 #pragma unroll
-    for (int k = 0; k < NO; ++k)
-      *reinterpret_cast<u32x4v*>(&lds.c[tile_off<DO>(tid / (DO / 8) + k * (2048 / DO), 8 * (tid % (DO / 8)))]) = cr[k];
-    __syncthreads();
-    if (t + kC < q.rows) load(t + kC);
+    for (int tt = 0; tt < 4; ++tt) iw[tt] = w.e_scale * *lds.weight(kPowers + 16 * tt + l16 + later);
+  }
+  char* const ta = reinterpret_cast<char*>(lds.a);
+  char* const tm = reinterpret_cast<char*>(lds.m);
+  constexpr int kPlane = kC * kC * 2;
 
-    f32x4 out[OT][4];  // element r: o = 16 (OT wave + ot) + g4 + r, row 16 tt + l16
+  // a chunk; false behind the segment's last
+  auto chunk = [&](int t, auto which) {
+    constexpr int turn = decltype(which)::value;
+    const int rows = chunk_rows(t);
+    const bool more = t + kC < q.rows;
+    const char *tb = reinterpret_cast<const char*>(lds.b[turn]), *tc = reinterpret_cast<const char*>(lds.c[STATE ? turn : 0]);
+    // what follows from the lane is rebuilt in every chunk: kept, it would take the registers
+    lane = opaque(lane);
+    l16 = lane % 16;
+    g4 = 4 * (lane / 16);
+    if constexpr (!STATE) load_c(t, 0);
+    if (more) {
+      load_b(t + kC, turn ^ 1);
+      if constexpr (STATE) load_c(t + kC, turn ^ 1);
+    }
+    if (!STATE && t > 0 && rows < kC) set_weights(rows);
+
+    f32x4 out[4];  // element r: o = 16 wave + g4 + r, row 16 tt + l16
     if constexpr (!STATE) {
       // M[t][s] = a^{t-s} (a_t . b_s), a lane with 4 consecutive s of a row t
+      const uint32_t rf = row_frag<DC>(lane), mf = quad_frag<kC>(lane);
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {
+      for (int i = 0; i < kPairs; ++i) {
         if (tile_t[i] > 3) continue;
-        f32x4 acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        const char *bs = tb + tile_s[i] * (16 * DC * 2), *as = ta + tile_t[i] * (16 * DC * 2);
+        f32x4 acc[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
-        for (int ks = 0; ks < DC / 32; ++ks) {
-          const u32x4v bs = lds16(&lds.b[tile_off<DC>(16 * tile_s[i] + l16, 32 * ks + 2 * g4)]);
-          const u32x4v as = lds16(&lds.a[tile_off<DC>(16 * tile_t[i] + l16, 32 * ks + 2 * g4)]);
-          acc = mfma_t<IO>::run(as_vec<IO>(bs), as_vec<IO>(as), acc);
-        }
+        for (int ks = 0; ks < DC / 32; ++ks)
+          acc[ks & 1] = mfma_t<IO>::run(as_vec<IO>(lds16(bs + (rf ^ (64 * ks)))), as_vec<IO>(lds16(as + (rf ^ (64 * ks)))), acc[ks & 1]);
+        acc[0] += acc[1];
         uint32_t h0, h1, l0, l1;
-        split2(acc[0] * mw[i][0], acc[1] * mw[i][1], h0, l0);
-        split2(acc[2] * mw[i][2], acc[3] * mw[i][3], h1, l1);
-        const int at = tile_off<kC>(16 * tile_t[i] + l16, 16 * tile_s[i] + g4);
-        *reinterpret_cast<uint2*>(&lds.m[0][at]) = make_uint2(h0, h1);
-        *reinterpret_cast<uint2*>(&lds.m[1][at]) = make_uint2(l0, l1);
+        split2(acc[0][0] * mw[i][0], acc[0][1] * mw[i][1], h0, l0);
+        split2(acc[0][2] * mw[i][2], acc[0][3] * mw[i][3], h1, l1);
+        char* at = tm + tile_t[i] * (16 * kC * 2) + (mf ^ (uint32_t)(32 * tile_s[i]));
+        *reinterpret_cast<uint2*>(at) = make_uint2(h0, h1);
+        *reinterpret_cast<uint2*>(at + kPlane) = make_uint2(l0, l1);
       }
       // E's part: the accumulators of H are the operand as they lie, its k axis being
       // c = 16 (2 kk) + g4 + 0..3, then 16 (2 kk + 1) + g4 + 0..3; a is read in that order
 #pragma unroll
-      for (int ot = 0; ot < OT; ++ot)
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt) out[ot][tt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int tt = 0; tt < 4; ++tt) out[tt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       if (have) {
+        const uint32_t qf = quad_frag<DC>(lane);
+        Scale sc{1.0f, 1.0f};
+        if constexpr (kTwo) {
+          float most = 0.0f;
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) most = fmaxf(most, fabsf(H[ct][r]));
+          sc = wave_scale(most);
+        }
 #pragma unroll
         for (int kk = 0; kk < CT / 2; ++kk) {
-          u32x4v eh[OT], el[OT];
-#pragma unroll
-          for (int ot = 0; ot < OT; ++ot)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-              for (int r = 0; r < 4; r += 2) {
-                uint32_t hi, lo;
-                split2(H[2 * kk + i][ot][r], H[2 * kk + i][ot][r + 1], hi, lo);
-                eh[ot][2 * i + r / 2] = hi;
-                el[ot][2 * i + r / 2] = lo;
-              }
+          u32x4v eh, el, as[4];
 #pragma unroll
           for (int tt = 0; tt < 4; ++tt) {
-            const uint2 a0 = lds8(&lds.a[tile_off<DC>(16 * tt + l16, 32 * kk + g4)]);
-            const uint2 a1 = lds8(&lds.a[tile_off<DC>(16 * tt + l16, 32 * kk + 16 + g4)]);
-            const Parts<IO> as(u32x4v{a0.x, a0.y, a1.x, a1.y});
-#pragma unroll
-            for (int ot = 0; ot < OT; ++ot) {
-              out[ot][tt] = BF::run(bfv(el[ot]), as.hi, out[ot][tt]);
-              if constexpr (kTwo) out[ot][tt] = BF::run(bfv(eh[ot]), as.lo, out[ot][tt]);
-              out[ot][tt] = BF::run(bfv(eh[ot]), as.hi, out[ot][tt]);
-            }
+            const uint2 a0 = lds8(ta + tt * (16 * DC * 2) + (qf ^ (64 * kk)));
+            const uint2 a1 = lds8(ta + tt * (16 * DC * 2) + (qf ^ (64 * kk + 32)));
+            as[tt] = u32x4v{a0.x, a0.y, a1.x, a1.y};
           }
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; r += 2) {
+              const float v0 = H[2 * kk + i][r], v1 = H[2 * kk + i][r + 1];
+              uint32_t hi, lo;
+              if constexpr (kTwo) split2_f16(v0 * sc.to, v1 * sc.to, hi, lo);
+              else split2(v0, v1, hi, lo);
+              eh[2 * i + r / 2] = hi;
+              el[2 * i + r / 2] = lo;
+            }
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt) out[tt] = mfma_t<IO>::run(as_vec<IO>(el), as_vec<IO>(as[tt]), out[tt]);
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt) out[tt] = mfma_t<IO>::run(as_vec<IO>(eh), as_vec<IO>(as[tt]), out[tt]);
         }
 #pragma unroll
-        for (int ot = 0; ot < OT; ++ot)
-#pragma unroll
-          for (int tt = 0; tt < 4; ++tt) out[ot][tt] *= iw[tt];
+        for (int tt = 0; tt < 4; ++tt) out[tt] *= kTwo ? iw[tt] * sc.from : iw[tt];
       }
-      __syncthreads();  // M is there
+      // M and c are there; b's next loads, issued behind c's, may be on their way
+      if (more) lds_barrier<tile_loads<DC, WAVES>()>();
+      else lds_barrier<0>();
+      if (more) load_a(t + kC);
+      asm volatile("" ::: "memory");  // the outputs' stores come behind
     }
-    u32x4v cf[2][OT];
+    const uint32_t cfa = time_frag<DO>(lane) ^ (uint32_t)(32 * wave);
+    u32x4v cf[2];
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-      for (int ot = 0; ot < OT; ++ot) cf[ks][ot] = time_frag<DO>(lds.c, 32 * ks, OT * wave + ot, lane);
+    for (int ks = 0; ks < 2; ++ks) cf[ks] = read_time_frag<DO>(tc, cfa, 32 * ks);
     if constexpr (!STATE) {
+      const uint32_t mf = row_frag<kC>(lane);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        bf16x8 ch[OT], cl[OT];
-#pragma unroll
-        for (int ot = 0; ot < OT; ++ot) {
-          const Parts<IO> cs(cf[ks][ot]);
-          ch[ot] = cs.hi;
-          cl[ot] = cs.lo;
-        }
+        const Parts<IO> cs(cf[ks]);
+        bf16x8 mh[4], ml[4];
 #pragma unroll
         for (int tt = 2 * ks; tt < 4; ++tt) {
-          const int at = tile_off<kC>(16 * tt + l16, 32 * ks + 2 * g4);
-          const bf16x8 mh = bfv(lds16(&lds.m[0][at])), ml = bfv(lds16(&lds.m[1][at]));
-#pragma unroll
-          for (int ot = 0; ot < OT; ++ot) {
-            out[ot][tt] = BF::run(ch[ot], ml, out[ot][tt]);
-            if constexpr (kTwo) out[ot][tt] = BF::run(cl[ot], mh, out[ot][tt]);
-            out[ot][tt] = BF::run(ch[ot], mh, out[ot][tt]);
-          }
+          const char* at = tm + tt * (16 * kC * 2) + (mf ^ (64 * ks));
+          mh[tt] = bfv(lds16(at));
+          ml[tt] = bfv(lds16(at + kPlane));
         }
+#pragma unroll
+        for (int tt = 2 * ks; tt < 4; ++tt) out[tt] = BF::run(cs.hi, ml[tt], out[tt]);
+        if constexpr (kTwo) {
+#pragma unroll
+          for (int tt = 2 * ks; tt < 4; ++tt) out[tt] = BF::run(cs.lo, mh[tt], out[tt]);
+        }
+#pragma unroll
+        for (int tt = 2 * ks; tt < 4; ++tt) out[tt] = BF::run(cs.hi, mh[tt], out[tt]);
       }
       // ---- outputs: rows past the segment's last go nowhere
-      const int64_t tok = rev ? (int64_t)q.begin + q.len - (q.t0 + t + rows) : (int64_t)q.begin + q.t0 + t;
       const int size = w.sum ? 4 : 2;
-      const auto ov = rows_view(static_cast<char*>(w.out) + (tok * p.heads + h) * (DO * size), (int64_t)p.heads * (DO * size),
-                                rows, DO * size);
+      const auto ov = rows_view(static_cast<char*>(w.out) + (chunk_tok(t, rows) * p.heads + h) * (DO * size),
+                                (int64_t)p.heads * (DO * size), rows, DO * size);
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
         const int row = 16 * tt + l16;
-        const uint32_t at = row < rows ? (uint32_t)(rev ? rows - 1 - row : row) * (uint32_t)(p.heads * DO) : 0x1ffff000u;
-#pragma unroll
-        for (int ot = 0; ot < OT; ++ot) {
-          const f32x4 v = out[ot][tt];
-          const uint32_t col = (uint32_t)(16 * (OT * wave + ot) + g4);
-          if (w.sum) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4v, v), ov, (at + col) * 4u, 0, 0);
-          else vstore8(ov, (at + col) * 2u, pack2<IO>(v[0], v[1]), pack2<IO>(v[2], v[3]));
-        }
+        const uint32_t at = (row < rows ? (uint32_t)(rev ? rows - 1 - row : row) * (uint32_t)(p.heads * DO) : 0x1ffff000u) +
+                            (uint32_t)(16 * wave + g4);
+        const f32x4 v = out[tt];
+        if (w.sum) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4v, v), ov, at * 4u, 0, 0);
+        else vstore8(ov, at * 2u, pack2<IO>(v[0], v[1]), pack2<IO>(v[2], v[3]));
       }
     }
     // ---- H <- a^rows H + sum_s a^{rows-1-s} b_s c_s^T
-    if (!STATE && t + kC >= q.rows && !(q.last && fin)) break;  // nobody takes it
-    if (rows < kC) set_uw(rows);
-    if (have) {
-      const float d = lds.decay[rows < kC ? 1 : 0];
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int ot = 0; ot < OT; ++ot)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) H[ct][ot][r] = fmaf(d, H[ct][ot][r], H[ct][ot][r]);
-    }
+    if (!STATE && !more && !(q.last && fin)) return false;  // nobody takes it
+    const float d = *lds.weight(kDecays + (rows < kC ? 1 : 0));
+    const uint32_t tf = time_frag<DC>(lane);
+    float wc[2][8];
+    Scale sc{1.0f, 1.0f};
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      u32x4v part[3][OT];
+      const f32x4 u0 = *reinterpret_cast<const f32x4*>(lds.weight(32 * ks + 2 * g4));
+      const f32x4 u1 = *reinterpret_cast<const f32x4*>(lds.weight(32 * ks + 2 * g4 + 4));
 #pragma unroll
-      for (int ot = 0; ot < OT; ++ot)
+      for (int e = 0; e < 4; ++e) {
+        wc[ks][2 * e] = low16<IO>(cf[ks][e]) * (e < 2 ? u0 : u1)[2 * e % 4];
+        wc[ks][2 * e + 1] = high16<IO>(cf[ks][e]) * (e < 2 ? u0 : u1)[2 * e % 4 + 1];
+      }
+    }
+    if constexpr (kTwo) {
+      float most = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t v[3];
-          split3(low16<IO>(cf[ks][ot][e]) * uw[ks][2 * e], high16<IO>(cf[ks][ot][e]) * uw[ks][2 * e + 1], v);
+      for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-          for (int i = 0; i < 3; ++i) part[i][ot][e] = v[i];
-        }
+        for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(wc[ks][e]));
+      sc = wave_scale(most);
+    }
+    constexpr int kParts = kTwo ? 2 : 3;
+    u32x4v part[2][kParts];
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        const Parts<IO> bs(time_frag<DC>(lds.b, 32 * ks, ct, lane));
+    for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-        for (int ot = 0; ot < OT; ++ot) {
-          f32x4 v = H[ct][ot];
-          v = BF::run(bs.hi, bfv(part[2][ot]), v);
-          if constexpr (kTwo) v = BF::run(bs.lo, bfv(part[1][ot]), v);
-          v = BF::run(bs.hi, bfv(part[1][ot]), v);
-          if constexpr (kTwo) v = BF::run(bs.lo, bfv(part[0][ot]), v);
-          H[ct][ot] = BF::run(bs.hi, bfv(part[0][ot]), v);
+      for (int e = 0; e < 4; ++e) {
+        uint32_t v[3];
+        if constexpr (kTwo) split2_f16(wc[ks][2 * e] * sc.to, wc[ks][2 * e + 1] * sc.to, v[0], v[1]);
+        else split3(wc[ks][2 * e], wc[ks][2 * e + 1], v);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) part[ks][i][e] = v[i];
+      }
+#pragma unroll
+    for (int c0 = 0; c0 < CT; c0 += 4) {
+      f32x4 own[4];  // of fp16 data apart, at their scale
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          H[c0 + i][r] = fmaf(d, H[c0 + i][r], H[c0 + i][r]);
+          own[i][r] = kTwo ? 0.0f : H[c0 + i][r];
         }
       }
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        u32x4v bs[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bs[i] = read_time_frag<DC>(tb, tf ^ (32 * (c0 + i)), 32 * ks);
+#pragma unroll
+        for (int j = kParts - 1; j >= 0; --j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) own[i] = mfma_t<IO>::run(as_vec<IO>(bs[i]), as_vec<IO>(part[ks][j]), own[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) H[c0 + i][r] = kTwo ? fmaf(own[i][r], sc.from, H[c0 + i][r]) : own[i][r];
     }
     have = true;
-    __syncthreads();  // the tiles are used up
-  }
+    // the next chunk's a and b are there (the outputs' stores, issued behind them, may be on
+    // their way), and everyone is done with this one
+    if (more) lds_barrier<STATE ? 0 : 4>();
+    return more;
+  };
+  if (q.rows > 0)
+    for (int t = 0; chunk(t, std::integral_constant<int, 0>{}) && chunk(t + kC, std::integral_constant<int, 1>{}); t += 2 * kC) {
+    }
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct)
+  for (int ct = 0; ct < CT; ++ct) {
+    if constexpr (STATE) {
+      *reinterpret_cast<f32x4*>(ws + ct * 256) = H[ct];
+    } else if (q.last && fin) {
+      float* at = fin + state_at(w, 16 * ct + g4, 16 * wave + l16);
+      if (w.c_inner) {
+        *reinterpret_cast<f32x4*>(at) = H[ct];
+      } else {
 #pragma unroll
-    for (int ot = 0; ot < OT; ++ot) {
-      if constexpr (STATE) {
-        *reinterpret_cast<f32x4*>(ws + (ct * OT + ot) * 256) = H[ct][ot];
-      } else if (q.last && fin) {
-        float* at = fin + state_at(w, 16 * ct + g4, 16 * (OT * wave + ot) + l16);
-        if (w.c_inner) {
-          *reinterpret_cast<f32x4*>(at) = H[ct][ot];
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) at[r * DO] = H[ct][ot][r];
-        }
+        for (int r = 0; r < 4; ++r) at[r * DO] = H[ct][r];
       }
     }
+  }
 }
 
 // ---- the states between the segments of a sequence ----------------------------------
@@ -443,17 +569,15 @@ __global__ void __launch_bounds__(256) lin_pass_kernel(LinParams p) {
   }
   if (len <= ((int64_t)1 << p.logq)) return;
   const int n = (int)(((int64_t)len + ((int64_t)1 << p.logq) - 1) >> p.logq);
-  const float d = (float)lin_power_m1(p.log_decay[h], 1 << p.logq);
+  const float d = lin_power_m1(p.log_decay[h], 1 << p.logq);
   const float* init;
   float* fin;
   lin_states(p, w, s, h, init, fin);
   f32x4 E = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   if (init) {
-    const int ct_n = w.dc / 16, ot_n = w.dout / 64, tile = e4 / 64, lane = e4 % 64;
-    const int ot = tile % ot_n, ct = tile / ot_n % ct_n, wave = tile / ot_n / ct_n;
+    const int ct_n = w.dc / 16, tile = e4 / 64, lane = e4 % 64, ct = tile % ct_n, wave = tile / ct_n;
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      E[r] = init[state_at(w, 16 * ct + 4 * (lane / 16) + r, 16 * (ot_n * wave + ot) + lane % 16)];
+    for (int r = 0; r < 4; ++r) E[r] = init[state_at(w, 16 * ct + 4 * (lane / 16) + r, 16 * wave + lane % 16)];
   }
   const int64_t step = (int64_t)p.jobs * p.heads * size;
   float* ws = p.ws + (((int64_t)first * p.jobs + job) * p.heads + h) * size + 4 * (int64_t)e4;
@@ -513,7 +637,7 @@ __global__ void __launch_bounds__(256) lin_step_kernel(LinStepParams p) {
     k[e] = load_io<IO>(p.k, r * p.k_stride + kvh * DK + 4 * l + e);
     q[e] = load_io<IO>(p.q, r * p.q_stride + h * DK + 4 * l + e);
   }
-  const float d = (float)lin_power_m1(p.log_decay[h], 1);
+  const float d = lin_power_m1(p.log_decay[h], 1);
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     float y = 0.0f;
@@ -537,8 +661,8 @@ __global__ void __launch_bounds__(256) lin_step_kernel(LinStepParams p) {
 template <int IO, int DC, int DO>
 hipError_t launch_walk(const LinParams& p, hipStream_t st) {
   const dim3 grid((uint32_t)(p.places * p.heads * p.njobs));
-  if (p.split) hipLaunchKernelGGL((lin_walk_kernel<IO, DC, DO, true>), grid, dim3(kWalkThreads), 0, st, p);
-  else hipLaunchKernelGGL((lin_walk_kernel<IO, DC, DO, false>), grid, dim3(kWalkThreads), 0, st, p);
+  if (p.split) hipLaunchKernelGGL((lin_walk_kernel<IO, DC, DO, true>), grid, dim3(walk_threads<DO>()), 0, st, p);
+  else hipLaunchKernelGGL((lin_walk_kernel<IO, DC, DO, false>), grid, dim3(walk_threads<DO>()), 0, st, p);
   return hipGetLastError();
 }
 template <int IO>
