@@ -25,43 +25,50 @@ namespace ss {
 namespace {
 
 constexpr int kC = 64;  // rows of a chunk
+typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
 
-// 16-bit tiles of W columns in LDS, the 16-byte pieces of a row exchanged by the row:
-// piece c of row r lies at c ^ x(r).  The 16 rows of a fragment read (16 or 8 bytes a
-// lane), in whichever halves they are served, and the 4 consecutive rows (32 bytes
-// each) of two of a transposing read's lane groups lie in different banks.
+// 16-bit tiles of W columns in LDS: 4 rows lie together, 64 bytes of each in turn, with the
+// 16-byte pieces of these exchanged by the 4 rows' number: piece c of row r is at
+//   W 8 (r / 4) + 256 (c' / 4) + 64 (r % 4) + 16 (c' % 4),   c' = c ^ tile_x(r / 4).
+// The 16 rows of a fragment read (16 or 8 bytes a lane), in whichever halves they are
+// served, and the 4 consecutive rows (32 bytes each) of two of a transposing read's
+// lane groups lie in different banks; further columns (of 32) and rows (of 16) are
+// immediate offsets.
+__device__ __forceinline__ constexpr int tile_x(int four) {  // Gray code of the quarter of 16 rows
+  const int q = four & 3;
+  return (q >> 1) | (((q ^ (q >> 1)) & 1) << 1);
+}
 template <int W>
-__device__ __forceinline__ constexpr int tile_x(int row) {
+__device__ __forceinline__ constexpr int tile_at(int row, int col) {  // in bytes
   static_assert(W == 64 || W == 128, "tile width");
-  const int q = (row >> 2) & 3, low = q >> 1, high = (q ^ (q >> 1)) & 1;  // Gray code of the row's quarter of 16
-  return W == 128 ? ((row & 3) << 1) | low | (high << 3) : (((row >> 1) & 1) << 1) | low | (high << 2);
+  const int c = (col >> 3) ^ tile_x(row >> 2);
+  return W * 8 * (row >> 2) + 256 * (c >> 2) + 64 * (row & 3) + 16 * (c & 3) + 2 * (col & 7);
 }
-template <int W>
-__device__ __forceinline__ constexpr int tile_off(int row, int col) {
-  return row * W + 8 * ((col >> 3) ^ tile_x<W>(row)) + (col & 7);
+// LDS by 32-bit address
+template <class T>
+__device__ __forceinline__ __attribute__((address_space(3))) T* lds_ptr(uint32_t at) {
+  return (__attribute__((address_space(3))) T*)(uintptr_t)at;
 }
-__device__ __forceinline__ u32x4v lds16(const char* at) { return *reinterpret_cast<const u32x4v*>(at); }
-__device__ __forceinline__ uint2 lds8(const char* at) { return *reinterpret_cast<const uint2*>(at); }
+__device__ __forceinline__ uint32_t lds_addr(void* p) { return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)p; }
+__device__ __forceinline__ u32x4v lds16(uint32_t at) { return *lds_ptr<u32x4v>(at); }
+__device__ __forceinline__ u32x2v lds8(uint32_t at) { return *lds_ptr<u32x2v>(at); }
 
-// Where a lane's fragments lie in a tile, in bytes: other columns are another power of
-// two exclusive-or'ed in, other rows (multiples of 16) an immediate offset.
-// rows l16, the columns 32 ks + 8 (lane / 16) ..: row_frag ^ 64 ks
+// Where a lane's fragments lie in a tile:
+// rows l16, the columns 32 ks + 8 (lane / 16) ..: row_frag + 256 ks
 template <int W>
-__device__ __forceinline__ uint32_t row_frag(int lane) { return 2 * tile_off<W>(lane % 16, 8 * (lane / 16)); }
-// rows l16, the columns 16 i + 4 (lane / 16) ..: quad_frag ^ 32 i
+__device__ __forceinline__ int row_frag(int lane) { return tile_at<W>(lane % 16, 8 * (lane / 16)); }
+// rows l16, the columns 16 i + 4 (lane / 16) ..: (quad_frag ^ 32 (i % 2)) + 256 (i / 2)
 template <int W>
-__device__ __forceinline__ uint32_t quad_frag(int lane) { return 2 * tile_off<W>(lane % 16, 4 * (lane / 16)); }
-// the columns 16 i .. as an operand whose k axis is the row: time_frag ^ 32 i
+__device__ __forceinline__ int quad_frag(int lane) { return tile_at<W>(lane % 16, 4 * (lane / 16)); }
+// the columns 16 i .. of 32 rows as an operand whose k axis is the row; even and odd: the lane's
+// place for even i and for odd i, each the other's for the rows 4 further on
 template <int W>
-__device__ __forceinline__ uint32_t time_frag(int lane) {
-  return 2 * tile_off<W>(8 * (lane / 16) + lane % 16 / 4, 4 * (lane % 4));
-}
-// rows row0 .. + 31 of it
+__device__ __forceinline__ int time_frag(int lane) { return tile_at<W>(8 * (lane / 16) + lane % 16 / 4, 4 * (lane % 4)); }
 template <int W>
-__device__ __forceinline__ u32x4v read_time_frag(const char* tile, uint32_t at, int row0) {
-  constexpr uint32_t kNext = W == 128 ? 128 : 64;  // the rows 4 further on: x differs in its highest bit
-  const uint16_t* rows = reinterpret_cast<const uint16_t*>(tile + row0 * (W * 2));
-  return tm_frag(rows, (int)(at / 2), (int)((at ^ kNext) / 2 + 4 * W));
+__device__ __forceinline__ u32x4v read_time_frag(uint32_t at, uint32_t next) {
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_ptr<s16x4>(at));
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_ptr<s16x4>(next + W * 8));
+  return __builtin_bit_cast(u32x4v, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
 // The rows that workgroup place `place` walks.
@@ -144,12 +151,12 @@ constexpr int walk_waves_per_simd(int dc, int dout) { return dout == 128 ? 4 : d
 constexpr int kPowers = 64, kDecays = 160;
 template <int DC, int DO, bool STATE>
 struct WalkLds {
-  __attribute__((aligned(16))) uint16_t a[STATE ? 8 : kC * DC];
-  __attribute__((aligned(16))) uint16_t b[2][kC * DC];
-  __attribute__((aligned(16))) uint16_t c[STATE ? 2 : 1][kC * DO];
-  __attribute__((aligned(16))) uint16_t m[STATE ? 1 : 2][STATE ? 512 : kC * kC];
+  __attribute__((aligned(16))) char m[STATE ? 1024 : 2 * kC * kC * 2];
+  __attribute__((aligned(16))) char a[STATE ? 16 : kC * DC * 2];
+  __attribute__((aligned(16))) char b[2][kC * DC * 2];
+  __attribute__((aligned(16))) char c[STATE ? 2 : 1][kC * DO * 2];
   __device__ __forceinline__ float* weight(int i) {
-    return reinterpret_cast<float*>(&m[0][STATE ? 2 * i : tile_off<kC>(i / 16, 32 + 2 * (i % 16))]);
+    return reinterpret_cast<float*>(m + (STATE ? 4 * i : tile_at<kC>(i / 16, 32 + 2 * (i % 16))));
   }
 };
 
@@ -200,32 +207,54 @@ __device__ __forceinline__ void lds_barrier() {
   else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(AHEAD) : "memory");
 }
 
-// `rows` rows of W columns into a tile: a wave's load fills 1 KB of it, 16 bytes a lane in
-// the lanes' order, so that the exchange of pieces is made on the memory's side.  Rows
-// behind the last one repeat it: no weight but 0 meets them, and their outputs go nowhere.
+// The rows of a chunk into a tile: a wave's load fills 1 KB of it, 16 bytes a lane in the
+// lanes' order, so that the exchange of pieces is made on the memory's side.  In a
+// chunk of fewer rows those behind the last one repeat it: no weight but 0 meets
+// them, and their outputs go nowhere.
 template <int W, int WAVES> constexpr int tile_loads() { return kC * W / 512 / WAVES; }
 template <int W, int WAVES>
-__device__ __forceinline__ void load_tile(uint16_t* tile, const void* at, int64_t stride, int rows, bool rev, int wave, int lane) {
-  constexpr int kRows = 512 / W, kLoads = tile_loads<W, WAVES>();  // rows of a load, loads of a wave
-  const auto v = rows_view(at, stride * 2, rows, W * 2);
-#pragma unroll
-  for (int k = 0; k < kLoads; ++k) {
-    const int first = (wave * kLoads + k) * kRows, row = first + lane / (W / 8);
-    const int piece = lane % (W / 8) ^ tile_x<W>(row);
-    const int in = row < rows ? row : rows - 1;
-    const uint32_t off = (uint32_t)(rev ? rows - 1 - in : in) * (uint32_t)(stride * 2) + (uint32_t)piece * 16u;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(v, (__attribute__((address_space(3))) void*)(tile + first * W), 16, off, 0, 0, 0);
+struct TileLoad {
+  static constexpr int kRows = 512 / W, kLoads = tile_loads<W, WAVES>();  // rows of a load, loads of a wave
+  uint32_t whole;  // the offset of this lane's piece of the wave's first load in a whole chunk
+  // this lane's row and piece of the wave's first load
+  __device__ __forceinline__ static void lane_piece(int wave, int lane, int& row, int& piece) {
+    const int in = W == 128 ? lane : lane % 32;
+    row = wave * kRows + lane / 4 % 4 + (W == 128 ? 0 : lane / 32 * 4);
+    piece = (in / 16 * 4 + in % 4) ^ tile_x(row >> 2);
   }
-}
+  __device__ __forceinline__ TileLoad(int wave, int lane, int64_t stride, bool rev) {
+    int row, piece;
+    lane_piece(wave, lane, row, piece);
+    whole = (uint32_t)(rev ? kRows * WAVES - 1 - row : row) * (uint32_t)(stride * 2) + (uint32_t)piece * 16u;
+  }
+  __device__ __forceinline__ void load(char* tile, const char* at, int64_t stride, int rows, bool rev, int wave, int lane) const {
+    const auto v = rows_view(at, stride * 2, rows, W * 2);
+    if (rows == kC) {
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(v, (__attribute__((address_space(3))) void*)(tile + (wave + WAVES * k) * 1024), 16, whole, (rev ? kLoads - 1 - k : k) * (kRows * WAVES) * (int)(stride * 2), 0, 0);
+      return;
+    }
+    int row, piece;
+    lane_piece(wave, opaque(lane), row, piece);
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      const int r = row + k * (kRows * WAVES), in = r < rows ? r : rows - 1;
+      const uint32_t off = (uint32_t)(rev ? rows - 1 - in : in) * (uint32_t)(stride * 2) + (uint32_t)piece * 16u;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(v, (__attribute__((address_space(3))) void*)(tile + (wave + WAVES * k) * 1024), 16, off, 0, 0, 0);
+    }
+  }
+};
 
 template <int IO, int DC, int DO, bool STATE>
 __global__ void __launch_bounds__(walk_threads<DO>(), walk_waves_per_simd(DC, DO)) lin_walk_kernel(LinParams p) {
   constexpr int CT = DC / 16, WAVES = DO / 16;
   constexpr int kPairs = (10 + WAVES - 1) / WAVES;  // 16 x 16 tiles of pairs a wave
   constexpr bool kTwo = IO == SS_F16;
+  constexpr int kPlane = kC * kC * 2, kTile = kC * DC * 2;
   __shared__ WalkLds<DC, DO, STATE> lds;
   const int tid = threadIdx.x, wave = uniform(tid / 64);
-  int lane = tid % 64, l16 = lane % 16, g4 = 4 * (lane / 16);
+  const int lane = tid % 64, l16 = lane % 16, g4 = 4 * (lane / 16);
   const int lb = (int)xcd_logical_block();
   const int job = p.job0 + lb % p.njobs, h = lb / p.njobs % p.heads, place = lb / p.njobs / p.heads;
   const LinWalk& w = p.job[job];
@@ -253,14 +282,16 @@ __global__ void __launch_bounds__(walk_threads<DO>(), walk_waves_per_simd(DC, DO
   auto chunk_at = [&](const void* base, int t, int64_t stride, int head, int cols) {
     return static_cast<const char*>(base) + (chunk_tok(t, chunk_rows(t)) * stride + head * cols) * 2;
   };
+  const TileLoad<DC, WAVES> la(wave, lane, w.a_stride, rev), lb_(wave, lane, w.b_stride, rev);
+  const TileLoad<DO, WAVES> lc(wave, lane, w.c_stride, rev);
   auto load_a = [&](int t) {
-    load_tile<DC, WAVES>(lds.a, chunk_at(w.a, t, w.a_stride, w.a_kv ? kvh : h, DC), w.a_stride, chunk_rows(t), rev, wave, lane);
+    la.load(lds.a, chunk_at(w.a, t, w.a_stride, w.a_kv ? kvh : h, DC), w.a_stride, chunk_rows(t), rev, wave, lane);
   };
   auto load_b = [&](int t, int turn) {
-    load_tile<DC, WAVES>(lds.b[turn], chunk_at(w.b, t, w.b_stride, w.b_kv ? kvh : h, DC), w.b_stride, chunk_rows(t), rev, wave, lane);
+    lb_.load(lds.b[turn], chunk_at(w.b, t, w.b_stride, w.b_kv ? kvh : h, DC), w.b_stride, chunk_rows(t), rev, wave, lane);
   };
   auto load_c = [&](int t, int turn) {
-    load_tile<DO, WAVES>(lds.c[turn], chunk_at(w.c, t, w.c_stride, w.c_kv ? kvh : h, DO), w.c_stride, chunk_rows(t), rev, wave, lane);
+    lc.load(lds.c[turn], chunk_at(w.c, t, w.c_stride, w.c_kv ? kvh : h, DO), w.c_stride, chunk_rows(t), rev, wave, lane);
   };
   if (q.rows > 0) {
     load_b(0, 0);
@@ -279,7 +310,8 @@ __global__ void __launch_bounds__(walk_threads<DO>(), walk_waves_per_simd(DC, DO
   if constexpr (!STATE) {  // M's 16 x 16 tiles above the diagonal that are read with their neighbours
     if (tid < 128) {
       const int tile = tid / 32 % 2, row = tid / 2 % 16;
-      *reinterpret_cast<u32x4v*>(&lds.m[tid / 64][tile_off<kC>(32 * tile + row, 16 + 32 * tile + 8 * (tid % 2))]) = u32x4v{0, 0, 0, 0};
+      *reinterpret_cast<u32x4v*>(lds.m + tid / 64 * kPlane + tile_at<kC>(32 * tile + row, 16 + 32 * tile + 8 * (tid % 2))) =
+          u32x4v{0, 0, 0, 0};
     }
   }
 
@@ -326,20 +358,20 @@ __global__ void __launch_bounds__(walk_threads<DO>(), walk_waves_per_simd(DC, DO
 #pragma unroll
     for (int tt = 0; tt < 4; ++tt) iw[tt] = w.e_scale * *lds.weight(kPowers + 16 * tt + l16 + later);
   }
-  char* const ta = reinterpret_cast<char*>(lds.a);
-  char* const tm = reinterpret_cast<char*>(lds.m);
-  constexpr int kPlane = kC * kC * 2;
+  // the lane's places in the tiles
+  const uint32_t at_a = lds_addr(lds.a), at_b = lds_addr(lds.b[0]), at_c = lds_addr(lds.c[0]), at_m = lds_addr(lds.m);
+  const uint32_t rows_dc = row_frag<DC>(lane), quad_dc = quad_frag<DC>(lane), time_dc = time_frag<DC>(lane);
+  const uint32_t c_at = at_c + (time_frag<DO>(lane) ^ (32 * (wave % 2))) + 256 * (wave / 2);
+  const uint32_t c_next = at_c + (time_frag<DO>(lane) ^ (32 - 32 * (wave % 2))) + 256 * (wave / 2);
+  const uint32_t m_rows = at_m + row_frag<kC>(lane), m_quad = quad_frag<kC>(lane);
+  const uint32_t row_bytes = (uint32_t)(p.heads * DO) * (w.sum ? 4u : 2u);
+  const uint32_t out_at = (uint32_t)(rev ? kC - 1 - l16 : l16) * row_bytes + (uint32_t)(16 * wave + g4) * (w.sum ? 4u : 2u);
 
   // a chunk; false behind the segment's last
   auto chunk = [&](int t, auto which) {
     constexpr int turn = decltype(which)::value;
     const int rows = chunk_rows(t);
     const bool more = t + kC < q.rows;
-    const char *tb = reinterpret_cast<const char*>(lds.b[turn]), *tc = reinterpret_cast<const char*>(lds.c[STATE ? turn : 0]);
-    // what follows from the lane is rebuilt in every chunk: kept, it would take the registers
-    lane = opaque(lane);
-    l16 = lane % 16;
-    g4 = 4 * (lane / 16);
     if constexpr (!STATE) load_c(t, 0);
     if (more) {
       load_b(t + kC, turn ^ 1);
@@ -350,29 +382,29 @@ __global__ void __launch_bounds__(walk_threads<DO>(), walk_waves_per_simd(DC, DO
     f32x4 out[4];  // element r: o = 16 wave + g4 + r, row 16 tt + l16
     if constexpr (!STATE) {
       // M[t][s] = a^{t-s} (a_t . b_s), a lane with 4 consecutive s of a row t
-      const uint32_t rf = row_frag<DC>(lane), mf = quad_frag<kC>(lane);
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
         if (tile_t[i] > 3) continue;
-        const char *bs = tb + tile_s[i] * (16 * DC * 2), *as = ta + tile_t[i] * (16 * DC * 2);
+        const uint32_t bs = opaque(rows_dc) + at_b + turn * kTile + tile_s[i] * (16 * DC * 2);
+        const uint32_t as = opaque(rows_dc) + at_a + tile_t[i] * (16 * DC * 2);
         f32x4 acc[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
         for (int ks = 0; ks < DC / 32; ++ks)
-          acc[ks & 1] = mfma_t<IO>::run(as_vec<IO>(lds16(bs + (rf ^ (64 * ks)))), as_vec<IO>(lds16(as + (rf ^ (64 * ks)))), acc[ks & 1]);
+          acc[ks & 1] = mfma_t<IO>::run(as_vec<IO>(lds16(bs + 256 * ks)), as_vec<IO>(lds16(as + 256 * ks)), acc[ks & 1]);
         acc[0] += acc[1];
         uint32_t h0, h1, l0, l1;
         split2(acc[0][0] * mw[i][0], acc[0][1] * mw[i][1], h0, l0);
         split2(acc[0][2] * mw[i][2], acc[0][3] * mw[i][3], h1, l1);
-        char* at = tm + tile_t[i] * (16 * kC * 2) + (mf ^ (uint32_t)(32 * tile_s[i]));
-        *reinterpret_cast<uint2*>(at) = make_uint2(h0, h1);
-        *reinterpret_cast<uint2*>(at + kPlane) = make_uint2(l0, l1);
+        const uint32_t at = (opaque(m_quad) ^ (uint32_t)(32 * (tile_s[i] % 2))) + at_m + tile_t[i] * (16 * kC * 2) + 256 * (tile_s[i] / 2);
+        *lds_ptr<u32x2v>(at) = u32x2v{h0, h1};
+        *lds_ptr<u32x2v>(at + kPlane) = u32x2v{l0, l1};
       }
       // E's part: the accumulators of H are the operand as they lie, its k axis being
-      // c = 16 (2 kk) + g4 + 0..3, then 16 (2 kk + 1) + g4 + 0..3; a is read in that order
+      // c = 16 i + g4 + 0..3, then 16 (i + 2) + g4 + 0..3; a is read in that order
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) out[tt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       if (have) {
-        const uint32_t qf = quad_frag<DC>(lane);
+        const uint32_t even = opaque(quad_dc) + at_a, odd = (opaque(quad_dc) ^ 32u) + at_a;
         Scale sc{1.0f, 1.0f};
         if constexpr (kTwo) {
           float most = 0.0f;
@@ -384,18 +416,19 @@ __global__ void __launch_bounds__(walk_threads<DO>(), walk_waves_per_simd(DC, DO
         }
 #pragma unroll
         for (int kk = 0; kk < CT / 2; ++kk) {
+          const int i0 = 4 * (kk / 2) + kk % 2;
+          const uint32_t from = kk % 2 ? odd : even;
           u32x4v eh, el, as[4];
 #pragma unroll
           for (int tt = 0; tt < 4; ++tt) {
-            const uint2 a0 = lds8(ta + tt * (16 * DC * 2) + (qf ^ (64 * kk)));
-            const uint2 a1 = lds8(ta + tt * (16 * DC * 2) + (qf ^ (64 * kk + 32)));
-            as[tt] = u32x4v{a0.x, a0.y, a1.x, a1.y};
+            const u32x2v a0 = lds8(from + tt * (16 * DC * 2) + 512 * (kk / 2)), a1 = lds8(from + tt * (16 * DC * 2) + 512 * (kk / 2) + 256);
+            as[tt] = u32x4v{a0[0], a0[1], a1[0], a1[1]};
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int r = 0; r < 4; r += 2) {
-              const float v0 = H[2 * kk + i][r], v1 = H[2 * kk + i][r + 1];
+              const float v0 = H[i0 + 2 * i][r], v1 = H[i0 + 2 * i][r + 1];
               uint32_t hi, lo;
               if constexpr (kTwo) split2_f16(v0 * sc.to, v1 * sc.to, hi, lo);
               else split2(v0, v1, hi, lo);
@@ -416,19 +449,20 @@ __global__ void __launch_bounds__(walk_threads<DO>(), walk_waves_per_simd(DC, DO
       if (more) load_a(t + kC);
       asm volatile("" ::: "memory");  // the outputs' stores come behind
     }
-    const uint32_t cfa = time_frag<DO>(lane) ^ (uint32_t)(32 * wave);
     u32x4v cf[2];
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) cf[ks] = read_time_frag<DO>(tc, cfa, 32 * ks);
+    for (int ks = 0; ks < 2; ++ks) {
+      const int at = (STATE ? turn * (kC * DO * 2) : 0) + 32 * ks * (DO * 2);
+      cf[ks] = read_time_frag<DO>(c_at + at, c_next + at);
+    }
     if constexpr (!STATE) {
-      const uint32_t mf = row_frag<kC>(lane);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         const Parts<IO> cs(cf[ks]);
         bf16x8 mh[4], ml[4];
 #pragma unroll
         for (int tt = 2 * ks; tt < 4; ++tt) {
-          const char* at = tm + tt * (16 * kC * 2) + (mf ^ (64 * ks));
+          const uint32_t at = m_rows + tt * (16 * kC * 2) + 256 * ks;
           mh[tt] = bfv(lds16(at));
           ml[tt] = bfv(lds16(at + kPlane));
         }
@@ -443,79 +477,107 @@ __global__ void __launch_bounds__(walk_threads<DO>(), walk_waves_per_simd(DC, DO
       }
       // ---- outputs: rows past the segment's last go nowhere
       const int size = w.sum ? 4 : 2;
-      const auto ov = rows_view(static_cast<char*>(w.out) + (chunk_tok(t, rows) * p.heads + h) * (DO * size),
-                                (int64_t)p.heads * (DO * size), rows, DO * size);
+      const auto ov = rows_view(static_cast<char*>(w.out) + (chunk_tok(t, rows) * p.heads + h) * (DO * size), row_bytes, rows, DO * size);
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
-        const int row = 16 * tt + l16;
-        const uint32_t at = (row < rows ? (uint32_t)(rev ? rows - 1 - row : row) * (uint32_t)(p.heads * DO) : 0x1ffff000u) +
-                            (uint32_t)(16 * wave + g4);
         const f32x4 v = out[tt];
-        if (w.sum) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4v, v), ov, at * 4u, 0, 0);
-        else vstore8(ov, at * 2u, pack2<IO>(v[0], v[1]), pack2<IO>(v[2], v[3]));
+        uint32_t at = out_at;
+        int ahead = (rev ? -16 * tt : 16 * tt) * (int)row_bytes;
+        if (rows < kC) {
+          const int row = 16 * tt + l16;
+          at = row < rows ? (uint32_t)(rev ? rows - 1 - row : row) * row_bytes + (uint32_t)((16 * wave + g4) * size) : 0x3fffe000u;
+          ahead = 0;
+        } else if (rev) {
+          at += (uint32_t)ahead;
+          ahead = 0;
+        }
+        if (w.sum) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4v, v), ov, at, ahead, 0);
+        else __builtin_amdgcn_raw_buffer_store_b64(u32x2v{pack2<IO>(v[0], v[1]), pack2<IO>(v[2], v[3])}, ov, at, ahead, 0);
       }
     }
     // ---- H <- a^rows H + sum_s a^{rows-1-s} b_s c_s^T
     if (!STATE && !more && !(q.last && fin)) return false;  // nobody takes it
     const float d = *lds.weight(kDecays + (rows < kC ? 1 : 0));
-    const uint32_t tf = time_frag<DC>(lane);
-    float wc[2][8];
-    Scale sc{1.0f, 1.0f};
+    const uint32_t even = opaque(time_dc) + at_b, odd = (opaque(time_dc) ^ 32u) + at_b;
+    auto b_frag = [&](int ks, int ct) {
+      const uint32_t at = turn * kTile + 32 * ks * (DC * 2) + 256 * (ct / 2);
+      return as_vec<IO>(read_time_frag<DC>((ct % 2 ? odd : even) + at, (ct % 2 ? even : odd) + at));
+    };
+    // w_s c_s of the rows 32 ks + 2 g4 + 2 e, + 1
+    auto weighted = [&](int ks, int e, float& v0, float& v1) {
+      const f32x2 u = *lds_ptr<f32x2>(lds_addr(lds.weight(32 * ks + 2 * g4 + 2 * e)));
+      v0 = low16<IO>(cf[ks][e]) * u[0];
+      v1 = high16<IO>(cf[ks][e]) * u[1];
+    };
+    if constexpr (!kTwo) {
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      const f32x4 u0 = *reinterpret_cast<const f32x4*>(lds.weight(32 * ks + 2 * g4));
-      const f32x4 u1 = *reinterpret_cast<const f32x4*>(lds.weight(32 * ks + 2 * g4 + 4));
+      for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        wc[ks][2 * e] = low16<IO>(cf[ks][e]) * (e < 2 ? u0 : u1)[2 * e % 4];
-        wc[ks][2 * e + 1] = high16<IO>(cf[ks][e]) * (e < 2 ? u0 : u1)[2 * e % 4 + 1];
+        for (int r = 0; r < 4; ++r) H[ct][r] = fmaf(d, H[ct][r], H[ct][r]);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        u32x4v part[3];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float v0, v1;
+          uint32_t v[3];
+          weighted(ks, e, v0, v1);
+          split3(v0, v1, v);
+#pragma unroll
+          for (int i = 0; i < 3; ++i) part[i][e] = v[i];
+        }
+#pragma unroll
+        for (int c0 = 0; c0 < CT; c0 += 4) {
+          typename mfma_t<IO>::V bs[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) bs[i] = b_frag(ks, c0 + i);
+#pragma unroll
+          for (int j = 2; j >= 0; --j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) H[c0 + i] = mfma_t<IO>::run(bs[i], as_vec<IO>(part[j]), H[c0 + i]);
+        }
       }
-    }
-    if constexpr (kTwo) {
-      float most = 0.0f;
+    } else {
+      float wc[2][8], most = 0.0f;
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(wc[ks][e]));
-      sc = wave_scale(most);
-    }
-    constexpr int kParts = kTwo ? 2 : 3;
-    u32x4v part[2][kParts];
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t v[3];
-        if constexpr (kTwo) split2_f16(wc[ks][2 * e] * sc.to, wc[ks][2 * e + 1] * sc.to, v[0], v[1]);
-        else split3(wc[ks][2 * e], wc[ks][2 * e + 1], v);
-#pragma unroll
-        for (int i = 0; i < kParts; ++i) part[ks][i][e] = v[i];
-      }
-#pragma unroll
-    for (int c0 = 0; c0 < CT; c0 += 4) {
-      f32x4 own[4];  // of fp16 data apart, at their scale
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          H[c0 + i][r] = fmaf(d, H[c0 + i][r], H[c0 + i][r]);
-          own[i][r] = kTwo ? 0.0f : H[c0 + i][r];
+        for (int e = 0; e < 4; ++e) {
+          weighted(ks, e, wc[ks][2 * e], wc[ks][2 * e + 1]);
+          most = fmaxf(most, fmaxf(fabsf(wc[ks][2 * e]), fabsf(wc[ks][2 * e + 1])));
         }
+      const Scale sc = wave_scale(most);
+      u32x4v part[2][2];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t hi, lo;
+          split2_f16(wc[ks][2 * e] * sc.to, wc[ks][2 * e + 1] * sc.to, hi, lo);
+          part[ks][0][e] = hi;
+          part[ks][1][e] = lo;
+        }
+#pragma unroll
+      for (int c0 = 0; c0 < CT; c0 += 4) {
+        f32x4 own[4];  // at their scale
+#pragma unroll
+        for (int i = 0; i < 4; ++i) own[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          typename mfma_t<IO>::V bs[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) bs[i] = b_frag(ks, c0 + i);
+#pragma unroll
+          for (int j = 1; j >= 0; --j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) own[i] = mfma_t<IO>::run(bs[i], as_vec<IO>(part[ks][j]), own[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            H[c0 + i][r] = fmaf(own[i][r], sc.from, fmaf(d, H[c0 + i][r], H[c0 + i][r]));
       }
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        u32x4v bs[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) bs[i] = read_time_frag<DC>(tb, tf ^ (32 * (c0 + i)), 32 * ks);
-#pragma unroll
-        for (int j = kParts - 1; j >= 0; --j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) own[i] = mfma_t<IO>::run(as_vec<IO>(bs[i]), as_vec<IO>(part[ks][j]), own[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) H[c0 + i][r] = kTwo ? fmaf(own[i][r], sc.from, H[c0 + i][r]) : own[i][r];
     }
     have = true;
     // the next chunk's a and b are there (the outputs' stores, issued behind them, may be on
