@@ -138,13 +138,15 @@ __device__ __forceinline__ float lin_power_m1(float g, int n) {
 }
 
 // ---- the walk ----------------------------------------------------------------------
-// Wave w has the columns o = 16 w .. of the outputs and of the state, the state as
-// accumulators.  Two workgroups share a CU.  A chunk's operands come into LDS without
-// registers in between: b, which is in use from a chunk's begin to its end, a chunk
-// ahead in one of two buffers; a, once the last chunk's is used, for the next; c, which
-// is not needed before the pairs' weights are made, at its chunk's begin.
-template <int DO> constexpr int walk_threads() { return 4 * DO; }
-constexpr int walk_waves_per_simd(int dc, int dout) { return dout == 128 ? 4 : dc == 64 ? 3 : 2; }
+// Four waves, each with a quarter of the columns o of the outputs and of the state, the
+// state as accumulators: what a wave reads of LDS meets two tiles of o (heads of 128).
+// Two workgroups share a CU, so that one's products, the other's vector work
+// (both halves of the walk take as long) and the reads of LDS go on at once.  A chunk's
+// operands come into LDS without registers in between: b, which is in use from a
+// chunk's begin to its end, a chunk ahead in one of two buffers; a, once the last
+// chunk's is used, for the next; c, which is not needed before the pairs' weights are
+// made, at its chunk's begin.
+constexpr int kWaves = 4, kWalkThreads = 64 * kWaves;
 // Weights by number, of rows in E' (0 .. 63), powers of a (64 .. 129) and a^rows - 1
 // of a whole chunk and of the last one (160, 161): with M they lie in the columns of
 // its first rows that no pair has, so that two workgroups have LDS's 160 KB
@@ -207,14 +209,25 @@ __device__ __forceinline__ void lds_barrier() {
   else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(AHEAD) : "memory");
 }
 
+// 16 bytes a lane from a view (its four words) into LDS at `to` + 16 lane.  In assembly, for the
+// compiler would wait for such a load before the next access to LDS that it cannot tell apart
+// from its target: it ends before the barrier that waits for memory (lds_barrier), and nothing
+// between reads what it writes.
+__device__ __forceinline__ void lds_load(u32x4v view, uint32_t to, uint32_t off, int ahead) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(uniform((int)to)), "v"(off), "s"(view),
+      "s"(uniform(ahead))
+      : "memory");  // m0 is nobody else's
+}
+
 // The rows of a chunk into a tile: a wave's load fills 1 KB of it, 16 bytes a lane in the
 // lanes' order, so that the exchange of pieces is made on the memory's side.  In a
 // chunk of fewer rows those behind the last one repeat it: no weight but 0 meets
 // them, and their outputs go nowhere.
-template <int W, int WAVES> constexpr int tile_loads() { return kC * W / 512 / WAVES; }
-template <int W, int WAVES>
+template <int W> constexpr int tile_loads() { return kC * W / 512 / kWaves; }
+template <int W>
 struct TileLoad {
-  static constexpr int kRows = 512 / W, kLoads = tile_loads<W, WAVES>();  // rows of a load, loads of a wave
+  static constexpr int kRows = 512 / W, kLoads = tile_loads<W>();  // rows of a load, loads of a wave
   uint32_t whole;  // the offset of this lane's piece of the wave's first load in a whole chunk
   // this lane's row and piece of the wave's first load
   __device__ __forceinline__ static void lane_piece(int wave, int lane, int& row, int& piece) {
@@ -225,31 +238,33 @@ struct TileLoad {
   __device__ __forceinline__ TileLoad(int wave, int lane, int64_t stride, bool rev) {
     int row, piece;
     lane_piece(wave, lane, row, piece);
-    whole = (uint32_t)(rev ? kRows * WAVES - 1 - row : row) * (uint32_t)(stride * 2) + (uint32_t)piece * 16u;
+    whole = (uint32_t)(rev ? kRows * kWaves - 1 - row : row) * (uint32_t)(stride * 2) + (uint32_t)piece * 16u;
   }
   __device__ __forceinline__ void load(char* tile, const char* at, int64_t stride, int rows, bool rev, int wave, int lane) const {
-    const auto v = rows_view(at, stride * 2, rows, W * 2);
+    const uint64_t base = (uint64_t)(uintptr_t)at;
+    const u32x4v v = {(uint32_t)uniform((int)(uint32_t)base), (uint32_t)uniform((int)((base >> 32) & 0xffffu)),
+                      (uint32_t)uniform((int)view_bytes(stride * 2, rows, W * 2)), (uint32_t)kRsrcWord3};
+    const uint32_t to = lds_addr(tile) + (uint32_t)wave * 1024u;
     if (rows == kC) {
 #pragma unroll
       for (int k = 0; k < kLoads; ++k)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(v, (__attribute__((address_space(3))) void*)(tile + (wave + WAVES * k) * 1024), 16, whole, (rev ? kLoads - 1 - k : k) * (kRows * WAVES) * (int)(stride * 2), 0, 0);
+        lds_load(v, to + kWaves * 1024 * k, whole, (rev ? kLoads - 1 - k : k) * (kRows * kWaves) * (int)(stride * 2));
       return;
     }
     int row, piece;
     lane_piece(wave, opaque(lane), row, piece);
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) {
-      const int r = row + k * (kRows * WAVES), in = r < rows ? r : rows - 1;
-      const uint32_t off = (uint32_t)(rev ? rows - 1 - in : in) * (uint32_t)(stride * 2) + (uint32_t)piece * 16u;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(v, (__attribute__((address_space(3))) void*)(tile + (wave + WAVES * k) * 1024), 16, off, 0, 0, 0);
+      const int r = row + k * (kRows * kWaves), in = r < rows ? r : rows - 1;
+      lds_load(v, to + kWaves * 1024 * k, (uint32_t)(rev ? rows - 1 - in : in) * (uint32_t)(stride * 2) + (uint32_t)piece * 16u, 0);
     }
   }
 };
 
 template <int IO, int DC, int DO, bool STATE>
-__global__ void __launch_bounds__(walk_threads<DO>(), walk_waves_per_simd(DC, DO)) lin_walk_kernel(LinParams p) {
-  constexpr int CT = DC / 16, WAVES = DO / 16;
-  constexpr int kPairs = (10 + WAVES - 1) / WAVES;  // 16 x 16 tiles of pairs a wave
+__global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) {
+  constexpr int CT = DC / 16, OT = DO / 64;  // tiles of a wave's state: all of c, a quarter of o
+  constexpr int kPairs = 3;                  // 16 x 16 tiles of pairs a wave, at the most
   constexpr bool kTwo = IO == SS_F16;
   constexpr int kPlane = kC * kC * 2, kTile = kC * DC * 2;
   __shared__ WalkLds<DC, DO, STATE> lds;
@@ -282,8 +297,8 @@ __global__ void __launch_bounds__(walk_threads<DO>(), walk_waves_per_simd(DC, DO
   auto chunk_at = [&](const void* base, int t, int64_t stride, int head, int cols) {
     return static_cast<const char*>(base) + (chunk_tok(t, chunk_rows(t)) * stride + head * cols) * 2;
   };
-  const TileLoad<DC, WAVES> la(wave, lane, w.a_stride, rev), lb_(wave, lane, w.b_stride, rev);
-  const TileLoad<DO, WAVES> lc(wave, lane, w.c_stride, rev);
+  const TileLoad<DC> la(wave, lane, w.a_stride, rev), lb_(wave, lane, w.b_stride, rev);
+  const TileLoad<DO> lc(wave, lane, w.c_stride, rev);
   auto load_a = [&](int t) {
     la.load(lds.a, chunk_at(w.a, t, w.a_stride, w.a_kv ? kvh : h, DC), w.a_stride, chunk_rows(t), rev, wave, lane);
   };
@@ -320,24 +335,26 @@ __global__ void __launch_bounds__(walk_threads<DO>(), walk_waves_per_simd(DC, DO
   float* fin;
   lin_states(p, w, q.seq, h, init, fin);
   const bool several = q.len > q.rows;  // the segments' states are in the workspace
-  float* ws = p.ws + (((int64_t)place * p.jobs + job) * p.heads + h) * (DC * DO) + wave * (CT * 256) + lane * 4;
-  f32x4 H[CT];  // element r: c = 16 ct + g4 + r, o = 16 wave + l16
+  float* ws = p.ws + (((int64_t)place * p.jobs + job) * p.heads + h) * (DC * DO) + wave * (CT * OT * 256) + lane * 4;
+  f32x4 H[CT][OT];  // element r: c = 16 ct + g4 + r, o = 16 (OT wave + ot) + l16
   bool have = !STATE && (several || init);
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    H[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (!STATE && several) {
-      H[ct] = *reinterpret_cast<const f32x4*>(ws + ct * 256);
-    } else if (have) {
-      const float* at = init + state_at(w, 16 * ct + g4, 16 * wave + l16);
-      if (w.c_inner) {
-        H[ct] = *reinterpret_cast<const f32x4*>(at);
-      } else {
+  for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) H[ct][r] = at[r * DO];
+    for (int ot = 0; ot < OT; ++ot) {
+      H[ct][ot] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (!STATE && several) {
+        H[ct][ot] = *reinterpret_cast<const f32x4*>(ws + (ct * OT + ot) * 256);
+      } else if (have) {
+        const float* at = init + state_at(w, 16 * ct + g4, 16 * (OT * wave + ot) + l16);
+        if (w.c_inner) {
+          H[ct][ot] = *reinterpret_cast<const f32x4*>(at);
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) H[ct][ot][r] = at[r * DO];
+        }
       }
     }
-  }
   lds_barrier<0>();  // the weights and the first chunk are there
 
   // weights of the pairs (row t, row s <= t) of this wave's tiles and of E in row t
@@ -346,7 +363,7 @@ __global__ void __launch_bounds__(walk_threads<DO>(), walk_waves_per_simd(DC, DO
   if constexpr (!STATE) {
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
-      const int n = wave + WAVES * i;
+      const int n = wave + kWaves * i;
       tile_t[i] = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : n < 10 ? 3 : 4;
       tile_s[i] = n - tile_t[i] * (tile_t[i] + 1) / 2;
 #pragma unroll
@@ -361,11 +378,12 @@ __global__ void __launch_bounds__(walk_threads<DO>(), walk_waves_per_simd(DC, DO
   // the lane's places in the tiles
   const uint32_t at_a = lds_addr(lds.a), at_b = lds_addr(lds.b[0]), at_c = lds_addr(lds.c[0]), at_m = lds_addr(lds.m);
   const uint32_t rows_dc = row_frag<DC>(lane), quad_dc = quad_frag<DC>(lane), time_dc = time_frag<DC>(lane);
-  const uint32_t c_at = at_c + (time_frag<DO>(lane) ^ (32 * (wave % 2))) + 256 * (wave / 2);
-  const uint32_t c_next = at_c + (time_frag<DO>(lane) ^ (32 - 32 * (wave % 2))) + 256 * (wave / 2);
+  // of c: the wave's first tile of o, and the same one's rows 4 further on (its second tile's are exchanged)
+  const uint32_t time_do = time_frag<DO>(lane) ^ (uint32_t)(32 * (OT * wave % 2));
+  const uint32_t c_at = at_c + time_do + 256 * (OT * wave / 2), c_next = at_c + (time_do ^ 32u) + 256 * (OT * wave / 2);
   const uint32_t m_rows = at_m + row_frag<kC>(lane), m_quad = quad_frag<kC>(lane);
   const uint32_t row_bytes = (uint32_t)(p.heads * DO) * (w.sum ? 4u : 2u);
-  const uint32_t out_at = (uint32_t)(rev ? kC - 1 - l16 : l16) * row_bytes + (uint32_t)(16 * wave + g4) * (w.sum ? 4u : 2u);
+  const uint32_t out_at = (uint32_t)(rev ? kC - 1 - l16 : l16) * row_bytes + (uint32_t)(16 * OT * wave + g4) * (w.sum ? 4u : 2u);
 
   // a chunk; false behind the segment's last
   auto chunk = [&](int t, auto which) {
@@ -379,7 +397,7 @@ __global__ void __launch_bounds__(walk_threads<DO>(), walk_waves_per_simd(DC, DO
     }
     if (!STATE && t > 0 && rows < kC) set_weights(rows);
 
-    f32x4 out[4];  // element r: o = 16 wave + g4 + r, row 16 tt + l16
+    f32x4 out[OT][4];  // element r: o = 16 (OT wave + ot) + g4 + r, row 16 tt + l16
     if constexpr (!STATE) {
       // M[t][s] = a^{t-s} (a_t . b_s), a lane with 4 consecutive s of a row t
 #pragma unroll
@@ -402,7 +420,9 @@ __global__ void __launch_bounds__(walk_threads<DO>(), walk_waves_per_simd(DC, DO
       // E's part: the accumulators of H are the operand as they lie, its k axis being
       // c = 16 i + g4 + 0..3, then 16 (i + 2) + g4 + 0..3; a is read in that order
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) out[tt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int ot = 0; ot < OT; ++ot)
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) out[ot][tt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       if (have) {
         const uint32_t even = opaque(quad_dc) + at_a, odd = (opaque(quad_dc) ^ 32u) + at_a;
         Scale sc{1.0f, 1.0f};
@@ -411,55 +431,66 @@ __global__ void __launch_bounds__(walk_threads<DO>(), walk_waves_per_simd(DC, DO
 #pragma unroll
           for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) most = fmaxf(most, fabsf(H[ct][r]));
+            for (int ot = 0; ot < OT; ++ot)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) most = fmaxf(most, fabsf(H[ct][ot][r]));
           sc = wave_scale(most);
         }
 #pragma unroll
         for (int kk = 0; kk < CT / 2; ++kk) {
           const int i0 = 4 * (kk / 2) + kk % 2;
-          const uint32_t from = kk % 2 ? odd : even;
-          u32x4v eh, el, as[4];
+          const uint32_t from = (kk % 2 ? odd : even) + 512 * (kk / 2);
+          u32x4v eh[OT], el[OT], as[4];
 #pragma unroll
           for (int tt = 0; tt < 4; ++tt) {
-            const u32x2v a0 = lds8(from + tt * (16 * DC * 2) + 512 * (kk / 2)), a1 = lds8(from + tt * (16 * DC * 2) + 512 * (kk / 2) + 256);
+            const u32x2v a0 = lds8(from + tt * (16 * DC * 2)), a1 = lds8(from + tt * (16 * DC * 2) + 256);
             as[tt] = u32x4v{a0[0], a0[1], a1[0], a1[1]};
           }
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int ot = 0; ot < OT; ++ot)
 #pragma unroll
-            for (int r = 0; r < 4; r += 2) {
-              const float v0 = H[i0 + 2 * i][r], v1 = H[i0 + 2 * i][r + 1];
-              uint32_t hi, lo;
-              if constexpr (kTwo) split2_f16(v0 * sc.to, v1 * sc.to, hi, lo);
-              else split2(v0, v1, hi, lo);
-              eh[2 * i + r / 2] = hi;
-              el[2 * i + r / 2] = lo;
-            }
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int tt = 0; tt < 4; ++tt) out[tt] = mfma_t<IO>::run(as_vec<IO>(el), as_vec<IO>(as[tt]), out[tt]);
+              for (int r = 0; r < 4; r += 2) {
+                const float v0 = H[i0 + 2 * i][ot][r], v1 = H[i0 + 2 * i][ot][r + 1];
+                uint32_t hi, lo;
+                if constexpr (kTwo) split2_f16(v0 * sc.to, v1 * sc.to, hi, lo);
+                else split2(v0, v1, hi, lo);
+                eh[ot][2 * i + r / 2] = hi;
+                el[ot][2 * i + r / 2] = lo;
+              }
 #pragma unroll
-          for (int tt = 0; tt < 4; ++tt) out[tt] = mfma_t<IO>::run(as_vec<IO>(eh), as_vec<IO>(as[tt]), out[tt]);
+          for (int ot = 0; ot < OT; ++ot)
+#pragma unroll
+            for (int tt = 0; tt < 4; ++tt) out[ot][tt] = mfma_t<IO>::run(as_vec<IO>(el[ot]), as_vec<IO>(as[tt]), out[ot][tt]);
+#pragma unroll
+          for (int ot = 0; ot < OT; ++ot)
+#pragma unroll
+            for (int tt = 0; tt < 4; ++tt) out[ot][tt] = mfma_t<IO>::run(as_vec<IO>(eh[ot]), as_vec<IO>(as[tt]), out[ot][tt]);
         }
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt) out[tt] *= kTwo ? iw[tt] * sc.from : iw[tt];
+        for (int ot = 0; ot < OT; ++ot)
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt) out[ot][tt] *= kTwo ? iw[tt] * sc.from : iw[tt];
       }
       // M and c are there; b's next loads, issued behind c's, may be on their way
-      if (more) lds_barrier<tile_loads<DC, WAVES>()>();
+      if (more) lds_barrier<tile_loads<DC>()>();
       else lds_barrier<0>();
       if (more) load_a(t + kC);
       asm volatile("" ::: "memory");  // the outputs' stores come behind
     }
-    u32x4v cf[2];
+    u32x4v cf[2][OT];
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      const int at = (STATE ? turn * (kC * DO * 2) : 0) + 32 * ks * (DO * 2);
-      cf[ks] = read_time_frag<DO>(c_at + at, c_next + at);
-    }
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int ot = 0; ot < OT; ++ot) {
+        const int at = (STATE ? turn * (kC * DO * 2) : 0) + 32 * ks * (DO * 2);
+        cf[ks][ot] = read_time_frag<DO>((ot ? c_next : c_at) + at, (ot ? c_at : c_next) + at);
+      }
     if constexpr (!STATE) {
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        const Parts<IO> cs(cf[ks]);
-        bf16x8 mh[4], ml[4];
+        bf16x8 mh[4], ml[4], ch[OT], cl[OT];
 #pragma unroll
         for (int tt = 2 * ks; tt < 4; ++tt) {
           const uint32_t at = m_rows + tt * (16 * kC * 2) + 256 * ks;
@@ -467,65 +498,84 @@ __global__ void __launch_bounds__(walk_threads<DO>(), walk_waves_per_simd(DC, DO
           ml[tt] = bfv(lds16(at + kPlane));
         }
 #pragma unroll
-        for (int tt = 2 * ks; tt < 4; ++tt) out[tt] = BF::run(cs.hi, ml[tt], out[tt]);
-        if constexpr (kTwo) {
-#pragma unroll
-          for (int tt = 2 * ks; tt < 4; ++tt) out[tt] = BF::run(cs.lo, mh[tt], out[tt]);
+        for (int ot = 0; ot < OT; ++ot) {
+          const Parts<IO> cs(cf[ks][ot]);
+          ch[ot] = cs.hi;
+          cl[ot] = cs.lo;
         }
 #pragma unroll
-        for (int tt = 2 * ks; tt < 4; ++tt) out[tt] = BF::run(cs.hi, mh[tt], out[tt]);
+        for (int ot = 0; ot < OT; ++ot)
+#pragma unroll
+          for (int tt = 2 * ks; tt < 4; ++tt) out[ot][tt] = BF::run(ch[ot], ml[tt], out[ot][tt]);
+        if constexpr (kTwo) {
+#pragma unroll
+          for (int ot = 0; ot < OT; ++ot)
+#pragma unroll
+            for (int tt = 2 * ks; tt < 4; ++tt) out[ot][tt] = BF::run(cl[ot], mh[tt], out[ot][tt]);
+        }
+#pragma unroll
+        for (int ot = 0; ot < OT; ++ot)
+#pragma unroll
+          for (int tt = 2 * ks; tt < 4; ++tt) out[ot][tt] = BF::run(ch[ot], mh[tt], out[ot][tt]);
       }
       // ---- outputs: rows past the segment's last go nowhere
       const int size = w.sum ? 4 : 2;
       const auto ov = rows_view(static_cast<char*>(w.out) + (chunk_tok(t, rows) * p.heads + h) * (DO * size), row_bytes, rows, DO * size);
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
-        const f32x4 v = out[tt];
         uint32_t at = out_at;
         int ahead = (rev ? -16 * tt : 16 * tt) * (int)row_bytes;
         if (rows < kC) {
           const int row = 16 * tt + l16;
-          at = row < rows ? (uint32_t)(rev ? rows - 1 - row : row) * row_bytes + (uint32_t)((16 * wave + g4) * size) : 0x3fffe000u;
+          at = row < rows ? (uint32_t)(rev ? rows - 1 - row : row) * row_bytes + (uint32_t)((16 * OT * wave + g4) * size) : 0x3fffe000u;
           ahead = 0;
         } else if (rev) {
           at += (uint32_t)ahead;
           ahead = 0;
         }
-        if (w.sum) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4v, v), ov, at, ahead, 0);
-        else __builtin_amdgcn_raw_buffer_store_b64(u32x2v{pack2<IO>(v[0], v[1]), pack2<IO>(v[2], v[3])}, ov, at, ahead, 0);
+#pragma unroll
+        for (int ot = 0; ot < OT; ++ot) {
+          const f32x4 v = out[ot][tt];
+          if (w.sum) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4v, v), ov, at + 64 * ot, ahead, 0);
+          else __builtin_amdgcn_raw_buffer_store_b64(u32x2v{pack2<IO>(v[0], v[1]), pack2<IO>(v[2], v[3])}, ov, at + 32 * ot, ahead, 0);
+        }
       }
     }
     // ---- H <- a^rows H + sum_s a^{rows-1-s} b_s c_s^T
     if (!STATE && !more && !(q.last && fin)) return false;  // nobody takes it
     const float d = *lds.weight(kDecays + (rows < kC ? 1 : 0));
-    const uint32_t even = opaque(time_dc) + at_b, odd = (opaque(time_dc) ^ 32u) + at_b;
+    const uint32_t even = opaque(time_dc) + at_b + turn * kTile, odd = (opaque(time_dc) ^ 32u) + at_b + turn * kTile;
     auto b_frag = [&](int ks, int ct) {
-      const uint32_t at = turn * kTile + 32 * ks * (DC * 2) + 256 * (ct / 2);
+      const uint32_t at = 32 * ks * (DC * 2) + 256 * (ct / 2);
       return as_vec<IO>(read_time_frag<DC>((ct % 2 ? odd : even) + at, (ct % 2 ? even : odd) + at));
     };
     // w_s c_s of the rows 32 ks + 2 g4 + 2 e, + 1
-    auto weighted = [&](int ks, int e, float& v0, float& v1) {
+    auto weighted = [&](int ks, int e, int ot, float& v0, float& v1) {
       const f32x2 u = *lds_ptr<f32x2>(lds_addr(lds.weight(32 * ks + 2 * g4 + 2 * e)));
-      v0 = low16<IO>(cf[ks][e]) * u[0];
-      v1 = high16<IO>(cf[ks][e]) * u[1];
+      v0 = low16<IO>(cf[ks][ot][e]) * u[0];
+      v1 = high16<IO>(cf[ks][ot][e]) * u[1];
     };
     if constexpr (!kTwo) {
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) H[ct][r] = fmaf(d, H[ct][r], H[ct][r]);
+        for (int ot = 0; ot < OT; ++ot)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) H[ct][ot][r] = fmaf(d, H[ct][ot][r], H[ct][ot][r]);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        u32x4v part[3];
+        u32x4v part[OT][3];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float v0, v1;
-          uint32_t v[3];
-          weighted(ks, e, v0, v1);
-          split3(v0, v1, v);
+        for (int ot = 0; ot < OT; ++ot)
 #pragma unroll
-          for (int i = 0; i < 3; ++i) part[i][e] = v[i];
-        }
+          for (int e = 0; e < 4; ++e) {
+            float v0, v1;
+            uint32_t v[3];
+            weighted(ks, e, ot, v0, v1);
+            split3(v0, v1, v);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) part[ot][i][e] = v[i];
+          }
 #pragma unroll
         for (int c0 = 0; c0 < CT; c0 += 4) {
           typename mfma_t<IO>::V bs[4];
@@ -534,34 +584,42 @@ __global__ void __launch_bounds__(walk_threads<DO>(), walk_waves_per_simd(DC, DO
 #pragma unroll
           for (int j = 2; j >= 0; --j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) H[c0 + i] = mfma_t<IO>::run(bs[i], as_vec<IO>(part[j]), H[c0 + i]);
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int ot = 0; ot < OT; ++ot) H[c0 + i][ot] = mfma_t<IO>::run(bs[i], as_vec<IO>(part[ot][j]), H[c0 + i][ot]);
         }
       }
     } else {
-      float wc[2][8], most = 0.0f;
+      float wc[2][OT][8], most = 0.0f;
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          weighted(ks, e, wc[ks][2 * e], wc[ks][2 * e + 1]);
-          most = fmaxf(most, fmaxf(fabsf(wc[ks][2 * e]), fabsf(wc[ks][2 * e + 1])));
-        }
+        for (int ot = 0; ot < OT; ++ot)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            weighted(ks, e, ot, wc[ks][ot][2 * e], wc[ks][ot][2 * e + 1]);
+            most = fmaxf(most, fmaxf(fabsf(wc[ks][ot][2 * e]), fabsf(wc[ks][ot][2 * e + 1])));
+          }
       const Scale sc = wave_scale(most);
-      u32x4v part[2][2];
+      u32x4v part[2][OT][2];
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t hi, lo;
-          split2_f16(wc[ks][2 * e] * sc.to, wc[ks][2 * e + 1] * sc.to, hi, lo);
-          part[ks][0][e] = hi;
-          part[ks][1][e] = lo;
-        }
+        for (int ot = 0; ot < OT; ++ot)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t hi, lo;
+            split2_f16(wc[ks][ot][2 * e] * sc.to, wc[ks][ot][2 * e + 1] * sc.to, hi, lo);
+            part[ks][ot][0][e] = hi;
+            part[ks][ot][1][e] = lo;
+          }
 #pragma unroll
       for (int c0 = 0; c0 < CT; c0 += 4) {
-        f32x4 own[4];  // at their scale
+        f32x4 own[4][OT];  // at their scale
 #pragma unroll
-        for (int i = 0; i < 4; ++i) own[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int ot = 0; ot < OT; ++ot) own[i][ot] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
           typename mfma_t<IO>::V bs[4];
@@ -570,38 +628,44 @@ __global__ void __launch_bounds__(walk_threads<DO>(), walk_waves_per_simd(DC, DO
 #pragma unroll
           for (int j = 1; j >= 0; --j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) own[i] = mfma_t<IO>::run(bs[i], as_vec<IO>(part[ks][j]), own[i]);
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int ot = 0; ot < OT; ++ot) own[i][ot] = mfma_t<IO>::run(bs[i], as_vec<IO>(part[ks][ot][j]), own[i][ot]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            H[c0 + i][r] = fmaf(own[i][r], sc.from, fmaf(d, H[c0 + i][r], H[c0 + i][r]));
+          for (int ot = 0; ot < OT; ++ot)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              H[c0 + i][ot][r] = fmaf(own[i][ot][r], sc.from, fmaf(d, H[c0 + i][ot][r], H[c0 + i][ot][r]));
       }
     }
     have = true;
     // the next chunk's a and b are there (the outputs' stores, issued behind them, may be on
     // their way), and everyone is done with this one
-    if (more) lds_barrier<STATE ? 0 : 4>();
+    if (more) lds_barrier<STATE ? 0 : 4 * OT>();
     return more;
   };
   if (q.rows > 0)
     for (int t = 0; chunk(t, std::integral_constant<int, 0>{}) && chunk(t + kC, std::integral_constant<int, 1>{}); t += 2 * kC) {
     }
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    if constexpr (STATE) {
-      *reinterpret_cast<f32x4*>(ws + ct * 256) = H[ct];
-    } else if (q.last && fin) {
-      float* at = fin + state_at(w, 16 * ct + g4, 16 * wave + l16);
-      if (w.c_inner) {
-        *reinterpret_cast<f32x4*>(at) = H[ct];
-      } else {
+  for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) at[r * DO] = H[ct][r];
+    for (int ot = 0; ot < OT; ++ot) {
+      if constexpr (STATE) {
+        *reinterpret_cast<f32x4*>(ws + (ct * OT + ot) * 256) = H[ct][ot];
+      } else if (q.last && fin) {
+        float* at = fin + state_at(w, 16 * ct + g4, 16 * (OT * wave + ot) + l16);
+        if (w.c_inner) {
+          *reinterpret_cast<f32x4*>(at) = H[ct][ot];
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) at[r * DO] = H[ct][ot][r];
+        }
       }
     }
-  }
 }
 
 // ---- the states between the segments of a sequence ----------------------------------
@@ -637,9 +701,11 @@ __global__ void __launch_bounds__(256) lin_pass_kernel(LinParams p) {
   lin_states(p, w, s, h, init, fin);
   f32x4 E = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   if (init) {
-    const int ct_n = w.dc / 16, tile = e4 / 64, lane = e4 % 64, ct = tile % ct_n, wave = tile / ct_n;
+    const int ct_n = w.dc / 16, ot_n = w.dout / 64, tile = e4 / 64, lane = e4 % 64;
+    const int ot = tile % ot_n, ct = tile / ot_n % ct_n, wave = tile / ot_n / ct_n;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) E[r] = init[state_at(w, 16 * ct + 4 * (lane / 16) + r, 16 * wave + lane % 16)];
+    for (int r = 0; r < 4; ++r)
+      E[r] = init[state_at(w, 16 * ct + 4 * (lane / 16) + r, 16 * (ot_n * wave + ot) + lane % 16)];
   }
   const int64_t step = (int64_t)p.jobs * p.heads * size;
   float* ws = p.ws + (((int64_t)first * p.jobs + job) * p.heads + h) * size + 4 * (int64_t)e4;
@@ -723,8 +789,8 @@ __global__ void __launch_bounds__(256) lin_step_kernel(LinStepParams p) {
 template <int IO, int DC, int DO>
 hipError_t launch_walk(const LinParams& p, hipStream_t st) {
   const dim3 grid((uint32_t)(p.places * p.heads * p.njobs));
-  if (p.split) hipLaunchKernelGGL((lin_walk_kernel<IO, DC, DO, true>), grid, dim3(walk_threads<DO>()), 0, st, p);
-  else hipLaunchKernelGGL((lin_walk_kernel<IO, DC, DO, false>), grid, dim3(walk_threads<DO>()), 0, st, p);
+  if (p.split) hipLaunchKernelGGL((lin_walk_kernel<IO, DC, DO, true>), grid, dim3(kWalkThreads), 0, st, p);
+  else hipLaunchKernelGGL((lin_walk_kernel<IO, DC, DO, false>), grid, dim3(kWalkThreads), 0, st, p);
   return hipGetLastError();
 }
 template <int IO>
