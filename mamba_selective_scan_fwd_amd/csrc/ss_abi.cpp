@@ -915,7 +915,7 @@ ss_status check_linattn_heads(const ss_linattn_problem* p) {
   return SS_OK;
 }
 struct LinPlan {
-  int logq;
+  int segment;
   int64_t places;
   size_t states, parts, total;  // bytes of the segments' states, and where the shared heads' parts begin
 };
@@ -928,12 +928,11 @@ ss_status plan_linattn(const ss_linattn_problem* p, int jobs, LinPlan* plan) {
   if (p->q_stride % 8 || p->k_stride % 8 || p->v_stride % 8) return SS_ERR_MISALIGNED;
   const int64_t longest = p->packed ? p->tokens : p->tokens / p->nseqs, walks = p->nheads * jobs;
   LinPlan l{};
-  l.logq = ss::lin_segments(p->tokens, p->nseqs, longest, walks, 256);
-  l.places = p->packed ? (p->tokens >> l.logq) + p->nseqs
-                       : p->nseqs * ((longest + ((int64_t)1 << l.logq) - 1) >> l.logq);
+  l.segment = ss::lin_segment(p->tokens, p->nseqs, longest, walks, 256);
+  l.places = p->packed ? p->tokens / l.segment + p->nseqs : p->nseqs * ((longest + l.segment - 1) / l.segment);
   if (l.places * walks > kMaxGrid || p->nseqs * walks * (p->dk * p->dv / 1024) > kMaxGrid) return SS_ERR_BAD_SHAPE;
   if (jobs > 1 && p->tokens * p->nheads > kMaxGrid * 8) return SS_ERR_BAD_SHAPE;  // the shared heads' sums
-  l.states = l.logq == ss::kLinWhole ? 0 : align256((size_t)(l.places * walks) * (size_t)(p->dk * p->dv) * 4);
+  l.states = l.segment == ss::kLinWhole ? 0 : align256((size_t)(l.places * walks) * (size_t)(p->dk * p->dv) * 4);
   l.parts = l.states;
   l.total = l.parts + (jobs > 1 && p->kv_heads != p->nheads
                            ? align256((size_t)(p->tokens * p->nheads) * (size_t)(p->dk + p->dv) * 4) : 0);
@@ -956,11 +955,11 @@ ss::LinParams linattn_params(const ss_linattn_problem* p, const LinPlan& l, cons
   k.io = p->io_dtype;
   k.log_decay = log_decay;
   k.cu = cu;
-  k.split = l.logq != ss::kLinWhole;
+  k.split = l.segment != ss::kLinWhole;
   k.ws = static_cast<float*>(workspace);
   k.tokens = (int32_t)p->tokens; k.nseqs = (int32_t)p->nseqs;
   k.heads = (int32_t)p->nheads; k.share = (int32_t)(p->nheads / p->kv_heads);
-  k.logq = l.logq; k.places = (int32_t)l.places;
+  k.segment = l.segment; k.places = (int32_t)l.places;
   return k;
 }
 ss::LinWalk linattn_forward(const ss_linattn_problem* p, const void* q, const void* k, const void* v,

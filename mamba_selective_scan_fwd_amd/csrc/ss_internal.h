@@ -325,7 +325,7 @@ struct LinParams {
   int32_t split;             // this launch computes the segments' own states
   float* ws;                 // (places, jobs, heads, dk * dv): a segment's own state, then the state that enters it
   int32_t tokens, nseqs, nslots, heads, share;  // share: heads to a key and value
-  int32_t logq;              // a segment has 2^logq rows
+  int32_t segment;           // rows of a segment, a multiple of 64
   int32_t places;
 };
 

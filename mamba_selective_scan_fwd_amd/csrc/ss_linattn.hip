@@ -74,31 +74,31 @@ __device__ __forceinline__ u32x4v read_time_frag(uint32_t at, uint32_t next) {
 // The rows that workgroup place `place` walks.
 struct LinRows {
   int seq, begin, len;  // the sequence
-  int part;             // of its segments of 2^logq rows; the place is empty if out of range
-  int t0, rows;         // the segment's rows, in the walk's order
-  bool live, last;
+  int t0, rows;         // its segment's rows, in the walk's order
+  bool live, last;      // the place has a segment (of an empty sequence too); the sequence's last
 };
 __device__ __forceinline__ LinRows lin_rows(const LinParams& p, int place) {
   LinRows r;
+  int part;
   if (p.cu) {
-    const SeqChunk q = find_chunk(p.cu, p.nseqs, p.tokens, place, p.logq);
+    const uint32_t segment = (uint32_t)p.segment;
+    const SeqChunk q = find_chunk_by(p.cu, p.nseqs, p.tokens, place, [=](int row) { return (int)((uint32_t)row / segment); });
     r.seq = q.seq;
     r.begin = q.begin;
     r.len = q.len;
-    r.part = q.chunk;
+    part = q.chunk;
   } else {
     r.len = p.tokens / p.nseqs;
-    const int parts = (int)(((int64_t)r.len + ((int64_t)1 << p.logq) - 1) >> p.logq);
+    const int parts = (r.len + p.segment - 1) / p.segment;
     r.seq = place / parts;
-    r.part = place - r.seq * parts;
+    part = place - r.seq * parts;
     r.begin = r.seq * r.len;
   }
-  const int64_t t0 = (int64_t)r.part << p.logq;
-  r.live = r.part >= 0 && t0 < (r.len > 0 ? r.len : 1);
+  const int64_t t0 = (int64_t)part * p.segment, left = r.len - t0;
+  r.live = part >= 0 && t0 < (r.len > 0 ? r.len : 1);
   r.t0 = r.live ? (int)t0 : 0;
-  const int64_t left = r.len - t0, most = (int64_t)1 << p.logq;
-  r.rows = r.live ? (int)(left < most ? left : most) : 0;
-  r.last = left <= most;
+  r.rows = r.live ? (int)(left < p.segment ? left : p.segment) : 0;
+  r.last = left <= p.segment;
   return r;
 }
 // A sequence's first state (null: zeros) and where its last one goes (null: nowhere)
@@ -178,6 +178,32 @@ struct Parts {
   }
 };
 
+// ss_mfma.h's split2 and split3 with a remainder in one instruction: v - p of a pair of bf16 p is a
+// dot product with (-1, 0) or (0, -1) onto v, exact as the remainder is (checked on the chip).
+// The constants come from registers, for as an inline operand -1 is one of fp32.
+struct Remainder {
+  bf16x2 low, high;
+  __device__ __forceinline__ Remainder() {
+    uint32_t a, b;
+    asm("s_mov_b32 %0, 0xbf80" : "=s"(a));
+    asm("s_mov_b32 %0, 0xbf800000" : "=s"(b));
+    low = __builtin_bit_cast(bf16x2, a);
+    high = __builtin_bit_cast(bf16x2, b);
+  }
+  __device__ __forceinline__ void take(uint32_t p, float& v0, float& v1) const {
+    v0 = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p), low, v0, false);
+    v1 = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p), high, v1, false);
+  }
+  template <int N>
+  __device__ __forceinline__ void split(float v0, float v1, uint32_t (&w)[N]) const {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      w[k] = pack2<SS_BF16>(v0, v1);
+      if (k + 1 < N) take(w[k], v0, v1);
+    }
+  }
+};
+
 // v as two fp16 parts, |v - hi - lo| <= 2^-22 |v| where |v| is within a factor of 2^15 of the
 // largest that its scale is taken from (2^-38 of that one below)
 __device__ __forceinline__ void split2_f16(float v0, float v1, uint32_t& hi, uint32_t& lo) {
@@ -211,13 +237,12 @@ __device__ __forceinline__ void lds_barrier() {
 
 // 16 bytes a lane from a view (its four words) into LDS at `to` + 16 lane.  In assembly, for the
 // compiler would wait for such a load before the next access to LDS that it cannot tell apart
-// from its target: it ends before the barrier that waits for memory (lds_barrier), and nothing
-// between reads what it writes.
+// from its target.  A load keeps its place among the barriers (lds_barrier), which tell both
+// the compiler and the waves when LDS changes; between them accesses may pass it, for nobody
+// reads its target before the next barrier that waits for memory, or after the last one.
 __device__ __forceinline__ void lds_load(u32x4v view, uint32_t to, uint32_t off, int ahead) {
-  asm volatile(
-      "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(uniform((int)to)), "v"(off), "s"(view),
-      "s"(uniform(ahead))
-      : "memory");  // m0 is nobody else's
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(uniform((int)to)), "v"(off),
+               "s"(view), "s"(uniform(ahead)));  // m0 is nobody else's
 }
 
 // The rows of a chunk into a tile: a wave's load fills 1 KB of it, 16 bytes a lane in the
@@ -240,7 +265,9 @@ struct TileLoad {
     lane_piece(wave, lane, row, piece);
     whole = (uint32_t)(rev ? kRows * kWaves - 1 - row : row) * (uint32_t)(stride * 2) + (uint32_t)piece * 16u;
   }
-  __device__ __forceinline__ void load(char* tile, const char* at, int64_t stride, int rows, bool rev, int wave, int lane) const {
+  // loads k0 .. k1 - 1 of a chunk
+  __device__ __forceinline__ void load(char* tile, const char* at, int64_t stride, int rows, bool rev, int wave, int lane, int k0 = 0,
+                                       int k1 = kLoads) const {
     const uint64_t base = (uint64_t)(uintptr_t)at;
     const u32x4v v = {(uint32_t)uniform((int)(uint32_t)base), (uint32_t)uniform((int)((base >> 32) & 0xffffu)),
                       (uint32_t)uniform((int)view_bytes(stride * 2, rows, W * 2)), (uint32_t)kRsrcWord3};
@@ -248,20 +275,22 @@ struct TileLoad {
     if (rows == kC) {
 #pragma unroll
       for (int k = 0; k < kLoads; ++k)
-        lds_load(v, to + kWaves * 1024 * k, whole, (rev ? kLoads - 1 - k : k) * (kRows * kWaves) * (int)(stride * 2));
+        if (k >= k0 && k < k1)
+          lds_load(v, to + kWaves * 1024 * k, whole, (rev ? kLoads - 1 - k : k) * (kRows * kWaves) * (int)(stride * 2));
       return;
     }
     int row, piece;
     lane_piece(wave, opaque(lane), row, piece);
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) {
+      if (k < k0 || k >= k1) continue;
       const int r = row + k * (kRows * kWaves), in = r < rows ? r : rows - 1;
       lds_load(v, to + kWaves * 1024 * k, (uint32_t)(rev ? rows - 1 - in : in) * (uint32_t)(stride * 2) + (uint32_t)piece * 16u, 0);
     }
   }
 };
 
-template <int IO, int DC, int DO, bool STATE>
+template <int IO, int DC, int DO, bool STATE, bool FULL>
 __global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) {
   constexpr int CT = DC / 16, OT = DO / 64;  // tiles of a wave's state: all of c, a quarter of o
   constexpr int kPairs = 3;                  // 16 x 16 tiles of pairs a wave, at the most
@@ -338,23 +367,25 @@ __global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) 
   float* ws = p.ws + (((int64_t)place * p.jobs + job) * p.heads + h) * (DC * DO) + wave * (CT * OT * 256) + lane * 4;
   f32x4 H[CT][OT];  // element r: c = 16 ct + g4 + r, o = 16 (OT wave + ot) + l16
   bool have = !STATE && (several || init);
+  auto each = [&](auto f) {
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct)
+    for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-    for (int ot = 0; ot < OT; ++ot) {
-      H[ct][ot] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      if (!STATE && several) {
-        H[ct][ot] = *reinterpret_cast<const f32x4*>(ws + (ct * OT + ot) * 256);
-      } else if (have) {
-        const float* at = init + state_at(w, 16 * ct + g4, 16 * (OT * wave + ot) + l16);
-        if (w.c_inner) {
-          H[ct][ot] = *reinterpret_cast<const f32x4*>(at);
-        } else {
+      for (int ot = 0; ot < OT; ++ot) f(ct, ot);
+  };
+  const int at0 = state_at(w, g4, 16 * OT * wave + l16), at_c1 = state_at(w, 16, 0), at_o1 = state_at(w, 0, 16);
+  if (!STATE && several) {
+    each([&](int ct, int ot) { H[ct][ot] = *reinterpret_cast<const f32x4*>(ws + (ct * OT + ot) * 256); });
+  } else if (have && w.c_inner) {
+    each([&](int ct, int ot) { H[ct][ot] = *reinterpret_cast<const f32x4*>(init + at0 + ct * at_c1 + ot * at_o1); });
+  } else if (have) {
+    each([&](int ct, int ot) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) H[ct][ot][r] = at[r * DO];
-        }
-      }
-    }
+      for (int r = 0; r < 4; ++r) H[ct][ot][r] = init[at0 + ct * at_c1 + ot * at_o1 + r * DO];
+    });
+  } else {
+    each([&](int ct, int ot) { H[ct][ot] = f32x4{0.0f, 0.0f, 0.0f, 0.0f}; });
+  }
   lds_barrier<0>();  // the weights and the first chunk are there
 
   // weights of the pairs (row t, row s <= t) of this wave's tiles and of E in row t
@@ -383,17 +414,22 @@ __global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) 
   const uint32_t c_at = at_c + time_do + 256 * (OT * wave / 2), c_next = at_c + (time_do ^ 32u) + 256 * (OT * wave / 2);
   const uint32_t m_rows = at_m + row_frag<kC>(lane), m_quad = quad_frag<kC>(lane);
   const uint32_t row_bytes = (uint32_t)(p.heads * DO) * (w.sum ? 4u : 2u);
-  const uint32_t out_at = (uint32_t)(rev ? kC - 1 - l16 : l16) * row_bytes + (uint32_t)(16 * OT * wave + g4) * (w.sum ? 4u : 2u);
+  // the lane's columns of an output's row, in bytes
+  const uint32_t out_col = (uint32_t)(32 * OT * wave) * (w.sum ? 2u : 1u) +
+                           (w.sum || OT == 1 ? (uint32_t)g4 * (w.sum ? 4u : 2u) : (uint32_t)(lane / 16 % 2 * 32 + lane / 32 * 16));
+  const uint32_t out_at = (uint32_t)(rev ? kC - 1 - l16 : l16) * row_bytes + out_col;
 
+  const Remainder rem;
   // a chunk; false behind the segment's last
   auto chunk = [&](int t, auto which) {
     constexpr int turn = decltype(which)::value;
     const int rows = chunk_rows(t);
     const bool more = t + kC < q.rows;
-    if constexpr (!STATE) load_c(t, 0);
-    if (more) {
+    if constexpr (!STATE) {
+      load_c(t, 0);
+    } else if (more) {
       load_b(t + kC, turn ^ 1);
-      if constexpr (STATE) load_c(t + kC, turn ^ 1);
+      load_c(t + kC, turn ^ 1);
     }
     if (!STATE && t > 0 && rows < kC) set_weights(rows);
 
@@ -410,13 +446,14 @@ __global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) 
         for (int ks = 0; ks < DC / 32; ++ks)
           acc[ks & 1] = mfma_t<IO>::run(as_vec<IO>(lds16(bs + 256 * ks)), as_vec<IO>(lds16(as + 256 * ks)), acc[ks & 1]);
         acc[0] += acc[1];
-        uint32_t h0, h1, l0, l1;
-        split2(acc[0][0] * mw[i][0], acc[0][1] * mw[i][1], h0, l0);
-        split2(acc[0][2] * mw[i][2], acc[0][3] * mw[i][3], h1, l1);
+        uint32_t m0[2], m1[2];
+        rem.split(acc[0][0] * mw[i][0], acc[0][1] * mw[i][1], m0);
+        rem.split(acc[0][2] * mw[i][2], acc[0][3] * mw[i][3], m1);
         const uint32_t at = (opaque(m_quad) ^ (uint32_t)(32 * (tile_s[i] % 2))) + at_m + tile_t[i] * (16 * kC * 2) + 256 * (tile_s[i] / 2);
-        *lds_ptr<u32x2v>(at) = u32x2v{h0, h1};
-        *lds_ptr<u32x2v>(at + kPlane) = u32x2v{l0, l1};
+        *lds_ptr<u32x2v>(at) = u32x2v{m0[0], m1[0]};
+        *lds_ptr<u32x2v>(at + kPlane) = u32x2v{m0[1], m1[1]};
       }
+      if (more) load_b(t + kC, turn ^ 1);
       // E's part: the accumulators of H are the operand as they lie, its k axis being
       // c = 16 i + g4 + 0..3, then 16 (i + 2) + g4 + 0..3; a is read in that order
 #pragma unroll
@@ -453,11 +490,11 @@ __global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) 
 #pragma unroll
               for (int r = 0; r < 4; r += 2) {
                 const float v0 = H[i0 + 2 * i][ot][r], v1 = H[i0 + 2 * i][ot][r + 1];
-                uint32_t hi, lo;
-                if constexpr (kTwo) split2_f16(v0 * sc.to, v1 * sc.to, hi, lo);
-                else split2(v0, v1, hi, lo);
-                eh[ot][2 * i + r / 2] = hi;
-                el[ot][2 * i + r / 2] = lo;
+                uint32_t v[2];
+                if constexpr (kTwo) split2_f16(v0 * sc.to, v1 * sc.to, v[0], v[1]);
+                else rem.split(v0, v1, v);
+                eh[ot][2 * i + r / 2] = v[0];
+                el[ot][2 * i + r / 2] = v[1];
               }
 #pragma unroll
           for (int ot = 0; ot < OT; ++ot)
@@ -527,17 +564,24 @@ __global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) 
         int ahead = (rev ? -16 * tt : 16 * tt) * (int)row_bytes;
         if (rows < kC) {
           const int row = 16 * tt + l16;
-          at = row < rows ? (uint32_t)(rev ? rows - 1 - row : row) * row_bytes + (uint32_t)((16 * OT * wave + g4) * size) : 0x3fffe000u;
+          at = row < rows ? (uint32_t)(rev ? rows - 1 - row : row) * row_bytes + out_col : 0x3fffe000u;
           ahead = 0;
         } else if (rev) {
           at += (uint32_t)ahead;
           ahead = 0;
         }
+        if (w.sum) {
 #pragma unroll
-        for (int ot = 0; ot < OT; ++ot) {
-          const f32x4 v = out[ot][tt];
-          if (w.sum) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4v, v), ov, at + 64 * ot, ahead, 0);
-          else __builtin_amdgcn_raw_buffer_store_b64(u32x2v{pack2<IO>(v[0], v[1]), pack2<IO>(v[2], v[3])}, ov, at + 32 * ot, ahead, 0);
+          for (int ot = 0; ot < OT; ++ot)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4v, out[ot][tt]), ov, at + 64 * ot, ahead, 0);
+        } else if constexpr (OT == 1) {
+          const f32x4 v = out[0][tt];
+          __builtin_amdgcn_raw_buffer_store_b64(u32x2v{pack2<IO>(v[0], v[1]), pack2<IO>(v[2], v[3])}, ov, at, ahead, 0);
+        } else {  // lane groups exchange their halves, so that each has 8 columns of one of the tiles
+          const f32x4 v0 = out[0][tt], v1 = out[OT - 1][tt];
+          const auto x = __builtin_amdgcn_permlane16_swap(pack2<IO>(v0[0], v0[1]), pack2<IO>(v1[0], v1[1]), false, false);
+          const auto y = __builtin_amdgcn_permlane16_swap(pack2<IO>(v0[2], v0[3]), pack2<IO>(v1[2], v1[3]), false, false);
+          __builtin_amdgcn_raw_buffer_store_b128(u32x4v{x[0], y[0], x[1], y[1]}, ov, at, ahead, 0);
         }
       }
     }
@@ -556,6 +600,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) 
       v1 = high16<IO>(cf[ks][ot][e]) * u[1];
     };
     if constexpr (!kTwo) {
+      constexpr int kParts = FULL ? 3 : 2;
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
@@ -564,17 +609,17 @@ __global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) 
           for (int r = 0; r < 4; ++r) H[ct][ot][r] = fmaf(d, H[ct][ot][r], H[ct][ot][r]);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        u32x4v part[OT][3];
+        u32x4v part[OT][kParts];
 #pragma unroll
         for (int ot = 0; ot < OT; ++ot)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float v0, v1;
-            uint32_t v[3];
+            uint32_t v[kParts];
             weighted(ks, e, ot, v0, v1);
-            split3(v0, v1, v);
+            rem.split(v0, v1, v);
 #pragma unroll
-            for (int i = 0; i < 3; ++i) part[ot][i][e] = v[i];
+            for (int i = 0; i < kParts; ++i) part[ot][i][e] = v[i];
           }
 #pragma unroll
         for (int c0 = 0; c0 < CT; c0 += 4) {
@@ -582,7 +627,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) 
 #pragma unroll
           for (int i = 0; i < 4; ++i) bs[i] = b_frag(ks, c0 + i);
 #pragma unroll
-          for (int j = 2; j >= 0; --j)
+          for (int j = kParts - 1; j >= 0; --j)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -642,30 +687,24 @@ __global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) 
       }
     }
     have = true;
-    // the next chunk's a and b are there (the outputs' stores, issued behind them, may be on
-    // their way), and everyone is done with this one
-    if (more) lds_barrier<STATE ? 0 : 4 * OT>();
+    // the next chunk's a and b are there (the outputs' stores, four at the least, issued behind them,
+    // may be on their way), and everyone is done with this one
+    if (more) lds_barrier<STATE ? 0 : 4>();
     return more;
   };
   if (q.rows > 0)
     for (int t = 0; chunk(t, std::integral_constant<int, 0>{}) && chunk(t + kC, std::integral_constant<int, 1>{}); t += 2 * kC) {
     }
+  if constexpr (STATE) {
+    each([&](int ct, int ot) { *reinterpret_cast<f32x4*>(ws + (ct * OT + ot) * 256) = H[ct][ot]; });
+  } else if (q.last && fin && w.c_inner) {
+    each([&](int ct, int ot) { *reinterpret_cast<f32x4*>(fin + at0 + ct * at_c1 + ot * at_o1) = H[ct][ot]; });
+  } else if (q.last && fin) {
+    each([&](int ct, int ot) {
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-    for (int ot = 0; ot < OT; ++ot) {
-      if constexpr (STATE) {
-        *reinterpret_cast<f32x4*>(ws + (ct * OT + ot) * 256) = H[ct][ot];
-      } else if (q.last && fin) {
-        float* at = fin + state_at(w, 16 * ct + g4, 16 * (OT * wave + ot) + l16);
-        if (w.c_inner) {
-          *reinterpret_cast<f32x4*>(at) = H[ct][ot];
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) at[r * DO] = H[ct][ot][r];
-        }
-      }
-    }
+      for (int r = 0; r < 4; ++r) fin[at0 + ct * at_c1 + ot * at_o1 + r * DO] = H[ct][ot][r];
+    });
+  }
 }
 
 // ---- the states between the segments of a sequence ----------------------------------
@@ -688,14 +727,14 @@ __global__ void __launch_bounds__(256) lin_pass_kernel(LinParams p) {
   if (p.cu) {
     begin = uniform(seq_row(p.cu, s, p.tokens));
     len = uniform(seq_row(p.cu, s + 1, p.tokens)) - begin;
-    first = (begin >> p.logq) + s;
+    first = begin / p.segment + s;
   } else {
     len = p.tokens / p.nseqs;
-    first = s * (int)(((int64_t)len + ((int64_t)1 << p.logq) - 1) >> p.logq);
+    first = s * ((len + p.segment - 1) / p.segment);
   }
-  if (len <= ((int64_t)1 << p.logq)) return;
-  const int n = (int)(((int64_t)len + ((int64_t)1 << p.logq) - 1) >> p.logq);
-  const float d = lin_power_m1(p.log_decay[h], 1 << p.logq);
+  if (len <= p.segment) return;
+  const int n = (len + p.segment - 1) / p.segment;
+  const float d = lin_power_m1(p.log_decay[h], p.segment);
   const float* init;
   float* fin;
   lin_states(p, w, s, h, init, fin);
@@ -786,12 +825,23 @@ __global__ void __launch_bounds__(256) lin_step_kernel(LinStepParams p) {
   }
 }
 
-template <int IO, int DC, int DO>
+template <int IO, int DC, int DO, bool FULL>
 hipError_t launch_walk(const LinParams& p, hipStream_t st) {
   const dim3 grid((uint32_t)(p.places * p.heads * p.njobs));
-  if (p.split) hipLaunchKernelGGL((lin_walk_kernel<IO, DC, DO, true>), grid, dim3(kWalkThreads), 0, st, p);
-  else hipLaunchKernelGGL((lin_walk_kernel<IO, DC, DO, false>), grid, dim3(kWalkThreads), 0, st, p);
+  if (p.split) hipLaunchKernelGGL((lin_walk_kernel<IO, DC, DO, true, FULL>), grid, dim3(kWalkThreads), 0, st, p);
+  else hipLaunchKernelGGL((lin_walk_kernel<IO, DC, DO, false, FULL>), grid, dim3(kWalkThreads), 0, st, p);
   return hipGetLastError();
+}
+// fp16's weighted rows are two parts (split2_f16).  Of bf16's, three keep fp32's error in the last states;
+// where no walk has any, its outputs are all that shows and two do (a training layer's
+// gradients: PARTS2 us against PARTS3).
+template <int IO, int DC, int DO>
+hipError_t launch_walk(const LinParams& p, hipStream_t st) {
+  bool full = false;
+  for (int j = 0; j < p.jobs; ++j) full = full || p.job[j].fin;
+  if constexpr (IO == SS_BF16)
+    if (full) return launch_walk<IO, DC, DO, true>(p, st);
+  return launch_walk<IO, DC, DO, false>(p, st);
 }
 template <int IO>
 hipError_t launch_walks_io(LinParams p, hipStream_t st) {

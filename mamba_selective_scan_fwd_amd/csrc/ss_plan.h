@@ -37,15 +37,23 @@ inline int pass_ahead(int64_t workgroups, int64_t chunks, int64_t nseqs, int64_t
   return workgroups <= 4 * cus && chunks >= 8 * nseqs ? 16 : 4;
 }
 
-// Rows of the segments, 2^this, in which linear attention walks its sequences: the
-// longest that give two workgroups to a CU (a sequence of `longest` rows at the
-// most, all of them `tokens`), 128 at the least; kLinWhole where that splits none.
-constexpr int kLinWhole = 30;
-inline int lin_segments(int64_t tokens, int64_t nseqs, int64_t longest, int64_t walks, int64_t cus) {
-  if (nseqs * longest == tokens && nseqs * walks >= cus) return kLinWhole;  // all alike, and enough of them
-  int logq = 7;
-  while (logq < kLinWhole && (tokens >> (logq + 1)) * walks >= 2 * cus) ++logq;
-  return ((int64_t)1 << logq) >= longest ? kLinWhole : logq;
+// Rows of the segments in which linear attention walks its sequences (the longest
+// of `longest` rows, all of them of `tokens`; `walks` of each), a multiple of 64, or
+// kLinWhole where none is split: as many segments as give every CU two workgroups at
+// once, none of less than kLinLeast rows.
+constexpr int kLinWhole = 1 << 30, kLinLeast = 512;
+inline int lin_segment(int64_t tokens, int64_t nseqs, int64_t longest, int64_t walks, int64_t cus) {
+  int64_t rows;
+  if (nseqs * longest == tokens) {  // all alike
+    const int64_t n = 2 * cus / (nseqs * walks);
+    if (n < 2) return kLinWhole;
+    rows = (longest + n - 1) / n;
+  } else {
+    rows = tokens * walks / (2 * cus);
+  }
+  rows = (rows + 63) / 64 * 64;
+  if (rows < kLinLeast) rows = kLinLeast;
+  return rows >= longest ? kLinWhole : (int)rows;
 }
 
 }  // namespace ss
