@@ -182,17 +182,31 @@ struct Parts {
 // dot product with (-1, 0) or (0, -1) onto v, exact as the remainder is (checked on the chip).
 // The constants come from registers, for as an inline operand -1 is one of fp32.
 struct Remainder {
-  bf16x2 low, high;
+  uint32_t low, high;
   __device__ __forceinline__ Remainder() {
-    uint32_t a, b;
-    asm("s_mov_b32 %0, 0xbf80" : "=s"(a));
-    asm("s_mov_b32 %0, 0xbf800000" : "=s"(b));
-    low = __builtin_bit_cast(bf16x2, a);
-    high = __builtin_bit_cast(bf16x2, b);
+    asm("s_mov_b32 %0, 0xbf80" : "=s"(low));
+    asm("s_mov_b32 %0, 0xbf800000" : "=s"(high));
   }
   __device__ __forceinline__ void take(uint32_t p, float& v0, float& v1) const {
-    v0 = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p), low, v0, false);
-    v1 = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p), high, v1, false);
+    v0 = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p), __builtin_bit_cast(bf16x2, low), v0, false);
+    v1 = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, p), __builtin_bit_cast(bf16x2, high), v1, false);
+  }
+  // The parts of eight values that outlive them, where the builtin overwrites its v: in assembly, with
+  // the three cycles that a dot product's result takes to other instructions at the end.  The
+  // values may be matrix results: the first parts, made before, have waited for them.
+  __device__ __forceinline__ void split8_of(const float (&v)[8], u32x4v& hi, u32x4v& lo) const {
+    float r[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) hi[k] = pack2<SS_BF16>(v[2 * k], v[2 * k + 1]);
+    asm("v_dot2_f32_bf16 %0, %8, %20, %12\n\tv_dot2_f32_bf16 %1, %8, %21, %13\n\t"
+        "v_dot2_f32_bf16 %2, %9, %20, %14\n\tv_dot2_f32_bf16 %3, %9, %21, %15\n\t"
+        "v_dot2_f32_bf16 %4, %10, %20, %16\n\tv_dot2_f32_bf16 %5, %10, %21, %17\n\t"
+        "v_dot2_f32_bf16 %6, %11, %20, %18\n\tv_dot2_f32_bf16 %7, %11, %21, %19\n\ts_nop 2"
+        : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5]), "=&v"(r[6]), "=&v"(r[7])
+        : "v"(hi[0]), "v"(hi[1]), "v"(hi[2]), "v"(hi[3]), "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(v[4]), "v"(v[5]),
+          "v"(v[6]), "v"(v[7]), "s"(low), "s"(high));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) lo[k] = pack2<SS_BF16>(r[2 * k], r[2 * k + 1]);
   }
   template <int N>
   __device__ __forceinline__ void split(float v0, float v1, uint32_t (&w)[N]) const {
@@ -394,8 +408,8 @@ __global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) 
   if constexpr (!STATE) {
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
-      const int n = wave + kWaves * i;
-      tile_t[i] = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : n < 10 ? 3 : 4;
+      const int n = wave + kWaves * i < 10 ? wave + kWaves * i : 9;  // two waves have the last tile too: the same values
+      tile_t[i] = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3;
       tile_s[i] = n - tile_t[i] * (tile_t[i] + 1) / 2;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -425,9 +439,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) 
     constexpr int turn = decltype(which)::value;
     const int rows = chunk_rows(t);
     const bool more = t + kC < q.rows;
-    if constexpr (!STATE) {
-      load_c(t, 0);
-    } else if (more) {
+    if (STATE && more) {
       load_b(t + kC, turn ^ 1);
       load_c(t + kC, turn ^ 1);
     }
@@ -436,24 +448,36 @@ __global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) 
     f32x4 out[OT][4];  // element r: o = 16 (OT wave + ot) + g4 + r, row 16 tt + l16
     if constexpr (!STATE) {
       // M[t][s] = a^{t-s} (a_t . b_s), a lane with 4 consecutive s of a row t
+      constexpr int KS = DC / 32;
+      u32x4v bs[kPairs][KS], as[kPairs][KS];
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
-        if (tile_t[i] > 3) continue;
-        const uint32_t bs = opaque(rows_dc) + at_b + turn * kTile + tile_s[i] * (16 * DC * 2);
-        const uint32_t as = opaque(rows_dc) + at_a + tile_t[i] * (16 * DC * 2);
-        f32x4 acc[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
+        const uint32_t b_at = opaque(rows_dc) + at_b + turn * kTile + tile_s[i] * (16 * DC * 2);
+        const uint32_t a_at = opaque(rows_dc) + at_a + tile_t[i] * (16 * DC * 2);
 #pragma unroll
-        for (int ks = 0; ks < DC / 32; ++ks)
-          acc[ks & 1] = mfma_t<IO>::run(as_vec<IO>(lds16(bs + 256 * ks)), as_vec<IO>(lds16(as + 256 * ks)), acc[ks & 1]);
-        acc[0] += acc[1];
+        for (int ks = 0; ks < KS; ++ks) {
+          bs[i][ks] = lds16(b_at + 256 * ks);
+          as[i][ks] = lds16(a_at + 256 * ks);
+        }
+      }
+      load_c(t, 0);
+      if (more) load_b(t + kC, turn ^ 1);
+      f32x4 pair[kPairs];
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) pair[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) pair[i] = mfma_t<IO>::run(as_vec<IO>(bs[i][ks]), as_vec<IO>(as[i][ks]), pair[i]);
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
         uint32_t m0[2], m1[2];
-        rem.split(acc[0][0] * mw[i][0], acc[0][1] * mw[i][1], m0);
-        rem.split(acc[0][2] * mw[i][2], acc[0][3] * mw[i][3], m1);
+        rem.split(pair[i][0] * mw[i][0], pair[i][1] * mw[i][1], m0);
+        rem.split(pair[i][2] * mw[i][2], pair[i][3] * mw[i][3], m1);
         const uint32_t at = (opaque(m_quad) ^ (uint32_t)(32 * (tile_s[i] % 2))) + at_m + tile_t[i] * (16 * kC * 2) + 256 * (tile_s[i] / 2);
         *lds_ptr<u32x2v>(at) = u32x2v{m0[0], m1[0]};
         *lds_ptr<u32x2v>(at + kPlane) = u32x2v{m0[1], m1[1]};
       }
-      if (more) load_b(t + kC, turn ^ 1);
       // E's part: the accumulators of H are the operand as they lie, its k axis being
       // c = 16 i + g4 + 0..3, then 16 (i + 2) + g4 + 0..3; a is read in that order
 #pragma unroll
@@ -484,18 +508,22 @@ __global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) 
             as[tt] = u32x4v{a0[0], a0[1], a1[0], a1[1]};
           }
 #pragma unroll
-          for (int ot = 0; ot < OT; ++ot)
+          for (int ot = 0; ot < OT; ++ot) {
+            float v[8];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int e = 0; e < 8; ++e) v[e] = kTwo ? H[i0 + e / 4 * 2][ot][e % 4] * sc.to : H[i0 + e / 4 * 2][ot][e % 4];
+            if constexpr (kTwo) {
 #pragma unroll
-              for (int r = 0; r < 4; r += 2) {
-                const float v0 = H[i0 + 2 * i][ot][r], v1 = H[i0 + 2 * i][ot][r + 1];
-                uint32_t v[2];
-                if constexpr (kTwo) split2_f16(v0 * sc.to, v1 * sc.to, v[0], v[1]);
-                else rem.split(v0, v1, v);
-                eh[ot][2 * i + r / 2] = v[0];
-                el[ot][2 * i + r / 2] = v[1];
+              for (int k = 0; k < 4; ++k) {
+                uint32_t hi, lo;
+                split2_f16(v[2 * k], v[2 * k + 1], hi, lo);
+                eh[ot][k] = hi;
+                el[ot][k] = lo;
               }
+            } else {
+              rem.split8_of(v, eh[ot], el[ot]);
+            }
+          }
 #pragma unroll
           for (int ot = 0; ot < OT; ++ot)
 #pragma unroll

@@ -40,9 +40,10 @@ inline int pass_ahead(int64_t workgroups, int64_t chunks, int64_t nseqs, int64_t
 // Rows of the segments in which linear attention walks its sequences (the longest
 // of `longest` rows, all of them of `tokens`; `walks` of each), a multiple of 64, or
 // kLinWhole where none is split: as many segments as give every CU two workgroups at
-// once, none of less than kLinLeast rows.
-constexpr int kLinWhole = 1 << 30, kLinLeast = 512;
+// once, none of less than kLinLeast rows, and no sequence of no more than twice these.
+constexpr int kLinWhole = 1 << 30, kLinLeast = 128;
 inline int lin_segment(int64_t tokens, int64_t nseqs, int64_t longest, int64_t walks, int64_t cus) {
+  if (longest <= 2 * kLinLeast) return kLinWhole;
   int64_t rows;
   if (nseqs * longest == tokens) {  // all alike
     const int64_t n = 2 * cus / (nseqs * walks);
