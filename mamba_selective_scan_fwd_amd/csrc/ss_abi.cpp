@@ -1140,20 +1140,28 @@ ss_status check_norm(const ss_norm_problem* p) {
   if (p->x_stride < p->channels || p->x_stride > kMaxStride) return SS_ERR_BAD_SHAPE;
   return SS_OK;
 }
-// workgroups over the rows: enough to fill the GPU; the backward's each leave sums behind
+// Threads and workgroups.  A workgroup takes whole rows' groups where 1024 threads hold
+// them.  Forward: 256 threads or more, as many workgroups as the GPU holds at once.
+// Backward: up to 1024 threads, for a workgroup's rows end in one sum of dw and db, and
+// one workgroup a CU (two of at most 512 threads).
+constexpr int64_t kNormBwdGroups = 512;
 void norm_layout(const ss_norm_problem* p, int vec, bool bwd, ss::NormParams* k) {
   const int size = (int)(p->channels / p->ngroups), nvec = size / vec;
   int lanes = 1;
-  while (lanes < nvec && lanes < 1024) lanes *= 2;
-  const int slots = lanes >= 256 ? 1 : 256 / lanes;
+  while (lanes < nvec && lanes < 64) lanes *= 2;
+  if (nvec > 64) lanes = nvec < 1024 ? (nvec + 63) / 64 * 64 : 1024;
+  const int slots = 1024 / lanes, want = (bwd ? 1024 : 256) / lanes;
   k->io = p->io_dtype; k->mode = p->mode; k->center = p->center != 0; k->eps = p->eps;
   k->rows = p->rows; k->groups = (int)p->ngroups; k->size = size; k->vec = vec; k->lanes = lanes;
   k->block_groups = p->ngroups < slots ? (int)p->ngroups : slots;
-  k->row_lanes = slots / k->block_groups;
+  k->row_lanes = want > k->block_groups ? want / k->block_groups : 1;
+  if (p->rows < k->row_lanes) k->row_lanes = (int)p->rows;
+  k->threads = (k->row_lanes * k->block_groups * lanes + 63) / 64 * 64;
   k->blocks = (int)((p->ngroups + k->block_groups - 1) / k->block_groups);
-  const int64_t most = bwd ? 1024 : 4096, rows = (p->rows + k->row_lanes - 1) / k->row_lanes;
-  const int64_t want = most / k->blocks > 0 ? most / k->blocks : 1;
-  k->row_blocks = (int)(rows < want ? rows : want);
+  const int64_t cus = 256, groups = bwd ? (k->threads <= 512 ? 2 * cus : cus) : cus * 2048 / k->threads;
+  const int64_t rows = (p->rows + k->row_lanes - 1) / k->row_lanes;
+  const int64_t most = groups / k->blocks > 0 ? groups / k->blocks : 1;
+  k->row_blocks = (int)(rows < most ? rows : most);
 }
 // the widest vector that sizes allow: the workspace is by sizes alone
 int norm_vec(const ss_norm_problem* p, bool aligned_rows) {
@@ -1166,7 +1174,7 @@ int norm_vec(const ss_norm_problem* p, bool aligned_rows) {
 
 size_t ss_group_norm_bwd_workspace_size(const ss_norm_problem* p) {
   if (check_norm(p) != SS_OK) return 0;
-  return (size_t)(p->rows < 1024 ? p->rows : 1024) * (size_t)p->channels * 8;
+  return (size_t)(p->rows < kNormBwdGroups ? p->rows : kNormBwdGroups) * (size_t)p->channels * 8;
 }
 
 ss_status ss_group_norm(const ss_norm_problem* p, const void* x, const float* weight, const float* bias, const void* z,

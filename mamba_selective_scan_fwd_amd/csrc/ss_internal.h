@@ -341,7 +341,7 @@ struct LinStepParams {
   int32_t rows, nslots, heads, share, dk, dv;
 };
 
-// A workgroup: block_groups groups of row_lanes rows, `lanes` threads a group.
+// A workgroup: block_groups groups of row_lanes rows, `lanes` threads a group (a power of two up to 64, or whole waves).
 struct NormParams {
   int32_t io;
   int32_t mode;              // ss_norm_mode
@@ -353,7 +353,7 @@ struct NormParams {
   float* ws;                 // (row_blocks, 2, groups * size): sums of dw and db
   int64_t x_stride, z_stride, dy_stride, y_stride, rows;
   float eps;
-  int32_t groups, size, vec, lanes, block_groups, row_lanes;
+  int32_t groups, size, vec, lanes, block_groups, row_lanes, threads;
   int32_t blocks, row_blocks;  // workgroups over the groups and over the rows
 };
 
