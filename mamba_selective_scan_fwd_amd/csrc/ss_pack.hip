@@ -51,13 +51,150 @@ __device__ __forceinline__ void block_sums(Counts own, Counts* waves, Counts& be
   __syncthreads();
   before = {run.steps - own.steps, run.prompts - own.prompts, run.rows - own.rows};
   all = {0, 0, 0};
+#pragma unroll 2
   for (int k = 0; k < kScanThreads / 64; ++k) {
     if (k < wave) before = before + waves[k];
     all = all + waves[k];
   }
 }
 
-// One workgroup: what goes by request and by sequence
+// ---- up to 4096 requests: one launch --------------------------------------------------------
+// Every workgroup takes the sums over all requests, ITEMS a thread, and lists in LDS the
+// requests that have rows, in the rows' order.  It writes what goes by request for its
+// share of the waves and by row for its rows, whose requests it finds in the list by
+// bisection.  Reading all requests in each workgroup (48 KiB at most, from L2) costs less
+// than a second launch that waits for the first.
+struct Sums {
+  uint32_t number;  // of steps, and of prompts * 2^16
+  uint32_t rows;    // of prompts, up to 2^31 - 1
+};
+__device__ __forceinline__ Sums operator+(Sums a, Sums b) {
+  const uint32_t r = a.rows + b.rows;
+  return {a.number + b.number, r < 0x7fffffffu ? r : 0x7fffffffu};
+}
+template <int THREADS, int ITEMS>
+__global__ void __launch_bounds__(THREADS) pack_kernel(PackParams p) {
+  constexpr int kMost = THREADS * ITEMS;
+  __shared__ Sums waves[THREADS / 64];
+  __shared__ int32_t start[kMost], who[kMost];
+  __shared__ uint32_t base[kMost];
+  __shared__ int32_t last;
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  int32_t n[ITEMS], slot[ITEMS], seen[ITEMS];
+  if (ITEMS == 4 && 4 * tid + 3 < p.requests) {
+    typedef int32_t int4_t __attribute__((ext_vector_type(4)));
+    const int4_t a = reinterpret_cast<const int4_t*>(p.new_tokens)[tid], b = reinterpret_cast<const int4_t*>(p.slots)[tid],
+                 c = reinterpret_cast<const int4_t*>(p.seen)[tid];
+#pragma unroll
+    for (int e = 0; e < ITEMS; ++e) {
+      n[e] = a[e % 4];
+      slot[e] = b[e % 4];
+      seen[e] = c[e % 4];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < ITEMS; ++e) {
+      const int i = ITEMS * tid + e;
+      const bool in = i < p.requests;
+      n[e] = in ? p.new_tokens[i] : 0;
+      slot[e] = in ? p.slots[i] : -1;
+      seen[e] = in ? p.seen[i] : 0;
+    }
+  }
+  Sums own{0, 0};
+#pragma unroll
+  for (int e = 0; e < ITEMS; ++e) {
+    if (slot[e] < 0 || n[e] < 0) n[e] = 0;
+    const bool step = n[e] == 1 && seen[e] > 0;
+    own = own + Sums{step ? 1u : n[e] > 0 ? 0x10000u : 0u, step ? 0u : (uint32_t)n[e]};
+  }
+  // sums over the lanes before this one; saturating sums are not taken apart again, so the
+  // scan leaves this lane's own out
+  Sums run = own;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const Sums o = {(uint32_t)__shfl_up((int)run.number, off, 64), (uint32_t)__shfl_up((int)run.rows, off, 64)};
+    if (lane >= off) run = run + o;
+  }
+  if (lane == 63) waves[wave] = run;
+  if (tid == 0) last = 0;
+  Sums before = {(uint32_t)__shfl_up((int)run.number, 1, 64), (uint32_t)__shfl_up((int)run.rows, 1, 64)};
+  if (lane == 0) before = {0, 0};
+  __syncthreads();
+  Sums all{0, 0};
+  {
+    Sums front{0, 0};
+#pragma unroll
+    for (int k = 0; k < THREADS / 64; ++k) {
+      if (k == wave) front = all;
+      all = all + waves[k];
+    }
+    before = front + before;
+  }
+  const uint32_t most = (uint32_t)p.tokens, steps = all.number & 0xffffu;
+  const uint32_t listed_steps = steps < most ? steps : most;
+  const int32_t end = (int32_t)(steps + all.rows < most ? steps + all.rows : most);
+  const bool write = (uint32_t)wave % gridDim.x == blockIdx.x;
+  int32_t listed = 0;
+#pragma unroll
+  for (int e = 0; e < ITEMS; ++e) {
+    const int i = ITEMS * tid + e;
+    const bool step = n[e] == 1 && seen[e] > 0;
+    const uint32_t nstep = before.number & 0xffffu, nprompt = before.number >> 16;
+    const uint32_t at = step ? nstep : steps + before.rows;
+    const uint32_t left = at < most ? most - at : 0u, taken = (uint32_t)n[e] < left ? (uint32_t)n[e] : left;
+    if (taken) {
+      const uint32_t k = step ? nstep : steps + nprompt;
+      start[k] = (int32_t)at;
+      who[k] = i;
+      base[k] = (uint32_t)(seen[e] > 0 ? seen[e] : 0) - at;
+      if (!step) listed = (int32_t)nprompt + 1;
+    }
+    if (write && i < p.requests) {
+      p.rows[i] = taken ? (int32_t)at : -1;
+      p.taken[i] = (int32_t)taken;
+      if (taken && step) p.step_slots[nstep] = slot[e];
+      if (taken && !step) {
+        p.cu[nprompt] = (int32_t)at;
+        p.prompt_slots[nprompt] = slot[e];
+        p.has_state[nprompt] = seen[e] > 0;
+      }
+    }
+    before = before + Sums{step ? 1u : n[e] > 0 ? 0x10000u : 0u, step ? 0u : (uint32_t)n[e]};
+  }
+  if (listed) atomicMax(&last, listed);
+  __syncthreads();
+  listed = last;
+  const int first = (int)blockIdx.x * THREADS + tid, stride = (int)gridDim.x * THREADS;
+  for (int i = first; i <= p.requests; i += stride) {
+    if (i >= listed) p.cu[i] = end;
+    if (i >= p.requests) continue;
+    if (i >= (int)listed_steps) p.step_slots[i] = -1;
+    if (i >= listed) {
+      p.prompt_slots[i] = -1;
+      p.has_state[i] = 0;
+    }
+  }
+  int top = 1;
+  while (2 * top < listed) top *= 2;
+  for (int64_t k = first; k < p.tokens; k += stride) {
+    int32_t request = -1, position = -1;
+    if (k < end) {
+      int at = (int)k;
+      if (k >= listed_steps) {
+        at = (int)steps;  // the last prompt that starts at this row or before it
+        for (int b = top; b; b /= 2)
+          if (at + b < (int)steps + listed && start[at + b] <= k) at += b;
+      }
+      request = who[at];
+      position = (int32_t)(base[at] + (uint32_t)k);
+    }
+    p.row_request[k] = request;
+    p.row_position[k] = position;
+  }
+}
+
+// ---- more requests: what goes by request and by sequence in one workgroup, then what goes by row ----
 __global__ void __launch_bounds__(kScanThreads) pack_requests_kernel(PackParams p) {
   __shared__ Counts waves[kScanThreads / 64];
   const int tid = threadIdx.x;
@@ -144,6 +281,14 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(PackParams p) {
 }  // namespace
 
 hipError_t launch_pack(const PackParams& p, hipStream_t st) {
+  if (p.requests <= 4096) {
+    const int threads = p.requests <= 256 ? 256 : 1024;
+    const int64_t rows = ((int64_t)p.tokens + threads - 1) / threads;
+    const dim3 grid((uint32_t)(rows < 256 ? rows : 256));
+    if (threads == 256) hipLaunchKernelGGL((pack_kernel<256, 1>), grid, dim3(256), 0, st, p);
+    else hipLaunchKernelGGL((pack_kernel<1024, 4>), grid, dim3(1024), 0, st, p);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(pack_requests_kernel, dim3(1), dim3(kScanThreads), 0, st, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

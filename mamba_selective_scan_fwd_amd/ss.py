@@ -1130,15 +1130,19 @@ def pack_requests(new_tokens, slots, seen, tokens):
     R = new_tokens.numel()
     at = [_in(t, i32, name, (R,), dev, keep)
           for t, name in ((new_tokens, "new_tokens"), (slots, "slots"), (seen, "seen"))]
-    # every output on a 16-byte boundary of one allocation
-    sizes = dict(rows=R, taken=R, step_slots=R, cu_seqlens=R + 1, prompt_slots=R, has_state=R, row_request=tokens,
-                 row_position=tokens)
-    buf = new_tokens.new_empty(sum((n + 3) // 4 * 4 for n in sizes.values()))
-    out, base = {}, 0
-    for name, n in sizes.items():
-        out[name] = buf[base:base + n]
-        base += (n + 3) // 4 * 4
-    _launch(dev, lib.ss_pack_requests, R, tokens, *at, *(t.data_ptr() for t in out.values()))
+    # one allocation, every output on a 16-byte boundary
+    r, t = R + 3 & -4, tokens + 3 & -4
+    parts = [r, r, r, r, r, t, t, R + 1]
+    buf = new_tokens.new_empty(5 * r + 2 * t + R + 1)
+    out = dict(zip(("rows", "taken", "step_slots", "prompt_slots", "has_state", "row_request", "row_position", "cu_seqlens"),
+                   buf.split_with_sizes(parts)))
+    to = buf.data_ptr()
+    _launch(dev, lib.ss_pack_requests, R, tokens, *at, to, to + 4 * r, to + 8 * r, to + 20 * r + 8 * t, to + 12 * r,
+            to + 16 * r, to + 20 * r, to + 20 * r + 4 * t)
+    if r != R or t != tokens:
+        for name in out:
+            if name != "cu_seqlens":
+                out[name] = out[name][:tokens if name[:4] == "row_" else R]
     return out
 
 

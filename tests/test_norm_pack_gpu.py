@@ -166,7 +166,7 @@ def _pack(new, slots, seen, tokens):
         assert np.array_equal(got[k].cpu().numpy(), v), k
 
 
-@pytest.mark.parametrize("n", [1, 2, 63, 64, 65, 1000, 1024, 1025, 2500, 9000])
+@pytest.mark.parametrize("n", [1, 2, 63, 64, 65, 255, 256, 257, 1000, 1024, 1025, 2500, 4095, 4096, 4097, 9000])
 def test_pack(n):
     r = np.random.default_rng(n)
     new = np.where(r.random(n) < 0.6, 1, r.integers(0, 40, n))
