@@ -315,7 +315,6 @@ struct LinParams {
   int32_t io;
   LinWalk job[3];
   int32_t jobs;              // walks
-  int32_t job0, njobs;       // those of a launch
   const float* log_decay;    // (heads)
   const int32_t* cu;         // (nseqs + 1) or null: sequences of tokens / nseqs rows
   const int32_t* slots;      // with pool: (nseqs) or null, sequence s has slot s

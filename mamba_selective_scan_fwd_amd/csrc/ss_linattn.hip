@@ -305,16 +305,13 @@ struct TileLoad {
 };
 
 template <int IO, int DC, int DO, bool STATE, bool FULL>
-__global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) {
+__device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>& lds, int job, int h, int place) {
   constexpr int CT = DC / 16, OT = DO / 64;  // tiles of a wave's state: all of c, a quarter of o
   constexpr int kPairs = 3;                  // 16 x 16 tiles of pairs a wave, at the most
   constexpr bool kTwo = IO == SS_F16;
   constexpr int kPlane = kC * kC * 2, kTile = kC * DC * 2;
-  __shared__ WalkLds<DC, DO, STATE> lds;
   const int tid = threadIdx.x, wave = uniform(tid / 64);
   const int lane = tid % 64, l16 = lane % 16, g4 = 4 * (lane / 16);
-  const int lb = (int)xcd_logical_block();
-  const int job = p.job0 + lb % p.njobs, h = lb / p.njobs % p.heads, place = lb / p.njobs / p.heads;
   const LinWalk& w = p.job[job];
   const LinRows q = lin_rows(p, place);
   const int kvh = h / p.share;
@@ -735,6 +732,26 @@ __global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) 
   }
 }
 
+// Workgroup = (segment, head, walk)
+template <int IO, int DC, int DO, bool STATE, bool FULL>
+__global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) {
+  __shared__ WalkLds<DC, DO, STATE> lds;
+  const int lb = (int)xcd_logical_block();
+  walk<IO, DC, DO, STATE, FULL>(p, lds, lb % p.jobs, lb / p.jobs % p.heads, lb / p.jobs / p.heads);
+}
+// The gradients' three walks where dv = DC and dk = DO differ: dq's and dk's have the states' sides
+// the one way, dv's the other; in one launch they run beside each other
+template <int IO, int DC, int DO, bool STATE, bool FULL>
+__global__ void __launch_bounds__(kWalkThreads, 2) lin_walks_kernel(LinParams p) {
+  __shared__ union {
+    WalkLds<DC, DO, STATE> two;
+    WalkLds<DO, DC, STATE> one;
+  } lds;
+  const int lb = (int)xcd_logical_block(), job = lb % 3, h = lb / 3 % p.heads, place = lb / 3 / p.heads;
+  if (job < 2) walk<IO, DC, DO, STATE, false>(p, lds.two, job, h, place);
+  else walk<IO, DO, DC, STATE, FULL>(p, lds.one, job, h, place);
+}
+
 // ---- the states between the segments of a sequence ----------------------------------
 // Workgroup = (sequence of several segments, head, walk, 1024 elements): E <- the
 // sequence's first state; per segment, S <- E in the workspace and E <- decay E + S,
@@ -792,16 +809,22 @@ __global__ void __launch_bounds__(256) lin_pass_kernel(LinParams p) {
   }
 }
 
-// ---- gradients of a shared key or value: the sum over the heads that share it ---------
-// A thread has 4 channels of a row; parts in fp32, (tokens, heads, d).
+// ---- gradients of shared keys and values: the sums over the heads that share them -----
+// A thread has 4 channels of a row of one of them; parts in fp32, (tokens, heads, d).
 template <int IO>
-__global__ void __launch_bounds__(256) lin_share_kernel(const float* part, void* out, int64_t quads, int share, int d4) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= quads) return;
-  const f32x4* at = reinterpret_cast<const f32x4*>(part) + i / d4 * d4 * share + i % d4;
+__global__ void __launch_bounds__(256) lin_share_kernel(LinParams p) {
+  int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t rows = (int64_t)p.tokens * (p.heads / p.share);
+  const int dk4 = p.job[1].dout / 4, dv4 = p.job[2].dout / 4;
+  const bool second = i >= rows * dk4;
+  if (second) i -= rows * dk4;
+  const int d4 = second ? dv4 : dk4;
+  if (i >= rows * d4) return;
+  const LinWalk& w = p.job[second ? 2 : 1];
+  const f32x4* at = static_cast<const f32x4*>(w.out) + i / d4 * d4 * p.share + i % d4;
   f32x4 sum = at[0];
-  for (int k = 1; k < share; ++k) sum += at[(int64_t)k * d4];
-  reinterpret_cast<uint2*>(out)[i] = make_uint2(pack2<IO>(sum[0], sum[1]), pack2<IO>(sum[2], sum[3]));
+  for (int k = 1; k < p.share; ++k) sum += at[(int64_t)k * d4];
+  static_cast<uint2*>(w.sum)[i] = make_uint2(pack2<IO>(sum[0], sum[1]), pack2<IO>(sum[2], sum[3]));
 }
 
 // ---- one token of many requests -----------------------------------------------------
@@ -855,9 +878,16 @@ __global__ void __launch_bounds__(256) lin_step_kernel(LinStepParams p) {
 
 template <int IO, int DC, int DO, bool FULL>
 hipError_t launch_walk(const LinParams& p, hipStream_t st) {
-  const dim3 grid((uint32_t)(p.places * p.heads * p.njobs));
-  if (p.split) hipLaunchKernelGGL((lin_walk_kernel<IO, DC, DO, true, FULL>), grid, dim3(kWalkThreads), 0, st, p);
-  else hipLaunchKernelGGL((lin_walk_kernel<IO, DC, DO, false, FULL>), grid, dim3(kWalkThreads), 0, st, p);
+  const dim3 grid((uint32_t)(p.places * p.heads * p.jobs)), threads(kWalkThreads);
+  if constexpr (DC != DO) {
+    if (p.jobs == 3) {
+      if (p.split) hipLaunchKernelGGL((lin_walks_kernel<IO, DC, DO, true, FULL>), grid, threads, 0, st, p);
+      else hipLaunchKernelGGL((lin_walks_kernel<IO, DC, DO, false, FULL>), grid, threads, 0, st, p);
+      return hipGetLastError();
+    }
+  }
+  if (p.split) hipLaunchKernelGGL((lin_walk_kernel<IO, DC, DO, true, FULL>), grid, threads, 0, st, p);
+  else hipLaunchKernelGGL((lin_walk_kernel<IO, DC, DO, false, FULL>), grid, threads, 0, st, p);
   return hipGetLastError();
 }
 // fp16's weighted rows are two parts (split2_f16).  Of bf16's, three keep fp32's error in the last states;
@@ -872,19 +902,10 @@ hipError_t launch_walk(const LinParams& p, hipStream_t st) {
   return launch_walk<IO, DC, DO, false>(p, st);
 }
 template <int IO>
-hipError_t launch_walks_io(LinParams p, hipStream_t st) {
-  // walks of the same sides share a launch
-  for (int j = 0; j < p.jobs; j += p.njobs) {
-    p.job0 = j;
-    p.njobs = 1;
-    while (j + p.njobs < p.jobs && p.job[j + p.njobs].dc == p.job[j].dc && p.job[j + p.njobs].dout == p.job[j].dout)
-      ++p.njobs;
-    const int dc = p.job[j].dc, dout = p.job[j].dout;
-    const hipError_t e = dc == 64 ? (dout == 64 ? launch_walk<IO, 64, 64>(p, st) : launch_walk<IO, 64, 128>(p, st))
-                                  : (dout == 64 ? launch_walk<IO, 128, 64>(p, st) : launch_walk<IO, 128, 128>(p, st));
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+hipError_t launch_walks_io(const LinParams& p, hipStream_t st) {
+  const int dc = p.job[0].dc, dout = p.job[0].dout;
+  return dc == 64 ? (dout == 64 ? launch_walk<IO, 64, 64>(p, st) : launch_walk<IO, 64, 128>(p, st))
+                  : (dout == 64 ? launch_walk<IO, 128, 64>(p, st) : launch_walk<IO, 128, 128>(p, st));
 }
 template <int IO>
 hipError_t launch_linattn_io(LinParams p, hipStream_t st) {
@@ -898,16 +919,10 @@ hipError_t launch_linattn_io(LinParams p, hipStream_t st) {
     p.split = 0;
   }
   const hipError_t e = launch_walks_io<IO>(p, st);
-  if (e != hipSuccess) return e;
-  for (int j = 0; j < p.jobs; ++j)
-    if (p.job[j].sum) {
-      const int64_t quads = (int64_t)p.tokens * (p.heads / p.share) * p.job[j].dout / 4;
-      hipLaunchKernelGGL((lin_share_kernel<IO>), dim3((uint32_t)((quads + 255) / 256)), dim3(256), 0, st,
-                         static_cast<const float*>(p.job[j].out), p.job[j].sum, quads, p.share, p.job[j].dout / 4);
-      const hipError_t f = hipGetLastError();
-      if (f != hipSuccess) return f;
-    }
-  return hipSuccess;
+  if (e != hipSuccess || p.jobs < 3 || !p.job[1].sum) return e;
+  const int64_t quads = (int64_t)p.tokens * (p.heads / p.share) * ((p.job[1].dout + p.job[2].dout) / 4);
+  hipLaunchKernelGGL((lin_share_kernel<IO>), dim3((uint32_t)((quads + 255) / 256)), dim3(256), 0, st, p);
+  return hipGetLastError();
 }
 
 template <int IO, int DK>
