@@ -891,8 +891,8 @@ hipError_t launch_walk(const LinParams& p, hipStream_t st) {
   return hipGetLastError();
 }
 // fp16's weighted rows are two parts (split2_f16).  Of bf16's, three keep fp32's error in the last states;
-// where no walk has any, its outputs are all that shows and two do (a training layer's
-// gradients: PARTS2 us against PARTS3).
+// where no walk has any, its outputs are all that shows and two do (8 rows of 2048 tokens, 12 heads of
+// 128 x 128: 81 us against 90 with three, the gradients 172 against 194).
 template <int IO, int DC, int DO>
 hipError_t launch_walk(const LinParams& p, hipStream_t st) {
   bool full = false;
