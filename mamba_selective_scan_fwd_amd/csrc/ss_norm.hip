@@ -147,13 +147,13 @@ __device__ __forceinline__ void statistics(const NormParams& p, const float (&u)
   rstd = rsqrtf(fmaf(s[0], inv, p.eps));
 }
 
-template <int IO, int VEC, int THREADS>
-__global__ void __launch_bounds__(THREADS) group_norm_kernel(NormParams p) {
+template <int IO, int VEC, int MODE>
+__global__ void __launch_bounds__(1024) group_norm_kernel(NormParams p) {
   using V = Vec<IO, VEC>;
   __shared__ float waves[4 * kMaxWaves];
   const NormPlace q = norm_place(p);
   const bool mine = q.in && q.lane < p.size / VEC;
-  const bool first = p.mode == SS_NORM_GATE_FIRST, behind = p.mode == SS_NORM_GATE;
+  constexpr bool first = MODE == SS_NORM_GATE_FIRST, behind = MODE == SS_NORM_GATE;
   int turn = 0;
   float w[VEC], b[VEC];
   if (mine) {
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(THREADS) group_norm_kernel(NormParams p) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const float o = fmaf((u[e] - mean) * rstd, w[e], b[e]);
-      y[e] = behind ? o * silu_f(V::get(zw, e)) : p.mode == SS_NORM_SILU ? silu_f(o) : o;
+      y[e] = behind ? o * silu_f(V::get(zw, e)) : MODE == SS_NORM_SILU ? silu_f(o) : o;
     }
     V::store(p.y, r * p.y_stride + q.c, y);
   }
@@ -199,14 +199,14 @@ __device__ __forceinline__ float outer_grad(int mode, float dy, float zs, float 
 
 // Every workgroup leaves its sums of dw and db, over the rows it walks, in the workspace:
 // (row block, 2, channels).
-template <int IO, int VEC, int THREADS>
-__global__ void __launch_bounds__(THREADS) group_norm_bwd_kernel(NormParams p) {
+template <int IO, int VEC, int MODE>
+__global__ void __launch_bounds__(1024) group_norm_bwd_kernel(NormParams p) {
   using V = Vec<IO, VEC>;
   __shared__ float waves[4 * kMaxWaves];
   extern __shared__ float sums[];  // (row lanes, groups of the block, vectors) of dw, then db
   const NormPlace q = norm_place(p);
   const bool mine = q.in && q.lane < p.size / VEC;
-  const bool first = p.mode == SS_NORM_GATE_FIRST, gated = first || p.mode == SS_NORM_GATE;
+  constexpr bool first = MODE == SS_NORM_GATE_FIRST, gated = first || MODE == SS_NORM_GATE;
   const int channels = p.groups * p.size, rb = (int)(blockIdx.x / (uint32_t)p.blocks);
   const float inv = 1.0f / (float)p.size;
   int turn = 0;
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(THREADS) group_norm_bwd_kernel(NormParams p) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const float n = (u[e] - mean) * rstd, o = fmaf(n, w[e], b[e]);
-      const float d = in ? outer_grad(p.mode, V::get(gw, e), gated ? silu_f(V::get(zw, e)) : 0.0f, o) : 0.0f;
+      const float d = in ? outer_grad(MODE, V::get(gw, e), gated ? silu_f(V::get(zw, e)) : 0.0f, o) : 0.0f;
       dw[e] = in ? fmaf(d, n, dw[e]) : dw[e];
       db[e] += d;
       u[e] = n;
@@ -397,18 +397,22 @@ __global__ void __launch_bounds__(1024) group_norm_sum_kernel(NormParams p) {
   }
 }
 
+template <int IO, int VEC, int MODE>
+hipError_t launch_norm_mode(const NormParams& p, hipStream_t st) {
+  const dim3 grid((uint32_t)((int64_t)p.blocks * p.row_blocks)), threads((uint32_t)p.threads);
+  const uint32_t lds = (uint32_t)(p.row_lanes * p.block_groups * p.lanes * VEC * 4);
+  if (!p.dy) hipLaunchKernelGGL((group_norm_kernel<IO, VEC, MODE>), grid, threads, 0, st, p);
+  else hipLaunchKernelGGL((group_norm_bwd_kernel<IO, VEC, MODE>), grid, threads, lds, st, p);
+  return hipGetLastError();
+}
 template <int IO, int VEC>
 hipError_t launch_norm_vec(const NormParams& p, hipStream_t st) {
-  const dim3 grid((uint32_t)((int64_t)p.blocks * p.row_blocks)), threads((uint32_t)p.threads);
-  if (!p.dy) {
-    if (p.threads <= 256) hipLaunchKernelGGL((group_norm_kernel<IO, VEC, 256>), grid, threads, 0, st, p);
-    else hipLaunchKernelGGL((group_norm_kernel<IO, VEC, 1024>), grid, threads, 0, st, p);
-    return hipGetLastError();
+  switch (p.mode) {
+    case SS_NORM_SILU: return launch_norm_mode<IO, VEC, SS_NORM_SILU>(p, st);
+    case SS_NORM_GATE: return launch_norm_mode<IO, VEC, SS_NORM_GATE>(p, st);
+    case SS_NORM_GATE_FIRST: return launch_norm_mode<IO, VEC, SS_NORM_GATE_FIRST>(p, st);
+    default: return launch_norm_mode<IO, VEC, SS_NORM_PLAIN>(p, st);
   }
-  const uint32_t lds = (uint32_t)(p.row_lanes * p.block_groups * p.lanes * VEC * 4);
-  if (p.threads <= 512) hipLaunchKernelGGL((group_norm_bwd_kernel<IO, VEC, 512>), grid, threads, lds, st, p);
-  else hipLaunchKernelGGL((group_norm_bwd_kernel<IO, VEC, 1024>), grid, threads, lds, st, p);
-  return hipGetLastError();
 }
 template <int IO>
 hipError_t launch_norm_io(const NormParams& p, hipStream_t st) {
