@@ -10,11 +10,16 @@
 // All in fp32; the variance is taken about the mean, in a second sum over
 // registers, so that a mean far from zero costs no bits.
 //
-// Bound by HBM.  A group has `lanes` threads, each with one vector of its channels in
-// registers, so that a row's data are read once, the next row's while this one is worked
-// on.  A thread keeps its channels, and their w and b, over all the rows that its
-// workgroup walks, which is what dw and db are summed over.  Groups of more than 1024
-// vectors are walked by 1024 threads that read the row once for every sum.
+// Bound by HBM: 16384 rows of 1536 in bf16, 12 groups, the gate behind, take 26 us forward
+// (151 MB) and 54 + 5 us for the gradients (252 MB, 4.7 TB/s); 64 such rows 3.6 us, the
+// latency of one load, two sums and a store.  A group has `lanes` threads, each with one
+// vector of its channels in registers, so that a row's data are read once, the next
+// row's while this one is worked on.  A thread keeps its channels, and their w and b,
+// over all the rows that its workgroup walks, which is what dw and db are summed over.
+// A kernel for each mode: with the mode as an argument the gradients' kernel branched
+// for each element and took 62 us, for it issues as long as it loads.  Groups of more
+// than 1024 vectors are walked by 1024 threads, element by element, that read the row
+// once for every sum.
 #include <type_traits>
 
 #include "ss_device.h"
@@ -371,7 +376,8 @@ __global__ void __launch_bounds__(1024) group_norm_big_bwd_kernel(NormParams p) 
   }
 }
 
-// dw and db from the workgroups' sums: 32 channels of 32 row lanes a workgroup
+// dw and db from the workgroups' sums: 32 channels of 32 row lanes a workgroup, each with 4
+// loads at a time (256 sums of 1536 channels: 4.7 us; 1024 sums, one load at a time: 21)
 __global__ void __launch_bounds__(1024) group_norm_sum_kernel(NormParams p) {
   __shared__ float sums[32][33];
   const int channels = p.groups * p.size, k = (int)threadIdx.x % 32, c = (int)blockIdx.x * 32 + k, l = (int)threadIdx.x / 32;

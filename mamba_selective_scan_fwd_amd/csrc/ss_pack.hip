@@ -63,7 +63,10 @@ __device__ __forceinline__ void block_sums(Counts own, Counts* waves, Counts& be
 // requests that have rows, in the rows' order.  It writes what goes by request for its
 // share of the waves and by row for its rows, whose requests it finds in the list by
 // bisection.  Reading all requests in each workgroup (48 KiB at most, from L2) costs less
-// than a second launch that waits for the first.
+// than a second launch that waits for the first: 64 requests and 2048 rows 3.9 us against
+// 14.4 + 2.8, 4001 and 65536 rows 6.8 against 30 + 5.3.  Bound by latency: a load, two
+// barriers, the bisection's reads of LDS.  4096 requests fill 4 a thread and 48 KiB of
+// LDS, which two workgroups have room for on a CU.
 struct Sums {
   uint32_t number;  // of steps, and of prompts * 2^16
   uint32_t rows;    // of prompts, up to 2^31 - 1

@@ -96,6 +96,15 @@ def test_linattn_workspace_and_overlaps():
     assert _calls(p, y=G)[3] == 5 and _calls(p, state=6 * G)[3] == 5
 
 
+@pytest.mark.parametrize("nseqs,length,segments", [(1, 384, 0), (1, 385, 4), (1, 5000, 40), (4, 4096, 32), (1, 1 << 20, 128),
+                                                   (64, 4096, 2), (65, 4096, 0)])
+def test_linattn_segments(nseqs, length, segments):
+    """Short sequences, and so many that they fill the GPU, are walked whole; else in segments of 128 rows or more, two
+    workgroups of the 4 heads to a CU: a state of every head each."""
+    p = _lin(packed=0, tokens=nseqs * length, nseqs=nseqs)
+    assert ss.load_library().ss_linattn_workspace_size(R(p)) == nseqs * segments * 4 * 64 * 128 * 4
+
+
 def _norm(**kw):
     d = dict(rows=10, channels=48, ngroups=4, x_stride=96, z_stride=96, y_stride=48, dy_stride=48, eps=1e-5, io_dtype=2, mode=2,
              center=1)
