@@ -11,8 +11,10 @@
  * kernels on `stream` (a hipStream_t, NULL = the null stream) and returns
  * without synchronising.  A failed launch returns SS_ERR_HIP.  Beside the
  * scan (forward, decode step, backward) it exports the depthwise causal
- * conv1d + SiLU that feeds the scan, and the Mamba-2 SSD chunked scan on the
- * matrix cores, each declared below with its own layouts.
+ * conv1d + SiLU that feeds the scan, the Mamba-2 SSD chunked scan on the
+ * matrix cores, linear attention with a decay for each head, the grouped norm
+ * that stands behind either, and the maps of a serving batch, each declared
+ * below with its own layouts.
  *
  * Problem (page "Mamba", Part IV Stage 5, the selective_scan_fn interface):
  *   per batch row b, channel d (d < dim = d_inner) and state n (n < dstate):
