@@ -915,9 +915,9 @@ ss_status check_linattn_heads(const ss_linattn_problem* p) {
   return SS_OK;
 }
 struct LinPlan {
-  int segment;
+  int span;
   int64_t places;
-  size_t states, parts, total;  // bytes of the segments' states, and where the shared heads' parts begin
+  size_t states, parts, total;  // bytes of the states between pieces, and where the shared heads' parts begin
 };
 // `jobs` walks of every head: one forward, three backward
 ss_status plan_linattn(const ss_linattn_problem* p, int jobs, LinPlan* plan) {
@@ -928,11 +928,13 @@ ss_status plan_linattn(const ss_linattn_problem* p, int jobs, LinPlan* plan) {
   if (p->q_stride % 8 || p->k_stride % 8 || p->v_stride % 8) return SS_ERR_MISALIGNED;
   const int64_t longest = p->packed ? p->tokens : p->tokens / p->nseqs, walks = p->nheads * jobs;
   LinPlan l{};
-  l.segment = ss::lin_segment(p->tokens, p->nseqs, longest, walks, 256);
-  l.places = p->packed ? p->tokens / l.segment + p->nseqs : p->nseqs * ((longest + l.segment - 1) / l.segment);
+  const bool ragged = p->packed && p->nseqs > 1;
+  const int64_t chunks = ragged ? p->tokens / 64 + p->nseqs : (longest + 63) / 64;  // of all sequences, or of each
+  l.span = ss::lin_span(chunks, ragged ? 1 : p->nseqs, longest, walks, 256);
+  l.places = !l.span ? p->nseqs : (ragged ? 1 : p->nseqs) * ((chunks + l.span - 1) / l.span);
   if (l.places * walks > kMaxGrid || p->nseqs * walks * (p->dk * p->dv / 1024) > kMaxGrid) return SS_ERR_BAD_SHAPE;
   if (jobs > 1 && p->tokens * p->nheads > kMaxGrid * 8) return SS_ERR_BAD_SHAPE;  // the shared heads' sums
-  l.states = l.segment == ss::kLinWhole ? 0 : align256((size_t)(l.places * walks) * (size_t)(p->dk * p->dv) * 4);
+  l.states = l.span ? align256((size_t)(2 * l.places * walks) * (size_t)(p->dk * p->dv) * 4) : 0;
   l.parts = l.states;
   l.total = l.parts + (jobs > 1 && p->kv_heads != p->nheads
                            ? align256((size_t)(p->tokens * p->nheads) * (size_t)(p->dk + p->dv) * 4) : 0);
@@ -955,11 +957,11 @@ ss::LinParams linattn_params(const ss_linattn_problem* p, const LinPlan& l, cons
   k.io = p->io_dtype;
   k.log_decay = log_decay;
   k.cu = cu;
-  k.split = l.segment != ss::kLinWhole;
+  k.split = l.span != 0;
   k.ws = static_cast<float*>(workspace);
   k.tokens = (int32_t)p->tokens; k.nseqs = (int32_t)p->nseqs;
   k.heads = (int32_t)p->nheads; k.share = (int32_t)(p->nheads / p->kv_heads);
-  k.segment = l.segment; k.places = (int32_t)l.places;
+  k.span = l.span; k.places = (int32_t)l.places;
   return k;
 }
 ss::LinWalk linattn_forward(const ss_linattn_problem* p, const void* q, const void* k, const void* v,

@@ -321,11 +321,14 @@ struct LinParams {
   const int32_t* has_state;  // with pool: (nseqs) or null, none has
   int32_t pool;              // states lie in slots, else by sequence
   int32_t zero_rest;         // rows of no sequence get outputs of zero
-  int32_t split;             // this launch computes the segments' own states
-  float* ws;                 // (places, jobs, heads, dk * dv): a segment's own state, then the state that enters it
+  int32_t split;             // this launch computes the pieces' own states
+  // (2, places, jobs, heads, dk * dv).  First a piece's own state, of its last sequence's rows, if
+  // that goes on behind it; then the state that enters that sequence, if it begins there.
+  // Second the state that enters a piece in which a sequence goes on.
+  float* ws;
   int32_t tokens, nseqs, nslots, heads, share;  // share: heads to a key and value
-  int32_t segment;           // rows of a segment, a multiple of 64
-  int32_t places;
+  int32_t span;              // chunk places of 64 rows to a piece; 0: a piece is a sequence
+  int32_t places;            // pieces
 };
 
 struct LinStepParams {

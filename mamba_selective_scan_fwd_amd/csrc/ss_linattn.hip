@@ -71,35 +71,46 @@ __device__ __forceinline__ u32x4v read_time_frag(uint32_t at, uint32_t next) {
   return __builtin_bit_cast(u32x4v, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// The rows that workgroup place `place` walks.
+// A sequence's rows and the places of its chunks: packed ones are numbered one after the other, an empty
+// sequence having one; those of one length begin a piece each.
+struct LinSeq {
+  int begin, len, first, chunks;
+};
+__device__ __forceinline__ int lin_stride(const LinParams& p) {  // places of a sequence of tokens / nseqs rows
+  const int chunks = (p.tokens / p.nseqs + kC - 1) / kC;
+  return p.span ? (chunks + p.span - 1) / p.span * p.span : chunks;
+}
+__device__ __forceinline__ LinSeq lin_seq(const LinParams& p, int s) {
+  LinSeq q;
+  if (p.cu) {
+    q.begin = uniform(seq_row(p.cu, s, p.tokens));
+    const int end = uniform(seq_row(p.cu, s + 1, p.tokens));
+    q.len = end > q.begin ? end - q.begin : 0;
+    q.chunks = q.len > 0 ? (q.len + kC - 1) / kC : 1;
+    q.first = q.begin / kC + s;
+  } else {
+    q.len = p.tokens / p.nseqs;
+    q.begin = s * q.len;
+    q.chunks = (q.len + kC - 1) / kC;
+    q.first = s * lin_stride(p);
+  }
+  return q;
+}
+// the sequence that chunk place `place` lies in, or is behind
+__device__ __forceinline__ int lin_seq_at(const LinParams& p, int place) {
+  if (p.cu) return find_chunk<6>(p.cu, p.nseqs, p.tokens, place).seq;
+  return place / lin_stride(p);
+}
+// Some of a sequence's chunks, in the walk's order
 struct LinRows {
   int seq, begin, len;  // the sequence
-  int t0, rows;         // its segment's rows, in the walk's order
-  bool live, last;      // the place has a segment (of an empty sequence too); the sequence's last
+  int t0, rows;
+  bool last;            // the sequence's last row is among them
+  int piece;
 };
-__device__ __forceinline__ LinRows lin_rows(const LinParams& p, int place) {
-  LinRows r;
-  int part;
-  if (p.cu) {
-    const uint32_t segment = (uint32_t)p.segment;
-    const SeqChunk q = find_chunk_by(p.cu, p.nseqs, p.tokens, place, [=](int row) { return (int)((uint32_t)row / segment); });
-    r.seq = q.seq;
-    r.begin = q.begin;
-    r.len = q.len;
-    part = q.chunk;
-  } else {
-    r.len = p.tokens / p.nseqs;
-    const int parts = (r.len + p.segment - 1) / p.segment;
-    r.seq = place / parts;
-    part = place - r.seq * parts;
-    r.begin = r.seq * r.len;
-  }
-  const int64_t t0 = (int64_t)part * p.segment, left = r.len - t0;
-  r.live = part >= 0 && t0 < (r.len > 0 ? r.len : 1);
-  r.t0 = r.live ? (int)t0 : 0;
-  r.rows = r.live ? (int)(left < p.segment ? left : p.segment) : 0;
-  r.last = left <= p.segment;
-  return r;
+__device__ __forceinline__ LinRows lin_rows(const LinSeq& q, int s, int i0, int i1, int piece) {
+  const int end = i1 < q.chunks ? i1 * kC : q.len;
+  return {s, q.begin, q.len, i0 * kC, end - i0 * kC, i1 >= q.chunks, piece};
 }
 // A sequence's first state (null: zeros) and where its last one goes (null: nowhere)
 __device__ __forceinline__ void lin_states(const LinParams& p, const LinWalk& w, int seq, int h, const float*& init,
@@ -305,7 +316,7 @@ struct TileLoad {
 };
 
 template <int IO, int DC, int DO, bool STATE, bool FULL>
-__device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>& lds, int job, int h, int place) {
+__device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>& lds, int job, int h, const LinRows& q) {
   constexpr int CT = DC / 16, OT = DO / 64;  // tiles of a wave's state: all of c, a quarter of o
   constexpr int kPairs = 3;                  // 16 x 16 tiles of pairs a wave, at the most
   constexpr bool kTwo = IO == SS_F16;
@@ -313,22 +324,9 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
   const int tid = threadIdx.x, wave = uniform(tid / 64);
   const int lane = tid % 64, l16 = lane % 16, g4 = 4 * (lane / 16);
   const LinWalk& w = p.job[job];
-  const LinRows q = lin_rows(p, place);
   const int kvh = h / p.share;
-  if (!STATE && p.zero_rest && p.cu) {  // rows of no sequence have outputs of zero
-    const int lead = seq_row(p.cu, 0, p.tokens), behind = seq_row(p.cu, p.nseqs, p.tokens);
-    const int end = behind > lead ? behind : lead;
-    for (int r = place; r < lead + p.tokens - end; r += p.places) {
-      const int64_t at = ((int64_t)(r < lead ? r : end + r - lead) * p.heads + h) * DO;
-      if (tid < DO) {
-        if (w.sum) static_cast<float*>(w.out)[at + tid] = 0.0f;
-        else static_cast<uint16_t*>(w.out)[at + tid] = 0;
-      }
-    }
-  }
-  if (!q.live || (STATE && q.last)) return;
 
-  // ---- loads for the chunk that begins at row t of the segment, in the walk's order
+  // ---- loads for the chunk that begins at row t of these, in the walk's order
   const bool rev = w.rev != 0;
   auto chunk_rows = [&](int t) { return q.rows - t < kC ? q.rows - t : kC; };
   auto chunk_tok = [&](int t, int rows) {
@@ -374,8 +372,10 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
   const float* init;
   float* fin;
   lin_states(p, w, q.seq, h, init, fin);
-  const bool several = q.len > q.rows;  // the segments' states are in the workspace
-  float* ws = p.ws + (((int64_t)place * p.jobs + job) * p.heads + h) * (DC * DO) + wave * (CT * OT * 256) + lane * 4;
+  // a sequence of several pieces: its states between them are in the workspace (LinParams)
+  const bool several = q.len > q.rows;
+  float* ws = p.ws + ((int64_t)job * p.heads + h) * (DC * DO) + wave * (CT * OT * 256) + lane * 4;
+  ws += ((int64_t)(!STATE && q.t0 > 0 ? p.places : 0) + q.piece) * p.jobs * p.heads * (DC * DO);
   f32x4 H[CT][OT];  // element r: c = 16 ct + g4 + r, o = 16 (OT wave + ot) + l16
   bool have = !STATE && (several || init);
   auto each = [&](auto f) {
@@ -431,7 +431,7 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
   const uint32_t out_at = (uint32_t)(rev ? kC - 1 - l16 : l16) * row_bytes + out_col;
 
   const Remainder rem;
-  // a chunk; false behind the segment's last
+  // a chunk; false behind the last
   auto chunk = [&](int t, auto which) {
     constexpr int turn = decltype(which)::value;
     const int rows = chunk_rows(t);
@@ -580,7 +580,7 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
 #pragma unroll
           for (int tt = 2 * ks; tt < 4; ++tt) out[ot][tt] = BF::run(ch[ot], mh[tt], out[ot][tt]);
       }
-      // ---- outputs: rows past the segment's last go nowhere
+      // ---- outputs: rows past the last go nowhere
       const int size = w.sum ? 4 : 2;
       const auto ov = rows_view(static_cast<char*>(w.out) + (chunk_tok(t, rows) * p.heads + h) * (DO * size), row_bytes, rows, DO * size);
 #pragma unroll
@@ -732,12 +732,54 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
   }
 }
 
-// Workgroup = (segment, head, walk)
+// A piece: `span` chunk places, and in them the rest of a packed sequence, whole ones and the begin
+// of another; or, where there is no span, a sequence.  For the states between the pieces only
+// a piece's last sequence matters, if it goes on behind.
+template <int IO, int DC, int DO, bool STATE, bool FULL>
+__device__ __forceinline__ void walk_piece(const LinParams& p, WalkLds<DC, DO, STATE>& lds, int job, int h, int piece) {
+  const int c0 = piece * p.span, c1 = c0 + p.span;
+  if constexpr (STATE) {
+    const int s = lin_seq_at(p, c1 - 1);
+    const LinSeq q = lin_seq(p, s);
+    const int i0 = c0 > q.first ? c0 - q.first : 0, i1 = c1 - q.first;
+    if (i1 <= i0 || i1 >= q.chunks) return;
+    walk<IO, DC, DO, STATE, FULL>(p, lds, job, h, lin_rows(q, s, i0, i1, piece));
+  } else {
+    const LinWalk& w = p.job[job];
+    if (p.zero_rest && p.cu) {  // rows of no sequence have outputs of zero
+      const int lead = seq_row(p.cu, 0, p.tokens), behind = seq_row(p.cu, p.nseqs, p.tokens);
+      const int end = behind > lead ? behind : lead, tid = threadIdx.x;
+      for (int r = piece; r < lead + p.tokens - end; r += p.places) {
+        const int64_t at = ((int64_t)(r < lead ? r : end + r - lead) * p.heads + h) * DO;
+        if (tid < DO) {
+          if (w.sum) static_cast<float*>(w.out)[at + tid] = 0.0f;
+          else static_cast<uint16_t*>(w.out)[at + tid] = 0;
+        }
+      }
+    }
+    // no more sequences than places, whatever the offsets hold
+    int s = p.span ? lin_seq_at(p, c0) : piece;
+    const int end = p.span ? (p.span < p.nseqs - s ? s + p.span : p.nseqs) : piece + 1;
+    for (; s < end; ++s) {
+      const LinSeq q = lin_seq(p, s);
+      int i0 = 0, i1 = q.chunks;
+      if (p.span) {
+        if (q.first >= c1) break;
+        i0 = c0 > q.first ? c0 - q.first : 0;
+        i1 = i1 < c1 - q.first ? i1 : c1 - q.first;
+        if (i0 >= i1) continue;
+      }
+      lds_barrier<-1>();  // everyone is done with the sequence before
+      walk<IO, DC, DO, STATE, FULL>(p, lds, job, h, lin_rows(q, s, i0, i1, piece));
+    }
+  }
+}
+// Workgroup = (piece, head, walk)
 template <int IO, int DC, int DO, bool STATE, bool FULL>
 __global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) {
   __shared__ WalkLds<DC, DO, STATE> lds;
   const int lb = (int)xcd_logical_block();
-  walk<IO, DC, DO, STATE, FULL>(p, lds, lb % p.jobs, lb / p.jobs % p.heads, lb / p.jobs / p.heads);
+  walk_piece<IO, DC, DO, STATE, FULL>(p, lds, lb % p.jobs, lb / p.jobs % p.heads, lb / p.jobs / p.heads);
 }
 // The gradients' three walks where dv = DC and dk = DO differ: dq's and dk's have the states' sides
 // the one way, dv's the other; in one launch they run beside each other
@@ -747,17 +789,17 @@ __global__ void __launch_bounds__(kWalkThreads, 2) lin_walks_kernel(LinParams p)
     WalkLds<DC, DO, STATE> two;
     WalkLds<DO, DC, STATE> one;
   } lds;
-  const int lb = (int)xcd_logical_block(), job = lb % 3, h = lb / 3 % p.heads, place = lb / 3 / p.heads;
-  if (job < 2) walk<IO, DC, DO, STATE, false>(p, lds.two, job, h, place);
-  else walk<IO, DO, DC, STATE, FULL>(p, lds.one, job, h, place);
+  const int lb = (int)xcd_logical_block(), job = lb % 3, h = lb / 3 % p.heads, piece = lb / 3 / p.heads;
+  if (job < 2) walk_piece<IO, DC, DO, STATE, false>(p, lds.two, job, h, piece);
+  else walk_piece<IO, DO, DC, STATE, FULL>(p, lds.one, job, h, piece);
 }
 
-// ---- the states between the segments of a sequence ----------------------------------
-// Workgroup = (sequence of several segments, head, walk, 1024 elements): E <- the
-// sequence's first state; per segment, S <- E in the workspace and E <- decay E + S,
-// S being the segment's own state (the last one has none: its walk ends with the
-// sequence's).  The first state goes through the workspace too, so that a walk's
-// end may overwrite it in the pool while others begin.
+// ---- the states between the pieces of a sequence ------------------------------------
+// Workgroup = (sequence of several pieces, head, walk, 1024 elements): E <- the
+// sequence's first state; per piece, E to the workspace and E <- decay E + S, S being
+// the state of the sequence's rows in the piece (the last one has none: its walk ends
+// with the sequence's).  The first state goes through the workspace too, so that a
+// walk's end may overwrite it in the pool while others begin.
 __global__ void __launch_bounds__(256) lin_pass_kernel(LinParams p) {
   constexpr int kAhead = 8;
   const int size = p.job[0].dc * p.job[0].dout, parts = size / 1024;
@@ -768,18 +810,11 @@ __global__ void __launch_bounds__(256) lin_pass_kernel(LinParams p) {
   i /= p.jobs;
   const int h = i % p.heads, s = i / p.heads;
   const LinWalk& w = p.job[job];
-  int begin, len, first;
-  if (p.cu) {
-    begin = uniform(seq_row(p.cu, s, p.tokens));
-    len = uniform(seq_row(p.cu, s + 1, p.tokens)) - begin;
-    first = begin / p.segment + s;
-  } else {
-    len = p.tokens / p.nseqs;
-    first = s * ((len + p.segment - 1) / p.segment);
-  }
-  if (len <= p.segment) return;
-  const int n = (len + p.segment - 1) / p.segment;
-  const float d = lin_power_m1(p.log_decay[h], p.segment);
+  const LinSeq q = lin_seq(p, s);
+  const int first = q.first / p.span, n = (q.first + q.chunks - 1) / p.span - first + 1;
+  if (n < 2) return;
+  float d = lin_power_m1(p.log_decay[h], ((first + 1) * p.span - q.first) * kC);
+  const float whole = lin_power_m1(p.log_decay[h], p.span * kC);
   const float* init;
   float* fin;
   lin_states(p, w, s, h, init, fin);
@@ -792,18 +827,20 @@ __global__ void __launch_bounds__(256) lin_pass_kernel(LinParams p) {
       E[r] = init[state_at(w, 16 * ct + 4 * (lane / 16) + r, 16 * (ot_n * wave + ot) + lane % 16)];
   }
   const int64_t step = (int64_t)p.jobs * p.heads * size;
-  float* ws = p.ws + (((int64_t)first * p.jobs + job) * p.heads + h) * size + 4 * (int64_t)e4;
+  float* own = p.ws + (((int64_t)first * p.jobs + job) * p.heads + h) * size + 4 * (int64_t)e4;
+  float* enter = own + p.places * step;
   f32x4 S[kAhead];
   for (int c = 0; c < n; c += kAhead) {
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
-      if (c + k < n - 1) S[k] = *reinterpret_cast<const f32x4*>(ws + (c + k) * step);
+      if (c + k < n - 1) S[k] = *reinterpret_cast<const f32x4*>(own + (c + k) * step);
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      if (c + k < n) *reinterpret_cast<f32x4*>(ws + (c + k) * step) = E;
+      if (c + k < n) *reinterpret_cast<f32x4*>((c + k ? enter : own) + (c + k) * step) = E;
       if (c + k < n - 1) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) E[r] = fmaf(d, E[r], E[r]) + S[k][r];
+        d = whole;
       }
     }
   }

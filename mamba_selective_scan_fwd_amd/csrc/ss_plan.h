@@ -37,32 +37,26 @@ inline int pass_ahead(int64_t workgroups, int64_t chunks, int64_t nseqs, int64_t
   return workgroups <= 4 * cus && chunks >= 8 * nseqs ? 16 : 4;
 }
 
-// Rows of the segments in which linear attention walks its sequences (the longest
-// of `longest` rows, all of them of `tokens`; `walks` of each), a multiple of 64, or
-// kLinWhole where none is split: as many segments as give every CU two workgroups at
-// once, none of less than kLinLeast rows, and no sequence of no more than three times
-// these.  A walk takes 3.5 us a chunk of 64 rows, a split two more launches (12 heads of
-// 128 x 128 in bf16, whole against segments of 128 rows: 1 sequence of 256 rows 17.5 and
-// 22.7 us, of 512 31.6 and 24.1, of 1024 60.1 and 27.5; 4 of 384 24.9 and 32.4, of 1024
-// 61.2 and 40.3).  One prompt of 32769 rows with 16 walks: segments of 448 rows 151 us,
-// 704 139, 1088 (31: 496 workgroups) 136, 1280 151, whole 1700; 24 ragged prompts of
-// 16384 rows with 12 walks 126 with 384, 119 with 448 or 512 (its choice); a layer's 8 x 2048
-// rows with 12 walks 82.6 with 384 (its choice is 448: 83.5), 89.5 with 256, 118 whole, and with
-// the gradients' 36 walks 200 with 512 to 1024 against 176 whole.
-constexpr int kLinWhole = 1 << 30, kLinLeast = 128;
-inline int lin_segment(int64_t tokens, int64_t nseqs, int64_t longest, int64_t walks, int64_t cus) {
-  if (longest <= 3 * kLinLeast) return kLinWhole;
-  int64_t rows;
-  if (nseqs * longest == tokens) {  // all alike
-    const int64_t n = 2 * cus / (nseqs * walks);
-    if (n < 2) return kLinWhole;
-    rows = (longest + n - 1) / n;
-  } else {
-    rows = tokens * walks * 5 / (8 * cus);  // most sequences' last segments are short
-  }
-  rows = (rows + 63) / 64 * 64;
-  if (rows < kLinLeast) rows = kLinLeast;
-  return rows >= longest ? kLinWhole : (int)rows;
+// Chunk places of 64 rows to a piece in which linear attention walks its sequences, or
+// 0: each whole.  `chunks`: the places of all packed sequences, or of each of `runs` of
+// one length (the longest of `longest` rows); `walks` of each.  As many pieces as give
+// every CU two workgroups at once, none of less than 128 rows, and none of sequences of up to
+// 384 rows.  A walk takes 3.5 us a chunk, a split two more launches (12 heads of 128 x 128
+// in bf16, whole against segments of 128 rows: 1 sequence of 256 rows 17.5 and 22.7 us, of
+// 512 31.6 and 24.1, of 1024 60.1 and 27.5; 4 of 384 24.9 and 32.4, of 1024 61.2 and
+// 40.3).  One prompt of 32769 rows with 16 walks: pieces of 448 rows 151 us, 704 139, 1088 (its
+// choice: 496 workgroups) 136, 1280 151, whole 1700; a layer's 8 x 2048 rows with 12 walks
+// 83 with 384 or 448 (its choice), 89.5 with 256, 118 whole, and with the gradients' 36 walks
+// (one piece each) 176 whole, 200 with 512 to 1024.  Pieces of packed sequences go on over
+// their ends, for their lengths are not known: 24 ragged prompts of 16384 rows with 12
+// walks 113 us, 119 to 132 in pieces that begin with their sequences.  Of sequences of one
+// length they do not: the layer's gradients take 208 us in 14 equal pieces a head.
+inline int lin_span(int64_t chunks, int64_t runs, int64_t longest, int64_t walks, int64_t cus) {
+  if (longest <= 384) return 0;
+  const int64_t pieces = 2 * cus / (runs * walks);
+  if (pieces < 2) return 0;
+  const int64_t span = chunks <= 2 * pieces ? 2 : (chunks + pieces - 1) / pieces;
+  return span < chunks ? (int)span : 0;
 }
 
 }  // namespace ss
