@@ -915,8 +915,7 @@ ss_status check_linattn_heads(const ss_linattn_problem* p) {
   return SS_OK;
 }
 struct LinPlan {
-  int span;
-  int64_t places;
+  ss::LinCut cut;
   size_t states, parts, total;  // bytes of the states between pieces, and where the shared heads' parts begin
 };
 // `jobs` walks of every head: one forward, three backward
@@ -928,13 +927,10 @@ ss_status plan_linattn(const ss_linattn_problem* p, int jobs, LinPlan* plan) {
   if (p->q_stride % 8 || p->k_stride % 8 || p->v_stride % 8) return SS_ERR_MISALIGNED;
   const int64_t longest = p->packed ? p->tokens : p->tokens / p->nseqs, walks = p->nheads * jobs;
   LinPlan l{};
-  const bool ragged = p->packed && p->nseqs > 1;
-  const int64_t chunks = ragged ? p->tokens / 64 + p->nseqs : (longest + 63) / 64;  // of all sequences, or of each
-  l.span = ss::lin_span(chunks, ragged ? 1 : p->nseqs, longest, walks, 256);
-  l.places = !l.span ? p->nseqs : (ragged ? 1 : p->nseqs) * ((chunks + l.span - 1) / l.span);
-  if (l.places * walks > kMaxGrid || p->nseqs * walks * (p->dk * p->dv / 1024) > kMaxGrid) return SS_ERR_BAD_SHAPE;
+  if (p->nseqs * walks * (p->dk * p->dv / 1024) > kMaxGrid) return SS_ERR_BAD_SHAPE;
+  l.cut = ss::lin_cut(p->packed != 0, p->tokens, p->nseqs, longest, walks, 256);
   if (jobs > 1 && p->tokens * p->nheads > kMaxGrid * 8) return SS_ERR_BAD_SHAPE;  // the shared heads' sums
-  l.states = l.span ? align256((size_t)(2 * l.places * walks) * (size_t)(p->dk * p->dv) * 4) : 0;
+  l.states = align256((size_t)(2 * l.cut.pieces * l.cut.stride) * (size_t)(p->dk * p->dv) * 4);
   l.parts = l.states;
   l.total = l.parts + (jobs > 1 && p->kv_heads != p->nheads
                            ? align256((size_t)(p->tokens * p->nheads) * (size_t)(p->dk + p->dv) * 4) : 0);
@@ -957,11 +953,11 @@ ss::LinParams linattn_params(const ss_linattn_problem* p, const LinPlan& l, cons
   k.io = p->io_dtype;
   k.log_decay = log_decay;
   k.cu = cu;
-  k.split = l.span != 0;
+  k.split = l.cut.pieces != 0;
   k.ws = static_cast<float*>(workspace);
   k.tokens = (int32_t)p->tokens; k.nseqs = (int32_t)p->nseqs;
   k.heads = (int32_t)p->nheads; k.share = (int32_t)(p->nheads / p->kv_heads);
-  k.span = l.span; k.places = (int32_t)l.places;
+  k.whole = l.cut.whole; k.span = l.cut.span; k.pieces = l.cut.pieces; k.stride = l.cut.stride;
   return k;
 }
 ss::LinWalk linattn_forward(const ss_linattn_problem* p, const void* q, const void* k, const void* v,

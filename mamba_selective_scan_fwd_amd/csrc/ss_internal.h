@@ -322,13 +322,15 @@ struct LinParams {
   int32_t pool;              // states lie in slots, else by sequence
   int32_t zero_rest;         // rows of no sequence get outputs of zero
   int32_t split;             // this launch computes the pieces' own states
-  // (2, places, jobs, heads, dk * dv).  First a piece's own state, of its last sequence's rows, if
+  // (2, pieces, stride, dk * dv).  First a piece's own state, of its last sequence's rows, if
   // that goes on behind it; then the state that enters that sequence, if it begins there.
   // Second the state that enters a piece in which a sequence goes on.
   float* ws;
   int32_t tokens, nseqs, nslots, heads, share;  // share: heads to a key and value
-  int32_t span;              // chunk places of 64 rows to a piece; 0: a piece is a sequence
-  int32_t places;            // pieces
+  int32_t whole;             // walks (sequence, head, job) that run whole, the first ones
+  int32_t span;              // chunks of 64 rows to a piece of the others
+  int32_t pieces;            // of each of the others; of all packed sequences together
+  int32_t stride;            // the others; heads * jobs where the sequences are packed
 };
 
 struct LinStepParams {

@@ -71,46 +71,35 @@ __device__ __forceinline__ u32x4v read_time_frag(uint32_t at, uint32_t next) {
   return __builtin_bit_cast(u32x4v, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// A sequence's rows and the places of its chunks: packed ones are numbered one after the other, an empty
-// sequence having one; those of one length begin a piece each.
+// A sequence's rows, and the places of a packed one's chunks, numbered over all of them (an empty one has one)
 struct LinSeq {
   int begin, len, first, chunks;
 };
-__device__ __forceinline__ int lin_stride(const LinParams& p) {  // places of a sequence of tokens / nseqs rows
-  const int chunks = (p.tokens / p.nseqs + kC - 1) / kC;
-  return p.span ? (chunks + p.span - 1) / p.span * p.span : chunks;
-}
 __device__ __forceinline__ LinSeq lin_seq(const LinParams& p, int s) {
   LinSeq q;
   if (p.cu) {
     q.begin = uniform(seq_row(p.cu, s, p.tokens));
     const int end = uniform(seq_row(p.cu, s + 1, p.tokens));
     q.len = end > q.begin ? end - q.begin : 0;
-    q.chunks = q.len > 0 ? (q.len + kC - 1) / kC : 1;
     q.first = q.begin / kC + s;
   } else {
     q.len = p.tokens / p.nseqs;
     q.begin = s * q.len;
-    q.chunks = (q.len + kC - 1) / kC;
-    q.first = s * lin_stride(p);
+    q.first = 0;
   }
+  q.chunks = q.len > 0 ? (q.len + kC - 1) / kC : 1;
   return q;
-}
-// the sequence that chunk place `place` lies in, or is behind
-__device__ __forceinline__ int lin_seq_at(const LinParams& p, int place) {
-  if (p.cu) return find_chunk<6>(p.cu, p.nseqs, p.tokens, place).seq;
-  return place / lin_stride(p);
 }
 // Some of a sequence's chunks, in the walk's order
 struct LinRows {
   int seq, begin, len;  // the sequence
   int t0, rows;
   bool last;            // the sequence's last row is among them
-  int piece;
+  int slot;             // of the piece's states in the workspace
 };
-__device__ __forceinline__ LinRows lin_rows(const LinSeq& q, int s, int i0, int i1, int piece) {
+__device__ __forceinline__ LinRows lin_rows(const LinSeq& q, int s, int i0, int i1, int slot) {
   const int end = i1 < q.chunks ? i1 * kC : q.len;
-  return {s, q.begin, q.len, i0 * kC, end - i0 * kC, i1 >= q.chunks, piece};
+  return {s, q.begin, q.len, i0 * kC, end - i0 * kC, i1 >= q.chunks, slot};
 }
 // A sequence's first state (null: zeros) and where its last one goes (null: nowhere)
 __device__ __forceinline__ void lin_states(const LinParams& p, const LinWalk& w, int seq, int h, const float*& init,
@@ -374,8 +363,7 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
   lin_states(p, w, q.seq, h, init, fin);
   // a sequence of several pieces: its states between them are in the workspace (LinParams)
   const bool several = q.len > q.rows;
-  float* ws = p.ws + ((int64_t)job * p.heads + h) * (DC * DO) + wave * (CT * OT * 256) + lane * 4;
-  ws += ((int64_t)(!STATE && q.t0 > 0 ? p.places : 0) + q.piece) * p.jobs * p.heads * (DC * DO);
+  float* ws = p.ws + (!STATE && q.t0 > 0 ? p.pieces * (int64_t)p.stride + q.slot : q.slot) * (DC * DO) + wave * (CT * OT * 256) + lane * 4;
   f32x4 H[CT][OT];  // element r: c = 16 ct + g4 + r, o = 16 (OT wave + ot) + l16
   bool have = !STATE && (several || init);
   auto each = [&](auto f) {
@@ -732,25 +720,52 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
   }
 }
 
-// A piece: `span` chunk places, and in them the rest of a packed sequence, whole ones and the begin
-// of another; or, where there is no span, a sequence.  For the states between the pieces only
-// a piece's last sequence matters, if it goes on behind.
+// Workgroups: p.whole sequences of a walk each, then p.pieces of p.stride walks each.  A piece is
+// `span` chunks of a sequence; or, of packed ones, `span` chunk places, and in them the rest
+// of a sequence, whole ones and the begin of another.  For the states between the pieces
+// only a piece's last sequence matters, if it goes on behind.
+struct LinWork {
+  int seq, job, h, piece, slot;  // piece < 0: the whole sequence
+};
+__device__ __forceinline__ int xcd_logical(int bid, int nb) {  // as xcd_logical_block, among nb workgroups
+  const int per = nb / 8, rem = nb % 8, xcd = bid % 8;
+  return xcd * per + (xcd < rem ? xcd : rem) + bid / 8;
+}
+template <bool STATE>
+__device__ __forceinline__ LinWork lin_work(const LinParams& p) {
+  LinWork k{0, 0, 0, -1, 0};
+  const int bid = (int)blockIdx.x, whole = STATE ? 0 : p.whole;
+  int u;
+  if (bid < whole) {
+    u = xcd_logical(bid, whole);
+  } else {
+    k.slot = xcd_logical(bid - whole, (int)gridDim.x - whole);
+    k.piece = k.slot / p.stride;
+    u = p.whole + k.slot % p.stride;
+  }
+  k.job = u % p.jobs;
+  u /= p.jobs;
+  k.h = u % p.heads;
+  k.seq = u / p.heads;  // 0 in pieces of packed sequences
+  return k;
+}
 template <int IO, int DC, int DO, bool STATE, bool FULL>
-__device__ __forceinline__ void walk_piece(const LinParams& p, WalkLds<DC, DO, STATE>& lds, int job, int h, int piece) {
-  const int c0 = piece * p.span, c1 = c0 + p.span;
+__device__ __forceinline__ void walk_piece(const LinParams& p, WalkLds<DC, DO, STATE>& lds, const LinWork& k) {
+  const int c0 = k.piece * p.span, c1 = c0 + p.span;
   if constexpr (STATE) {
-    const int s = lin_seq_at(p, c1 - 1);
+    int s = k.seq;
+    if (p.cu) s = find_chunk<6>(p.cu, p.nseqs, p.tokens, c1 - 1).seq;
     const LinSeq q = lin_seq(p, s);
     const int i0 = c0 > q.first ? c0 - q.first : 0, i1 = c1 - q.first;
     if (i1 <= i0 || i1 >= q.chunks) return;
-    walk<IO, DC, DO, STATE, FULL>(p, lds, job, h, lin_rows(q, s, i0, i1, piece));
+    walk<IO, DC, DO, STATE, FULL>(p, lds, k.job, k.h, lin_rows(q, s, i0, i1, k.slot));
   } else {
-    const LinWalk& w = p.job[job];
     if (p.zero_rest && p.cu) {  // rows of no sequence have outputs of zero
+      const LinWalk& w = p.job[k.job];
       const int lead = seq_row(p.cu, 0, p.tokens), behind = seq_row(p.cu, p.nseqs, p.tokens);
       const int end = behind > lead ? behind : lead, tid = threadIdx.x;
-      for (int r = piece; r < lead + p.tokens - end; r += p.places) {
-        const int64_t at = ((int64_t)(r < lead ? r : end + r - lead) * p.heads + h) * DO;
+      for (int r = k.piece < 0 ? k.seq : k.piece; r < lead + p.tokens - end; r += k.piece < 0 ? p.nseqs : p.pieces) {
+        const int64_t at = ((int64_t)(r < lead ? r : end + r - lead) * p.heads + k.h) * DO;
         if (tid < DO) {
           if (w.sum) static_cast<float*>(w.out)[at + tid] = 0.0f;
           else static_cast<uint16_t*>(w.out)[at + tid] = 0;
@@ -758,28 +773,27 @@ __device__ __forceinline__ void walk_piece(const LinParams& p, WalkLds<DC, DO, S
       }
     }
     // no more sequences than places, whatever the offsets hold
-    int s = p.span ? lin_seq_at(p, c0) : piece;
-    const int end = p.span ? (p.span < p.nseqs - s ? s + p.span : p.nseqs) : piece + 1;
+    const bool over = k.piece >= 0 && p.cu;
+    int s = over ? find_chunk<6>(p.cu, p.nseqs, p.tokens, c0).seq : k.seq;
+    const int end = over ? (p.span < p.nseqs - s ? s + p.span : p.nseqs) : s + 1;
     for (; s < end; ++s) {
       const LinSeq q = lin_seq(p, s);
       int i0 = 0, i1 = q.chunks;
-      if (p.span) {
+      if (k.piece >= 0) {
         if (q.first >= c1) break;
         i0 = c0 > q.first ? c0 - q.first : 0;
         i1 = i1 < c1 - q.first ? i1 : c1 - q.first;
         if (i0 >= i1) continue;
       }
       lds_barrier<-1>();  // everyone is done with the sequence before
-      walk<IO, DC, DO, STATE, FULL>(p, lds, job, h, lin_rows(q, s, i0, i1, piece));
+      walk<IO, DC, DO, STATE, FULL>(p, lds, k.job, k.h, lin_rows(q, s, i0, i1, k.slot));
     }
   }
 }
-// Workgroup = (piece, head, walk)
 template <int IO, int DC, int DO, bool STATE, bool FULL>
 __global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) {
   __shared__ WalkLds<DC, DO, STATE> lds;
-  const int lb = (int)xcd_logical_block();
-  walk_piece<IO, DC, DO, STATE, FULL>(p, lds, lb % p.jobs, lb / p.jobs % p.heads, lb / p.jobs / p.heads);
+  walk_piece<IO, DC, DO, STATE, FULL>(p, lds, lin_work<STATE>(p));
 }
 // The gradients' three walks where dv = DC and dk = DO differ: dq's and dk's have the states' sides
 // the one way, dv's the other; in one launch they run beside each other
@@ -789,9 +803,9 @@ __global__ void __launch_bounds__(kWalkThreads, 2) lin_walks_kernel(LinParams p)
     WalkLds<DC, DO, STATE> two;
     WalkLds<DO, DC, STATE> one;
   } lds;
-  const int lb = (int)xcd_logical_block(), job = lb % 3, h = lb / 3 % p.heads, piece = lb / 3 / p.heads;
-  if (job < 2) walk_piece<IO, DC, DO, STATE, false>(p, lds.two, job, h, piece);
-  else walk_piece<IO, DO, DC, STATE, FULL>(p, lds.one, job, h, piece);
+  const LinWork k = lin_work<STATE>(p);
+  if (k.job < 2) walk_piece<IO, DC, DO, STATE, false>(p, lds.two, k);
+  else walk_piece<IO, DO, DC, STATE, FULL>(p, lds.one, k);
 }
 
 // ---- the states between the pieces of a sequence ------------------------------------
@@ -806,9 +820,8 @@ __global__ void __launch_bounds__(256) lin_pass_kernel(LinParams p) {
   int i = (int)blockIdx.x;
   const int e4 = i % parts * 256 + (int)threadIdx.x;
   i /= parts;
-  const int job = i % p.jobs;
-  i /= p.jobs;
-  const int h = i % p.heads, s = i / p.heads;
+  i += p.whole;
+  const int job = i % p.jobs, h = i / p.jobs % p.heads, s = i / p.jobs / p.heads;
   const LinWalk& w = p.job[job];
   const LinSeq q = lin_seq(p, s);
   const int first = q.first / p.span, n = (q.first + q.chunks - 1) / p.span - first + 1;
@@ -826,9 +839,9 @@ __global__ void __launch_bounds__(256) lin_pass_kernel(LinParams p) {
     for (int r = 0; r < 4; ++r)
       E[r] = init[state_at(w, 16 * ct + 4 * (lane / 16) + r, 16 * (ot_n * wave + ot) + lane % 16)];
   }
-  const int64_t step = (int64_t)p.jobs * p.heads * size;
-  float* own = p.ws + (((int64_t)first * p.jobs + job) * p.heads + h) * size + 4 * (int64_t)e4;
-  float* enter = own + p.places * step;
+  const int64_t step = (int64_t)p.stride * size;
+  float* own = p.ws + ((int64_t)first * p.stride + (p.cu ? h * p.jobs + job : i - p.whole)) * size + 4 * (int64_t)e4;
+  float* enter = own + p.pieces * step;
   f32x4 S[kAhead];
   for (int c = 0; c < n; c += kAhead) {
 #pragma unroll
@@ -915,7 +928,7 @@ __global__ void __launch_bounds__(256) lin_step_kernel(LinStepParams p) {
 
 template <int IO, int DC, int DO, bool FULL>
 hipError_t launch_walk(const LinParams& p, hipStream_t st) {
-  const dim3 grid((uint32_t)(p.places * p.heads * p.jobs)), threads(kWalkThreads);
+  const dim3 grid((uint32_t)(p.split ? (p.pieces - 1) * p.stride : p.whole + p.pieces * p.stride)), threads(kWalkThreads);
   if constexpr (DC != DO) {
     if (p.jobs == 3) {
       if (p.split) hipLaunchKernelGGL((lin_walks_kernel<IO, DC, DO, true, FULL>), grid, threads, 0, st, p);
@@ -950,7 +963,8 @@ hipError_t launch_linattn_io(LinParams p, hipStream_t st) {
     hipError_t e = launch_walks_io<IO>(p, st);
     if (e != hipSuccess) return e;
     const int parts = p.job[0].dc * p.job[0].dout / 1024;
-    hipLaunchKernelGGL(lin_pass_kernel, dim3((uint32_t)(p.nseqs * p.heads * p.jobs * parts)), dim3(256), 0, st, p);
+    const int walks = p.nseqs * p.heads * p.jobs - p.whole;
+    hipLaunchKernelGGL(lin_pass_kernel, dim3((uint32_t)(walks * parts)), dim3(256), 0, st, p);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     p.split = 0;

@@ -37,26 +37,40 @@ inline int pass_ahead(int64_t workgroups, int64_t chunks, int64_t nseqs, int64_t
   return workgroups <= 4 * cus && chunks >= 8 * nseqs ? 16 : 4;
 }
 
-// Chunk places of 64 rows to a piece in which linear attention walks its sequences, or
-// 0: each whole.  `chunks`: the places of all packed sequences, or of each of `runs` of
-// one length (the longest of `longest` rows); `walks` of each.  As many pieces as give
-// every CU two workgroups at once, none of less than 128 rows, and none of sequences of up to
-// 384 rows.  A walk takes 3.5 us a chunk, a split two more launches (12 heads of 128 x 128
-// in bf16, whole against segments of 128 rows: 1 sequence of 256 rows 17.5 and 22.7 us, of
-// 512 31.6 and 24.1, of 1024 60.1 and 27.5; 4 of 384 24.9 and 32.4, of 1024 61.2 and
-// 40.3).  One prompt of 32769 rows with 16 walks: pieces of 448 rows 151 us, 704 139, 1088 (its
+// How linear attention walks its sequences (`walks` of each, the longest of `longest`
+// rows): whole, or cut into pieces of some chunks of 64 rows, as many as give every CU
+// two workgroups at once, none of less than 128 rows and none of sequences of up to 384
+// rows.  A walk takes 3.5 us a chunk, a cut two more launches (12 heads of 128 x 128 in
+// bf16, whole against pieces of 128 rows: 1 sequence of 256 rows 17.5 and 22.7 us, of 512
+// 31.6 and 24.1, of 1024 60.1 and 27.5; 4 of 384 24.9 and 32.4, of 1024 61.2 and 40.3).
+// One prompt of 32769 rows with 16 walks: pieces of 448 rows 151 us, 704 139, 1088 (its
 // choice: 496 workgroups) 136, 1280 151, whole 1700; a layer's 8 x 2048 rows with 12 walks
-// 83 with 384 or 448 (its choice), 89.5 with 256, 118 whole, and with the gradients' 36 walks
-// (one piece each) 176 whole, 200 with 512 to 1024.  Pieces of packed sequences go on over
-// their ends, for their lengths are not known: 24 ragged prompts of 16384 rows with 12
-// walks 113 us, 119 to 132 in pieces that begin with their sequences.  Of sequences of one
-// length they do not: the layer's gradients take 208 us in 14 equal pieces a head.
-inline int lin_span(int64_t chunks, int64_t runs, int64_t longest, int64_t walks, int64_t cus) {
-  if (longest <= 384) return 0;
-  const int64_t pieces = 2 * cus / (runs * walks);
-  if (pieces < 2) return 0;
-  const int64_t span = chunks <= 2 * pieces ? 2 : (chunks + pieces - 1) / pieces;
-  return span < chunks ? (int)span : 0;
+// 83 with 384 or 448 (its choice), 89.5 with 256, 118 whole.
+// Packed sequences' pieces go on over their ends, for their lengths are not known: 24
+// ragged prompts of 16384 rows with 12 walks 113 us, 119 to 132 in pieces that begin with
+// their sequences.
+// Of more walks than CUs, all alike, those beyond the last multiple of the CUs would run
+// on as long as the others: these alone are cut, one piece for every CU, where they are a
+// quarter of the CUs at most and long enough (the layer's gradients, 36 walks: 256 whole
+// and 32 in 8 pieces 175 us, all whole 191, all in 14 equal pieces a head 208).
+struct LinCut {
+  int whole, span, pieces, stride;  // as in LinParams
+};
+inline LinCut lin_cut(bool packed, int64_t tokens, int64_t nseqs, int64_t longest, int64_t walks, int64_t cus) {
+  const int64_t all = nseqs * walks;
+  const LinCut none{(int)all, 1, 0, 1};
+  if (longest <= 384) return none;
+  const int64_t chunks = packed ? tokens / 64 + nseqs : (longest + 63) / 64;  // of all sequences, or of each
+  int64_t cut = packed ? walks : all, n = 2 * cus / cut;
+  if (!packed && all > cus) {
+    cut = all % cus;
+    if (cut == 0 || cut > cus / 4 || chunks < 24) return none;
+    n = cus / cut;
+  }
+  if (n < 2) return none;
+  const int64_t span = chunks <= 2 * n ? 2 : (chunks + n - 1) / n;
+  if (span >= chunks) return none;
+  return {packed ? 0 : (int)(all - cut), (int)span, (int)((chunks + span - 1) / span), (int)cut};
 }
 
 }  // namespace ss

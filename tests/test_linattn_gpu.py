@@ -225,6 +225,17 @@ def test_training_rows(io, H, G, dk, dv, state):
     _check_train(q, *_train(q, B, L, False, state), state)
 
 
+@pytest.mark.parametrize("io,G,dk,dv", [("f16", 2, 64, 128), ("bf16", 4, 128, 128)])
+def test_training_walks_beyond_a_round(io, G, dk, dv):
+    """22 rows of 4 heads have 264 walks of gradients: 256 run whole beside the last 8, those of the last row, in pieces."""
+    B, L = 22, 1537
+    q = _problem([L] * B, 4, G, dk, dv, io, seed=50)
+    y, fin, gr = _train(q, B, L, False, True)
+    t = (B - 2) * L
+    last = dict(q, cu=q["cu"][:3], T=2 * L, h0=q["h0"][B - 2:], df=q["df"][B - 2:], **{n: q[n][t:] for n in ("q", "k", "v", "dy")})
+    _check_train(last, y[t:], fin[B - 2:], {n: v[B - 2:] if n == "dh0" else v[t:] for n, v in gr.items()}, True)
+
+
 @pytest.mark.parametrize("L", [1, 2, 63, 64, 65, 129, 500])
 def test_training_lengths(L):
     q = _problem([L] * 2, 2, 1, 64, 64, "bf16", seed=L)

@@ -96,14 +96,15 @@ def test_linattn_workspace_and_overlaps():
     assert _calls(p, y=G)[3] == 5 and _calls(p, state=6 * G)[3] == 5
 
 
-@pytest.mark.parametrize("nseqs,length,packed,pieces", [(1, 384, 0, 0), (1, 385, 0, 4), (1, 5000, 0, 40), (4, 4096, 0, 32),
-                                                        (1, 1 << 20, 0, 128), (64, 4096, 0, 2), (65, 4096, 0, 0),
-                                                        (64, 4096, 1, -(-(4096 + 64) // 33)), (3, 130, 1, 5)])
+@pytest.mark.parametrize("nseqs,length,packed,pieces", [
+    (1, 384, 0, 0), (1, 385, 0, 4), (1, 5000, 0, 40), (4, 4096, 0, 4 * 32), (1, 1 << 20, 0, 128), (64, 4096, 0, 64 * 2),
+    (65, 4096, 0, 32), (65, 1536, 0, 12), (65, 1472, 0, 0), (80, 4096, 0, 16 * 4), (81, 4096, 0, 0), (128, 4096, 0, 0),
+    (64, 4096, 1, -(-(4096 + 64) // 33)), (3, 130, 1, 5)])
 def test_linattn_pieces(nseqs, length, packed, pieces):
-    """Short sequences, and so many that they fill the GPU, are walked whole; else in pieces of 128 rows or more, two
-    workgroups of the 4 heads to a CU, those of packed sequences over their ends: two states of every head each."""
+    """Short sequences are walked whole; else in pieces of 128 rows or more, two workgroups of the 4 heads to a CU, those of
+    packed sequences over their ends.  Where there are more walks than CUs, those beyond the last multiple of these
+    are cut if they are a quarter at most: two states of every head each."""
     p = _lin(packed=packed, tokens=nseqs * length, nseqs=nseqs)
-    pieces = pieces if packed else nseqs * pieces
     assert ss.load_library().ss_linattn_workspace_size(R(p)) == 2 * pieces * 4 * 64 * 128 * 4
 
 
