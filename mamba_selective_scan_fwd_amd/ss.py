@@ -1132,18 +1132,16 @@ def pack_requests(new_tokens, slots, seen, tokens):
           for t, name in ((new_tokens, "new_tokens"), (slots, "slots"), (seen, "seen"))]
     # one allocation, every output on a 16-byte boundary
     r, t = R + 3 & -4, tokens + 3 & -4
-    parts = [r, r, r, r, r, t, t, R + 1]
     buf = new_tokens.new_empty(5 * r + 2 * t + R + 1)
-    out = dict(zip(("rows", "taken", "step_slots", "prompt_slots", "has_state", "row_request", "row_position", "cu_seqlens"),
-                   buf.split_with_sizes(parts)))
+    if r == R and t == tokens:
+        parts = buf.split_with_sizes([R] * 5 + [tokens] * 2 + [R + 1])
+    else:
+        parts = buf.split_with_sizes([R, r - R] * 5 + [tokens, t - tokens] * 2 + [R + 1])[::2]
     to = buf.data_ptr()
     _launch(dev, lib.ss_pack_requests, R, tokens, *at, to, to + 4 * r, to + 8 * r, to + 20 * r + 8 * t, to + 12 * r,
             to + 16 * r, to + 20 * r, to + 20 * r + 4 * t)
-    if r != R or t != tokens:
-        for name in out:
-            if name != "cu_seqlens":
-                out[name] = out[name][:tokens if name[:4] == "row_" else R]
-    return out
+    return dict(zip(("rows", "taken", "step_slots", "prompt_slots", "has_state", "row_request", "row_position", "cu_seqlens"),
+                    parts))
 
 
 def copy_probe(src, dst):
