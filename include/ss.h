@@ -578,11 +578,12 @@ ss_status ss_ssd_step(const ss_ssd_step_problem *p, const void *xbc, const void 
  * as declared with the serving calls above (a device array, clamped to
  * 0 .. tokens, sequences may be empty); zero: cu_seqlens is NULL, tokens is a
  * multiple of nseqs and every sequence has tokens / nseqs rows.
- * The workspace is needed where the sequences are too few to fill the GPU and
- * are walked in pieces: per piece, two states of every head (the backward's: six of
- * every head, and with shared heads their parts of dk and dv in fp32).  Its
- * size goes by sizes alone (0: none is needed, NULL); its contents on entry do not
- * matter, and calls that share one must be ordered by the caller.
+ * The workspace is needed where sequences are walked in pieces, because they are too
+ * few to fill the GPU or to fill its last round: per piece, two states of every head (the
+ * backward's: six), and in the backward, where heads share keys and values, their
+ * parts of dk and dv in fp32.  Its size goes by sizes alone (0: none is needed, NULL);
+ * its contents on entry do not matter, and calls that share one must be ordered by the
+ * caller.
  */
 typedef struct ss_linattn_problem {
     int64_t tokens;       /* rows of q, k, v and y */
