@@ -930,11 +930,14 @@ def _heads16(t, name):
     return t.dtype
 
 
-def _flat(t, name):
-    """(B * L, heads, d) of a (B, L, heads, d) tensor: the same memory where its rows lie evenly."""
+def _flat(t, name, keep):
+    """(B * L, heads, d) of a (B, L, heads, d) tensor: the same memory where its rows lie evenly, else a copy, which
+    goes into keep."""
     if not isinstance(t, torch.Tensor) or t.dim() != 4:
         raise ValueError("%s must be a (B, L, heads, d) tensor" % name)
-    return t.flatten(0, 1)
+    t = t.flatten(0, 1)
+    keep.append(t)
+    return t
 
 
 def _linattn(q, k, v, log_decay, cu_seqlens, scale, nseqs, nslots, size, keep, vector=True):
@@ -966,8 +969,8 @@ def linattn_fwd(q, k, v, log_decay, scale=None, cu_seqlens=None, h0=None, return
     B, L, Hn, dk = q.shape
     dv = v.shape[-1]
     S = B if cu_seqlens is None else cu_seqlens.numel() - 1
-    pr, wsz, at = _linattn(_flat(q, "q"), _flat(k, "k"), _flat(v, "v"), log_decay, cu_seqlens, scale, S, 0,
-                           "ss_linattn_workspace_size", keep)
+    pr, wsz, at = _linattn(_flat(q, "q", keep), _flat(k, "k", keep), _flat(v, "v", keep), log_decay, cu_seqlens, scale,
+                           S, 0, "ss_linattn_workspace_size", keep)
     if y is None:
         y = q.new_empty((B, L, Hn, dv))
     fin = q.new_empty((S, Hn, dv, dk), dtype=f32) if return_final_state else None
@@ -992,8 +995,8 @@ def linattn_bwd(q, k, v, log_decay, dy, scale=None, cu_seqlens=None, h0=None, df
     dv = v.shape[-1]
     S = B if cu_seqlens is None else cu_seqlens.numel() - 1
     st = (S, Hn, dv, dk)
-    pr, wsz, at = _linattn(_flat(q, "q"), _flat(k, "k"), _flat(v, "v"), log_decay, cu_seqlens, scale, S, 0,
-                           "ss_linattn_bwd_workspace_size", keep)
+    pr, wsz, at = _linattn(_flat(q, "q", keep), _flat(k, "k", keep), _flat(v, "v", keep), log_decay, cu_seqlens, scale,
+                           S, 0, "ss_linattn_bwd_workspace_size", keep)
     g = {"dq": q.new_empty(q.shape), "dk": k.new_empty(k.shape), "dv": v.new_empty(v.shape)}
     if want_dh0:
         g["dh0"] = q.new_empty(st, dtype=f32)
@@ -1066,7 +1069,10 @@ def _norm(x, weight, bias, z, ngroups, eps, center, silu, gate_first, size, keep
             return None, 0
         if t.dtype is not io or t.shape != rows or t.get_device() != dev:
             _refuse(t, io, name, rows, dev)
-        return _rows(t.reshape(two) if t.dim() != 2 else t, io, name, two, dev, keep, False)
+        if t.dim() != 2:
+            t = t.reshape(two)
+            keep.append(t)  # a copy where its rows do not lie evenly
+        return _rows(t, io, name, two, dev, keep, False)
 
     xa, xs = flat(x, "x", keep)
     za, zs = flat(z, "z", keep)
