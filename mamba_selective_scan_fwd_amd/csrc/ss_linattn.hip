@@ -227,24 +227,21 @@ struct Remainder {
 };
 
 // v as two fp16 parts, |v - hi - lo| <= 2^-22 |v| where |v| is within a factor of 2^15 of the
-// largest that its scale is taken from (2^-38 of that one below)
+// largest that its scale is taken from (2^-38 of that one below).  Every output column o has a
+// scale of its own: one that holds an infinity, or far larger values, takes nothing from the others.
 __device__ __forceinline__ void split2_f16(float v0, float v1, uint32_t& hi, uint32_t& lo) {
   hi = pack2<SS_F16>(v0, v1);
   lo = pack2<SS_F16>(v0 - low16<SS_F16>(hi), v1 - high16<SS_F16>(hi));
 }
-// the power of two that takes a wave's largest magnitude to 2^14 .. 2^15, and its inverse
+// the power of two that takes the largest magnitude of the lanes l16 of all rows to 2^14 .. 2^15, and its inverse
 struct Scale {
   float to, from;
 };
-__device__ __forceinline__ Scale wave_scale(float most) {
-  most = fmaxf(most, row_ror<8>(most));
-  most = fmaxf(most, row_ror<4>(most));
-  most = fmaxf(most, row_ror<2>(most));
-  most = fmaxf(most, row_ror<1>(most));
+__device__ __forceinline__ Scale column_scale(float most) {
   float x, y;
   swap_rows(most, x, y);
   swap_halves(fmaxf(x, y), x, y);
-  const int e = uniform((int)(__float_as_uint(fmaxf(x, y)) >> 23) & 255);
+  const int e = (int)(__float_as_uint(fmaxf(x, y)) >> 23) & 255;
   const int field = 268 - e < 253 ? 268 - e : 253;
   return {__uint_as_float((uint32_t)field << 23), __uint_as_float((uint32_t)(254 - field) << 23)};
 }
@@ -479,16 +476,17 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
         for (int tt = 0; tt < 4; ++tt) out[ot][tt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       if (have) {
         const uint32_t even = opaque(quad_dc) + at_a, odd = (opaque(quad_dc) ^ 32u) + at_a;
-        Scale sc{1.0f, 1.0f};
+        Scale sc[OT];
         if constexpr (kTwo) {
-          float most = 0.0f;
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct)
+          for (int ot = 0; ot < OT; ++ot) {
+            float most = 0.0f;
 #pragma unroll
-            for (int ot = 0; ot < OT; ++ot)
+            for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
               for (int r = 0; r < 4; ++r) most = fmaxf(most, fabsf(H[ct][ot][r]));
-          sc = wave_scale(most);
+            sc[ot] = column_scale(most);
+          }
         }
 #pragma unroll
         for (int kk = 0; kk < CT / 2; ++kk) {
@@ -504,7 +502,7 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
           for (int ot = 0; ot < OT; ++ot) {
             float v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = kTwo ? H[i0 + e / 4 * 2][ot][e % 4] * sc.to : H[i0 + e / 4 * 2][ot][e % 4];
+            for (int e = 0; e < 8; ++e) v[e] = kTwo ? H[i0 + e / 4 * 2][ot][e % 4] * sc[ot].to : H[i0 + e / 4 * 2][ot][e % 4];
             if constexpr (kTwo) {
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
@@ -527,9 +525,17 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
             for (int tt = 0; tt < 4; ++tt) out[ot][tt] = mfma_t<IO>::run(as_vec<IO>(eh[ot]), as_vec<IO>(as[tt]), out[ot][tt]);
         }
 #pragma unroll
-        for (int ot = 0; ot < OT; ++ot)
+        for (int ot = 0; ot < OT; ++ot) {
+          if constexpr (kTwo) {  // the lane's four columns' scales, from the lanes that have these as l16
+            f32x4 from;
 #pragma unroll
-          for (int tt = 0; tt < 4; ++tt) out[ot][tt] *= kTwo ? iw[tt] * sc.from : iw[tt];
+            for (int r = 0; r < 4; ++r) from[r] = __shfl(sc[ot].from, g4 + r, 64);
+#pragma unroll
+            for (int tt = 0; tt < 4; ++tt) out[ot][tt] *= from;
+          }
+#pragma unroll
+          for (int tt = 0; tt < 4; ++tt) out[ot][tt] *= iw[tt];
+        }
       }
       // M and c are there; b's next loads, issued behind c's, may be on their way
       if (more) lds_barrier<tile_loads<DC>()>();
@@ -656,17 +662,20 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
         }
       }
     } else {
-      float wc[2][OT][8], most = 0.0f;
+      float wc[2][OT][8];
+      Scale sc[OT];
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
+      for (int ot = 0; ot < OT; ++ot) {
+        float most = 0.0f;
 #pragma unroll
-        for (int ot = 0; ot < OT; ++ot)
+        for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             weighted(ks, e, ot, wc[ks][ot][2 * e], wc[ks][ot][2 * e + 1]);
             most = fmaxf(most, fmaxf(fabsf(wc[ks][ot][2 * e]), fabsf(wc[ks][ot][2 * e + 1])));
           }
-      const Scale sc = wave_scale(most);
+        sc[ot] = column_scale(most);
+      }
       u32x4v part[2][OT][2];
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
@@ -675,7 +684,7 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint32_t hi, lo;
-            split2_f16(wc[ks][ot][2 * e] * sc.to, wc[ks][ot][2 * e + 1] * sc.to, hi, lo);
+            split2_f16(wc[ks][ot][2 * e] * sc[ot].to, wc[ks][ot][2 * e + 1] * sc[ot].to, hi, lo);
             part[ks][ot][0][e] = hi;
             part[ks][ot][1][e] = lo;
           }
@@ -704,7 +713,7 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
           for (int ot = 0; ot < OT; ++ot)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              H[c0 + i][ot][r] = fmaf(own[i][ot][r], sc.from, fmaf(d, H[c0 + i][ot][r], H[c0 + i][ot][r]));
+              H[c0 + i][ot][r] = fmaf(own[i][ot][r], sc[ot].from, fmaf(d, H[c0 + i][ot][r], H[c0 + i][ot][r]));
       }
     }
     have = true;
