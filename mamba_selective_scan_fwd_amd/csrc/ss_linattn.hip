@@ -126,11 +126,16 @@ __device__ __forceinline__ float lin_power(float g, int n) {
   const double whole = rint(x);
   return ldexpf(exp2_hw((float)(x - whole)), (int)whole);
 }
-// exp(n g) - 1, for H <- H + (exp(n g) - 1) H: a slow decay's own rounding would add up
-// over the chunks that it takes
-__device__ __forceinline__ float lin_power_m1(float g, int n) {
+// What H <- exp(n g) H multiplies with.  A slow decay's own rounding would add up over the
+// chunks that it takes, so there it is exp(n g) - 1, and H <- H + (exp(n g) - 1) H; a fast one's
+// difference from 1 would leave a rounding of the old H where only exp(n g) H is left.
+__device__ __forceinline__ bool lin_slow(float g, int n) {
+  const double x = (double)n * (double)g;
+  return n == 0 || (x > -0.25 && x < 0.25);
+}
+__device__ __forceinline__ float lin_decay(float g, int n) {
+  if (!lin_slow(g, n)) return lin_power(g, n);
   const double x = n ? (double)n * (double)g : 0.0;
-  if (!(x > -0.25 && x < 0.25)) return (float)((double)lin_power(g, n) - 1.0);
   double s = 1.0;  // the power series: 0.25^12 / 13! is below 2^-56
 #pragma unroll
   for (int k = 12; k > 1; --k) s = fma(s, x * (1.0 / k), 1.0);
@@ -155,8 +160,8 @@ __device__ __forceinline__ float lin_power_m1(float g, int n) {
 // TFLOP/s of the formula's operations in all; fp16, in more parts, 32769 rows of 16 heads of
 // 64 x 128 in 102, 41 and 11 us.
 constexpr int kWaves = 4, kWalkThreads = 64 * kWaves;
-// Weights by number, of rows in E' (0 .. 63), powers of a (64 .. 129) and a^rows - 1
-// of a whole chunk and of the last one (160, 161): with M they lie in the columns of
+// Weights by number, of rows in E' (0 .. 63), powers of a (64 .. 129) and the decays
+// (lin_decay) of a whole chunk and of the last one (160, 161): with M they lie in the columns of
 // its first rows that no pair has, so that two workgroups have LDS's 160 KB
 constexpr int kPowers = 64, kDecays = 160;
 template <int DC, int DO, bool STATE>
@@ -353,7 +358,8 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
   };
   set_weights(chunk_rows(0));
   if (tid >= 64 && tid < 64 + kC + 2) *lds.weight(kPowers + tid - 64) = lin_power(g, tid - 64);
-  if (tid >= 192 && tid < 194) *lds.weight(kDecays + tid - 192) = lin_power_m1(g, tid == 192 ? kC : q.rows % kC);
+  if (tid >= 192 && tid < 194) *lds.weight(kDecays + tid - 192) = lin_decay(g, tid == 192 ? kC : q.rows % kC);
+  const bool slow_whole = uniform(lin_slow(g, kC)), slow_last = uniform(lin_slow(g, q.rows % kC));
   if constexpr (!STATE) {  // M's 16 x 16 tiles above the diagonal that are read with their neighbours
     if (tid < 128) {
       const int tile = tid / 32 % 2, row = tid / 2 % 16;
@@ -614,7 +620,8 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
     }
     // ---- H <- a^rows H + sum_s a^{rows-1-s} b_s c_s^T
     if (!STATE && !more && !(q.last && fin)) return false;  // nobody takes it
-    const float d = *lds.weight(kDecays + (rows < kC ? 1 : 0));
+    const float d = __int_as_float(uniform(__float_as_int(*lds.weight(kDecays + (rows < kC ? 1 : 0)))));
+    const bool slow = rows < kC ? slow_last : slow_whole;
     const uint32_t even = opaque(time_dc) + at_b + turn * kTile, odd = (opaque(time_dc) ^ 32u) + at_b + turn * kTile;
     auto b_frag = [&](int ks, int ct) {
       const uint32_t at = 32 * ks * (DC * 2) + 256 * (ct / 2);
@@ -626,14 +633,19 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
       v0 = low16<IO>(cf[ks][ot][e]) * u[0];
       v1 = high16<IO>(cf[ks][ot][e]) * u[1];
     };
-    if constexpr (!kTwo) {
-      constexpr int kParts = FULL ? 3 : 2;
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int ot = 0; ot < OT; ++ot)
+    auto decay_state = [&]() {
+      if (slow) {
+        each([&](int ct, int ot) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) H[ct][ot][r] = fmaf(d, H[ct][ot][r], H[ct][ot][r]);
+        });
+      } else {
+        each([&](int ct, int ot) { H[ct][ot] *= d; });
+      }
+    };
+    if constexpr (!kTwo) {
+      constexpr int kParts = FULL ? 3 : 2;
+      decay_state();
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         u32x4v part[OT][kParts];
@@ -688,6 +700,7 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
             part[ks][ot][0][e] = hi;
             part[ks][ot][1][e] = lo;
           }
+      decay_state();
 #pragma unroll
       for (int c0 = 0; c0 < CT; c0 += 4) {
         f32x4 own[4][OT];  // at their scale
@@ -713,7 +726,7 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
           for (int ot = 0; ot < OT; ++ot)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              H[c0 + i][ot][r] = fmaf(own[i][ot][r], sc[ot].from, fmaf(d, H[c0 + i][ot][r], H[c0 + i][ot][r]));
+              H[c0 + i][ot][r] = fmaf(own[i][ot][r], sc[ot].from, H[c0 + i][ot][r]);
       }
     }
     have = true;
@@ -844,8 +857,12 @@ __global__ void __launch_bounds__(256) lin_pass_kernel(LinParams p) {
   const LinSeq q = lin_seq(p, s);
   const int first = q.first / p.span, n = (q.first + q.chunks - 1) / p.span - first + 1;
   if (n < 2) return;
-  float d = lin_power_m1(p.log_decay[h], ((first + 1) * p.span - q.first) * kC);
-  const float whole = lin_power_m1(p.log_decay[h], p.span * kC);
+  const float g = p.log_decay[h];
+  const int rows = ((first + 1) * p.span - q.first) * kC;  // of the first piece
+  float d = lin_decay(g, rows);
+  bool slow = lin_slow(g, rows);
+  const float whole = lin_decay(g, p.span * kC);
+  const bool slow_whole = lin_slow(g, p.span * kC);
   const float* init;
   float* fin;
   lin_states(p, w, s, h, init, fin);
@@ -870,8 +887,9 @@ __global__ void __launch_bounds__(256) lin_pass_kernel(LinParams p) {
       if (c + k < n) *reinterpret_cast<f32x4*>((c + k ? enter : own) + (c + k) * step) = E;
       if (c + k < n - 1) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) E[r] = fmaf(d, E[r], E[r]) + S[k][r];
+        for (int r = 0; r < 4; ++r) E[r] = fmaf(d, E[r], slow ? E[r] : 0.0f) + S[k][r];
         d = whole;
+        slow = slow_whole;
       }
     }
   }
@@ -924,13 +942,14 @@ __global__ void __launch_bounds__(256) lin_step_kernel(LinStepParams p) {
     k[e] = load_io<IO>(p.k, r * p.k_stride + kvh * DK + 4 * l + e);
     q[e] = load_io<IO>(p.q, r * p.q_stride + h * DK + 4 * l + e);
   }
-  const float d = lin_power_m1(p.log_decay[h], 1);
+  const float d = lin_decay(p.log_decay[h], 1);
+  const bool slow = lin_slow(p.log_decay[h], 1);
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     float y = 0.0f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float s = fmaf(v[j], k[e], fmaf(d, st[j][e], st[j][e]));
+      const float s = fmaf(v[j], k[e], fmaf(d, st[j][e], slow ? st[j][e] : 0.0f));
       st[j][e] = s;
       y = fmaf(s, q[e], y);
     }
