@@ -930,11 +930,13 @@ def _heads16(t, name):
     return t.dtype
 
 
-def _flat(t, name, keep):
-    """(B * L, heads, d) of a (B, L, heads, d) tensor: the same memory where its rows lie evenly, else a copy, which
-    goes into keep."""
+def _flat(t, name, rows, keep):
+    """(B * L, heads, d) of a (B, L, heads, d) tensor, rows being (B, L): the same memory where its rows lie evenly, else a
+    copy, which goes into keep."""
     if not isinstance(t, torch.Tensor) or t.dim() != 4:
         raise ValueError("%s must be a (B, L, heads, d) tensor" % name)
+    if t.shape[:2] != rows:
+        raise ValueError("%s must have %d rows of %d tokens, got %s" % (name, *rows, tuple(t.shape)))
     t = t.flatten(0, 1)
     keep.append(t)
     return t
@@ -969,8 +971,8 @@ def linattn_fwd(q, k, v, log_decay, scale=None, cu_seqlens=None, h0=None, return
     B, L, Hn, dk = q.shape
     dv = v.shape[-1]
     S = B if cu_seqlens is None else cu_seqlens.numel() - 1
-    pr, wsz, at = _linattn(_flat(q, "q", keep), _flat(k, "k", keep), _flat(v, "v", keep), log_decay, cu_seqlens, scale,
-                           S, 0, "ss_linattn_workspace_size", keep)
+    pr, wsz, at = _linattn(*(_flat(t, n, (B, L), keep) for t, n in ((q, "q"), (k, "k"), (v, "v"))), log_decay, cu_seqlens,
+                           scale, S, 0, "ss_linattn_workspace_size", keep)
     if y is None:
         y = q.new_empty((B, L, Hn, dv))
     fin = q.new_empty((S, Hn, dv, dk), dtype=f32) if return_final_state else None
@@ -995,8 +997,8 @@ def linattn_bwd(q, k, v, log_decay, dy, scale=None, cu_seqlens=None, h0=None, df
     dv = v.shape[-1]
     S = B if cu_seqlens is None else cu_seqlens.numel() - 1
     st = (S, Hn, dv, dk)
-    pr, wsz, at = _linattn(_flat(q, "q", keep), _flat(k, "k", keep), _flat(v, "v", keep), log_decay, cu_seqlens, scale,
-                           S, 0, "ss_linattn_bwd_workspace_size", keep)
+    pr, wsz, at = _linattn(*(_flat(t, n, (B, L), keep) for t, n in ((q, "q"), (k, "k"), (v, "v"))), log_decay, cu_seqlens,
+                           scale, S, 0, "ss_linattn_bwd_workspace_size", keep)
     g = {"dq": q.new_empty(q.shape), "dk": k.new_empty(k.shape), "dv": v.new_empty(v.shape)}
     if want_dh0:
         g["dh0"] = q.new_empty(st, dtype=f32)
