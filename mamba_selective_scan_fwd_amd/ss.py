@@ -1132,19 +1132,20 @@ def pack_requests(new_tokens, slots, seen, tokens):
     Returns a dict of int32 tensors: rows, taken (R,): a request's first row (-1: none) and its rows; step_slots
     (R,): for ssd_step and linattn_step on the batch's first rows; cu_seqlens (R + 1,), prompt_slots and
     has_state (R,): for conv1d_prompt, ssd_prompt and linattn_prompt; row_request, row_position (tokens,): a
-    row's request and its token's position (-1 behind the last row)."""
+    row's request and its token's position (-1 behind the last row).  They lie in one allocation, which lives as long
+    as one of them; a change of one in place is none of another."""
     lib = load_library()
     dev, keep, i32 = _device(new_tokens), [], torch.int32
     R = new_tokens.numel()
     at = [_in(t, i32, name, (R,), dev, keep)
           for t, name in ((new_tokens, "new_tokens"), (slots, "slots"), (seen, "seen"))]
-    # one allocation, every output on a 16-byte boundary
+    # one allocation, every output on a 16-byte boundary; split so that each counts its own changes
     r, t = R + 3 & -4, tokens + 3 & -4
     buf = new_tokens.new_empty(5 * r + 2 * t + R + 1)
     if r == R and t == tokens:
-        parts = buf.split_with_sizes([R] * 5 + [tokens] * 2 + [R + 1])
+        parts = buf.unsafe_split_with_sizes([R] * 5 + [tokens] * 2 + [R + 1])
     else:
-        parts = buf.split_with_sizes([R, r - R] * 5 + [tokens, t - tokens] * 2 + [R + 1])[::2]
+        parts = buf.unsafe_split_with_sizes([R, r - R] * 5 + [tokens, t - tokens] * 2 + [R + 1])[::2]
     to = buf.data_ptr()
     _launch(dev, lib.ss_pack_requests, R, tokens, *at, to, to + 4 * r, to + 8 * r, to + 20 * r + 8 * t, to + 12 * r,
             to + 16 * r, to + 20 * r, to + 20 * r + 4 * t)
