@@ -585,9 +585,12 @@ ss_status ss_ssd_step(const ss_ssd_step_problem *p, const void *xbc, const void 
  * The workspace is needed where sequences are walked in pieces, because they are too
  * few to fill the GPU or to fill its last round: per piece, two states of every head (the
  * backward's: six), and in the backward, where heads share keys and values, their
- * parts of dk and dv in fp32.  Its size goes by sizes alone (0: none is needed, NULL);
- * its contents on entry do not matter, and calls that share one must be ordered by the
- * caller.
+ * parts of dk and dv in fp32.  Its size goes by sizes alone (0: none is needed, NULL,
+ * or the problem is one that the call refuses); its contents on entry do not matter, and
+ * calls that share one must be ordered by the caller.
+ * tokens <= 2^30, nseqs <= 2^20 and nseqs * nheads * dk * dv (the backward: three times
+ * that, and where heads share keys and values tokens * kv_heads * (dk + dv)) at most
+ * 2^33 - 2^10.
  */
 typedef struct ss_linattn_problem {
     int64_t tokens;       /* rows of q, k, v and y */

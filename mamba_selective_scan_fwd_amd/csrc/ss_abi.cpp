@@ -929,11 +929,11 @@ ss_status plan_linattn(const ss_linattn_problem* p, int jobs, LinPlan* plan) {
   LinPlan l{};
   if (p->nseqs * walks * (p->dk * p->dv / 1024) > kMaxGrid) return SS_ERR_BAD_SHAPE;
   l.cut = ss::lin_cut(p->packed != 0, p->tokens, p->nseqs, longest, walks, 256);
-  if (jobs > 1 && p->tokens * p->nheads > kMaxGrid * 8) return SS_ERR_BAD_SHAPE;  // the shared heads' sums
+  const bool sums = jobs > 1 && p->kv_heads != p->nheads;  // over the heads that share keys and values, 1024 channels a workgroup
+  if (sums && p->tokens * p->kv_heads * ((p->dk + p->dv) / 64) > kMaxGrid * 16) return SS_ERR_BAD_SHAPE;
   l.states = align256((size_t)(2 * l.cut.pieces * l.cut.stride) * (size_t)(p->dk * p->dv) * 4);
   l.parts = l.states;
-  l.total = l.parts + (jobs > 1 && p->kv_heads != p->nheads
-                           ? align256((size_t)(p->tokens * p->nheads) * (size_t)(p->dk + p->dv) * 4) : 0);
+  l.total = l.parts + (sums ? align256((size_t)(p->tokens * p->nheads) * (size_t)(p->dk + p->dv) * 4) : 0);
   *plan = l;
   return SS_OK;
 }
