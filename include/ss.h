@@ -588,9 +588,9 @@ ss_status ss_ssd_step(const ss_ssd_step_problem *p, const void *xbc, const void 
  * parts of dk and dv in fp32.  Its size goes by sizes alone (0: none is needed, NULL,
  * or the problem is one that the call refuses); its contents on entry do not matter, and
  * calls that share one must be ordered by the caller.
- * tokens <= 2^30, nseqs <= 2^20 and nseqs * nheads * dk * dv (the backward: three times
- * that, and where heads share keys and values tokens * kv_heads * (dk + dv)) at most
- * 2^33 - 2^10.
+ * tokens <= 2^30 and nseqs <= 2^20; nseqs * nheads (the backward: three times that) at
+ * most 2^23 - 1, but for packed sequences that are walked in pieces; the backward's
+ * tokens * kv_heads * (dk + dv) at most 2^33 - 2^10 where heads share keys and values.
  */
 typedef struct ss_linattn_problem {
     int64_t tokens;       /* rows of q, k, v and y */

@@ -927,8 +927,9 @@ ss_status plan_linattn(const ss_linattn_problem* p, int jobs, LinPlan* plan) {
   if (p->q_stride % 8 || p->k_stride % 8 || p->v_stride % 8) return SS_ERR_MISALIGNED;
   const int64_t longest = p->packed ? p->tokens : p->tokens / p->nseqs, walks = p->nheads * jobs;
   LinPlan l{};
-  if (p->nseqs * walks * (p->dk * p->dv / 1024) > kMaxGrid) return SS_ERR_BAD_SHAPE;
   l.cut = ss::lin_cut(p->packed != 0, p->tokens, p->nseqs, longest, walks, 256);
+  // pieces of packed sequences are few, whatever the sequences
+  if (!(p->packed && l.cut.pieces) && p->nseqs * walks > kMaxGrid) return SS_ERR_BAD_SHAPE;
   const bool sums = jobs > 1 && p->kv_heads != p->nheads;  // over the heads that share keys and values, 1024 channels a workgroup
   if (sums && p->tokens * p->kv_heads * ((p->dk + p->dv) / 64) > kMaxGrid * 16) return SS_ERR_BAD_SHAPE;
   l.states = align256((size_t)(2 * l.cut.pieces * l.cut.stride) * (size_t)(p->dk * p->dv) * 4);

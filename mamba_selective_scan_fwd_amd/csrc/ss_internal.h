@@ -324,11 +324,12 @@ struct LinParams {
   int32_t split;             // this launch computes the pieces' own states
   // (2, pieces, stride, dk * dv).  First a piece's own state, of its last sequence's rows, if
   // that goes on behind it; then the state that enters that sequence, if it begins there.
-  // Second the state that enters a piece in which a sequence goes on.
+  // Second the state that enters a piece in which a sequence goes on; no sequence goes on in the
+  // first piece, whose place has what the launches share of packed sequences' places.
   float* ws;
   int32_t tokens, nseqs, nslots, heads, share;  // share: heads to a key and value
   int32_t whole;             // walks (sequence, head, job) that run whole, the first ones
-  int32_t span;              // chunks of 64 rows to a piece of the others
+  int32_t span;              // chunks of 64 rows to a piece of the others, of packed sequences at the most
   int32_t pieces;            // of each of the others; of all packed sequences together
   int32_t stride;            // the others; heads * jobs where the sequences are packed
 };

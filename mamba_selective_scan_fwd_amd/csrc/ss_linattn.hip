@@ -75,20 +75,68 @@ __device__ __forceinline__ u32x4v read_time_frag(uint32_t at, uint32_t next) {
 struct LinSeq {
   int begin, len, first, chunks;
 };
-__device__ __forceinline__ LinSeq lin_seq(const LinParams& p, int s) {
+__device__ __forceinline__ LinSeq lin_seq_of(int s, int begin, int end) {  // a packed one
   LinSeq q;
-  if (p.cu) {
-    q.begin = uniform(seq_row(p.cu, s, p.tokens));
-    const int end = uniform(seq_row(p.cu, s + 1, p.tokens));
-    q.len = end > q.begin ? end - q.begin : 0;
-    q.first = q.begin / kC + s;
-  } else {
-    q.len = p.tokens / p.nseqs;
-    q.begin = s * q.len;
-    q.first = 0;
-  }
+  q.begin = uniform(begin);
+  end = uniform(end);
+  q.len = end > q.begin ? end - q.begin : 0;
+  q.first = q.begin / kC + s;
   q.chunks = q.len > 0 ? (q.len + kC - 1) / kC : 1;
   return q;
+}
+__device__ __forceinline__ LinSeq lin_seq(const LinParams& p, int s) {
+  if (p.cu) return lin_seq_of(s, seq_row(p.cu, s, p.tokens), seq_row(p.cu, s + 1, p.tokens));
+  const int len = p.tokens / p.nseqs;
+  return {s * len, len, 0, (len + kC - 1) / kC};
+}
+// What pieces of packed sequences share out: the places from the first row's on, of the sequences up to
+// the last row, as many to each piece as these take.  (The empty ones behind the last row, which a batch's
+// maps have for every request without a prompt, would leave most pieces without a row.)  The launch for
+// the states between pieces finds them and leaves them in the workspace, in the place of the state that
+// would enter the first piece, for the launches behind it.
+struct LinPlaces {
+  int seqs;  // sequences before the empty ones behind the last row
+  int base;  // the first place
+  int span;  // places of a piece
+  int row;   // of up to 64 sequences: the lane's first row
+};
+__device__ __forceinline__ LinPlaces lin_places(const LinParams& p) {
+  const int lane = threadIdx.x % 64;
+  // a search for the first one that begins at the end, as find_chunk's, its first probes loaded with the ends
+  int lo = 0, n = p.nseqs;
+  auto probe = [&](int step) { return lane * step < n ? seq_row(p.cu, lo + lane * step, p.tokens) : 0x7fffffff; };
+  int step = (n + 63) >> 6, row = probe(step);
+  const int rows = row;
+  const int first = seq_row(p.cu, 0, p.tokens), last = seq_row(p.cu, p.nseqs, p.tokens);
+  const int base = uniform(first) / kC, end = uniform(last);
+  for (;;) {
+    const int cnt = (int)__builtin_popcountll(__builtin_amdgcn_ballot_w64(row < end));  // <= ceil(n / step): lo stays inside
+    if (cnt == 0) break;
+    lo += (cnt - 1) * step + 1;
+    n -= (cnt - 1) * step + 1;
+    n = n < step - 1 ? n : step - 1;
+    if (n <= 0) break;
+    step = (n + 63) >> 6;
+    row = probe(step);
+  }
+  // never more than span was planned for: end / kC + lo <= tokens / kC + nseqs
+  const int used = end / kC + lo - base, span = (used + p.pieces - 1) / p.pieces;
+  return {lo, base, span > 2 ? span : 2, rows};
+}
+__device__ __forceinline__ int32_t* lin_places_at(const LinParams& p) {
+  return reinterpret_cast<int32_t*>(p.ws + (int64_t)p.pieces * p.stride * (p.job[0].dc * p.job[0].dout));
+}
+__device__ __forceinline__ LinPlaces lin_places_found(const LinParams& p) {
+  const int lane = threadIdx.x % 64;
+  const int32_t* at = lin_places_at(p);
+  const int seqs = at[0], base = at[1], span = at[2], row = lane < p.nseqs ? seq_row(p.cu, lane, p.tokens) : 0;
+  return {uniform(seqs), uniform(base), uniform(span), row};
+}
+__device__ __forceinline__ int lin_find(const LinParams& p, const LinPlaces& pl, int place) {  // as find_chunk
+  if (p.nseqs > 64) return find_chunk<6>(p.cu, pl.seqs, p.tokens, place).seq;
+  const int lane = threadIdx.x % 64;
+  const int cnt = (int)__builtin_popcountll(__builtin_amdgcn_ballot_w64(lane < pl.seqs && pl.row / kC + lane <= place));
+  return cnt < 1 ? 0 : cnt - 1;
 }
 // Some of a sequence's chunks, in the walk's order
 struct LinRows {
@@ -114,6 +162,15 @@ __device__ __forceinline__ void lin_states(const LinParams& p, const LinWalk& w,
   init = i >= 0 && carried && w.init ? w.init + at : nullptr;
   fin = i >= 0 && w.fin ? w.fin + at : nullptr;
 }
+// A sequence without rows: its first state is its last one
+__device__ __forceinline__ void lin_empty(const LinParams& p, const LinWalk& w, int seq, int h) {
+  const float* init;
+  float* fin;
+  lin_states(p, w, seq, h, init, fin);
+  if (!fin || fin == init) return;
+  for (int i = (int)threadIdx.x; i < w.dc * w.dout / 4; i += (int)blockDim.x)
+    reinterpret_cast<f32x4*>(fin)[i] = init ? reinterpret_cast<const f32x4*>(init)[i] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+}
 // element (c, o) of a state in memory: (dv, dk), c being the side that is contracted with a
 __device__ __forceinline__ int state_at(const LinWalk& w, int c, int o) { return w.c_inner ? o * w.dc + c : c * w.dout + o; }
 
@@ -126,21 +183,18 @@ __device__ __forceinline__ float lin_power(float g, int n) {
   const double whole = rint(x);
   return ldexpf(exp2_hw((float)(x - whole)), (int)whole);
 }
-// What H <- exp(n g) H multiplies with.  A slow decay's own rounding would add up over the
-// chunks that it takes, so there it is exp(n g) - 1, and H <- H + (exp(n g) - 1) H; a fast one's
-// difference from 1 would leave a rounding of the old H where only exp(n g) H is left.
-__device__ __forceinline__ bool lin_slow(float g, int n) {
-  const double x = (double)n * (double)g;
-  return n == 0 || (x > -0.25 && x < 0.25);
-}
+// H <- exp(n g) H.  A slow decay's own rounding would add up over the chunks that it takes: there the
+// factor is exp(n g) - 1, and H <- H + (exp(n g) - 1) H.  That of a fast one would leave a rounding of the
+// old H, where only exp(n g) H is left: there it is exp(n g).  The sign bit tells them apart.
 __device__ __forceinline__ float lin_decay(float g, int n) {
-  if (!lin_slow(g, n)) return lin_power(g, n);
   const double x = n ? (double)n * (double)g : 0.0;
+  if (!(x > -0.25 && x <= 0.0)) return lin_power(g, n);
   double s = 1.0;  // the power series: 0.25^12 / 13! is below 2^-56
 #pragma unroll
   for (int k = 12; k > 1; --k) s = fma(s, x * (1.0 / k), 1.0);
-  return (float)(s * x);
+  return -fabsf((float)(s * x));
 }
+__device__ __forceinline__ bool lin_slow(float decay) { return __float_as_int(decay) < 0; }
 
 // ---- the walk ----------------------------------------------------------------------
 // Four waves, each with a quarter of the columns o of the outputs and of the state, the
@@ -345,11 +399,9 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
   auto load_c = [&](int t, int turn) {
     lc.load(lds.c[turn], chunk_at(w.c, t, w.c_stride, w.c_kv ? kvh : h, DO), w.c_stride, chunk_rows(t), rev, wave, lane);
   };
-  if (q.rows > 0) {
-    load_b(0, 0);
-    if constexpr (STATE) load_c(0, 0);
-    else load_a(0);
-  }
+  load_b(0, 0);
+  if constexpr (STATE) load_c(0, 0);
+  else load_a(0);
 
   const float g = p.log_decay[h];
   const int later = rev ? 0 : 1;  // the entering state decays before its first row, or behind the last
@@ -359,7 +411,6 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
   set_weights(chunk_rows(0));
   if (tid >= 64 && tid < 64 + kC + 2) *lds.weight(kPowers + tid - 64) = lin_power(g, tid - 64);
   if (tid >= 192 && tid < 194) *lds.weight(kDecays + tid - 192) = lin_decay(g, tid == 192 ? kC : q.rows % kC);
-  const bool slow_whole = uniform(lin_slow(g, kC)), slow_last = uniform(lin_slow(g, q.rows % kC));
   if constexpr (!STATE) {  // M's 16 x 16 tiles above the diagonal that are read with their neighbours
     if (tid < 128) {
       const int tile = tid / 32 % 2, row = tid / 2 % 16;
@@ -620,8 +671,6 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
     }
     // ---- H <- a^rows H + sum_s a^{rows-1-s} b_s c_s^T
     if (!STATE && !more && !(q.last && fin)) return false;  // nobody takes it
-    const float d = __int_as_float(uniform(__float_as_int(*lds.weight(kDecays + (rows < kC ? 1 : 0)))));
-    const bool slow = rows < kC ? slow_last : slow_whole;
     const uint32_t even = opaque(time_dc) + at_b + turn * kTile, odd = (opaque(time_dc) ^ 32u) + at_b + turn * kTile;
     auto b_frag = [&](int ks, int ct) {
       const uint32_t at = 32 * ks * (DC * 2) + 256 * (ct / 2);
@@ -633,8 +682,9 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
       v0 = low16<IO>(cf[ks][ot][e]) * u[0];
       v1 = high16<IO>(cf[ks][ot][e]) * u[1];
     };
+    const float d = __int_as_float(uniform(__float_as_int(*lds.weight(kDecays + (rows < kC ? 1 : 0)))));
     auto decay_state = [&]() {
-      if (slow) {
+      if (lin_slow(d)) {
         each([&](int ct, int ot) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) H[ct][ot][r] = fmaf(d, H[ct][ot][r], H[ct][ot][r]);
@@ -735,9 +785,8 @@ __device__ __forceinline__ void walk(const LinParams& p, WalkLds<DC, DO, STATE>&
     if (more) lds_barrier<STATE ? 0 : 4>();
     return more;
   };
-  if (q.rows > 0)
-    for (int t = 0; chunk(t, std::integral_constant<int, 0>{}) && chunk(t + kC, std::integral_constant<int, 1>{}); t += 2 * kC) {
-    }
+  for (int t = 0; chunk(t, std::integral_constant<int, 0>{}) && chunk(t + kC, std::integral_constant<int, 1>{}); t += 2 * kC) {
+  }
   if constexpr (STATE) {
     each([&](int ct, int ot) { *reinterpret_cast<f32x4*>(ws + (ct * OT + ot) * 256) = H[ct][ot]; });
   } else if (q.last && fin && w.c_inner) {
@@ -781,17 +830,23 @@ __device__ __forceinline__ LinWork lin_work(const LinParams& p) {
 }
 template <int IO, int DC, int DO, bool STATE, bool FULL>
 __device__ __forceinline__ void walk_piece(const LinParams& p, WalkLds<DC, DO, STATE>& lds, const LinWork& k) {
-  const int c0 = k.piece * p.span, c1 = c0 + p.span;
+  const bool over = k.piece >= 0 && p.cu;
+  const LinPlaces pl = !over ? LinPlaces{p.nseqs, 0, p.span, 0} : STATE ? lin_places(p) : lin_places_found(p);
+  const int c0 = pl.base + k.piece * pl.span, c1 = c0 + pl.span;
   if constexpr (STATE) {
     int s = k.seq;
-    if (p.cu) s = find_chunk<6>(p.cu, p.nseqs, p.tokens, c1 - 1).seq;
+    if (over) {
+      if (k.slot == 0 && threadIdx.x < 3) lin_places_at(p)[threadIdx.x] = threadIdx.x == 0 ? pl.seqs : threadIdx.x == 1 ? pl.base : pl.span;
+      if (pl.seqs == 0) return;
+      s = lin_find(p, pl, c1 - 1);
+    }
     const LinSeq q = lin_seq(p, s);
     const int i0 = c0 > q.first ? c0 - q.first : 0, i1 = c1 - q.first;
     if (i1 <= i0 || i1 >= q.chunks) return;
     walk<IO, DC, DO, STATE, FULL>(p, lds, k.job, k.h, lin_rows(q, s, i0, i1, k.slot));
   } else {
+    const LinWalk& w = p.job[k.job];
     if (p.zero_rest && p.cu) {  // rows of no sequence have outputs of zero
-      const LinWalk& w = p.job[k.job];
       const int lead = seq_row(p.cu, 0, p.tokens), behind = seq_row(p.cu, p.nseqs, p.tokens);
       const int end = behind > lead ? behind : lead, tid = threadIdx.x;
       for (int r = k.piece < 0 ? k.seq : k.piece; r < lead + p.tokens - end; r += k.piece < 0 ? p.nseqs : p.pieces) {
@@ -802,10 +857,19 @@ __device__ __forceinline__ void walk_piece(const LinParams& p, WalkLds<DC, DO, S
         }
       }
     }
-    // no more sequences than places, whatever the offsets hold
-    const bool over = k.piece >= 0 && p.cu;
-    int s = over ? find_chunk<6>(p.cu, p.nseqs, p.tokens, c0).seq : k.seq;
-    const int end = over ? (p.span < p.nseqs - s ? s + p.span : p.nseqs) : s + 1;
+    int s = k.seq, end = s + 1;
+    if (over) {
+      // the empty sequences behind the last row, 64 at a time: those whose state is to be written
+      for (int s0 = pl.seqs + 64 * k.piece; w.fin && s0 < p.nseqs; s0 += 64 * p.pieces) {
+        const int e = s0 + (int)threadIdx.x % 64;
+        const bool writes = e < p.nseqs && (!p.pool || (slot_of(p.slots, e, p.nslots) >= 0 && !(p.has_state && p.has_state[e])));
+        for (uint64_t left = __builtin_amdgcn_ballot_w64(writes); left; left &= left - 1)
+          lin_empty(p, w, s0 + (int)__builtin_ctzll(left), k.h);
+      }
+      if (pl.seqs == 0) return;
+      s = lin_find(p, pl, c0);
+      end = pl.span < pl.seqs - s ? s + pl.span : pl.seqs;  // no more sequences than places, whatever the offsets hold
+    }
     for (; s < end; ++s) {
       const LinSeq q = lin_seq(p, s);
       int i0 = 0, i1 = q.chunks;
@@ -814,6 +878,10 @@ __device__ __forceinline__ void walk_piece(const LinParams& p, WalkLds<DC, DO, S
         i0 = c0 > q.first ? c0 - q.first : 0;
         i1 = i1 < c1 - q.first ? i1 : c1 - q.first;
         if (i0 >= i1) continue;
+      }
+      if (q.len == 0) {
+        lin_empty(p, w, s, k.h);
+        continue;
       }
       lds_barrier<-1>();  // everyone is done with the sequence before
       walk<IO, DC, DO, STATE, FULL>(p, lds, k.job, k.h, lin_rows(q, s, i0, i1, k.slot));
@@ -839,8 +907,9 @@ __global__ void __launch_bounds__(kWalkThreads, 2) lin_walks_kernel(LinParams p)
 }
 
 // ---- the states between the pieces of a sequence ------------------------------------
-// Workgroup = (sequence of several pieces, head, walk, 1024 elements): E <- the
-// sequence's first state; per piece, E to the workspace and E <- decay E + S, S being
+// Workgroup = (sequence of several pieces, head, walk, 1024 elements), a packed one found
+// among the sequences or, where these are more, as the one that crosses the end of its
+// first piece: E <- the sequence's first state; per piece, E to the workspace and E <- decay E + S, S being
 // the state of the sequence's rows in the piece (the last one has none: its walk ends
 // with the sequence's).  The first state goes through the workspace too, so that a
 // walk's end may overwrite it in the pool while others begin.  Bound by memory: the layer's 57
@@ -851,18 +920,35 @@ __global__ void __launch_bounds__(256) lin_pass_kernel(LinParams p) {
   int i = (int)blockIdx.x;
   const int e4 = i % parts * 256 + (int)threadIdx.x;
   i /= parts;
-  i += p.whole;
-  const int job = i % p.jobs, h = i / p.jobs % p.heads, s = i / p.jobs / p.heads;
+  const int slot = i % p.stride, u = p.whole + slot, job = u % p.jobs, h = u / p.jobs % p.heads;
   const LinWalk& w = p.job[job];
-  const LinSeq q = lin_seq(p, s);
-  const int first = q.first / p.span, n = (q.first + q.chunks - 1) / p.span - first + 1;
+  int s = p.cu ? i / p.stride : u / p.jobs / p.heads, span = p.span;
+  LinSeq q;
+  if (p.cu) {
+    const int begin = seq_row(p.cu, s, p.tokens), next = seq_row(p.cu, s + 1, p.tokens);  // loaded with the places'
+    const LinPlaces pl = lin_places_found(p);
+    if (pl.seqs == 0) return;
+    span = pl.span;
+    q = lin_seq_of(s, begin, next);
+    const int ends = (s + 1) * span;  // of piece s
+    const bool by_end = p.nseqs >= p.pieces;
+    if (by_end) {
+      s = lin_find(p, pl, pl.base + ends);
+      q = lin_seq(p, s);
+    }
+    q.first -= pl.base;
+    if (q.first < 0 || (by_end && (q.first >= ends || q.first < ends - span))) return;
+  } else {
+    q = lin_seq(p, s);
+  }
+  // offsets out of order may name places behind the last piece
+  const int first = q.first / span, end = (q.first + q.chunks - 1) / span + 1;
+  const int n = (end < p.pieces ? end : p.pieces) - first;
   if (n < 2) return;
   const float g = p.log_decay[h];
-  const int rows = ((first + 1) * p.span - q.first) * kC;  // of the first piece
+  const int rows = ((first + 1) * span - q.first) * kC;  // of the first piece
   float d = lin_decay(g, rows);
-  bool slow = lin_slow(g, rows);
-  const float whole = lin_decay(g, p.span * kC);
-  const bool slow_whole = lin_slow(g, p.span * kC);
+  const float whole = lin_decay(g, span * kC);
   const float* init;
   float* fin;
   lin_states(p, w, s, h, init, fin);
@@ -875,7 +961,7 @@ __global__ void __launch_bounds__(256) lin_pass_kernel(LinParams p) {
       E[r] = init[state_at(w, 16 * ct + 4 * (lane / 16) + r, 16 * (ot_n * wave + ot) + lane % 16)];
   }
   const int64_t step = (int64_t)p.stride * size;
-  float* own = p.ws + ((int64_t)first * p.stride + (p.cu ? h * p.jobs + job : i - p.whole)) * size + 4 * (int64_t)e4;
+  float* own = p.ws + ((int64_t)first * p.stride + slot) * size + 4 * (int64_t)e4;
   float* enter = own + p.pieces * step;
   f32x4 S[kAhead];
   for (int c = 0; c < n; c += kAhead) {
@@ -887,9 +973,8 @@ __global__ void __launch_bounds__(256) lin_pass_kernel(LinParams p) {
       if (c + k < n) *reinterpret_cast<f32x4*>((c + k ? enter : own) + (c + k) * step) = E;
       if (c + k < n - 1) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) E[r] = fmaf(d, E[r], slow ? E[r] : 0.0f) + S[k][r];
+        for (int r = 0; r < 4; ++r) E[r] = fmaf(d, E[r], lin_slow(d) ? E[r] : 0.0f) + S[k][r];
         d = whole;
-        slow = slow_whole;
       }
     }
   }
@@ -943,13 +1028,12 @@ __global__ void __launch_bounds__(256) lin_step_kernel(LinStepParams p) {
     q[e] = load_io<IO>(p.q, r * p.q_stride + h * DK + 4 * l + e);
   }
   const float d = lin_decay(p.log_decay[h], 1);
-  const bool slow = lin_slow(p.log_decay[h], 1);
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     float y = 0.0f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float s = fmaf(v[j], k[e], fmaf(d, st[j][e], slow ? st[j][e] : 0.0f));
+      const float s = fmaf(v[j], k[e], fmaf(d, st[j][e], lin_slow(d) ? st[j][e] : 0.0f));
       st[j][e] = s;
       y = fmaf(s, q[e], y);
     }
@@ -1001,8 +1085,8 @@ hipError_t launch_linattn_io(LinParams p, hipStream_t st) {
     hipError_t e = launch_walks_io<IO>(p, st);
     if (e != hipSuccess) return e;
     const int parts = p.job[0].dc * p.job[0].dout / 1024;
-    const int walks = p.nseqs * p.heads * p.jobs - p.whole;
-    hipLaunchKernelGGL(lin_pass_kernel, dim3((uint32_t)(walks * parts)), dim3(256), 0, st, p);
+    const int seqs = !p.cu ? 1 : p.nseqs < p.pieces ? p.nseqs : p.pieces - 1;
+    hipLaunchKernelGGL(lin_pass_kernel, dim3((uint32_t)(seqs * p.stride * parts)), dim3(256), 0, st, p);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     p.split = 0;

@@ -37,3 +37,13 @@ def test_sums_over_shared_heads_have_a_limit():
     assert _codes(**kw, nheads=8, kv_heads=8) == (1, 1, 1)
     assert _codes(**kw, nheads=8, kv_heads=2) == (1, 1, 1)      # 2^24 * 2 * 48 threads, 3 * 2^21 workgroups
     assert _codes(**kw, nheads=8, kv_heads=4) == (1, 1, 2)
+
+
+def test_packed_sequences_in_pieces_have_no_limit_of_their_own():
+    """Pieces go by rows and places, however many sequences there are; whole walks are a workgroup each."""
+    kw = dict(tokens=65536, nheads=12, kv_heads=12, dk=128, dv=128, q_stride=4096, k_stride=4096, v_stride=4096)
+    assert _codes(**kw, nseqs=1 << 20) == (1, 1, 1)
+    whole = dict(kw, tokens=384)
+    assert _codes(**whole, nseqs=1 << 18) == (1, 1, 2)          # 12 and 36 walks of each
+    assert _codes(**whole, nseqs=1 << 20) == (2, 2, 2)
+    assert _codes(**dict(kw, tokens=1 << 20, packed=0), nseqs=1 << 20) == (2, 2, 2)
