@@ -571,13 +571,14 @@ ss_status ss_ssd_step(const ss_ssd_step_problem *p, const void *xbc, const void 
  * dk and dv are 64 or 128 each; strides are multiples of 8 and at most 2^21; every
  * pointer is 16-byte aligned.  States are kept in fp32, and computed operands
  * multiplied as sums of 16-bit parts: y and the gradients carry, before their rounding,
- * about 2^-17 of their terms, final states and dh0 nearly fp32's error.  With fp16 data
- * that holds of the terms of a chunk, and of the entering state's, down to 2^-15 of the
- * largest one of the same output channel; smaller ones have 2^-38 of that.  A value
- * that is not finite spreads to other rows of the same 64-row chunk of its sequence,
- * earlier ones among them, to the rows behind it (of dk and dv, whose walk goes from the
- * end: before it), and to no other sequence; one in v (k, q, dy) to no other channel
- * of y (dq, dk, dv) and of the state's same side.
+ * about 2^-17 of their terms, final states and dh0 nearly fp32's error (bf16 data's by
+ * one part more where they are asked for, which may change the last bit of y, or dv).
+ * With fp16 data that holds of the terms of a chunk, and of the entering state's, down to
+ * 2^-15 of the largest one of the same output channel; smaller ones have 2^-38 of that.
+ * A value that is not finite spreads to other rows of the same 64-row chunk of its
+ * sequence, earlier ones among them, to the rows behind it (of dk and dv, whose walk goes
+ * from the end: before it), and to no other sequence; one in v (k, q, dy) to no other
+ * channel of y (dq, dk, dv) and of the state's same side.
  * `packed` nonzero: the rows of sequence s are cu_seqlens[s] .. cu_seqlens[s+1]-1,
  * as declared with the serving calls above (a device array, clamped to
  * 0 .. tokens, sequences may be empty); zero: cu_seqlens is NULL, tokens is a

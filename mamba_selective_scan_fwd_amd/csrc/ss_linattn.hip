@@ -893,8 +893,9 @@ __global__ void __launch_bounds__(kWalkThreads, 2) lin_walk_kernel(LinParams p) 
   __shared__ WalkLds<DC, DO, STATE> lds;
   walk_piece<IO, DC, DO, STATE, FULL>(p, lds, lin_work<STATE>(p));
 }
-// The gradients' three walks where dv = DC and dk = DO differ: dq's and dk's have the states' sides
-// the one way, dv's the other; in one launch they run beside each other
+// The gradients' three walks where dv = DC and dk = DO differ, or where dh0 is asked for: dq's and
+// dk's have the states' sides the one way, dv's the other, and dh0 is what dv's ends with; in one
+// launch they run beside each other
 template <int IO, int DC, int DO, bool STATE, bool FULL>
 __global__ void __launch_bounds__(kWalkThreads, 2) lin_walks_kernel(LinParams p) {
   __shared__ union {
@@ -1051,7 +1052,7 @@ __global__ void __launch_bounds__(256) lin_step_kernel(LinStepParams p) {
 template <int IO, int DC, int DO, bool FULL>
 hipError_t launch_walk(const LinParams& p, hipStream_t st) {
   const dim3 grid((uint32_t)(p.split ? (p.pieces - 1) * p.stride : p.whole + p.pieces * p.stride)), threads(kWalkThreads);
-  if constexpr (DC != DO) {
+  if constexpr (DC != DO || FULL) {
     if (p.jobs == 3) {
       if (p.split) hipLaunchKernelGGL((lin_walks_kernel<IO, DC, DO, true, FULL>), grid, threads, 0, st, p);
       else hipLaunchKernelGGL((lin_walks_kernel<IO, DC, DO, false, FULL>), grid, threads, 0, st, p);
@@ -1064,7 +1065,9 @@ hipError_t launch_walk(const LinParams& p, hipStream_t st) {
 }
 // fp16's weighted rows are two parts (split2_f16).  Of bf16's, three keep fp32's error in the last states;
 // where no walk has any, its outputs are all that shows and two do (8 rows of 2048 tokens, 12 heads of
-// 128 x 128: 81 us against 90 with three, the gradients 172 against 194).
+// 128 x 128: 81 us against 90 with three, the gradients 172 against 194): a term is then off by 2^-18,
+// as the pairs' weights are.  Only the walk that leaves a state has three, so that dq and dk are the
+// same with and without dh0; the last bit of y (dv) may go by final_state (dh0).
 template <int IO, int DC, int DO>
 hipError_t launch_walk(const LinParams& p, hipStream_t st) {
   bool full = false;
