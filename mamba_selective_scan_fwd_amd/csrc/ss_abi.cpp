@@ -916,7 +916,7 @@ ss_status check_linattn_heads(const ss_linattn_problem* p) {
 }
 struct LinPlan {
   ss::LinCut cut;
-  size_t states, parts, total;  // bytes of the states between pieces, and where the shared heads' parts begin
+  size_t states, total;  // bytes of the states between pieces, behind which the shared heads' parts lie
 };
 // `jobs` walks of every head: one forward, three backward
 ss_status plan_linattn(const ss_linattn_problem* p, int jobs, LinPlan* plan) {
@@ -927,14 +927,13 @@ ss_status plan_linattn(const ss_linattn_problem* p, int jobs, LinPlan* plan) {
   if (p->q_stride % 8 || p->k_stride % 8 || p->v_stride % 8) return SS_ERR_MISALIGNED;
   const int64_t longest = p->packed ? p->tokens : p->tokens / p->nseqs, walks = p->nheads * jobs;
   LinPlan l{};
-  l.cut = ss::lin_cut(p->packed != 0, p->tokens, p->nseqs, longest, walks, 256);
+  l.cut = ss::lin_cut(p->packed != 0, p->tokens, p->nseqs, longest, walks, ss::kPlanCus);
   // pieces of packed sequences are few, whatever the sequences
   if (!(p->packed && l.cut.pieces) && p->nseqs * walks > kMaxGrid) return SS_ERR_BAD_SHAPE;
   const bool sums = jobs > 1 && p->kv_heads != p->nheads;  // over the heads that share keys and values, 1024 channels a workgroup
   if (sums && p->tokens * p->kv_heads * ((p->dk + p->dv) / 64) > kMaxGrid * 16) return SS_ERR_BAD_SHAPE;
   l.states = align256((size_t)(2 * l.cut.pieces * l.cut.stride) * (size_t)(p->dk * p->dv) * 4);
-  l.parts = l.states;
-  l.total = l.parts + (sums ? align256((size_t)(p->tokens * p->nheads) * (size_t)(p->dk + p->dv) * 4) : 0);
+  l.total = l.states + (sums ? align256((size_t)(p->tokens * p->nheads) * (size_t)(p->dk + p->dv) * 4) : 0);
   *plan = l;
   return SS_OK;
 }
@@ -1067,7 +1066,7 @@ ss_status ss_linattn_bwd(const ss_linattn_problem* p, const void* q, const void*
   k_.jobs = 3;
   const int64_t dys = p->nheads * p->dv;
   const bool shared = p->kv_heads != p->nheads;
-  float* parts = shared ? reinterpret_cast<float*>(static_cast<char*>(workspace) + l.parts) : nullptr;
+  float* parts = shared ? reinterpret_cast<float*>(static_cast<char*>(workspace) + l.states) : nullptr;
   ss::LinWalk& a = k_.job[0];  // dq
   a.a = dy; a.b = v; a.c = k;
   a.a_stride = dys; a.b_stride = p->v_stride; a.c_stride = p->k_stride;
@@ -1159,7 +1158,7 @@ void norm_layout(const ss_norm_problem* p, int vec, bool bwd, ss::NormParams* k)
   if (p->rows < k->row_lanes) k->row_lanes = (int)p->rows;
   k->threads = (k->row_lanes * k->block_groups * lanes + 63) / 64 * 64;
   k->blocks = (int)((p->ngroups + k->block_groups - 1) / k->block_groups);
-  const int64_t cus = 256, groups = bwd ? (k->threads <= 512 ? 2 * cus : cus) : cus * 4096 / k->threads;
+  const int64_t cus = ss::kPlanCus, groups = bwd ? (k->threads <= 512 ? 2 * cus : cus) : cus * 4096 / k->threads;
   const int64_t rows = (p->rows + k->row_lanes - 1) / k->row_lanes;
   const int64_t most = groups / k->blocks > 0 ? groups / k->blocks : 1;
   const int64_t steps = (rows + most - 1) / most;  // as many for each of them

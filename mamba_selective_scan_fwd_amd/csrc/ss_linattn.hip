@@ -343,9 +343,7 @@ struct TileLoad {
     lane_piece(wave, lane, row, piece);
     whole = (uint32_t)(rev ? kRows * kWaves - 1 - row : row) * (uint32_t)(stride * 2) + (uint32_t)piece * 16u;
   }
-  // loads k0 .. k1 - 1 of a chunk
-  __device__ __forceinline__ void load(char* tile, const char* at, int64_t stride, int rows, bool rev, int wave, int lane, int k0 = 0,
-                                       int k1 = kLoads) const {
+  __device__ __forceinline__ void load(char* tile, const char* at, int64_t stride, int rows, bool rev, int wave, int lane) const {
     const uint64_t base = (uint64_t)(uintptr_t)at;
     const u32x4v v = {(uint32_t)uniform((int)(uint32_t)base), (uint32_t)uniform((int)((base >> 32) & 0xffffu)),
                       (uint32_t)uniform((int)view_bytes(stride * 2, rows, W * 2)), (uint32_t)kRsrcWord3};
@@ -353,15 +351,13 @@ struct TileLoad {
     if (rows == kC) {
 #pragma unroll
       for (int k = 0; k < kLoads; ++k)
-        if (k >= k0 && k < k1)
-          lds_load(v, to + kWaves * 1024 * k, whole, (rev ? kLoads - 1 - k : k) * (kRows * kWaves) * (int)(stride * 2));
+        lds_load(v, to + kWaves * 1024 * k, whole, (rev ? kLoads - 1 - k : k) * (kRows * kWaves) * (int)(stride * 2));
       return;
     }
     int row, piece;
     lane_piece(wave, opaque(lane), row, piece);
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) {
-      if (k < k0 || k >= k1) continue;
       const int r = row + k * (kRows * kWaves), in = r < rows ? r : rows - 1;
       lds_load(v, to + kWaves * 1024 * k, (uint32_t)(rev ? rows - 1 - in : in) * (uint32_t)(stride * 2) + (uint32_t)piece * 16u, 0);
     }

@@ -1,11 +1,11 @@
 // ss_packed.h -- packed sequences (device side).  Internal to libss.so.
 //
 // cu holds nseqs + 1 row offsets; sequence s is rows cu[s] .. cu[s + 1] - 1.
-// A workgroup takes a chunk of Q rows counted from its sequence's first
+// A workgroup takes a chunk of 2^LOGQ rows counted from its sequence's first
 // row, so that no chunk holds two sequences.  Sequence s owns the chunk places
-// floor(cu[s] / Q) + s onwards: from one sequence to the next these grow by at
+// (cu[s] >> LOGQ) + s onwards: from one sequence to the next these grow by at
 // least the number of chunks of the first (floor(b / Q) - floor(a / Q) + 1 >=
-// ceil((b - a) / Q)), so places never collide, floor(tokens / Q) + nseqs places
+// ceil((b - a) / Q)), so places never collide, (tokens >> LOGQ) + nseqs places
 // hold every batch, and neither the host nor an extra kernel has to see the
 // lengths.  Places behind a sequence's last chunk stay empty.
 //
@@ -29,17 +29,16 @@ __device__ __forceinline__ int seq_row(const int32_t* cu, int i, int tokens) {
   return v < 0 ? 0 : v > tokens ? tokens : v;
 }
 
-// The sequence whose chunk place `place` is (uniform over the wave), number(r) being
-// floor(r / Q): a search with 64 probes a step, so up to 64 sequences take one
-// load, 4096 two.
-template <class Number>
-__device__ __forceinline__ SeqChunk find_chunk_by(const int32_t* cu, int nseqs, int tokens, int place, Number number) {
+// The sequence whose chunk place `place` is (uniform over the wave): a search
+// with 64 probes a step, so up to 64 sequences take one load, 4096 two.
+template <int LOGQ>
+__device__ __forceinline__ SeqChunk find_chunk(const int32_t* cu, int nseqs, int tokens, int place) {
   const int lane = threadIdx.x % 64;
   int lo = 0, n = nseqs;
   while (n > 1) {
     const int step = (n + 63) >> 6, k = lane * step;
     bool le = false;
-    if (k < n) le = number(seq_row(cu, lo + k, tokens)) + lo + k <= place;
+    if (k < n) le = (seq_row(cu, lo + k, tokens) >> LOGQ) + lo + k <= place;
     int cnt = (int)__builtin_popcountll(__builtin_amdgcn_ballot_w64(le));
     cnt = cnt < 1 ? 1 : cnt;  // cnt <= ceil(n / step): lo stays inside
     lo += (cnt - 1) * step;
@@ -51,12 +50,8 @@ __device__ __forceinline__ SeqChunk find_chunk_by(const int32_t* cu, int nseqs, 
   q.begin = uniform(seq_row(cu, q.seq, tokens));
   const int end = uniform(seq_row(cu, q.seq + 1, tokens));
   q.len = end > q.begin ? end - q.begin : 0;
-  q.chunk = place - (number(q.begin) + q.seq);
+  q.chunk = place - ((q.begin >> LOGQ) + q.seq);
   return q;
-}
-template <int LOGQ>
-__device__ __forceinline__ SeqChunk find_chunk(const int32_t* cu, int nseqs, int tokens, int place) {
-  return find_chunk_by(cu, nseqs, tokens, place, [](int row) { return row >> LOGQ; });
 }
 
 // the slot of sequence or row i, -1 for none (an index outside the pool is none)

@@ -7,6 +7,9 @@
 
 namespace ss {
 
+// The CUs of plans that sizes alone decide, workspaces among them: those of an MI355X
+constexpr int64_t kPlanCus = 256;
+
 // Heads per workgroup: of 1, 2 and 3 the one for which the workgroups' rounds
 // over 2 per CU take the least time, a workgroup's being its heads and two
 // heads' worth of its own (the weights, V, the first loads).  With 1, 2 and 3: 24
