@@ -671,7 +671,7 @@ ss_status ss_linattn_step(const ss_linattn_problem *p, const void *q, const void
  *   weight, bias : (channels) fp32, each may be NULL (1, 0); 16-byte aligned
  * Sums and norms are in fp32.  Data pointers are aligned to the element; groups of a
  * multiple of 4 (fp32) or 8 (16-bit) channels, in rows on 16-byte boundaries, run
- * fastest.  No output may overlap any other buffer (SS_ERR_UNSUPPORTED), nor may its
+ * fastest, 16-bit ones of 4 channels on 8-byte boundaries next.  No output may overlap any other buffer (SS_ERR_UNSUPPORTED), nor may its
  * range of strided rows meet another's.  rows <= 2^30, channels and strides <= 2^21.
  */
 typedef enum ss_norm_mode {
