@@ -1104,7 +1104,7 @@ ss_status ss_linattn_step(const ss_linattn_problem* p, const void* q, const void
   const ss_status s = check_linattn_heads(p);
   if (s != SS_OK) return s;
   if (p->tokens > kMaxSeqs || p->nslots < 1 || p->nslots > kMaxSlots) return SS_ERR_BAD_SHAPE;
-  if (p->tokens * p->nheads * (p->dk * p->dv / 1024) > kMaxGrid) return SS_ERR_BAD_SHAPE;
+  if (p->tokens * p->nheads * (p->dk * p->dv / 4096) > kMaxGrid) return SS_ERR_BAD_SHAPE;
   if (!q || !k || !v || !log_decay || !state || !y) return SS_ERR_NULL_ARG;
   const void* ptrs[] = {log_decay, slots, state, y};
   for (const void* a : ptrs)
@@ -1141,10 +1141,12 @@ ss_status check_norm(const ss_norm_problem* p) {
 }
 // Threads and workgroups.  A workgroup takes whole rows' groups where 1024 threads hold
 // them.  Forward: 256 threads or more, and twice as many workgroups as the GPU holds at
-// once (16384 rows of 1536 in bf16, 12 groups, a gate: 26.1 us; 28.9 with as many, 28.3 with
-// half).  Backward: up to 1024 threads, for a workgroup's rows end in one sum of dw and
-// db, and one workgroup a CU, or two of at most 512 threads (the same rows: 65.8 us;
-// 70.1 with two of 512 threads, 74.8 with four of 256, 78 with two of 1024).
+// once (16384 rows of 1536 in bf16, 12 groups, a gate: 26.1 us; 27.4 with as many, 26.3 with
+// half, 24.7 with four times; 4097 of 700 in fp32, 7 groups, 9.5 with any).  Backward: up to 1024
+// threads, for a workgroup's rows end in one sum of dw and db, and one workgroup a CU, or
+// two of at most 512 threads (the same rows: 55.2 us; 61.9 with two of 512 threads, 65.7 with
+// four of 256, 68.4 with two of 1024; the fp32 rows 18.0, 18.9, 23.4 and 22.1; 2048 rows
+// 20.9, 22.2, 30.3 and 29.3).
 constexpr int64_t kNormBwdGroups = 512;
 void norm_layout(const ss_norm_problem* p, int vec, bool bwd, ss::NormParams* k) {
   const int size = (int)(p->channels / p->ngroups), nvec = size / vec;

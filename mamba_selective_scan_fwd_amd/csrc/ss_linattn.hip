@@ -996,13 +996,15 @@ __global__ void __launch_bounds__(256) lin_share_kernel(LinParams p) {
 }
 
 // ---- one token of many requests -----------------------------------------------------
-// Workgroup = (row, head, J passes over 1024 / dk rows p of the state): dk / 4 lanes
+// Workgroup = (row, head, four passes over 1024 / dk rows p of the state): dk / 4 lanes
 // share a row of H, each with 4 consecutive n, so that a wave reads whole kilobytes;
 // all loads are issued before the first use.  Bound by HBM (201 rows of 16 heads, 128 x 64, 210 MB of
-// states in and out: 32 us, 6.5 TB/s with what the last level cache holds); one row 2.8 us.
-template <int IO, int DK, int J>
+// states in and out: 32 us, 6.5 TB/s with what the last level cache holds).  Four times as many
+// workgroups of one pass are not sooner with few rows either (16 heads of 128 x 128, other states
+// every time: one row 3.0 us against 3.2, 2 rows 3.6 and 3.6, 16 rows 10.6 and 10.1, 32 15.1 and 15.1).
+template <int IO, int DK>
 __global__ void __launch_bounds__(256) lin_step_kernel(LinStepParams p) {
-  constexpr int L = DK / 4, R = 256 / L;  // lanes of a state row, rows of a pass
+  constexpr int L = DK / 4, R = 256 / L, J = 4;  // lanes of a state row, rows of a pass, passes
   const int tid = threadIdx.x, l = tid % L;
   const int parts = p.dv / (R * J);
   const int part = (int)(blockIdx.x % (uint32_t)parts), i = (int)(blockIdx.x / (uint32_t)parts);
@@ -1097,20 +1099,12 @@ hipError_t launch_linattn_io(LinParams p, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int IO, int DK>
-hipError_t launch_step_dk(const LinStepParams& p, hipStream_t st) {
-  constexpr int R = 1024 / DK;
-  const int64_t rows = (int64_t)p.rows * p.heads;
-  // a thread's rows of the state: few where the workgroups would not fill the GPU
-  if (rows * (p.dv / (4 * R)) >= 4 * device_cus())
-    hipLaunchKernelGGL((lin_step_kernel<IO, DK, 4>), dim3((uint32_t)(rows * (p.dv / (4 * R)))), dim3(256), 0, st, p);
-  else
-    hipLaunchKernelGGL((lin_step_kernel<IO, DK, 1>), dim3((uint32_t)(rows * (p.dv / R))), dim3(256), 0, st, p);
-  return hipGetLastError();
-}
 template <int IO>
 hipError_t launch_linattn_step_io(const LinStepParams& p, hipStream_t st) {
-  return p.dk == 64 ? launch_step_dk<IO, 64>(p, st) : launch_step_dk<IO, 128>(p, st);
+  const dim3 grid((uint32_t)((int64_t)p.rows * p.heads * (p.dk * p.dv / 4096)));
+  if (p.dk == 64) hipLaunchKernelGGL((lin_step_kernel<IO, 64>), grid, dim3(256), 0, st, p);
+  else hipLaunchKernelGGL((lin_step_kernel<IO, 128>), grid, dim3(256), 0, st, p);
+  return hipGetLastError();
 }
 
 }  // namespace

@@ -55,7 +55,11 @@ inline int pass_ahead(int64_t workgroups, int64_t chunks, int64_t nseqs, int64_t
 // Of more walks than CUs, all alike, those beyond the last multiple of the CUs would run
 // on as long as the others: these alone are cut, one piece for every CU, where they are a
 // quarter of the CUs at most and long enough (the layer's gradients, 36 walks: 256 whole
-// and 32 in 8 pieces 175 us, all whole 191, all in 14 equal pieces a head 208).
+// and 32 in 8 pieces 175 us, all whole 191, all in 14 equal pieces a head 208).  Of 256 and some
+// more forward walks of 128 x 128, 24 chunks each, those beyond cut and all whole: 16 more 120 and
+// 141 us, 32 125 and 141, 64 135 and 144, 96 151 and 145, 128 167 and 149; 64 chunks: 16 297 and 361,
+// 64 346 and 368, 96 385 and 376; 16 chunks: 16 84 and 95, 64 97 and 97; 8 chunks: 16 53 and 51, 64 57
+// and 50.
 struct LinCut {
   int whole, span, pieces, stride;  // as in LinParams
 };
