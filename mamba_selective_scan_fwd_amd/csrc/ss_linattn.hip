@@ -207,12 +207,12 @@ __device__ __forceinline__ bool lin_slow(float decay) { return __float_as_int(de
 // made, at its chunk's begin.  Eight waves with a tile each read LDS twice as often (a layer
 // of 8 x 2048 rows, 12 heads of 128 x 128, bf16: 352 us against 335 then); operands through
 // registers left one workgroup to a CU (682 against 369).
-// Bound by instructions: a chunk of two workgroups takes a CU 12 thousand cycles, in half of
-// which the matrix units are busy; the rest is fp32 values taken apart (a chunk has 164
-// matrix and some 720 vector instructions a wave).  That layer takes 57 us forward, with 27
-// and 10 for the states between the pieces, and 153, 13 and 7 for the gradients, 180
-// TFLOP/s of the formula's operations in all; fp16, in more parts, 32769 rows of 16 heads of
-// 64 x 128 in 102, 41 and 11 us.
+// Bound by instructions of both kinds that seldom run at once: a chunk of two workgroups takes a CU 12
+// thousand cycles, and its 164 matrix and some 720 vector instructions a wave, most of them taking
+// fp32 values apart, a SIMD 5.2 and 5.8 thousand (counters: 22 % and 26 % of the time, waves waiting in a
+// third of it).  Traced one by one, that layer's walk takes 57 us forward, with 26 and 10 for the states
+// between the pieces, and 156, 14 and 7 for the gradients (calls of both together: 250 us, 180 TFLOP/s of
+// the formula's operations); fp16, in more parts, 32769 rows of 16 heads of 64 x 128 109, 43 and 12.
 constexpr int kWaves = 4, kWalkThreads = 64 * kWaves;
 // Weights by number, of rows in E' (0 .. 63), powers of a (64 .. 129) and the decays
 // (lin_decay) of a whole chunk and of the last one (160, 161): with M they lie in the columns of
@@ -1062,10 +1062,10 @@ hipError_t launch_walk(const LinParams& p, hipStream_t st) {
   return hipGetLastError();
 }
 // fp16's weighted rows are two parts (split2_f16).  Of bf16's, three keep fp32's error in the last states;
-// where no walk has any, its outputs are all that shows and two do (8 rows of 2048 tokens, 12 heads of
-// 128 x 128: 81 us against 90 with three, the gradients 172 against 194): a term is then off by 2^-18,
-// as the pairs' weights are.  Only the walk that leaves a state has three, so that dq and dk are the
-// same with and without dh0; the last bit of y (dv) may go by final_state (dh0).
+// where a walk leaves none, its outputs are all that shows and two do (8 rows of 2048 tokens, 12 heads of
+// 128 x 128, forward and gradients: 242 us against 264 with three): a term is then off by 2^-18, as the
+// pairs' weights are.  dq's and dk's walks leave none, so that they are the same with and without dh0; the
+// last bit of y (dv) may go by final_state (dh0).
 template <int IO, int DC, int DO>
 hipError_t launch_walk(const LinParams& p, hipStream_t st) {
   bool full = false;

@@ -43,23 +43,22 @@ inline int pass_ahead(int64_t workgroups, int64_t chunks, int64_t nseqs, int64_t
 // How linear attention walks its sequences (`walks` of each, the longest of `longest`
 // rows): whole, or cut into pieces of some chunks of 64 rows, as many as give every CU
 // two workgroups at once, none of less than 128 rows and none of sequences of up to 384
-// rows.  A walk takes 3.5 us a chunk, a cut two more launches (12 heads of 128 x 128 in
-// bf16, whole against pieces of 128 rows: 1 sequence of 256 rows 17.5 and 22.7 us, of 512
-// 31.6 and 24.1, of 1024 60.1 and 27.5; 4 of 384 24.9 and 32.4, of 1024 61.2 and 40.3).
-// One prompt of 32769 rows with 16 walks: pieces of 448 rows 151 us, 704 139, 1088 (its
-// choice: 496 workgroups) 136, 1280 151, whole 1700; a layer's 8 x 2048 rows with 12 walks
-// 83 with 384 or 448 (its choice), 89.5 with 256, 118 whole.
+// rows.  A walk takes 3.6 us a chunk, a cut two more launches (12 heads of 128 x 128 in
+// bf16, whole against pieces of 128 rows: 1 sequence of 256 rows 18.5 and 23.7 us, of 512
+// 33.1 and 24.5, of 1024 62.6 and 28.7; 4 of 384 26.3 and 31.7, of 512 33.9 and 30.4, of 1024
+// 63.3 and 41.6).  One prompt of 32769 rows with 16 walks: pieces of 448 rows 175 us, 704 157,
+// 1088 (its choice: 496 workgroups) 144, 1280 157, whole 1794; a layer's 8 x 2048 rows with 12
+// walks 83 with 448 (its choice), 86 with 512, 98 with 384, 94 with 256, 122 whole.
 // Packed sequences' pieces go on over their ends, for their lengths are not known: 24
-// ragged prompts of 16384 rows with 12 walks 113 us, 119 to 132 in pieces that begin with
-// their sequences.
+// ragged prompts of 16384 rows with 12 walks 113 us, in pieces that began with their
+// sequences 119 to 132.
 // Of more walks than CUs, all alike, those beyond the last multiple of the CUs would run
 // on as long as the others: these alone are cut, one piece for every CU, where they are a
 // quarter of the CUs at most and long enough (the layer's gradients, 36 walks: 256 whole
-// and 32 in 8 pieces 175 us, all whole 191, all in 14 equal pieces a head 208).  Of 256 and some
-// more forward walks of 128 x 128, 24 chunks each, those beyond cut and all whole: 16 more 120 and
-// 141 us, 32 125 and 141, 64 135 and 144, 96 151 and 145, 128 167 and 149; 64 chunks: 16 297 and 361,
-// 64 346 and 368, 96 385 and 376; 16 chunks: 16 84 and 95, 64 97 and 97; 8 chunks: 16 53 and 51, 64 57
-// and 50.
+// and 32 in 8 pieces 159 us, all whole 175).  Of 256 and some more forward walks of 128 x 128,
+// 24 chunks each, those beyond cut and all whole: 16 more 120 and 141 us, 32 125 and 141, 64
+// 135 and 144, 96 151 and 145, 128 167 and 149; 64 chunks: 16 297 and 361, 64 346 and 368, 96 385
+// and 376; 16 chunks: 16 84 and 95, 64 97 and 97; 8 chunks: 16 53 and 51, 64 57 and 50.
 struct LinCut {
   int whole, span, pieces, stride;  // as in LinParams
 };

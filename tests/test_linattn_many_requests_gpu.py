@@ -96,3 +96,36 @@ def test_maps_of_a_large_batch():
     # the pieces' ends lie elsewhere, so that states differ by their roundings
     assert float((y.float() - z.float()).abs().max()) <= 2.0 ** -7 * float(z.float().abs().max())
     assert float((st - su).abs().max()) <= 2.0 ** -18 * float(su.abs().max())
+
+
+@pytest.mark.parametrize("lens", [[300, 0, 1, 900, 64] + [0] * 300, [900, 300, 5]])
+def test_workspaces_of_exactly_their_size(lens):
+    """Whatever they hold, and nothing behind them is written."""
+    ss = base._ss()
+    q = base._problem(lens, 2, 1, 64, 128, "bf16", seed=109, lead=3, tail=2)
+    g = base._dev(q)
+    a = (g["q"], g["k"], g["v"], g["g"], g["cu"])
+    rows = tuple(t.unsqueeze(0) for t in a[:3]) + (g["g"], g["dy"].unsqueeze(0))
+    kw = dict(cu_seqlens=g["cu"], h0=g["h0"], dfinal=g["df"], want_dh0=True)
+
+    def sizes():
+        pr = ss.ss_linattn_problem(q["T"], len(lens), len(lens) + 2, 2, 1, a[0].stride(0), a[1].stride(0), a[2].stride(0), 64, 128, 2,
+                                   1, 0.125, 0)
+        lib, p = ss.load_library(), ss.ctypes.byref(pr)
+        return lib.ss_linattn_workspace_size(p), lib.ss_linattn_bwd_workspace_size(p)
+
+    outs = []
+    for fill in (None, 0xff, 0x7f):
+        st = g["state"].clone()
+        wide = [None, None] if fill is None else [torch.full((n + 512,), fill, dtype=torch.uint8, device="cuda") for n in sizes()]
+        ws = [None if w is None else w[:-512] for w in wide]
+        y = torch.zeros(q["T"], 2, 128, dtype=torch.bfloat16, device="cuda")
+        ss.linattn_prompt(*a, st, slots=g["slots"], has_state=g["has"], y=y, workspace=ws[0])
+        gr = ss.linattn_bwd(*rows, workspace=ws[1], **kw)
+        torch.cuda.synchronize()
+        outs.append([y, st, *gr.values()])
+        for w in wide:
+            assert w is None or bool((w[-512:] == fill).all())
+    for o in outs[1:]:
+        for x, z in zip(o, outs[0]):
+            assert torch.equal(x, z)
