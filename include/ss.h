@@ -652,7 +652,8 @@ ss_status ss_linattn_prompt(const ss_linattn_problem *p, const void *q, const vo
 /*
  * One token of p->tokens requests, in fp32 over state slots: slots as in
  * ss_ssd_step (a row without one is not computed, its y stays as it was).  q, k
- * and v are aligned to the element, their strides any.
+ * and v are aligned to the element, their strides any; tokens <= 2^20, and
+ * tokens * nheads * dk * dv at most 2^35 - 2^12.
  */
 ss_status ss_linattn_step(const ss_linattn_problem *p, const void *q, const void *k, const void *v,
                           const float *log_decay, const int32_t *slots, float *state, void *y, void *stream);

@@ -942,9 +942,18 @@ __global__ void __launch_bounds__(256) lin_pass_kernel(LinParams p) {
   const int first = q.first / span, end = (q.first + q.chunks - 1) / span + 1;
   const int n = (end < p.pieces ? end : p.pieces) - first;
   if (n < 2) return;
+  const int64_t step = (int64_t)p.stride * size;
+  float* own = p.ws + ((int64_t)first * p.stride + slot) * size + 4 * (int64_t)e4;
+  float* enter = own + p.pieces * step;
+  f32x4 S[kAhead];
+  auto load = [&](int c) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (c + k < n - 1) S[k] = *reinterpret_cast<const f32x4*>(own + (c + k) * step);
+  };
+  load(0);  // while the decays are made and the first state comes
   const float g = p.log_decay[h];
-  const int rows = ((first + 1) * span - q.first) * kC;  // of the first piece
-  float d = lin_decay(g, rows);
+  float d = lin_decay(g, ((first + 1) * span - q.first) * kC);  // over the first piece's rows
   const float whole = lin_decay(g, span * kC);
   const float* init;
   float* fin;
@@ -957,14 +966,8 @@ __global__ void __launch_bounds__(256) lin_pass_kernel(LinParams p) {
     for (int r = 0; r < 4; ++r)
       E[r] = init[state_at(w, 16 * ct + 4 * (lane / 16) + r, 16 * (ot_n * wave + ot) + lane % 16)];
   }
-  const int64_t step = (int64_t)p.stride * size;
-  float* own = p.ws + ((int64_t)first * p.stride + slot) * size + 4 * (int64_t)e4;
-  float* enter = own + p.pieces * step;
-  f32x4 S[kAhead];
   for (int c = 0; c < n; c += kAhead) {
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (c + k < n - 1) S[k] = *reinterpret_cast<const f32x4*>(own + (c + k) * step);
+    if (c) load(c);
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       if (c + k < n) *reinterpret_cast<f32x4*>((c + k ? enter : own) + (c + k) * step) = E;
