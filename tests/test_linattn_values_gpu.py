@@ -122,3 +122,20 @@ def test_channels_of_other_sizes(io, lens):
     check(y[:, :, ok], want[:, :, ok], mag[:, :, ok], "y")
     for s in range(2):
         check(g["state"][int(q["slots"][s])], last[s], lm[s], "state")
+
+
+@pytest.mark.parametrize("io", IOS)
+def test_terms_below_the_largest_of_their_channel(io):
+    """Keys of zero behind the first rows, whose weights a strong decay then takes far below the others': bf16 holds its
+    bounds there too, fp16 what its parts leave, 2^-38 of a channel's largest row for each of up to 64 of them."""
+    q = base._problem([64, 100, 300], 3, 3, 64, 128, io, seed=74, g=torch.tensor([-0.05, -0.3, -0.7]))
+    for a, n in zip((0, 64, 164), (64, 100, 300)):
+        q["k"][a + 5:a + n] = 0
+    g = base._dev(q)
+    y = _prompts(g, q)
+    want, mag, last, lm = _prompts_want(q)
+    check(y, want, mag, "y")
+    most = float(q["k"].abs().max()) * float(q["v"].abs().max())
+    floor = 64 * 2.0 ** -38 * most if io == "f16" else 0.0
+    for s in range(3):
+        check(g["state"][int(q["slots"][s])], last[s], lm[s] + floor * 2.0 ** 15, "state")
